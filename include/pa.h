@@ -407,6 +407,163 @@ size_t pa_varlen_args_bytes(void);
 pa_status pa_attention_varlen_packed(const pa_varlen_args *args);
 
 /*
+ * Draft trees (speculative decoding over the paged cache).
+ *
+ * A step checks, for every sequence, a tree of drafted tokens in one pass of the
+ * target model: pa_tree_attention attends every node to its sequence's context
+ * and its own ancestors, pa_tree_verify accepts or rejects the drafted tokens
+ * against the target's probabilities, and pa_tree_accept moves the accepted
+ * nodes' K/V rows up behind the context.  (The pages list speculative decoding
+ * with a draft model among the engine's features.)
+ *
+ * The tree arguments are the same in the three calls:
+ *   cu_tree_lens  [num_seqs+1] int32 row offsets, cu_tree_lens[0] == 0,
+ *                 non-decreasing: sequence s's tree has T = cu_tree_lens[s+1] -
+ *                 cu_tree_lens[s] nodes, 0 <= T <= max_tree_len, held by rows
+ *                 cu_tree_lens[s] .. cu_tree_lens[s+1]-1 of the node arrays
+ *   parents       [total_nodes] int32: a node's parent as an index within its
+ *                 own tree, smaller than the node's own index, or -1.  Node 0 is
+ *                 the root, the last committed token, whose K/V are new as well;
+ *                 a chain has parents -1, 0, 1, 2, ...
+ *   total_nodes   rows of the node arrays (>= cu_tree_lens[num_seqs])
+ *   max_tree_len  host bound of T, 1 .. PA_TREE_MAX_NODES (else
+ *                 PA_ERR_UNSUPPORTED)
+ *   seq_lens      [num_seqs] int32: context + T.  Node i's K/V sit at position
+ *                 seq_lens[s] - T + i of its sequence and are already written
+ *                 (pa_cache_write) when attended or moved.
+ * A sequence whose offsets or length break these bounds is skipped (what it
+ * would write is left as it was) and flagged PA_ERR_OOB; a parent outside
+ * [-1, i-1] is flagged PA_ERR_OOB and taken as -1.
+ */
+#define PA_TREE_MAX_NODES 64
+
+/*
+ * Workspace pa_tree_attention needs on the current device for these shapes, in
+ * bytes.  Depends on the device's SM count, not on sequence lengths.  Returns 0
+ * for invalid arguments.
+ */
+size_t pa_tree_attention_workspace_bytes(int num_seqs, int max_tree_len, int num_heads,
+                                         int num_kv_heads, int head_size);
+
+/*
+ * pa_tree_attention - attention of draft trees over their paged contexts.
+ *
+ * Node i of sequence s attends to the context, tokens 0 .. seq_lens[s]-T-1, to
+ * its ancestors and to itself: out[i][h] = sum_t softmax_t(scale * q[i][h] .
+ * K[t][h/G]) V[t][h/G] over those tokens t.  Nodes that are no ancestors of a
+ * node have no part in its result, whatever their K/V hold.  A tree of one node
+ * is pa_decode, a chain is pa_prefill_chunk of its rows.
+ *   out, q        [total_nodes][num_heads][head_size] bf16
+ *   max_seq_len   host-side upper bound of seq_lens (sizes the launch only)
+ *   workspace     device scratch of >= pa_tree_attention_workspace_bytes(...)
+ *                 bytes, 256-byte aligned, caller-owned, no initialisation
+ *                 needed; two calls that overlap on the GPU must not share one
+ * Products in bf16 with fp32 accumulation, softmax statistics in fp32.  The
+ * result is the same bits on every call.  num_seqs == 0 or total_nodes == 0 is a
+ * no-op.  Other arguments and errors as pa_decode.
+ */
+pa_status pa_tree_attention(void *out, const void *q, const int32_t *cu_tree_lens,
+                            const int32_t *parents, int num_seqs, int total_nodes,
+                            int max_tree_len, const void *kv_cache, int num_blocks,
+                            int block_size, int num_heads, int num_kv_heads, int head_size,
+                            const int32_t *block_tables, int max_blocks_per_seq,
+                            const int32_t *seq_lens, int max_seq_len, float scale,
+                            void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_tree_attention_fp8 - pa_tree_attention over an FP8 pool: K = code value *
+ * k_scale, V = code value * v_scale.  head_size must be 128 (else
+ * PA_ERR_UNSUPPORTED).  Codes convert to f16 exactly, each query row is scaled by
+ * a power of two into f16 range first (exact), P is rounded to f16.  Workspace:
+ * pa_tree_attention_workspace_bytes.  Other arguments, results and errors as
+ * pa_tree_attention.
+ */
+pa_status pa_tree_attention_fp8(void *out, const void *q, const int32_t *cu_tree_lens,
+                                const int32_t *parents, int num_seqs, int total_nodes,
+                                int max_tree_len, const void *kv_cache, int num_blocks,
+                                int block_size, int num_heads, int num_kv_heads, int head_size,
+                                const int32_t *block_tables, int max_blocks_per_seq,
+                                const int32_t *seq_lens, int max_seq_len, float scale,
+                                float k_scale, float v_scale, void *workspace,
+                                size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_tree_verify - accept drafted tokens against the target's probabilities.
+ *
+ * Per sequence, a walk from the root.  At the last accepted node n (first the
+ * root) let r(x) = p_n(x), the target's probabilities of the token after n, and
+ * Z = 1.  Its children are tried in increasing order of index; child c with token
+ * t is accepted when
+ *   accept_u[c] * q_n(t) * Z < r(t)    with draft probabilities q_n,
+ *   accept_u[c] * Z < r(t)             without (draft_probs NULL: tokens that
+ *                                      were proposed, not drawn);
+ * the walk goes on from it.  Rejected, it leaves
+ *   r(x) := max(r(x) / Z - q_n(x), 0),  Z := sum_x r(x)    with,
+ *   r(t) := 0,                          Z := Z - (old r(t))  without,
+ * and no further child is tried once Z <= 0.  Where no child is accepted, the
+ * next token is drawn from r: the smallest x with r(0) + .. + r(x) > sample_u[s]
+ * * sum r (the last x with r(x) > 0 should rounding leave none; the lowest x of
+ * the largest p_n(x) should sum r be 0).  When siblings were drawn independently
+ * from q_n (or proposed without probabilities) and accept_u, sample_u are
+ * independent uniform numbers, the tokens follow the target's distribution.
+ *   accepted      [num_seqs][max_tree_len] int32, written: the accepted nodes'
+ *                 indices within their tree, the root first; -1 after the last
+ *   num_accepted  [num_seqs] int32, written: nodes in that list (>= 1; 0 for an
+ *                 empty tree)
+ *   next_tokens   [num_seqs] int32, written (-1 for an empty tree)
+ *   target_probs  [total_nodes][vocab_size] fp32, row i at element i *
+ *                 target_row_stride (>= vocab_size): p after node i
+ *   draft_probs   the same shape with draft_row_stride, row i: what the children
+ *                 of node i were drawn from (rows of childless nodes unread); or
+ *                 NULL
+ *   tokens        [total_nodes] int32; one outside [0, vocab_size) has
+ *                 probability 0 and is flagged PA_ERR_OOB (the roots' are unread)
+ *   accept_u      [total_nodes] fp32 in [0, 1) (the roots' are unread)
+ *   sample_u      [num_seqs] fp32 in [0, 1)
+ * Probabilities (finite, >= 0) are taken as they are, not normalised.  Sums and
+ * differences carry at least 48 bits, so the result is that of the formulas.
+ * vocab_size from 1 to 1048576 (else PA_ERR_UNSUPPORTED).  fp32 pointers must be
+ * 4-byte aligned.  No workspace.  num_seqs == 0 is a no-op.
+ */
+pa_status pa_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t *next_tokens,
+                         const float *target_probs, int64_t target_row_stride,
+                         const float *draft_probs, int64_t draft_row_stride,
+                         const int32_t *tokens, const int32_t *cu_tree_lens,
+                         const int32_t *parents, int num_seqs, int total_nodes,
+                         int max_tree_len, int vocab_size, const float *accept_u,
+                         const float *sample_u, pa_stream_t stream);
+
+/*
+ * pa_tree_accept - keep the accepted nodes' K/V rows in the cache.
+ *
+ * For every sequence the K and V rows of node accepted[s][i] (at position
+ * seq_lens[s] - T + accepted[s][i]) move to position seq_lens[s] - T + i, i <
+ * num_accepted[s], in place, so that the rows behind the context are the accepted
+ * tokens in order; the rest of the pool keeps its bits.  One call per layer's
+ * pool.
+ *   accepted      [num_seqs][max_tree_len] int32, strictly increasing indices
+ *                 within the tree (as pa_tree_verify writes them)
+ *   num_accepted  [num_seqs] int32, 0 .. T.  A sequence whose list breaks this is
+ *                 skipped (its new length is its old one) and flagged PA_ERR_OOB
+ *   new_seq_lens  [num_seqs] int32, written: seq_lens[s] - T + num_accepted[s];
+ *                 may be NULL, must not be seq_lens
+ * Bit-exact.  num_seqs == 0 is a no-op.
+ */
+pa_status pa_tree_accept(void *kv_cache, int num_blocks, int block_size, int num_kv_heads,
+                         int head_size, const int32_t *accepted, const int32_t *num_accepted,
+                         const int32_t *cu_tree_lens, int num_seqs, int max_tree_len,
+                         const int32_t *block_tables, int max_blocks_per_seq,
+                         const int32_t *seq_lens, int32_t *new_seq_lens, pa_stream_t stream);
+
+/* pa_tree_accept_fp8 - the same over an FP8 pool (codes move as they are). */
+pa_status pa_tree_accept_fp8(void *kv_cache, int num_blocks, int block_size, int num_kv_heads,
+                             int head_size, const int32_t *accepted,
+                             const int32_t *num_accepted, const int32_t *cu_tree_lens,
+                             int num_seqs, int max_tree_len, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *seq_lens,
+                             int32_t *new_seq_lens, pa_stream_t stream);
+
+/*
  * Synchronise `stream`, then read and clear the device error word the kernels
  * of this library set on the current device.  Returns PA_OK, PA_ERR_TIMEOUT,
  * PA_ERR_OOB or PA_ERR_PRECONDITION (the first of these that was set, in this

@@ -33,7 +33,11 @@ EXPORTS = ("pa_status_string", "pa_kv_block_bytes", "pa_kv_block_bytes_dtype", "
            "pa_prefill_chunk",
            "pa_attention_varlen_workspace_bytes", "pa_attention_varlen",
            "pa_attention_varlen_fp8", "pa_varlen_args_bytes", "pa_attention_varlen_packed",
-           "pa_error_check")
+           "pa_tree_attention_workspace_bytes", "pa_tree_attention", "pa_tree_attention_fp8",
+           "pa_tree_verify", "pa_tree_accept", "pa_tree_accept_fp8", "pa_error_check")
+
+# Nodes of a draft tree, at most (PA_TREE_MAX_NODES).
+TREE_MAX_NODES = 64
 
 # pa_varlen_args as laid out on a 64-bit little-endian target: out, q, k_new,
 # v_new, slot_mapping, cu_q_lens, kv_cache, block_tables, seq_lens, workspace,
@@ -41,7 +45,7 @@ EXPORTS = ("pa_status_string", "pa_kv_block_bytes", "pa_kv_block_bytes_dtype", "
 # max_prefill_q_len, num_blocks, block_size, num_heads, num_kv_heads, head_size,
 # max_blocks_per_seq, max_seq_len, kv8; scale, k_scale, v_scale.
 VARLEN_ARGS = struct.Struct("<12Q12i3f")
-_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+_BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
 _tls = threading.local()  # one packed-argument buffer per thread
 
 
@@ -115,6 +119,19 @@ def lib(path: Optional[str] = None):
     L.pa_attention_varlen_packed.argtypes = [P]
     if L.pa_varlen_args_bytes() < VARLEN_ARGS.size:
         raise RuntimeError("pa_varlen_args is smaller than this binding's layout")
+    L.pa_tree_attention_workspace_bytes.restype = sz
+    L.pa_tree_attention_workspace_bytes.argtypes = [i, i, i, i, i]
+    L.pa_tree_attention.restype = i
+    L.pa_tree_attention.argtypes = [P, P, P, P, i, i, i, P, i, i, i, i, i, P, i, P, i,
+                                    ctypes.c_float, P, sz, P]
+    L.pa_tree_attention_fp8.restype = i
+    L.pa_tree_attention_fp8.argtypes = [P, P, P, P, i, i, i, P, i, i, i, i, i, P, i, P, i,
+                                        ctypes.c_float, ctypes.c_float, ctypes.c_float, P, sz, P]
+    L.pa_tree_verify.restype = i
+    L.pa_tree_verify.argtypes = [P, P, P, P, i64, P, i64, P, P, P, i, i, i, i, P, P, P]
+    for f in (L.pa_tree_accept, L.pa_tree_accept_fp8):
+        f.restype = i
+        f.argtypes = [P, i, i, i, i, P, P, P, i, i, P, i, P, P, P]
     L.pa_error_check.restype = i
     L.pa_error_check.argtypes = [P]
     if path is None:
@@ -513,6 +530,241 @@ def pa_attention_varlen(out: torch.Tensor, q: torch.Tensor, k_new: Optional[torc
     st = L.pa_attention_varlen_packed(addr)
     if st:
         raise PaError(st, "pa_attention_varlen_fp8" if fp8 else "pa_attention_varlen")
+
+
+def pa_tree_attention_workspace_bytes(num_seqs: int, max_tree_len: int, num_heads: int,
+                                      num_kv_heads: int, head_size: int) -> int:
+    return int(lib().pa_tree_attention_workspace_bytes(num_seqs, max_tree_len, num_heads,
+                                                       num_kv_heads, head_size))
+
+
+def _same_device(first: torch.Tensor, *others: torch.Tensor) -> None:
+    for t in others:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != first.get_device():
+            raise ValueError("every tensor of a call must be on one device")
+
+
+def _on_current_device(dev: int) -> None:
+    """The library launches on the current device: tensors elsewhere are refused."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _tree_attention(fp8, out, q, cu_tree_lens, parents, max_tree_len, kv_cache, block_tables,
+                    seq_lens, max_seq_len, scale, scales, workspace, stream):
+    try:  # every tensor at once; on failure the per-argument checks name the culprit
+        dev = kv_cache.get_device()
+        ks, qs, bts = kv_cache.shape, q.shape, block_tables.shape
+        ok = (len(ks) == 5 and ks[1] == 2 and len(qs) == 3 and len(bts) == 2
+              and kv_cache.dtype is (_U8 if fp8 else _BF16) and dev >= 0
+              and kv_cache.is_contiguous()
+              and q.dtype is _BF16 and q.get_device() == dev and q.is_contiguous()
+              and out.dtype is _BF16 and out.get_device() == dev and out.is_contiguous()
+              and cu_tree_lens.dtype is _I32 and cu_tree_lens.get_device() == dev
+              and cu_tree_lens.dim() == 1 and cu_tree_lens.is_contiguous()
+              and parents.dtype is _I32 and parents.get_device() == dev and parents.dim() == 1
+              and parents.is_contiguous()
+              and block_tables.dtype is _I32 and block_tables.get_device() == dev
+              and block_tables.is_contiguous()
+              and seq_lens.dtype is _I32 and seq_lens.get_device() == dev and seq_lens.dim() == 1
+              and seq_lens.is_contiguous()
+              and workspace.dtype is _U8 and workspace.get_device() == dev and workspace.dim() == 1
+              and workspace.is_contiguous())
+    except (AttributeError, TypeError):
+        ok = False
+    if not ok:
+        (_pool8_geom if fp8 else _pool_geom)(kv_cache)
+        _need(q, "q", _BF16, 3)
+        _need(out, "out", _BF16, 3)
+        _need(cu_tree_lens, "cu_tree_lens", _I32, 1)
+        _need(parents, "parents", _I32, 1)
+        _need(block_tables, "block_tables", _I32, 2)
+        _need(seq_lens, "seq_lens", _I32, 1)
+        _need(workspace, "workspace", _U8, 1)
+        _same_device(kv_cache, q, out, cu_tree_lens, parents, block_tables, seq_lens, workspace)
+        ks, qs, bts = kv_cache.shape, q.shape, block_tables.shape
+    _on_current_device(dev)
+    NB, _, Hkv, bs, D = ks
+    B = seq_lens.shape[0]
+    rows, Hq, Dq = qs
+    if Dq != D or out.shape != qs or parents.shape[0] != rows or bts[0] != B or \
+            cu_tree_lens.shape[0] != B + 1:
+        raise ValueError("inconsistent tree attention shapes")
+    L = _lib if _lib is not None else lib()
+    args = (out.data_ptr(), q.data_ptr(), cu_tree_lens.data_ptr(), parents.data_ptr(), B, rows,
+            int(max_tree_len), kv_cache.data_ptr(), NB, bs, Hq, Hkv, D, block_tables.data_ptr(),
+            bts[1], seq_lens.data_ptr(), int(max_seq_len), float(scale))
+    tail = (workspace.data_ptr(), workspace.numel(), _stream(stream))
+    if fp8:
+        st = L.pa_tree_attention_fp8(*args, float(scales[0]), float(scales[1]), *tail)
+    else:
+        st = L.pa_tree_attention(*args, *tail)
+    if st:
+        raise PaError(st, "pa_tree_attention_fp8" if fp8 else "pa_tree_attention")
+
+
+def pa_tree_attention(out: torch.Tensor, q: torch.Tensor, cu_tree_lens: torch.Tensor,
+                      parents: torch.Tensor, max_tree_len: int, kv_cache: torch.Tensor,
+                      block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                      scale: float, workspace: torch.Tensor, stream=None,
+                      kv_scales: Optional[tuple] = None) -> None:
+    """Attention of draft trees: q/out [total_nodes, Hq, D], parents [total_nodes],
+    cu_tree_lens [B+1]; seq_lens counts context and tree.
+
+    A uint8 (FP8 e4m3) pool goes to pa_tree_attention_fp8 with
+    kv_scales = (k_scale, v_scale)."""
+    fp8 = getattr(kv_cache, "dtype", None) is _U8
+    if fp8 and kv_scales is None:
+        raise ValueError("an FP8 pool needs kv_scales=(k_scale, v_scale)")
+    _tree_attention(fp8, out, q, cu_tree_lens, parents, max_tree_len, kv_cache, block_tables,
+                    seq_lens, max_seq_len, scale, kv_scales, workspace, stream)
+
+
+def pa_tree_attention_fp8(out: torch.Tensor, q: torch.Tensor, cu_tree_lens: torch.Tensor,
+                          parents: torch.Tensor, max_tree_len: int, kv_cache: torch.Tensor,
+                          block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                          scale: float, k_scale: float, v_scale: float, workspace: torch.Tensor,
+                          stream=None) -> None:
+    """pa_tree_attention over an FP8 pool (uint8 e4m3 codes times k_scale / v_scale)."""
+    _tree_attention(True, out, q, cu_tree_lens, parents, max_tree_len, kv_cache, block_tables,
+                    seq_lens, max_seq_len, scale, (k_scale, v_scale), workspace, stream)
+
+
+def _prob_rows(t: torch.Tensor, name: str, rows: int, vocab: int) -> int:
+    """Row stride of a [rows, vocab] fp32 tensor whose rows may lie further apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not _F32:
+        raise ValueError(f"{name} must be {_F32}, got {t.dtype}")
+    if t.shape != (rows, vocab):
+        raise ValueError(f"{name} must be [total_nodes, vocab_size]")
+    if rows <= 1 and (vocab <= 1 or t.stride(1) == 1):
+        return vocab
+    if (vocab > 1 and t.stride(1) != 1) or t.stride(0) < vocab:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0)
+
+
+def pa_tree_verify(accepted: torch.Tensor, num_accepted: torch.Tensor, next_tokens: torch.Tensor,
+                   target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor],
+                   tokens: torch.Tensor, cu_tree_lens: torch.Tensor, parents: torch.Tensor,
+                   accept_u: torch.Tensor, sample_u: torch.Tensor, stream=None) -> None:
+    """Accept drafted tokens: target_probs / draft_probs [total_nodes, V] fp32 (rows may
+    be strided; draft_probs None: tokens proposed without probabilities), tokens, parents,
+    accept_u [total_nodes], sample_u [B]; writes accepted [B, max_tree_len] (node indices,
+    -1 padded), num_accepted [B] and next_tokens [B]."""
+    try:  # every tensor at once; on failure the per-argument checks name the culprit
+        dev = accepted.get_device()
+        ok = (accepted.dtype is _I32 and dev >= 0 and accepted.dim() == 2
+              and accepted.is_contiguous()
+              and num_accepted.dtype is _I32 and num_accepted.get_device() == dev
+              and num_accepted.dim() == 1 and num_accepted.is_contiguous()
+              and next_tokens.dtype is _I32 and next_tokens.get_device() == dev and next_tokens.dim() == 1
+              and next_tokens.is_contiguous()
+              and tokens.dtype is _I32 and tokens.get_device() == dev and tokens.dim() == 1
+              and tokens.is_contiguous()
+              and cu_tree_lens.dtype is _I32 and cu_tree_lens.get_device() == dev
+              and cu_tree_lens.dim() == 1 and cu_tree_lens.is_contiguous()
+              and parents.dtype is _I32 and parents.get_device() == dev and parents.dim() == 1
+              and parents.is_contiguous()
+              and accept_u.dtype is _F32 and accept_u.get_device() == dev and accept_u.dim() == 1
+              and accept_u.is_contiguous()
+              and sample_u.dtype is _F32 and sample_u.get_device() == dev and sample_u.dim() == 1
+              and sample_u.is_contiguous())
+    except (AttributeError, TypeError):
+        ok = False
+    if not ok:
+        _need(accepted, "accepted", _I32, 2)
+        _need(num_accepted, "num_accepted", _I32, 1)
+        _need(next_tokens, "next_tokens", _I32, 1)
+        _need(tokens, "tokens", _I32, 1)
+        _need(cu_tree_lens, "cu_tree_lens", _I32, 1)
+        _need(parents, "parents", _I32, 1)
+        _need(accept_u, "accept_u", _F32, 1)
+        _need(sample_u, "sample_u", _F32, 1)
+        _same_device(accepted, num_accepted, next_tokens, tokens, cu_tree_lens, parents,
+                     accept_u, sample_u)
+    _on_current_device(dev)
+    B, max_tree = accepted.shape
+    rows = tokens.shape[0]
+    if num_accepted.shape[0] != B or next_tokens.shape[0] != B or sample_u.shape[0] != B or \
+            cu_tree_lens.shape[0] != B + 1 or parents.shape[0] != rows or \
+            accept_u.shape[0] != rows:
+        raise ValueError("inconsistent tree verification shapes")
+    if getattr(target_probs, "ndim", 0) != 2:
+        raise ValueError("target_probs must be [total_nodes, vocab_size]")
+    V = target_probs.shape[1]
+    _same_device(accepted, target_probs)
+    ts = _prob_rows(target_probs, "target_probs", rows, V)
+    dp, ds = None, 0
+    if draft_probs is not None:
+        _same_device(accepted, draft_probs)
+        ds = _prob_rows(draft_probs, "draft_probs", rows, V)
+        # An empty batch's tensor has no address; the call must still see a draft.
+        dp = draft_probs.data_ptr() or None
+    L = _lib if _lib is not None else lib()
+    st = L.pa_tree_verify(accepted.data_ptr(), num_accepted.data_ptr(), next_tokens.data_ptr(),
+                          target_probs.data_ptr(), ts, dp, ds, tokens.data_ptr(),
+                          cu_tree_lens.data_ptr(), parents.data_ptr(), B, rows, max_tree, V,
+                          accept_u.data_ptr(), sample_u.data_ptr(), _stream(stream))
+    if st:
+        raise PaError(st, "pa_tree_verify")
+
+
+def pa_tree_accept(kv_cache: torch.Tensor, accepted: torch.Tensor, num_accepted: torch.Tensor,
+                   cu_tree_lens: torch.Tensor, block_tables: torch.Tensor,
+                   seq_lens: torch.Tensor, new_seq_lens: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """Move the accepted nodes' K/V rows (accepted [B, max_tree_len], num_accepted [B])
+    up behind their contexts, in place, in a bf16 or uint8 (FP8) pool; new_seq_lens [B],
+    if given, receives the new lengths."""
+    try:  # every tensor at once; on failure the per-argument checks name the culprit
+        dev = kv_cache.get_device()
+        ks, bts = kv_cache.shape, block_tables.shape
+        fp8 = kv_cache.dtype is _U8
+        ok = (len(ks) == 5 and ks[1] == 2 and len(bts) == 2
+              and (fp8 or kv_cache.dtype is _BF16) and dev >= 0
+              and kv_cache.is_contiguous()
+              and accepted.dtype is _I32 and accepted.get_device() == dev and accepted.dim() == 2
+              and accepted.is_contiguous()
+              and num_accepted.dtype is _I32 and num_accepted.get_device() == dev
+              and num_accepted.dim() == 1 and num_accepted.is_contiguous()
+              and cu_tree_lens.dtype is _I32 and cu_tree_lens.get_device() == dev
+              and cu_tree_lens.dim() == 1 and cu_tree_lens.is_contiguous()
+              and block_tables.dtype is _I32 and block_tables.get_device() == dev
+              and block_tables.is_contiguous()
+              and seq_lens.dtype is _I32 and seq_lens.get_device() == dev and seq_lens.dim() == 1
+              and seq_lens.is_contiguous())
+    except (AttributeError, TypeError):
+        ok = False
+    if not ok:
+        fp8 = getattr(kv_cache, "dtype", None) is _U8
+        (_pool8_geom if fp8 else _pool_geom)(kv_cache)
+        _need(accepted, "accepted", _I32, 2)
+        _need(num_accepted, "num_accepted", _I32, 1)
+        _need(cu_tree_lens, "cu_tree_lens", _I32, 1)
+        _need(block_tables, "block_tables", _I32, 2)
+        _need(seq_lens, "seq_lens", _I32, 1)
+        _same_device(kv_cache, accepted, num_accepted, cu_tree_lens, block_tables, seq_lens)
+        ks, bts = kv_cache.shape, block_tables.shape
+    if new_seq_lens is not None:
+        _need(new_seq_lens, "new_seq_lens", _I32, 1)
+        _same_device(kv_cache, new_seq_lens)
+    _on_current_device(dev)
+    NB, _, Hkv, bs, D = ks
+    B, max_tree = accepted.shape
+    if num_accepted.shape[0] != B or cu_tree_lens.shape[0] != B + 1 or bts[0] != B or \
+            seq_lens.shape[0] != B or (new_seq_lens is not None and new_seq_lens.shape[0] != B):
+        raise ValueError("inconsistent tree acceptance shapes")
+    L = _lib if _lib is not None else lib()
+    st = (L.pa_tree_accept_fp8 if fp8 else L.pa_tree_accept)(
+        kv_cache.data_ptr(), NB, bs, Hkv, D, accepted.data_ptr(), num_accepted.data_ptr(),
+        cu_tree_lens.data_ptr(), B, max_tree, block_tables.data_ptr(), bts[1],
+        seq_lens.data_ptr(), None if new_seq_lens is None else new_seq_lens.data_ptr(),
+        _stream(stream))
+    if st:
+        raise PaError(st, "pa_tree_accept_fp8" if fp8 else "pa_tree_accept")
 
 
 def pa_error_check(stream=None) -> None:

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
 SOURCES = ["pa_api.cu", "pa_cache_write.cu", "pa_attention.cu",
-           "pa_decode_noalloc.cu"]
+           "pa_decode_noalloc.cu", "pa_tree_attention.cu", "pa_tree_verify.cu",
+           "pa_tree_accept.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -666,6 +666,166 @@ pa_status pa_prefill_chunk_fp8(void *out, const void *q, const int32_t *cu_q_len
                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// The tree arguments shared by the pa_tree_* calls.
+static pa_status tree_checks(const int32_t *cu, int num_seqs, int total_nodes, int max_tree_len) {
+    if (num_seqs < 0 || total_nodes < 0 || max_tree_len <= 0) return PA_ERR_INVALID_ARG;
+    if (max_tree_len > PA_TREE_MAX_NODES) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > 0 && (!cu || !aligned(cu, 4))) return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+
+size_t pa_tree_attention_workspace_bytes(int num_seqs, int max_tree_len, int num_heads,
+                                         int num_kv_heads, int head_size) {
+    if (num_seqs < 0 || max_tree_len <= 0 || max_tree_len > PA_TREE_MAX_NODES) return 0;
+    if (num_kv_heads <= 0 || check_heads(num_heads, num_kv_heads) != PA_OK) return 0;
+    if (head_size != 64 && head_size != 128) return 0;
+    return pa::tree_attention_workspace_bytes(num_seqs, max_tree_len, num_heads / num_kv_heads,
+                                              head_size, pa::device_sm_count());
+}
+
+// pa_tree_attention and pa_tree_attention_fp8 (kv8: an FP8 pool, head size 128).
+static pa_status tree_attention_impl(void *out, const void *q, const int32_t *cu_tree_lens,
+                                     const int32_t *parents, int num_seqs, int total_nodes,
+                                     int max_tree_len, const void *kv_cache, int num_blocks,
+                                     int block_size, int num_heads, int num_kv_heads,
+                                     int head_size, const int32_t *block_tables,
+                                     int max_blocks_per_seq, const int32_t *seq_lens,
+                                     int max_seq_len, float scale, bool kv8, float k_scale,
+                                     float v_scale, void *workspace, size_t workspace_bytes,
+                                     pa_stream_t stream) {
+    pa_status st = check_pool(kv_cache, num_blocks, block_size, num_kv_heads, head_size);
+    if (st != PA_OK) return st;
+    if ((st = check_heads(num_heads, num_kv_heads)) != PA_OK) return st;
+    if ((st = tree_checks(cu_tree_lens, num_seqs, total_nodes, max_tree_len)) != PA_OK) return st;
+    if (kv8 && head_size != 128) return PA_ERR_UNSUPPORTED;
+    if (max_seq_len < 0 || max_blocks_per_seq <= 0) return PA_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return PA_ERR_INVALID_ARG;
+    if (kv8 && (!good_scale(k_scale) || !good_scale(v_scale))) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_nodes == 0) return PA_OK;
+    if (!out || !q || !parents || !block_tables || !seq_lens || !aligned(out, 16) ||
+        !aligned(q, 16) || !aligned(parents, 4) || !aligned(block_tables, 4) ||
+        !aligned(seq_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    if (max_seq_len > (long long)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
+    // Tile indices over (sequence, KV head, 16 tokens at least) fit 31 bits.
+    if ((long long)num_seqs * num_kv_heads *
+            (((long long)max_blocks_per_seq * block_size + 15) / 16) >= (1LL << 31))
+        return PA_ERR_UNSUPPORTED;
+    const size_t need = pa::tree_attention_workspace_bytes(
+        num_seqs, max_tree_len, num_heads / num_kv_heads, head_size, pa::device_sm_count());
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return PA_ERR_WORKSPACE;
+    pa::KvGeom g{num_blocks, block_size, num_kv_heads, head_size};
+    pa::TreeGeom t{cu_tree_lens, parents, num_seqs, total_nodes, max_tree_len};
+    return from_cuda(pa::launch_tree_attention(out, q, t, kv_cache, g, num_heads, block_tables,
+                                               max_blocks_per_seq, seq_lens, max_seq_len, scale,
+                                               kv8, k_scale, v_scale, workspace,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_tree_attention(void *out, const void *q, const int32_t *cu_tree_lens,
+                            const int32_t *parents, int num_seqs, int total_nodes,
+                            int max_tree_len, const void *kv_cache, int num_blocks,
+                            int block_size, int num_heads, int num_kv_heads, int head_size,
+                            const int32_t *block_tables, int max_blocks_per_seq,
+                            const int32_t *seq_lens, int max_seq_len, float scale,
+                            void *workspace, size_t workspace_bytes, pa_stream_t stream) {
+    return tree_attention_impl(out, q, cu_tree_lens, parents, num_seqs, total_nodes,
+                               max_tree_len, kv_cache, num_blocks, block_size, num_heads,
+                               num_kv_heads, head_size, block_tables, max_blocks_per_seq,
+                               seq_lens, max_seq_len, scale, false, 1.f, 1.f, workspace,
+                               workspace_bytes, stream);
+}
+
+pa_status pa_tree_attention_fp8(void *out, const void *q, const int32_t *cu_tree_lens,
+                                const int32_t *parents, int num_seqs, int total_nodes,
+                                int max_tree_len, const void *kv_cache, int num_blocks,
+                                int block_size, int num_heads, int num_kv_heads, int head_size,
+                                const int32_t *block_tables, int max_blocks_per_seq,
+                                const int32_t *seq_lens, int max_seq_len, float scale,
+                                float k_scale, float v_scale, void *workspace,
+                                size_t workspace_bytes, pa_stream_t stream) {
+    return tree_attention_impl(out, q, cu_tree_lens, parents, num_seqs, total_nodes,
+                               max_tree_len, kv_cache, num_blocks, block_size, num_heads,
+                               num_kv_heads, head_size, block_tables, max_blocks_per_seq,
+                               seq_lens, max_seq_len, scale, true, k_scale, v_scale, workspace,
+                               workspace_bytes, stream);
+}
+
+pa_status pa_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t *next_tokens,
+                         const float *target_probs, int64_t target_row_stride,
+                         const float *draft_probs, int64_t draft_row_stride,
+                         const int32_t *tokens, const int32_t *cu_tree_lens,
+                         const int32_t *parents, int num_seqs, int total_nodes,
+                         int max_tree_len, int vocab_size, const float *accept_u,
+                         const float *sample_u, pa_stream_t stream) {
+    pa_status st = tree_checks(cu_tree_lens, num_seqs, total_nodes, max_tree_len);
+    if (st != PA_OK) return st;
+    if (vocab_size <= 0 || target_row_stride < vocab_size ||
+        (draft_probs && draft_row_stride < vocab_size))
+        return PA_ERR_INVALID_ARG;
+    if (vocab_size > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!accepted || !num_accepted || !next_tokens || !sample_u || !aligned(accepted, 4) ||
+        !aligned(num_accepted, 4) || !aligned(next_tokens, 4) || !aligned(sample_u, 4))
+        return PA_ERR_INVALID_ARG;
+    if (total_nodes > 0 &&
+        (!target_probs || !tokens || !parents || !accept_u || !aligned(target_probs, 4) ||
+         !aligned(draft_probs, 4) || !aligned(tokens, 4) || !aligned(parents, 4) ||
+         !aligned(accept_u, 4)))
+        return PA_ERR_INVALID_ARG;
+    pa::TreeGeom t{cu_tree_lens, parents, num_seqs, total_nodes, max_tree_len};
+    return from_cuda(pa::launch_tree_verify(accepted, num_accepted, next_tokens, target_probs,
+                                            target_row_stride, draft_probs, draft_row_stride,
+                                            tokens, t, vocab_size, accept_u, sample_u,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// pa_tree_accept and pa_tree_accept_fp8 (elem_bytes 2 and 1).
+static pa_status tree_accept_impl(void *kv_cache, int num_blocks, int block_size,
+                                  int num_kv_heads, int head_size, int elem_bytes,
+                                  const int32_t *accepted, const int32_t *num_accepted,
+                                  const int32_t *cu_tree_lens, int num_seqs, int max_tree_len,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *seq_lens, int32_t *new_seq_lens,
+                                  pa_stream_t stream) {
+    pa_status st = check_pool(kv_cache, num_blocks, block_size, num_kv_heads, head_size);
+    if (st != PA_OK) return st;
+    if ((st = tree_checks(cu_tree_lens, num_seqs, 0, max_tree_len)) != PA_OK) return st;
+    if (max_blocks_per_seq <= 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!accepted || !num_accepted || !block_tables || !seq_lens || !aligned(accepted, 4) ||
+        !aligned(num_accepted, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+        !aligned(new_seq_lens, 4) || new_seq_lens == seq_lens)
+        return PA_ERR_INVALID_ARG;
+    pa::KvGeom g{num_blocks, block_size, num_kv_heads, head_size};
+    pa::TreeGeom t{cu_tree_lens, nullptr, num_seqs, INT32_MAX, max_tree_len};
+    return from_cuda(pa::launch_tree_accept(kv_cache, g, elem_bytes, accepted, num_accepted, t,
+                                            block_tables, max_blocks_per_seq, seq_lens,
+                                            new_seq_lens,
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pa_status pa_tree_accept(void *kv_cache, int num_blocks, int block_size, int num_kv_heads,
+                         int head_size, const int32_t *accepted, const int32_t *num_accepted,
+                         const int32_t *cu_tree_lens, int num_seqs, int max_tree_len,
+                         const int32_t *block_tables, int max_blocks_per_seq,
+                         const int32_t *seq_lens, int32_t *new_seq_lens, pa_stream_t stream) {
+    return tree_accept_impl(kv_cache, num_blocks, block_size, num_kv_heads, head_size, 2,
+                            accepted, num_accepted, cu_tree_lens, num_seqs, max_tree_len,
+                            block_tables, max_blocks_per_seq, seq_lens, new_seq_lens, stream);
+}
+
+pa_status pa_tree_accept_fp8(void *kv_cache, int num_blocks, int block_size, int num_kv_heads,
+                             int head_size, const int32_t *accepted,
+                             const int32_t *num_accepted, const int32_t *cu_tree_lens,
+                             int num_seqs, int max_tree_len, const int32_t *block_tables,
+                             int max_blocks_per_seq, const int32_t *seq_lens,
+                             int32_t *new_seq_lens, pa_stream_t stream) {
+    return tree_accept_impl(kv_cache, num_blocks, block_size, num_kv_heads, head_size, 1,
+                            accepted, num_accepted, cu_tree_lens, num_seqs, max_tree_len,
+                            block_tables, max_blocks_per_seq, seq_lens, new_seq_lens, stream);
+}
+
 pa_status pa_error_check(pa_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return PA_ERR_CUDA;
@@ -675,6 +835,12 @@ pa_status pa_error_check(pa_stream_t stream) {
     if (pa::take_error_decode(&b) != cudaSuccess) return PA_ERR_CUDA;
     bits |= b;
     if (pa::take_error_prefill(&b) != cudaSuccess) return PA_ERR_CUDA;
+    bits |= b;
+    if (pa::take_error_tree_attention(&b) != cudaSuccess) return PA_ERR_CUDA;
+    bits |= b;
+    if (pa::take_error_tree_verify(&b) != cudaSuccess) return PA_ERR_CUDA;
+    bits |= b;
+    if (pa::take_error_tree_accept(&b) != cudaSuccess) return PA_ERR_CUDA;
     bits |= b;
     if (bits & 2u) return PA_ERR_TIMEOUT;
     if (bits & 1u) return PA_ERR_OOB;

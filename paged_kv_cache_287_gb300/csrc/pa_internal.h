@@ -44,6 +44,9 @@ struct KvGeom {
 cudaError_t take_error_cache_write(unsigned *bits);
 cudaError_t take_error_decode(unsigned *bits);
 cudaError_t take_error_prefill(unsigned *bits);
+cudaError_t take_error_tree_attention(unsigned *bits);
+cudaError_t take_error_tree_verify(unsigned *bits);
+cudaError_t take_error_tree_accept(unsigned *bits);
 
 // Encode a 2-D TMA map over the pool viewed as rows of head_size bf16 elements,
 // box = 64 elements x box_rows rows, 128-byte swizzle.  False on failure.  Maps
@@ -173,5 +176,33 @@ cudaError_t launch_prefill(void *out, const void *q, const int32_t *cu_q_lens, i
                            int max_q_len, const void *kv_cache, const KvGeom &g, int num_heads,
                            const int32_t *block_tables, int max_blocks_per_seq,
                            const int32_t *seq_lens, float scale, cudaStream_t stream);
+
+
+// Draft trees (pa_tree_*.cu): rows cu[s] .. cu[s+1]-1 of the node arrays are
+// sequence s's tree.
+struct TreeGeom {
+    const int32_t *cu;       // [num_seqs + 1]
+    const int32_t *parents;  // [total_nodes], -1 or an earlier node of the same tree
+    int num_seqs, total_nodes, max_tree;
+};
+size_t tree_attention_workspace_bytes(int num_seqs, int max_tree, int group, int head_size,
+                                      int sm_count);
+cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
+                                  const void *kv_cache, const KvGeom &g, int num_heads,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *seq_lens, int max_seq_len, float scale, bool kv8,
+                                  float k_scale, float v_scale, void *workspace,
+                                  cudaStream_t stream);
+cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t *next_tokens,
+                               const float *target, int64_t target_stride, const float *draft,
+                               int64_t draft_stride, const int32_t *tokens, const TreeGeom &t,
+                               int vocab, const float *accept_u, const float *sample_u,
+                               cudaStream_t stream);
+// elem_bytes: 2 (bf16 pool) or 1 (FP8 pool).
+cudaError_t launch_tree_accept(void *kv_cache, const KvGeom &g, int elem_bytes,
+                               const int32_t *accepted, const int32_t *num_accepted,
+                               const TreeGeom &t, const int32_t *block_tables,
+                               int max_blocks_per_seq, const int32_t *seq_lens,
+                               int32_t *new_seq_lens, cudaStream_t stream);
 
 }  // namespace pa

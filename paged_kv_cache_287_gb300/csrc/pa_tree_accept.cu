@@ -1,0 +1,125 @@
+// pa_tree_accept.cu - keep the accepted nodes of draft trees in the KV cache.
+//
+// A tree's nodes were written behind their context, node j at position base + j
+// (base = seq_len - T).  The accepted path p_0 < p_1 < ... moves to base, base + 1,
+// ...: row base + i := row base + p_i, for K and V of every KV head, in place.
+//
+// Since p is strictly increasing, p_i >= i: when the rows move in ascending i, a
+// destination i lies at or below its own source and strictly below every later
+// source p_k (k > i), so no move overwrites a row that is still to be read.  The
+// columns of a row are independent.  A thread therefore owns one 16-byte column
+// (side, head, chunk) of its sequence and moves it row by row, up to kBatch rows
+// loaded before the first is stored, with no barrier and no staging: a pure copy
+// of (accepted - 1) * 2 * Hkv * D * element bytes each way.
+#include <algorithm>
+
+#include "pa_tree.cuh"
+
+namespace pa {
+namespace {
+
+__device__ unsigned g_err_tree_accept;
+
+constexpr int kBatch = 8;
+
+struct AcceptArgs {
+    uint4 *kv;
+    const int32_t *accepted, *num_accepted, *block_tables, *seq_lens;
+    int32_t *new_seq_lens;
+    TreeGeom t;
+    int num_blocks, block_size, num_kv_heads, max_blocks;
+    int vecs;  // 16-byte vectors in one head's row
+};
+
+__global__ void __launch_bounds__(256) tree_accept_kernel(const AcceptArgs a) {
+    const int s = blockIdx.x;
+    const TreeSpan span = tree_span(a.t, s);
+    const int len = a.seq_lens[s], n = a.num_accepted[s];
+    const int32_t *path = a.accepted + (size_t)s * a.t.max_tree;
+    bool bad = span.n < 0 || len < span.n || len > (long long)a.max_blocks * a.block_size ||
+               n < 0 || n > span.n;
+    // The whole list is checked before a row moves.
+    __shared__ int s_path[64];
+    if (!bad && (int)threadIdx.x < n) {
+        const int p = path[threadIdx.x];
+        s_path[threadIdx.x] = p;
+        bad = p < 0 || p >= span.n || (threadIdx.x > 0 && p <= path[threadIdx.x - 1]);
+    }
+    bad = __syncthreads_or(bad);
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        if (bad) atomicOr(&g_err_tree_accept, kErrOob);
+        if (a.new_seq_lens) a.new_seq_lens[s] = bad ? len : len - span.n + n;
+    }
+    if (bad) return;
+    const int col = blockIdx.y * blockDim.x + threadIdx.x;  // (side, head, vector)
+    const int per_side = a.num_kv_heads * a.vecs;
+    if (col >= 2 * per_side) return;
+    const int row = col / a.vecs, c = col - row * a.vecs;  // row = side * Hkv + head
+    const int base = len - span.n;
+    const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks;
+    // Vector index of this column at position pos; -1 outside the pool.
+    auto at = [&](int pos) -> int64_t {
+        const int blk = bt[pos / a.block_size];
+        if (blk < 0 || blk >= a.num_blocks) {
+            if (c == 0) atomicOr(&g_err_tree_accept, kErrOob);
+            return -1;
+        }
+        return (((int64_t)blk * 2 * a.num_kv_heads + row) * a.block_size + pos % a.block_size) *
+                   a.vecs + c;
+    };
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+        uint4 x[kBatch];
+        int64_t dst[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k;
+            dst[k] = -1;
+            if (i < n && s_path[i] != i) {
+                const int64_t src = at(base + s_path[i]);
+                dst[k] = at(base + i);
+                if (src < 0) dst[k] = -1;
+                if (dst[k] >= 0) x[k] = a.kv[src];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (dst[k] >= 0) a.kv[dst[k]] = x[k];
+    }
+}
+
+}  // namespace
+
+cudaError_t take_error_tree_accept(unsigned *bits) {
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(bits, g_err_tree_accept, sizeof(unsigned));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_err_tree_accept, &zero, sizeof(unsigned));
+    return e;
+}
+
+cudaError_t launch_tree_accept(void *kv_cache, const KvGeom &g, int elem_bytes,
+                               const int32_t *accepted, const int32_t *num_accepted,
+                               const TreeGeom &t, const int32_t *block_tables,
+                               int max_blocks_per_seq, const int32_t *seq_lens,
+                               int32_t *new_seq_lens, cudaStream_t stream) {
+    AcceptArgs a;
+    a.kv = static_cast<uint4 *>(kv_cache);
+    a.accepted = accepted;
+    a.num_accepted = num_accepted;
+    a.block_tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.new_seq_lens = new_seq_lens;
+    a.t = t;
+    a.num_blocks = g.num_blocks;
+    a.block_size = g.block_size;
+    a.num_kv_heads = g.num_kv_heads;
+    a.max_blocks = max_blocks_per_seq;
+    a.vecs = g.head_size * elem_bytes / 16;
+    const int cols = 2 * g.num_kv_heads * a.vecs;
+    // At least the 64 threads that check a path.
+    const int threads = std::min(256, std::max(64, (cols + 31) / 32 * 32));
+    const dim3 grid((unsigned)t.num_seqs, (unsigned)((cols + threads - 1) / threads));
+    tree_accept_kernel<<<grid, threads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace pa
