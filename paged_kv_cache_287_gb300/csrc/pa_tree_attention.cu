@@ -1,11 +1,35 @@
 // pa_tree_attention.cu - attention of draft trees over a paged KV cache.
 //
-// Node i of a sequence's tree (T nodes behind a context of seq_len - T tokens)
-// attends to the context, to its ancestors and to itself:
-//   out = sum_t softmax_t(scale q.K_t) V_t.
-// One warp per (node, query head): the lanes share the head's dims, the keys are
-// taken one at a time with a running maximum and sum.
+// Node i of a sequence's tree (n nodes behind a context of len - n tokens) attends
+// to the context, to its ancestors and to itself:
+//   out = sum_t softmax_t(scale q.K_t) V_t,
+// computed in one pass over the keys with a running maximum m and sum l.
+//
+// Design (tcgen05)
+//   * A query tile is up to 128 rows: floor(128 / G) nodes times the G query heads
+//     of one KV head, so a K/V tile of 128 keys is fetched once for all of them.
+//     Trees of more rows have several row groups.
+//   * Work = the list of 128-key tiles over (sequence, KV head), cut into equal
+//     contiguous ranges, one per worker; a worker is one CTA per row group, and two
+//     CTAs share an SM (each with half of its shared memory and tensor memory), so
+//     that one CTA's loads and products run under the other's softmax.  A segment
+//     (sequence, KV head) that falls across ranges leaves its pieces' (m, l, O) in
+//     the workspace, merged by log-sum-exp in a second, dependent kernel; a segment
+//     that lies in one range is written at once.
+//   * warp 0 streams K and V tiles through the block table with 128B-swizzled TMA
+//     copies; warp 1 issues the products S = Q.K^T (shared memory) and O += P.V (P
+//     from tensor memory, in two 64-key halves); warps 2-5 hold one query row per
+//     thread: softmax, P written over its own scores, the O rescale (rare: only when
+//     a row's maximum rises by more than 2^8), the epilogue.  A warp whose 32 rows
+//     hold no query skips the softmax.  An FP8 pool's tiles land as codes in the
+//     upper half of their slot and two more warps convert them in place to f16.
+//   * Masks: a row's ancestors are a 64-bit word (pointer doubling over the parents,
+//     six shuffle rounds); only tiles that reach past the context look at it.  What
+//     a row does not see gets the score -inf, and V rows of tree nodes are cleared of
+//     NaN and infinities before the product (0 * NaN would reach every row); the rows
+//     that do see one get it added back in the epilogue.
 #include <algorithm>
+#include <cmath>
 
 #include "pa_tree.cuh"
 
@@ -14,88 +38,896 @@ namespace {
 
 __device__ unsigned g_err_tree_attention;
 
+constexpr int kRows = 128;  // query rows per tile (the MMA's M)
+constexpr int kKeys = 128;  // keys per K/V tile
+constexpr float kSlack = 8.0f;
+constexpr uint32_t kCols = 256, kColO = 128;  // tensor memory: S / P, then O
+
 struct TreeAttnArgs {
     __nv_bfloat16 *out;
     const __nv_bfloat16 *q;
-    const uint8_t *kv;
+    const void *kv;
     const int32_t *block_tables, *seq_lens;
     TreeGeom t;
+    int4 *starts;    // [workers]: (sequence, KV head, tile) each range starts at
+    float *part_ml;  // [2 * CTAs][part_rows][2]: m (log2 units), l
+    float *part_acc; // [2 * CTAs][part_rows][D]
+    int part_rows;
     int num_heads, num_kv_heads, group;
-    int block_size, max_blocks, num_blocks;
-    float scale, k_scale, v_scale;
+    int block_size, max_blocks, num_blocks, max_len;
+    int q_tile;      // nodes per query tile: floor(128 / group)
+    int row_groups;  // CTAs per worker
+    int workers;
+    int negate_q;
+    float scale_log2;  // |scale| * log2(e), at least 1e-30
+    float k_scale, v_scale;
 };
 
 template <int D, bool KV8>
-__global__ void __launch_bounds__(128) tree_attention_kernel(const TreeAttnArgs a) {
-    constexpr int kPer = D / 32;  // dims a lane holds
-    const int s = blockIdx.y, lane = threadIdx.x & 31;
-    const TreeSpan span = tree_span(a.t, s);
+struct Tlay {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kPanel = kRows * 128;      // 64 dims of 128 rows or keys
+    static constexpr int kTile = kPanels * kPanel;  // a Q, K or V tile
+    static constexpr int kSlots = D == 64 ? 2 : 1;  // K (and V) tiles held
+    static constexpr int kOperands = (1 + 2 * kSlots) * kTile;
+    static constexpr size_t kSmem = 1024 + (size_t)kOperands;
+    static constexpr int kConv = KV8 ? 2 : 0;  // converting warps
+    static constexpr int kThreads = (6 + kConv) * 32;
+};
+
+// Sequence s as this kernel sees it: no tiles where its data break the bounds.
+struct SeqInfo {
+    int row0, n, len;
+    __device__ __forceinline__ int tiles() const {
+        return n > 0 ? (len + kKeys - 1) / kKeys : 0;
+    }
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs &a, int s) {
+    const TreeSpan t = tree_span(a.t, s);
     const int len = a.seq_lens[s];
-    if (span.n < 0 || len < span.n || len > (long long)a.max_blocks * a.block_size) {
-        if (threadIdx.x == 0) atomicOr(&g_err_tree_attention, kErrOob);
-        return;
+    if (t.n < 0 || len < t.n || len > a.max_len) {
+        atomicOr(&g_err_tree_attention, kErrOob);
+        return {0, 0, 0};
     }
-    const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int node = w / a.num_heads, hq = w - node * a.num_heads;
-    if (node >= span.n) return;
-    const int h = hq / a.group;
-    const size_t row = ((size_t)(span.row0 + node) * a.num_heads + hq) * D + lane * kPer;
-    float q[kPer], acc[kPer], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        q[i] = __bfloat162float(a.q[row + i]);
-        acc[i] = 0.f;
+    return {t.row0, t.n, len};
+}
+
+// The segments of a worker's range, walked by a whole warp in step: the sequences'
+// data come 32 at a time, one per lane.
+struct Walk {
+    int s, pre, x, end;        // sequence, tiles (per head) before it, position, range end
+    int begin, at;             // the range's and the current segment's first position
+    int base;                  // first sequence of the window
+    SeqInfo mine;              // sequence base + lane
+    int h, j0, j1, nt;         // the current segment's head, tiles [j0, j1) of nt
+    SeqInfo cur;
+
+    __device__ __forceinline__ void window(const TreeAttnArgs &a, int s0) {
+        base = s0;
+        const int i = s0 + (int)(threadIdx.x & 31);
+        mine = i < a.t.num_seqs ? seq_info(a, i) : SeqInfo{0, 0, 0};
     }
-    const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks;
-    auto key = [&](int pos) {
-        const int blk = bt[pos / a.block_size];
-        float k[kPer] = {}, v[kPer] = {};
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) atomicOr(&g_err_tree_attention, kErrOob);
-        } else {
-            const size_t kr = (((size_t)blk * 2 * a.num_kv_heads + h) * a.block_size +
-                               pos % a.block_size) * D + lane * kPer;
-            const size_t vr = kr + (size_t)a.num_kv_heads * a.block_size * D;
+    __device__ __forceinline__ void start(const TreeAttnArgs &a, int s0, int pre0, int x0,
+                                          int x1) {
+        s = s0;
+        pre = pre0;
+        x = begin = x0;
+        end = x1;
+        window(a, s0);
+    }
+    // The next segment with rows for row group rg; false at the range's end.
+    __device__ __forceinline__ bool next(const TreeAttnArgs &a, int rg) {
+        while (x < end) {
+            if (s - base >= 32) window(a, s);
+            cur.row0 = __shfl_sync(0xffffffffu, mine.row0, s - base);
+            cur.n = __shfl_sync(0xffffffffu, mine.n, s - base);
+            cur.len = __shfl_sync(0xffffffffu, mine.len, s - base);
+            nt = cur.tiles();
+            const int r = x - a.num_kv_heads * pre;
+            if (r >= a.num_kv_heads * nt) {
+                pre += nt;
+                ++s;
+                continue;
+            }
+            h = r / nt;
+            j0 = r - h * nt;
+            j1 = min(nt, j0 + end - x);
+            at = x;
+            x += j1 - j0;
+            if (cur.n > rg * a.q_tile) return true;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap kv_map, const TreeAttnArgs a) {
+    using L = Tlay<D, KV8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<size_t>(smem_raw) + 1023) & ~static_cast<size_t>(1023));
+    uint8_t *sQ = smem, *sK = smem + L::kTile, *sV = sK + L::kSlots * L::kTile;
+    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], k_staged[2], v_staged[2];
+    __shared__ uint64_t s_full, p_lo, p_hi, pv_done, q_full, o_free, sane, drain;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int s_part[L::kThreads / 32];
+    __shared__ int s_start[2];
+    __shared__ int s_bad[2];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int worker = blockIdx.x / a.row_groups, rg = blockIdx.x - worker * a.row_groups;
+    const int Hkv = a.num_kv_heads, B = a.t.num_seqs, G = a.group, QT = a.q_tile;
+
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    // Tiles per head over all sequences, and where this worker's range starts: every
+    // thread sums a contiguous share of the sequences.
+    int t_begin, t_end;
+    {
+        const int per = (B + L::kThreads - 1) / L::kThreads;
+        const int s0 = min(B, tid * per), s1 = min(B, s0 + per);
+        int sum = 0;
+        for (int s = s0; s < s1; ++s) sum += seq_info(a, s).tiles();
+        int incl = sum;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                if constexpr (KV8) {
-                    uint32_t x, y, z;
-                    e4m3x4_to_f16x4((uint32_t)a.kv[kr + i] | (uint32_t)a.kv[vr + i] << 8, x, y);
-                    z = x;
-                    k[i] = f16_lo(z) * a.k_scale;
-                    v[i] = f16_hi(z) * a.v_scale;
-                } else {
-                    const __nv_bfloat16 *kv = reinterpret_cast<const __nv_bfloat16 *>(a.kv);
-                    k[i] = __bfloat162float(kv[kr + i]);
-                    v[i] = __bfloat162float(kv[vr + i]);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (lane == 31) s_part[warp] = incl;
+        if (tid == 0) s_start[0] = -1;
+        __syncthreads();
+        int before = 0, total = 0;
+        for (int w = 0; w < L::kThreads / 32; ++w) {
+            if (w < warp) before += s_part[w];
+            total += s_part[w];
+        }
+        const long long T = (long long)total * Hkv;
+        const long long We = a.workers < T ? a.workers : (T > 0 ? T : 1);
+        t_begin = worker < We ? (int)(worker * T / We) : 0;
+        t_end = worker < We ? (int)((worker + 1) * T / We) : 0;
+        if (T == 0) t_end = 0;
+        int pre = before + incl - sum;
+        if (t_begin < t_end && t_begin >= (long long)Hkv * pre &&
+            t_begin < (long long)Hkv * (pre + sum)) {
+            int s = s0;
+            for (;; ++s) {
+                const int nt = seq_info(a, s).tiles();
+                if (t_begin < (long long)Hkv * (pre + nt)) break;
+                pre += nt;
+            }
+            s_start[0] = s;
+            s_start[1] = pre;
+        }
+    }
+    if (tid == 0) {
+        prefetch_tensormap(&kv_map);
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(&k_full[i], KV8 ? L::kConv : 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], KV8 ? L::kConv : 1);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&k_staged[i], 1);
+            mbar_init(&v_staged[i], 1);
+        }
+        mbar_init(&s_full, 1);
+        mbar_init(&p_lo, 4);
+        mbar_init(&p_hi, 4);
+        mbar_init(&pv_done, 1);
+        mbar_init(&q_full, 4);
+        mbar_init(&o_free, 4);
+        mbar_init(&sane, 4);
+        mbar_init(&drain, 1);
+        s_bad[0] = s_bad[1] = -1;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int seq0 = s_start[0], pre0 = s_start[1];
+    const bool work = seq0 >= 0;
+    if (tid == 0 && rg == 0) {
+        int4 st = make_int4(-1, 0, 0, 0);
+        if (work) {
+            const int nt = seq_info(a, seq0).tiles(), r = t_begin - Hkv * pre0;
+            st = make_int4(seq0, r / nt, r % nt, 0);
+        }
+        a.starts[worker] = st;
+    }
+
+    if (!work) {
+        // Nothing to do: only the barriers below.
+    } else if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        Walk w;
+        w.start(a, seq0, pre0, t_begin, t_end);
+        const int bs = a.block_size, box_rows = bs >= 16 ? 16 : bs, nbox = kKeys / box_rows;
+        const int v_off = Hkv * bs;
+        const uint64_t policy = policy_evict_first();
+        auto load = [&](uint8_t *dst, uint64_t *bar, int row) {
+            if constexpr (KV8) {
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kKeys * 128));
+                __syncwarp();
+                if (lane < nbox)
+                    tma_load_2d_hint(dst + L::kTile / 2 + lane * box_rows * 128, &kv_map, bar, 0,
+                                     row, policy);
+            } else {
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
+                __syncwarp();
+                if (lane < nbox) {
+#pragma unroll
+                    for (int p = 0; p < L::kPanels; ++p)
+                        tma_load_2d_hint(dst + p * L::kPanel + lane * box_rows * 128, &kv_map, bar,
+                                         64 * p, row, policy);
                 }
             }
+        };
+        int it = 0, k_issued = 0, v_issued = 0;
+        bool ok = true;
+        while (ok && w.next(a, rg)) {
+            const int32_t *bt = a.block_tables + (size_t)w.s * a.max_blocks;
+            for (int j = w.j0; j < w.j1; ++j, ++it) {
+                // This lane's box: a TMA row of the pool, wholly outside the map (zeros,
+                // nothing read) past the sequence or for a bad block id.
+                const int tok = j * kKeys + lane * box_rows;
+                int row = -(1 << 30);
+                if (lane < nbox && tok < w.cur.len) {
+                    const int blk = bt[tok / bs];
+                    if (blk >= 0 && blk < a.num_blocks)
+                        row = ((blk * 2) * Hkv + w.h) * bs + tok % bs;
+                    else
+                        atomicOr(&g_err_tree_attention, kErrOob);
+                }
+                const int st = it % L::kSlots;
+                const uint32_t par = (uint32_t)(it / L::kSlots - 1) & 1u;
+                if (it >= L::kSlots && !(ok = all_wait(&k_empty[st], par))) break;
+                load(sK + st * L::kTile, KV8 ? &k_staged[st] : &k_full[st], row);
+                ++k_issued;
+                if (it >= L::kSlots && !(ok = all_wait(&v_empty[st], par))) break;
+                load(sV + st * L::kTile, KV8 ? &v_staged[st] : &v_full[st],
+                     row < -(1 << 29) ? row : row + v_off);
+                ++v_issued;
+            }
         }
-        float x = 0.f;
+        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
+        // Never leave with copies in flight into this CTA's shared memory.
+        for (int i = max(0, k_issued - L::kSlots); i < k_issued; ++i)
+            mbar_wait_bounded(KV8 ? &k_staged[i % L::kSlots] : &k_full[i % L::kSlots],
+                              (uint32_t)(i / L::kSlots) & 1u);
+        for (int i = max(0, v_issued - L::kSlots); i < v_issued; ++i)
+            mbar_wait_bounded(KV8 ? &v_staged[i % L::kSlots] : &v_full[i % L::kSlots],
+                              (uint32_t)(i / L::kSlots) & 1u);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        Walk w;
+        w.start(a, seq0, pre0, t_begin, t_end);
+        const uint32_t idesc_s =
+            KV8 ? tc_idesc_f16(kRows, kKeys, 0) : tc_idesc_bf16(kRows, kKeys, 0);
+        const uint32_t idesc_pv = KV8 ? tc_idesc_f16(kRows, D, 1) : tc_idesc_bf16(kRows, D, 1);
+        const uint64_t q_desc = tc_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t k_desc = tc_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t v_desc = tc_desc_sw128(smem_u32(sV), L::kPanel, 1024);
+        int it = 0, seg = 0;
+        bool ok = true;
+        while (ok && w.next(a, rg)) {
+            for (int j = w.j0; j < w.j1; ++j, ++it) {
+                const int st = it % L::kSlots;
+                const uint32_t par = (uint32_t)(it / L::kSlots) & 1u;
+                const uint32_t prev = (uint32_t)(it - 1) & 1u;
+                // S = Q.K^T, over the previous tile's P: its product must be done.
+                if (!(ok = all_wait(&k_full[st], par))) break;
+                if (j == w.j0 && !(ok = all_wait(&q_full, (uint32_t)seg & 1u))) break;
+                if (it > 0 && !(ok = all_wait(&pv_done, prev))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t kd = k_desc + (uint64_t)((st * L::kTile) >> 4);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x += q[i] * k[i];
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        x *= a.scale;
-        const float mn = fmaxf(m, x);
-        const float c = __expf(m - mn), p = __expf(x - mn);
-        m = mn;
-        l = l * c + p;
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * L::kPanel + (k & 3) * 32) >> 4;
+                        tc_mma_ss(tmem, q_desc + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&s_full);
+                    tc_commit(&k_empty[st]);
+                }
+                __syncwarp();
+                // O += P.V, the first half while the softmax works on keys 64-127.
+                if (!(ok = all_wait(&v_full[st], par))) break;
+                if (j == w.j0 && seg > 0 && !(ok = all_wait(&o_free, (uint32_t)(seg - 1) & 1u)))
+                    break;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * c + p * v[i];
-    };
-    const int ctx = len - span.n;
-    for (int pos = 0; pos < ctx; ++pos) key(pos);
-    for (int j = node; j >= 0;) {
-        key(ctx + j);
-        const int up = a.t.parents[span.row0 + j];
-        if (up < -1 || up >= j) {
-            if (lane == 0) atomicOr(&g_err_tree_attention, kErrOob);
-            break;
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = all_wait(half ? &p_hi : &p_lo, (uint32_t)it & 1u))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t vd = v_desc + (uint64_t)((st * L::kTile) >> 4);
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            tc_mma_ts(tmem + kColO, tmem + kk * 8,
+                                      vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
+                                      (j > w.j0 || kk > 0) ? 1u : 0u);
+                        if (half) {
+                            tc_commit(&pv_done);
+                            tc_commit(&v_empty[st]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+            ++seg;
         }
-        j = up;
+        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
+        // Every product must be done before tensor memory is freed.
+        if (lane == 0) tc_commit(&drain);
+        __syncwarp();
+        mbar_wait_bounded(&drain, 0);
+    } else if (warp < 6) {
+        // ------------------------------------------------------------ softmax
+        Walk w;
+        w.start(a, seq0, pre0, t_begin, t_end);
+        const int row = 32 * (warp & 3) + lane;  // TMEM lane = query row of the tile
+        const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int r_node = row / G, r_head = row - r_node * G;
+        const bool in_tile = row < QT * G;
+        float sl2 = 0.f;
+        // Ancestors of the current sequence's nodes (lane and lane + 32), and of this row.
+        int anc_seq = -1;
+        uint64_t anc_lo = 0, anc_hi = 0;
+        auto real_in = [&](const SeqInfo &si) { return in_tile && rg * QT + r_node < si.n; };
+        // The segment's query rows into shared memory (K-major, 128B swizzle).
+        auto load_q = [&]() {
+            const bool real = real_in(w.cur);
+            sl2 = a.scale_log2;
+            if (__any_sync(0xffffffffu, real)) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + ((size_t)(w.cur.row0 + rg * QT + r_node) * a.num_heads +
+                           (size_t)w.h * G + r_head) * D);
+                const uint32_t flip = a.negate_q ? 0x80008000u : 0u;  // exact bf16 negation
+                uint4 v[D / 8];
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    v[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                    v[c].x ^= flip;
+                    v[c].y ^= flip;
+                    v[c].z ^= flip;
+                    v[c].w ^= flip;
+                }
+                if constexpr (KV8) {
+                    // f16 query: the row times the power of two that puts its largest
+                    // element in [1, 2), exactly; sl2 takes it back, with k_scale.
+                    float mx = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        mx = fmax3(mx, fabsf(bf16_lo(v[c].x)), fabsf(bf16_hi(v[c].x)));
+                        mx = fmax3(mx, fabsf(bf16_lo(v[c].y)), fabsf(bf16_hi(v[c].y)));
+                        mx = fmax3(mx, fabsf(bf16_lo(v[c].z)), fabsf(bf16_hi(v[c].z)));
+                        mx = fmax3(mx, fabsf(bf16_lo(v[c].w)), fabsf(bf16_hi(v[c].w)));
+                    }
+                    int ex = mx > 0.f ? (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127 : 0;
+                    ex = max(-126, min(126, ex));
+                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // 2^-ex
+                    sl2 *= a.k_scale * __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        v[c] = make_uint4(
+                            pack_f16(bf16_lo(v[c].x) * down, bf16_hi(v[c].x) * down),
+                            pack_f16(bf16_lo(v[c].y) * down, bf16_hi(v[c].y) * down),
+                            pack_f16(bf16_lo(v[c].z) * down, bf16_hi(v[c].z) * down),
+                            pack_f16(bf16_lo(v[c].w) * down, bf16_hi(v[c].w) * down));
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4 *>(sQ + (c / 8) * L::kPanel + row * 128 +
+                                               (((c & 7) ^ (row & 7)) << 4)) = v[c];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full);
+        };
+        // Ancestors of every node of the current sequence: node lane in anc_lo, node
+        // lane + 32 in anc_hi.  Each of six rounds joins a node's set with that of the
+        // node its pointer has reached, and doubles the pointer's stride.
+        auto ancestors = [&]() {
+            if (anc_seq == w.s) return;
+            anc_seq = w.s;
+            int p0 = -1, p1 = -1;
+            auto parent = [&](int i) {
+                if (i >= w.cur.n) return -1;
+                const int p = a.t.parents[w.cur.row0 + i];
+                if (p < -1 || p >= i) {
+                    atomicOr(&g_err_tree_attention, kErrOob);
+                    return -1;
+                }
+                return p;
+            };
+            p0 = parent(lane);
+            p1 = parent(lane + 32);
+            anc_lo = 1ull << lane;
+            anc_hi = 1ull << (lane + 32);
+#pragma unroll 1
+            for (int k = 0; k < 6; ++k) {
+                auto up = [&](int p, uint64_t &m, int &pp) {
+                    const uint64_t x = __shfl_sync(0xffffffffu, anc_lo, p & 31);
+                    const uint64_t y = __shfl_sync(0xffffffffu, anc_hi, p & 31);
+                    const int u = __shfl_sync(0xffffffffu, p0, p & 31);
+                    const int v = __shfl_sync(0xffffffffu, p1, p & 31);
+                    m = p < 0 ? 0ull : (p < 32 ? x : y);
+                    pp = p < 0 ? -1 : (p < 32 ? u : v);
+                };
+                uint64_t m0, m1;
+                int q0, q1;
+                up(p0, m0, q0);
+                up(p1, m1, q1);
+                anc_lo |= m0;
+                anc_hi |= m1;
+                p0 = q0;
+                p1 = q1;
+            }
+        };
+        int it = 0, seg = 0;
+        uint32_t sane_par = 0;
+        bool ok = true, more = w.next(a, rg);
+        if (more) load_q();
+        while (ok && more) {
+            const SeqInfo si = w.cur;
+            const int s_h = w.h, j0 = w.j0, j1 = w.j1;
+            const bool whole = j0 == 0 && j1 == w.nt;
+            const int which = w.at == w.begin ? 0 : 1;  // record of a piece: first in the range?
+            const float scale = sl2;
+            const int ctx = si.len - si.n;
+            const bool real = real_in(si);
+            const bool busy = __any_sync(0xffffffffu, real);
+            const bool tree = j1 * kKeys > ctx;  // the piece holds tree nodes
+            uint64_t anc = 0;
+            if (tree) {
+                ancestors();
+                const int i = real ? rg * QT + r_node : 0;
+                const uint64_t x = __shfl_sync(0xffffffffu, anc_lo, i & 31);
+                const uint64_t y = __shfl_sync(0xffffffffu, anc_hi, i & 31);
+                anc = i < 32 ? x : y;
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int j = j0; j < j1; ++j, ++it) {
+                if (!(ok = all_wait(&s_full, (uint32_t)it & 1u))) break;
+                tc_fence_after();
+                const int k0 = j * kKeys;
+                // V of this tile, where it reaches past the context: rows behind the
+                // sequence are zeroed, tree nodes cleared of NaN and infinities.
+                auto clean_v = [&]() -> bool {
+                    const int st = it % L::kSlots;
+                    if (!all_wait(&v_full[st], (uint32_t)(it / L::kSlots) & 1u)) return false;
+                    uint8_t *vs = sV + st * L::kTile;
+                    const int r0 = max(ctx - k0, 0), r1 = min(si.len - k0, kKeys);
+                    bool bad = false;
+                    for (int e = row; e < (kKeys - r0) * 8 * L::kPanels; e += kRows) {
+                        const int p = e / ((kKeys - r0) * 8), r = r0 + (e >> 3) % (kKeys - r0);
+                        uint4 *at = reinterpret_cast<uint4 *>(vs + p * L::kPanel + r * 128 +
+                                                              (e & 7) * 16);
+                        if (r >= r1) {
+                            *at = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint4 v = *at;
+                        constexpr uint32_t kExp = KV8 ? 0x7C00u : 0x7F80u;
+                        bool hit = false;
+                        auto clear = [&](uint32_t x) {
+                            if ((x & kExp) == kExp) {
+                                x &= 0xffff0000u;
+                                hit = true;
+                            }
+                            if ((x & (kExp << 16)) == (kExp << 16)) {
+                                x &= 0x0000ffffu;
+                                hit = true;
+                            }
+                            return x;
+                        };
+                        v.x = clear(v.x);
+                        v.y = clear(v.y);
+                        v.z = clear(v.z);
+                        v.w = clear(v.w);
+                        if (hit) {
+                            *at = v;
+                            bad = true;
+                        }
+                    }
+                    if (bad) atomicExch(&s_bad[seg & 1], seg);
+                    fence_proxy_async_smem();
+                    return true;
+                };
+                const bool past = k0 + kKeys > ctx;
+                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, nm = 0.f, cr = 1.f;
+                bool rescale = false;
+                float x[KV8 ? 32 : kKeys];
+                // Visible keys of 32-key group g, as a bit word.
+                auto seen = [&](int g) -> uint32_t {
+                    const int d = ctx - k0 - 32 * g;  // context keys in or before this group
+                    if (d >= 32) return 0xffffffffu;
+                    if (d > 0) return ((1u << d) - 1u) | (uint32_t)(anc << d);
+                    return d > -64 ? (uint32_t)(anc >> (-d)) : 0u;
+                };
+                auto mask = [&](float *v, int g) {
+                    const uint32_t word = seen(g);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!((word >> c) & 1u)) v[c] = -INFINITY;
+                };
+                // 32 scores of group g to P, packed into columns 16 g ..
+                auto probs = [&](const float *v, int g) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        float t0, t1, t2, t3;
+                        fma2(t0, t1, v[2 * c], v[2 * c + 1], scale, scale, nm, nm);
+                        fma2(t2, t3, v[2 * c + 2], v[2 * c + 3], scale, scale, nm, nm);
+                        const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+                        const float p2 = fast_exp2(t2), p3 = fast_exp2(t3);
+                        add2(s0, s1, p0, p1);
+                        add2(s2, s3, p2, p3);
+                        pk[c] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                        pk[c + 1] = KV8 ? pack_f16(p2, p3) : pack_bf16(p2, p3);
+                    }
+                    tmem_st16(trow + 16 * g, pk);
+                };
+                if (busy) {
+                    // Row maximum of the raw scores (the scale goes into the exponent).
+                    float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float *v = KV8 ? x : x + 32 * g;
+                        tmem_ld32(trow + 32 * g, *reinterpret_cast<float(*)[32]>(v));
+                        if (KV8) {
+                            tc_wait_ld();
+                            if (past) mask(v, g);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                mx = fmax3(mx, v[c], v[c + 1]);
+                                my = fmax3(my, v[c + 2], v[c + 3]);
+                            }
+                        }
+                    }
+                    if constexpr (!KV8) {
+                        tc_wait_ld();
+                        if (past)
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) mask(x + 32 * g, g);
+                        float mz = -INFINITY, mw = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < kKeys; c += 8) {
+                            mx = fmax3(mx, x[c], x[c + 1]);
+                            my = fmax3(my, x[c + 2], x[c + 3]);
+                            mz = fmax3(mz, x[c + 4], x[c + 5]);
+                            mw = fmax3(mw, x[c + 6], x[c + 7]);
+                        }
+                        mx = fmaxf(mx, mz);
+                        my = fmaxf(my, mw);
+                    }
+                    mx = fmaxf(mx, my) * scale;
+                    const bool grow = mx > m + kSlack;
+                    rescale = __any_sync(0xffffffffu, grow);
+                    if (rescale) {
+                        const float mn = grow ? fmaxf(m, mx) : m;
+                        cr = grow ? fast_exp2(m - mn) : 1.f;
+                        l *= cr;
+                        m = mn;
+                    }
+                    // A row that has seen no key yet keeps m = -inf and P = 0.
+                    nm = m == -INFINITY ? 0.f : -m;
+                    if constexpr (KV8) {
+                        // The scores are read again, 32 at a time (a register per score
+                        // for all of them would spill beside the converting warps).
+#pragma unroll 1
+                        for (int g = 0; g < 2; ++g) {
+                            tmem_ld32(trow + 32 * g, *reinterpret_cast<float(*)[32]>(x));
+                            tc_wait_ld();
+                            if (past) mask(x, g);
+                            probs(x, g);
+                        }
+                    } else {
+                        probs(x, 0);
+                        probs(x + 32, 1);
+                    }
+                    if (rescale && j > j0) {
+                        // Scores ready: every earlier P.V is done, the next one waits.
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            tmem_ld32(trow + kColO + 32 * c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= cr;
+                            tmem_st32(trow + kColO + 32 * c,
+                                      *reinterpret_cast<const uint32_t(*)[32]>(o));
+                        }
+                    }
+                    tc_wait_st();
+                }
+                if (past && !(ok = clean_v())) break;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_lo);
+                if (busy) {
+                    if constexpr (KV8) {
+#pragma unroll 1
+                        for (int g = 2; g < 4; ++g) {
+                            tmem_ld32(trow + 32 * g, *reinterpret_cast<float(*)[32]>(x));
+                            tc_wait_ld();
+                            if (past) mask(x, g);
+                            probs(x, g);
+                        }
+                    } else {
+                        probs(x + 64, 2);
+                        probs(x + 96, 3);
+                    }
+                    l += (s0 + s1) + (s2 + s3);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_hi);
+            }
+            if (!ok) break;
+            const int my_s = w.s;
+            // The next segment's queries while the last products run (this segment's
+            // scores are all read).
+            more = w.next(a, rg);
+            if (more) load_q();
+            bool bad = false;
+            if (tree) {  // did any warp find NaN or infinities in the tree's V?
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sane);
+                if (!(ok = all_wait(&sane, sane_par))) break;
+                sane_par ^= 1u;
+                bad = *reinterpret_cast<volatile int *>(&s_bad[seg & 1]) == seg;
+            }
+            if (!(ok = all_wait(&pv_done, (uint32_t)(it - 1) & 1u))) break;
+            tc_fence_after();
+            if (busy) {
+                const float vsc = KV8 ? a.v_scale : 1.f;
+                const size_t rec = ((size_t)blockIdx.x * 2 + which) * a.part_rows + row;
+                const size_t orow = ((size_t)(si.row0 + rg * QT + r_node) * a.num_heads +
+                                     (size_t)s_h * G + r_head) * D;
+                const float mul = whole ? vsc / l : vsc;
+                const uint64_t keep = policy_evict_last();
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(trow + kColO + 32 * c, o);
+                    tc_wait_ld();
+                    if (bad && real) {
+                        // What this row sees of the values that were cleared.
+                        const int32_t *bt = a.block_tables + (size_t)my_s * a.max_blocks;
+                        for (int i = 0; i < si.n; ++i) {
+                            const int pos = ctx + i;
+                            if (!((anc >> i) & 1ull) || pos < j0 * kKeys || pos >= j1 * kKeys)
+                                continue;
+                            const int blk = bt[pos / a.block_size];
+                            if (blk < 0 || blk >= a.num_blocks) continue;
+                            const size_t v0 =
+                                ((((size_t)blk * 2 + 1) * Hkv + s_h) * a.block_size +
+                                 pos % a.block_size) * D + 32 * c;
+                            const uint8_t *kv = reinterpret_cast<const uint8_t *>(a.kv);
+#pragma unroll 1
+                            for (int e = 0; e < 32; ++e) {
+                                float v;
+                                if constexpr (KV8)
+                                    v = (kv[v0 + e] & 0x7f) == 0x7f ? NAN : 0.f;
+                                else
+                                    v = __bfloat162float(
+                                        reinterpret_cast<const __nv_bfloat16 *>(kv)[v0 + e]);
+                                if (!isfinite(v)) {
+#pragma unroll
+                                    for (int f = 0; f < 32; ++f)
+                                        if (f == e) o[f] += v;
+                                }
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= mul;
+                    if (real && whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow) + 4 * c;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]),
+                                                pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                                pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                                                pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                    } else if (real) {
+                        float4 *dst = reinterpret_cast<float4 *>(a.part_acc + rec * D) + 8 * c;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            st_hint(dst + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                                                         o[4 * e + 3]), keep);
+                    }
+                    __syncwarp();
+                }
+                if (real && !whole)
+                    st_hint(reinterpret_cast<float2 *>(a.part_ml) + rec, make_float2(m, l), keep);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free);
+            ++seg;
+        }
+        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
+    } else if constexpr (KV8) {
+        // ------------------------------------------------------------ e4m3 -> f16
+        // A lane converts whole rows: it reads the row's 128 codes (128B-swizzled as TMA
+        // left them in the slot's upper half), then writes its 128 f16 values into the
+        // two 64-dim panels; row r of the upper panel is exactly the bytes of code row r.
+        Walk w;
+        w.start(a, seq0, pre0, t_begin, t_end);
+        auto convert = [&](uint8_t *slot) {
+            const uint8_t *codes = slot + L::kTile / 2;
+#pragma unroll 1
+            for (int r = (warp - 6) * 32 + lane; r < kKeys; r += 32 * L::kConv) {
+                uint4 in[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    in[c] = *reinterpret_cast<const uint4 *>(codes + r * 128 +
+                                                             ((c ^ (r & 7)) << 4));
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t f[8];
+                    e4m3x4_to_f16x4(in[c].x, f[0], f[1]);
+                    e4m3x4_to_f16x4(in[c].y, f[2], f[3]);
+                    e4m3x4_to_f16x4(in[c].z, f[4], f[5]);
+                    e4m3x4_to_f16x4(in[c].w, f[6], f[7]);
+                    uint8_t *dst = slot + (c >> 2) * L::kPanel + r * 128;
+                    const int ch = 2 * (c & 3);
+                    *reinterpret_cast<uint4 *>(dst + ((ch ^ (r & 7)) << 4)) =
+                        make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(dst + (((ch + 1) ^ (r & 7)) << 4)) =
+                        make_uint4(f[4], f[5], f[6], f[7]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        int it = 0;
+        bool ok = true;
+        while (ok && w.next(a, rg)) {
+            for (int j = w.j0; j < w.j1; ++j, ++it) {
+                const int st = it % L::kSlots;
+                const uint32_t par = (uint32_t)(it / L::kSlots) & 1u;
+                if (!(ok = all_wait(&k_staged[st], par))) break;
+                convert(sK + st * L::kTile);
+                if (lane == 0) mbar_arrive(&k_full[st]);
+                if (!(ok = all_wait(&v_staged[st], par))) break;
+                convert(sV + st * L::kTile);
+                if (lane == 0) mbar_arrive(&v_full[st]);
+            }
+        }
+        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+// Merge the pieces of segments that were split across workers: CTA (w, row group,
+// slice of rows) looks whether worker w's range starts inside a segment whose first
+// piece is worker w - 1's; a warp per row joins the pieces by log-sum-exp.
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeAttnArgs a) {
+    constexpr int kPer = D / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int w = blockIdx.x + 1, rg = blockIdx.y;
+    const int4 me = a.starts[w];
+    if (me.x < 0 || me.z == 0) return;  // idle, or a segment's start
+    const int4 prev = a.starts[w - 1];
+    const bool prev_same = prev.x == me.x && prev.y == me.y;
+    if (prev_same && prev.z > 0) return;  // an earlier CTA merges this segment
+    // Workers w .. w + more - 1 start inside this segment.
+    int more = 0;
+    for (int base = w;; base += kMergeWarps * 32) {
+        const int i = base + (int)threadIdx.x;
+        bool in = false;
+        if (i < a.workers) {
+            const int4 st = a.starts[i];
+            in = st.x == me.x && st.y == me.y;
+        }
+        const int c = __syncthreads_count(in);
+        more += c;
+        if (c < kMergeWarps * 32) break;
+    }
+    const TreeSpan span = tree_span(a.t, me.x);
+    const int rows = min(a.q_tile, span.n - rg * a.q_tile) * a.group;
+    const int row = blockIdx.z * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    auto rec = [&](int k) -> size_t {  // record of piece k (0: worker w - 1's)
+        const size_t cta = (size_t)(w - 1 + k) * a.row_groups + rg;
+        return (cta * 2 + (k == 0 && !prev_same ? 1 : 0)) * a.part_rows + row;
+    };
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+    const int n = more + 1;
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, ml[rec(k)].x);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) a.out[row + i] = __float2bfloat16_rn(acc[i] / l);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float den = 0.f, num[kPer] = {};
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+        const size_t r = rec(k);
+        const float2 e = ml[r];
+        const float wgt = fast_exp2(e.x - M);
+        den += wgt * e.y;
+        const float *acc = a.part_acc + r * D + lane * kPer;
+        float v[kPer];
+        if constexpr (kPer == 4)
+            *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(acc);
+        else
+            *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(acc);
+#pragma unroll
+        for (int e2 = 0; e2 < kPer; ++e2) num[e2] += wgt * v[e2];
+    }
+    const float inv = 1.f / den;
+    const int node = rg * a.q_tile + row / a.group, head = me.y * a.group + row % a.group;
+    __nv_bfloat16 *dst =
+        a.out + ((size_t)(span.row0 + node) * a.num_heads + head) * D + lane * kPer;
+    if constexpr (kPer == 4)
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16(num[0] * inv, num[1] * inv);
+}
+
+// Launch shape for trees of at most max_tree nodes.
+struct Shape {
+    int q_tile, row_groups, workers, part_rows;
+    size_t ml_off, acc_off, bytes;
+};
+
+Shape shape_of(int max_tree, int group, int head_size, int sm_count) {
+    Shape s;
+    s.q_tile = kRows / group;
+    s.row_groups = (max_tree + s.q_tile - 1) / s.q_tile;
+    s.workers = std::max(1, 2 * sm_count / s.row_groups);
+    s.part_rows = std::min(s.q_tile, max_tree) * group;
+    const size_t recs = (size_t)s.workers * s.row_groups * 2 * s.part_rows;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    s.ml_off = up((size_t)s.workers * sizeof(int4));
+    s.acc_off = s.ml_off + up(recs * 8);
+    s.bytes = s.acc_off + recs * head_size * 4;
+    return s;
+}
+
+template <int D, bool KV8>
+cudaError_t launch(const CUtensorMap &map, const TreeAttnArgs &a, bool split,
+                   cudaStream_t stream) {
+    using L = Tlay<D, KV8>;
+    auto kern = tree_attention_kernel<D, KV8>;
+    cudaError_t e = ensure_smem<tree_attention_kernel<D, KV8>>(L::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(a.workers * a.row_groups), L::kThreads, L::kSmem, stream>>>(map, a);
+    if ((e = cudaGetLastError()) != cudaSuccess || !split || a.workers < 2) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.workers - 1), (unsigned)a.row_groups,
+                       (unsigned)((a.part_rows + kMergeWarps - 1) / kMergeWarps));
+    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
 }
 
 }  // namespace
@@ -109,7 +941,7 @@ cudaError_t take_error_tree_attention(unsigned *bits) {
 
 size_t tree_attention_workspace_bytes(int num_seqs, int max_tree, int group, int head_size,
                                       int sm_count) {
-    return 256;
+    return shape_of(max_tree, group, head_size, sm_count).bytes;
 }
 
 cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
@@ -118,31 +950,47 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
                                   const int32_t *seq_lens, int max_seq_len, float scale, bool kv8,
                                   float k_scale, float v_scale, void *workspace,
                                   cudaStream_t stream) {
+    CUtensorMap map;
+    const int box_rows = g.block_size >= 16 ? 16 : g.block_size;
+    if (kv8 ? !encode_kv_map_fp8(&map, kv_cache, g, box_rows)
+            : !encode_kv_map(&map, kv_cache, g, box_rows))
+        return cudaErrorInvalidValue;
     TreeAttnArgs a;
+    a.group = num_heads / g.num_kv_heads;
+    const Shape sh = shape_of(t.max_tree, a.group, g.head_size, device_sm_count());
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.q = static_cast<const __nv_bfloat16 *>(q);
-    a.kv = static_cast<const uint8_t *>(kv_cache);
+    a.kv = kv_cache;
     a.block_tables = block_tables;
     a.seq_lens = seq_lens;
     a.t = t;
+    a.starts = reinterpret_cast<int4 *>(ws);
+    a.part_ml = reinterpret_cast<float *>(ws + sh.ml_off);
+    a.part_acc = reinterpret_cast<float *>(ws + sh.acc_off);
+    a.part_rows = sh.part_rows;
     a.num_heads = num_heads;
     a.num_kv_heads = g.num_kv_heads;
-    a.group = num_heads / g.num_kv_heads;
     a.block_size = g.block_size;
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = g.num_blocks;
-    a.scale = scale;
+    a.max_len = max_seq_len;
+    a.q_tile = sh.q_tile;
+    a.row_groups = sh.row_groups;
+    // No more workers than tiles.
+    const long long tiles = (long long)t.num_seqs * g.num_kv_heads *
+                            (((long long)max_seq_len + kKeys - 1) / kKeys);
+    a.workers = (int)std::max(1LL, std::min<long long>(sh.workers, tiles));
+    // A positive scale is folded into the exponent; a negative one negates Q (exact),
+    // zero becomes a value far too small to change any finite score.
+    a.negate_q = scale < 0.f ? 1 : 0;
+    a.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    const dim3 grid((unsigned)((t.max_tree * num_heads + 3) / 4), (unsigned)t.num_seqs);
-    if (t.num_seqs > 65535) return cudaErrorInvalidValue;
-    if (kv8)
-        tree_attention_kernel<128, true><<<grid, 128, 0, stream>>>(a);
-    else if (g.head_size == 128)
-        tree_attention_kernel<128, false><<<grid, 128, 0, stream>>>(a);
-    else
-        tree_attention_kernel<64, false><<<grid, 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    const bool split = max_seq_len > kKeys;  // one tile is never split
+    if (kv8) return launch<128, true>(map, a, split, stream);
+    if (g.head_size == 128) return launch<128, false>(map, a, split, stream);
+    return launch<64, false>(map, a, split, stream);
 }
 
 }  // namespace pa
