@@ -33,6 +33,7 @@ __device__ unsigned g_err_tree_verify;
 constexpr int kNodes = 64;
 constexpr int kWarps = 16;
 constexpr int kMaxCluster = 8;
+constexpr int kU = 8;  // tokens of p and q a thread loads at once
 
 struct VerifyArgs {
     int32_t *accepted, *num_accepted, *next;
@@ -45,10 +46,11 @@ struct VerifyArgs {
     int cluster;     // CTAs per sequence
     int cta_slice;   // tokens per CTA, a multiple of 32
     int warp_slice;  // tokens per warp, a multiple of 32
+    int cached;      // with draft: r and q of the slice are kept in shared memory
 };
 
 // A number held as head + tail.
-struct Pair {
+struct __align__(8) Pair {
     float h, l;
 };
 
@@ -64,35 +66,89 @@ __device__ __forceinline__ void add_to(Pair &acc, Pair x) {
     acc.l = __fadd_rn(acc.l, __fadd_rn(s.l, x.l));
 }
 
-__device__ __forceinline__ double value(Pair x) { return (double)x.h + (double)x.l; }
-
-// 1 / Z as (head, tail) of 1 / (Z 2^-e), and 2^-e in two factors (e up to 149).
-__device__ __forceinline__ float4 reciprocal(double z) {
-    int e;
-    const double m = frexp(z, &e);  // z = m 2^e, m in [0.5, 1)
-    const double inv = 1.0 / m;
-    const float h = (float)inv;
-    const int e1 = -e / 2;
-    return make_float4(h, (float)(inv - (double)h), ldexpf(1.f, e1), ldexpf(1.f, -e - e1));
+// The sum over kLanes consecutive lanes (those behind them hold nothing where fewer
+// than 32 are summed), the same bits in each of them.
+template <int kLanes = 32>
+__device__ __forceinline__ Pair warp_sum(Pair x) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        add_to(x, {__shfl_xor_sync(0xffffffffu, x.h, o), __shfl_xor_sync(0xffffffffu, x.l, o)});
+    return x;
 }
 
-// r at a token after nrej rejections with draft probabilities: first p - q (exact),
-// then r / Z - q with each later Z.
+// h + l with |l| at most half a unit of h: such pairs compare by h, then l.
+__device__ __forceinline__ Pair normal(Pair x) { return two_sum(x.h, x.l); }
+__device__ __forceinline__ bool above(Pair x, Pair y) {
+    return x.h > y.h || (x.h == y.h && x.l > y.l);
+}
+
+// x * y to about 47 bits.
+__device__ __forceinline__ Pair times(Pair x, Pair y) {
+    const float m = __fmul_rn(x.h, y.h);
+    return normal({m, __fmaf_rn(x.h, y.l, __fmaf_rn(x.l, y.h, __fmaf_rn(x.h, y.h, -m)))});
+}
+
+// 1 / Z: (head, tail) of 1 / (Z 2^-e) by one Newton step from the fp32 reciprocal
+// (whose error e1 it leaves squared, below 2^-46), and 2^-e in two factors.
+__device__ __forceinline__ float4 reciprocal(Pair z) {
+    int e;
+    const float h = frexpf(z.h, &e);  // z.h = h 2^e, h in [0.5, 1)
+    const int e1 = -e / 2;
+    const float f1 = __int_as_float((127 + e1) << 23), f2 = __int_as_float((127 - e - e1) << 23);
+    const float l = __fmul_rn(__fmul_rn(z.l, f1), f2);
+    const float x = __frcp_rn(h);
+    const float err = __fmaf_rn(-l, x, __fmaf_rn(-h, x, 1.f));
+    return make_float4(x, __fmul_rn(x, err), f1, f2);
+}
+
+// max(p - q, 0), the difference exact (NaN stays).
+__device__ __forceinline__ Pair first_residual(float p, float q) {
+    const Pair r = two_sum(p, -q);
+    return r.h <= 0.f ? Pair{0.f, 0.f} : r;
+}
+
+// max(r / Z - q, 0), z = reciprocal(Z).
+__device__ __forceinline__ Pair next_residual(Pair r, float q, float4 z) {
+    const float h = __fmul_rn(__fmul_rn(r.h, z.z), z.w), l = __fmul_rn(__fmul_rn(r.l, z.z), z.w);
+    const float m = __fmul_rn(h, z.x);
+    const float n = __fmaf_rn(h, z.y, __fmaf_rn(l, z.x, __fmaf_rn(h, z.x, -m)));
+    const Pair d = two_sum(m, -q);
+    const float e = __fadd_rn(d.l, n);
+    const float s = __fadd_rn(d.h, e);
+    return s <= 0.f ? Pair{0.f, 0.f} : Pair{s, __fadd_rn(e, -__fadd_rn(s, -d.h))};
+}
+
+// r at a token after nrej > 0 rejections with draft probabilities.
 __device__ __forceinline__ Pair residual(float p, float q, int nrej, const float4 *zinv) {
-    Pair r = two_sum(p, -q);
-    if (!(r.h > 0.f)) return {r.h != r.h ? r.h : 0.f, 0.f};
-    for (int k = 1; k < nrej; ++k) {
-        const float4 z = zinv[k];
-        const float h = __fmul_rn(__fmul_rn(r.h, z.z), z.w), l = __fmul_rn(__fmul_rn(r.l, z.z), z.w);
-        const float m = __fmul_rn(h, z.x);
-        const float n = __fmaf_rn(h, z.y, __fmaf_rn(l, z.x, __fmaf_rn(h, z.x, -m)));
-        const Pair d = two_sum(m, -q);
-        const float e = __fadd_rn(d.l, n);
-        r.h = __fadd_rn(d.h, e);
-        r.l = __fadd_rn(e, -__fadd_rn(r.h, -d.h));
-        if (!(r.h > 0.f)) return {r.h != r.h ? r.h : 0.f, 0.f};
-    }
+    Pair r = first_residual(p, q);
+    for (int k = 1; k < nrej && r.h != 0.f; ++k) r = next_residual(r, q, zinv[k]);
     return r;
+}
+
+// The first lane whose running sum (of the lanes' weights, >= 0) exceeds goal, with
+// goal lessened by the sum before it and found set; where there is none the last lane
+// with weight (-1 without any), with goal lessened by the whole.
+template <int kLanes = 32>
+__device__ __forceinline__ int locate(Pair mine, Pair &goal, bool &found) {
+    const int lane = threadIdx.x & 31;
+    Pair incl = mine;
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) {
+        const Pair u = {__shfl_up_sync(0xffffffffu, incl.h, o),
+                        __shfl_up_sync(0xffffffffu, incl.l, o)};
+        if (lane >= o) add_to(incl, u);
+    }
+    incl = normal(incl);
+    const unsigned some = __ballot_sync(0xffffffffu, mine.h > 0.f);
+    const unsigned over = __ballot_sync(0xffffffffu, above(incl, goal)) & some;
+    found = over != 0;
+    const int at = found ? __ffs((int)over) - 1 : 31 - __clz((int)some);  // clz(0) = 32
+    const int upto = found ? at - 1 : kLanes - 1;
+    const float h = __shfl_sync(0xffffffffu, incl.h, max(upto, 0));
+    const float l = __shfl_sync(0xffffffffu, incl.l, max(upto, 0));
+    if (upto >= 0) add_to(goal, {-h, -l});
+    goal = normal(goal);
+    return at;
 }
 
 __device__ __forceinline__ uint32_t peer_addr(const void *p, int rank) {
@@ -106,21 +162,26 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kWarps * 32) tree_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 32 / kWarps) tree_verify_kernel(const VerifyArgs a) {
     __shared__ int s_par[kNodes], s_tok[kNodes];
     __shared__ float s_p[kNodes], s_q[kNodes], s_u[kNodes];
-    __shared__ double s_z[kNodes];       // Z before each rejection at the current node
-    __shared__ float4 s_zinv[kNodes];
-    __shared__ double s_tot[kWarps];     // warp sums of the last pass
-    __shared__ double s_cta[2][kMaxCluster];  // CTA sums of the cluster, by turns
+    __shared__ float4 s_zinv[kNodes];    // 1 / Z before each rejection at the current node
+    __shared__ Pair s_tot[kWarps];       // warp sums of the last pass
+    __shared__ Pair s_cta[2][kMaxCluster];  // CTA sums of the cluster, by turns
     __shared__ int s_cmd[3];             // what warp 0 asks for: node, rejections, last pass
-    __shared__ double s_goal;
+    __shared__ Pair s_goal;
+    __shared__ Pair s_sub[kWarps];       // the same over the parts of the drawn warp's part
     __shared__ int s_pick;
     __shared__ float s_best[kWarps > kMaxCluster ? kWarps : kMaxCluster];
     __shared__ int s_arg[kWarps > kMaxCluster ? kWarps : kMaxCluster];
     __shared__ float s_cbest[kMaxCluster];
     __shared__ int s_carg[kMaxCluster];
-    extern __shared__ uint32_t s_gone[];  // without draft: a bit per token of the slice
+    // Without draft: a bit per token of the slice.  With, where the slice fits (cached):
+    // r's heads and tails, and q, after the last rejection.
+    extern __shared__ uint32_t s_dyn[];
+    uint32_t *s_gone = s_dyn;
+    float *s_rh = reinterpret_cast<float *>(s_dyn), *s_rl = s_rh + a.cta_slice,
+          *s_qc = s_rl + a.cta_slice;
 
     const int C = a.cluster, s = blockIdx.x / C, rank = blockIdx.x - s * C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -172,20 +233,41 @@ __global__ void __launch_bounds__(kWarps * 32) tree_verify_kernel(const VerifyAr
     __syncthreads();
 
     const int v0 = min(c1, c0 + warp * a.warp_slice), v1 = min(c1, v0 + a.warp_slice);
-    // Warp 0's walk.
+    // Warp 0's walk; lane i holds nodes i and i + 32.
     int cur = 0, nrej = 0, count = 1;
-    double mass = 1.0;
-    uint64_t todo = 0;  // children of cur still to be tried
+    Pair mass = {1.f, 0.f};  // Z
+    uint64_t todo = 0;   // children of cur still to be tried
+    uint64_t ok_first = 0;  // nodes that are accepted when they are tried with Z = 1
+    uint64_t twin = 0;   // nodes with an earlier sibling of the same token
     int my_par[2] = {-1, -1}, my_tok[2] = {-1, -1};
-    auto children = [&](int node) {
-        const unsigned lo = __ballot_sync(0xffffffffu, my_par[0] == node);
-        const unsigned hi = __ballot_sync(0xffffffffu, my_par[1] == node);
-        return (uint64_t)hi << 32 | lo;
+    float my_p[2] = {0.f, 0.f}, my_u[2] = {0.f, 0.f};
+    auto nodes = [&](bool lo, bool hi) {
+        const unsigned x = __ballot_sync(0xffffffffu, lo), y = __ballot_sync(0xffffffffu, hi);
+        return (uint64_t)y << 32 | x;
     };
+    auto children = [&](int node) { return nodes(my_par[0] == node, my_par[1] == node); };
     if (warp == 0) {
+        bool first[2];
         for (int i = 0; i < 2; ++i) {
             my_par[i] = s_par[lane + 32 * i];
             my_tok[i] = s_tok[lane + 32 * i];
+            my_p[i] = s_p[lane + 32 * i];
+            my_u[i] = s_u[lane + 32 * i];
+            // u q < p with the product exact (u < p without draft): its rounding error
+            // decides only where the rounded product equals p.
+            const float q = with ? s_q[lane + 32 * i] : 1.f;
+            const float x = __fmul_rn(my_u[i], q), e = __fmaf_rn(my_u[i], q, -x);
+            first[i] = x < my_p[i] || (x == my_p[i] && e < 0.f);
+        }
+        ok_first = nodes(first[0], first[1]);
+        if (!with) {
+            const unsigned key0 = (unsigned)(my_par[0] + 1) << 21 | (unsigned)(my_tok[0] + 1);
+            const unsigned key1 = (unsigned)(my_par[1] + 1) << 21 | (unsigned)(my_tok[1] + 1);
+            const unsigned below = (1u << lane) - 1u;
+            bool t0 = __match_any_sync(0xffffffffu, key0) & below;
+            bool t1 = __match_any_sync(0xffffffffu, key1) & below;
+            for (int i = 0; i < 32; ++i) t1 |= __shfl_sync(0xffffffffu, key0, i) == key1;
+            twin = nodes(t0, t1);
         }
         todo = children(0);
         if (rank == 0 && lane == 0) path[0] = 0;
@@ -193,74 +275,89 @@ __global__ void __launch_bounds__(kWarps * 32) tree_verify_kernel(const VerifyAr
     auto row_of = [&](const float *m, int64_t stride, int node) {
         return m + (int64_t)(span.row0 + node) * stride;
     };
-    // r at token x of this CTA's slice.
-    auto r_at = [&](const float *p, const float *q, int rej, int x) -> Pair {
-        if (!with) {
-            const int i = x - c0;
-            return {(s_gone[i >> 5] >> (i & 31)) & 1u ? 0.f : p[x], 0.f};
-        }
-        if (rej == 0) return {p[x], 0.f};
-        return residual(p[x], q[x], rej, s_zinv);
-    };
     int turn = 0, last_node = 0, last_rej = 0;
     bool have = false;  // the warp sums are those of (cur, nrej)
-    double whole = 0.0;
+    Pair whole = {0.f, 0.f};
     for (;;) {
         if (warp == 0) {
             // On to the next pass: a rejection's sum, or the last one.
             bool ask = false;
-            while (!ask && todo && mass > 0.0) {
-                const int i = __ffsll((long long)todo) - 1;
-                todo &= todo - 1;
-                const int tok = s_tok[i];
-                const double p = s_p[i], q = s_q[i], u = s_u[i];
-                bool ok;
-                double r = p;
-                if (with) {
-                    for (int k = 0; k < nrej; ++k) r = fmax(r / s_z[k] - q, 0.0);
-                    ok = u * q * mass < r;
+            uint64_t tried = 0;  // without draft: cur's children that were tried
+            while (todo && mass.h > 0.f) {
+                int i = __ffsll((long long)todo) - 1;  // the child that is accepted, or -1
+                if (nrej == 0) {
+                    if (!((ok_first >> i) & 1ull)) i = -1;
                 } else {
-                    // Gone already when an earlier sibling had the same token.
-                    const bool twin =
-                        (my_par[0] == cur && lane < i && my_tok[0] == tok) ||
-                        (my_par[1] == cur && lane + 32 < i && my_tok[1] == tok);
-                    if (__any_sync(0xffffffffu, twin)) r = 0.0;
-                    ok = u * mass < r;
+                    const float q = s_q[i];
+                    const Pair r = residual(s_p[i], q, nrej, s_zinv);
+                    const Pair need = times(times({s_u[i], 0.f}, {q, 0.f}), mass);
+                    if (!above(normal(r), need)) i = -1;
                 }
-                if (ok) {
-                    if (rank == 0 && lane == 0) path[count] = i;
-                    ++count;
-                    cur = i;
-                    nrej = 0;
-                    mass = 1.0;
-                    have = false;
-                    todo = children(i);
-                } else if (with) {
-                    if (lane == 0) {
-                        s_z[nrej] = mass;
-                        s_zinv[nrej] = reciprocal(mass);
-                    }
+                if (i < 0 && with) {  // rejected: Z of the next round is a pass's sum
+                    todo &= todo - 1;
+                    // The first round's Z is 1.
+                    if (nrej > 0 && lane == 0) s_zinv[nrej] = reciprocal(mass);
                     __syncwarp();
                     ++nrej;
                     ask = true;
-                } else {
-                    mass -= r;
+                    break;
                 }
+                if (i < 0) {
+                    // The first child is rejected: the others at once, Z before each from
+                    // the running sum of the probabilities before it.
+                    Pair sum[2];
+                    float own[2];
+                    for (int k = 0; k < 2; ++k) {
+                        const bool in = (todo >> (lane + 32 * k)) & 1ull;
+                        const bool gone = (twin >> (lane + 32 * k)) & 1ull;
+                        own[k] = in && !gone ? my_p[k] : 0.f;
+                        sum[k] = {own[k], 0.f};
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const Pair u = {__shfl_up_sync(0xffffffffu, sum[k].h, o),
+                                            __shfl_up_sync(0xffffffffu, sum[k].l, o)};
+                            if (lane >= o) add_to(sum[k], u);
+                        }
+                    }
+                    add_to(sum[1], {__shfl_sync(0xffffffffu, sum[0].h, 31),
+                                    __shfl_sync(0xffffffffu, sum[0].l, 31)});
+                    bool ok[2], may[2];
+                    for (int k = 0; k < 2; ++k) {
+                        Pair z = {1.f, 0.f};
+                        add_to(z, {-sum[k].h, -sum[k].l});
+                        add_to(z, {own[k], 0.f});
+                        z = normal(z);
+                        may[k] = ((todo >> (lane + 32 * k)) & 1ull) && z.h > 0.f;
+                        ok[k] = may[k] && above({own[k], 0.f}, times({my_u[k], 0.f}, z));
+                    }
+                    const uint64_t hit = nodes(ok[0], ok[1]);
+                    if (!hit) {
+                        tried = nodes(may[0], may[1]);
+                        break;
+                    }
+                    i = __ffsll((long long)hit) - 1;
+                }
+                if (rank == 0 && lane == 0) path[count] = i;
+                ++count;
+                cur = i;
+                nrej = 0;
+                mass = {1.f, 0.f};
+                have = false;
+                todo = children(i);
             }
-            const bool last = !ask;
-            if (last && !with) {  // every child of cur was tried and rejected
+            // The last pass: nothing to try after it.
+            const bool last = !ask || !todo;
+            if (last && !with) {
                 for (int i = 0; i < 2; ++i) {
                     const int t = my_tok[i] - c0;
-                    // Only those tried: mass may have run out before the others.
-                    const bool tried = my_par[i] == cur && !((todo >> (lane + 32 * i)) & 1ull);
-                    if (tried && my_tok[i] >= c0 && my_tok[i] < c1)
+                    if (((tried >> (lane + 32 * i)) & 1ull) && my_tok[i] >= c0 && my_tok[i] < c1)
                         atomicOr(&s_gone[t >> 5], 1u << (t & 31));
                 }
             }
             if (lane == 0) {
                 s_cmd[0] = cur;
                 s_cmd[1] = nrej;
-                s_cmd[2] = (last ? 1 : 0) | (last && have ? 2 : 0);
+                s_cmd[2] = (last ? 1 : 0) | (!ask && have ? 2 : 0);
             }
         }
         __syncthreads();
@@ -270,40 +367,69 @@ __global__ void __launch_bounds__(kWarps * 32) tree_verify_kernel(const VerifyAr
         if (!(flags & 2)) {
             const float *p = row_of(a.target, a.target_stride, node);
             const float *q = with ? row_of(a.draft, a.draft_stride, node) : p;
-            Pair acc[4] = {};
-            int x = v0 + lane;
-            for (; x + 96 < v1; x += 128) {
-                Pair r[4];
-                if (with && rej > 0) {
-                    float pv[4], qv[4];
+            // Every load of a step is issued before the first is used; what lies past the
+            // warp's part counts as p = q = 0, which leaves r = 0.
+            Pair acc[2] = {};
+            if (with && rej > 1 && a.cached) {
+                // A thread's tokens are the same in every pass.
+                for (int i = v0 + lane - c0; i < v1 - c0; i += 32) {
+                    const Pair r = next_residual({s_rh[i], s_rl[i]}, s_qc[i], s_zinv[rej - 1]);
+                    s_rh[i] = r.h;
+                    s_rl[i] = r.l;
+                    add_to(acc[0], r);
+                }
+            } else if (with && rej > 0) {
+                constexpr int U = kU;
+                for (int x = v0 + lane; x < v1; x += 32 * U) {
+                    float pv[U], qv[U];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        pv[k] = p[x + 32 * k];
-                        qv[k] = q[x + 32 * k];
+                    for (int k = 0; k < U; ++k) {
+                        pv[k] = x + 32 * k < v1 ? p[x + 32 * k] : 0.f;
+                        qv[k] = x + 32 * k < v1 ? q[x + 32 * k] : 0.f;
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) r[k] = residual(pv[k], qv[k], rej, s_zinv);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) r[k] = r_at(p, q, rej, x + 32 * k);
+                    for (int k = 0; k < U; ++k) {
+                        Pair r = first_residual(pv[k], qv[k]);
+                        if (a.cached) {
+                            if (x + 32 * k < v1) {
+                                s_rh[x + 32 * k - c0] = r.h;
+                                s_rl[x + 32 * k - c0] = r.l;
+                                s_qc[x + 32 * k - c0] = qv[k];
+                            }
+                        } else if (rej > 1) {
+                            r = residual(pv[k], qv[k], rej, s_zinv);
+                        }
+                        add_to(acc[k & 1], r);
+                    }
                 }
+            } else {
+                constexpr int U = 2 * kU;
+                for (int x = v0 + lane; x < v1; x += 32 * U) {
+                    float pv[U];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) add_to(acc[k], r[k]);
+                    for (int k = 0; k < U; ++k) pv[k] = x + 32 * k < v1 ? p[x + 32 * k] : 0.f;
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        if (!with && x + 32 * k < v1) {
+                            const int i = x + 32 * k - c0;
+                            if ((s_gone[i >> 5] >> (i & 31)) & 1u) pv[k] = 0.f;
+                        }
+                        add_to(acc[k & 1], {pv[k], 0.f});
+                    }
+                }
             }
-            for (; x < v1; x += 32) add_to(acc[0], r_at(p, q, rej, x));
-            double t = (value(acc[0]) + value(acc[1])) + (value(acc[2]) + value(acc[3]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            add_to(acc[0], acc[1]);
+            const Pair t = warp_sum(acc[0]);
             if (lane == 0) s_tot[warp] = t;
             __syncthreads();
             if (warp == 0) {
-                // This CTA's sum, in warp order, to every CTA of the cluster.
-                double sum = 0.0;
-                for (int w = 0; w < kWarps; ++w) sum += s_tot[w];
+                // This CTA's sum to every CTA of the cluster.
+                const Pair sum =
+                    warp_sum<kWarps>(lane < kWarps ? s_tot[lane] : Pair{0.f, 0.f});
                 if (lane < C)
-                    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
                                      peer_addr(&s_cta[turn][rank], lane)),
-                                 "d"(sum)
+                                 "f"(sum.h), "f"(sum.l)
                                  : "memory");
             }
             __syncwarp();
@@ -312,8 +438,10 @@ __global__ void __launch_bounds__(kWarps * 32) tree_verify_kernel(const VerifyAr
             else
                 __syncthreads();
             if (warp == 0) {
-                whole = 0.0;
-                for (int c = 0; c < C; ++c) whole += s_cta[turn][c];
+                whole = normal(warp_sum<kMaxCluster>(lane < C ? s_cta[turn][lane]
+                                                              : Pair{0.f, 0.f}));
+                whole.h = __shfl_sync(0xffffffffu, whole.h, 0);
+                whole.l = __shfl_sync(0xffffffffu, whole.l, 0);
                 mass = whole;
                 have = true;
             }
@@ -327,89 +455,103 @@ __global__ void __launch_bounds__(kWarps * 32) tree_verify_kernel(const VerifyAr
             for (int i = count + lane; i < a.t.max_tree; i += 32) path[i] = -1;
             if (lane == 0) a.num_accepted[s] = count;
         }
-        // The CTA, and there the warp, that holds the goal; where rounding leaves none
-        // (or sample_u >= 1) the last with weight, and the last token with weight in it.
-        const double *cta = s_cta[turn ^ 1];
-        double goal = (double)a.sample_u[s] * whole, before = 0.0;
-        int pick = -1;
-        for (int c = 0; c < C && pick < 0; ++c) {
-            if (before + cta[c] > goal)
-                pick = c;
-            else
-                before += cta[c];
-        }
-        if (pick < 0) {
-            goal = INFINITY;
-            for (int c = 0; c < C; ++c)
-                if (cta[c] > 0.0) pick = c;
-        }
+        // The CTA, and there the warp, that holds the goal u * whole; where rounding leaves
+        // none (or sample_u >= 1) the last with weight, to the last token with weight.
+        const float u = a.sample_u[s];
+        Pair goal = times({u, 0.f}, whole);
+        bool found;
+        const int pick = locate<kMaxCluster>(
+            lane < C ? s_cta[turn ^ 1][lane] : Pair{0.f, 0.f}, goal, found);
         int w_pick = pick < 0 ? -2 : -1;
         if (pick == rank) {
-            for (int w = 0; w < kWarps && w_pick < 0; ++w) {
-                if (before + s_tot[w] > goal)
-                    w_pick = w;
-                else
-                    before += s_tot[w];
-            }
-            if (w_pick < 0) {
-                goal = INFINITY;
-                for (int w = 0; w < kWarps; ++w)
-                    if (s_tot[w] > 0.0) w_pick = w;
-            }
+            if (!found) goal = {INFINITY, 0.f};
+            w_pick = locate<kWarps>(lane < kWarps ? s_tot[lane] : Pair{0.f, 0.f}, goal, found);
+            if (!found) goal = {INFINITY, 0.f};
         }
         if (lane == 0) {
-            s_goal = goal - before;
+            s_goal = goal;
             s_pick = w_pick;
         }
     }
     __syncthreads();
     const float *p = row_of(a.target, a.target_stride, last_node);
-    if (s_pick != -2) {
-        if (warp != s_pick) return;
+    if (s_pick == -1) return;  // another CTA draws
+    if (s_pick >= 0) {
+        // The drawn warp's part again, shared by all warps; then the part of that which
+        // holds the goal, 256 tokens at a time, eight consecutive ones per lane.
         const float *q = with ? row_of(a.draft, a.draft_stride, last_node) : p;
-        double goal = s_goal;
-        // 32 contiguous shares of the warp's tokens, one per lane, then the share that
-        // holds the goal, 32 tokens at a time.
-        const int per = (v1 - v0 + 31) / 32;
-        const int x0 = min(v1, v0 + lane * per), x1 = min(v1, x0 + per);
-        Pair acc = {0.f, 0.f};
-        for (int x = x0; x < x1; ++x) add_to(acc, r_at(p, q, last_rej, x));
-        const double mine = value(acc);
-        double incl = mine;
+        const int w0 = min(c1, c0 + s_pick * a.warp_slice), w1 = min(c1, w0 + a.warp_slice);
+        // (A part of at most 512 tokens is scanned by its own warp at once.)
+        const bool shared = w1 - w0 > 512;
+        if (!shared && warp != s_pick) return;
+        const int sub = ((w1 - w0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+        const int y0 = shared ? min(w1, w0 + warp * sub) : w0;
+        const int y1 = shared ? min(w1, y0 + sub) : w1;
+        Pair goal = s_goal, acc = {0.f, 0.f};
+        // r of eight tokens x0, x0 + step, ..: their p and q are loaded first.
+        auto eight = [&](int x0, int step, int end, Pair (&r)[8]) {
+            if (with && last_rej > 0 && a.cached) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
+                for (int k = 0; k < 8; ++k) {
+                    const int x = x0 + k * step, i = x - c0;
+                    r[k] = x < end ? Pair{s_rh[i], s_rl[i]} : Pair{0.f, 0.f};
+                }
+                return;
+            }
+            float pv[8], qv[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int x = x0 + k * step;
+                pv[k] = x < end ? p[x] : 0.f;
+                qv[k] = with && last_rej > 0 && x < end ? q[x] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int x = x0 + k * step, i = x - c0;
+                if (!with && x < end && ((s_gone[i >> 5] >> (i & 31)) & 1u)) pv[k] = 0.f;
+                r[k] = with && last_rej ? residual(pv[k], qv[k], last_rej, s_zinv)
+                                        : Pair{pv[k], 0.f};
+            }
+        };
+        Pair r[8];
+        bool found;
+        if (shared) {
+            for (int x = y0 + lane; x < y1; x += 256) {
+                eight(x, 32, y1, r);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) add_to(acc, r[k]);
+            }
+            acc = warp_sum(acc);
+            if (lane == 0) s_sub[warp] = acc;
+            __syncthreads();
+            const int at =
+                locate<kWarps>(lane < kWarps ? s_sub[lane] : Pair{0.f, 0.f}, goal, found);
+            if (warp != max(at, 0)) return;
+            if (!found) goal = {INFINITY, 0.f};
         }
-        const unsigned over = __ballot_sync(0xffffffffu, mine > 0.0 && incl > goal);
-        const unsigned some = __ballot_sync(0xffffffffu, mine > 0.0);
-        int at = 0;
-        if (over) {
-            at = __ffs((int)over) - 1;
-            goal -= __shfl_sync(0xffffffffu, incl - mine, at);
-        } else {
-            at = some ? 31 - __clz((int)some) : 0;
-            goal = INFINITY;
-        }
-        const int y0 = min(v1, v0 + at * per), y1 = min(v1, y0 + per);
         int last = y0;
-        for (int b = y0; b < y1; b += 32) {
-            const int x = b + lane;
-            const double r = x < y1 ? value(r_at(p, q, last_rej, x)) : 0.0;
-            double c = r;
+        for (int b = y0; b < y1; b += 256) {
+            const int x = b + 8 * lane;
+            eight(x, 1, y1, r);
+            Pair mine = {0.f, 0.f};
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double u = __shfl_up_sync(0xffffffffu, c, o);
-                if (lane >= o) c += u;
+            for (int k = 0; k < 8; ++k) add_to(mine, r[k]);
+            const int hit = locate(mine, goal, found);
+            if (hit < 0) continue;
+            // In that lane: the first token past the goal, else its last with weight.
+            int tok = x;
+            bool done = false;
+            Pair run = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                add_to(run, r[k]);
+                if (!done && r[k].h > 0.f) {
+                    tok = x + k;
+                    done = found && above(normal(run), goal);
+                }
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, r > 0.0 && c > goal);
-            const unsigned any = __ballot_sync(0xffffffffu, r > 0.0);
-            if (hit) {
-                last = b + __ffs((int)hit) - 1;
-                break;
-            }
-            if (any) last = b + 31 - __clz((int)any);
-            goal -= __shfl_sync(0xffffffffu, c, 31);
+            last = __shfl_sync(0xffffffffu, tok, hit);
+            if (found) break;
         }
         if (lane == 0) a.next[s] = last;
         return;
@@ -462,10 +604,6 @@ cudaError_t take_error_tree_verify(unsigned *bits) {
     return e;
 }
 
-#ifndef PA_VERIFY_CTAS
-#define PA_VERIFY_CTAS 8
-#endif
-
 cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t *next_tokens,
                                const float *target, int64_t target_stride, const float *draft,
                                int64_t draft_stride, const int32_t *tokens, const TreeGeom &t,
@@ -484,12 +622,14 @@ cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t
     a.sample_u = sample_u;
     a.t = t;
     a.vocab = vocab;
-    // CTAs per sequence: a few per SM over the batch, each with at least four tokens
-    // per thread, and slices whose bit sets fit the default shared memory.
+    // CTAs per sequence: all of the batch resident at once (two per SM; with draft
+    // probabilities a quarter more, since sequences end after very different numbers of
+    // passes), each with at least 2048 tokens, and slices whose bit sets fit 32 KB.
+    const int sms = device_sm_count();
+    const long long room = draft ? 5LL * sms / 2 : 2LL * sms;
     int c = 1;
-    while (c < kMaxCluster && ((long long)c * t.num_seqs < PA_VERIFY_CTAS * device_sm_count() ||
-                               vocab / c > (1 << 18)) &&
-           vocab / (2 * c) >= kWarps * 32 * 4)
+    while (c < kMaxCluster && (2LL * c * t.num_seqs <= room || vocab / c > (1 << 18)) &&
+           vocab / (2 * c) >= 2048)
         c *= 2;
     a.cluster = c;
     auto up32 = [](int x) { return (x + 31) / 32 * 32; };
@@ -498,7 +638,16 @@ cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(t.num_seqs * c));
     cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = draft ? 0 : (size_t)a.cta_slice / 8;
+    // r and q in shared memory where two CTAs of that size share an SM, or one is enough
+    // for the batch; else a later rejection starts again from p and q.
+    const size_t keep = (size_t)a.cta_slice * 12;
+    a.cached = draft && t.max_tree > 2 &&
+               (keep <= 100 << 10 || (keep <= 200 << 10 && (long long)c * t.num_seqs <= sms));
+    cfg.dynamicSmemBytes = draft ? (a.cached ? keep : 0) : (size_t)a.cta_slice / 8;
+    if (a.cached) {
+        const cudaError_t e = ensure_smem<tree_verify_kernel>(keep);
+        if (e != cudaSuccess) return e;
+    }
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
