@@ -41,7 +41,7 @@ namespace {
 struct MapEntry {
     const void *pool;
     KvGeom g;
-    int box_rows, fp8;
+    int box_rows, fp8;  // fp8: 0 bf16 rows, 1 FP8 rows, 2 bf16 groups of 8 rows
     CUtensorMap map;
 };
 constexpr int kMapCache = 16;
@@ -94,6 +94,25 @@ bool encode_kv_map(CUtensorMap *map, const void *kv_cache, const KvGeom &g, int 
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
     keep_map(*map, kv_cache, g, box_rows, 0);
+    return true;
+}
+
+bool encode_kv_map_groups(CUtensorMap *map, const void *kv_cache, const KvGeom &g) {
+    if (cached_map(map, kv_cache, g, g.block_size, 2)) return true;
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t rows =
+        (cuuint64_t)g.num_blocks * 2u * (cuuint64_t)g.num_kv_heads * (cuuint64_t)g.block_size;
+    const cuuint64_t row_bytes = (cuuint64_t)g.head_size * 2u;
+    cuuint64_t dims[4] = {64u, 8u, (cuuint64_t)g.head_size / 64u, rows / 8u};
+    cuuint64_t strides[3] = {row_bytes, 128u, 8u * row_bytes};
+    cuuint32_t box[4] = {64u, 8u, (cuuint32_t)g.head_size / 64u, (cuuint32_t)g.block_size / 8u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv_cache), dims,
+                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return false;
+    keep_map(*map, kv_cache, g, g.block_size, 2);
     return true;
 }
 

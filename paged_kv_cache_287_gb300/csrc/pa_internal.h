@@ -56,6 +56,11 @@ bool encode_kv_map(CUtensorMap *map, const void *kv_cache, const KvGeom &g, int 
 // The same over an FP8 pool (rows of head_size bytes), box = 128 bytes x box_rows.
 bool encode_kv_map_fp8(CUtensorMap *map, const void *kv_cache, const KvGeom &g, int box_rows);
 
+// Encode a 4-D TMA map over the bf16 pool: 64 elements x 8 rows x (head_size / 64)
+// panels x groups of 8 rows, box = one block's rows of one side and head, 128-byte
+// swizzle: a box lands as [group of 8 rows][panel][row][64 elements].
+bool encode_kv_map_groups(CUtensorMap *map, const void *kv_cache, const KvGeom &g);
+
 int device_sm_count();
 
 // Inputs of the device-side split of a mixed launch's SMs (pa_plan.cuh).

@@ -39,9 +39,9 @@ namespace {
 __device__ unsigned g_err_tree_attention;
 
 constexpr int kRows = 128;  // query rows per tile (the MMA's M)
-constexpr int kKeys = 128;  // keys per K/V tile
+constexpr int kKeys = 64;   // keys per K/V tile
 constexpr float kSlack = 8.0f;
-constexpr uint32_t kCols = 256, kColO = 128;  // tensor memory: S / P, then O
+constexpr uint32_t kCols = 256, kColO = 128;  // tensor memory: two S / P tiles, then O
 
 struct TreeAttnArgs {
     __nv_bfloat16 *out;
@@ -66,14 +66,36 @@ struct TreeAttnArgs {
 template <int D, bool KV8>
 struct Tlay {
     static constexpr int kPanels = D / 64;
-    static constexpr int kPanel = kRows * 128;      // 64 dims of 128 rows or keys
-    static constexpr int kTile = kPanels * kPanel;  // a Q, K or V tile
-    static constexpr int kSlots = D == 64 ? 2 : 1;  // K (and V) tiles held
-    static constexpr int kOperands = (1 + 2 * kSlots) * kTile;
-    static constexpr size_t kSmem = 1024 + (size_t)kOperands;
+    static constexpr int kQPanel = kRows * 128;  // 64 dims of 128 rows
+    static constexpr int kQ = kPanels * kQPanel;
+    static constexpr int kTile = kPanels * kKeys * 128;  // a K or V tile
+    // Where 8 keys x 64 dims (1 KB, swizzled) of panel p, keys 8 g ..: kGroup g + kPanel p.
+    // A bf16 block lands in one copy with its panels side by side; an FP8 tile's f16
+    // values go panel by panel, the upper one over its codes.
+    static constexpr int kGroup = KV8 ? 1024 : 1024 * kPanels;
+    static constexpr int kPanel = KV8 ? kKeys * 128 : 1024;
+    static constexpr int kSlots = D == 64 ? 8 : 5;  // tiles in the ring
     static constexpr int kConv = KV8 ? 2 : 0;  // converting warps
     static constexpr int kThreads = (6 + kConv) * 32;
+    static constexpr int kOperands = kQ + kSlots * kTile;
+    static constexpr size_t kSmem = (size_t)kOperands + 512;  // + barriers
 };
+
+// Order of the tiles in the ring: K0 K1 V0 K2 V1 K3 V2 ..., the order in which the
+// products (scores one tile ahead) release them.
+__device__ __forceinline__ int ring_k(int i) { return i ? 2 * i - 1 : 0; }
+__device__ __forceinline__ int ring_v(int i) { return 2 * i + 2; }
+
+// What follows the operands in shared memory.
+struct Sync {
+    uint64_t full[8], empty[8], staged[8];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full, o_free, sane, drain;
+    uint32_t tmem;
+    int start[2], bad[2];
+    int part[10];
+};
+static_assert(sizeof(Sync) <= 512, "the barriers' room");
 
 // Sequence s as this kernel sees it: no tiles where its data break the bounds.
 struct SeqInfo {
@@ -149,16 +171,15 @@ template <int D, bool KV8>
 __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     tree_attention_kernel(const __grid_constant__ CUtensorMap kv_map, const TreeAttnArgs a) {
     using L = Tlay<D, KV8>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<size_t>(smem_raw) + 1023) & ~static_cast<size_t>(1023));
-    uint8_t *sQ = smem, *sK = smem + L::kTile, *sV = sK + L::kSlots * L::kTile;
-    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], k_staged[2], v_staged[2];
-    __shared__ uint64_t s_full, p_lo, p_hi, pv_done, q_full, o_free, sane, drain;
-    __shared__ uint32_t tmem_slot;
-    __shared__ int s_part[L::kThreads / 32];
-    __shared__ int s_start[2];
-    __shared__ int s_bad[2];
+    // No static shared memory: the dynamic part then starts at the (1024-byte aligned)
+    // beginning, and two CTAs' 112 KB of operands fit one SM.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *sQ = smem, *ring = smem + L::kQ;
+    Sync &sy = *reinterpret_cast<Sync *>(smem + L::kOperands);
+    if (smem_u32(smem) & 1023u) {  // the same for every thread: the swizzle needs it
+        if (threadIdx.x == 0) atomicOr(&g_err_tree_attention, kErrPrecondition);
+        return;
+    }
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int worker = blockIdx.x / a.row_groups, rg = blockIdx.x - worker * a.row_groups;
@@ -179,13 +200,13 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             const int u = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += u;
         }
-        if (lane == 31) s_part[warp] = incl;
-        if (tid == 0) s_start[0] = -1;
+        if (lane == 31) sy.part[warp] = incl;
+        if (tid == 0) sy.start[0] = -1;
         __syncthreads();
         int before = 0, total = 0;
         for (int w = 0; w < L::kThreads / 32; ++w) {
-            if (w < warp) before += s_part[w];
-            total += s_part[w];
+            if (w < warp) before += sy.part[w];
+            total += sy.part[w];
         }
         const long long T = (long long)total * Hkv;
         const long long We = a.workers < T ? a.workers : (T > 0 ? T : 1);
@@ -201,40 +222,38 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 if (t_begin < (long long)Hkv * (pre + nt)) break;
                 pre += nt;
             }
-            s_start[0] = s;
-            s_start[1] = pre;
+            sy.start[0] = s;
+            sy.start[1] = pre;
         }
     }
     if (tid == 0) {
         prefetch_tensormap(&kv_map);
         for (int i = 0; i < L::kSlots; ++i) {
-            mbar_init(&k_full[i], KV8 ? L::kConv : 1);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], KV8 ? L::kConv : 1);
-            mbar_init(&v_empty[i], 1);
-            mbar_init(&k_staged[i], 1);
-            mbar_init(&v_staged[i], 1);
+            mbar_init(&sy.full[i], KV8 ? L::kConv : 1);
+            mbar_init(&sy.empty[i], 1);
+            mbar_init(&sy.staged[i], 1);
         }
-        mbar_init(&s_full, 1);
-        mbar_init(&p_lo, 4);
-        mbar_init(&p_hi, 4);
-        mbar_init(&pv_done, 1);
-        mbar_init(&q_full, 4);
-        mbar_init(&o_free, 4);
-        mbar_init(&sane, 4);
-        mbar_init(&drain, 1);
-        s_bad[0] = s_bad[1] = -1;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sy.s_full[i], 1);
+            mbar_init(&sy.p_full[i], 4);
+            mbar_init(&sy.pv_done[i], 1);
+        }
+        mbar_init(&sy.q_full, 4);
+        mbar_init(&sy.o_free, 4);
+        mbar_init(&sy.sane, 4);
+        mbar_init(&sy.drain, 1);
+        sy.bad[0] = sy.bad[1] = -1;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(&tmem_slot, kCols);
+        tmem_alloc(&sy.tmem, kCols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    const int seq0 = s_start[0], pre0 = s_start[1];
+    const uint32_t tmem = sy.tmem;
+    const int seq0 = sy.start[0], pre0 = sy.start[1];
     const bool work = seq0 >= 0;
     if (tid == 0 && rg == 0) {
         int4 st = make_int4(-1, 0, 0, 0);
@@ -251,62 +270,86 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         // ------------------------------------------------------------ TMA producer
         Walk w;
         w.start(a, seq0, pre0, t_begin, t_end);
-        const int bs = a.block_size, box_rows = bs >= 16 ? 16 : bs, nbox = kKeys / box_rows;
+        const int bs = a.block_size, nbox = kKeys / bs;  // a box per block
         const int v_off = Hkv * bs;
         const uint64_t policy = policy_evict_first();
-        auto load = [&](uint8_t *dst, uint64_t *bar, int row) {
-            if constexpr (KV8) {
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(kKeys * 128));
-                __syncwarp();
-                if (lane < nbox)
-                    tma_load_2d_hint(dst + L::kTile / 2 + lane * box_rows * 128, &kv_map, bar, 0,
-                                     row, policy);
-            } else {
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
-                __syncwarp();
-                if (lane < nbox) {
-#pragma unroll
-                    for (int p = 0; p < L::kPanels; ++p)
-                        tma_load_2d_hint(dst + p * L::kPanel + lane * box_rows * 128, &kv_map, bar,
-                                         64 * p, row, policy);
+        // Tile u of the ring: wait until its slot is free, then copy the boxes.
+        auto load = [&](int u, int row) -> bool {
+            const int st = u % L::kSlots;
+            if (u >= L::kSlots &&
+                !all_wait(&sy.empty[st], (uint32_t)(u / L::kSlots - 1) & 1u))
+                return false;
+            uint8_t *dst = ring + st * L::kTile;
+            uint64_t *bar = KV8 ? &sy.staged[st] : &sy.full[st];
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, KV8 ? (uint32_t)(kKeys * 128) : (uint32_t)L::kTile);
+            __syncwarp();
+            if (lane < nbox) {
+                if constexpr (KV8) {
+                    tma_load_2d_hint(dst + L::kTile / 2 + lane * bs * 128, &kv_map, bar, 0, row,
+                                     policy);
+                } else {
+                    // The pool's rows in groups of 8 (blocks are whole groups).
+                    tma_load_4d_hint(dst + lane * (bs / 8) * L::kGroup, &kv_map, bar, row >> 3,
+                                     policy);
                 }
             }
+            return true;
         };
-        int it = 0, k_issued = 0, v_issued = 0;
-        bool ok = true;
-        while (ok && w.next(a, rg)) {
-            const int32_t *bt = a.block_tables + (size_t)w.s * a.max_blocks;
-            for (int j = w.j0; j < w.j1; ++j, ++it) {
-                // This lane's box: a TMA row of the pool, wholly outside the map (zeros,
-                // nothing read) past the sequence or for a bad block id.
-                const int tok = j * kKeys + lane * box_rows;
-                int row = -(1 << 30);
-                if (lane < nbox && tok < w.cur.len) {
-                    const int blk = bt[tok / bs];
-                    if (blk >= 0 && blk < a.num_blocks)
-                        row = ((blk * 2) * Hkv + w.h) * bs + tok % bs;
-                    else
-                        atomicOr(&g_err_tree_attention, kErrOob);
-                }
-                const int st = it % L::kSlots;
-                const uint32_t par = (uint32_t)(it / L::kSlots - 1) & 1u;
-                if (it >= L::kSlots && !(ok = all_wait(&k_empty[st], par))) break;
-                load(sK + st * L::kTile, KV8 ? &k_staged[st] : &k_full[st], row);
-                ++k_issued;
-                if (it >= L::kSlots && !(ok = all_wait(&v_empty[st], par))) break;
-                load(sV + st * L::kTile, KV8 ? &v_staged[st] : &v_full[st],
-                     row < -(1 << 29) ? row : row + v_off);
-                ++v_issued;
+        // This lane's box of V where its box of K is at TMA row r.
+        auto v_row = [&](int r) { return r < -(1 << 29) ? r : r + v_off; };
+        // This lane's box of the next tile, one tile ahead of the copies: the table entry
+        // is on its way while the tile before it is copied.
+        int seg_j = 0, seg_j1 = 0, blk = 0, head = 0;
+        const int32_t *bt = nullptr;
+        auto fetch = [&]() -> bool {
+            if (seg_j == seg_j1) {
+                if (!w.next(a, rg)) return false;
+                seg_j = w.j0;
+                seg_j1 = w.j1;
+                bt = a.block_tables + (size_t)w.s * a.max_blocks;
             }
+            const int tok = seg_j * kKeys + lane * bs;
+            blk = -1;
+            head = -1;  // no box: outside the tile or past the sequence
+            if (lane < nbox && tok < w.cur.len) {
+                blk = bt[tok / bs];
+                head = w.h;
+            }
+            ++seg_j;
+            return true;
+        };
+        // The fetched box's TMA row, wholly outside the map (zeros, nothing read) for no box
+        // or a bad block id.
+        auto row_of = [&]() {
+            if (head < 0) return -(1 << 30);
+            if (blk < 0 || blk >= a.num_blocks) {
+                atomicOr(&g_err_tree_attention, kErrOob);
+                return -(1 << 30);
+            }
+            return ((blk * 2) * Hkv + head) * bs;
+        };
+        int it = 0, prev = 0, last_u = -1;
+        bool ok = true, more = fetch();
+        for (; ok && more; ++it) {
+            const int row = row_of();
+            more = fetch();
+            if (!(ok = load(ring_k(it), row))) break;
+            last_u = ring_k(it);
+            if (it > 0) {
+                if (!(ok = load(ring_v(it - 1), v_row(prev)))) break;
+                last_u = ring_v(it - 1);
+            }
+            prev = row;
         }
+        if (ok && it > 0 && (ok = load(ring_v(it - 1), v_row(prev)))) last_u = ring_v(it - 1);
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
-        // Never leave with copies in flight into this CTA's shared memory.
-        for (int i = max(0, k_issued - L::kSlots); i < k_issued; ++i)
-            mbar_wait_bounded(KV8 ? &k_staged[i % L::kSlots] : &k_full[i % L::kSlots],
-                              (uint32_t)(i / L::kSlots) & 1u);
-        for (int i = max(0, v_issued - L::kSlots); i < v_issued; ++i)
-            mbar_wait_bounded(KV8 ? &v_staged[i % L::kSlots] : &v_full[i % L::kSlots],
-                              (uint32_t)(i / L::kSlots) & 1u);
+        // Never leave with copies in flight into this CTA's shared memory.  (The last V
+        // tile's place follows one that is never used.)
+        for (int u = max(0, last_u - L::kSlots + 1); u <= last_u; ++u)
+            if (!(ok && u == last_u - 1 && it > 0))
+                mbar_wait_bounded(KV8 ? &sy.staged[u % L::kSlots] : &sy.full[u % L::kSlots],
+                                  (uint32_t)(u / L::kSlots) & 1u);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         Walk w;
@@ -315,62 +358,71 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             KV8 ? tc_idesc_f16(kRows, kKeys, 0) : tc_idesc_bf16(kRows, kKeys, 0);
         const uint32_t idesc_pv = KV8 ? tc_idesc_f16(kRows, D, 1) : tc_idesc_bf16(kRows, D, 1);
         const uint64_t q_desc = tc_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t k_desc = tc_desc_sw128(smem_u32(sK), 16, 1024);
-        const uint64_t v_desc = tc_desc_sw128(smem_u32(sV), L::kPanel, 1024);
+        const uint64_t k_desc = tc_desc_sw128(smem_u32(ring), 16, L::kGroup);
+        const uint64_t v_desc = tc_desc_sw128(smem_u32(ring), L::kPanel, L::kGroup);
+        // S_i = Q.K^T into buffer i & 1, whose last P (tile i - 2) must be used up; a
+        // segment's first tile waits for its queries.
+        auto scores = [&](int i, bool first, int sg) -> bool {
+            const int u = ring_k(i), st = u % L::kSlots, b = i & 1;
+            if (!all_wait(&sy.full[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
+            if (first && !all_wait(&sy.q_full, (uint32_t)sg & 1u)) return false;
+            if (i >= 2 && !all_wait(&sy.pv_done[b], (uint32_t)(i / 2 - 1) & 1u)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t kd = k_desc + (uint64_t)((st * L::kTile) >> 4);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t qo = ((k >> 2) * L::kQPanel + (k & 3) * 32) >> 4;
+                    const uint32_t ko = ((k >> 2) * L::kPanel + (k & 3) * 32) >> 4;
+                    tc_mma_ss(tmem + b * kKeys, q_desc + qo, kd + ko, idesc_s, k > 0 ? 1u : 0u);
+                }
+                tc_commit(&sy.s_full[b]);
+                tc_commit(&sy.empty[st]);
+            }
+            __syncwarp();
+            return true;
+        };
+        // O += P_i.V, over O's old contents for a segment's first tile (once the epilogue
+        // of the segment before has read them).
+        auto output = [&](int i, bool first, int sg) -> bool {
+            const int u = ring_v(i), st = u % L::kSlots, b = i & 1;
+            if (!all_wait(&sy.full[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
+            if (first && sg > 0 && !all_wait(&sy.o_free, (uint32_t)(sg - 1) & 1u)) return false;
+            if (!all_wait(&sy.p_full[b], (uint32_t)(i / 2) & 1u)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t vd = v_desc + (uint64_t)((st * L::kTile) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    tc_mma_ts(tmem + kColO, tmem + b * kKeys + kk * 8,
+                              vd + (uint64_t)((kk * 2 * L::kGroup) >> 4), idesc_pv,
+                              (!first || kk > 0) ? 1u : 0u);
+                tc_commit(&sy.pv_done[b]);
+                tc_commit(&sy.empty[st]);
+            }
+            __syncwarp();
+            return true;
+        };
+        // The scores run one tile ahead of the outputs; at a segment's end the output goes
+        // first (the next scores wait for the next queries).
         int it = 0, seg = 0;
-        bool ok = true;
+        bool ok = true, out_first = false;  // is the waiting output a segment's first?
         while (ok && w.next(a, rg)) {
-            for (int j = w.j0; j < w.j1; ++j, ++it) {
-                const int st = it % L::kSlots;
-                const uint32_t par = (uint32_t)(it / L::kSlots) & 1u;
-                const uint32_t prev = (uint32_t)(it - 1) & 1u;
-                // S = Q.K^T, over the previous tile's P: its product must be done.
-                if (!(ok = all_wait(&k_full[st], par))) break;
-                if (j == w.j0 && !(ok = all_wait(&q_full, (uint32_t)seg & 1u))) break;
-                if (it > 0 && !(ok = all_wait(&pv_done, prev))) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t kd = k_desc + (uint64_t)((st * L::kTile) >> 4);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k >> 2) * L::kPanel + (k & 3) * 32) >> 4;
-                        tc_mma_ss(tmem, q_desc + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
-                    }
-                    tc_commit(&s_full);
-                    tc_commit(&k_empty[st]);
-                }
-                __syncwarp();
-                // O += P.V, the first half while the softmax works on keys 64-127.
-                if (!(ok = all_wait(&v_full[st], par))) break;
-                if (j == w.j0 && seg > 0 && !(ok = all_wait(&o_free, (uint32_t)(seg - 1) & 1u)))
-                    break;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!(ok = all_wait(half ? &p_hi : &p_lo, (uint32_t)it & 1u))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t vd = v_desc + (uint64_t)((st * L::kTile) >> 4);
-#pragma unroll
-                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            tc_mma_ts(tmem + kColO, tmem + kk * 8,
-                                      vd + (uint64_t)((kk * 16 * 128) >> 4), idesc_pv,
-                                      (j > w.j0 || kk > 0) ? 1u : 0u);
-                        if (half) {
-                            tc_commit(&pv_done);
-                            tc_commit(&v_empty[st]);
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
+            for (int j = w.j0; ok && j < w.j1; ++j, ++it) {
+                const bool first = j == w.j0;
+                if (first && it > 0) ok = output(it - 1, out_first, seg - 1);
+                ok = ok && scores(it, first, seg);
+                if (!first) ok = ok && output(it - 1, out_first, seg);
+                out_first = first;
             }
             ++seg;
         }
+        if (ok && it > 0) ok = output(it - 1, out_first, seg - 1);
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
         // Every product must be done before tensor memory is freed.
-        if (lane == 0) tc_commit(&drain);
+        if (lane == 0) tc_commit(&sy.drain);
         __syncwarp();
-        mbar_wait_bounded(&drain, 0);
+        mbar_wait_bounded(&sy.drain, 0);
     } else if (warp < 6) {
         // ------------------------------------------------------------ softmax
         Walk w;
@@ -427,12 +479,12 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 }
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4 *>(sQ + (c / 8) * L::kPanel + row * 128 +
+                    *reinterpret_cast<uint4 *>(sQ + (c / 8) * L::kQPanel + row * 128 +
                                                (((c & 7) ^ (row & 7)) << 4)) = v[c];
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full);
+            if (lane == 0) mbar_arrive(&sy.q_full);
         };
         // Ancestors of every node of the current sequence: node lane in anc_lo, node
         // lane + 32 in anc_hi.  Each of six rounds joins a node's set with that of the
@@ -498,21 +550,23 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             }
             float m = -INFINITY, l = 0.f;
             for (int j = j0; j < j1; ++j, ++it) {
-                if (!(ok = all_wait(&s_full, (uint32_t)it & 1u))) break;
+                const int b = it & 1;
+                const uint32_t cs = trow + b * kKeys;  // this tile's scores, then P
+                if (!(ok = all_wait(&sy.s_full[b], (uint32_t)(it / 2) & 1u))) break;
                 tc_fence_after();
                 const int k0 = j * kKeys;
                 // V of this tile, where it reaches past the context: rows behind the
                 // sequence are zeroed, tree nodes cleared of NaN and infinities.
                 auto clean_v = [&]() -> bool {
-                    const int st = it % L::kSlots;
-                    if (!all_wait(&v_full[st], (uint32_t)(it / L::kSlots) & 1u)) return false;
-                    uint8_t *vs = sV + st * L::kTile;
+                    const int u = ring_v(it), st = u % L::kSlots;
+                    if (!all_wait(&sy.full[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
+                    uint8_t *vs = ring + st * L::kTile;
                     const int r0 = max(ctx - k0, 0), r1 = min(si.len - k0, kKeys);
                     bool bad = false;
                     for (int e = row; e < (kKeys - r0) * 8 * L::kPanels; e += kRows) {
                         const int p = e / ((kKeys - r0) * 8), r = r0 + (e >> 3) % (kKeys - r0);
-                        uint4 *at = reinterpret_cast<uint4 *>(vs + p * L::kPanel + r * 128 +
-                                                              (e & 7) * 16);
+                        uint4 *at = reinterpret_cast<uint4 *>(
+                            vs + p * L::kPanel + (r >> 3) * L::kGroup + (r & 7) * 128 + (e & 7) * 16);
                         if (r >= r1) {
                             *at = make_uint4(0, 0, 0, 0);
                             continue;
@@ -540,14 +594,14 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                             bad = true;
                         }
                     }
-                    if (bad) atomicExch(&s_bad[seg & 1], seg);
+                    if (bad) atomicExch(&sy.bad[seg & 1], seg);
                     fence_proxy_async_smem();
                     return true;
                 };
                 const bool past = k0 + kKeys > ctx;
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, nm = 0.f, cr = 1.f;
                 bool rescale = false;
-                float x[KV8 ? 32 : kKeys];
+                float x[kKeys];
                 // Visible keys of 32-key group g, as a bit word.
                 auto seen = [&](int g) -> uint32_t {
                     const int d = ctx - k0 - 32 * g;  // context keys in or before this group
@@ -576,41 +630,27 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                         pk[c] = KV8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
                         pk[c + 1] = KV8 ? pack_f16(p2, p3) : pack_bf16(p2, p3);
                     }
-                    tmem_st16(trow + 16 * g, pk);
+                    tmem_st16(cs + 16 * g, pk);
                 };
                 if (busy) {
                     // Row maximum of the raw scores (the scale goes into the exponent).
-                    float mx = -INFINITY, my = -INFINITY;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        float *v = KV8 ? x : x + 32 * g;
-                        tmem_ld32(trow + 32 * g, *reinterpret_cast<float(*)[32]>(v));
-                        if (KV8) {
-                            tc_wait_ld();
-                            if (past) mask(v, g);
-#pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                mx = fmax3(mx, v[c], v[c + 1]);
-                                my = fmax3(my, v[c + 2], v[c + 3]);
-                            }
-                        }
+                    tmem_ld32(cs, *reinterpret_cast<float(*)[32]>(x));
+                    tmem_ld32(cs + 32, *reinterpret_cast<float(*)[32]>(x + 32));
+                    tc_wait_ld();
+                    if (past) {
+                        mask(x, 0);
+                        mask(x + 32, 1);
                     }
-                    if constexpr (!KV8) {
-                        tc_wait_ld();
-                        if (past)
+                    float mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
 #pragma unroll
-                            for (int g = 0; g < 4; ++g) mask(x + 32 * g, g);
-                        float mz = -INFINITY, mw = -INFINITY;
-#pragma unroll
-                        for (int c = 0; c < kKeys; c += 8) {
-                            mx = fmax3(mx, x[c], x[c + 1]);
-                            my = fmax3(my, x[c + 2], x[c + 3]);
-                            mz = fmax3(mz, x[c + 4], x[c + 5]);
-                            mw = fmax3(mw, x[c + 6], x[c + 7]);
-                        }
-                        mx = fmaxf(mx, mz);
-                        my = fmaxf(my, mw);
+                    for (int c = 0; c < kKeys; c += 8) {
+                        mx = fmax3(mx, x[c], x[c + 1]);
+                        my = fmax3(my, x[c + 2], x[c + 3]);
+                        mz = fmax3(mz, x[c + 4], x[c + 5]);
+                        mw = fmax3(mw, x[c + 6], x[c + 7]);
                     }
+                    mx = fmaxf(mx, mz);
+                    my = fmaxf(my, mw);
                     mx = fmaxf(mx, my) * scale;
                     const bool grow = mx > m + kSlack;
                     rescale = __any_sync(0xffffffffu, grow);
@@ -622,22 +662,14 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                     }
                     // A row that has seen no key yet keeps m = -inf and P = 0.
                     nm = m == -INFINITY ? 0.f : -m;
-                    if constexpr (KV8) {
-                        // The scores are read again, 32 at a time (a register per score
-                        // for all of them would spill beside the converting warps).
-#pragma unroll 1
-                        for (int g = 0; g < 2; ++g) {
-                            tmem_ld32(trow + 32 * g, *reinterpret_cast<float(*)[32]>(x));
-                            tc_wait_ld();
-                            if (past) mask(x, g);
-                            probs(x, g);
-                        }
-                    } else {
-                        probs(x, 0);
-                        probs(x + 32, 1);
-                    }
+                    probs(x, 0);
+                    probs(x + 32, 1);
+                    l += (s0 + s1) + (s2 + s3);
                     if (rescale && j > j0) {
-                        // Scores ready: every earlier P.V is done, the next one waits.
+                        // The product before this one must be done; the next one waits.
+                        if (!(ok = all_wait(&sy.pv_done[b ^ 1], (uint32_t)((it - 1) / 2) & 1u)))
+                            break;
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[32];
@@ -654,26 +686,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 if (past && !(ok = clean_v())) break;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_lo);
-                if (busy) {
-                    if constexpr (KV8) {
-#pragma unroll 1
-                        for (int g = 2; g < 4; ++g) {
-                            tmem_ld32(trow + 32 * g, *reinterpret_cast<float(*)[32]>(x));
-                            tc_wait_ld();
-                            if (past) mask(x, g);
-                            probs(x, g);
-                        }
-                    } else {
-                        probs(x + 64, 2);
-                        probs(x + 96, 3);
-                    }
-                    l += (s0 + s1) + (s2 + s3);
-                    tc_wait_st();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_hi);
+                if (lane == 0) mbar_arrive(&sy.p_full[b]);
             }
             if (!ok) break;
             const int my_s = w.s;
@@ -684,12 +697,12 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             bool bad = false;
             if (tree) {  // did any warp find NaN or infinities in the tree's V?
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sane);
-                if (!(ok = all_wait(&sane, sane_par))) break;
+                if (lane == 0) mbar_arrive(&sy.sane);
+                if (!(ok = all_wait(&sy.sane, sane_par))) break;
                 sane_par ^= 1u;
-                bad = *reinterpret_cast<volatile int *>(&s_bad[seg & 1]) == seg;
+                bad = *reinterpret_cast<volatile int *>(&sy.bad[seg & 1]) == seg;
             }
-            if (!(ok = all_wait(&pv_done, (uint32_t)(it - 1) & 1u))) break;
+            if (!(ok = all_wait(&sy.pv_done[(it - 1) & 1], (uint32_t)((it - 1) / 2) & 1u))) break;
             tc_fence_after();
             if (busy) {
                 const float vsc = KV8 ? a.v_scale : 1.f;
@@ -756,7 +769,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free);
+            if (lane == 0) mbar_arrive(&sy.o_free);
             ++seg;
         }
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
@@ -795,20 +808,22 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             fence_proxy_async_smem();
             __syncwarp();
         };
+        // Tiles in the ring's order.
+        auto tile = [&](int u) -> bool {
+            const int st = u % L::kSlots;
+            if (!all_wait(&sy.staged[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
+            convert(ring + st * L::kTile);
+            if (lane == 0) mbar_arrive(&sy.full[st]);
+            return true;
+        };
         int it = 0;
         bool ok = true;
-        while (ok && w.next(a, rg)) {
-            for (int j = w.j0; j < w.j1; ++j, ++it) {
-                const int st = it % L::kSlots;
-                const uint32_t par = (uint32_t)(it / L::kSlots) & 1u;
-                if (!(ok = all_wait(&k_staged[st], par))) break;
-                convert(sK + st * L::kTile);
-                if (lane == 0) mbar_arrive(&k_full[st]);
-                if (!(ok = all_wait(&v_staged[st], par))) break;
-                convert(sV + st * L::kTile);
-                if (lane == 0) mbar_arrive(&v_full[st]);
+        while (ok && w.next(a, rg))
+            for (int j = w.j0; ok && j < w.j1; ++j, ++it) {
+                ok = tile(ring_k(it));
+                if (it > 0) ok = ok && tile(ring_v(it - 1));
             }
-        }
+        if (ok && it > 0) ok = tile(ring_v(it - 1));
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     }
     tc_fence_before();
@@ -951,9 +966,8 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
                                   float k_scale, float v_scale, void *workspace,
                                   cudaStream_t stream) {
     CUtensorMap map;
-    const int box_rows = g.block_size >= 16 ? 16 : g.block_size;
-    if (kv8 ? !encode_kv_map_fp8(&map, kv_cache, g, box_rows)
-            : !encode_kv_map(&map, kv_cache, g, box_rows))
+    if (kv8 ? !encode_kv_map_fp8(&map, kv_cache, g, g.block_size)
+            : !encode_kv_map_groups(&map, kv_cache, g))
         return cudaErrorInvalidValue;
     TreeAttnArgs a;
     a.group = num_heads / g.num_kv_heads;
