@@ -544,34 +544,42 @@ def _same_device(first: torch.Tensor, *others: torch.Tensor) -> None:
             raise ValueError("every tensor of a call must be on one device")
 
 
-def _on_current_device(dev: int) -> None:
-    """The library launches on the current device: tensors elsewhere are refused."""
+def _launch_stream(stream, dev: int) -> int:
+    """The stream of a call whose tensors are on device dev.  The library launches on the
+    current device: tensors elsewhere are refused.  (The current stream's handle is read
+    without building a Stream object, which would cost more than the launch.)"""
     if dev != torch.cuda.current_device():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 def _tree_attention(fp8, out, q, cu_tree_lens, parents, max_tree_len, kv_cache, block_tables,
                     seq_lens, max_seq_len, scale, scales, workspace, stream):
     try:  # every tensor at once; on failure the per-argument checks name the culprit
         dev = kv_cache.get_device()
-        ks, qs, bts = kv_cache.shape, q.shape, block_tables.shape
-        ok = (len(ks) == 5 and ks[1] == 2 and len(qs) == 3 and len(bts) == 2
-              and kv_cache.dtype is (_U8 if fp8 else _BF16) and dev >= 0
-              and kv_cache.is_contiguous()
+        NB, two, Hkv, bs, D = kv_cache.shape
+        rows, Hq, Dq = qs = q.shape
+        B, MB = block_tables.shape
+        ok = (two == 2 and Dq == D and dev >= 0
+              and out.shape == qs and cu_tree_lens.shape == (B + 1,)
+              and parents.shape == (rows,) and seq_lens.shape == (B,) and workspace.dim() == 1
+              and kv_cache.dtype is (_U8 if fp8 else _BF16) and kv_cache.is_contiguous()
               and q.dtype is _BF16 and q.get_device() == dev and q.is_contiguous()
               and out.dtype is _BF16 and out.get_device() == dev and out.is_contiguous()
               and cu_tree_lens.dtype is _I32 and cu_tree_lens.get_device() == dev
-              and cu_tree_lens.dim() == 1 and cu_tree_lens.is_contiguous()
-              and parents.dtype is _I32 and parents.get_device() == dev and parents.dim() == 1
+              and cu_tree_lens.is_contiguous()
+              and parents.dtype is _I32 and parents.get_device() == dev
               and parents.is_contiguous()
               and block_tables.dtype is _I32 and block_tables.get_device() == dev
               and block_tables.is_contiguous()
-              and seq_lens.dtype is _I32 and seq_lens.get_device() == dev and seq_lens.dim() == 1
+              and seq_lens.dtype is _I32 and seq_lens.get_device() == dev
               and seq_lens.is_contiguous()
-              and workspace.dtype is _U8 and workspace.get_device() == dev and workspace.dim() == 1
+              and workspace.dtype is _U8 and workspace.get_device() == dev
               and workspace.is_contiguous())
-    except (AttributeError, TypeError):
+    except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
         (_pool8_geom if fp8 else _pool_geom)(kv_cache)
@@ -583,21 +591,14 @@ def _tree_attention(fp8, out, q, cu_tree_lens, parents, max_tree_len, kv_cache, 
         _need(seq_lens, "seq_lens", _I32, 1)
         _need(workspace, "workspace", _U8, 1)
         _same_device(kv_cache, q, out, cu_tree_lens, parents, block_tables, seq_lens, workspace)
-        ks, qs, bts = kv_cache.shape, q.shape, block_tables.shape
-    _on_current_device(dev)
-    NB, _, Hkv, bs, D = ks
-    B = seq_lens.shape[0]
-    rows, Hq, Dq = qs
-    if Dq != D or out.shape != qs or parents.shape[0] != rows or bts[0] != B or \
-            cu_tree_lens.shape[0] != B + 1:
         raise ValueError("inconsistent tree attention shapes")
     L = _lib if _lib is not None else lib()
     args = (out.data_ptr(), q.data_ptr(), cu_tree_lens.data_ptr(), parents.data_ptr(), B, rows,
-            int(max_tree_len), kv_cache.data_ptr(), NB, bs, Hq, Hkv, D, block_tables.data_ptr(),
-            bts[1], seq_lens.data_ptr(), int(max_seq_len), float(scale))
-    tail = (workspace.data_ptr(), workspace.numel(), _stream(stream))
+            max_tree_len, kv_cache.data_ptr(), NB, bs, Hq, Hkv, D, block_tables.data_ptr(),
+            MB, seq_lens.data_ptr(), max_seq_len, scale)
+    tail = (workspace.data_ptr(), workspace.numel(), _launch_stream(stream, dev))
     if fp8:
-        st = L.pa_tree_attention_fp8(*args, float(scales[0]), float(scales[1]), *tail)
+        st = L.pa_tree_attention_fp8(*args, scales[0], scales[1], *tail)
     else:
         st = L.pa_tree_attention(*args, *tail)
     if st:
@@ -639,11 +640,10 @@ def _prob_rows(t: torch.Tensor, name: str, rows: int, vocab: int) -> int:
         raise ValueError(f"{name} must be {_F32}, got {t.dtype}")
     if t.shape != (rows, vocab):
         raise ValueError(f"{name} must be [total_nodes, vocab_size]")
-    if rows <= 1 and (vocab <= 1 or t.stride(1) == 1):
-        return vocab
-    if (vocab > 1 and t.stride(1) != 1) or t.stride(0) < vocab:
+    s0, s1 = t.stride()
+    if vocab > 1 and s1 != 1 or rows > 1 and s0 < vocab:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.stride(0)
+    return s0 if rows > 1 else vocab
 
 
 def pa_tree_verify(accepted: torch.Tensor, num_accepted: torch.Tensor, next_tokens: torch.Tensor,
@@ -656,23 +656,27 @@ def pa_tree_verify(accepted: torch.Tensor, num_accepted: torch.Tensor, next_toke
     -1 padded), num_accepted [B] and next_tokens [B]."""
     try:  # every tensor at once; on failure the per-argument checks name the culprit
         dev = accepted.get_device()
-        ok = (accepted.dtype is _I32 and dev >= 0 and accepted.dim() == 2
-              and accepted.is_contiguous()
-              and num_accepted.dtype is _I32 and num_accepted.get_device() == dev
-              and num_accepted.dim() == 1 and num_accepted.is_contiguous()
-              and next_tokens.dtype is _I32 and next_tokens.get_device() == dev and next_tokens.dim() == 1
-              and next_tokens.is_contiguous()
-              and tokens.dtype is _I32 and tokens.get_device() == dev and tokens.dim() == 1
-              and tokens.is_contiguous()
-              and cu_tree_lens.dtype is _I32 and cu_tree_lens.get_device() == dev
-              and cu_tree_lens.dim() == 1 and cu_tree_lens.is_contiguous()
-              and parents.dtype is _I32 and parents.get_device() == dev and parents.dim() == 1
-              and parents.is_contiguous()
-              and accept_u.dtype is _F32 and accept_u.get_device() == dev and accept_u.dim() == 1
-              and accept_u.is_contiguous()
-              and sample_u.dtype is _F32 and sample_u.get_device() == dev and sample_u.dim() == 1
-              and sample_u.is_contiguous())
-    except (AttributeError, TypeError):
+        B, max_tree = accepted.shape
+        rows, V = target_probs.shape
+        per_seq, per_node = (B,), (rows,)
+        ok = (dev >= 0 and accepted.dtype is _I32 and accepted.is_contiguous()
+              and num_accepted.shape == per_seq and num_accepted.dtype is _I32
+              and num_accepted.get_device() == dev and num_accepted.is_contiguous()
+              and next_tokens.shape == per_seq and next_tokens.dtype is _I32
+              and next_tokens.get_device() == dev and next_tokens.is_contiguous()
+              and tokens.shape == per_node and tokens.dtype is _I32
+              and tokens.get_device() == dev and tokens.is_contiguous()
+              and cu_tree_lens.shape == (B + 1,) and cu_tree_lens.dtype is _I32
+              and cu_tree_lens.get_device() == dev and cu_tree_lens.is_contiguous()
+              and parents.shape == per_node and parents.dtype is _I32
+              and parents.get_device() == dev and parents.is_contiguous()
+              and accept_u.shape == per_node and accept_u.dtype is _F32
+              and accept_u.get_device() == dev and accept_u.is_contiguous()
+              and sample_u.shape == per_seq and sample_u.dtype is _F32
+              and sample_u.get_device() == dev and sample_u.is_contiguous()
+              and target_probs.get_device() == dev
+              and (draft_probs is None or draft_probs.get_device() == dev))
+    except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
         _need(accepted, "accepted", _I32, 2)
@@ -683,31 +687,22 @@ def pa_tree_verify(accepted: torch.Tensor, num_accepted: torch.Tensor, next_toke
         _need(parents, "parents", _I32, 1)
         _need(accept_u, "accept_u", _F32, 1)
         _need(sample_u, "sample_u", _F32, 1)
+        for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+            if t is not None and (not isinstance(t, torch.Tensor) or not t.is_cuda):
+                raise ValueError(f"{name} must be a CUDA tensor")
         _same_device(accepted, num_accepted, next_tokens, tokens, cu_tree_lens, parents,
-                     accept_u, sample_u)
-    _on_current_device(dev)
-    B, max_tree = accepted.shape
-    rows = tokens.shape[0]
-    if num_accepted.shape[0] != B or next_tokens.shape[0] != B or sample_u.shape[0] != B or \
-            cu_tree_lens.shape[0] != B + 1 or parents.shape[0] != rows or \
-            accept_u.shape[0] != rows:
+                     accept_u, sample_u, target_probs, draft_probs)
         raise ValueError("inconsistent tree verification shapes")
-    if getattr(target_probs, "ndim", 0) != 2:
-        raise ValueError("target_probs must be [total_nodes, vocab_size]")
-    V = target_probs.shape[1]
-    _same_device(accepted, target_probs)
     ts = _prob_rows(target_probs, "target_probs", rows, V)
     dp, ds = None, 0
     if draft_probs is not None:
-        _same_device(accepted, draft_probs)
         ds = _prob_rows(draft_probs, "draft_probs", rows, V)
-        # An empty batch's tensor has no address; the call must still see a draft.
-        dp = draft_probs.data_ptr() or None
+        dp = draft_probs.data_ptr()
     L = _lib if _lib is not None else lib()
     st = L.pa_tree_verify(accepted.data_ptr(), num_accepted.data_ptr(), next_tokens.data_ptr(),
                           target_probs.data_ptr(), ts, dp, ds, tokens.data_ptr(),
                           cu_tree_lens.data_ptr(), parents.data_ptr(), B, rows, max_tree, V,
-                          accept_u.data_ptr(), sample_u.data_ptr(), _stream(stream))
+                          accept_u.data_ptr(), sample_u.data_ptr(), _launch_stream(stream, dev))
     if st:
         raise PaError(st, "pa_tree_verify")
 
@@ -721,50 +716,48 @@ def pa_tree_accept(kv_cache: torch.Tensor, accepted: torch.Tensor, num_accepted:
     if given, receives the new lengths."""
     try:  # every tensor at once; on failure the per-argument checks name the culprit
         dev = kv_cache.get_device()
-        ks, bts = kv_cache.shape, block_tables.shape
-        fp8 = kv_cache.dtype is _U8
-        ok = (len(ks) == 5 and ks[1] == 2 and len(bts) == 2
-              and (fp8 or kv_cache.dtype is _BF16) and dev >= 0
+        dt = kv_cache.dtype
+        NB, two, Hkv, bs, D = kv_cache.shape
+        B, max_tree = accepted.shape
+        tB, MB = block_tables.shape
+        per_seq = (B,)
+        ok = (two == 2 and dev >= 0 and tB == B and (dt is _BF16 or dt is _U8)
               and kv_cache.is_contiguous()
-              and accepted.dtype is _I32 and accepted.get_device() == dev and accepted.dim() == 2
+              and accepted.dtype is _I32 and accepted.get_device() == dev
               and accepted.is_contiguous()
-              and num_accepted.dtype is _I32 and num_accepted.get_device() == dev
-              and num_accepted.dim() == 1 and num_accepted.is_contiguous()
-              and cu_tree_lens.dtype is _I32 and cu_tree_lens.get_device() == dev
-              and cu_tree_lens.dim() == 1 and cu_tree_lens.is_contiguous()
+              and num_accepted.shape == per_seq and num_accepted.dtype is _I32
+              and num_accepted.get_device() == dev and num_accepted.is_contiguous()
+              and cu_tree_lens.shape == (B + 1,) and cu_tree_lens.dtype is _I32
+              and cu_tree_lens.get_device() == dev and cu_tree_lens.is_contiguous()
               and block_tables.dtype is _I32 and block_tables.get_device() == dev
               and block_tables.is_contiguous()
-              and seq_lens.dtype is _I32 and seq_lens.get_device() == dev and seq_lens.dim() == 1
-              and seq_lens.is_contiguous())
-    except (AttributeError, TypeError):
+              and seq_lens.shape == per_seq and seq_lens.dtype is _I32
+              and seq_lens.get_device() == dev and seq_lens.is_contiguous()
+              and (new_seq_lens is None
+                   or new_seq_lens.shape == per_seq and new_seq_lens.dtype is _I32
+                   and new_seq_lens.get_device() == dev and new_seq_lens.is_contiguous()))
+    except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
-        fp8 = getattr(kv_cache, "dtype", None) is _U8
-        (_pool8_geom if fp8 else _pool_geom)(kv_cache)
+        (_pool8_geom if getattr(kv_cache, "dtype", None) is _U8 else _pool_geom)(kv_cache)
         _need(accepted, "accepted", _I32, 2)
         _need(num_accepted, "num_accepted", _I32, 1)
         _need(cu_tree_lens, "cu_tree_lens", _I32, 1)
         _need(block_tables, "block_tables", _I32, 2)
         _need(seq_lens, "seq_lens", _I32, 1)
-        _same_device(kv_cache, accepted, num_accepted, cu_tree_lens, block_tables, seq_lens)
-        ks, bts = kv_cache.shape, block_tables.shape
-    if new_seq_lens is not None:
-        _need(new_seq_lens, "new_seq_lens", _I32, 1)
-        _same_device(kv_cache, new_seq_lens)
-    _on_current_device(dev)
-    NB, _, Hkv, bs, D = ks
-    B, max_tree = accepted.shape
-    if num_accepted.shape[0] != B or cu_tree_lens.shape[0] != B + 1 or bts[0] != B or \
-            seq_lens.shape[0] != B or (new_seq_lens is not None and new_seq_lens.shape[0] != B):
+        if new_seq_lens is not None:
+            _need(new_seq_lens, "new_seq_lens", _I32, 1)
+        _same_device(kv_cache, accepted, num_accepted, cu_tree_lens, block_tables, seq_lens,
+                     new_seq_lens)
         raise ValueError("inconsistent tree acceptance shapes")
     L = _lib if _lib is not None else lib()
-    st = (L.pa_tree_accept_fp8 if fp8 else L.pa_tree_accept)(
+    st = (L.pa_tree_accept_fp8 if dt is _U8 else L.pa_tree_accept)(
         kv_cache.data_ptr(), NB, bs, Hkv, D, accepted.data_ptr(), num_accepted.data_ptr(),
-        cu_tree_lens.data_ptr(), B, max_tree, block_tables.data_ptr(), bts[1],
+        cu_tree_lens.data_ptr(), B, max_tree, block_tables.data_ptr(), MB,
         seq_lens.data_ptr(), None if new_seq_lens is None else new_seq_lens.data_ptr(),
-        _stream(stream))
+        _launch_stream(stream, dev))
     if st:
-        raise PaError(st, "pa_tree_accept_fp8" if fp8 else "pa_tree_accept")
+        raise PaError(st, "pa_tree_accept_fp8" if dt is _U8 else "pa_tree_accept")
 
 
 def pa_error_check(stream=None) -> None:

@@ -18,4 +18,33 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeGeom &t, int s) {
     return {lo, hi - lo};
 }
 
+// The top of every kernel launched by launch_pdl: the next launch may begin, and what
+// came before has completed.
+__device__ __forceinline__ void pdl_begin() {
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Launch as a programmatic dependent of whatever comes before on the stream (its launch
+// and set-up overlap that kernel's end): every kernel here waits (griddepcontrol.wait)
+// before it reads or writes memory.  cluster: CTAs per cluster.
+template <typename... P>
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                       cudaStream_t stream, P... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace pa

@@ -32,58 +32,55 @@ struct AcceptArgs {
 };
 
 __global__ void __launch_bounds__(256) tree_accept_kernel(const AcceptArgs a) {
-    const int s = blockIdx.x;
+    // Pool row (side K, head 0) of each move's source and destination; -1: no move.
+    __shared__ int s_src[64], s_dst[64];
+    pdl_begin();
+    const int s = blockIdx.x, i0 = threadIdx.x;
+    // The list's entries are read with the sequence's data, before its count is known.
+    int p = 0, p_before = -1;
+    if (i0 < a.t.max_tree) {
+        const int32_t *path = a.accepted + (size_t)s * a.t.max_tree;
+        p = path[i0];
+        if (i0 > 0) p_before = path[i0 - 1];
+    }
     const TreeSpan span = tree_span(a.t, s);
     const int len = a.seq_lens[s], n = a.num_accepted[s];
-    const int32_t *path = a.accepted + (size_t)s * a.t.max_tree;
     bool bad = span.n < 0 || len < span.n || len > (long long)a.max_blocks * a.block_size ||
                n < 0 || n > span.n;
     // The whole list is checked before a row moves.
-    __shared__ int s_path[64];
-    if (!bad && (int)threadIdx.x < n) {
-        const int p = path[threadIdx.x];
-        s_path[threadIdx.x] = p;
-        bad = p < 0 || p >= span.n || (threadIdx.x > 0 && p <= path[threadIdx.x - 1]);
+    const bool mine = !bad && i0 < n;
+    if (mine) bad = p < 0 || p >= span.n || p <= p_before;
+    if (mine && !bad) {
+        const int base = len - span.n;
+        const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks;
+        const int b0 = bt[(base + p) / a.block_size], b1 = bt[(base + i0) / a.block_size];
+        const bool out = b0 < 0 || b0 >= a.num_blocks || b1 < 0 || b1 >= a.num_blocks;
+        if (out && p != i0) atomicOr(&g_err_tree_accept, kErrOob);
+        const int rows = 2 * a.num_kv_heads * a.block_size;  // of a block
+        s_src[i0] = out || p == i0 ? -1 : b0 * rows + (base + p) % a.block_size;
+        s_dst[i0] = out || p == i0 ? -1 : b1 * rows + (base + i0) % a.block_size;
     }
     bad = __syncthreads_or(bad);
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
+    if (blockIdx.y == 0 && i0 == 0) {
         if (bad) atomicOr(&g_err_tree_accept, kErrOob);
         if (a.new_seq_lens) a.new_seq_lens[s] = bad ? len : len - span.n + n;
     }
     if (bad) return;
-    const int col = blockIdx.y * blockDim.x + threadIdx.x;  // (side, head, vector)
-    const int per_side = a.num_kv_heads * a.vecs;
-    if (col >= 2 * per_side) return;
+    const int col = blockIdx.y * blockDim.x + i0;  // (side, head, vector)
+    if (col >= 2 * a.num_kv_heads * a.vecs) return;
     const int row = col / a.vecs, c = col - row * a.vecs;  // row = side * Hkv + head
-    const int base = len - span.n;
-    const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks;
-    // Vector index of this column at position pos; -1 outside the pool.
-    auto at = [&](int pos) -> int64_t {
-        const int blk = bt[pos / a.block_size];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (c == 0) atomicOr(&g_err_tree_accept, kErrOob);
-            return -1;
-        }
-        return (((int64_t)blk * 2 * a.num_kv_heads + row) * a.block_size + pos % a.block_size) *
-                   a.vecs + c;
-    };
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
+    auto at = [&](int r) { return ((int64_t)r + row * a.block_size) * a.vecs + c; };
+    for (int i = 0; i < n; i += kBatch) {
         uint4 x[kBatch];
-        int64_t dst[kBatch];
+        int dst[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + k;
-            dst[k] = -1;
-            if (i < n && s_path[i] != i) {
-                const int64_t src = at(base + s_path[i]);
-                dst[k] = at(base + i);
-                if (src < 0) dst[k] = -1;
-                if (dst[k] >= 0) x[k] = a.kv[src];
-            }
+            dst[k] = i + k < n ? s_dst[i + k] : -1;
+            if (dst[k] >= 0) x[k] = a.kv[at(s_src[i + k])];
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (dst[k] >= 0) a.kv[dst[k]] = x[k];
+            if (dst[k] >= 0) a.kv[at(dst[k])] = x[k];
     }
 }
 
@@ -118,8 +115,7 @@ cudaError_t launch_tree_accept(void *kv_cache, const KvGeom &g, int elem_bytes,
     // At least the 64 threads that check a path.
     const int threads = std::min(256, std::max(64, (cols + 31) / 32 * 32));
     const dim3 grid((unsigned)t.num_seqs, (unsigned)((cols + threads - 1) / threads));
-    tree_accept_kernel<<<grid, threads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(tree_accept_kernel, grid, threads, 0, 1, stream, a);
 }
 
 }  // namespace pa

@@ -40,6 +40,7 @@ __device__ unsigned g_err_tree_attention;
 
 constexpr int kRows = 128;  // query rows per tile (the MMA's M)
 constexpr int kKeys = 64;   // keys per K/V tile
+constexpr int kWholeTiles = 6;  // longest segment (in tiles) that is never split
 constexpr float kSlack = 8.0f;
 constexpr uint32_t kCols = 256, kColO = 128;  // tensor memory: two S / P tiles, then O
 
@@ -49,7 +50,9 @@ struct TreeAttnArgs {
     const void *kv;
     const int32_t *block_tables, *seq_lens;
     TreeGeom t;
-    int4 *starts;    // [workers]: (sequence, KV head, tile) each range starts at
+    // [workers] where each range starts: (sequence, KV head | tree nodes << 8, tile, first
+    // node row).
+    int4 *starts;
     float *part_ml;  // [2 * CTAs][part_rows][2]: m (log2 units), l
     float *part_acc; // [2 * CTAs][part_rows][D]
     int part_rows;
@@ -58,6 +61,7 @@ struct TreeAttnArgs {
     int q_tile;      // nodes per query tile: floor(128 / group)
     int row_groups;  // CTAs per worker
     int workers;
+    int whole_segments;  // ranges hold whole segments: nothing to merge
     int negate_q;
     float scale_log2;  // |scale| * log2(e), at least 1e-30
     float k_scale, v_scale;
@@ -92,7 +96,7 @@ struct Sync {
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint64_t q_full, o_free, sane, drain;
     uint32_t tmem;
-    int start[2], bad[2];
+    int start[2], range[2], bad[2];
     int part[10];
 };
 static_assert(sizeof(Sync) <= 512, "the barriers' room");
@@ -185,9 +189,34 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     const int worker = blockIdx.x / a.row_groups, rg = blockIdx.x - worker * a.row_groups;
     const int Hkv = a.num_kv_heads, B = a.t.num_seqs, G = a.group, QT = a.q_tile;
 
+    // What needs no memory of the caller's, under the end of the launch before this one.
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    // Tiles per head over all sequences, and where this worker's range starts: every
-    // thread sums a contiguous share of the sequences.
+    if (tid == 0) {
+        prefetch_tensormap(&kv_map);
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(&sy.full[i], KV8 ? L::kConv : 1);
+            mbar_init(&sy.empty[i], 1);
+            mbar_init(&sy.staged[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sy.s_full[i], 1);
+            mbar_init(&sy.p_full[i], 4);
+            mbar_init(&sy.pv_done[i], 1);
+        }
+        mbar_init(&sy.q_full, 4);
+        mbar_init(&sy.o_free, 4);
+        mbar_init(&sy.sane, 4);
+        mbar_init(&sy.drain, 1);
+        sy.bad[0] = sy.bad[1] = -1;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sy.tmem, kCols);
+        tmem_relinquish();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Tiles per head over all sequences, and the sequences that hold this range's start
+    // and end: every thread sums a contiguous share of the sequences.
     int t_begin, t_end;
     {
         const int per = (B + L::kThreads - 1) / L::kThreads;
@@ -212,54 +241,52 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         const long long We = a.workers < T ? a.workers : (T > 0 ? T : 1);
         t_begin = worker < We ? (int)(worker * T / We) : 0;
         t_end = worker < We ? (int)((worker + 1) * T / We) : 0;
-        if (T == 0) t_end = 0;
-        int pre = before + incl - sum;
-        if (t_begin < t_end && t_begin >= (long long)Hkv * pre &&
-            t_begin < (long long)Hkv * (pre + sum)) {
-            int s = s0;
-            for (;; ++s) {
-                const int nt = seq_info(a, s).tiles();
-                if (t_begin < (long long)Hkv * (pre + nt)) break;
-                pre += nt;
+        const int pre = before + incl - sum;
+        // The sequence at position x < T lies in one thread's share.
+        auto holds = [&](int x) {
+            return x >= (long long)Hkv * pre && x < (long long)Hkv * (pre + sum);
+        };
+        auto find = [&](int x, int &s, int &p, int &nt) {
+            for (s = s0, p = pre;; ++s, p += nt) {
+                nt = seq_info(a, s).tiles();
+                if (x < (long long)Hkv * (p + nt)) return;
             }
+        };
+        // Whole segments: a range starts at the first segment start at or after its share's.
+        auto snap = [&](int x, int p, int nt) {
+            const int r = (x - Hkv * p) % nt;
+            return r ? x + nt - r : x;
+        };
+        if (tid == 0) sy.range[1] = t_end;
+        if (a.whole_segments) __syncthreads();
+        int s, p, nt;
+        if (t_begin < t_end && holds(t_begin)) {
+            find(t_begin, s, p, nt);
             sy.start[0] = s;
-            sy.start[1] = pre;
+            sy.start[1] = p;
+            sy.range[0] = a.whole_segments ? snap(t_begin, p, nt) : t_begin;
         }
-    }
-    if (tid == 0) {
-        prefetch_tensormap(&kv_map);
-        for (int i = 0; i < L::kSlots; ++i) {
-            mbar_init(&sy.full[i], KV8 ? L::kConv : 1);
-            mbar_init(&sy.empty[i], 1);
-            mbar_init(&sy.staged[i], 1);
+        if (a.whole_segments && t_end < T && holds(t_end)) {
+            find(t_end, s, p, nt);
+            sy.range[1] = snap(t_end, p, nt);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sy.s_full[i], 1);
-            mbar_init(&sy.p_full[i], 4);
-            mbar_init(&sy.pv_done[i], 1);
-        }
-        mbar_init(&sy.q_full, 4);
-        mbar_init(&sy.o_free, 4);
-        mbar_init(&sy.sane, 4);
-        mbar_init(&sy.drain, 1);
-        sy.bad[0] = sy.bad[1] = -1;
-        fence_barrier_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(&sy.tmem, kCols);
-        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sy.tmem;
     const int seq0 = sy.start[0], pre0 = sy.start[1];
-    const bool work = seq0 >= 0;
-    if (tid == 0 && rg == 0) {
+    if (seq0 >= 0) {
+        t_begin = sy.range[0];
+        t_end = sy.range[1];
+    }
+    const bool work = seq0 >= 0 && t_begin < t_end;
+    if (tid == 0 && rg == 0 && !a.whole_segments) {
         int4 st = make_int4(-1, 0, 0, 0);
         if (work) {
-            const int nt = seq_info(a, seq0).tiles(), r = t_begin - Hkv * pre0;
-            st = make_int4(seq0, r / nt, r % nt, 0);
+            const SeqInfo si = seq_info(a, seq0);
+            const int nt = si.tiles(), r = t_begin - Hkv * pre0;
+            st = make_int4(seq0, (r / nt) | si.n << 8, r % nt, si.row0);
         }
         a.starts[worker] = st;
     }
@@ -436,14 +463,16 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         int anc_seq = -1;
         uint64_t anc_lo = 0, anc_hi = 0;
         auto real_in = [&](const SeqInfo &si) { return in_tile && rg * QT + r_node < si.n; };
+        auto q_row = [&]() {
+            return a.q + ((size_t)(w.cur.row0 + rg * QT + r_node) * a.num_heads +
+                          (size_t)w.h * G + r_head) * D;
+        };
         // The segment's query rows into shared memory (K-major, 128B swizzle).
         auto load_q = [&]() {
             const bool real = real_in(w.cur);
             sl2 = a.scale_log2;
             if (__any_sync(0xffffffffu, real)) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + ((size_t)(w.cur.row0 + rg * QT + r_node) * a.num_heads +
-                           (size_t)w.h * G + r_head) * D);
+                const uint4 *src = reinterpret_cast<const uint4 *>(q_row());
                 const uint32_t flip = a.negate_q ? 0x80008000u : 0u;  // exact bf16 negation
                 uint4 v[D / 8];
 #pragma unroll
@@ -547,6 +576,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 const uint64_t x = __shfl_sync(0xffffffffu, anc_lo, i & 31);
                 const uint64_t y = __shfl_sync(0xffffffffu, anc_hi, i & 31);
                 anc = i < 32 ? x : y;
+            }
+            const int my_s = w.s;
+            // On to the next segment: its queries come to L2 meanwhile.
+            more = w.next(a, rg);
+            if (more && real_in(w.cur)) {
+                const __nv_bfloat16 *next_q = q_row();
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(next_q + 64 * c));
             }
             float m = -INFINITY, l = 0.f;
             for (int j = j0; j < j1; ++j, ++it) {
@@ -689,10 +727,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 if (lane == 0) mbar_arrive(&sy.p_full[b]);
             }
             if (!ok) break;
-            const int my_s = w.s;
             // The next segment's queries while the last products run (this segment's
             // scores are all read).
-            more = w.next(a, rg);
             if (more) load_q();
             bool bad = false;
             if (tree) {  // did any warp find NaN or infinities in the tree's V?
@@ -834,73 +870,88 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     }
 }
 
-// Merge the pieces of segments that were split across workers: CTA (w, row group,
-// slice of rows) looks whether worker w's range starts inside a segment whose first
-// piece is worker w - 1's; a warp per row joins the pieces by log-sum-exp.
-constexpr int kMergeWarps = 8;
+// Merge the pieces of segments that were split across workers.  Warps (w, row group, 4
+// rows) look whether worker w's range starts inside a segment whose first piece is worker
+// w - 1's; then they join the rows' pieces by log-sum-exp in one pass, four rows at a time.
+constexpr int kMergeWarps = 8, kMergeRows = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeAttnArgs a) {
     constexpr int kPer = D / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int w = blockIdx.x + 1, rg = blockIdx.y;
-    const int4 me = a.starts[w];
-    if (me.x < 0 || me.z == 0) return;  // idle, or a segment's start
-    const int4 prev = a.starts[w - 1];
-    const bool prev_same = prev.x == me.x && prev.y == me.y;
-    if (prev_same && prev.z > 0) return;  // an earlier CTA merges this segment
-    // Workers w .. w + more - 1 start inside this segment.
-    int more = 0;
-    for (int base = w;; base += kMergeWarps * 32) {
-        const int i = base + (int)threadIdx.x;
-        bool in = false;
-        if (i < a.workers) {
-            const int4 st = a.starts[i];
-            in = st.x == me.x && st.y == me.y;
-        }
-        const int c = __syncthreads_count(in);
-        more += c;
-        if (c < kMergeWarps * 32) break;
-    }
-    const TreeSpan span = tree_span(a.t, me.x);
-    const int rows = min(a.q_tile, span.n - rg * a.q_tile) * a.group;
-    const int row = blockIdx.z * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    auto rec = [&](int k) -> size_t {  // record of piece k (0: worker w - 1's)
-        const size_t cta = (size_t)(w - 1 + k) * a.row_groups + rg;
-        return (cta * 2 + (k == 0 && !prev_same ? 1 : 0)) * a.part_rows + row;
+    pdl_begin();
+    const int w = blockIdx.x + 1, rg = blockIdx.y, lane = threadIdx.x & 31;
+    const int row0 = (blockIdx.z * kMergeWarps + (threadIdx.x >> 5)) * kMergeRows;
+    // Workers w - 1 .. w + 30, one per lane.
+    auto start_of = [&](int i) {
+        return i < a.workers ? a.starts[i] : make_int4(-1, 0, 0, 0);
     };
-    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-    const int n = more + 1;
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, ml[rec(k)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float den = 0.f, num[kPer] = {};
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-        const size_t r = rec(k);
-        const float2 e = ml[r];
-        const float wgt = fast_exp2(e.x - M);
-        den += wgt * e.y;
-        const float *acc = a.part_acc + r * D + lane * kPer;
-        float v[kPer];
-        if constexpr (kPer == 4)
-            *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(acc);
-        else
-            *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(acc);
-#pragma unroll
-        for (int e2 = 0; e2 < kPer; ++e2) num[e2] += wgt * v[e2];
+    int4 st = start_of(w - 1 + lane);
+    const int seq = __shfl_sync(0xffffffffu, st.x, 1), key = __shfl_sync(0xffffffffu, st.y, 1);
+    const int tile = __shfl_sync(0xffffffffu, st.z, 1), node0 = __shfl_sync(0xffffffffu, st.w, 1);
+    if (seq < 0 || tile == 0) return;  // idle, or a segment's start
+    const bool prev_same = __shfl_sync(0xffffffffu, st.x == seq && st.y == key, 0);
+    if (prev_same && __shfl_sync(0xffffffffu, st.z, 0) > 0) return;  // an earlier one merges it
+    const int nodes = key >> 8, head = key & 255;
+    const int rows = min(a.q_tile, nodes - rg * a.q_tile) * a.group;
+    if (row0 >= rows) return;
+    // Pieces: worker w - 1's and those of the workers from w on that start in the segment.
+    int n = 1;
+    for (int base = w;; base += 32) {
+        const int4 e = start_of(base + lane);
+        const unsigned in = __ballot_sync(0xffffffffu, e.x == seq && e.y == key);
+        n += __popc(in);
+        if (in != 0xffffffffu) break;
     }
-    const float inv = 1.f / den;
-    const int node = rg * a.q_tile + row / a.group, head = me.y * a.group + row % a.group;
-    __nv_bfloat16 *dst =
-        a.out + ((size_t)(span.row0 + node) * a.num_heads + head) * D + lane * kPer;
-    if constexpr (kPer == 4)
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack_bf16(num[0] * inv, num[1] * inv), pack_bf16(num[2] * inv, num[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pack_bf16(num[0] * inv, num[1] * inv);
+    const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+    float M[kMergeRows], den[kMergeRows], num[kMergeRows][kPer];
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+        M[i] = -INFINITY;
+        den[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) num[i][e] = 0.f;
+    }
+    const int last = min(kMergeRows, rows - row0) - 1;
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+        const size_t cta = (size_t)(w - 1 + k) * a.row_groups + rg;
+        const size_t rec = (cta * 2 + (k == 0 && !prev_same ? 1 : 0)) * a.part_rows + row0;
+        float2 e[kMergeRows];
+        float v[kMergeRows][kPer];
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) {
+            const size_t r = rec + min(i, last);
+            e[i] = ml[r];
+            const float *acc = a.part_acc + r * D + lane * kPer;
+            if constexpr (kPer == 4)
+                *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(acc);
+            else
+                *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(acc);
+        }
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) {
+            // A row that sees no key of a piece has m = -inf and nothing in it.
+            const float mn = fmaxf(M[i], e[i].x), ref = mn == -INFINITY ? 0.f : mn;
+            const float c = fast_exp2(M[i] - ref), g = fast_exp2(e[i].x - ref);
+            M[i] = mn;
+            den[i] = den[i] * c + g * e[i].y;
+#pragma unroll
+            for (int f = 0; f < kPer; ++f) num[i][f] = num[i][f] * c + g * v[i][f];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+        if (i > last) break;
+        const int row = row0 + i, node = node0 + rg * a.q_tile + row / a.group;
+        const float inv = 1.f / den[i];
+        __nv_bfloat16 *dst = a.out + ((size_t)node * a.num_heads + (size_t)head * a.group +
+                                      row % a.group) * D + lane * kPer;
+        if constexpr (kPer == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(num[i][0] * inv, num[i][1] * inv),
+                                                         pack_bf16(num[i][2] * inv, num[i][3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(num[i][0] * inv, num[i][1] * inv);
+    }
 }
 
 // Launch shape for trees of at most max_tree nodes.
@@ -924,25 +975,18 @@ Shape shape_of(int max_tree, int group, int head_size, int sm_count) {
 }
 
 template <int D, bool KV8>
-cudaError_t launch(const CUtensorMap &map, const TreeAttnArgs &a, bool split,
-                   cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap &map, const TreeAttnArgs &a, cudaStream_t stream) {
     using L = Tlay<D, KV8>;
-    auto kern = tree_attention_kernel<D, KV8>;
     cudaError_t e = ensure_smem<tree_attention_kernel<D, KV8>>(L::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(a.workers * a.row_groups), L::kThreads, L::kSmem, stream>>>(map, a);
-    if ((e = cudaGetLastError()) != cudaSuccess || !split || a.workers < 2) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.workers - 1), (unsigned)a.row_groups,
-                       (unsigned)((a.part_rows + kMergeWarps - 1) / kMergeWarps));
-    cfg.blockDim = dim3(kMergeWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
+    e = launch_pdl(tree_attention_kernel<D, KV8>, dim3((unsigned)(a.workers * a.row_groups)),
+                   L::kThreads, L::kSmem, 1, stream, map, a);
+    if (e != cudaSuccess || a.whole_segments || a.workers < 2) return e;
+    constexpr int kRowsPerCta = kMergeWarps * kMergeRows;
+    return launch_pdl(tree_merge_kernel<D>,
+                      dim3((unsigned)(a.workers - 1), (unsigned)a.row_groups,
+                           (unsigned)((a.part_rows + kRowsPerCta - 1) / kRowsPerCta)),
+                      kMergeWarps * 32, 0, 1, stream, a);
 }
 
 }  // namespace
@@ -1001,10 +1045,12 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
     a.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    const bool split = max_seq_len > kKeys;  // one tile is never split
-    if (kv8) return launch<128, true>(map, a, split, stream);
-    if (g.head_size == 128) return launch<128, false>(map, a, split, stream);
-    return launch<64, false>(map, a, split, stream);
+    // Contexts of a few tiles: a range of whole segments costs at most those tiles (about
+    // 0.6 us each) and saves the merge's launch.
+    a.whole_segments = max_seq_len <= kWholeTiles * kKeys;
+    if (kv8) return launch<128, true>(map, a, stream);
+    if (g.head_size == 128) return launch<128, false>(map, a, stream);
+    return launch<64, false>(map, a, stream);
 }
 
 }  // namespace pa

@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps) tree_verify_kernel(c
     float *s_rh = reinterpret_cast<float *>(s_dyn), *s_rl = s_rh + a.cta_slice,
           *s_qc = s_rl + a.cta_slice;
 
+    pdl_begin();
     const int C = a.cluster, s = blockIdx.x / C, rank = blockIdx.x - s * C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const TreeSpan span = tree_span(a.t, s);
@@ -635,27 +636,18 @@ cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t
     auto up32 = [](int x) { return (x + 31) / 32 * 32; };
     a.cta_slice = up32((vocab + c - 1) / c);
     a.warp_slice = up32((a.cta_slice + kWarps - 1) / kWarps);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(t.num_seqs * c));
-    cfg.blockDim = dim3(kWarps * 32);
     // r and q in shared memory where two CTAs of that size share an SM, or one is enough
     // for the batch; else a later rejection starts again from p and q.
     const size_t keep = (size_t)a.cta_slice * 12;
     a.cached = draft && t.max_tree > 2 &&
                (keep <= 100 << 10 || (keep <= 200 << 10 && (long long)c * t.num_seqs <= sms));
-    cfg.dynamicSmemBytes = draft ? (a.cached ? keep : 0) : (size_t)a.cta_slice / 8;
+    const size_t smem = draft ? (a.cached ? keep : 0) : (size_t)a.cta_slice / 8;
     if (a.cached) {
         const cudaError_t e = ensure_smem<tree_verify_kernel>(keep);
         if (e != cudaSuccess) return e;
     }
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)c;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_verify_kernel, a);
+    return launch_pdl(tree_verify_kernel, dim3((unsigned)(t.num_seqs * c)), kWarps * 32, smem, c,
+                      stream, a);
 }
 
 }  // namespace pa
