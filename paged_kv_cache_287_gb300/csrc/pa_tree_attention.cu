@@ -54,7 +54,9 @@ struct TreeAttnArgs {
     // node row).
     int4 *starts;
     float *part_ml;  // [2 * CTAs][part_rows][2]: m (log2 units), l
-    float *part_acc; // [2 * CTAs][part_rows][D]
+    // [2 * CTAs][D / 4][part_rows][4]: a thread holds a row, so the lanes of a store (and of
+    // the merge's loads) lie side by side.
+    float *part_acc;
     int part_rows;
     int num_heads, num_kv_heads, group;
     int block_size, max_blocks, num_blocks, max_len;
@@ -601,10 +603,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                     uint8_t *vs = ring + st * L::kTile;
                     const int r0 = max(ctx - k0, 0), r1 = min(si.len - k0, kKeys);
                     bool bad = false;
-                    for (int e = row; e < (kKeys - r0) * 8 * L::kPanels; e += kRows) {
-                        const int p = e / ((kKeys - r0) * 8), r = r0 + (e >> 3) % (kKeys - r0);
-                        uint4 *at = reinterpret_cast<uint4 *>(
-                            vs + p * L::kPanel + (r >> 3) * L::kGroup + (r & 7) * 128 + (e & 7) * 16);
+                    // Two threads per key, each half of its 16-byte chunks.
+                    const int r = row & (kKeys - 1);
+                    uint8_t *at0 = vs + (r >> 3) * L::kGroup + (r & 7) * 128;
+#pragma unroll 4
+                    for (int c = 0; c < 4 * L::kPanels; ++c) {
+                        if (r < r0) break;
+                        const int e = (row / kKeys) * 4 * L::kPanels + c;
+                        uint4 *at = reinterpret_cast<uint4 *>(at0 + (e >> 3) * L::kPanel +
+                                                              (e & 7) * 16);
                         if (r >= r1) {
                             *at = make_uint4(0, 0, 0, 0);
                             continue;
@@ -742,7 +749,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             tc_fence_after();
             if (busy) {
                 const float vsc = KV8 ? a.v_scale : 1.f;
-                const size_t rec = ((size_t)blockIdx.x * 2 + which) * a.part_rows + row;
+                const size_t rec = (size_t)blockIdx.x * 2 + which;
                 const size_t orow = ((size_t)(si.row0 + rg * QT + r_node) * a.num_heads +
                                      (size_t)s_h * G + r_head) * D;
                 const float mul = whole ? vsc / l : vsc;
@@ -792,16 +799,18 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                                                 pack_bf16(o[8 * e + 4], o[8 * e + 5]),
                                                 pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                     } else if (real) {
-                        float4 *dst = reinterpret_cast<float4 *>(a.part_acc + rec * D) + 8 * c;
+                        float4 *dst = reinterpret_cast<float4 *>(a.part_acc) +
+                                      (rec * (D / 4) + 8 * c) * a.part_rows + row;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            st_hint(dst + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                            st_hint(dst + e * a.part_rows, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2],
                                                          o[4 * e + 3]), keep);
                     }
                     __syncwarp();
                 }
                 if (real && !whole)
-                    st_hint(reinterpret_cast<float2 *>(a.part_ml) + rec, make_float2(m, l), keep);
+                    st_hint(reinterpret_cast<float2 *>(a.part_ml) + rec * a.part_rows + row,
+                            make_float2(m, l), keep);
             }
             tc_fence_before();
             __syncwarp();
@@ -870,22 +879,23 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     }
 }
 
-// Merge the pieces of segments that were split across workers.  Warps (w, row group, 4
-// rows) look whether worker w's range starts inside a segment whose first piece is worker
-// w - 1's; then they join the rows' pieces by log-sum-exp in one pass, four rows at a time.
-constexpr int kMergeWarps = 8, kMergeRows = 4;
+// Merge the pieces of segments that were split across workers.  CTA (w, row group, 32 rows)
+// looks whether worker w's range starts inside a segment whose first piece is worker
+// w - 1's; then a lane per row and a warp per D / 16 dims joins the pieces by log-sum-exp
+// in one pass, several pieces' loads in flight.
+constexpr int kMergeWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeAttnArgs a) {
-    constexpr int kPer = D / 32;
+    constexpr int kUnits = D / 4 / kMergeWarps;  // float4 of a row that a thread joins
     pdl_begin();
     const int w = blockIdx.x + 1, rg = blockIdx.y, lane = threadIdx.x & 31;
-    const int row0 = (blockIdx.z * kMergeWarps + (threadIdx.x >> 5)) * kMergeRows;
+    const int row0 = blockIdx.z * 32;
     // Workers w - 1 .. w + 30, one per lane.
     auto start_of = [&](int i) {
         return i < a.workers ? a.starts[i] : make_int4(-1, 0, 0, 0);
     };
-    int4 st = start_of(w - 1 + lane);
+    const int4 st = start_of(w - 1 + lane);
     const int seq = __shfl_sync(0xffffffffu, st.x, 1), key = __shfl_sync(0xffffffffu, st.y, 1);
     const int tile = __shfl_sync(0xffffffffu, st.z, 1), node0 = __shfl_sync(0xffffffffu, st.w, 1);
     if (seq < 0 || tile == 0) return;  // idle, or a segment's start
@@ -902,56 +912,72 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
         n += __popc(in);
         if (in != 0xffffffffu) break;
     }
+    const int row = row0 + lane;
+    if (row >= rows) return;
+    const int unit0 = (threadIdx.x >> 5) * kUnits;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-    float M[kMergeRows], den[kMergeRows], num[kMergeRows][kPer];
+    const float4 *acc = reinterpret_cast<const float4 *>(a.part_acc);
+    float M = -INFINITY, den = 0.f;
+    float4 num[kUnits];
 #pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
-        M[i] = -INFINITY;
-        den[i] = 0.f;
+    for (int i = 0; i < kUnits; ++i) num[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 4;
+    for (int k0 = 0; k0 < n; k0 += kBatch) {
+        float2 e[kBatch];
+        float4 v[kBatch][kUnits];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) num[i][e] = 0.f;
-    }
-    const int last = min(kMergeRows, rows - row0) - 1;
-#pragma unroll 2
-    for (int k = 0; k < n; ++k) {
-        const size_t cta = (size_t)(w - 1 + k) * a.row_groups + rg;
-        const size_t rec = (cta * 2 + (k == 0 && !prev_same ? 1 : 0)) * a.part_rows + row0;
-        float2 e[kMergeRows];
-        float v[kMergeRows][kPer];
+        for (int k = 0; k < kBatch; ++k) {
+            if (k0 + k < n) {
+                const size_t cta = (size_t)(w - 1 + k0 + k) * a.row_groups + rg;
+                const size_t rec = cta * 2 + (k0 + k == 0 && !prev_same ? 1 : 0);
+                e[k] = ml[rec * a.part_rows + row];
 #pragma unroll
-        for (int i = 0; i < kMergeRows; ++i) {
-            const size_t r = rec + min(i, last);
-            e[i] = ml[r];
-            const float *acc = a.part_acc + r * D + lane * kPer;
-            if constexpr (kPer == 4)
-                *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(acc);
-            else
-                *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(acc);
+                for (int i = 0; i < kUnits; ++i)
+                    v[k][i] = acc[(rec * (D / 4) + unit0 + i) * a.part_rows + row];
+            }
+        }
+        // A row that sees no key of a piece has m = -inf and nothing in it.
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (k0 + k < n) mn = fmaxf(mn, e[k].x);
+        const float ref = mn == -INFINITY ? 0.f : mn, c = fast_exp2(M - ref);
+        M = mn;
+        den *= c;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            num[i].x *= c;
+            num[i].y *= c;
+            num[i].z *= c;
+            num[i].w *= c;
         }
 #pragma unroll
-        for (int i = 0; i < kMergeRows; ++i) {
-            // A row that sees no key of a piece has m = -inf and nothing in it.
-            const float mn = fmaxf(M[i], e[i].x), ref = mn == -INFINITY ? 0.f : mn;
-            const float c = fast_exp2(M[i] - ref), g = fast_exp2(e[i].x - ref);
-            M[i] = mn;
-            den[i] = den[i] * c + g * e[i].y;
+        for (int k = 0; k < kBatch; ++k) {
+            if (k0 + k >= n) break;
+            const float g = fast_exp2(e[k].x - ref);
+            den += g * e[k].y;
 #pragma unroll
-            for (int f = 0; f < kPer; ++f) num[i][f] = num[i][f] * c + g * v[i][f];
+            for (int i = 0; i < kUnits; ++i) {
+                num[i].x += g * v[k][i].x;
+                num[i].y += g * v[k][i].y;
+                num[i].z += g * v[k][i].z;
+                num[i].w += g * v[k][i].w;
+            }
         }
     }
+    const float inv = 1.f / den;
+    const int node = node0 + rg * a.q_tile + row / a.group;
+    uint2 *dst = reinterpret_cast<uint2 *>(
+        a.out + ((size_t)node * a.num_heads + (size_t)head * a.group + row % a.group) * D) + unit0;
+    uint2 o[kUnits];
 #pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
-        if (i > last) break;
-        const int row = row0 + i, node = node0 + rg * a.q_tile + row / a.group;
-        const float inv = 1.f / den[i];
-        __nv_bfloat16 *dst = a.out + ((size_t)node * a.num_heads + (size_t)head * a.group +
-                                      row % a.group) * D + lane * kPer;
-        if constexpr (kPer == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(num[i][0] * inv, num[i][1] * inv),
-                                                         pack_bf16(num[i][2] * inv, num[i][3] * inv));
-        else
-            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(num[i][0] * inv, num[i][1] * inv);
-    }
+    for (int i = 0; i < kUnits; ++i)
+        o[i] = make_uint2(pack_bf16(num[i].x * inv, num[i].y * inv),
+                          pack_bf16(num[i].z * inv, num[i].w * inv));
+    if constexpr (kUnits == 2)
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
+    else
+        dst[0] = o[0];
 }
 
 // Launch shape for trees of at most max_tree nodes.
@@ -982,10 +1008,9 @@ cudaError_t launch(const CUtensorMap &map, const TreeAttnArgs &a, cudaStream_t s
     e = launch_pdl(tree_attention_kernel<D, KV8>, dim3((unsigned)(a.workers * a.row_groups)),
                    L::kThreads, L::kSmem, 1, stream, map, a);
     if (e != cudaSuccess || a.whole_segments || a.workers < 2) return e;
-    constexpr int kRowsPerCta = kMergeWarps * kMergeRows;
     return launch_pdl(tree_merge_kernel<D>,
                       dim3((unsigned)(a.workers - 1), (unsigned)a.row_groups,
-                           (unsigned)((a.part_rows + kRowsPerCta - 1) / kRowsPerCta)),
+                           (unsigned)((a.part_rows + 31) / 32)),
                       kMergeWarps * 32, 0, 1, stream, a);
 }
 
