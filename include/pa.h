@@ -474,9 +474,10 @@ pa_status pa_tree_attention(void *out, const void *q, const int32_t *cu_tree_len
 /*
  * pa_tree_attention_fp8 - pa_tree_attention over an FP8 pool: K = code value *
  * k_scale, V = code value * v_scale.  head_size must be 128 (else
- * PA_ERR_UNSUPPORTED).  Codes convert to f16 exactly, each query row is scaled by
- * a power of two into f16 range first (exact), P is rounded to f16.  Workspace:
- * pa_tree_attention_workspace_bytes.  Other arguments, results and errors as
+ * PA_ERR_UNSUPPORTED).  K is multiplied as codes, each query row (scaled by a power
+ * of two) as the sum of two e4m3 rows: exact for elements down to 2^-9 of the row's
+ * largest, within 2^-17 of the largest below.  V converts to f16 exactly, P is
+ * rounded to f16.  Workspace: pa_tree_attention_workspace_bytes.  Other arguments, results and errors as
  * pa_tree_attention.
  */
 pa_status pa_tree_attention_fp8(void *out, const void *q, const int32_t *cu_tree_lens,

@@ -312,6 +312,17 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
+// The same, kind::f8f6f4 (e4m3 codes in, K = 32 per instruction, fp32 accumulate).
+__device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
 __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -388,6 +399,11 @@ __device__ __forceinline__ uint64_t tc_desc_sw128(uint32_t smem_addr, uint32_t l
 __host__ __device__ constexpr uint32_t tc_idesc_f16(int m, int n, int b_mn_major) {
     return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(m >> 4) << 24);
+}
+
+// kind::f8f6f4, e4m3 A and B (format fields 0), both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t tc_idesc_e4m3(int m, int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 __host__ __device__ constexpr uint32_t tc_idesc_bf16(int m, int n, int b_mn_major) {

@@ -74,28 +74,32 @@ struct Tlay {
     static constexpr int kPanels = D / 64;
     static constexpr int kQPanel = kRows * 128;  // 64 dims of 128 rows
     static constexpr int kQ = kPanels * kQPanel;
-    static constexpr int kTile = kPanels * kKeys * 128;  // a K or V tile
-    // Where 8 keys x 64 dims (1 KB, swizzled) of panel p, keys 8 g ..: kGroup g + kPanel p.
-    // A bf16 block lands in one copy with its panels side by side; an FP8 tile's f16
-    // values go panel by panel, the upper one over its codes.
-    static constexpr int kGroup = KV8 ? 1024 : 1024 * kPanels;
-    static constexpr int kPanel = KV8 ? kKeys * 128 : 1024;
-    static constexpr int kSlots = D == 64 ? 8 : 5;  // tiles in the ring
+    // Tiles of K and V as the products read them, and how many are held.  An FP8 pool's K
+    // is read as codes; its V lands as codes in a ring of their own and is converted.
+    static constexpr int kVTile = kPanels * kKeys * 128;
+    static constexpr int kKTile = KV8 ? kKeys * 128 : kVTile;
+    static constexpr int kKSlots = KV8 ? 3 : (D == 64 ? 4 : 2);
+    static constexpr int kVSlots = KV8 ? 2 : (D == 64 ? 4 : 3);
+    static constexpr int kStages = KV8 ? 3 : 0;
+    static constexpr int kStage = kKeys * 128;
+    // Where 8 keys x 64 dims (1 KB, swizzled) of panel p, keys 8 g .. lie in a 16-bit tile:
+    // kGroup g + kPanel p.  A bf16 block lands in one copy with its panels side by side.
+    static constexpr int kGroup = 1024 * kPanels;
+    static constexpr int kPanel = 1024;
     static constexpr int kConv = KV8 ? 2 : 0;  // converting warps
     static constexpr int kThreads = (6 + kConv) * 32;
-    static constexpr int kOperands = kQ + kSlots * kTile;
+    static constexpr int kK = kQ, kV = kK + kKSlots * kKTile, kCodes = kV + kVSlots * kVTile;
+    static constexpr int kOperands = kCodes + kStages * kStage;
     static constexpr size_t kSmem = (size_t)kOperands + 512;  // + barriers
 };
 
-// Order of the tiles in the ring: K0 K1 V0 K2 V1 K3 V2 ..., the order in which the
-// products (scores one tile ahead) release them.
-__device__ __forceinline__ int ring_k(int i) { return i ? 2 * i - 1 : 0; }
-__device__ __forceinline__ int ring_v(int i) { return 2 * i + 2; }
-
 // What follows the operands in shared memory.
 struct Sync {
-    uint64_t full[8], empty[8], staged[8];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t k_full[4], v_full[4], staged[3], stage_free[3];
+    // Scores of tile i done, by i % K slots: its K slot is free too.  Output of tile i done,
+    // by i % V slots: its V slot is free too.  (A commit costs the issuing thread some 200
+    // cycles, as much as four products, so one serves both.)
+    uint64_t s_full[4], pv_done[4], p_full[2];
     uint64_t q_full, o_free, sane, drain;
     uint32_t tmem;
     int start[2], range[2], bad[2];
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     // No static shared memory: the dynamic part then starts at the (1024-byte aligned)
     // beginning, and two CTAs' 112 KB of operands fit one SM.
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sQ = smem, *ring = smem + L::kQ;
+    uint8_t *sQ = smem, *sK = smem + L::kK, *sV = smem + L::kV;
     Sync &sy = *reinterpret_cast<Sync *>(smem + L::kOperands);
     if (smem_u32(smem) & 1023u) {  // the same for every thread: the swizzle needs it
         if (threadIdx.x == 0) atomicOr(&g_err_tree_attention, kErrPrecondition);
@@ -195,16 +199,20 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     asm volatile("griddepcontrol.launch_dependents;" :::);
     if (tid == 0) {
         prefetch_tensormap(&kv_map);
-        for (int i = 0; i < L::kSlots; ++i) {
-            mbar_init(&sy.full[i], KV8 ? L::kConv : 1);
-            mbar_init(&sy.empty[i], 1);
-            mbar_init(&sy.staged[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::kKSlots; ++i) {
+            mbar_init(&sy.k_full[i], 1);
             mbar_init(&sy.s_full[i], 1);
-            mbar_init(&sy.p_full[i], 4);
+        }
+        for (int i = 0; i < L::kVSlots; ++i) {
+            mbar_init(&sy.v_full[i], KV8 ? L::kConv : 1);
             mbar_init(&sy.pv_done[i], 1);
         }
+        for (int i = 0; i < L::kStages; ++i) {
+            mbar_init(&sy.staged[i], 1);
+            mbar_init(&sy.stage_free[i], L::kConv);
+        }
+        mbar_init(&sy.p_full[0], 4);
+        mbar_init(&sy.p_full[1], 4);
         mbar_init(&sy.q_full, 4);
         mbar_init(&sy.o_free, 4);
         mbar_init(&sy.sane, 4);
@@ -302,27 +310,37 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         const int bs = a.block_size, nbox = kKeys / bs;  // a box per block
         const int v_off = Hkv * bs;
         const uint64_t policy = policy_evict_first();
-        // Tile u of the ring: wait until its slot is free, then copy the boxes.
-        auto load = [&](int u, int row) -> bool {
-            const int st = u % L::kSlots;
-            if (u >= L::kSlots &&
-                !all_wait(&sy.empty[st], (uint32_t)(u / L::kSlots - 1) & 1u))
-                return false;
-            uint8_t *dst = ring + st * L::kTile;
-            uint64_t *bar = KV8 ? &sy.staged[st] : &sy.full[st];
-            if (lane == 0)
-                mbar_arrive_expect_tx(bar, KV8 ? (uint32_t)(kKeys * 128) : (uint32_t)L::kTile);
+        // Copy a tile's boxes (this lane's at TMA row `row`) to dst.
+        auto copy = [&](uint8_t *dst, uint64_t *bar, uint32_t bytes, int row) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
             __syncwarp();
             if (lane < nbox) {
-                if constexpr (KV8) {
-                    tma_load_2d_hint(dst + L::kTile / 2 + lane * bs * 128, &kv_map, bar, 0, row,
-                                     policy);
-                } else {
-                    // The pool's rows in groups of 8 (blocks are whole groups).
+                if constexpr (KV8)
+                    tma_load_2d_hint(dst + lane * bs * 128, &kv_map, bar, 0, row, policy);
+                else  // the pool's rows in groups of 8 (blocks are whole groups)
                     tma_load_4d_hint(dst + lane * (bs / 8) * L::kGroup, &kv_map, bar, row >> 3,
                                      policy);
-                }
             }
+        };
+        // K / V of tile i, once its slot is free.
+        auto load_k = [&](int i, int row) -> bool {
+            const int st = i % L::kKSlots;
+            if (i >= L::kKSlots &&
+                !all_wait(&sy.s_full[st], (uint32_t)(i / L::kKSlots - 1) & 1u))
+                return false;
+            copy(sK + st * L::kKTile, &sy.k_full[st], (uint32_t)L::kKTile, row);
+            return true;
+        };
+        auto load_v = [&](int i, int row) -> bool {
+            constexpr int kN = KV8 ? L::kStages : L::kVSlots;
+            const int st = i % kN;
+            if (i >= kN && !all_wait(KV8 ? &sy.stage_free[st] : &sy.pv_done[st],
+                                     (uint32_t)(i / kN - 1) & 1u))
+                return false;
+            if constexpr (KV8)
+                copy(smem + L::kCodes + st * L::kStage, &sy.staged[st], (uint32_t)L::kStage, row);
+            else
+                copy(sV + st * L::kVTile, &sy.v_full[st], (uint32_t)L::kVTile, row);
             return true;
         };
         // This lane's box of V where its box of K is at TMA row r.
@@ -358,95 +376,100 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             }
             return ((blk * 2) * Hkv + head) * bs;
         };
-        int it = 0, prev = 0, last_u = -1;
+        // K runs one tile ahead of V, as the products do.
+        int it = 0, prev = 0, k_issued = 0, v_issued = 0;
         bool ok = true, more = fetch();
         for (; ok && more; ++it) {
             const int row = row_of();
             more = fetch();
-            if (!(ok = load(ring_k(it), row))) break;
-            last_u = ring_k(it);
+            if (!(ok = load_k(it, row))) break;
+            ++k_issued;
             if (it > 0) {
-                if (!(ok = load(ring_v(it - 1), v_row(prev)))) break;
-                last_u = ring_v(it - 1);
+                if (!(ok = load_v(it - 1, v_row(prev)))) break;
+                ++v_issued;
             }
             prev = row;
         }
-        if (ok && it > 0 && (ok = load(ring_v(it - 1), v_row(prev)))) last_u = ring_v(it - 1);
+        if (ok && it > 0 && (ok = load_v(it - 1, v_row(prev)))) ++v_issued;
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
-        // Never leave with copies in flight into this CTA's shared memory.  (The last V
-        // tile's place follows one that is never used.)
-        for (int u = max(0, last_u - L::kSlots + 1); u <= last_u; ++u)
-            if (!(ok && u == last_u - 1 && it > 0))
-                mbar_wait_bounded(KV8 ? &sy.staged[u % L::kSlots] : &sy.full[u % L::kSlots],
-                                  (uint32_t)(u / L::kSlots) & 1u);
+        // Never leave with copies in flight into this CTA's shared memory.
+        for (int i = max(0, k_issued - L::kKSlots); i < k_issued; ++i)
+            mbar_wait_bounded(&sy.k_full[i % L::kKSlots], (uint32_t)(i / L::kKSlots) & 1u);
+        constexpr int kN = KV8 ? L::kStages : L::kVSlots;
+        for (int i = max(0, v_issued - kN); i < v_issued; ++i)
+            mbar_wait_bounded(KV8 ? &sy.staged[i % kN] : &sy.v_full[i % kN],
+                              (uint32_t)(i / kN) & 1u);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         Walk w;
         w.start(a, seq0, pre0, t_begin, t_end);
         const uint32_t idesc_s =
-            KV8 ? tc_idesc_f16(kRows, kKeys, 0) : tc_idesc_bf16(kRows, kKeys, 0);
+            KV8 ? tc_idesc_e4m3(kRows, kKeys) : tc_idesc_bf16(kRows, kKeys, 0);
         const uint32_t idesc_pv = KV8 ? tc_idesc_f16(kRows, D, 1) : tc_idesc_bf16(kRows, D, 1);
         const uint64_t q_desc = tc_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t k_desc = tc_desc_sw128(smem_u32(ring), 16, L::kGroup);
-        const uint64_t v_desc = tc_desc_sw128(smem_u32(ring), L::kPanel, L::kGroup);
-        // S_i = Q.K^T into buffer i & 1, whose last P (tile i - 2) must be used up; a
-        // segment's first tile waits for its queries.
-        auto scores = [&](int i, bool first, int sg) -> bool {
-            const int u = ring_k(i), st = u % L::kSlots, b = i & 1;
-            if (!all_wait(&sy.full[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
-            if (first && !all_wait(&sy.q_full, (uint32_t)sg & 1u)) return false;
-            if (i >= 2 && !all_wait(&sy.pv_done[b], (uint32_t)(i / 2 - 1) & 1u)) return false;
+        const uint64_t k_desc = tc_desc_sw128(smem_u32(sK), 16, KV8 ? 1024 : L::kGroup);
+        const uint64_t v_desc = tc_desc_sw128(smem_u32(sV), L::kPanel, L::kGroup);
+        // S_i = Q.K^T into buffer i & 1, over tile i - 2's P: this thread issued the product
+        // that reads it before, and the products of one thread run in order.
+        auto scores = [&](int i) -> bool {
+            const int st = i % L::kKSlots, b = i & 1;
+            if (!mbar_wait_bounded(&sy.k_full[st], (uint32_t)(i / L::kKSlots) & 1u)) return false;
             tc_fence_after();
-            if (lane == 0) {
-                const uint64_t kd = k_desc + (uint64_t)((st * L::kTile) >> 4);
+            const uint64_t kd = k_desc + (uint64_t)((st * L::kKTile) >> 4);
+            if constexpr (KV8) {
+                // The queries' two e4m3 parts, 32 dims at a time.
+#pragma unroll
+                for (int k = 0; k < 2 * (D / 32); ++k) {
+                    const uint32_t ko = (k & 3) * 32;
+                    tc_mma_f8_ss(tmem + b * kKeys, q_desc + (((k >> 2) * L::kQPanel + ko) >> 4),
+                                 kd + (ko >> 4), idesc_s, k > 0 ? 1u : 0u);
+                }
+            } else {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t qo = ((k >> 2) * L::kQPanel + (k & 3) * 32) >> 4;
                     const uint32_t ko = ((k >> 2) * L::kPanel + (k & 3) * 32) >> 4;
                     tc_mma_ss(tmem + b * kKeys, q_desc + qo, kd + ko, idesc_s, k > 0 ? 1u : 0u);
                 }
-                tc_commit(&sy.s_full[b]);
-                tc_commit(&sy.empty[st]);
             }
-            __syncwarp();
+            tc_commit(&sy.s_full[st]);
             return true;
         };
-        // O += P_i.V, over O's old contents for a segment's first tile (once the epilogue
-        // of the segment before has read them).
-        auto output = [&](int i, bool first, int sg) -> bool {
-            const int u = ring_v(i), st = u % L::kSlots, b = i & 1;
-            if (!all_wait(&sy.full[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
-            if (first && sg > 0 && !all_wait(&sy.o_free, (uint32_t)(sg - 1) & 1u)) return false;
-            if (!all_wait(&sy.p_full[b], (uint32_t)(i / 2) & 1u)) return false;
+        // O += P_i.V (over O's old contents for a segment's first tile).
+        auto output = [&](int i, bool first) -> bool {
+            const int st = i % L::kVSlots, b = i & 1;
+            if (!mbar_wait_bounded(&sy.v_full[st], (uint32_t)(i / L::kVSlots) & 1u)) return false;
+            if (!mbar_wait_bounded(&sy.p_full[b], (uint32_t)(i / 2) & 1u)) return false;
             tc_fence_after();
-            if (lane == 0) {
-                const uint64_t vd = v_desc + (uint64_t)((st * L::kTile) >> 4);
+            const uint64_t vd = v_desc + (uint64_t)((st * L::kVTile) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    tc_mma_ts(tmem + kColO, tmem + b * kKeys + kk * 8,
-                              vd + (uint64_t)((kk * 2 * L::kGroup) >> 4), idesc_pv,
-                              (!first || kk > 0) ? 1u : 0u);
-                tc_commit(&sy.pv_done[b]);
-                tc_commit(&sy.empty[st]);
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc_mma_ts(tmem + kColO, tmem + b * kKeys + kk * 8,
+                          vd + (uint64_t)((kk * 2 * L::kGroup) >> 4), idesc_pv,
+                          (!first || kk > 0) ? 1u : 0u);
+            tc_commit(&sy.pv_done[st]);
             return true;
         };
-        // The scores run one tile ahead of the outputs; at a segment's end the output goes
-        // first (the next scores wait for the next queries).
-        int it = 0, seg = 0;
-        bool ok = true, out_first = false;  // is the waiting output a segment's first?
-        while (ok && w.next(a, rg)) {
-            for (int j = w.j0; ok && j < w.j1; ++j, ++it) {
-                const bool first = j == w.j0;
-                if (first && it > 0) ok = output(it - 1, out_first, seg - 1);
-                ok = ok && scores(it, first, seg);
-                if (!first) ok = ok && output(it - 1, out_first, seg);
-                out_first = first;
+        // One thread runs a segment: its scores two tiles ahead of its outputs, from the
+        // arrival of its queries; its first output after the epilogue before it has read O.
+        auto segment = [&](int base, int n, int sg) -> bool {
+            if (!mbar_wait_bounded(&sy.q_full, (uint32_t)sg & 1u)) return false;
+            if (!scores(base) || (n > 1 && !scores(base + 1))) return false;
+            if (sg > 0 && !mbar_wait_bounded(&sy.o_free, (uint32_t)(sg - 1) & 1u)) return false;
+            for (int j = 0; j < n; ++j) {
+                if (!output(base + j, j == 0)) return false;
+                if (j + 2 < n && !scores(base + j + 2)) return false;
             }
+            return true;
+        };
+        int it = 0, seg = 0;
+        bool ok = true;
+        while (ok && w.next(a, rg)) {
+            if (lane == 0) ok = segment(it, w.j1 - w.j0, seg);
+            ok = __all_sync(0xffffffffu, ok);
+            it += w.j1 - w.j0;
             ++seg;
         }
-        if (ok && it > 0) ok = output(it - 1, out_first, seg - 1);
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
         // Every product must be done before tensor memory is freed.
         if (lane == 0) tc_commit(&sy.drain);
@@ -486,32 +509,61 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                     v[c].w ^= flip;
                 }
                 if constexpr (KV8) {
-                    // f16 query: the row times the power of two that puts its largest
-                    // element in [1, 2), exactly; sl2 takes it back, with k_scale.
+                    // K is multiplied as codes, so the query becomes the sum of two e4m3
+                    // rows: scaled by the power of two that puts its largest element in
+                    // [128, 256), q = hi + lo with hi the nearest e4m3 number (4 significant
+                    // bits of bf16's 8) and lo what is left.  That is exact for elements
+                    // down to 2^-9 of the largest; below, e4m3's smallest step leaves an
+                    // error of at most 2^-10, or 2^-17 of the largest element, no more than
+                    // fp32 loses in the 128-term sum.  sl2 takes the scaling back, with
+                    // k_scale; a row with NaN or infinities becomes NaN through it.
                     float mx = 0.f;
+                    uint32_t top = 0u;  // the largest exponent field
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
                         mx = fmax3(mx, fabsf(bf16_lo(v[c].x)), fabsf(bf16_hi(v[c].x)));
                         mx = fmax3(mx, fabsf(bf16_lo(v[c].y)), fabsf(bf16_hi(v[c].y)));
                         mx = fmax3(mx, fabsf(bf16_lo(v[c].z)), fabsf(bf16_hi(v[c].z)));
                         mx = fmax3(mx, fabsf(bf16_lo(v[c].w)), fabsf(bf16_hi(v[c].w)));
+                        auto exps = [&](uint32_t w) {
+                            top = max(top, max(w & 0x7f80u, (w >> 16) & 0x7f80u));
+                        };
+                        exps(v[c].x);
+                        exps(v[c].y);
+                        exps(v[c].z);
+                        exps(v[c].w);
                     }
                     int ex = mx > 0.f ? (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127 : 0;
-                    ex = max(-126, min(126, ex));
-                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);  // 2^-ex
-                    sl2 *= a.k_scale * __uint_as_float((uint32_t)(127 + ex) << 23);
+                    ex = max(-119, min(127, ex));
+                    const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+                    sl2 *= a.k_scale * __uint_as_float((uint32_t)(127 + ex - 7) << 23);
+                    if (top == 0x7f80u) sl2 = NAN;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {  // 16 dims: one chunk of codes each
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 &u = v[2 * c + (i >> 1)];
+                            const uint32_t w0 = i & 1 ? u.z : u.x, w1 = i & 1 ? u.w : u.y;
+                            const float x0 = bf16_lo(w0) * down, x1 = bf16_hi(w0) * down;
+                            const float x2 = bf16_lo(w1) * down, x3 = bf16_hi(w1) * down;
+                            hi[i] = pack_e4m3x2(x0, x1) | pack_e4m3x2(x2, x3) << 16;
+                            uint32_t f0, f1;
+                            e4m3x4_to_f16x4(hi[i], f0, f1);
+                            lo[i] = pack_e4m3x2(x0 - f16_lo(f0), x1 - f16_hi(f0)) |
+                                    pack_e4m3x2(x2 - f16_lo(f1), x3 - f16_hi(f1)) << 16;
+                        }
+                        uint8_t *dst = sQ + row * 128 + ((c ^ (row & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(dst + L::kQPanel) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                } else {
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c)
-                        v[c] = make_uint4(
-                            pack_f16(bf16_lo(v[c].x) * down, bf16_hi(v[c].x) * down),
-                            pack_f16(bf16_lo(v[c].y) * down, bf16_hi(v[c].y) * down),
-                            pack_f16(bf16_lo(v[c].z) * down, bf16_hi(v[c].z) * down),
-                            pack_f16(bf16_lo(v[c].w) * down, bf16_hi(v[c].w) * down));
+                        *reinterpret_cast<uint4 *>(sQ + (c / 8) * L::kQPanel + row * 128 +
+                                                   (((c & 7) ^ (row & 7)) << 4)) = v[c];
                 }
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4 *>(sQ + (c / 8) * L::kQPanel + row * 128 +
-                                               (((c & 7) ^ (row & 7)) << 4)) = v[c];
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -592,15 +644,17 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             for (int j = j0; j < j1; ++j, ++it) {
                 const int b = it & 1;
                 const uint32_t cs = trow + b * kKeys;  // this tile's scores, then P
-                if (!(ok = all_wait(&sy.s_full[b], (uint32_t)(it / 2) & 1u))) break;
+                if (!(ok = all_wait(&sy.s_full[it % L::kKSlots],
+                                    (uint32_t)(it / L::kKSlots) & 1u)))
+                    break;
                 tc_fence_after();
                 const int k0 = j * kKeys;
                 // V of this tile, where it reaches past the context: rows behind the
                 // sequence are zeroed, tree nodes cleared of NaN and infinities.
                 auto clean_v = [&]() -> bool {
-                    const int u = ring_v(it), st = u % L::kSlots;
-                    if (!all_wait(&sy.full[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
-                    uint8_t *vs = ring + st * L::kTile;
+                    const int st = it % L::kVSlots;
+                    if (!all_wait(&sy.v_full[st], (uint32_t)(it / L::kVSlots) & 1u)) return false;
+                    uint8_t *vs = sV + st * L::kVTile;
                     const int r0 = max(ctx - k0, 0), r1 = min(si.len - k0, kKeys);
                     bool bad = false;
                     // Two threads per key, each half of its 16-byte chunks.
@@ -712,7 +766,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                     l += (s0 + s1) + (s2 + s3);
                     if (rescale && j > j0) {
                         // The product before this one must be done; the next one waits.
-                        if (!(ok = all_wait(&sy.pv_done[b ^ 1], (uint32_t)((it - 1) / 2) & 1u)))
+                        if (!(ok = all_wait(&sy.pv_done[(it - 1) % L::kVSlots],
+                                            (uint32_t)((it - 1) / L::kVSlots) & 1u)))
                             break;
                         tc_fence_after();
 #pragma unroll 1
@@ -745,7 +800,9 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 sane_par ^= 1u;
                 bad = *reinterpret_cast<volatile int *>(&sy.bad[seg & 1]) == seg;
             }
-            if (!(ok = all_wait(&sy.pv_done[(it - 1) & 1], (uint32_t)((it - 1) / 2) & 1u))) break;
+            if (!(ok = all_wait(&sy.pv_done[(it - 1) % L::kVSlots],
+                                (uint32_t)((it - 1) / L::kVSlots) & 1u)))
+                break;
             tc_fence_after();
             if (busy) {
                 const float vsc = KV8 ? a.v_scale : 1.f;
@@ -819,56 +876,49 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         }
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     } else if constexpr (KV8) {
-        // ------------------------------------------------------------ e4m3 -> f16
-        // A lane converts whole rows: it reads the row's 128 codes (128B-swizzled as TMA
-        // left them in the slot's upper half), then writes its 128 f16 values into the
-        // two 64-dim panels; row r of the upper panel is exactly the bytes of code row r.
+        // ------------------------------------------------------------ V: e4m3 -> f16
+        // A lane converts a key's 128 codes (128B-swizzled as TMA left them) to f16 in the
+        // layout a bf16 tile has.
         Walk w;
         w.start(a, seq0, pre0, t_begin, t_end);
-        auto convert = [&](uint8_t *slot) {
-            const uint8_t *codes = slot + L::kTile / 2;
-#pragma unroll 1
-            for (int r = (warp - 6) * 32 + lane; r < kKeys; r += 32 * L::kConv) {
-                uint4 in[8];
+        const int r = (warp - 6) * 32 + lane;
+        auto tile = [&](int i) -> bool {
+            const int ss = i % L::kStages, st = i % L::kVSlots;
+            if (!all_wait(&sy.staged[ss], (uint32_t)(i / L::kStages) & 1u)) return false;
+            const uint8_t *codes = smem + L::kCodes + ss * L::kStage + r * 128;
+            uint4 in[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    in[c] = *reinterpret_cast<const uint4 *>(codes + r * 128 +
-                                                             ((c ^ (r & 7)) << 4));
-                asm volatile("" ::: "memory");
+            for (int c = 0; c < 8; ++c)
+                in[c] = *reinterpret_cast<const uint4 *>(codes + ((c ^ (r & 7)) << 4));
+            if (i >= L::kVSlots &&
+                !all_wait(&sy.pv_done[st], (uint32_t)(i / L::kVSlots - 1) & 1u))
+                return false;
+            __syncwarp();  // every lane's codes are read
+            if (lane == 0) mbar_arrive(&sy.stage_free[ss]);
+            uint8_t *base = sV + st * L::kVTile + (r >> 3) * L::kGroup + (r & 7) * 128;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t f[8];
-                    e4m3x4_to_f16x4(in[c].x, f[0], f[1]);
-                    e4m3x4_to_f16x4(in[c].y, f[2], f[3]);
-                    e4m3x4_to_f16x4(in[c].z, f[4], f[5]);
-                    e4m3x4_to_f16x4(in[c].w, f[6], f[7]);
-                    uint8_t *dst = slot + (c >> 2) * L::kPanel + r * 128;
-                    const int ch = 2 * (c & 3);
-                    *reinterpret_cast<uint4 *>(dst + ((ch ^ (r & 7)) << 4)) =
-                        make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint4 *>(dst + (((ch + 1) ^ (r & 7)) << 4)) =
-                        make_uint4(f[4], f[5], f[6], f[7]);
-                }
+            for (int c = 0; c < 8; ++c) {
+                uint32_t f[8];
+                e4m3x4_to_f16x4(in[c].x, f[0], f[1]);
+                e4m3x4_to_f16x4(in[c].y, f[2], f[3]);
+                e4m3x4_to_f16x4(in[c].z, f[4], f[5]);
+                e4m3x4_to_f16x4(in[c].w, f[6], f[7]);
+                uint8_t *dst = base + (c >> 2) * L::kPanel;
+                const int ch = 2 * (c & 3);
+                *reinterpret_cast<uint4 *>(dst + ((ch ^ (r & 7)) << 4)) =
+                    make_uint4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<uint4 *>(dst + (((ch + 1) ^ (r & 7)) << 4)) =
+                    make_uint4(f[4], f[5], f[6], f[7]);
             }
             fence_proxy_async_smem();
             __syncwarp();
-        };
-        // Tiles in the ring's order.
-        auto tile = [&](int u) -> bool {
-            const int st = u % L::kSlots;
-            if (!all_wait(&sy.staged[st], (uint32_t)(u / L::kSlots) & 1u)) return false;
-            convert(ring + st * L::kTile);
-            if (lane == 0) mbar_arrive(&sy.full[st]);
+            if (lane == 0) mbar_arrive(&sy.v_full[st]);
             return true;
         };
         int it = 0;
         bool ok = true;
         while (ok && w.next(a, rg))
-            for (int j = w.j0; ok && j < w.j1; ++j, ++it) {
-                ok = tile(ring_k(it));
-                if (it > 0) ok = ok && tile(ring_v(it - 1));
-            }
-        if (ok && it > 0) ok = tile(ring_v(it - 1));
+            for (int j = w.j0; ok && j < w.j1; ++j, ++it) ok = tile(it);
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     }
     tc_fence_before();

@@ -58,7 +58,11 @@ def tree_attention(q, pool, tables, seq_lens, tree_lens, parents, scale, kv_scal
     f16 2^-11 and 2^-25 below its normal range, on P >= 1 at the largest score)
     against an unrounded sum, that much of A; and in fp32 the products and sums of a
     score, at most (D + 8) 2^-24 sum_d |q_d k_d| |scale| each, twice (numerator and
-    sum), with 2^-20 for exp2 and the accumulation of P.V in blocks of at least 16.
+    sum), with 2^-20 for exp2 and the accumulation of P.V in blocks of at least 16.  Over
+    an FP8 pool a query is held as the sum of two e4m3 numbers after scaling its row's
+    largest element into [128, 256): e4m3's step is at least 2^-9, so an element is off
+    by at most 2^-10, that is 2^-17 of the largest, and the score by at most 2^-17
+    max|q| sum_d |k_d| |scale|, again twice.
     """
     fp8 = pool.dtype == torch.uint8
     vals = pool_values(pool, kv_scales)
@@ -91,7 +95,11 @@ def tree_attention(q, pool, tables, seq_lens, tree_lens, parents, scale, kv_scal
                 t += a * (2.0 ** -11 if fp8 else 2.0 ** -8)
                 if fp8:
                     t += 2.0 ** -25 * np.abs(v).sum(axis=0) / l
-                t += a * (2 * (D + 8) * 2.0 ** -24 * mag.max(axis=1, keepdims=True) + 2.0 ** -20)
+                off = (D + 8) * 2.0 ** -24 * mag.max(axis=1, keepdims=True)
+                if fp8:
+                    off = off + 2.0 ** -17 * np.abs(qh).max(axis=1, keepdims=True) * \
+                        np.abs(k).sum(axis=1).max() * abs(scale)
+                t += a * (2 * off + 2.0 ** -20)
                 out[cu[s] + i, h * G:(h + 1) * G] = o
                 tol[cu[s] + i, h * G:(h + 1) * G] = t * (1 + 2.0 ** -7)
     return out, tol
