@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         mbar_init(&sy.p_full[1], 4);
         mbar_init(&sy.q_full, 4);
         mbar_init(&sy.o_free, 4);
-        mbar_init(&sy.sane, 4);
+        mbar_init(&sy.sane, 1);
         mbar_init(&sy.drain, 1);
         sy.bad[0] = sy.bad[1] = -1;
         fence_barrier_init();
@@ -450,24 +450,83 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             tc_commit(&sy.pv_done[st]);
             return true;
         };
+        // Tile i's V in keys [r0, 64), past the context: rows from r1 on (behind the sequence)
+        // are zeroed, tree nodes' cleared of NaN and infinities.  True if there were any.
+        auto clean = [&](int i, int r0, int r1) -> bool {
+            constexpr int kC = 8 * L::kPanels;  // 16-byte chunks of a key
+            uint8_t *vs = sV + (i % L::kVSlots) * L::kVTile +
+                          ((lane % kC) >> 3) * L::kPanel + (lane & 7) * 16;
+            bool bad = false;
+            for (int r = r0 + lane / kC; r < kKeys; r += 32 / kC) {
+                uint4 *at = reinterpret_cast<uint4 *>(vs + (r >> 3) * L::kGroup + (r & 7) * 128);
+                if (r >= r1) {
+                    *at = make_uint4(0, 0, 0, 0);
+                    continue;
+                }
+                uint4 v = *at;
+                constexpr uint32_t kExp = KV8 ? 0x7C00u : 0x7F80u;
+                bool hit = false;
+                auto clear = [&](uint32_t x) {
+                    if ((x & kExp) == kExp) {
+                        x &= 0xffff0000u;
+                        hit = true;
+                    }
+                    if ((x & (kExp << 16)) == (kExp << 16)) {
+                        x &= 0x0000ffffu;
+                        hit = true;
+                    }
+                    return x;
+                };
+                v.x = clear(v.x);
+                v.y = clear(v.y);
+                v.z = clear(v.z);
+                v.w = clear(v.w);
+                if (hit) {
+                    *at = v;
+                    bad = true;
+                }
+            }
+            fence_proxy_async_smem();
+            return bad;
+        };
         // One thread runs a segment: its scores two tiles ahead of its outputs, from the
         // arrival of its queries; its first output after the epilogue before it has read O.
-        auto segment = [&](int base, int n, int sg) -> bool {
+        // The (at most two) tiles that reach past the context are cleaned by the warp first.
+        auto begin = [&](int base, int n, int sg) -> bool {
             if (!mbar_wait_bounded(&sy.q_full, (uint32_t)sg & 1u)) return false;
             if (!scores(base) || (n > 1 && !scores(base + 1))) return false;
-            if (sg > 0 && !mbar_wait_bounded(&sy.o_free, (uint32_t)(sg - 1) & 1u)) return false;
-            for (int j = 0; j < n; ++j) {
-                if (!output(base + j, j == 0)) return false;
-                if (j + 2 < n && !scores(base + j + 2)) return false;
-            }
-            return true;
+            return sg == 0 || mbar_wait_bounded(&sy.o_free, (uint32_t)(sg - 1) & 1u);
+        };
+        auto step = [&](int base, int j, int n) -> bool {
+            return output(base + j, j == 0) && (j + 2 >= n || scores(base + j + 2));
         };
         int it = 0, seg = 0;
         bool ok = true;
         while (ok && w.next(a, rg)) {
-            if (lane == 0) ok = segment(it, w.j1 - w.j0, seg);
+            const int n = w.j1 - w.j0, ctx = w.cur.len - w.cur.n;
+            const int plain = min(n, max(0, ctx / kKeys - w.j0));
+            if (lane == 0) {
+                ok = begin(it, n, seg);
+                for (int j = 0; ok && j < plain; ++j) ok = step(it, j, n);
+            }
             ok = __all_sync(0xffffffffu, ok);
-            it += w.j1 - w.j0;
+            bool bad = false;
+            for (int j = plain; ok && j < n; ++j) {
+                const int i = it + j, k0 = (w.j0 + j) * kKeys;
+                ok = all_wait(&sy.v_full[i % L::kVSlots], (uint32_t)(i / L::kVSlots) & 1u);
+                if (!ok) break;
+                bad |= clean(i, max(ctx - k0, 0), min(w.cur.len - k0, kKeys));
+                bad = __any_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    if (j == n - 1) {  // what was found, to the softmax warps
+                        if (bad) sy.bad[seg & 1] = seg;
+                        mbar_arrive(&sy.sane);
+                    }
+                    ok = step(it, j, n);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            it += n;
             ++seg;
         }
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
@@ -492,77 +551,93 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             return a.q + ((size_t)(w.cur.row0 + rg * QT + r_node) * a.num_heads +
                           (size_t)w.h * G + r_head) * D;
         };
-        // The segment's query rows into shared memory (K-major, 128B swizzle).
+        // The segment's query rows into shared memory (K-major, 128B swizzle): the warp takes
+        // its 32 rows a few at a time, 16 bytes per lane.
+        //
+        // K of an FP8 pool is multiplied as codes, so the query becomes the sum of two e4m3
+        // rows: scaled by the power of two that puts its largest element in [128, 256),
+        // q = hi + lo with hi the nearest e4m3 number (4 significant bits of bf16's 8) and lo
+        // what is left.  That is exact for elements down to 2^-9 of the largest; below, e4m3's
+        // smallest step leaves an error of at most 2^-10, or 2^-17 of the largest element, no
+        // more than fp32 loses in the 128-term sum.  sl2 takes the scaling back, with k_scale;
+        // a row with NaN or infinities becomes NaN through it.
         auto load_q = [&]() {
-            const bool real = real_in(w.cur);
+            constexpr int kC = D / 8, kR = 32 / kC;  // chunks of a row, rows at a time
+            constexpr int kBatch = KV8 ? 4 : 8;
             sl2 = a.scale_log2;
-            if (__any_sync(0xffffffffu, real)) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(q_row());
+            if (__any_sync(0xffffffffu, real_in(w.cur))) {
+                const int c = lane % kC, row0 = row - lane + lane / kC;
                 const uint32_t flip = a.negate_q ? 0x80008000u : 0u;  // exact bf16 negation
-                uint4 v[D / 8];
+                int node = row0 / G, head = row0 - node * G;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + ((size_t)(w.cur.row0 + rg * QT) * a.num_heads + (size_t)w.h * G) * D) + c;
+#pragma unroll 1
+                for (int k0 = 0; k0 < 32 / kR; k0 += kBatch) {
+                    uint4 v[kBatch];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    v[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                    v[c].x ^= flip;
-                    v[c].y ^= flip;
-                    v[c].z ^= flip;
-                    v[c].w ^= flip;
-                }
-                if constexpr (KV8) {
-                    // K is multiplied as codes, so the query becomes the sum of two e4m3
-                    // rows: scaled by the power of two that puts its largest element in
-                    // [128, 256), q = hi + lo with hi the nearest e4m3 number (4 significant
-                    // bits of bf16's 8) and lo what is left.  That is exact for elements
-                    // down to 2^-9 of the largest; below, e4m3's smallest step leaves an
-                    // error of at most 2^-10, or 2^-17 of the largest element, no more than
-                    // fp32 loses in the 128-term sum.  sl2 takes the scaling back, with
-                    // k_scale; a row with NaN or infinities becomes NaN through it.
-                    float mx = 0.f;
-                    uint32_t top = 0u;  // the largest exponent field
+                    for (int k = 0; k < kBatch; ++k) {
+                        const bool in = row0 + kR * (k0 + k) < QT * G &&
+                                        rg * QT + node < w.cur.n;
+                        v[k] = in ? __ldg(src + ((size_t)node * a.num_heads + head) * kC)
+                                  : make_uint4(0, 0, 0, 0);
+                        head += kR;
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        mx = fmax3(mx, fabsf(bf16_lo(v[c].x)), fabsf(bf16_hi(v[c].x)));
-                        mx = fmax3(mx, fabsf(bf16_lo(v[c].y)), fabsf(bf16_hi(v[c].y)));
-                        mx = fmax3(mx, fabsf(bf16_lo(v[c].z)), fabsf(bf16_hi(v[c].z)));
-                        mx = fmax3(mx, fabsf(bf16_lo(v[c].w)), fabsf(bf16_hi(v[c].w)));
-                        auto exps = [&](uint32_t w) {
-                            top = max(top, max(w & 0x7f80u, (w >> 16) & 0x7f80u));
-                        };
-                        exps(v[c].x);
-                        exps(v[c].y);
-                        exps(v[c].z);
-                        exps(v[c].w);
+                        for (int t = 0; t < kR; ++t)
+                            if (head >= G) {
+                                head -= G;
+                                ++node;
+                            }
                     }
-                    int ex = mx > 0.f ? (int)((__float_as_uint(mx) >> 23) & 0xffu) - 127 : 0;
-                    ex = max(-119, min(127, ex));
-                    const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-                    sl2 *= a.k_scale * __uint_as_float((uint32_t)(127 + ex - 7) << 23);
-                    if (top == 0x7f80u) sl2 = NAN;
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {  // 16 dims: one chunk of codes each
-                        uint32_t hi[4], lo[4];
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int r = row0 + kR * (k0 + k);
+                        v[k].x ^= flip;
+                        v[k].y ^= flip;
+                        v[k].z ^= flip;
+                        v[k].w ^= flip;
+                        if constexpr (!KV8) {
+                            *reinterpret_cast<uint4 *>(sQ + (c >> 3) * L::kQPanel + r * 128 +
+                                                       (((c & 7) ^ (r & 7)) << 4)) = v[k];
+                        } else {
+                            // The row's largest element, as bf16 bits without the sign.
+                            uint32_t top = 0u;
+                            auto up = [&](uint32_t x) {
+                                top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
+                            };
+                            up(v[k].x);
+                            up(v[k].y);
+                            up(v[k].z);
+                            up(v[k].w);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 &u = v[2 * c + (i >> 1)];
-                            const uint32_t w0 = i & 1 ? u.z : u.x, w1 = i & 1 ? u.w : u.y;
-                            const float x0 = bf16_lo(w0) * down, x1 = bf16_hi(w0) * down;
-                            const float x2 = bf16_lo(w1) * down, x3 = bf16_hi(w1) * down;
-                            hi[i] = pack_e4m3x2(x0, x1) | pack_e4m3x2(x2, x3) << 16;
-                            uint32_t f0, f1;
-                            e4m3x4_to_f16x4(hi[i], f0, f1);
-                            lo[i] = pack_e4m3x2(x0 - f16_lo(f0), x1 - f16_hi(f0)) |
-                                    pack_e4m3x2(x2 - f16_lo(f1), x3 - f16_hi(f1)) << 16;
+                            for (int o = kC / 2; o > 0; o >>= 1)
+                                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            const int ex =
+                                max(-119, min(127, top ? (int)(top >> 7) - 127 : 0));
+                            const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+                            uint32_t hi[2], lo[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t w0 = i ? v[k].z : v[k].x, w1 = i ? v[k].w : v[k].y;
+                                const float x0 = bf16_lo(w0) * down, x1 = bf16_hi(w0) * down;
+                                const float x2 = bf16_lo(w1) * down, x3 = bf16_hi(w1) * down;
+                                hi[i] = pack_e4m3x2(x0, x1) | pack_e4m3x2(x2, x3) << 16;
+                                uint32_t f0, f1;
+                                e4m3x4_to_f16x4(hi[i], f0, f1);
+                                lo[i] = pack_e4m3x2(x0 - f16_lo(f0), x1 - f16_hi(f0)) |
+                                        pack_e4m3x2(x2 - f16_lo(f1), x3 - f16_hi(f1)) << 16;
+                            }
+                            uint8_t *dst = sQ + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+                            *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2 *>(dst + L::kQPanel) = make_uint2(lo[0], lo[1]);
+                            // The scale of row `lane` to its thread.
+                            const float back = top >= 0x7f80u
+                                                   ? NAN
+                                                   : __uint_as_float((uint32_t)(127 + ex - 7) << 23);
+                            const float mine =
+                                __shfl_sync(0xffffffffu, back, (lane % kR) * kC);
+                            if (lane / kR == k0 + k) sl2 = a.scale_log2 * a.k_scale * mine;
                         }
-                        uint8_t *dst = sQ + row * 128 + ((c ^ (row & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(dst + L::kQPanel) =
-                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        *reinterpret_cast<uint4 *>(sQ + (c / 8) * L::kQPanel + row * 128 +
-                                                   (((c & 7) ^ (row & 7)) << 4)) = v[c];
                 }
             }
             fence_proxy_async_smem();
@@ -640,6 +715,9 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 for (int c = 0; c < D / 64; ++c)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(next_q + 64 * c));
             }
+            if (more && w.s != my_s && lane < 2)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.t.parents + w.cur.row0 +
+                                                             min(32 * lane, w.cur.n - 1)));
             float m = -INFINITY, l = 0.f;
             for (int j = j0; j < j1; ++j, ++it) {
                 const int b = it & 1;
@@ -649,54 +727,6 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                     break;
                 tc_fence_after();
                 const int k0 = j * kKeys;
-                // V of this tile, where it reaches past the context: rows behind the
-                // sequence are zeroed, tree nodes cleared of NaN and infinities.
-                auto clean_v = [&]() -> bool {
-                    const int st = it % L::kVSlots;
-                    if (!all_wait(&sy.v_full[st], (uint32_t)(it / L::kVSlots) & 1u)) return false;
-                    uint8_t *vs = sV + st * L::kVTile;
-                    const int r0 = max(ctx - k0, 0), r1 = min(si.len - k0, kKeys);
-                    bool bad = false;
-                    // Two threads per key, each half of its 16-byte chunks.
-                    const int r = row & (kKeys - 1);
-                    uint8_t *at0 = vs + (r >> 3) * L::kGroup + (r & 7) * 128;
-#pragma unroll 4
-                    for (int c = 0; c < 4 * L::kPanels; ++c) {
-                        if (r < r0) break;
-                        const int e = (row / kKeys) * 4 * L::kPanels + c;
-                        uint4 *at = reinterpret_cast<uint4 *>(at0 + (e >> 3) * L::kPanel +
-                                                              (e & 7) * 16);
-                        if (r >= r1) {
-                            *at = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint4 v = *at;
-                        constexpr uint32_t kExp = KV8 ? 0x7C00u : 0x7F80u;
-                        bool hit = false;
-                        auto clear = [&](uint32_t x) {
-                            if ((x & kExp) == kExp) {
-                                x &= 0xffff0000u;
-                                hit = true;
-                            }
-                            if ((x & (kExp << 16)) == (kExp << 16)) {
-                                x &= 0x0000ffffu;
-                                hit = true;
-                            }
-                            return x;
-                        };
-                        v.x = clear(v.x);
-                        v.y = clear(v.y);
-                        v.z = clear(v.z);
-                        v.w = clear(v.w);
-                        if (hit) {
-                            *at = v;
-                            bad = true;
-                        }
-                    }
-                    if (bad) atomicExch(&sy.bad[seg & 1], seg);
-                    fence_proxy_async_smem();
-                    return true;
-                };
                 const bool past = k0 + kKeys > ctx;
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, nm = 0.f, cr = 1.f;
                 bool rescale = false;
@@ -783,7 +813,6 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                     }
                     tc_wait_st();
                 }
-                if (past && !(ok = clean_v())) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sy.p_full[b]);
@@ -793,9 +822,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             // scores are all read).
             if (more) load_q();
             bool bad = false;
-            if (tree) {  // did any warp find NaN or infinities in the tree's V?
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sy.sane);
+            if (tree) {  // NaN or infinities in the tree's V?
                 if (!(ok = all_wait(&sy.sane, sane_par))) break;
                 sane_par ^= 1u;
                 bad = *reinterpret_cast<volatile int *>(&sy.bad[seg & 1]) == seg;
