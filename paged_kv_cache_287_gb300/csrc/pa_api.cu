@@ -726,9 +726,9 @@ static pa_status tree_attention_impl(void *out, const void *q, const int32_t *cu
         !aligned(seq_lens, 4))
         return PA_ERR_INVALID_ARG;
     if (max_seq_len > (long long)max_blocks_per_seq * block_size) return PA_ERR_INVALID_ARG;
-    // Tile indices over (sequence, KV head, 16 tokens at least) fit 31 bits.
+    // Units of work over (sequence, KV head), tiles and more, fit 31 bits.
     if ((long long)num_seqs * num_kv_heads *
-            (((long long)max_blocks_per_seq * block_size + 15) / 16) >= (1LL << 31))
+            ((long long)max_blocks_per_seq * block_size / 16 + 8) >= (1LL << 31))
         return PA_ERR_UNSUPPORTED;
     const size_t need = pa::tree_attention_workspace_bytes(
         num_seqs, max_tree_len, num_heads / num_kv_heads, head_size, pa::device_sm_count());

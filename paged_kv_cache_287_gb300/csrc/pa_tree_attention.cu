@@ -41,6 +41,9 @@ __device__ unsigned g_err_tree_attention;
 constexpr int kRows = 128;  // query rows per tile (the MMA's M)
 constexpr int kKeys = 64;   // keys per K/V tile
 constexpr int kWholeTiles = 6;  // longest segment (in tiles) that is never split
+// A worker's change to another segment (queries, epilogue) takes as long as this many
+// tiles; ranges are cut with that weight when they are at least kLongRange tiles long.
+constexpr int kLongRange = 12;
 constexpr float kSlack = 8.0f;
 constexpr uint32_t kCols = 256, kColO = 128;  // tensor memory: two S / P tiles, then O
 
@@ -64,6 +67,7 @@ struct TreeAttnArgs {
     int row_groups;  // CTAs per worker
     int workers;
     int whole_segments;  // ranges hold whole segments: nothing to merge
+    int change;          // units of a change of segment
     int negate_q;
     float scale_log2;  // |scale| * log2(e), at least 1e-30
     float k_scale, v_scale;
@@ -103,7 +107,7 @@ struct Sync {
     uint64_t q_full, o_free, sane, drain;
     uint32_t tmem;
     int start[2], range[2], bad[2];
-    int part[10];
+    unsigned long long part[10];
 };
 static_assert(sizeof(Sync) <= 512, "the barriers' room");
 
@@ -128,7 +132,8 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs &a, int s) {
 // The segments of a worker's range, walked by a whole warp in step: the sequences'
 // data come 32 at a time, one per lane.
 struct Walk {
-    int s, pre, x, end;        // sequence, tiles (per head) before it, position, range end
+    int s, pre, x, end;        // sequence, units (per head) before it, position, range end
+    int extra;                 // units of a segment besides its tiles
     int begin, at;             // the range's and the current segment's first position
     int base;                  // first sequence of the window
     SeqInfo mine;              // sequence base + lane
@@ -141,7 +146,8 @@ struct Walk {
         mine = i < a.t.num_seqs ? seq_info(a, i) : SeqInfo{0, 0, 0};
     }
     __device__ __forceinline__ void start(const TreeAttnArgs &a, int s0, int pre0, int x0,
-                                          int x1) {
+                                          int x1, int change) {
+        extra = change;
         s = s0;
         pre = pre0;
         x = begin = x0;
@@ -156,17 +162,21 @@ struct Walk {
             cur.n = __shfl_sync(0xffffffffu, mine.n, s - base);
             cur.len = __shfl_sync(0xffffffffu, mine.len, s - base);
             nt = cur.tiles();
+            const int units = nt ? nt + extra : 0;
             const int r = x - a.num_kv_heads * pre;
-            if (r >= a.num_kv_heads * nt) {
-                pre += nt;
+            if (r >= a.num_kv_heads * units) {
+                pre += units;
                 ++s;
                 continue;
             }
-            h = r / nt;
-            j0 = r - h * nt;
-            j1 = min(nt, j0 + end - x);
+            // Units [u0, u1) of the segment: first the change to it, then its tiles.
+            h = r / units;
+            const int u0 = r - h * units, u1 = min(units, u0 + end - x);
             at = x;
-            x += j1 - j0;
+            x += u1 - u0;
+            j0 = max(0, u0 - extra);
+            j1 = max(0, u1 - extra);
+            if (j0 >= j1) continue;
             if (cur.n > rg * a.q_tile) return true;
         }
         return false;
@@ -225,60 +235,70 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         tmem_relinquish();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // Tiles per head over all sequences, and the sequences that hold this range's start
-    // and end: every thread sums a contiguous share of the sequences.
-    int t_begin, t_end;
+    // Units of work per head over all sequences (a segment's tiles, and the change to it),
+    // and the sequences that hold this range's start and end: every thread sums a
+    // contiguous share of the sequences, tiles and sequences with tiles in one number.
+    int t_begin, t_end, change;
     {
         const int per = (B + L::kThreads - 1) / L::kThreads;
         const int s0 = min(B, tid * per), s1 = min(B, s0 + per);
-        int sum = 0;
-        for (int s = s0; s < s1; ++s) sum += seq_info(a, s).tiles();
-        int incl = sum;
+        unsigned long long sum = 0;
+        for (int s = s0; s < s1; ++s) {
+            const int nt = seq_info(a, s).tiles();
+            sum += nt ? (1ull << 32) + nt : 0ull;
+        }
+        unsigned long long incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            const unsigned long long u = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += u;
         }
         if (lane == 31) sy.part[warp] = incl;
         if (tid == 0) sy.start[0] = -1;
         __syncthreads();
-        int before = 0, total = 0;
+        unsigned long long before = 0, total = 0;
         for (int w = 0; w < L::kThreads / 32; ++w) {
             if (w < warp) before += sy.part[w];
             total += sy.part[w];
         }
-        const long long T = (long long)total * Hkv;
+        const long long tiles = (long long)(total & 0xffffffffu) * Hkv;
+        change = tiles >= (long long)kLongRange * a.workers ? a.change : 0;
+        auto units = [&](unsigned long long v) {
+            return (int)(v & 0xffffffffu) + change * (int)(v >> 32);
+        };
+        const long long T = (long long)units(total) * Hkv;
         const long long We = a.workers < T ? a.workers : (T > 0 ? T : 1);
         t_begin = worker < We ? (int)(worker * T / We) : 0;
         t_end = worker < We ? (int)((worker + 1) * T / We) : 0;
-        const int pre = before + incl - sum;
+        const int pre = units(before + incl - sum), mine = units(sum);
         // The sequence at position x < T lies in one thread's share.
         auto holds = [&](int x) {
-            return x >= (long long)Hkv * pre && x < (long long)Hkv * (pre + sum);
+            return x >= (long long)Hkv * pre && x < (long long)Hkv * (pre + mine);
         };
-        auto find = [&](int x, int &s, int &p, int &nt) {
-            for (s = s0, p = pre;; ++s, p += nt) {
-                nt = seq_info(a, s).tiles();
-                if (x < (long long)Hkv * (p + nt)) return;
+        auto find = [&](int x, int &s, int &p, int &n) {
+            for (s = s0, p = pre;; ++s, p += n) {
+                const int nt = seq_info(a, s).tiles();
+                n = nt ? nt + change : 0;
+                if (x < (long long)Hkv * (p + n)) return;
             }
         };
         // Whole segments: a range starts at the first segment start at or after its share's.
-        auto snap = [&](int x, int p, int nt) {
-            const int r = (x - Hkv * p) % nt;
-            return r ? x + nt - r : x;
+        auto snap = [&](int x, int p, int n) {
+            const int r = (x - Hkv * p) % n;
+            return r ? x + n - r : x;
         };
         if (tid == 0) sy.range[1] = t_end;
         if (a.whole_segments) __syncthreads();
-        int s, p, nt;
+        int s, p, n;
         if (t_begin < t_end && holds(t_begin)) {
-            find(t_begin, s, p, nt);
+            find(t_begin, s, p, n);
             sy.start[0] = s;
             sy.start[1] = p;
-            sy.range[0] = a.whole_segments ? snap(t_begin, p, nt) : t_begin;
+            sy.range[0] = a.whole_segments ? snap(t_begin, p, n) : t_begin;
         }
         if (a.whole_segments && t_end < T && holds(t_end)) {
-            find(t_end, s, p, nt);
-            sy.range[1] = snap(t_end, p, nt);
+            find(t_end, s, p, n);
+            sy.range[1] = snap(t_end, p, n);
         }
     }
     tc_fence_before();
@@ -295,8 +315,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         int4 st = make_int4(-1, 0, 0, 0);
         if (work) {
             const SeqInfo si = seq_info(a, seq0);
-            const int nt = si.tiles(), r = t_begin - Hkv * pre0;
-            st = make_int4(seq0, (r / nt) | si.n << 8, r % nt, si.row0);
+            const int n = si.tiles() + change, r = t_begin - Hkv * pre0;
+            st = make_int4(seq0, (r / n) | si.n << 8, max(0, r % n - change), si.row0);
         }
         a.starts[worker] = st;
     }
@@ -306,7 +326,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     } else if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end);
+        w.start(a, seq0, pre0, t_begin, t_end, change);
         const int bs = a.block_size, nbox = kKeys / bs;  // a box per block
         const int v_off = Hkv * bs;
         const uint64_t policy = policy_evict_first();
@@ -402,7 +422,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end);
+        w.start(a, seq0, pre0, t_begin, t_end, change);
         const uint32_t idesc_s =
             KV8 ? tc_idesc_e4m3(kRows, kKeys) : tc_idesc_bf16(kRows, kKeys, 0);
         const uint32_t idesc_pv = KV8 ? tc_idesc_f16(kRows, D, 1) : tc_idesc_bf16(kRows, D, 1);
@@ -537,7 +557,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     } else if (warp < 6) {
         // ------------------------------------------------------------ softmax
         Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end);
+        w.start(a, seq0, pre0, t_begin, t_end, change);
         const int row = 32 * (warp & 3) + lane;  // TMEM lane = query row of the tile
         const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int r_node = row / G, r_head = row - r_node * G;
@@ -563,7 +583,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         // a row with NaN or infinities becomes NaN through it.
         auto load_q = [&]() {
             constexpr int kC = D / 8, kR = 32 / kC;  // chunks of a row, rows at a time
-            constexpr int kBatch = KV8 ? 4 : 8;
+            constexpr int kBatch = 8;
             sl2 = a.scale_log2;
             if (__any_sync(0xffffffffu, real_in(w.cur))) {
                 const int c = lane % kC, row0 = row - lane + lane / kC;
@@ -907,7 +927,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         // A lane converts a key's 128 codes (128B-swizzled as TMA left them) to f16 in the
         // layout a bf16 tile has.
         Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end);
+        w.start(a, seq0, pre0, t_begin, t_end, change);
         const int r = (warp - 6) * 32 + lane;
         auto tile = [&](int i) -> bool {
             const int ss = i % L::kStages, st = i % L::kVSlots;
@@ -1150,6 +1170,10 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
     // Contexts of a few tiles: a range of whole segments costs at most those tiles (about
     // 0.6 us each) and saves the merge's launch.
     a.whole_segments = max_seq_len <= kWholeTiles * kKeys;
+    // Measured: about 7000 cycles a change; a tile takes 2400 where HBM bounds it (3: 32
+    // sequences 62.4 -> 60.1 us), 1600 from an FP8 pool or with several row groups, which
+    // the tensor pipe bounds (8: 64 FP8 chains 96 -> 83 us, 16 wide trees 158 -> 145).
+    a.change = kv8 || sh.row_groups > 1 ? 8 : 3;
     if (kv8) return launch<128, true>(map, a, stream);
     if (g.head_size == 128) return launch<128, false>(map, a, stream);
     return launch<64, false>(map, a, stream);
