@@ -477,8 +477,8 @@ pa_status pa_tree_attention(void *out, const void *q, const int32_t *cu_tree_len
  * PA_ERR_UNSUPPORTED).  K is multiplied as codes, each query row (scaled by a power
  * of two) as the sum of two e4m3 rows: exact for elements down to 2^-9 of the row's
  * largest, within 2^-17 of the largest below.  V converts to f16 exactly, P is
- * rounded to f16.  Workspace: pa_tree_attention_workspace_bytes.  Other arguments, results and errors as
- * pa_tree_attention.
+ * rounded to f16.  Workspace: pa_tree_attention_workspace_bytes.  Other arguments,
+ * results and errors as pa_tree_attention.
  */
 pa_status pa_tree_attention_fp8(void *out, const void *q, const int32_t *cu_tree_lens,
                                 const int32_t *parents, int num_seqs, int total_nodes,
@@ -522,8 +522,9 @@ pa_status pa_tree_attention_fp8(void *out, const void *q, const int32_t *cu_tree
  *                 probability 0 and is flagged PA_ERR_OOB (the roots' are unread)
  *   accept_u      [total_nodes] fp32 in [0, 1) (the roots' are unread)
  *   sample_u      [num_seqs] fp32 in [0, 1)
- * Probabilities (finite, >= 0) are taken as they are, not normalised.  Sums and
- * differences carry at least 48 bits, so the result is that of the formulas.
+ * Probabilities (finite, >= 0) are taken as they are, not normalised.  Sums,
+ * differences and products carry some 47 bits: the result is the formulas' unless
+ * the two sides of a comparison agree to that.
  * vocab_size from 1 to 1048576 (else PA_ERR_UNSUPPORTED).  fp32 pointers must be
  * 4-byte aligned.  No workspace.  num_seqs == 0 is a no-op.
  */
@@ -549,7 +550,8 @@ pa_status pa_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t *next
  *                 skipped (its new length is its old one) and flagged PA_ERR_OOB
  *   new_seq_lens  [num_seqs] int32, written: seq_lens[s] - T + num_accepted[s];
  *                 may be NULL, must not be seq_lens
- * Bit-exact.  num_seqs == 0 is a no-op.
+ * The blocks a tree lies in must not be shared (neither with another sequence nor
+ * twice in one table), as for any write.  Bit-exact.  num_seqs == 0 is a no-op.
  */
 pa_status pa_tree_accept(void *kv_cache, int num_blocks, int block_size, int num_kv_heads,
                          int head_size, const int32_t *accepted, const int32_t *num_accepted,

@@ -5,29 +5,50 @@
 //   out = sum_t softmax_t(scale q.K_t) V_t,
 // computed in one pass over the keys with a running maximum m and sum l.
 //
+// Bound: every K and V row once per KV head, 4 Hkv D bytes a token from a bf16 pool; up to
+// some 60 rows per KV head HBM binds, with more the tensor pipe.
+//
 // Design (tcgen05)
 //   * A query tile is up to 128 rows: floor(128 / G) nodes times the G query heads
-//     of one KV head, so a K/V tile of 128 keys is fetched once for all of them.
-//     Trees of more rows have several row groups.
-//   * Work = the list of 128-key tiles over (sequence, KV head), cut into equal
-//     contiguous ranges, one per worker; a worker is one CTA per row group, and two
-//     CTAs share an SM (each with half of its shared memory and tensor memory), so
-//     that one CTA's loads and products run under the other's softmax.  A segment
-//     (sequence, KV head) that falls across ranges leaves its pieces' (m, l, O) in
-//     the workspace, merged by log-sum-exp in a second, dependent kernel; a segment
-//     that lies in one range is written at once.
-//   * warp 0 streams K and V tiles through the block table with 128B-swizzled TMA
-//     copies; warp 1 issues the products S = Q.K^T (shared memory) and O += P.V (P
-//     from tensor memory, in two 64-key halves); warps 2-5 hold one query row per
-//     thread: softmax, P written over its own scores, the O rescale (rare: only when
-//     a row's maximum rises by more than 2^8), the epilogue.  A warp whose 32 rows
-//     hold no query skips the softmax.  An FP8 pool's tiles land as codes in the
-//     upper half of their slot and two more warps convert them in place to f16.
+//     of one KV head, so a K/V tile of 64 keys is fetched once for all of them.
+//     Trees of more rows have several row groups, whose CTAs walk the same keys side
+//     by side (all but the first fetch of a tile hit L2).
+//   * Work = the list of tiles over (sequence, KV head), cut into equal contiguous
+//     ranges, one per worker; a worker is one CTA per row group, and two CTAs share an
+//     SM (each with half of its shared memory and tensor memory), so that one CTA's
+//     loads and products run under the other's softmax.  A segment (sequence, KV
+//     head) that falls across ranges leaves its pieces' (m, l, O) in the workspace,
+//     merged by log-sum-exp in a second, dependent kernel; a segment that lies in one
+//     range is written at once.
+//   * warp 0 streams K and V tiles through the block table, a block's rows of one head
+//     per copy (its 8-row groups and 64-dim panels in one 4-D box: with a 2-D copy per
+//     panel of 16 rows the copies' issue bounded the kernel at some 125 cycles each);
+//     the table entries are read a tile ahead.
+//   * One thread of warp 1 issues the products: S = Q.K^T into two buffers by turns, up
+//     to two tiles ahead, and O += P.V with P from tensor memory over its own scores.
+//     A product costs it 46 cycles (64 keys) to 64 (128 dims), a commit some 200, a
+//     wait by the whole warp 130: one commit per product group, waits by that thread
+//     alone (16 trees of 33-64 nodes, 8 heads per KV head: 183 -> 159 us).
+//   * Warps 2-5 hold one query row per thread: softmax, P, the O rescale (rare: only
+//     when a row's maximum rises by more than 2^8), the epilogue, the next segment's
+//     queries.  A warp whose 32 rows hold no query skips the softmax.
+//   * From an FP8 pool K is multiplied as codes, the query being the sum of two e4m3
+//     rows (load_q); only V is converted, to f16, by two more warps.  (Converting both
+//     left the converting warps the bound: 64 sequences' chains 118 us, now 81.)
 //   * Masks: a row's ancestors are a 64-bit word (pointer doubling over the parents,
 //     six shuffle rounds); only tiles that reach past the context look at it.  What
 //     a row does not see gets the score -inf, and V rows of tree nodes are cleared of
 //     NaN and infinities before the product (0 * NaN would reach every row); the rows
 //     that do see one get it added back in the epilogue.
+//   * Rounding: scores, statistics and O in fp32; P to bf16 (f16 from an FP8 pool) as the
+//     product's operand, the row sum from the fp32 values; the output once to bf16.
+//
+// Measured (GB300, HBM copy 6689 GB/s, whole call): 32 sequences of 512-4096 tokens with
+// 12-16 nodes, 32 query and 8 KV heads of 128: 60 us, 5.1 TB/s; 8 sequences of 1024-131072
+// tokens: 140 us, 6.2 TB/s; 16 sequences of 1024-8192 tokens, 33-64 nodes, 64 and 8 heads:
+// 145 us, 820 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool, 64
+// sequences, chains of 3-8: 81 us, 3.8 TB/s.  What is left in the first: some 4 us until the
+// first tile arrives, 5 us for the merge, the spread of the CTAs' ends.
 #include <algorithm>
 #include <cmath>
 
@@ -39,11 +60,14 @@ namespace {
 __device__ unsigned g_err_tree_attention;
 
 constexpr int kRows = 128;  // query rows per tile (the MMA's M)
-constexpr int kKeys = 64;   // keys per K/V tile
+// Keys per K/V tile: two buffers of scores beside O fit half of tensor memory.  (One of 128
+// keys makes each tile a chain scores -> softmax -> output -> scores: 60 -> 81 us.)
+constexpr int kKeys = 64;
 constexpr int kWholeTiles = 6;  // longest segment (in tiles) that is never split
 // A worker's change to another segment (queries, epilogue) takes as long as this many
 // tiles; ranges are cut with that weight when they are at least kLongRange tiles long.
 constexpr int kLongRange = 12;
+// The exponent's reference rises only when a score exceeds it by this (log2 units).
 constexpr float kSlack = 8.0f;
 constexpr uint32_t kCols = 256, kColO = 128;  // tensor memory: two S / P tiles, then O
 
@@ -206,7 +230,6 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     const int Hkv = a.num_kv_heads, B = a.t.num_seqs, G = a.group, QT = a.q_tile;
 
     // What needs no memory of the caller's, under the end of the launch before this one.
-    asm volatile("griddepcontrol.launch_dependents;" :::);
     if (tid == 0) {
         prefetch_tensormap(&kv_map);
         for (int i = 0; i < L::kKSlots; ++i) {
@@ -230,11 +253,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         sy.bad[0] = sy.bad[1] = -1;
         fence_barrier_init();
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Tensor memory is taken after the launch before this one has ended, and the next one may
+    // begin once this CTA has its own: a kernel that held some while it waits for the
+    // other's end could keep the other from ever getting it.
     if (warp == 1) {
         tmem_alloc(&sy.tmem, kCols);
         tmem_relinquish();
+        asm volatile("griddepcontrol.launch_dependents;" :::);
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // Units of work per head over all sequences (a segment's tiles, and the change to it),
     // and the sequences that hold this range's start and end: every thread sums a
     // contiguous share of the sequences, tiles and sequences with tiles in one number.
@@ -907,8 +934,10 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                                       (rec * (D / 4) + 8 * c) * a.part_rows + row;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            st_hint(dst + e * a.part_rows, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2],
-                                                         o[4 * e + 3]), keep);
+                            st_hint(dst + e * a.part_rows,
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                                                o[4 * e + 3]),
+                                    keep);
                     }
                     __syncwarp();
                 }

@@ -6,21 +6,31 @@
 // u_c Z < r(t), else r(t) := 0, Z -= r(t)).  When no child is accepted the next
 // token is the smallest x with r(0) + .. + r(x) > u sum r.
 //
+// Bound: one row of p (and of q) per sequence for the draw, 4 or 8 bytes a token of the
+// vocabulary, from HBM; with few sequences the chain of dependent steps.
+//
 // Split: a cluster of CTAs per sequence, each over a contiguous slice of the
 // vocabulary, each warp over a contiguous part of the slice.  Warp 0 of every CTA
-// makes the same walk over the tree's scalars (gathered once by 64 threads); only a
-// rejection with draft probabilities and the final draw touch the vocabulary, by one
-// coalesced pass that recomputes r from p and q (nothing of the vocabulary's size is
-// kept between passes: a second pass over the same rows hits L2) and leaves each
-// warp's sum.  CTA sums cross the cluster through distributed shared memory, in rank
-// order, so every CTA continues with the same bits.  For the draw the warp that holds
-// the goal scans its own part: 32 contiguous shares, then the share that holds it.
+// makes the same walk over the tree's scalars (gathered once by 64 threads, two nodes a
+// lane; children are found by ballots, and a child that is the first to be tried, or all
+// children without draft probabilities, are decided at once).  Only a rejection with draft
+// probabilities and the final draw touch the vocabulary, by one coalesced pass that leaves
+// each warp's sum.  Where the slice fits, r and q stay in shared memory between rejections
+// at a node; else r is recomputed from p and q.  CTA sums cross the cluster through
+// distributed shared memory, in rank order, so every CTA continues with the same bits.  For
+// the draw the CTA and the warp's part that hold the goal are scanned again.
 //
 // Precision: whole numbers come out, so a sum must not be off by what separates
 // neighbouring tokens.  r and its sums are held as unevaluated pairs of fp32 numbers
 // (a head and the rounding error of the operation before; about 48 bits), since this
 // GPU's 64-bit units are some 60 times slower than its 32-bit ones: one CTA of 64-bit
-// sums took 1433 us where the batch's bytes take 40 (256 chains, 131072 tokens).
+// sums took 1433 us where the batch's bytes take 40 (256 chains, 131072 tokens), and
+// 64-bit sums across the 16 warps of each CTA alone some 2 us a pass.
+//
+// Measured (GB300): those 256 chains 56 us, 4.8 TB/s; 48 trees of 9-31 nodes with sibling
+// rounds, 50021 tokens, 28 us; 64 trees of 33-64 proposed nodes, 131072 tokens, 23 us; one
+// chain of 6, 32000 tokens, 7 us (13 000 cycles: gathers 2000, walk 1200, pass 3000, cluster
+// sum 2000, draw 4500).
 #include <algorithm>
 
 #include "pa_tree.cuh"
@@ -554,7 +564,7 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps) tree_verify_kernel(c
             last = __shfl_sync(0xffffffffu, tok, hit);
             if (found) break;
         }
-        if (lane == 0) a.next[s] = last;
+        if (lane == 0) a.next[s] = min(last, V - 1);
         return;
     }
     // Nothing left to draw from: the lowest token of the largest p.
@@ -625,7 +635,9 @@ cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t
     a.vocab = vocab;
     // CTAs per sequence: all of the batch resident at once (two per SM; with draft
     // probabilities up to three, since sequences end after very different numbers of
-    // passes: 48 trees, 50021 tokens, 41 us with 8 CTAs each, 63 with 4), each with at least 2048 tokens, and slices whose bit sets fit 32 KB.
+    // passes: 48 trees, 50021 tokens, 41 us with 8 CTAs each, 63 with 4 before r was
+    // kept between rejections), each with at least 2048 tokens, and slices whose bit
+    // sets fit 32 KB.
     const int sms = device_sm_count();
     const long long room = (draft ? 3LL : 2LL) * sms;
     int c = 1;

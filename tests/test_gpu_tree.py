@@ -302,6 +302,73 @@ def test_attention_on_a_side_stream_and_in_two_graphs():
     _tree.assert_attention(outs[0], *a.reference())
 
 
+def test_attention_of_sequences_that_share_their_prefix_blocks():
+    """The same blocks in every table, split contexts and tiles of the trees' own."""
+    Case([1024 + c for c in (0, 5, 64, 700)], [3, 64, 17, 1], 8, 2, 128, 16, seed=17,
+         shared_prefix_blocks=64).check()
+
+
+@pytest.mark.parametrize("ctx_max,fp8", [(40, False), (40, True), (900, False)])
+def test_attention_of_thousands_of_small_trees(ctx_max, fp8):
+    """Batches of more sequences than workers, a fifth of them empty and padded."""
+    rng = np.random.default_rng(18)
+    B = 2500 if ctx_max == 40 else 600
+    T = (rng.integers(0, 5, B)).tolist()
+    ctx = [int(rng.integers(0, ctx_max + 1)) if t else 0 for t in T]
+    Case(ctx, T, 2, 1, 128, 16, seed=18, fp8=fp8).check()
+
+
+def test_tree_calls_beside_others_on_two_streams():
+    """Calls that overlap on the GPU, with workspaces of their own, and the chunked prefill
+    beside them: the same bits as one after the other."""
+    a = Case([3000, 40, 900], [40, 64, 16], 8, 2, 128, 16, seed=19)
+    b = Case([2000, 2100], [9, 12], 4, 4, 64, 16, seed=20)
+    p = make_batch(name="chunks", seq_lens=[900, 300], q_lens=[600, 300], num_heads=8,
+                   num_kv_heads=2, head_size=64, block_size=16, scale=0.125, seed=22, device=DEV)
+    gpu_write(p)
+    max_q = int(p.q_lens.max())
+    d = _tree.random_drafts(23, [20, 3], 40000, True)
+    args = [x.to(DEV) for x in (d.target, d.draft, d.tokens, d.cu, d.parents, d.accept_u,
+                                d.sample_u)]
+    acc = torch.empty(2, 20, dtype=I32, device=DEV)
+    num, nxt = (torch.empty(2, dtype=I32, device=DEV) for _ in range(2))
+    pre = torch.empty_like(p.q)
+
+    def first(out, ws):
+        a.run(out=out, ws=ws)
+        binding.pa_tree_verify(acc, num, nxt, *args)
+        a.run(out=out, ws=ws)
+
+    def second(out, ws):
+        b.run(out=out, ws=ws)
+        binding.pa_prefill_chunk(pre, p.q, p.cu_q_lens, max_q, p.kv_cache, p.block_tables,
+                                 p.seq_lens, p.scale)
+        b.run(out=out, ws=ws)
+
+    work = [(first, a), (second, b)]
+    bufs = [(torch.empty_like(c.b.q), c.workspace()) for _, c in work]
+    for (f, _), x in zip(work, bufs):
+        f(*x)
+    torch.cuda.synchronize()
+    want = [x[0].clone() for x in bufs] + [pre.clone(), acc.clone(), num.clone(), nxt.clone()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for t in (bufs[0][0], bufs[1][0], pre):
+            t.fill_(float("nan"))
+        acc.zero_()
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for _ in range(4):
+            for s, (f, _), x in zip(streams, work, bufs):
+                with torch.cuda.stream(s):
+                    f(*x)
+        torch.cuda.synchronize()
+        got = [bufs[0][0], bufs[1][0], pre, acc, num, nxt]
+        for g, w in zip(got, want):
+            assert torch.equal(g.view(torch.int16), w.view(torch.int16))
+    assert nxt.tolist() == d.reference[1]
+
+
 # ---------------------------------------------------------------- verification
 def run_verify(d, stream=None, max_tree=None, pad=0):
     """The call's (paths, next tokens), checked for its padding."""
