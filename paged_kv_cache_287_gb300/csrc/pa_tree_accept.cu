@@ -13,9 +13,9 @@
 // of (accepted - 1) * 2 * Hkv * D * element bytes each way.
 //
 // Bound: a chain of dependent reads (lengths, path, block table, rows), not the bytes: 256
-// paths of up to 33 nodes, 8 heads of 128, move 8 MB in 6 us on the device, in a call
-// whose arguments' checks take 14 us of the host.  Eight rows in flight per thread cover
-// the rows' latency (paths of more than nine nodes take it twice).
+// paths of 1 to 9 nodes, 8 heads of 128, read and write 8 MB in some 6 us on the device,
+// in a call whose arguments' checks take the host longer.  Eight rows in flight per thread
+// cover the rows' latency (paths of more than nine nodes take it twice).
 #include <algorithm>
 
 #include "pa_tree.cuh"

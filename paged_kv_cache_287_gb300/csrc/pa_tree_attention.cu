@@ -11,10 +11,10 @@
 // Design (tcgen05)
 //   * A query tile is up to 128 rows: floor(128 / G) nodes times the G query heads
 //     of one KV head, so a K/V tile of 64 keys is fetched once for all of them.
-//     Trees of more rows have several row groups, whose CTAs walk the same keys side
-//     by side (all but the first fetch of a tile hit L2).
-//   * Work = the list of tiles over (sequence, KV head), cut into equal contiguous
-//     ranges, one per worker; a worker is one CTA per row group, and two CTAs share an
+//     Trees of more rows have several row groups, whose CTAs (a team) walk the same keys
+//     side by side (all but the first fetch of a tile hit L2).
+//   * Work = the list of tiles over (sequence, KV head), a list per number of row groups,
+//     each cut into equal contiguous ranges, one per team.  Two CTAs share an
 //     SM (each with half of its shared memory and tensor memory), so that one CTA's
 //     loads and products run under the other's softmax.  A segment (sequence, KV
 //     head) that falls across ranges leaves its pieces' (m, l, O) in the workspace,
@@ -63,8 +63,9 @@ constexpr int kRows = 128;  // query rows per tile (the MMA's M)
 // Keys per K/V tile: two buffers of scores beside O fit half of tensor memory.  (One of 128
 // keys makes each tile a chain scores -> softmax -> output -> scores: 60 -> 81 us.)
 constexpr int kKeys = 64;
+constexpr int kGroups = 4;  // row groups, at most: 64 nodes x 8 heads
 constexpr int kWholeTiles = 6;  // longest segment (in tiles) that is never split
-// A worker's change to another segment (queries, epilogue) takes as long as this many
+// A CTA's change to another segment (queries, epilogue) takes as long as this many
 // tiles; ranges are cut with that weight when they are at least kLongRange tiles long.
 constexpr int kLongRange = 12;
 // The exponent's reference rises only when a score exceeds it by this (log2 units).
@@ -77,19 +78,19 @@ struct TreeAttnArgs {
     const void *kv;
     const int32_t *block_tables, *seq_lens;
     TreeGeom t;
-    // [workers] where each range starts: (sequence, KV head | tree nodes << 8, tile, first
-    // node row).
+    // [ctas] where each range starts: (sequence, KV head | tree nodes << 8 | row group << 16,
+    // tile, first node row).
     int4 *starts;
-    float *part_ml;  // [2 * CTAs][part_rows][2]: m (log2 units), l
-    // [2 * CTAs][D / 4][part_rows][4]: a thread holds a row, so the lanes of a store (and of
+    float *part_ml;  // [2 * ctas][part_rows][2]: m (log2 units), l
+    // [2 * ctas][D / 4][part_rows][4]: a thread holds a row, so the lanes of a store (and of
     // the merge's loads) lie side by side.
     float *part_acc;
     int part_rows;
     int num_heads, num_kv_heads, group;
     int block_size, max_blocks, num_blocks, max_len;
     int q_tile;      // nodes per query tile: floor(128 / group)
-    int row_groups;  // CTAs per worker
-    int workers;
+    int row_groups;  // of the largest tree
+    int ctas;
     int whole_segments;  // ranges hold whole segments: nothing to merge
     int change;          // units of a change of segment
     int negate_q;
@@ -97,7 +98,8 @@ struct TreeAttnArgs {
     float k_scale, v_scale;
 };
 
-template <int D, bool KV8>
+// Two: queries of up to 64 rows, held twice.
+template <int D, bool KV8, bool Two>
 struct Tlay {
     static constexpr int kPanels = D / 64;
     static constexpr int kQPanel = kRows * 128;  // 64 dims of 128 rows
@@ -115,11 +117,27 @@ struct Tlay {
     static constexpr int kGroup = 1024 * kPanels;
     static constexpr int kPanel = 1024;
     static constexpr int kConv = KV8 ? 2 : 0;  // converting warps
-    static constexpr int kThreads = (6 + kConv) * 32;
+    static constexpr int kThreads = (KV8 ? 8 : Two ? 6 : 7) * 32;
     static constexpr int kK = kQ, kV = kK + kKSlots * kKTile, kCodes = kV + kVSlots * kVTile;
     static constexpr int kOperands = kCodes + kStages * kStage;
-    static constexpr size_t kSmem = (size_t)kOperands + 512;  // + barriers
+    static constexpr size_t kSmem = (size_t)kOperands + 1024;  // + barriers
 };
+
+// A segment of a CTA's range: tiles [j0, j1) of KV head h of sequence s, for row group rg.
+// The range ends with one of no tiles.
+struct Seg {
+    int s, row0, len, n_h_first;  // n | h << 8 | (the range starts in it) << 16 | rg << 17
+    int j0, j1;
+    __device__ __forceinline__ int n() const { return n_h_first & 255; }
+    __device__ __forceinline__ int h() const { return (n_h_first >> 8) & 255; }
+    __device__ __forceinline__ bool first() const { return (n_h_first >> 16) & 1; }
+    __device__ __forceinline__ int rg() const { return n_h_first >> 17; }
+};
+
+// Segments in flight, at most: the producer publishes a segment when it opens the one
+// before it, one tile ahead of its copies.  A copy of V waits for the output of at most
+// seven tiles before, and that for every warp's P, so at most nine segments are unread.
+constexpr int kSegs = 16;
 
 // What follows the operands in shared memory.
 struct Sync {
@@ -128,12 +146,14 @@ struct Sync {
     // by i % V slots: its V slot is free too.  (A commit costs the issuing thread some 200
     // cycles, as much as four products, so one serves both.)
     uint64_t s_full[4], pv_done[4], p_full[2];
-    uint64_t q_full, o_free, sane, drain;
+    uint64_t q_full[2], q_free[2], o_free, sane[4], drain;
+    uint64_t seg_full[kSegs];
     uint32_t tmem;
-    int start[2], range[2], bad[2];
-    unsigned long long part[10];
+    int bad[4];
+    uint8_t q_exp[2][64];  // an FP8 pool's queries: exponent + 127 of each row's scale
+    Seg seg[kSegs];
 };
-static_assert(sizeof(Sync) <= 512, "the barriers' room");
+static_assert(sizeof(Sync) <= 1024, "the barriers' room");
 
 // Sequence s as this kernel sees it: no tiles where its data break the bounds.
 struct SeqInfo {
@@ -153,39 +173,172 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs &a, int s) {
     return {t.row0, t.n, len};
 }
 
-// The segments of a worker's range, walked by a whole warp in step: the sequences'
-// data come 32 at a time, one per lane.
+// Row groups of a tree of n nodes.
+__device__ __forceinline__ int groups_of(const TreeAttnArgs &a, int n) {
+    return a.row_groups == 1 ? 1 : (n + a.q_tile - 1) / a.q_tile;
+}
+
+// This CTA's range, walked by a whole warp in step: the sequences' data come 32 at a time,
+// one per lane.
+//
+// The work of sequences with as many row groups is a list (per segment the change to it and
+// its tiles), shared out evenly over teams of one CTA per row group, and the CTAs are shared
+// out over those lists by their work.
 struct Walk {
     int s, pre, x, end;        // sequence, units (per head) before it, position, range end
     int extra;                 // units of a segment besides its tiles
     int begin, at;             // the range's and the current segment's first position
-    int base;                  // first sequence of the window
+    int base;                  // first sequence of the window, a multiple of 32
+    int groups, rg;            // row groups of the sequences walked, this CTA's
     SeqInfo mine;              // sequence base + lane
+    int mine_nt;               // its tiles (0: other row groups)
     int h, j0, j1, nt;         // the current segment's head, tiles [j0, j1) of nt
     SeqInfo cur;
+    SeqInfo four[4];           // sequences four0 + lane, + 32, ..
+    int four0;
 
+    __device__ __forceinline__ void load(const TreeAttnArgs &a, int s0) {
+        four0 = s0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = s0 + 32 * u + (int)(threadIdx.x & 31);
+            four[u] = i < a.t.num_seqs ? seq_info(a, i) : SeqInfo{0, 0, 0};
+        }
+    }
+    __device__ __forceinline__ int tiles_of(const TreeAttnArgs &a, const SeqInfo &si) const {
+        return groups_of(a, si.n) == groups ? si.tiles() : 0;
+    }
     __device__ __forceinline__ void window(const TreeAttnArgs &a, int s0) {
         base = s0;
         const int i = s0 + (int)(threadIdx.x & 31);
         mine = i < a.t.num_seqs ? seq_info(a, i) : SeqInfo{0, 0, 0};
+        mine_nt = tiles_of(a, mine);
     }
-    __device__ __forceinline__ void start(const TreeAttnArgs &a, int s0, int pre0, int x0,
-                                          int x1, int change) {
-        extra = change;
-        s = s0;
-        pre = pre0;
-        x = begin = x0;
-        end = x1;
-        window(a, s0);
+
+    // To the range's start; load(a, 0) comes before.
+    __device__ __forceinline__ void start(const TreeAttnArgs &a) {
+        const int lane = threadIdx.x & 31, Hkv = a.num_kv_heads, B = a.t.num_seqs;
+        // Per number of row groups the tiles (below 2^31 with all heads) and sequences.
+        int tiles[kGroups] = {}, seqs[kGroups] = {};
+        for (int b0 = 0; b0 < B; b0 += 128) {
+            if (b0) load(a, b0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int nt = four[u].tiles(), c = groups_of(a, four[u].n);
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k)
+                    if (nt && c == k + 1) {
+                        tiles[k] += nt;
+                        ++seqs[k];
+                    }
+            }
+        }
+        long long all_tiles = 0;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            if (k >= a.row_groups) break;
+            tiles[k] = __reduce_add_sync(0xffffffffu, tiles[k]);
+            seqs[k] = __reduce_add_sync(0xffffffffu, seqs[k]);
+            all_tiles += (long long)tiles[k] * (Hkv * (k + 1));
+        }
+        extra = all_tiles >= (long long)kLongRange * a.ctas ? a.change : 0;
+        // This CTA's list and team.  A list gets the teams that its work comes to, rounded
+        // up (a short one would else take twice as long), the longest what is left.
+        int teams = a.ctas, team = blockIdx.x, total = tiles[0] + extra * seqs[0];
+        groups = 1;
+        rg = 0;
+        if (a.row_groups > 1) {
+            int units[kGroups], n[kGroups], big = 0, rest = 0, left = a.ctas, at_cta = team;
+            float all = 0.f, most = 0.f;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                units[k] = tiles[k] + extra * seqs[k];
+                const float u = (float)units[k] * (float)(k + 1);
+                if (u > most) big = k;
+                most = fmaxf(most, u);
+                all += u;
+                rest += units[k] ? k + 1 : 0;
+            }
+            const float per = (float)a.ctas / all;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                n[k] = 0;
+                if (k == big || !units[k]) continue;
+                rest -= k + 1;  // one team of each list that is still to come
+                n[k] = max(1, min((int)ceilf(per * (float)units[k]), (left - rest) / (k + 1)));
+                left -= n[k] * (k + 1);
+            }
+            team = teams;  // left over
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                if (k == big) n[k] = left / (k + 1);
+                if (at_cta >= 0 && at_cta < n[k] * (k + 1)) {
+                    groups = k + 1;
+                    teams = n[k];
+                    total = units[k];
+                    team = at_cta / (k + 1);
+                    rg = at_cta - team * (k + 1);
+                }
+                at_cta -= n[k] * (k + 1);
+            }
+        }
+        // The first total % teams get one more.
+        const int T = total * Hkv, share = T / teams, more = T - share * teams;
+        begin = x = team < teams ? team * share + min(team, more) : 0;
+        end = team < teams ? begin + share + (team < more ? 1 : 0) : 0;
+        s = pre = base = 0;
+        if (x >= end) return;
+        // The sequence that holds x: its 128, its 32, itself.
+        for (int b0 = 0; b0 < B; b0 += 128) {
+            if (four0 != b0) load(a, b0);
+            int units[4], sum[4], block = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int nt = tiles_of(a, four[u]);
+                units[u] = nt ? nt + extra : 0;
+                sum[u] = __reduce_add_sync(0xffffffffu, units[u]);
+                block += sum[u];
+            }
+            if (x >= Hkv * (pre + block)) {
+                pre += block;
+                continue;
+            }
+            int mine_units = units[0];
+            base = b0;
+            mine = four[0];
+            bool here = x < Hkv * (pre + sum[0]);
+#pragma unroll
+            for (int u = 1; u < 4; ++u) {
+                if (here) continue;
+                pre += sum[u - 1];
+                here = x < Hkv * (pre + sum[u]);
+                base = b0 + 32 * u;
+                mine = four[u];
+                mine_units = units[u];
+            }
+            mine_nt = mine_units ? mine_units - extra : 0;
+            int incl = mine_units;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, x < Hkv * (pre + incl));
+            const int at_lane = __ffs((int)past) - 1;
+            s = base + at_lane;
+            pre += __shfl_sync(0xffffffffu, incl - mine_units, at_lane);
+            return;
+        }
+        x = end;  // (not reached)
     }
-    // The next segment with rows for row group rg; false at the range's end.
-    __device__ __forceinline__ bool next(const TreeAttnArgs &a, int rg) {
+    // The next segment; false at the range's end.
+    __device__ __forceinline__ bool next(const TreeAttnArgs &a) {
         while (x < end) {
-            if (s - base >= 32) window(a, s);
+            if (s - base >= 32) window(a, s & ~31);
             cur.row0 = __shfl_sync(0xffffffffu, mine.row0, s - base);
             cur.n = __shfl_sync(0xffffffffu, mine.n, s - base);
             cur.len = __shfl_sync(0xffffffffu, mine.len, s - base);
-            nt = cur.tiles();
+            nt = __shfl_sync(0xffffffffu, mine_nt, s - base);
             const int units = nt ? nt + extra : 0;
             const int r = x - a.num_kv_heads * pre;
             if (r >= a.num_kv_heads * units) {
@@ -193,15 +346,16 @@ struct Walk {
                 ++s;
                 continue;
             }
-            // Units [u0, u1) of the segment: first the change to it, then its tiles.
+            // Units [u0, u1) of the segment: first the change to it, then its tiles.  Whole
+            // segments are those that start in the range.
             h = r / units;
-            const int u0 = r - h * units, u1 = min(units, u0 + end - x);
+            const int u0 = r - h * units;
+            const int u1 = a.whole_segments ? units : min(units, u0 + end - x);
             at = x;
             x += u1 - u0;
             j0 = max(0, u0 - extra);
             j1 = max(0, u1 - extra);
-            if (j0 >= j1) continue;
-            if (cur.n > rg * a.q_tile) return true;
+            if (j0 < j1 && !(a.whole_segments && u0)) return true;
         }
         return false;
     }
@@ -211,10 +365,10 @@ __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
 
-template <int D, bool KV8>
-__global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
+template <int D, bool KV8, bool Two>
+__global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
     tree_attention_kernel(const __grid_constant__ CUtensorMap kv_map, const TreeAttnArgs a) {
-    using L = Tlay<D, KV8>;
+    using L = Tlay<D, KV8, Two>;
     // No static shared memory: the dynamic part then starts at the (1024-byte aligned)
     // beginning, and two CTAs' 112 KB of operands fit one SM.
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -226,8 +380,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     }
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int worker = blockIdx.x / a.row_groups, rg = blockIdx.x - worker * a.row_groups;
-    const int Hkv = a.num_kv_heads, B = a.t.num_seqs, G = a.group, QT = a.q_tile;
+    const int Hkv = a.num_kv_heads, G = a.group, QT = a.q_tile;
+    // Queries of up to 64 rows are held twice, in the halves of their tile (the product
+    // reads 128 rows from either: what lies behind a half comes out in rows that nobody
+    // reads), and the two warps without rows load them a segment ahead.
+    constexpr bool two_q = Two;
+    constexpr uint32_t soft = two_q ? 2 : 4;  // softmax warps
+    // The warp that issues the scores' products: a seventh of a bf16 pool's CTA with more
+    // rows, else that of the outputs'.
+    constexpr int s_warp = two_q || KV8 ? 1 : 6;
 
     // What needs no memory of the caller's, under the end of the launch before this one.
     if (tid == 0) {
@@ -244,13 +405,18 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             mbar_init(&sy.staged[i], 1);
             mbar_init(&sy.stage_free[i], L::kConv);
         }
-        mbar_init(&sy.p_full[0], 4);
-        mbar_init(&sy.p_full[1], 4);
-        mbar_init(&sy.q_full, 4);
-        mbar_init(&sy.o_free, 4);
-        mbar_init(&sy.sane, 1);
-        mbar_init(&sy.drain, 1);
-        sy.bad[0] = sy.bad[1] = -1;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sy.p_full[i], soft);
+            mbar_init(&sy.q_full[i], two_q ? 2 : 4);
+            mbar_init(&sy.q_free[i], soft);
+        }
+        for (int i = 0; i < kSegs; ++i) mbar_init(&sy.seg_full[i], 1);
+        mbar_init(&sy.o_free, soft);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sy.sane[i], KV8 ? L::kConv : 1);
+            sy.bad[i] = -1;
+        }
+        mbar_init(&sy.drain, s_warp == 1 ? 1 : 2);
         fence_barrier_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -262,98 +428,123 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         tmem_relinquish();
         asm volatile("griddepcontrol.launch_dependents;" :::);
     }
-    // Units of work per head over all sequences (a segment's tiles, and the change to it),
-    // and the sequences that hold this range's start and end: every thread sums a
-    // contiguous share of the sequences, tiles and sequences with tiles in one number.
-    int t_begin, t_end, change;
-    {
-        const int per = (B + L::kThreads - 1) / L::kThreads;
-        const int s0 = min(B, tid * per), s1 = min(B, s0 + per);
-        unsigned long long sum = 0;
-        for (int s = s0; s < s1; ++s) {
-            const int nt = seq_info(a, s).tiles();
-            sum += nt ? (1ull << 32) + nt : 0ull;
-        }
-        unsigned long long incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        if (lane == 31) sy.part[warp] = incl;
-        if (tid == 0) sy.start[0] = -1;
-        __syncthreads();
-        unsigned long long before = 0, total = 0;
-        for (int w = 0; w < L::kThreads / 32; ++w) {
-            if (w < warp) before += sy.part[w];
-            total += sy.part[w];
-        }
-        const long long tiles = (long long)(total & 0xffffffffu) * Hkv;
-        change = tiles >= (long long)kLongRange * a.workers ? a.change : 0;
-        auto units = [&](unsigned long long v) {
-            return (int)(v & 0xffffffffu) + change * (int)(v >> 32);
-        };
-        const long long T = (long long)units(total) * Hkv;
-        const long long We = a.workers < T ? a.workers : (T > 0 ? T : 1);
-        t_begin = worker < We ? (int)(worker * T / We) : 0;
-        t_end = worker < We ? (int)((worker + 1) * T / We) : 0;
-        const int pre = units(before + incl - sum), mine = units(sum);
-        // The sequence at position x < T lies in one thread's share.
-        auto holds = [&](int x) {
-            return x >= (long long)Hkv * pre && x < (long long)Hkv * (pre + mine);
-        };
-        auto find = [&](int x, int &s, int &p, int &n) {
-            for (s = s0, p = pre;; ++s, p += n) {
-                const int nt = seq_info(a, s).tiles();
-                n = nt ? nt + change : 0;
-                if (x < (long long)Hkv * (p + n)) return;
-            }
-        };
-        // Whole segments: a range starts at the first segment start at or after its share's.
-        auto snap = [&](int x, int p, int n) {
-            const int r = (x - Hkv * p) % n;
-            return r ? x + n - r : x;
-        };
-        if (tid == 0) sy.range[1] = t_end;
-        if (a.whole_segments) __syncthreads();
-        int s, p, n;
-        if (t_begin < t_end && holds(t_begin)) {
-            find(t_begin, s, p, n);
-            sy.start[0] = s;
-            sy.start[1] = p;
-            sy.range[0] = a.whole_segments ? snap(t_begin, p, n) : t_begin;
-        }
-        if (a.whole_segments && t_end < T && holds(t_end)) {
-            find(t_end, s, p, n);
-            sy.range[1] = snap(t_end, p, n);
-        }
-    }
+    // The producer's warp finds this CTA's range; the sequences' data come meanwhile.
+    Walk w;
+    if (warp == 0) w.load(a, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sy.tmem;
-    const int seq0 = sy.start[0], pre0 = sy.start[1];
-    if (seq0 >= 0) {
-        t_begin = sy.range[0];
-        t_end = sy.range[1];
-    }
-    const bool work = seq0 >= 0 && t_begin < t_end;
-    if (tid == 0 && rg == 0 && !a.whole_segments) {
-        int4 st = make_int4(-1, 0, 0, 0);
-        if (work) {
-            const SeqInfo si = seq_info(a, seq0);
-            const int n = si.tiles() + change, r = t_begin - Hkv * pre0;
-            st = make_int4(seq0, (r / n) | si.n << 8, max(0, r % n - change), si.row0);
-        }
-        a.starts[worker] = st;
-    }
 
-    if (!work) {
-        // Nothing to do: only the barriers below.
-    } else if (warp == 0) {
+    // Segment k, once it is known.
+    auto segment = [&](int k, Seg &g) -> bool {
+        const bool ok = mbar_wait_bounded(&sy.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1u);
+        g = sy.seg[k % kSegs];
+        return ok;
+    };
+
+    // Rows row0 .. row0 + 31 of a segment's queries into shared memory at dst (K-major, 128B
+    // swizzle): the warp takes them a few at a time, 16 bytes per lane.  Over an FP8 pool the
+    // lane of a row gets its scale's exponent + 127.
+    //
+    // K of an FP8 pool is multiplied as codes, so the query becomes the sum of two e4m3
+    // rows: scaled by the power of two that puts its largest element in [128, 256),
+    // q = hi + lo with hi the nearest e4m3 number (4 significant bits of bf16's 8) and lo
+    // what is left.  That is exact for elements down to 2^-9 of the largest; below, e4m3's
+    // smallest step leaves an error of at most 2^-10, or 2^-17 of the largest element, no
+    // more than fp32 loses in the 128-term sum.  The softmax takes the scaling back; a row
+    // with NaN or infinities becomes NaN through it (exponent 255).
+    auto load_rows = [&](const Seg &g, int first, uint8_t *dst) -> int {
+        constexpr int kC = D / 8, kR = 32 / kC;  // chunks of a row, rows at a time
+        constexpr int kBatch = 8;
+        int exponent = 127;
+        const int rg = g.rg(), nodes = min(QT, g.n() - rg * QT);
+        if (first < nodes * G) {
+            const int c = lane % kC, row0 = first + lane / kC;
+            const uint32_t flip = a.negate_q ? 0x80008000u : 0u;  // exact bf16 negation
+            int node = row0 / G, head = row0 - node * G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                a.q + ((size_t)(g.row0 + rg * QT) * a.num_heads + (size_t)g.h() * G) * D) + c;
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32 / kR; k0 += kBatch) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    v[k] = node < nodes
+                               ? __ldg(src + ((size_t)node * a.num_heads + head) * kC)
+                               : make_uint4(0, 0, 0, 0);
+                    head += kR;
+#pragma unroll
+                    for (int t = 0; t < kR; ++t)
+                        if (head >= G) {
+                            head -= G;
+                            ++node;
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int r = row0 + kR * (k0 + k);
+                    v[k].x ^= flip;
+                    v[k].y ^= flip;
+                    v[k].z ^= flip;
+                    v[k].w ^= flip;
+                    if constexpr (!KV8) {
+                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * L::kQPanel + r * 128 +
+                                                   (((c & 7) ^ (r & 7)) << 4)) = v[k];
+                    } else {
+                        // The row's largest element, as bf16 bits without the sign.
+                        uint32_t top = 0u;
+                        auto up = [&](uint32_t x) {
+                            top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
+                        };
+                        up(v[k].x);
+                        up(v[k].y);
+                        up(v[k].z);
+                        up(v[k].w);
+#pragma unroll
+                        for (int o = kC / 2; o > 0; o >>= 1)
+                            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int ex =
+                            max(-119, min(127, top ? (int)(top >> 7) - 127 : 0));
+                        const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t w0 = i ? v[k].z : v[k].x, w1 = i ? v[k].w : v[k].y;
+                            const float x0 = bf16_lo(w0) * down, x1 = bf16_hi(w0) * down;
+                            const float x2 = bf16_lo(w1) * down, x3 = bf16_hi(w1) * down;
+                            hi[i] = pack_e4m3x2(x0, x1) | pack_e4m3x2(x2, x3) << 16;
+                            uint32_t f0, f1;
+                            e4m3x4_to_f16x4(hi[i], f0, f1);
+                            lo[i] = pack_e4m3x2(x0 - f16_lo(f0), x1 - f16_hi(f0)) |
+                                    pack_e4m3x2(x2 - f16_lo(f1), x3 - f16_hi(f1)) << 16;
+                        }
+                        uint8_t *at = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2 *>(at + L::kQPanel) = make_uint2(lo[0], lo[1]);
+                        // To the lane of the row.
+                        const int mine = __shfl_sync(
+                            0xffffffffu, top >= 0x7f80u ? 255 : 127 + ex - 7, (lane % kR) * kC);
+                        if (lane / kR == k0 + k) exponent = mine;
+                    }
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        return exponent;
+    };
+    // What a row's scores are multiplied with, from its exponent.
+    auto row_scale = [&](int exponent) -> float {
+        if constexpr (!KV8) return a.scale_log2;
+        return exponent == 255
+               ? NAN
+               : a.scale_log2 * a.k_scale * __uint_as_float((uint32_t)exponent << 23);
+    };
+
+    if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end, change);
+        w.start(a);
         const int bs = a.block_size, nbox = kKeys / bs;  // a box per block
         const int v_off = Hkv * bs;
         const uint64_t policy = policy_evict_first();
@@ -392,23 +583,46 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         };
         // This lane's box of V where its box of K is at TMA row r.
         auto v_row = [&](int r) { return r < -(1 << 29) ? r : r + v_off; };
+        // The walk is a segment ahead of the copies; what it finds, for every warp.
+        int segs = 0;
+        bool have = true;
+        auto publish = [&]() {
+            have = w.next(a);
+            if (lane == 0) {
+                const int i = segs % kSegs;
+                sy.seg[i] = {w.s, w.cur.row0, w.cur.len,
+                             w.cur.n | w.h << 8 | (w.at == w.begin ? 1 : 0) << 16 | w.rg << 17,
+                             have ? w.j0 : 0, have ? w.j1 : 0};
+                mbar_arrive(&sy.seg_full[i]);
+            }
+            ++segs;
+        };
+        publish();
+        if (lane == 0 && !a.whole_segments)
+            a.starts[blockIdx.x] = have && w.at == w.begin
+                                       ? make_int4(w.s, w.h | w.cur.n << 8 | w.rg << 16, w.j0,
+                                                   w.cur.row0)
+                                       : make_int4(-1, 0, 0, 0);
         // This lane's box of the next tile, one tile ahead of the copies: the table entry
         // is on its way while the tile before it is copied.
-        int seg_j = 0, seg_j1 = 0, blk = 0, head = 0;
+        int seg_j = 0, seg_j1 = 0, blk = 0, head = 0, seg_h = 0, seg_len = 0;
         const int32_t *bt = nullptr;
         auto fetch = [&]() -> bool {
             if (seg_j == seg_j1) {
-                if (!w.next(a, rg)) return false;
+                if (!have) return false;
                 seg_j = w.j0;
                 seg_j1 = w.j1;
+                seg_h = w.h;
+                seg_len = w.cur.len;
                 bt = a.block_tables + (size_t)w.s * a.max_blocks;
+                publish();
             }
             const int tok = seg_j * kKeys + lane * bs;
             blk = -1;
             head = -1;  // no box: outside the tile or past the sequence
-            if (lane < nbox && tok < w.cur.len) {
+            if (lane < nbox && tok < seg_len) {
                 blk = bt[tok / bs];
-                head = w.h;
+                head = seg_h;
             }
             ++seg_j;
             return true;
@@ -446,20 +660,28 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         for (int i = max(0, v_issued - kN); i < v_issued; ++i)
             mbar_wait_bounded(KV8 ? &sy.staged[i % kN] : &sy.v_full[i % kN],
                               (uint32_t)(i / kN) & 1u);
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end, change);
+    } else if (warp == 1 || warp == s_warp) {
+        // ------------------------------------------------------------ products
+        // A product costs the thread that issues it its share of the tensor pipe, and a commit
+        // some 200 cycles more.  Of many rows the tensor pipe is the bound: the scores' and the
+        // outputs' have a thread each (16 wide trees 140 -> 136 us).  Of up to 64 rows the
+        // chain scores, softmax, output is: one thread, whose products run in order, need
+        // not wait for an output's end before it issues scores over its P (64 FP8 chains 82
+        // us, 90 with two).
         const uint32_t idesc_s =
             KV8 ? tc_idesc_e4m3(kRows, kKeys) : tc_idesc_bf16(kRows, kKeys, 0);
         const uint32_t idesc_pv = KV8 ? tc_idesc_f16(kRows, D, 1) : tc_idesc_bf16(kRows, D, 1);
         const uint64_t q_desc = tc_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t k_desc = tc_desc_sw128(smem_u32(sK), 16, KV8 ? 1024 : L::kGroup);
         const uint64_t v_desc = tc_desc_sw128(smem_u32(sV), L::kPanel, L::kGroup);
-        // S_i = Q.K^T into buffer i & 1, over tile i - 2's P: this thread issued the product
-        // that reads it before, and the products of one thread run in order.
-        auto scores = [&](int i) -> bool {
+        // S_i = Q.K^T into buffer i & 1, over tile i - 2's P, once the product that reads it
+        // is done.  half: 64-row half of the query tile, in units of 16 bytes.
+        auto scores = [&](int i, uint32_t half) -> bool {
             const int st = i % L::kKSlots, b = i & 1;
+            if (i >= 2 && s_warp != 1 &&  // (one thread's products run in order)
+                !mbar_wait_bounded(&sy.pv_done[(i - 2) % L::kVSlots],
+                                   (uint32_t)((i - 2) / L::kVSlots) & 1u))
+                return false;
             if (!mbar_wait_bounded(&sy.k_full[st], (uint32_t)(i / L::kKSlots) & 1u)) return false;
             tc_fence_after();
             const uint64_t kd = k_desc + (uint64_t)((st * L::kKTile) >> 4);
@@ -468,7 +690,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
 #pragma unroll
                 for (int k = 0; k < 2 * (D / 32); ++k) {
                     const uint32_t ko = (k & 3) * 32;
-                    tc_mma_f8_ss(tmem + b * kKeys, q_desc + (((k >> 2) * L::kQPanel + ko) >> 4),
+                    tc_mma_f8_ss(tmem + b * kKeys,
+                                 q_desc + half + (((k >> 2) * L::kQPanel + ko) >> 4),
                                  kd + (ko >> 4), idesc_s, k > 0 ? 1u : 0u);
                 }
             } else {
@@ -476,7 +699,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t qo = ((k >> 2) * L::kQPanel + (k & 3) * 32) >> 4;
                     const uint32_t ko = ((k >> 2) * L::kPanel + (k & 3) * 32) >> 4;
-                    tc_mma_ss(tmem + b * kKeys, q_desc + qo, kd + ko, idesc_s, k > 0 ? 1u : 0u);
+                    tc_mma_ss(tmem + b * kKeys, q_desc + half + qo, kd + ko, idesc_s,
+                              k > 0 ? 1u : 0u);
                 }
             }
             tc_commit(&sy.s_full[st]);
@@ -500,207 +724,150 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         // Tile i's V in keys [r0, 64), past the context: rows from r1 on (behind the sequence)
         // are zeroed, tree nodes' cleared of NaN and infinities.  True if there were any.
         auto clean = [&](int i, int r0, int r1) -> bool {
-            constexpr int kC = 8 * L::kPanels;  // 16-byte chunks of a key
+            constexpr int kC = 8 * L::kPanels, kN = 4;  // 16-byte chunks of a key; loads at once
             uint8_t *vs = sV + (i % L::kVSlots) * L::kVTile +
                           ((lane % kC) >> 3) * L::kPanel + (lane & 7) * 16;
+            auto at = [&](int r) {
+                return reinterpret_cast<uint4 *>(vs + (r >> 3) * L::kGroup + (r & 7) * 128);
+            };
             bool bad = false;
-            for (int r = r0 + lane / kC; r < kKeys; r += 32 / kC) {
-                uint4 *at = reinterpret_cast<uint4 *>(vs + (r >> 3) * L::kGroup + (r & 7) * 128);
-                if (r >= r1) {
-                    *at = make_uint4(0, 0, 0, 0);
-                    continue;
-                }
-                uint4 v = *at;
-                constexpr uint32_t kExp = KV8 ? 0x7C00u : 0x7F80u;
-                bool hit = false;
-                auto clear = [&](uint32_t x) {
-                    if ((x & kExp) == kExp) {
-                        x &= 0xffff0000u;
-                        hit = true;
+            for (int r = r0 + lane / kC; r < r1; r += kN * (32 / kC)) {
+                uint4 v[kN];
+#pragma unroll
+                for (int k = 0; k < kN; ++k)
+                    v[k] = r + k * (32 / kC) < r1 ? *at(r + k * (32 / kC))
+                                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < kN; ++k) {
+                    bool hit = false;
+                    auto clear = [&](uint32_t x) {
+                        if ((x & 0x7F80u) == 0x7F80u) {
+                            x &= 0xffff0000u;
+                            hit = true;
+                        }
+                        if ((x & 0x7F800000u) == 0x7F800000u) {
+                            x &= 0x0000ffffu;
+                            hit = true;
+                        }
+                        return x;
+                    };
+                    v[k].x = clear(v[k].x);
+                    v[k].y = clear(v[k].y);
+                    v[k].z = clear(v[k].z);
+                    v[k].w = clear(v[k].w);
+                    if (hit) {
+                        *at(r + k * (32 / kC)) = v[k];
+                        bad = true;
                     }
-                    if ((x & (kExp << 16)) == (kExp << 16)) {
-                        x &= 0x0000ffffu;
-                        hit = true;
-                    }
-                    return x;
-                };
-                v.x = clear(v.x);
-                v.y = clear(v.y);
-                v.z = clear(v.z);
-                v.w = clear(v.w);
-                if (hit) {
-                    *at = v;
-                    bad = true;
                 }
             }
+            for (int r = max(r0, r1) + lane / kC; r < kKeys; r += 32 / kC)
+                *at(r) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             return bad;
         };
-        // One thread runs a segment: its scores two tiles ahead of its outputs, from the
-        // arrival of its queries; its first output after the epilogue before it has read O.
-        // The (at most two) tiles that reach past the context are cleaned by the warp first.
-        auto begin = [&](int base, int n, int sg) -> bool {
-            if (!mbar_wait_bounded(&sy.q_full, (uint32_t)sg & 1u)) return false;
-            if (!scores(base) || (n > 1 && !scores(base + 1))) return false;
-            return sg == 0 || mbar_wait_bounded(&sy.o_free, (uint32_t)(sg - 1) & 1u);
+        // Up to `last` tiles' scores, of segments up to max_seg, one thread.
+        int s_next = 0, s_left = 0, s_seg = 0;  // next tile, tiles left of its segment, segments
+        uint32_t half = 0;
+        bool s_end = false;
+        auto fill = [&](int last, int max_seg) -> bool {
+            while (s_next < last && !s_end) {
+                if (s_left == 0) {
+                    if (s_seg > max_seg) break;
+                    Seg g;
+                    if (!segment(s_seg, g)) return false;
+                    s_left = g.j1 - g.j0;
+                    s_end = s_left == 0;
+                    if (s_end) break;
+                    const int b = two_q ? s_seg & 1 : 0;
+                    if (!mbar_wait_bounded(&sy.q_full[b],
+                                           (uint32_t)(two_q ? s_seg >> 1 : s_seg) & 1u))
+                        return false;
+                    half = b ? 64 * 128 >> 4 : 0;
+                    ++s_seg;
+                }
+                if (!scores(s_next, half)) return false;
+                ++s_next;
+                --s_left;
+            }
+            return true;
         };
-        auto step = [&](int base, int j, int n) -> bool {
-            return output(base + j, j == 0) && (j + 2 >= n || scores(base + j + 2));
-        };
-        int it = 0, seg = 0;
         bool ok = true;
-        while (ok && w.next(a, rg)) {
-            const int n = w.j1 - w.j0, ctx = w.cur.len - w.cur.n;
-            const int plain = min(n, max(0, ctx / kKeys - w.j0));
+        if (warp != 1 && lane == 0) ok = fill(1 << 30, 1 << 30);
+        // The outputs: a segment's first after the epilogue of the one before has read O.  With
+        // the scores in the same thread, those come up to two tiles ahead, into the next
+        // segment where its queries have a place of their own.  Of a bf16 pool the (at most
+        // two) tiles that reach past the context are cleaned by the warp first.
+        int it = 0;
+        for (int seg = 0; ok && warp == 1; ++seg) {
+            Seg g;
+            if (!(ok = __all_sync(0xffffffffu, segment(seg, g)))) break;
+            const int n = g.j1 - g.j0, ctx = g.len - g.n();
+            if (n == 0) break;
+            const int plain = KV8 ? n : min(n, max(0, ctx / kKeys - g.j0));
+            auto ahead = [&](int tiles) {
+                return s_warp != 1 || fill(it + tiles, seg + (two_q ? 1 : 0));
+            };
             if (lane == 0) {
-                ok = begin(it, n, seg);
-                for (int j = 0; ok && j < plain; ++j) ok = step(it, j, n);
+                ok = ahead(2) &&
+                     (seg == 0 || mbar_wait_bounded(&sy.o_free, (uint32_t)(seg - 1) & 1u));
+                for (int j = 0; ok && j < plain; ++j) ok = output(it + j, j == 0) && ahead(j + 3);
             }
             ok = __all_sync(0xffffffffu, ok);
             bool bad = false;
             for (int j = plain; ok && j < n; ++j) {
-                const int i = it + j, k0 = (w.j0 + j) * kKeys;
+                const int i = it + j, k0 = (g.j0 + j) * kKeys;
                 ok = all_wait(&sy.v_full[i % L::kVSlots], (uint32_t)(i / L::kVSlots) & 1u);
                 if (!ok) break;
-                bad |= clean(i, max(ctx - k0, 0), min(w.cur.len - k0, kKeys));
+                bad |= clean(i, max(ctx - k0, 0), min(g.len - k0, kKeys));
                 bad = __any_sync(0xffffffffu, bad);
-                if (lane == 0) {
-                    if (j == n - 1) {  // what was found, to the softmax warps
-                        if (bad) sy.bad[seg & 1] = seg;
-                        mbar_arrive(&sy.sane);
-                    }
-                    ok = step(it, j, n);
-                }
+                if (j == n - 1 && bad && lane == 0) sy.bad[seg & 3] = seg;
+                if (lane == 0) ok = output(i, j == 0) && ahead(j + 3);
                 ok = __all_sync(0xffffffffu, ok);
             }
+            if (!KV8 && lane == 0) mbar_arrive(&sy.sane[seg & 3]);
             it += n;
-            ++seg;
         }
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
         // Every product must be done before tensor memory is freed.
         if (lane == 0) tc_commit(&sy.drain);
         __syncwarp();
-        mbar_wait_bounded(&sy.drain, 0);
+        if (warp == 1) mbar_wait_bounded(&sy.drain, 0);
+    } else if (warp < 4 && two_q) {
+        // ------------------------------------------------------------ queries, a segment ahead
+        const int first = 32 * (warp - 2);
+        bool ok = true;
+        for (int k = 0;; ++k) {
+            Seg g;
+            if (!(ok = __all_sync(0xffffffffu, segment(k, g))) || g.j0 >= g.j1) break;
+            const int b = k & 1;
+            if (k >= 2 && !(ok = all_wait(&sy.q_free[b], (uint32_t)((k >> 1) - 1) & 1u))) break;
+            const int e = load_rows(g, first, sQ + b * (64 * 128));
+            if (KV8) sy.q_exp[b][first + lane] = (uint8_t)e;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sy.q_full[b]);
+        }
+        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     } else if (warp < 6) {
         // ------------------------------------------------------------ softmax
-        Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end, change);
         const int row = 32 * (warp & 3) + lane;  // TMEM lane = query row of the tile
         const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int r_node = row / G, r_head = row - r_node * G;
         const bool in_tile = row < QT * G;
-        float sl2 = 0.f;
         // Ancestors of the current sequence's nodes (lane and lane + 32), and of this row.
         int anc_seq = -1;
         uint64_t anc_lo = 0, anc_hi = 0;
-        auto real_in = [&](const SeqInfo &si) { return in_tile && rg * QT + r_node < si.n; };
-        auto q_row = [&]() {
-            return a.q + ((size_t)(w.cur.row0 + rg * QT + r_node) * a.num_heads +
-                          (size_t)w.h * G + r_head) * D;
-        };
-        // The segment's query rows into shared memory (K-major, 128B swizzle): the warp takes
-        // its 32 rows a few at a time, 16 bytes per lane.
-        //
-        // K of an FP8 pool is multiplied as codes, so the query becomes the sum of two e4m3
-        // rows: scaled by the power of two that puts its largest element in [128, 256),
-        // q = hi + lo with hi the nearest e4m3 number (4 significant bits of bf16's 8) and lo
-        // what is left.  That is exact for elements down to 2^-9 of the largest; below, e4m3's
-        // smallest step leaves an error of at most 2^-10, or 2^-17 of the largest element, no
-        // more than fp32 loses in the 128-term sum.  sl2 takes the scaling back, with k_scale;
-        // a row with NaN or infinities becomes NaN through it.
-        auto load_q = [&]() {
-            constexpr int kC = D / 8, kR = 32 / kC;  // chunks of a row, rows at a time
-            constexpr int kBatch = 8;
-            sl2 = a.scale_log2;
-            if (__any_sync(0xffffffffu, real_in(w.cur))) {
-                const int c = lane % kC, row0 = row - lane + lane / kC;
-                const uint32_t flip = a.negate_q ? 0x80008000u : 0u;  // exact bf16 negation
-                int node = row0 / G, head = row0 - node * G;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    a.q + ((size_t)(w.cur.row0 + rg * QT) * a.num_heads + (size_t)w.h * G) * D) + c;
-#pragma unroll 1
-                for (int k0 = 0; k0 < 32 / kR; k0 += kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const bool in = row0 + kR * (k0 + k) < QT * G &&
-                                        rg * QT + node < w.cur.n;
-                        v[k] = in ? __ldg(src + ((size_t)node * a.num_heads + head) * kC)
-                                  : make_uint4(0, 0, 0, 0);
-                        head += kR;
-#pragma unroll
-                        for (int t = 0; t < kR; ++t)
-                            if (head >= G) {
-                                head -= G;
-                                ++node;
-                            }
-                    }
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int r = row0 + kR * (k0 + k);
-                        v[k].x ^= flip;
-                        v[k].y ^= flip;
-                        v[k].z ^= flip;
-                        v[k].w ^= flip;
-                        if constexpr (!KV8) {
-                            *reinterpret_cast<uint4 *>(sQ + (c >> 3) * L::kQPanel + r * 128 +
-                                                       (((c & 7) ^ (r & 7)) << 4)) = v[k];
-                        } else {
-                            // The row's largest element, as bf16 bits without the sign.
-                            uint32_t top = 0u;
-                            auto up = [&](uint32_t x) {
-                                top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
-                            };
-                            up(v[k].x);
-                            up(v[k].y);
-                            up(v[k].z);
-                            up(v[k].w);
-#pragma unroll
-                            for (int o = kC / 2; o > 0; o >>= 1)
-                                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            const int ex =
-                                max(-119, min(127, top ? (int)(top >> 7) - 127 : 0));
-                            const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-                            uint32_t hi[2], lo[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t w0 = i ? v[k].z : v[k].x, w1 = i ? v[k].w : v[k].y;
-                                const float x0 = bf16_lo(w0) * down, x1 = bf16_hi(w0) * down;
-                                const float x2 = bf16_lo(w1) * down, x3 = bf16_hi(w1) * down;
-                                hi[i] = pack_e4m3x2(x0, x1) | pack_e4m3x2(x2, x3) << 16;
-                                uint32_t f0, f1;
-                                e4m3x4_to_f16x4(hi[i], f0, f1);
-                                lo[i] = pack_e4m3x2(x0 - f16_lo(f0), x1 - f16_hi(f0)) |
-                                        pack_e4m3x2(x2 - f16_lo(f1), x3 - f16_hi(f1)) << 16;
-                            }
-                            uint8_t *dst = sQ + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-                            *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2 *>(dst + L::kQPanel) = make_uint2(lo[0], lo[1]);
-                            // The scale of row `lane` to its thread.
-                            const float back = top >= 0x7f80u
-                                                   ? NAN
-                                                   : __uint_as_float((uint32_t)(127 + ex - 7) << 23);
-                            const float mine =
-                                __shfl_sync(0xffffffffu, back, (lane % kR) * kC);
-                            if (lane / kR == k0 + k) sl2 = a.scale_log2 * a.k_scale * mine;
-                        }
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sy.q_full);
-        };
+        auto real_in = [&](const Seg &g) { return in_tile && g.rg() * QT + r_node < g.n(); };
         // Ancestors of every node of the current sequence: node lane in anc_lo, node
         // lane + 32 in anc_hi.  Each of six rounds joins a node's set with that of the
         // node its pointer has reached, and doubles the pointer's stride.
-        auto ancestors = [&]() {
-            if (anc_seq == w.s) return;
-            anc_seq = w.s;
+        auto ancestors = [&](const Seg &g) {
+            if (anc_seq == g.s) return;
+            anc_seq = g.s;
             int p0 = -1, p1 = -1;
             auto parent = [&](int i) {
-                if (i >= w.cur.n) return -1;
-                const int p = a.t.parents[w.cur.row0 + i];
+                if (i >= g.n()) return -1;
+                const int p = a.t.parents[g.row0 + i];
                 if (p < -1 || p >= i) {
                     atomicOr(&g_err_tree_attention, kErrOob);
                     return -1;
@@ -732,39 +899,49 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
             }
         };
         int it = 0, seg = 0;
-        uint32_t sane_par = 0;
-        bool ok = true, more = w.next(a, rg);
-        if (more) load_q();
-        while (ok && more) {
-            const SeqInfo si = w.cur;
-            const int s_h = w.h, j0 = w.j0, j1 = w.j1;
-            const bool whole = j0 == 0 && j1 == w.nt;
-            const int which = w.at == w.begin ? 0 : 1;  // record of a piece: first in the range?
-            const float scale = sl2;
-            const int ctx = si.len - si.n;
+        Seg si;
+        bool ok = __all_sync(0xffffffffu, segment(0, si));
+        int exponent = 0;
+        if (!two_q && ok && si.j0 < si.j1) {
+            exponent = load_rows(si, row - lane, sQ);
+            if (lane == 0) mbar_arrive(&sy.q_full[0]);
+        }
+        while (ok && si.j0 < si.j1) {
+            const int s_h = si.h(), s_n = si.n(), j0 = si.j0, j1 = si.j1, rg = si.rg();
+            const bool whole = j0 == 0 && j1 * kKeys >= si.len;
+            const int which = si.first() ? 0 : 1;  // record of a piece: first in the range?
+            const int ctx = si.len - s_n;
             const bool real = real_in(si);
             const bool busy = __any_sync(0xffffffffu, real);
             const bool tree = j1 * kKeys > ctx;  // the piece holds tree nodes
+            if (two_q) {
+                if (!(ok = all_wait(&sy.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u))) break;
+                exponent = sy.q_exp[seg & 1][row & 63];
+            }
+            const float scale = row_scale(exponent);
             uint64_t anc = 0;
             if (tree) {
-                ancestors();
+                ancestors(si);
                 const int i = real ? rg * QT + r_node : 0;
                 const uint64_t x = __shfl_sync(0xffffffffu, anc_lo, i & 31);
                 const uint64_t y = __shfl_sync(0xffffffffu, anc_hi, i & 31);
                 anc = i < 32 ? x : y;
             }
-            const int my_s = w.s;
-            // On to the next segment: its queries come to L2 meanwhile.
-            more = w.next(a, rg);
-            if (more && real_in(w.cur)) {
-                const __nv_bfloat16 *next_q = q_row();
+            // The next segment (published when this one was opened): its data come to L2.
+            Seg next;
+            if (!(ok = __all_sync(0xffffffffu, segment(seg + 1, next)))) break;
+            const bool more = next.j0 < next.j1;
+            if (!two_q && more && real_in(next)) {
+                const __nv_bfloat16 *next_q =
+                    a.q + ((size_t)(next.row0 + rg * QT + r_node) * a.num_heads +
+                           (size_t)next.h() * G + r_head) * D;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(next_q + 64 * c));
             }
-            if (more && w.s != my_s && lane < 2)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.t.parents + w.cur.row0 +
-                                                             min(32 * lane, w.cur.n - 1)));
+            if (more && next.s != si.s && lane < 2)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.t.parents + next.row0 +
+                                                             min(32 * lane, next.n() - 1)));
             float m = -INFINITY, l = 0.f;
             for (int j = j0; j < j1; ++j, ++it) {
                 const int b = it & 1;
@@ -865,14 +1042,18 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 if (lane == 0) mbar_arrive(&sy.p_full[b]);
             }
             if (!ok) break;
-            // The next segment's queries while the last products run (this segment's
-            // scores are all read).
-            if (more) load_q();
+            // This segment's scores are all read: the queries' place is free.
+            if (two_q) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sy.q_free[seg & 1]);
+            } else if (more) {  // the next segment's, while the last products run
+                exponent = load_rows(next, row - lane, sQ);
+                if (lane == 0) mbar_arrive(&sy.q_full[0]);
+            }
             bool bad = false;
             if (tree) {  // NaN or infinities in the tree's V?
-                if (!(ok = all_wait(&sy.sane, sane_par))) break;
-                sane_par ^= 1u;
-                bad = *reinterpret_cast<volatile int *>(&sy.bad[seg & 1]) == seg;
+                if (!(ok = all_wait(&sy.sane[seg & 3], (uint32_t)(seg >> 2) & 1u))) break;
+                bad = *reinterpret_cast<volatile int *>(&sy.bad[seg & 3]) == seg;
             }
             if (!(ok = all_wait(&sy.pv_done[(it - 1) % L::kVSlots],
                                 (uint32_t)((it - 1) / L::kVSlots) & 1u)))
@@ -890,10 +1071,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                     float o[32];
                     tmem_ld32(trow + kColO + 32 * c, o);
                     tc_wait_ld();
+                    if (c == D / 32 - 1) {  // O is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sy.o_free);
+                    }
                     if (bad && real) {
                         // What this row sees of the values that were cleared.
-                        const int32_t *bt = a.block_tables + (size_t)my_s * a.max_blocks;
-                        for (int i = 0; i < si.n; ++i) {
+                        const int32_t *bt = a.block_tables + (size_t)si.s * a.max_blocks;
+                        for (int i = 0; i < s_n; ++i) {
                             const int pos = ctx + i;
                             if (!((anc >> i) & 1ull) || pos < j0 * kKeys || pos >= j1 * kKeys)
                                 continue;
@@ -944,21 +1130,20 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
                 if (real && !whole)
                     st_hint(reinterpret_cast<float2 *>(a.part_ml) + rec * a.part_rows + row,
                             make_float2(m, l), keep);
+            } else if (lane == 0) {
+                mbar_arrive(&sy.o_free);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sy.o_free);
             ++seg;
+            si = next;
         }
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     } else if constexpr (KV8) {
         // ------------------------------------------------------------ V: e4m3 -> f16
         // A lane converts a key's 128 codes (128B-swizzled as TMA left them) to f16 in the
-        // layout a bf16 tile has.
-        Walk w;
-        w.start(a, seq0, pre0, t_begin, t_end, change);
+        // layout a bf16 tile has.  Keys behind the sequence become zeros, NaN of tree nodes'
+        // keys too.
         const int r = (warp - 6) * 32 + lane;
-        auto tile = [&](int i) -> bool {
+        auto tile = [&](int i, int key, const Seg &g, bool &bad) -> bool {
             const int ss = i % L::kStages, st = i % L::kVSlots;
             if (!all_wait(&sy.staged[ss], (uint32_t)(i / L::kStages) & 1u)) return false;
             const uint8_t *codes = smem + L::kCodes + ss * L::kStage + r * 128;
@@ -966,6 +1151,18 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 in[c] = *reinterpret_cast<const uint4 *>(codes + ((c ^ (r & 7)) << 4));
+            if (key >= g.len - g.n()) {
+                const bool none = key >= g.len;
+                auto clear = [&](uint32_t x) {
+                    const uint32_t nan = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    bad |= !none && nan != 0u;
+                    return none ? 0u : x & ~((nan >> 7) * 0xffu);
+                };
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    in[c] = make_uint4(clear(in[c].x), clear(in[c].y), clear(in[c].z),
+                                       clear(in[c].w));
+            }
             if (i >= L::kVSlots &&
                 !all_wait(&sy.pv_done[st], (uint32_t)(i / L::kVSlots - 1) & 1u))
                 return false;
@@ -993,8 +1190,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
         };
         int it = 0;
         bool ok = true;
-        while (ok && w.next(a, rg))
-            for (int j = w.j0; ok && j < w.j1; ++j, ++it) ok = tile(it);
+        for (int k = 0; ok; ++k) {
+            Seg g;
+            if (!(ok = __all_sync(0xffffffffu, segment(k, g))) || g.j0 >= g.j1) break;
+            bool bad = false;
+            for (int j = g.j0; ok && j < g.j1; ++j, ++it) ok = tile(it, j * kKeys + r, g, bad);
+            if (bad) sy.bad[k & 3] = k;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sy.sane[k & 3]);
+        }
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     }
     tc_fence_before();
@@ -1005,35 +1209,37 @@ __global__ void __launch_bounds__(Tlay<D, KV8>::kThreads, 2)
     }
 }
 
-// Merge the pieces of segments that were split across workers.  CTA (w, row group, 32 rows)
-// looks whether worker w's range starts inside a segment whose first piece is worker
-// w - 1's; then a lane per row and a warp per D / 16 dims joins the pieces by log-sum-exp
-// in one pass, several pieces' loads in flight.
+// Merge the pieces of segments that were split across CTAs.  Block (w, 32 rows) looks whether
+// CTA w's range starts inside a segment whose first piece is that of the team before; then a
+// lane per row and a warp per D / 16 dims joins the pieces by log-sum-exp in one pass, several
+// pieces' loads in flight.
 constexpr int kMergeWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeAttnArgs a) {
     constexpr int kUnits = D / 4 / kMergeWarps;  // float4 of a row that a thread joins
     pdl_begin();
-    const int w = blockIdx.x + 1, rg = blockIdx.y, lane = threadIdx.x & 31;
-    const int row0 = blockIdx.z * 32;
-    // Workers w - 1 .. w + 30, one per lane.
+    const int w = blockIdx.x, lane = threadIdx.x & 31;
+    const int row0 = blockIdx.y * 32;
     auto start_of = [&](int i) {
-        return i < a.workers ? a.starts[i] : make_int4(-1, 0, 0, 0);
+        return i >= 0 && i < a.ctas ? a.starts[i] : make_int4(-1, 0, 0, 0);
     };
-    const int4 st = start_of(w - 1 + lane);
+    // Teams of the same segment lie a team's CTAs apart.  That before w's, w's and the next,
+    // one per lane.
+    const int step = a.row_groups == 1 ? 1 : max(1, groups_of(a, (start_of(w).y >> 8) & 255));
+    const int4 st = start_of(w + (lane - 1) * step);
     const int seq = __shfl_sync(0xffffffffu, st.x, 1), key = __shfl_sync(0xffffffffu, st.y, 1);
     const int tile = __shfl_sync(0xffffffffu, st.z, 1), node0 = __shfl_sync(0xffffffffu, st.w, 1);
     if (seq < 0 || tile == 0) return;  // idle, or a segment's start
     const bool prev_same = __shfl_sync(0xffffffffu, st.x == seq && st.y == key, 0);
     if (prev_same && __shfl_sync(0xffffffffu, st.z, 0) > 0) return;  // an earlier one merges it
-    const int nodes = key >> 8, head = key & 255;
+    const int nodes = (key >> 8) & 255, head = key & 255, rg = key >> 16;
     const int rows = min(a.q_tile, nodes - rg * a.q_tile) * a.group;
     if (row0 >= rows) return;
-    // Pieces: worker w - 1's and those of the workers from w on that start in the segment.
+    // Pieces: the team before's and those of the teams from w's on that start in the segment.
     int n = 1;
-    for (int base = w;; base += 32) {
-        const int4 e = start_of(base + lane);
+    for (int base = w;; base += 32 * step) {
+        const int4 e = start_of(base + lane * step);
         const unsigned in = __ballot_sync(0xffffffffu, e.x == seq && e.y == key);
         n += __popc(in);
         if (in != 0xffffffffu) break;
@@ -1054,7 +1260,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if (k0 + k < n) {
-                const size_t cta = (size_t)(w - 1 + k0 + k) * a.row_groups + rg;
+                const size_t cta = (size_t)(w + (k0 + k - 1) * step);
                 const size_t rec = cta * 2 + (k0 + k == 0 && !prev_same ? 1 : 0);
                 e[k] = ml[rec * a.part_rows + row];
 #pragma unroll
@@ -1108,7 +1314,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
 
 // Launch shape for trees of at most max_tree nodes.
 struct Shape {
-    int q_tile, row_groups, workers, part_rows;
+    int q_tile, row_groups, ctas, part_rows;
     size_t ml_off, acc_off, bytes;
 };
 
@@ -1116,28 +1322,33 @@ Shape shape_of(int max_tree, int group, int head_size, int sm_count) {
     Shape s;
     s.q_tile = kRows / group;
     s.row_groups = (max_tree + s.q_tile - 1) / s.q_tile;
-    s.workers = std::max(1, 2 * sm_count / s.row_groups);
+    s.ctas = std::max(kGroups * (kGroups + 1) / 2, 2 * sm_count);  // a team of every class
     s.part_rows = std::min(s.q_tile, max_tree) * group;
-    const size_t recs = (size_t)s.workers * s.row_groups * 2 * s.part_rows;
+    const size_t recs = (size_t)s.ctas * 2 * s.part_rows;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    s.ml_off = up((size_t)s.workers * sizeof(int4));
+    s.ml_off = up((size_t)s.ctas * sizeof(int4));
     s.acc_off = s.ml_off + up(recs * 8);
     s.bytes = s.acc_off + recs * head_size * 4;
     return s;
 }
 
+template <int D, bool KV8, bool Two>
+cudaError_t launch_rows(const CUtensorMap &map, const TreeAttnArgs &a, cudaStream_t stream) {
+    using L = Tlay<D, KV8, Two>;
+    cudaError_t e = ensure_smem<tree_attention_kernel<D, KV8, Two>>(L::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(tree_attention_kernel<D, KV8, Two>, dim3((unsigned)a.ctas),
+                   L::kThreads, L::kSmem, 1, stream, map, a);
+    if (e != cudaSuccess || a.whole_segments || a.ctas < 2) return e;
+    return launch_pdl(tree_merge_kernel<D>,
+                      dim3((unsigned)a.ctas, (unsigned)((a.part_rows + 31) / 32)),
+                      kMergeWarps * 32, 0, 1, stream, a);
+}
+
 template <int D, bool KV8>
 cudaError_t launch(const CUtensorMap &map, const TreeAttnArgs &a, cudaStream_t stream) {
-    using L = Tlay<D, KV8>;
-    cudaError_t e = ensure_smem<tree_attention_kernel<D, KV8>>(L::kSmem);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(tree_attention_kernel<D, KV8>, dim3((unsigned)(a.workers * a.row_groups)),
-                   L::kThreads, L::kSmem, 1, stream, map, a);
-    if (e != cudaSuccess || a.whole_segments || a.workers < 2) return e;
-    return launch_pdl(tree_merge_kernel<D>,
-                      dim3((unsigned)(a.workers - 1), (unsigned)a.row_groups,
-                           (unsigned)((a.part_rows + 31) / 32)),
-                      kMergeWarps * 32, 0, 1, stream, a);
+    return a.part_rows <= 64 ? launch_rows<D, KV8, true>(map, a, stream)
+                             : launch_rows<D, KV8, false>(map, a, stream);
 }
 
 }  // namespace
@@ -1186,10 +1397,10 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
     a.max_len = max_seq_len;
     a.q_tile = sh.q_tile;
     a.row_groups = sh.row_groups;
-    // No more workers than tiles.
+    // No more teams than tiles.
     const long long tiles = (long long)t.num_seqs * g.num_kv_heads *
                             (((long long)max_seq_len + kKeys - 1) / kKeys);
-    a.workers = (int)std::max(1LL, std::min<long long>(sh.workers, tiles));
+    a.ctas = (int)std::min<long long>(sh.ctas, std::max(1LL, tiles) * sh.row_groups);
     // A positive scale is folded into the exponent; a negative one negates Q (exact),
     // zero becomes a value far too small to change any finite score.
     a.negate_q = scale < 0.f ? 1 : 0;
