@@ -116,6 +116,21 @@ bool encode_kv_map_groups(CUtensorMap *map, const void *kv_cache, const KvGeom &
     return true;
 }
 
+bool encode_rows_map(CUtensorMap *map, const void *q, int head_size, int num_heads, int rows,
+                     int box_heads, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)head_size, (cuuint64_t)num_heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)head_size * 2u,
+                             (cuuint64_t)num_heads * (cuuint64_t)head_size * 2u};
+    cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 bool encode_kv_map_fp8(CUtensorMap *map, const void *kv_cache, const KvGeom &g, int box_rows) {
     if (g.head_size != 128) return false;
     if (cached_map(map, kv_cache, g, box_rows, 1)) return true;

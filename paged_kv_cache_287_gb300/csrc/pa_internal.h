@@ -61,6 +61,11 @@ bool encode_kv_map_fp8(CUtensorMap *map, const void *kv_cache, const KvGeom &g, 
 // swizzle: a box lands as [group of 8 rows][panel][row][64 elements].
 bool encode_kv_map_groups(CUtensorMap *map, const void *kv_cache, const KvGeom &g);
 
+// Encode a 3-D TMA map over query rows [rows][num_heads][head_size] bf16, box = 64 elements
+// x box_heads x box_rows, 128-byte swizzle.
+bool encode_rows_map(CUtensorMap *map, const void *q, int head_size, int num_heads, int rows,
+                     int box_heads, int box_rows);
+
 int device_sm_count();
 
 // Inputs of the device-side split of a mixed launch's SMs (pa_plan.cuh).

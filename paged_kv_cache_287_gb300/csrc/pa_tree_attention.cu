@@ -89,6 +89,7 @@ struct TreeAttnArgs {
     int num_heads, num_kv_heads, group;
     int block_size, max_blocks, num_blocks, max_len;
     int q_tile;      // nodes per query tile: floor(128 / group)
+    int q_recip;     // 2^16 / q_tile, rounded up
     int row_groups;  // of the largest tree
     int ctas;
     int whole_segments;  // ranges hold whole segments: nothing to merge
@@ -104,23 +105,55 @@ struct Tlay {
     static constexpr int kPanels = D / 64;
     static constexpr int kQPanel = kRows * 128;  // 64 dims of 128 rows
     static constexpr int kQ = kPanels * kQPanel;
-    // Tiles of K and V as the products read them, and how many are held.  An FP8 pool's K
-    // is read as codes; its V lands as codes in a ring of their own and is converted.
+    // Tiles of K and V as the products read them.  A bf16 pool's share a ring in the order of
+    // their use, K of a tile two outputs ahead: K0 K1 V0 K2 V1 K3 V2 ..  (A ring of two for K
+    // and one of three for V left K's loads in the chain: 16 wide trees 137 us.)
+    // An FP8 pool's K is read as codes; its V lands as codes and is converted.
     static constexpr int kVTile = kPanels * kKeys * 128;
     static constexpr int kKTile = KV8 ? kKeys * 128 : kVTile;
-    static constexpr int kKSlots = KV8 ? 3 : (D == 64 ? 4 : 2);
-    static constexpr int kVSlots = KV8 ? 2 : (D == 64 ? 4 : 3);
-    static constexpr int kStages = KV8 ? 3 : 0;
+    static constexpr int kRing = D == 64 ? 8 : 5;  // bf16
+    static constexpr int kKSlots = 3, kVSlots = 2, kStages = KV8 ? 3 : 0;  // FP8
+    static constexpr int kSlots = KV8 ? kKSlots + kVSlots : kRing;
+    // The warp that issues the scores' products (1: the outputs' one), and the one that fetches
+    // V (0: K's one).  A thread each for the products and a warp each for the copies let wide
+    // bf16 trees run at 1400 cycles a tile instead of 1750.  Of up to 64 rows V stays with K
+    // (32 trees of 12-16 nodes 60.2 -> 59.4 us), over an FP8 pool both do (64 chains 79 us,
+    // 82 with the products and 90 with the copies apart).
+    static constexpr int kScoreWarp = KV8 ? 1 : Two ? 3 : 6;
+    static constexpr int kVWarp = KV8 || Two ? 0 : 7;
+    static constexpr int kSplitWarp = KV8 && Two ? 2 : -1;
     static constexpr int kStage = kKeys * 128;
     // Where 8 keys x 64 dims (1 KB, swizzled) of panel p, keys 8 g .. lie in a 16-bit tile:
     // kGroup g + kPanel p.  A bf16 block lands in one copy with its panels side by side.
     static constexpr int kGroup = 1024 * kPanels;
     static constexpr int kPanel = 1024;
     static constexpr int kConv = KV8 ? 2 : 0;  // converting warps
-    static constexpr int kThreads = (KV8 ? 8 : Two ? 6 : 7) * 32;
-    static constexpr int kK = kQ, kV = kK + kKSlots * kKTile, kCodes = kV + kVSlots * kVTile;
+    static constexpr int kThreads = (!KV8 && Two ? 6 : 8) * 32;
+    static constexpr int kCodes =
+        kQ + (KV8 ? kKSlots * kKTile + kVSlots * kVTile : kRing * kVTile);
     static constexpr int kOperands = kCodes + kStages * kStage;
     static constexpr size_t kSmem = (size_t)kOperands + 1024;  // + barriers
+
+    // Where tile i's K and V lie: slot, how often it was filled before, byte offset.
+    struct Place {
+        int slot, use;
+        uint32_t at;
+        __device__ __forceinline__ uint32_t parity() const { return (uint32_t)use & 1u; }
+    };
+    static __device__ __forceinline__ Place in_ring(int n) {
+        return {n % kRing, n / kRing, (uint32_t)(kQ + n % kRing * kVTile)};
+    }
+    static __device__ __forceinline__ Place k(int i) {
+        if constexpr (KV8)
+            return {i % kKSlots, i / kKSlots, (uint32_t)(kQ + i % kKSlots * kKTile)};
+        return in_ring(i ? 2 * i - 1 : 0);
+    }
+    static __device__ __forceinline__ Place v(int i) {
+        if constexpr (KV8)
+            return {kKSlots + i % kVSlots, i / kVSlots,
+                    (uint32_t)(kQ + kKSlots * kKTile + i % kVSlots * kVTile)};
+        return in_ring(2 * i + 2);
+    }
 };
 
 // A segment of a CTA's range: tiles [j0, j1) of KV head h of sequence s, for row group rg.
@@ -141,16 +174,17 @@ constexpr int kSegs = 16;
 
 // What follows the operands in shared memory.
 struct Sync {
-    uint64_t k_full[4], v_full[4], staged[3], stage_free[3];
-    // Scores of tile i done, by i % K slots: its K slot is free too.  Output of tile i done,
-    // by i % V slots: its V slot is free too.  (A commit costs the issuing thread some 200
-    // cycles, as much as four products, so one serves both.)
-    uint64_t s_full[4], pv_done[4], p_full[2];
-    uint64_t q_full[2], q_free[2], o_free, sane[4], drain;
+    // Per slot: its tile has arrived (of an FP8 pool's V: is converted).  Per tile i, by i % 4:
+    // its scores, its output are done, and with that the slot that the product read is free.
+    // (A commit costs the issuing thread some 200 cycles, as much as four products, so one
+    // serves both.)
+    uint64_t full[8], s_done[4], pv_done[4], staged[3], stage_free[3];
+    uint64_t p_full[2], pv_issued[2];
+    uint64_t q_raw[2], q_full[2], exp_read[2], o_free, sane[4], drain;
     uint64_t seg_full[kSegs];
     uint32_t tmem;
     int bad[4];
-    uint8_t q_exp[2][64];  // an FP8 pool's queries: exponent + 127 of each row's scale
+    uint8_t q_exp[kRows];  // an FP8 pool's queries: exponent + 127 of each row's scale
     Seg seg[kSegs];
 };
 static_assert(sizeof(Sync) <= 1024, "the barriers' room");
@@ -163,19 +197,16 @@ struct SeqInfo {
     }
 };
 
-__device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs &a, int s) {
+__device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs &a, int s, bool &bad) {
     const TreeSpan t = tree_span(a.t, s);
     const int len = a.seq_lens[s];
-    if (t.n < 0 || len < t.n || len > a.max_len) {
-        atomicOr(&g_err_tree_attention, kErrOob);
-        return {0, 0, 0};
-    }
-    return {t.row0, t.n, len};
+    bad = t.n < 0 || len < t.n || len > a.max_len;
+    return bad ? SeqInfo{0, 0, 0} : SeqInfo{t.row0, t.n, len};
 }
 
-// Row groups of a tree of n nodes.
+// Row groups of a tree of n <= 64 nodes (the quotient is exact for these sizes).
 __device__ __forceinline__ int groups_of(const TreeAttnArgs &a, int n) {
-    return a.row_groups == 1 ? 1 : (n + a.q_tile - 1) / a.q_tile;
+    return ((n + a.q_tile - 1) * a.q_recip) >> 16;
 }
 
 // This CTA's range, walked by a whole warp in step: the sequences' data come 32 at a time,
@@ -184,7 +215,9 @@ __device__ __forceinline__ int groups_of(const TreeAttnArgs &a, int n) {
 // The work of sequences with as many row groups is a list (per segment the change to it and
 // its tiles), shared out evenly over teams of one CTA per row group, and the CTAs are shared
 // out over those lists by their work.
+template <bool Many>  // trees of several row groups
 struct Walk {
+    static constexpr int kG = Many ? kGroups : 1;
     int s, pre, x, end;        // sequence, units (per head) before it, position, range end
     int extra;                 // units of a segment besides its tiles
     int begin, at;             // the range's and the current segment's first position
@@ -194,49 +227,38 @@ struct Walk {
     int mine_nt;               // its tiles (0: other row groups)
     int h, j0, j1, nt;         // the current segment's head, tiles [j0, j1) of nt
     SeqInfo cur;
-    SeqInfo four[4];           // sequences four0 + lane, + 32, ..
-    int four0;
 
-    __device__ __forceinline__ void load(const TreeAttnArgs &a, int s0) {
-        four0 = s0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = s0 + 32 * u + (int)(threadIdx.x & 31);
-            four[u] = i < a.t.num_seqs ? seq_info(a, i) : SeqInfo{0, 0, 0};
-        }
-    }
-    __device__ __forceinline__ int tiles_of(const TreeAttnArgs &a, const SeqInfo &si) const {
-        return groups_of(a, si.n) == groups ? si.tiles() : 0;
-    }
     __device__ __forceinline__ void window(const TreeAttnArgs &a, int s0) {
         base = s0;
         const int i = s0 + (int)(threadIdx.x & 31);
-        mine = i < a.t.num_seqs ? seq_info(a, i) : SeqInfo{0, 0, 0};
-        mine_nt = tiles_of(a, mine);
+        bool bad;
+        mine = i < a.t.num_seqs ? seq_info(a, i, bad) : SeqInfo{0, 0, 0};
+        mine_nt = !Many || groups_of(a, mine.n) == groups ? mine.tiles() : 0;
     }
 
-    // To the range's start; load(a, 0) comes before.
+    // To the range's start.  (Little code: it runs once and comes from memory each time.)
     __device__ __forceinline__ void start(const TreeAttnArgs &a) {
         const int lane = threadIdx.x & 31, Hkv = a.num_kv_heads, B = a.t.num_seqs;
         // Per number of row groups the tiles (below 2^31 with all heads) and sequences.
-        int tiles[kGroups] = {}, seqs[kGroups] = {};
-        for (int b0 = 0; b0 < B; b0 += 128) {
-            if (b0) load(a, b0);
+        int tiles[kG] = {}, seqs[kG] = {};
+        bool any_bad = false;
+#pragma unroll 1
+        for (int i = lane; i < B; i += 64) {
+            bool bad[2] = {};
+            const SeqInfo x = seq_info(a, i, bad[0]);
+            const SeqInfo y = i + 32 < B ? seq_info(a, i + 32, bad[1]) : SeqInfo{0, 0, 0};
+            any_bad |= bad[0] || bad[1];
+            const int cx = x.n ? groups_of(a, x.n) : 0, cy = y.n ? groups_of(a, y.n) : 0;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int nt = four[u].tiles(), c = groups_of(a, four[u].n);
-#pragma unroll
-                for (int k = 0; k < kGroups; ++k)
-                    if (nt && c == k + 1) {
-                        tiles[k] += nt;
-                        ++seqs[k];
-                    }
+            for (int k = 0; k < kG; ++k) {
+                tiles[k] += (cx == k + 1 ? x.tiles() : 0) + (cy == k + 1 ? y.tiles() : 0);
+                seqs[k] += (cx == k + 1) + (cy == k + 1);
             }
         }
+        if (any_bad) atomicOr(&g_err_tree_attention, kErrOob);
         long long all_tiles = 0;
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            if (k >= a.row_groups) break;
+        for (int k = 0; k < kG; ++k) {
             tiles[k] = __reduce_add_sync(0xffffffffu, tiles[k]);
             seqs[k] = __reduce_add_sync(0xffffffffu, seqs[k]);
             all_tiles += (long long)tiles[k] * (Hkv * (k + 1));
@@ -247,7 +269,7 @@ struct Walk {
         int teams = a.ctas, team = blockIdx.x, total = tiles[0] + extra * seqs[0];
         groups = 1;
         rg = 0;
-        if (a.row_groups > 1) {
+        if constexpr (Many) {
             int units[kGroups], n[kGroups], big = 0, rest = 0, left = a.ctas, at_cta = team;
             float all = 0.f, most = 0.f;
 #pragma unroll
@@ -288,46 +310,25 @@ struct Walk {
         end = team < teams ? begin + share + (team < more ? 1 : 0) : 0;
         s = pre = base = 0;
         if (x >= end) return;
-        // The sequence that holds x: its 128, its 32, itself.
-        for (int b0 = 0; b0 < B; b0 += 128) {
-            if (four0 != b0) load(a, b0);
-            int units[4], sum[4], block = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int nt = tiles_of(a, four[u]);
-                units[u] = nt ? nt + extra : 0;
-                sum[u] = __reduce_add_sync(0xffffffffu, units[u]);
-                block += sum[u];
-            }
-            if (x >= Hkv * (pre + block)) {
-                pre += block;
-                continue;
-            }
-            int mine_units = units[0];
-            base = b0;
-            mine = four[0];
-            bool here = x < Hkv * (pre + sum[0]);
-#pragma unroll
-            for (int u = 1; u < 4; ++u) {
-                if (here) continue;
-                pre += sum[u - 1];
-                here = x < Hkv * (pre + sum[u]);
-                base = b0 + 32 * u;
-                mine = four[u];
-                mine_units = units[u];
-            }
-            mine_nt = mine_units ? mine_units - extra : 0;
-            int incl = mine_units;
+        // The sequence that holds x: its 32, itself.
+#pragma unroll 1
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            window(a, b0);
+            const int units = mine_nt ? mine_nt + extra : 0;
+            int incl = units;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
             const unsigned past = __ballot_sync(0xffffffffu, x < Hkv * (pre + incl));
-            const int at_lane = __ffs((int)past) - 1;
-            s = base + at_lane;
-            pre += __shfl_sync(0xffffffffu, incl - mine_units, at_lane);
-            return;
+            if (past) {
+                const int at_lane = __ffs((int)past) - 1;
+                s = b0 + at_lane;
+                pre += __shfl_sync(0xffffffffu, incl - units, at_lane);
+                return;
+            }
+            pre += __shfl_sync(0xffffffffu, incl, 31);
         }
         x = end;  // (not reached)
     }
@@ -367,12 +368,13 @@ __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) {
 
 template <int D, bool KV8, bool Two>
 __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
-    tree_attention_kernel(const __grid_constant__ CUtensorMap kv_map, const TreeAttnArgs a) {
+    tree_attention_kernel(const __grid_constant__ CUtensorMap kv_map,
+                          const __grid_constant__ CUtensorMap q_map, const TreeAttnArgs a) {
     using L = Tlay<D, KV8, Two>;
     // No static shared memory: the dynamic part then starts at the (1024-byte aligned)
     // beginning, and two CTAs' 112 KB of operands fit one SM.
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sQ = smem, *sK = smem + L::kK, *sV = smem + L::kV;
+    uint8_t *sQ = smem;
     Sync &sy = *reinterpret_cast<Sync *>(smem + L::kOperands);
     if (smem_u32(smem) & 1023u) {  // the same for every thread: the swizzle needs it
         if (threadIdx.x == 0) atomicOr(&g_err_tree_attention, kErrPrecondition);
@@ -386,20 +388,14 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
     // reads), and the two warps without rows load them a segment ahead.
     constexpr bool two_q = Two;
     constexpr uint32_t soft = two_q ? 2 : 4;  // softmax warps
-    // The warp that issues the scores' products: a seventh of a bf16 pool's CTA with more
-    // rows, else that of the outputs'.
-    constexpr int s_warp = two_q || KV8 ? 1 : 6;
+    constexpr int s_warp = L::kScoreWarp, v_warp = L::kVWarp;
 
     // What needs no memory of the caller's, under the end of the launch before this one.
     if (tid == 0) {
         prefetch_tensormap(&kv_map);
-        for (int i = 0; i < L::kKSlots; ++i) {
-            mbar_init(&sy.k_full[i], 1);
-            mbar_init(&sy.s_full[i], 1);
-        }
-        for (int i = 0; i < L::kVSlots; ++i) {
-            mbar_init(&sy.v_full[i], KV8 ? L::kConv : 1);
-            mbar_init(&sy.pv_done[i], 1);
+        prefetch_tensormap(&q_map);
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(&sy.full[i], KV8 && i >= L::kKSlots ? L::kConv : 1);
         }
         for (int i = 0; i < L::kStages; ++i) {
             mbar_init(&sy.staged[i], 1);
@@ -407,12 +403,16 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sy.p_full[i], soft);
-            mbar_init(&sy.q_full[i], two_q ? 2 : 4);
-            mbar_init(&sy.q_free[i], soft);
+            mbar_init(&sy.pv_issued[i], 1);
+            mbar_init(&sy.q_raw[i], 1);
+            mbar_init(&sy.q_full[i], KV8 && !two_q ? soft : 1);
+            mbar_init(&sy.exp_read[i], soft);
         }
         for (int i = 0; i < kSegs; ++i) mbar_init(&sy.seg_full[i], 1);
         mbar_init(&sy.o_free, soft);
         for (int i = 0; i < 4; ++i) {
+            mbar_init(&sy.s_done[i], 1);
+            mbar_init(&sy.pv_done[i], 1);
             mbar_init(&sy.sane[i], KV8 ? L::kConv : 1);
             sy.bad[i] = -1;
         }
@@ -428,14 +428,14 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         tmem_relinquish();
         asm volatile("griddepcontrol.launch_dependents;" :::);
     }
-    // The producer's warp finds this CTA's range; the sequences' data come meanwhile.
-    Walk w;
-    if (warp == 0) w.load(a, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sy.tmem;
 
+    auto tile_wait = [&](uint64_t (&bars)[4], int i) {
+        return all_wait(&bars[i & 3], (uint32_t)(i >> 2) & 1u);
+    };
     // Segment k, once it is known.
     auto segment = [&](int k, Seg &g) -> bool {
         const bool ok = mbar_wait_bounded(&sy.seg_full[k % kSegs], (uint32_t)(k / kSegs) & 1u);
@@ -443,146 +443,168 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         return ok;
     };
 
-    // Rows row0 .. row0 + 31 of a segment's queries into shared memory at dst (K-major, 128B
-    // swizzle): the warp takes them a few at a time, 16 bytes per lane.  Over an FP8 pool the
-    // lane of a row gets its scale's exponent + 127.
+    // A segment's queries come by TMA: its nodes, the heads of its KV head, a panel of 64 dims
+    // per copy.  (Rows behind the tree's are other queries: nobody reads what they give.)  One
+    // thread.
+    auto fetch_q = [&](const Seg &g, int b) {
+        uint64_t *bar = KV8 ? &sy.q_raw[b] : &sy.q_full[b];
+        mbar_arrive_expect_tx(bar, (uint32_t)(L::kPanels * a.part_rows * 128));
+#pragma unroll
+        for (int p = 0; p < L::kPanels; ++p)
+            tma_load_3d(sQ + b * (64 * 128) + p * L::kQPanel, &q_map, bar, 64 * p, g.h() * G,
+                        g.row0 + g.rg() * QT);
+    };
+    // K of an FP8 pool is multiplied as codes, so the query becomes the sum of two e4m3 rows:
+    // scaled by the power of two that puts its largest element in [128, 256), q = hi + lo with
+    // hi the nearest e4m3 number (4 significant bits of bf16's 8) and lo what is left.  That is
+    // exact for elements down to 2^-9 of the largest; below, e4m3's smallest step leaves an
+    // error of at most 2^-10, or 2^-17 of the largest element, no more than fp32 loses in the
+    // 128-term sum.  The softmax takes the scaling back; a row with NaN or infinities becomes
+    // NaN through it (exponent 255).
     //
-    // K of an FP8 pool is multiplied as codes, so the query becomes the sum of two e4m3
-    // rows: scaled by the power of two that puts its largest element in [128, 256),
-    // q = hi + lo with hi the nearest e4m3 number (4 significant bits of bf16's 8) and lo
-    // what is left.  That is exact for elements down to 2^-9 of the largest; below, e4m3's
-    // smallest step leaves an error of at most 2^-10, or 2^-17 of the largest element, no
-    // more than fp32 loses in the 128-term sum.  The softmax takes the scaling back; a row
-    // with NaN or infinities becomes NaN through it (exponent 255).
-    auto load_rows = [&](const Seg &g, int first, uint8_t *dst) -> int {
-        constexpr int kC = D / 8, kR = 32 / kC;  // chunks of a row, rows at a time
-        constexpr int kBatch = 8;
-        int exponent = 127;
-        const int rg = g.rg(), nodes = min(QT, g.n() - rg * QT);
-        if (first < nodes * G) {
-            const int c = lane % kC, row0 = first + lane / kC;
-            const uint32_t flip = a.negate_q ? 0x80008000u : 0u;  // exact bf16 negation
-            int node = row0 / G, head = row0 - node * G;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + ((size_t)(g.row0 + rg * QT) * a.num_heads + (size_t)g.h() * G) * D) + c;
-#pragma unroll 1
-            for (int k0 = 0; k0 < 32 / kR; k0 += kBatch) {
-                uint4 v[kBatch];
+    // Rows [first, end) of a segment's queries, in place, two at a time: a row's 256 bytes lie
+    // where its two e4m3 rows will.  (Little code, since it runs once a segment and comes from
+    // memory each time: unrolled eight times, with the loads, it took 15000 cycles.)
+    auto split_q = [&](int b, int first, int end) {
+        uint8_t *q = sQ + b * (64 * 128);
+        const int c = lane & 15;
+#pragma unroll 2
+        for (int r = first + (lane >> 4); r < end + (lane >> 4); r += 2) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(
+                q + (c >> 3) * L::kQPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            // The row's largest element, as bf16 bits without the sign.
+            uint32_t top = 0u;
+            auto up = [&](uint32_t x) { top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu)); };
+            up(v.x);
+            up(v.y);
+            up(v.z);
+            up(v.w);
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    v[k] = node < nodes
-                               ? __ldg(src + ((size_t)node * a.num_heads + head) * kC)
-                               : make_uint4(0, 0, 0, 0);
-                    head += kR;
+            for (int o = 8; o > 0; o >>= 1)
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int ex = max(-119, min(127, top ? (int)(top >> 7) - 127 : 0));
+            const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+            uint32_t hi[2], lo[2];
 #pragma unroll
-                    for (int t = 0; t < kR; ++t)
-                        if (head >= G) {
-                            head -= G;
-                            ++node;
-                        }
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int r = row0 + kR * (k0 + k);
-                    v[k].x ^= flip;
-                    v[k].y ^= flip;
-                    v[k].z ^= flip;
-                    v[k].w ^= flip;
-                    if constexpr (!KV8) {
-                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * L::kQPanel + r * 128 +
-                                                   (((c & 7) ^ (r & 7)) << 4)) = v[k];
-                    } else {
-                        // The row's largest element, as bf16 bits without the sign.
-                        uint32_t top = 0u;
-                        auto up = [&](uint32_t x) {
-                            top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
-                        };
-                        up(v[k].x);
-                        up(v[k].y);
-                        up(v[k].z);
-                        up(v[k].w);
-#pragma unroll
-                        for (int o = kC / 2; o > 0; o >>= 1)
-                            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int ex =
-                            max(-119, min(127, top ? (int)(top >> 7) - 127 : 0));
-                        const float down = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-                        uint32_t hi[2], lo[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t w0 = i ? v[k].z : v[k].x, w1 = i ? v[k].w : v[k].y;
-                            const float x0 = bf16_lo(w0) * down, x1 = bf16_hi(w0) * down;
-                            const float x2 = bf16_lo(w1) * down, x3 = bf16_hi(w1) * down;
-                            hi[i] = pack_e4m3x2(x0, x1) | pack_e4m3x2(x2, x3) << 16;
-                            uint32_t f0, f1;
-                            e4m3x4_to_f16x4(hi[i], f0, f1);
-                            lo[i] = pack_e4m3x2(x0 - f16_lo(f0), x1 - f16_hi(f0)) |
-                                    pack_e4m3x2(x2 - f16_lo(f1), x3 - f16_hi(f1)) << 16;
-                        }
-                        uint8_t *at = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-                        *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2 *>(at + L::kQPanel) = make_uint2(lo[0], lo[1]);
-                        // To the lane of the row.
-                        const int mine = __shfl_sync(
-                            0xffffffffu, top >= 0x7f80u ? 255 : 127 + ex - 7, (lane % kR) * kC);
-                        if (lane / kR == k0 + k) exponent = mine;
-                    }
-                }
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t w0 = i ? v.z : v.x, w1 = i ? v.w : v.y;
+                const float x0 = bf16_lo(w0) * down, x1 = bf16_hi(w0) * down;
+                const float x2 = bf16_lo(w1) * down, x3 = bf16_hi(w1) * down;
+                hi[i] = pack_e4m3x2(x0, x1) | pack_e4m3x2(x2, x3) << 16;
+                uint32_t f0, f1;
+                e4m3x4_to_f16x4(hi[i], f0, f1);
+                lo[i] = pack_e4m3x2(x0 - f16_lo(f0), x1 - f16_hi(f0)) |
+                        pack_e4m3x2(x2 - f16_lo(f1), x3 - f16_hi(f1)) << 16;
             }
+            __syncwarp();  // the row is read
+            uint8_t *at = q + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+            *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(at + L::kQPanel) = make_uint2(lo[0], lo[1]);
+            if (c == 0)
+                sy.q_exp[b * 64 + r] = (uint8_t)(top >= 0x7f80u ? 255 : 127 + ex - 7);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        return exponent;
     };
-    // What a row's scores are multiplied with, from its exponent.
+    auto rows_of = [&](const Seg &g) { return min(QT, g.n() - g.rg() * QT) * G; };
+    // What a row's scores are multiplied with (FP8: from its exponent).
     auto row_scale = [&](int exponent) -> float {
         if constexpr (!KV8) return a.scale_log2;
         return exponent == 255
-               ? NAN
-               : a.scale_log2 * a.k_scale * __uint_as_float((uint32_t)exponent << 23);
+                   ? NAN
+                   : a.scale_log2 * a.k_scale * __uint_as_float((uint32_t)exponent << 23);
+    };
+
+    // K and V come through the block table, a block's rows of one head per copy (a box), the
+    // boxes of a tile issued by as many lanes.
+    const int bs = a.block_size, bs_bits = 31 - __clz(bs), nbox = kKeys / bs;
+    const uint64_t policy = policy_evict_first();
+    // This lane's table entry for tile j; -1 << 30 for no box: outside the tile or past the
+    // sequence.
+    auto entry = [&](const int32_t *bt, int j, int len) {
+        const int tok = j * kKeys + lane * bs;
+        return lane < nbox && tok < len ? bt[tok >> bs_bits] : -(1 << 30);
+    };
+    // Its TMA row for K, wholly outside the map (zeros, nothing read) for no box or a bad
+    // block id; and V's.
+    auto row_of = [&](int blk, int head) {
+        if (blk == -(1 << 30)) return blk;
+        if (blk < 0 || blk >= a.num_blocks) {
+            atomicOr(&g_err_tree_attention, kErrOob);
+            return -(1 << 30);
+        }
+        return ((blk * 2) * Hkv + head) * bs;
+    };
+    auto v_row = [&](int r) { return r < -(1 << 29) ? r : r + Hkv * bs; };
+    auto copy = [&](uint8_t *dst, uint64_t *bar, uint32_t bytes, int row) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (lane < nbox) {
+            if constexpr (KV8)
+                tma_load_2d_hint(dst + lane * bs * 128, &kv_map, bar, 0, row, policy);
+            else  // the pool's rows in groups of 8 (blocks are whole groups)
+                tma_load_4d_hint(dst + lane * (bs / 8) * L::kGroup, &kv_map, bar, row >> 3,
+                                 policy);
+        }
+    };
+    // K / V of tile i, once what lay in the slot before is read.
+    auto load_k = [&](int i, int row) -> bool {
+        const auto p = L::k(i);
+        bool ok = true;
+        if constexpr (KV8) {
+            if (i >= L::kKSlots) ok = tile_wait(sy.s_done, i - L::kKSlots);
+        } else if constexpr (D == 128) {  // V of tile i - 4 (K 0 before K 3)
+            if (i >= 4) ok = tile_wait(sy.pv_done, i - 4);
+            if (i == 3) ok = tile_wait(sy.s_done, 0);
+        } else {
+            if (i >= 5) ok = tile_wait(sy.s_done, i - 4);
+        }
+        if (ok) copy(smem + p.at, &sy.full[p.slot], (uint32_t)L::kKTile, row);
+        return ok;
+    };
+    auto load_v = [&](int i, int row) -> bool {
+        if constexpr (KV8) {
+            const int st = i % L::kStages;
+            if (i >= L::kStages &&
+                !all_wait(&sy.stage_free[st], (uint32_t)(i / L::kStages - 1) & 1u))
+                return false;
+            copy(smem + L::kCodes + st * L::kStage, &sy.staged[st], (uint32_t)L::kStage, row);
+            return true;
+        } else {
+            const auto p = L::v(i);
+            bool ok = true;
+            if constexpr (D == 128) {  // K of tile i - 1
+                if (i >= 2) ok = tile_wait(sy.s_done, i - 1);
+            } else {  // V of tile i - 4 (K 0 before V 3)
+                if (i >= 4) ok = tile_wait(sy.pv_done, i - 4);
+                if (i == 3) ok = tile_wait(sy.s_done, 0);
+            }
+            if (ok) copy(smem + p.at, &sy.full[p.slot], (uint32_t)L::kVTile, row);
+            return ok;
+        }
+    };
+    // The copies of the first n tiles have landed.
+    auto land_k = [&](int n) {
+        for (int i = max(0, n - (KV8 ? 3 : 4)); i < n; ++i) {
+            if constexpr (!KV8 && D == 128)  // (V of tile i + 1 may already have the slot)
+                tile_wait(sy.s_done, i);
+            else
+                mbar_wait_bounded(&sy.full[L::k(i).slot], L::k(i).parity());
+        }
+    };
+    auto land_v = [&](int n) {
+        for (int i = max(0, n - (KV8 ? 3 : 4)); i < n; ++i) {
+            if constexpr (KV8)
+                mbar_wait_bounded(&sy.staged[i % L::kStages], (uint32_t)(i / L::kStages) & 1u);
+            else
+                mbar_wait_bounded(&sy.full[L::v(i).slot], L::v(i).parity());
+        }
     };
 
     if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
+        // ------------------------------------------------------------ K (and the segments)
+        Walk<!Two> w;  // this CTA's range
         w.start(a);
-        const int bs = a.block_size, nbox = kKeys / bs;  // a box per block
-        const int v_off = Hkv * bs;
-        const uint64_t policy = policy_evict_first();
-        // Copy a tile's boxes (this lane's at TMA row `row`) to dst.
-        auto copy = [&](uint8_t *dst, uint64_t *bar, uint32_t bytes, int row) {
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-            __syncwarp();
-            if (lane < nbox) {
-                if constexpr (KV8)
-                    tma_load_2d_hint(dst + lane * bs * 128, &kv_map, bar, 0, row, policy);
-                else  // the pool's rows in groups of 8 (blocks are whole groups)
-                    tma_load_4d_hint(dst + lane * (bs / 8) * L::kGroup, &kv_map, bar, row >> 3,
-                                     policy);
-            }
-        };
-        // K / V of tile i, once its slot is free.
-        auto load_k = [&](int i, int row) -> bool {
-            const int st = i % L::kKSlots;
-            if (i >= L::kKSlots &&
-                !all_wait(&sy.s_full[st], (uint32_t)(i / L::kKSlots - 1) & 1u))
-                return false;
-            copy(sK + st * L::kKTile, &sy.k_full[st], (uint32_t)L::kKTile, row);
-            return true;
-        };
-        auto load_v = [&](int i, int row) -> bool {
-            constexpr int kN = KV8 ? L::kStages : L::kVSlots;
-            const int st = i % kN;
-            if (i >= kN && !all_wait(KV8 ? &sy.stage_free[st] : &sy.pv_done[st],
-                                     (uint32_t)(i / kN - 1) & 1u))
-                return false;
-            if constexpr (KV8)
-                copy(smem + L::kCodes + st * L::kStage, &sy.staged[st], (uint32_t)L::kStage, row);
-            else
-                copy(sV + st * L::kVTile, &sy.v_full[st], (uint32_t)L::kVTile, row);
-            return true;
-        };
-        // This lane's box of V where its box of K is at TMA row r.
-        auto v_row = [&](int r) { return r < -(1 << 29) ? r : r + v_off; };
         // The walk is a segment ahead of the copies; what it finds, for every warp.
         int segs = 0;
         bool have = true;
@@ -597,94 +619,116 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             }
             ++segs;
         };
-        publish();
-        if (lane == 0 && !a.whole_segments)
-            a.starts[blockIdx.x] = have && w.at == w.begin
-                                       ? make_int4(w.s, w.h | w.cur.n << 8 | w.rg << 16, w.j0,
-                                                   w.cur.row0)
-                                       : make_int4(-1, 0, 0, 0);
-        // This lane's box of the next tile, one tile ahead of the copies: the table entry
-        // is on its way while the tile before it is copied.
-        int seg_j = 0, seg_j1 = 0, blk = 0, head = 0, seg_h = 0, seg_len = 0;
+        // The table entries come one tile ahead of the copies: entry `blk` is tile it's.
+        int j = 0, j1 = 0, head = 0, len = 0, blk = 0, blk_head = 0;
         const int32_t *bt = nullptr;
-        auto fetch = [&]() -> bool {
-            if (seg_j == seg_j1) {
-                if (!have) return false;
-                seg_j = w.j0;
-                seg_j1 = w.j1;
-                seg_h = w.h;
-                seg_len = w.cur.len;
-                bt = a.block_tables + (size_t)w.s * a.max_blocks;
+        int it = 0, prev = 0;
+        bool ok = true, held = false;
+        for (;;) {
+            if (j == j1 && have) {
+                if (segs > 0) {
+                    j = w.j0;
+                    j1 = w.j1;
+                    head = w.h;
+                    len = w.cur.len;
+                    bt = a.block_tables + (size_t)w.s * a.max_blocks;
+                }
                 publish();
+                if (segs == 1) {
+                    if (lane == 0 && !a.whole_segments)
+                        a.starts[blockIdx.x] =
+                            have && w.at == w.begin
+                                ? make_int4(w.s, w.h | w.cur.n << 8 | w.rg << 16, w.j0, w.cur.row0)
+                                : make_int4(-1, 0, 0, 0);
+                    continue;
+                }
             }
-            const int tok = seg_j * kKeys + lane * bs;
-            blk = -1;
-            head = -1;  // no box: outside the tile or past the sequence
-            if (lane < nbox && tok < seg_len) {
-                blk = bt[tok / bs];
-                head = seg_h;
+            const bool more = j < j1;
+            const int next = more ? entry(bt, j++, len) : 0;
+            if (held) {
+                const int row = row_of(blk, blk_head);
+                if (!(ok = load_k(it, row))) break;
+                // (One warp for both: V a tile behind, as the products go.)
+                if (v_warp == 0 && it > 0 && !(ok = load_v(it - 1, v_row(prev)))) break;
+                prev = row;
+                ++it;
             }
-            ++seg_j;
-            return true;
-        };
-        // The fetched box's TMA row, wholly outside the map (zeros, nothing read) for no box
-        // or a bad block id.
-        auto row_of = [&]() {
-            if (head < 0) return -(1 << 30);
-            if (blk < 0 || blk >= a.num_blocks) {
-                atomicOr(&g_err_tree_attention, kErrOob);
-                return -(1 << 30);
-            }
-            return ((blk * 2) * Hkv + head) * bs;
-        };
-        // K runs one tile ahead of V, as the products do.
-        int it = 0, prev = 0, k_issued = 0, v_issued = 0;
-        bool ok = true, more = fetch();
-        for (; ok && more; ++it) {
-            const int row = row_of();
-            more = fetch();
-            if (!(ok = load_k(it, row))) break;
-            ++k_issued;
-            if (it > 0) {
-                if (!(ok = load_v(it - 1, v_row(prev)))) break;
-                ++v_issued;
-            }
-            prev = row;
+            if (!more) break;
+            held = true;
+            blk = next;
+            blk_head = head;
         }
-        if (ok && it > 0 && (ok = load_v(it - 1, v_row(prev)))) ++v_issued;
+        if (v_warp == 0 && ok && it > 0) ok = load_v(it - 1, v_row(prev));
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
         // Never leave with copies in flight into this CTA's shared memory.
-        for (int i = max(0, k_issued - L::kKSlots); i < k_issued; ++i)
-            mbar_wait_bounded(&sy.k_full[i % L::kKSlots], (uint32_t)(i / L::kKSlots) & 1u);
-        constexpr int kN = KV8 ? L::kStages : L::kVSlots;
-        for (int i = max(0, v_issued - kN); i < v_issued; ++i)
-            mbar_wait_bounded(KV8 ? &sy.staged[i % kN] : &sy.v_full[i % kN],
-                              (uint32_t)(i / kN) & 1u);
+        land_k(it);
+        if (v_warp == 0) land_v(it);
+    } else if (warp == v_warp) {
+        // ------------------------------------------------------------ V
+        int it = 0, k = 0, j = 0, j1 = 0, head = 0, blk = 0;
+        bool ok = true, held = false;
+        Seg g = {};
+        for (;;) {
+            bool more = true;
+            if (j == j1) {
+                if (!(ok = __all_sync(0xffffffffu, segment(k, g)))) break;
+                more = g.j0 < g.j1;
+                j = g.j0;
+                j1 = g.j1;
+                ++k;
+            }
+            const int next =
+                more ? entry(a.block_tables + (size_t)g.s * a.max_blocks, j++, g.len) : 0;
+            if (held) {
+                if (!(ok = load_v(it, v_row(row_of(blk, head))))) break;
+                ++it;
+            }
+            if (!more) break;
+            held = true;
+            blk = next;
+            head = g.h();
+        }
+        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
+        land_v(it);
+    } else if (warp == L::kSplitWarp) {
+        // ------------------------------------------------------------ an FP8 pool's queries
+        // Of up to 64 rows, once the softmax has read the exponents of the segment before the
+        // last.
+        bool ok = true;
+        for (int k = 0;; ++k) {
+            Seg g;
+            const int b = k & 1;
+            const uint32_t par = (uint32_t)(k >> 1) & 1u;
+            if (!(ok = __all_sync(0xffffffffu, segment(k, g))) || g.j0 >= g.j1) break;
+            if (k >= 2 && !(ok = all_wait(&sy.exp_read[b], par ^ 1u))) break;
+            if (!(ok = all_wait(&sy.q_raw[b], par))) break;
+            split_q(b, 0, rows_of(g));
+            if (lane == 0) mbar_arrive(&sy.q_full[b]);
+        }
+        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     } else if (warp == 1 || warp == s_warp) {
         // ------------------------------------------------------------ products
         // A product costs the thread that issues it its share of the tensor pipe, and a commit
-        // some 200 cycles more.  Of many rows the tensor pipe is the bound: the scores' and the
-        // outputs' have a thread each (16 wide trees 140 -> 136 us).  Of up to 64 rows the
-        // chain scores, softmax, output is: one thread, whose products run in order, need
-        // not wait for an output's end before it issues scores over its P (64 FP8 chains 82
-        // us, 90 with two).
+        // some 200 cycles more, so the scores' and the outputs' have a thread each (but for
+        // more than 64 rows over an FP8 pool, whose warps are all in use).
         const uint32_t idesc_s =
             KV8 ? tc_idesc_e4m3(kRows, kKeys) : tc_idesc_bf16(kRows, kKeys, 0);
         const uint32_t idesc_pv = KV8 ? tc_idesc_f16(kRows, D, 1) : tc_idesc_bf16(kRows, D, 1);
         const uint64_t q_desc = tc_desc_sw128(smem_u32(sQ), 16, 1024);
-        const uint64_t k_desc = tc_desc_sw128(smem_u32(sK), 16, KV8 ? 1024 : L::kGroup);
-        const uint64_t v_desc = tc_desc_sw128(smem_u32(sV), L::kPanel, L::kGroup);
-        // S_i = Q.K^T into buffer i & 1, over tile i - 2's P, once the product that reads it
-        // is done.  half: 64-row half of the query tile, in units of 16 bytes.
+        const uint64_t k_desc = tc_desc_sw128(smem_u32(smem), 16, KV8 ? 1024 : L::kGroup);
+        const uint64_t v_desc = tc_desc_sw128(smem_u32(smem), L::kPanel, L::kGroup);
+        // S_i = Q.K^T into buffer i & 1, over tile i - 2's P: the product that reads it was
+        // issued before (products run in the order of their issue).  half: 64-row half of the
+        // query tile, in units of 16 bytes.
         auto scores = [&](int i, uint32_t half) -> bool {
-            const int st = i % L::kKSlots, b = i & 1;
-            if (i >= 2 && s_warp != 1 &&  // (one thread's products run in order)
-                !mbar_wait_bounded(&sy.pv_done[(i - 2) % L::kVSlots],
-                                   (uint32_t)((i - 2) / L::kVSlots) & 1u))
+            const auto p = L::k(i);
+            const int b = i & 1;
+            if (s_warp != 1 && i >= 2 &&
+                !mbar_wait_bounded(&sy.pv_issued[b], (uint32_t)(i / 2 - 1) & 1u))
                 return false;
-            if (!mbar_wait_bounded(&sy.k_full[st], (uint32_t)(i / L::kKSlots) & 1u)) return false;
+            if (!mbar_wait_bounded(&sy.full[p.slot], p.parity())) return false;
             tc_fence_after();
-            const uint64_t kd = k_desc + (uint64_t)((st * L::kKTile) >> 4);
+            const uint64_t kd = k_desc + (uint64_t)(p.at >> 4);
             if constexpr (KV8) {
                 // The queries' two e4m3 parts, 32 dims at a time.
 #pragma unroll
@@ -703,29 +747,34 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                               k > 0 ? 1u : 0u);
                 }
             }
-            tc_commit(&sy.s_full[st]);
+            tc_commit(&sy.s_done[i & 3]);
             return true;
         };
         // O += P_i.V (over O's old contents for a segment's first tile).
         auto output = [&](int i, bool first) -> bool {
-            const int st = i % L::kVSlots, b = i & 1;
-            if (!mbar_wait_bounded(&sy.v_full[st], (uint32_t)(i / L::kVSlots) & 1u)) return false;
+            const auto p = L::v(i);
+            const int b = i & 1;
             if (!mbar_wait_bounded(&sy.p_full[b], (uint32_t)(i / 2) & 1u)) return false;
+            if (!mbar_wait_bounded(&sy.full[p.slot], p.parity())) return false;
             tc_fence_after();
-            const uint64_t vd = v_desc + (uint64_t)((st * L::kVTile) >> 4);
+            const uint64_t vd = v_desc + (uint64_t)(p.at >> 4);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
                 tc_mma_ts(tmem + kColO, tmem + b * kKeys + kk * 8,
                           vd + (uint64_t)((kk * 2 * L::kGroup) >> 4), idesc_pv,
                           (!first || kk > 0) ? 1u : 0u);
-            tc_commit(&sy.pv_done[st]);
+            if (s_warp != 1) {  // scores may be issued over P_i
+                tc_fence_before();
+                mbar_arrive(&sy.pv_issued[b]);
+            }
+            tc_commit(&sy.pv_done[i & 3]);
             return true;
         };
         // Tile i's V in keys [r0, 64), past the context: rows from r1 on (behind the sequence)
         // are zeroed, tree nodes' cleared of NaN and infinities.  True if there were any.
         auto clean = [&](int i, int r0, int r1) -> bool {
             constexpr int kC = 8 * L::kPanels, kN = 4;  // 16-byte chunks of a key; loads at once
-            uint8_t *vs = sV + (i % L::kVSlots) * L::kVTile +
+            uint8_t *vs = smem + L::v(i).at +
                           ((lane % kC) >> 3) * L::kPanel + (lane & 7) * 16;
             auto at = [&](int r) {
                 return reinterpret_cast<uint4 *>(vs + (r >> 3) * L::kGroup + (r & 7) * 128);
@@ -766,10 +815,25 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             fence_proxy_async_smem();
             return bad;
         };
-        // Up to `last` tiles' scores, of segments up to max_seg, one thread.
+        // Up to `last` tiles' scores, of segments up to max_seg, one thread.  It also fetches the
+        // queries: with a place for two segments' in the middle of the segment
+        // before, when the scores of the one before that are done, else after the segment's.
         int s_next = 0, s_left = 0, s_seg = 0;  // next tile, tiles left of its segment, segments
+        int s_first = 0, q_seg = 0;             // the segment's first tile; queries fetched
         uint32_t half = 0;
         bool s_end = false;
+        auto next_q = [&](int tile) -> bool {  // after that tile's scores
+            Seg g;
+            if (!segment(q_seg, g)) return false;
+            if (g.j0 < g.j1) {
+                if (tile >= 0 &&
+                    !mbar_wait_bounded(&sy.s_done[tile & 3], (uint32_t)(tile >> 2) & 1u))
+                    return false;
+                fetch_q(g, two_q ? q_seg & 1 : 0);
+            }
+            ++q_seg;
+            return true;
+        };
         auto fill = [&](int last, int max_seg) -> bool {
             while (s_next < last && !s_end) {
                 if (s_left == 0) {
@@ -779,16 +843,21 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                     s_left = g.j1 - g.j0;
                     s_end = s_left == 0;
                     if (s_end) break;
+                    if (q_seg == s_seg && !next_q(s_next - 1)) return false;
                     const int b = two_q ? s_seg & 1 : 0;
                     if (!mbar_wait_bounded(&sy.q_full[b],
                                            (uint32_t)(two_q ? s_seg >> 1 : s_seg) & 1u))
                         return false;
                     half = b ? 64 * 128 >> 4 : 0;
+                    s_first = s_next;
                     ++s_seg;
                 }
                 if (!scores(s_next, half)) return false;
                 ++s_next;
                 --s_left;
+                if (two_q && q_seg == s_seg && (s_next - s_first == 3 || s_left == 0) &&
+                    !next_q(s_first - 1))
+                    return false;
             }
             return true;
         };
@@ -817,7 +886,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             bool bad = false;
             for (int j = plain; ok && j < n; ++j) {
                 const int i = it + j, k0 = (g.j0 + j) * kKeys;
-                ok = all_wait(&sy.v_full[i % L::kVSlots], (uint32_t)(i / L::kVSlots) & 1u);
+                ok = all_wait(&sy.full[L::v(i).slot], L::v(i).parity());
                 if (!ok) break;
                 bad |= clean(i, max(ctx - k0, 0), min(g.len - k0, kKeys));
                 bad = __any_sync(0xffffffffu, bad);
@@ -829,25 +898,17 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             it += n;
         }
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
+        if (!ok && lane == 0 && warp == s_warp && q_seg > 0) {  // queries in flight
+            const int b = two_q ? (q_seg - 1) & 1 : 0;
+            mbar_wait_bounded(KV8 ? &sy.q_raw[b] : &sy.q_full[b],
+                              (uint32_t)(two_q ? (q_seg - 1) >> 1 : q_seg - 1) & 1u);
+        }
         // Every product must be done before tensor memory is freed.
         if (lane == 0) tc_commit(&sy.drain);
         __syncwarp();
         if (warp == 1) mbar_wait_bounded(&sy.drain, 0);
-    } else if (warp < 4 && two_q) {
-        // ------------------------------------------------------------ queries, a segment ahead
-        const int first = 32 * (warp - 2);
-        bool ok = true;
-        for (int k = 0;; ++k) {
-            Seg g;
-            if (!(ok = __all_sync(0xffffffffu, segment(k, g))) || g.j0 >= g.j1) break;
-            const int b = k & 1;
-            if (k >= 2 && !(ok = all_wait(&sy.q_free[b], (uint32_t)((k >> 1) - 1) & 1u))) break;
-            const int e = load_rows(g, first, sQ + b * (64 * 128));
-            if (KV8) sy.q_exp[b][first + lane] = (uint8_t)e;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sy.q_full[b]);
-        }
-        if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
+    } else if (two_q && warp < 4) {
+        // (Without a task: an FP8 pool's scores and outputs share a thread.)
     } else if (warp < 6) {
         // ------------------------------------------------------------ softmax
         const int row = 32 * (warp & 3) + lane;  // TMEM lane = query row of the tile
@@ -901,11 +962,14 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         int it = 0, seg = 0;
         Seg si;
         bool ok = __all_sync(0xffffffffu, segment(0, si));
-        int exponent = 0;
-        if (!two_q && ok && si.j0 < si.j1) {
-            exponent = load_rows(si, row - lane, sQ);
+        // More than 64 rows over an FP8 pool: a segment's queries, 32 rows per warp.
+        auto queries = [&](const Seg &g, int k) -> bool {
+            if (!all_wait(&sy.q_raw[0], (uint32_t)k & 1u)) return false;
+            split_q(0, row - lane, min(row - lane + 32, rows_of(g)));
             if (lane == 0) mbar_arrive(&sy.q_full[0]);
-        }
+            return true;
+        };
+        if (KV8 && !two_q && ok && si.j0 < si.j1) ok = queries(si, 0);
         while (ok && si.j0 < si.j1) {
             const int s_h = si.h(), s_n = si.n(), j0 = si.j0, j1 = si.j1, rg = si.rg();
             const bool whole = j0 == 0 && j1 * kKeys >= si.len;
@@ -914,9 +978,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             const bool real = real_in(si);
             const bool busy = __any_sync(0xffffffffu, real);
             const bool tree = j1 * kKeys > ctx;  // the piece holds tree nodes
-            if (two_q) {
-                if (!(ok = all_wait(&sy.q_full[seg & 1], (uint32_t)(seg >> 1) & 1u))) break;
-                exponent = sy.q_exp[seg & 1][row & 63];
+            int exponent = 0;
+            if constexpr (KV8) {
+                if (two_q) {
+                    const int b = seg & 1;
+                    if (!(ok = all_wait(&sy.q_full[b], (uint32_t)(seg >> 1) & 1u))) break;
+                    exponent = sy.q_exp[64 * b + (row & 63)];
+                } else {
+                    exponent = sy.q_exp[row];
+                }
             }
             const float scale = row_scale(exponent);
             uint64_t anc = 0;
@@ -946,9 +1016,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             for (int j = j0; j < j1; ++j, ++it) {
                 const int b = it & 1;
                 const uint32_t cs = trow + b * kKeys;  // this tile's scores, then P
-                if (!(ok = all_wait(&sy.s_full[it % L::kKSlots],
-                                    (uint32_t)(it / L::kKSlots) & 1u)))
-                    break;
+                if (!(ok = tile_wait(sy.s_done, it))) break;
                 tc_fence_after();
                 const int k0 = j * kKeys;
                 const bool past = k0 + kKeys > ctx;
@@ -990,6 +1058,10 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                     tmem_ld32(cs, *reinterpret_cast<float(*)[32]>(x));
                     tmem_ld32(cs + 32, *reinterpret_cast<float(*)[32]>(x + 32));
                     tc_wait_ld();
+                    if (a.negate_q) {
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c) x[c] = -x[c];
+                    }
                     if (past) {
                         mask(x, 0);
                         mask(x + 32, 1);
@@ -1005,7 +1077,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                     mx = fmaxf(mx, mz);
                     my = fmaxf(my, mw);
                     mx = fmaxf(mx, my) * scale;
-                    const bool grow = mx > m + kSlack;
+                    const bool grow = real && mx > m + kSlack;  // (other rows hold anything)
                     rescale = __any_sync(0xffffffffu, grow);
                     if (rescale) {
                         const float mn = grow ? fmaxf(m, mx) : m;
@@ -1020,9 +1092,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                     l += (s0 + s1) + (s2 + s3);
                     if (rescale && j > j0) {
                         // The product before this one must be done; the next one waits.
-                        if (!(ok = all_wait(&sy.pv_done[(it - 1) % L::kVSlots],
-                                            (uint32_t)((it - 1) / L::kVSlots) & 1u)))
-                            break;
+                        if (!(ok = tile_wait(sy.pv_done, it - 1))) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
@@ -1042,22 +1112,18 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                 if (lane == 0) mbar_arrive(&sy.p_full[b]);
             }
             if (!ok) break;
-            // This segment's scores are all read: the queries' place is free.
-            if (two_q) {
+            if (KV8 && two_q) {  // (the exponents were used)
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sy.q_free[seg & 1]);
-            } else if (more) {  // the next segment's, while the last products run
-                exponent = load_rows(next, row - lane, sQ);
-                if (lane == 0) mbar_arrive(&sy.q_full[0]);
+                if (lane == 0) mbar_arrive(&sy.exp_read[seg & 1]);
             }
+            // This segment's scores are all done: the next one's queries are on their way.
+            if (KV8 && !two_q && more && !(ok = queries(next, seg + 1))) break;
             bool bad = false;
             if (tree) {  // NaN or infinities in the tree's V?
                 if (!(ok = all_wait(&sy.sane[seg & 3], (uint32_t)(seg >> 2) & 1u))) break;
                 bad = *reinterpret_cast<volatile int *>(&sy.bad[seg & 3]) == seg;
             }
-            if (!(ok = all_wait(&sy.pv_done[(it - 1) % L::kVSlots],
-                                (uint32_t)((it - 1) / L::kVSlots) & 1u)))
-                break;
+            if (!(ok = tile_wait(sy.pv_done, it - 1))) break;
             tc_fence_after();
             if (busy) {
                 const float vsc = KV8 ? a.v_scale : 1.f;
@@ -1144,7 +1210,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         // keys too.
         const int r = (warp - 6) * 32 + lane;
         auto tile = [&](int i, int key, const Seg &g, bool &bad) -> bool {
-            const int ss = i % L::kStages, st = i % L::kVSlots;
+            const int ss = i % L::kStages;
+            const auto p = L::v(i);
             if (!all_wait(&sy.staged[ss], (uint32_t)(i / L::kStages) & 1u)) return false;
             const uint8_t *codes = smem + L::kCodes + ss * L::kStage + r * 128;
             uint4 in[8];
@@ -1163,12 +1230,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                     in[c] = make_uint4(clear(in[c].x), clear(in[c].y), clear(in[c].z),
                                        clear(in[c].w));
             }
-            if (i >= L::kVSlots &&
-                !all_wait(&sy.pv_done[st], (uint32_t)(i / L::kVSlots - 1) & 1u))
-                return false;
-            __syncwarp();  // every lane's codes are read
-            if (lane == 0) mbar_arrive(&sy.stage_free[ss]);
-            uint8_t *base = sV + st * L::kVTile + (r >> 3) * L::kGroup + (r & 7) * 128;
+            if (i >= L::kVSlots && !tile_wait(sy.pv_done, i - L::kVSlots)) return false;
+            uint8_t *base = smem + p.at + (r >> 3) * L::kGroup + (r & 7) * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 uint32_t f[8];
@@ -1185,7 +1248,12 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sy.v_full[st]);
+            // (The stage is freed after the codes' use: freed after their loads alone, the next
+            // tile's copy could overtake them.)
+            if (lane == 0) {
+                mbar_arrive(&sy.stage_free[ss]);
+                mbar_arrive(&sy.full[p.slot]);
+            }
             return true;
         };
         int it = 0;
@@ -1333,12 +1401,13 @@ Shape shape_of(int max_tree, int group, int head_size, int sm_count) {
 }
 
 template <int D, bool KV8, bool Two>
-cudaError_t launch_rows(const CUtensorMap &map, const TreeAttnArgs &a, cudaStream_t stream) {
+cudaError_t launch_rows(const CUtensorMap &map, const CUtensorMap &q_map, const TreeAttnArgs &a,
+                        cudaStream_t stream) {
     using L = Tlay<D, KV8, Two>;
     cudaError_t e = ensure_smem<tree_attention_kernel<D, KV8, Two>>(L::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(tree_attention_kernel<D, KV8, Two>, dim3((unsigned)a.ctas),
-                   L::kThreads, L::kSmem, 1, stream, map, a);
+                   L::kThreads, L::kSmem, 1, stream, map, q_map, a);
     if (e != cudaSuccess || a.whole_segments || a.ctas < 2) return e;
     return launch_pdl(tree_merge_kernel<D>,
                       dim3((unsigned)a.ctas, (unsigned)((a.part_rows + 31) / 32)),
@@ -1346,9 +1415,10 @@ cudaError_t launch_rows(const CUtensorMap &map, const TreeAttnArgs &a, cudaStrea
 }
 
 template <int D, bool KV8>
-cudaError_t launch(const CUtensorMap &map, const TreeAttnArgs &a, cudaStream_t stream) {
-    return a.part_rows <= 64 ? launch_rows<D, KV8, true>(map, a, stream)
-                             : launch_rows<D, KV8, false>(map, a, stream);
+cudaError_t launch(const CUtensorMap &map, const CUtensorMap &q_map, const TreeAttnArgs &a,
+                   cudaStream_t stream) {
+    return a.part_rows <= 64 ? launch_rows<D, KV8, true>(map, q_map, a, stream)
+                             : launch_rows<D, KV8, false>(map, q_map, a, stream);
 }
 
 }  // namespace
@@ -1396,6 +1466,7 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
     a.num_blocks = g.num_blocks;
     a.max_len = max_seq_len;
     a.q_tile = sh.q_tile;
+    a.q_recip = ((1 << 16) + sh.q_tile - 1) / sh.q_tile;
     a.row_groups = sh.row_groups;
     // No more teams than tiles.
     const long long tiles = (long long)t.num_seqs * g.num_kv_heads *
@@ -1410,13 +1481,17 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
     // Contexts of a few tiles: a range of whole segments costs at most those tiles (about
     // 0.6 us each) and saves the merge's launch.
     a.whole_segments = max_seq_len <= kWholeTiles * kKeys;
-    // Measured: about 7000 cycles a change; a tile takes 2400 where HBM bounds it (3: 32
-    // sequences 62.4 -> 60.1 us), 1600 from an FP8 pool or with several row groups, which
-    // the tensor pipe bounds (8: 64 FP8 chains 96 -> 83 us, 16 wide trees 158 -> 145).
-    a.change = kv8 || sh.row_groups > 1 ? 8 : 3;
-    if (kv8) return launch<128, true>(map, a, stream);
-    if (g.head_size == 128) return launch<128, false>(map, a, stream);
-    return launch<64, false>(map, a, stream);
+    // A change costs some 7000 cycles, a tile 2400 where HBM bounds it (without: 32 sequences
+    // 62.7 us, 61.2 with), 1400 to 1800 from an FP8 pool or with several row groups (without:
+    // 64 FP8 chains 93 us, 79 with; 16 wide trees 151, 141).
+    a.change = kv8 || sh.row_groups > 1 ? 6 : 2;
+    CUtensorMap q_map = {};
+    if (!encode_rows_map(&q_map, q, g.head_size, num_heads, t.total_nodes, a.group,
+                         sh.part_rows / a.group))
+        return cudaErrorInvalidValue;
+    if (kv8) return launch<128, true>(map, q_map, a, stream);
+    if (g.head_size == 128) return launch<128, false>(map, q_map, a, stream);
+    return launch<64, false>(map, q_map, a, stream);
 }
 
 }  // namespace pa

@@ -369,6 +369,25 @@ def test_tree_calls_beside_others_on_two_streams():
     assert nxt.tolist() == d.reference[1]
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_does_not_depend_on_what_ran_before(fp8):
+    """The same bits whatever the calls before left in the chip's memories (rows without
+    a query, places not yet written), for few rows in ranges of a few tiles."""
+    others = [Case([700, 1500, 64, 900], [64, 40, 33, 20], 16, 2, 128, 16, seed=24, fp8=f,
+                   q_mult=m) for f in (True, False) for m in (1.0, 30.0)]
+    c = Case([2500] * 5, [3] * 5, 8, 8, 128, 16, seed=7, fp8=fp8, q_mult=2.0)
+    ws, out = c.workspace(), torch.empty_like(c.b.q)
+    work = [(o, o.workspace(), torch.empty_like(o.b.q)) for o in others]
+    want = c.run(ws=ws)
+    _tree.assert_attention(want, *c.reference())
+    for i in range(80):
+        o, ws_o, out_o = work[i % 4]
+        o.run(out=out_o, ws=ws_o)
+        out.fill_(float("nan"))
+        c.run(out=out, ws=ws)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), i
+
+
 # ---------------------------------------------------------------- verification
 def run_verify(d, stream=None, max_tree=None, pad=0):
     """The call's (paths, next tokens), checked for its padding."""
