@@ -14,27 +14,27 @@
 //     Trees of more rows have several row groups, whose CTAs (a team) walk the same keys
 //     side by side (all but the first fetch of a tile hit L2).
 //   * Work = the list of tiles over (sequence, KV head), a list per number of row groups,
-//     each cut into equal contiguous ranges, one per team.  Two CTAs share an
+//     each cut into equal contiguous ranges, one per team (Walk).  Two CTAs share an
 //     SM (each with half of its shared memory and tensor memory), so that one CTA's
 //     loads and products run under the other's softmax.  A segment (sequence, KV
 //     head) that falls across ranges leaves its pieces' (m, l, O) in the workspace,
 //     merged by log-sum-exp in a second, dependent kernel; a segment that lies in one
 //     range is written at once.
-//   * warp 0 streams K and V tiles through the block table, a block's rows of one head
+//   * Warp 0 finds the range, publishes its segments to the other warps and streams K (and
+//     V, or another warp does: kVWarp) through the block table, a block's rows of one head
 //     per copy (its 8-row groups and 64-dim panels in one 4-D box: with a 2-D copy per
-//     panel of 16 rows the copies' issue bounded the kernel at some 125 cycles each);
-//     the table entries are read a tile ahead.
-//   * One thread of warp 1 issues the products: S = Q.K^T into two buffers by turns, up
-//     to two tiles ahead, and O += P.V with P from tensor memory over its own scores.
-//     A product costs it 46 cycles (64 keys) to 64 (128 dims), a commit some 200, a
-//     wait by the whole warp 130: one commit per product group, waits by that thread
-//     alone (16 trees of 33-64 nodes, 8 heads per KV head: 183 -> 159 us).
-//   * Warps 2-5 hold one query row per thread: softmax, P, the O rescale (rare: only
-//     when a row's maximum rises by more than 2^8), the epilogue, the next segment's
-//     queries.  A warp whose 32 rows hold no query skips the softmax.
+//     panel of 16 rows the copies' issue bounded the kernel at some 100 cycles each);
+//     the table entries are read a tile ahead.  The segment's queries come by TMA as well,
+//     those of up to 64 rows a segment ahead.
+//   * Single threads issue the products: S = Q.K^T into two buffers by turns, up to two tiles
+//     ahead, and O += P.V with P from tensor memory over its own scores.  A product takes
+//     46 cycles (64 keys) to 64 (128 dims), a commit some 200 of its thread.
+//   * The softmax warps (two for up to 64 rows, else four) hold one query row per thread:
+//     softmax, P, the O rescale (rare: only when a row's maximum rises by more than 2^8), the
+//     epilogue.  A warp whose 32 rows hold no query skips all that.
 //   * From an FP8 pool K is multiplied as codes, the query being the sum of two e4m3
-//     rows (load_q); only V is converted, to f16, by two more warps.  (Converting both
-//     left the converting warps the bound: 64 sequences' chains 118 us, now 81.)
+//     rows (split_q); only V is converted, to f16, by two more warps.  (Converting both
+//     left the converting warps the bound: 64 sequences' chains 118 us, now 78.)
 //   * Masks: a row's ancestors are a 64-bit word (pointer doubling over the parents,
 //     six shuffle rounds); only tiles that reach past the context look at it.  What
 //     a row does not see gets the score -inf, and V rows of tree nodes are cleared of
@@ -44,11 +44,13 @@
 //     product's operand, the row sum from the fp32 values; the output once to bf16.
 //
 // Measured (GB300, HBM copy 6689 GB/s, whole call): 32 sequences of 512-4096 tokens with
-// 12-16 nodes, 32 query and 8 KV heads of 128: 60 us, 5.1 TB/s; 8 sequences of 1024-131072
-// tokens: 140 us, 6.2 TB/s; 16 sequences of 1024-8192 tokens, 33-64 nodes, 64 and 8 heads:
-// 145 us, 820 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool, 64
-// sequences, chains of 3-8: 81 us, 3.8 TB/s.  What is left in the first: some 4 us until the
-// first tile arrives, 5 us for the merge, the spread of the CTAs' ends.
+// 12-16 nodes, 32 query and 8 KV heads of 128: 60 us, 5.2 TB/s; 8 sequences of 1024-131072
+// tokens with 7-23 nodes: 142 us, 6.1 TB/s; 16 sequences of 1024-8192 tokens, 33-64 nodes,
+// 64 and 8 heads: 131 us, 910 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool,
+// 64 sequences, chains of 3-8: 78 us, 3.9 TB/s.  Per call some 5 us until the first products,
+// 4 to 6 us for the merge.  In the wide case and the FP8 one shared memory bounds a tile: the
+// products read the query tile anew for every 64 keys, some 100 KB a tile and CTA with V's
+// conversion, 1500 cycles for a pair of CTAs at 128 bytes a cycle (measured 1400 to 1800).
 #include <algorithm>
 #include <cmath>
 
@@ -394,9 +396,8 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
     if (tid == 0) {
         prefetch_tensormap(&kv_map);
         prefetch_tensormap(&q_map);
-        for (int i = 0; i < L::kSlots; ++i) {
+        for (int i = 0; i < L::kSlots; ++i)
             mbar_init(&sy.full[i], KV8 && i >= L::kKSlots ? L::kConv : 1);
-        }
         for (int i = 0; i < L::kStages; ++i) {
             mbar_init(&sy.staged[i], 1);
             mbar_init(&sy.stage_free[i], L::kConv);
@@ -708,9 +709,6 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         if (!ok && lane == 0) atomicOr(&g_err_tree_attention, kErrTimeout);
     } else if (warp == 1 || warp == s_warp) {
         // ------------------------------------------------------------ products
-        // A product costs the thread that issues it its share of the tensor pipe, and a commit
-        // some 200 cycles more, so the scores' and the outputs' have a thread each (but for
-        // more than 64 rows over an FP8 pool, whose warps are all in use).
         const uint32_t idesc_s =
             KV8 ? tc_idesc_e4m3(kRows, kKeys) : tc_idesc_bf16(kRows, kKeys, 0);
         const uint32_t idesc_pv = KV8 ? tc_idesc_f16(kRows, D, 1) : tc_idesc_bf16(kRows, D, 1);
@@ -718,8 +716,9 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         const uint64_t k_desc = tc_desc_sw128(smem_u32(smem), 16, KV8 ? 1024 : L::kGroup);
         const uint64_t v_desc = tc_desc_sw128(smem_u32(smem), L::kPanel, L::kGroup);
         // S_i = Q.K^T into buffer i & 1, over tile i - 2's P: the product that reads it was
-        // issued before (products run in the order of their issue).  half: 64-row half of the
-        // query tile, in units of 16 bytes.
+        // issued before (products run in the order of their issue, between two threads that
+        // which the fences and the barrier give).  half: 64-row half of the query tile, in
+        // units of 16 bytes.
         auto scores = [&](int i, uint32_t half) -> bool {
             const auto p = L::k(i);
             const int b = i & 1;
@@ -908,7 +907,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         __syncwarp();
         if (warp == 1) mbar_wait_bounded(&sy.drain, 0);
     } else if (two_q && warp < 4) {
-        // (Without a task: an FP8 pool's scores and outputs share a thread.)
+        // (Without a task.)
     } else if (warp < 6) {
         // ------------------------------------------------------------ softmax
         const int row = 32 * (warp & 3) + lane;  // TMEM lane = query row of the tile
@@ -1277,44 +1276,85 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
     }
 }
 
-// Merge the pieces of segments that were split across CTAs.  Block (w, 32 rows) looks whether
-// CTA w's range starts inside a segment whose first piece is that of the team before; then a
-// lane per row and a warp per D / 16 dims joins the pieces by log-sum-exp in one pass, several
-// pieces' loads in flight.
+// Merge the pieces of segments that were split across CTAs: a lane per row, a warp per
+// D / 16 dims, joined by log-sum-exp in one pass, several pieces' loads in flight.
+//
+// With many segments a block (w, 32 rows) looks whether CTA w's range starts inside a segment
+// whose first piece is that of the team before.  Few segments (at most a quarter of the CTAs)
+// are split into many pieces: a block per segment, 32 rows and quarter of the dims, whose warps
+// also share the pieces out among four groups, joined through shared memory (8 sequences of
+// 1024 .. 131072 tokens, up to some 80 pieces: 143.6 -> 142.4 us for the whole call).
 constexpr int kMergeWarps = 16;
 
-template <int D>
+template <int D, bool kFew>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeAttnArgs a) {
     constexpr int kUnits = D / 4 / kMergeWarps;  // float4 of a row that a thread joins
+    constexpr int kSplit = kFew ? 4 : 1;         // groups of warps that share the pieces
+    __shared__ int s_first, s_count;
+    __shared__ float s_part[kFew ? kMergeWarps : 1][4 * kUnits + 2][32];
     pdl_begin();
-    const int w = blockIdx.x, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row0 = blockIdx.y * 32;
     auto start_of = [&](int i) {
         return i >= 0 && i < a.ctas ? a.starts[i] : make_int4(-1, 0, 0, 0);
     };
-    // Teams of the same segment lie a team's CTAs apart.  That before w's, w's and the next,
-    // one per lane.
-    const int step = a.row_groups == 1 ? 1 : max(1, groups_of(a, (start_of(w).y >> 8) & 255));
-    const int4 st = start_of(w + (lane - 1) * step);
-    const int seq = __shfl_sync(0xffffffffu, st.x, 1), key = __shfl_sync(0xffffffffu, st.y, 1);
-    const int tile = __shfl_sync(0xffffffffu, st.z, 1), node0 = __shfl_sync(0xffffffffu, st.w, 1);
-    if (seq < 0 || tile == 0) return;  // idle, or a segment's start
-    const bool prev_same = __shfl_sync(0xffffffffu, st.x == seq && st.y == key, 0);
-    if (prev_same && __shfl_sync(0xffffffffu, st.z, 0) > 0) return;  // an earlier one merges it
+    auto step_of = [&](int key) {  // a team's CTAs
+        return a.row_groups == 1 ? 1 : max(1, groups_of(a, (key >> 8) & 255));
+    };
+    int w, n, key, node0, step;  // first CTA that starts inside, pieces
+    bool prev_same;
+    if constexpr (kFew) {
+        const int rg = blockIdx.x % a.row_groups, sh = blockIdx.x / a.row_groups;
+        const int seq = sh / a.num_kv_heads, head = sh - seq * a.num_kv_heads;
+        if (threadIdx.x == 0) {
+            s_first = a.ctas;
+            s_count = 0;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.ctas; i += blockDim.x) {
+            const int4 e = a.starts[i];
+            if (e.x == seq && (e.y & 255) == head && e.y >> 16 == rg && e.z > 0) {
+                atomicMin(&s_first, i);
+                atomicAdd(&s_count, 1);
+            }
+        }
+        __syncthreads();
+        if (s_count == 0) return;
+        w = s_first;
+        n = s_count + 1;
+        const int4 st = start_of(w);
+        key = st.y;
+        node0 = st.w;
+        step = step_of(key);
+        const int4 before = start_of(w - step);
+        prev_same = before.x == seq && before.y == key;
+    } else {
+        w = blockIdx.x;
+        step = a.row_groups == 1 ? 1 : step_of(start_of(w).y);
+        // The team before w's, w's and the next, one per lane.
+        const int4 st = start_of(w + (lane - 1) * step);
+        const int seq = __shfl_sync(0xffffffffu, st.x, 1);
+        key = __shfl_sync(0xffffffffu, st.y, 1);
+        node0 = __shfl_sync(0xffffffffu, st.w, 1);
+        // Idle, or a segment's start.
+        if (seq < 0 || __shfl_sync(0xffffffffu, st.z, 1) == 0) return;
+        prev_same = __shfl_sync(0xffffffffu, st.x == seq && st.y == key, 0);
+        if (prev_same && __shfl_sync(0xffffffffu, st.z, 0) > 0) return;  // an earlier one's
+        n = 1;
+        for (int base = w;; base += 32 * step) {
+            const int4 e = start_of(base + lane * step);
+            const unsigned in = __ballot_sync(0xffffffffu, e.x == seq && e.y == key);
+            n += __popc(in);
+            if (in != 0xffffffffu) break;
+        }
+    }
     const int nodes = (key >> 8) & 255, head = key & 255, rg = key >> 16;
     const int rows = min(a.q_tile, nodes - rg * a.q_tile) * a.group;
     if (row0 >= rows) return;
-    // Pieces: the team before's and those of the teams from w's on that start in the segment.
-    int n = 1;
-    for (int base = w;; base += 32 * step) {
-        const int4 e = start_of(base + lane * step);
-        const unsigned in = __ballot_sync(0xffffffffu, e.x == seq && e.y == key);
-        n += __popc(in);
-        if (in != 0xffffffffu) break;
-    }
-    const int row = row0 + lane;
-    if (row >= rows) return;
-    const int unit0 = (threadIdx.x >> 5) * kUnits;
+    const int row = min(row0 + lane, rows - 1);
+    const int unit0 = (kFew ? blockIdx.z * (kMergeWarps / kSplit) + warp % (kMergeWarps / kSplit)
+                            : warp) * kUnits;
+    const int first = kFew ? warp / (kMergeWarps / kSplit) : 0;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
     const float4 *acc = reinterpret_cast<const float4 *>(a.part_acc);
     float M = -INFINITY, den = 0.f;
@@ -1322,14 +1362,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) num[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kBatch = 4;
-    for (int k0 = 0; k0 < n; k0 += kBatch) {
+    for (int k0 = first; k0 < n; k0 += kBatch * kSplit) {
+        auto at = [&](int k) { return k0 + k * kSplit; };  // the batch's k-th piece
         float2 e[kBatch];
         float4 v[kBatch][kUnits];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if (k0 + k < n) {
-                const size_t cta = (size_t)(w + (k0 + k - 1) * step);
-                const size_t rec = cta * 2 + (k0 + k == 0 && !prev_same ? 1 : 0);
+            if (at(k) < n) {
+                const size_t cta = (size_t)(w + (at(k) - 1) * step);
+                const size_t rec = cta * 2 + (at(k) == 0 && !prev_same ? 1 : 0);
                 e[k] = ml[rec * a.part_rows + row];
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i)
@@ -1340,7 +1381,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
         float mn = M;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (k0 + k < n) mn = fmaxf(mn, e[k].x);
+            if (at(k) < n) mn = fmaxf(mn, e[k].x);
         const float ref = mn == -INFINITY ? 0.f : mn, c = fast_exp2(M - ref);
         M = mn;
         den *= c;
@@ -1353,7 +1394,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if (k0 + k >= n) break;
+            if (at(k) >= n) break;
             const float g = fast_exp2(e[k].x - ref);
             den += g * e[k].y;
 #pragma unroll
@@ -1365,6 +1406,36 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
             }
         }
     }
+    if constexpr (kFew) {
+        float *own = &s_part[warp][0][lane];
+        own[0] = M;
+        own[32] = den;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            own[32 * (2 + 4 * i)] = num[i].x;
+            own[32 * (3 + 4 * i)] = num[i].y;
+            own[32 * (4 + 4 * i)] = num[i].z;
+            own[32 * (5 + 4 * i)] = num[i].w;
+        }
+        __syncthreads();
+        if (first != 0) return;
+#pragma unroll
+        for (int p = 1; p < kSplit; ++p) {
+            const float *o = &s_part[warp + p * (kMergeWarps / kSplit)][0][lane];
+            const float mn = fmaxf(M, o[0]), ref = mn == -INFINITY ? 0.f : mn;
+            const float c = fast_exp2(M - ref), g = fast_exp2(o[0] - ref);
+            M = mn;
+            den = den * c + g * o[32];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+                num[i].x = num[i].x * c + g * o[32 * (2 + 4 * i)];
+                num[i].y = num[i].y * c + g * o[32 * (3 + 4 * i)];
+                num[i].z = num[i].z * c + g * o[32 * (4 + 4 * i)];
+                num[i].w = num[i].w * c + g * o[32 * (5 + 4 * i)];
+            }
+        }
+    }
+    if (row0 + lane >= rows) return;
     const float inv = 1.f / den;
     const int node = node0 + rg * a.q_tile + row / a.group;
     uint2 *dst = reinterpret_cast<uint2 *>(
@@ -1409,8 +1480,12 @@ cudaError_t launch_rows(const CUtensorMap &map, const CUtensorMap &q_map, const 
     e = launch_pdl(tree_attention_kernel<D, KV8, Two>, dim3((unsigned)a.ctas),
                    L::kThreads, L::kSmem, 1, stream, map, q_map, a);
     if (e != cudaSuccess || a.whole_segments || a.ctas < 2) return e;
-    return launch_pdl(tree_merge_kernel<D>,
-                      dim3((unsigned)a.ctas, (unsigned)((a.part_rows + 31) / 32)),
+    const unsigned rows = (unsigned)((a.part_rows + 31) / 32);
+    const long long segments = (long long)a.t.num_seqs * a.num_kv_heads * a.row_groups;
+    if (4 * segments <= a.ctas)
+        return launch_pdl(tree_merge_kernel<D, true>, dim3((unsigned)segments, rows, 4),
+                          kMergeWarps * 32, 0, 1, stream, a);
+    return launch_pdl(tree_merge_kernel<D, false>, dim3((unsigned)a.ctas, rows),
                       kMergeWarps * 32, 0, 1, stream, a);
 }
 
