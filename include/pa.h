@@ -568,6 +568,54 @@ pa_status pa_tree_accept_fp8(void *kv_cache, int num_blocks, int block_size, int
                              int32_t *new_seq_lens, pa_stream_t stream);
 
 /*
+ * The arguments of the three calls as structs, for callers to whom one argument is
+ * cheaper than twenty (the Python binding): the same calls, checks and statuses.
+ * kv8 != 0: the FP8 form.  *args is not kept; PA_ERR_INVALID_ARG for NULL.
+ */
+typedef struct pa_tree_attention_args {
+    void *out;
+    const void *q;
+    const int32_t *cu_tree_lens;
+    const int32_t *parents;
+    const void *kv_cache;
+    const int32_t *block_tables;
+    const int32_t *seq_lens;
+    void *workspace;
+    size_t workspace_bytes;
+    pa_stream_t stream;
+    int32_t num_seqs, total_nodes, max_tree_len, num_blocks, block_size, num_heads, num_kv_heads;
+    int32_t head_size, max_blocks_per_seq, max_seq_len, kv8;
+    float scale, k_scale, v_scale;
+} pa_tree_attention_args;
+
+typedef struct pa_tree_verify_args {
+    int32_t *accepted, *num_accepted, *next_tokens;
+    const float *target_probs, *draft_probs;
+    const int32_t *tokens, *cu_tree_lens, *parents;
+    const float *accept_u, *sample_u;
+    pa_stream_t stream;
+    int64_t target_row_stride, draft_row_stride;
+    int32_t num_seqs, total_nodes, max_tree_len, vocab_size;
+} pa_tree_verify_args;
+
+typedef struct pa_tree_accept_args {
+    void *kv_cache;
+    const int32_t *accepted, *num_accepted, *cu_tree_lens, *block_tables, *seq_lens;
+    int32_t *new_seq_lens;
+    pa_stream_t stream;
+    int32_t num_blocks, block_size, num_kv_heads, head_size, num_seqs, max_tree_len;
+    int32_t max_blocks_per_seq, kv8;
+} pa_tree_accept_args;
+
+pa_status pa_tree_attention_packed(const pa_tree_attention_args *args);
+pa_status pa_tree_verify_packed(const pa_tree_verify_args *args);
+pa_status pa_tree_accept_packed(const pa_tree_accept_args *args);
+
+/* sizeof the struct of pa_tree_attention (0), pa_tree_verify (1), pa_tree_accept (2), for
+ * callers that lay it out themselves; 0 for another call. */
+size_t pa_tree_args_bytes(int call);
+
+/*
  * Synchronise `stream`, then read and clear the device error word the kernels
  * of this library set on the current device.  Returns PA_OK, PA_ERR_TIMEOUT,
  * PA_ERR_OOB or PA_ERR_PRECONDITION (the first of these that was set, in this

@@ -34,7 +34,9 @@ EXPORTS = ("pa_status_string", "pa_kv_block_bytes", "pa_kv_block_bytes_dtype", "
            "pa_attention_varlen_workspace_bytes", "pa_attention_varlen",
            "pa_attention_varlen_fp8", "pa_varlen_args_bytes", "pa_attention_varlen_packed",
            "pa_tree_attention_workspace_bytes", "pa_tree_attention", "pa_tree_attention_fp8",
-           "pa_tree_verify", "pa_tree_accept", "pa_tree_accept_fp8", "pa_error_check")
+           "pa_tree_verify", "pa_tree_accept", "pa_tree_accept_fp8", "pa_tree_attention_packed",
+           "pa_tree_verify_packed", "pa_tree_accept_packed", "pa_tree_args_bytes",
+           "pa_error_check")
 
 # Nodes of a draft tree, at most (PA_TREE_MAX_NODES).
 TREE_MAX_NODES = 64
@@ -45,6 +47,9 @@ TREE_MAX_NODES = 64
 # max_prefill_q_len, num_blocks, block_size, num_heads, num_kv_heads, head_size,
 # max_blocks_per_seq, max_seq_len, kv8; scale, k_scale, v_scale.
 VARLEN_ARGS = struct.Struct("<12Q12i3f")
+# pa_tree_attention_args, pa_tree_verify_args and pa_tree_accept_args likewise, in the order
+# of their members.
+TREE_ARGS = (struct.Struct("<10Q11i3f"), struct.Struct("<11Q2q4i"), struct.Struct("<8Q8i"))
 _BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
 _tls = threading.local()  # one packed-argument buffer per thread
 
@@ -132,6 +137,14 @@ def lib(path: Optional[str] = None):
     for f in (L.pa_tree_accept, L.pa_tree_accept_fp8):
         f.restype = i
         f.argtypes = [P, i, i, i, i, P, P, P, i, i, P, i, P, P, P]
+    for f in (L.pa_tree_attention_packed, L.pa_tree_verify_packed, L.pa_tree_accept_packed):
+        f.restype = i
+        f.argtypes = [P]
+    L.pa_tree_args_bytes.restype = sz
+    L.pa_tree_args_bytes.argtypes = [i]
+    for call, layout in enumerate(TREE_ARGS):
+        if L.pa_tree_args_bytes(call) != layout.size:
+            raise RuntimeError("the tree calls' argument structs differ from this binding's")
     L.pa_error_check.restype = i
     L.pa_error_check.argtypes = [P]
     if path is None:
@@ -548,12 +561,22 @@ def _launch_stream(stream, dev: int) -> int:
     """The stream of a call whose tensors are on device dev.  The library launches on the
     current device: tensors elsewhere are refused.  (The current stream's handle is read
     without building a Stream object, which would cost more than the launch.)"""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
+
+
+def _tree_args():
+    """This thread's buffer for the tree calls' arguments, and its address."""
+    try:
+        return _tls.tree
+    except AttributeError:
+        buf = ctypes.create_string_buffer(max(layout.size for layout in TREE_ARGS))
+        _tls.tree = (buf, ctypes.addressof(buf))
+        return _tls.tree
 
 
 def _tree_attention(fp8, out, q, cu_tree_lens, parents, max_tree_len, kv_cache, block_tables,
@@ -593,14 +616,14 @@ def _tree_attention(fp8, out, q, cu_tree_lens, parents, max_tree_len, kv_cache, 
         _same_device(kv_cache, q, out, cu_tree_lens, parents, block_tables, seq_lens, workspace)
         raise ValueError("inconsistent tree attention shapes")
     L = _lib if _lib is not None else lib()
-    args = (out.data_ptr(), q.data_ptr(), cu_tree_lens.data_ptr(), parents.data_ptr(), B, rows,
-            max_tree_len, kv_cache.data_ptr(), NB, bs, Hq, Hkv, D, block_tables.data_ptr(),
-            MB, seq_lens.data_ptr(), max_seq_len, scale)
-    tail = (workspace.data_ptr(), workspace.numel(), _launch_stream(stream, dev))
-    if fp8:
-        st = L.pa_tree_attention_fp8(*args, scales[0], scales[1], *tail)
-    else:
-        st = L.pa_tree_attention(*args, *tail)
+    ks, vs = scales if fp8 else (1.0, 1.0)
+    buf, addr = _tree_args()
+    TREE_ARGS[0].pack_into(
+        buf, 0, out.data_ptr(), q.data_ptr(), cu_tree_lens.data_ptr(), parents.data_ptr(),
+        kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _launch_stream(stream, dev) or 0, B, rows, max_tree_len, NB, bs, Hq,
+        Hkv, D, MB, max_seq_len, fp8, scale, ks, vs)
+    st = L.pa_tree_attention_packed(addr)
     if st:
         raise PaError(st, "pa_tree_attention_fp8" if fp8 else "pa_tree_attention")
 
@@ -694,15 +717,18 @@ def pa_tree_verify(accepted: torch.Tensor, num_accepted: torch.Tensor, next_toke
                      accept_u, sample_u, target_probs, draft_probs)
         raise ValueError("inconsistent tree verification shapes")
     ts = _prob_rows(target_probs, "target_probs", rows, V)
-    dp, ds = None, 0
+    dp = ds = 0
     if draft_probs is not None:
         ds = _prob_rows(draft_probs, "draft_probs", rows, V)
         dp = draft_probs.data_ptr()
     L = _lib if _lib is not None else lib()
-    st = L.pa_tree_verify(accepted.data_ptr(), num_accepted.data_ptr(), next_tokens.data_ptr(),
-                          target_probs.data_ptr(), ts, dp, ds, tokens.data_ptr(),
-                          cu_tree_lens.data_ptr(), parents.data_ptr(), B, rows, max_tree, V,
-                          accept_u.data_ptr(), sample_u.data_ptr(), _launch_stream(stream, dev))
+    buf, addr = _tree_args()
+    TREE_ARGS[1].pack_into(
+        buf, 0, accepted.data_ptr(), num_accepted.data_ptr(), next_tokens.data_ptr(),
+        target_probs.data_ptr(), dp, tokens.data_ptr(), cu_tree_lens.data_ptr(),
+        parents.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
+        _launch_stream(stream, dev) or 0, ts, ds, B, rows, max_tree, V)
+    st = L.pa_tree_verify_packed(addr)
     if st:
         raise PaError(st, "pa_tree_verify")
 
@@ -751,11 +777,13 @@ def pa_tree_accept(kv_cache: torch.Tensor, accepted: torch.Tensor, num_accepted:
                      new_seq_lens)
         raise ValueError("inconsistent tree acceptance shapes")
     L = _lib if _lib is not None else lib()
-    st = (L.pa_tree_accept_fp8 if dt is _U8 else L.pa_tree_accept)(
-        kv_cache.data_ptr(), NB, bs, Hkv, D, accepted.data_ptr(), num_accepted.data_ptr(),
-        cu_tree_lens.data_ptr(), B, max_tree, block_tables.data_ptr(), MB,
-        seq_lens.data_ptr(), None if new_seq_lens is None else new_seq_lens.data_ptr(),
-        _launch_stream(stream, dev))
+    buf, addr = _tree_args()
+    TREE_ARGS[2].pack_into(
+        buf, 0, kv_cache.data_ptr(), accepted.data_ptr(), num_accepted.data_ptr(),
+        cu_tree_lens.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+        0 if new_seq_lens is None else new_seq_lens.data_ptr(), _launch_stream(stream, dev) or 0,
+        NB, bs, Hkv, D, B, max_tree, MB, dt is _U8)
+    st = L.pa_tree_accept_packed(addr)
     if st:
         raise PaError(st, "pa_tree_accept_fp8" if dt is _U8 else "pa_tree_accept")
 

@@ -860,6 +860,39 @@ pa_status pa_tree_accept_fp8(void *kv_cache, int num_blocks, int block_size, int
                             block_tables, max_blocks_per_seq, seq_lens, new_seq_lens, stream);
 }
 
+pa_status pa_tree_attention_packed(const pa_tree_attention_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    return tree_attention_impl(a->out, a->q, a->cu_tree_lens, a->parents, a->num_seqs,
+                               a->total_nodes, a->max_tree_len, a->kv_cache, a->num_blocks,
+                               a->block_size, a->num_heads, a->num_kv_heads, a->head_size,
+                               a->block_tables, a->max_blocks_per_seq, a->seq_lens,
+                               a->max_seq_len, a->scale, a->kv8 != 0, a->k_scale, a->v_scale,
+                               a->workspace, a->workspace_bytes, a->stream);
+}
+
+pa_status pa_tree_verify_packed(const pa_tree_verify_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    return pa_tree_verify(a->accepted, a->num_accepted, a->next_tokens, a->target_probs,
+                          a->target_row_stride, a->draft_probs, a->draft_row_stride, a->tokens,
+                          a->cu_tree_lens, a->parents, a->num_seqs, a->total_nodes,
+                          a->max_tree_len, a->vocab_size, a->accept_u, a->sample_u, a->stream);
+}
+
+pa_status pa_tree_accept_packed(const pa_tree_accept_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    return tree_accept_impl(a->kv_cache, a->num_blocks, a->block_size, a->num_kv_heads,
+                            a->head_size, a->kv8 ? 1 : 2, a->accepted, a->num_accepted,
+                            a->cu_tree_lens, a->num_seqs, a->max_tree_len, a->block_tables,
+                            a->max_blocks_per_seq, a->seq_lens, a->new_seq_lens, a->stream);
+}
+
+size_t pa_tree_args_bytes(int call) {
+    return call == 0   ? sizeof(pa_tree_attention_args)
+           : call == 1 ? sizeof(pa_tree_verify_args)
+           : call == 2 ? sizeof(pa_tree_accept_args)
+                       : 0;
+}
+
 pa_status pa_error_check(pa_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return PA_ERR_CUDA;

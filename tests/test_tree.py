@@ -4,6 +4,7 @@ write), and the calls refuse bad arguments before anything is enqueued."""
 
 from __future__ import annotations
 
+import ctypes
 import os
 
 import numpy as np
@@ -200,3 +201,68 @@ def test_tree_bindings_name_the_tensor_at_fault(lib):
     with pytest.raises(ValueError, match="kv_scales"):
         binding.pa_tree_attention(q, q, d.cu, d.parents, 3, pool.to(torch.uint8), bt, sl, 8, 0.1,
                                   ws)
+
+
+def _packed(lib, call, values):
+    """The packed call of these members (pointers None or int)."""
+    buf = ctypes.create_string_buffer(lib.pa_tree_args_bytes(call))
+    binding.TREE_ARGS[call].pack_into(buf, 0, *(0 if v is None else v for v in values))
+    f = (lib.pa_tree_attention_packed, lib.pa_tree_verify_packed, lib.pa_tree_accept_packed)[call]
+    return f(ctypes.addressof(buf))
+
+
+def test_packed_structs_have_the_headers_layout(lib):
+    assert [lib.pa_tree_args_bytes(i) for i in (0, 1, 2, 3, -1)] == [136, 120, 96, 0, 0]
+    for f in (lib.pa_tree_attention_packed, lib.pa_tree_verify_packed, lib.pa_tree_accept_packed):
+        assert f(None) == 1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(kv=None), dict(out=None), dict(q=FAKE + 8), dict(cu=None), dict(parents=None),
+    dict(bt=None), dict(seq_lens=None), dict(num_seqs=-1), dict(total=-1), dict(max_tree=0),
+    dict(max_tree=65), dict(max_blocks=0), dict(max_seq=65), dict(scale=float("nan")),
+    dict(num_kv_heads=5), dict(num_heads=64, num_kv_heads=4), dict(head_size=96),
+    dict(block_size=12), dict(ws=None), dict(ws_bytes=1), dict(num_seqs=0), dict(total=0),
+    dict(num_blocks=0)])
+def test_packed_tree_attention_decides_as_the_plain_call(lib, kw):
+    """Each case is decided by another member."""
+    a = dict(zip(("out", "q", "cu", "parents", "num_seqs", "total", "max_tree", "kv", "num_blocks",
+                  "block_size", "num_heads", "num_kv_heads", "head_size", "bt", "max_blocks",
+                  "seq_lens", "max_seq", "scale", "ws", "ws_bytes", "stream"), _attn(**kw)))
+    names = ("out q cu parents kv bt seq_lens ws ws_bytes stream num_seqs total max_tree "
+             "num_blocks block_size num_heads num_kv_heads head_size max_blocks max_seq").split()
+    members = [a[n] for n in names]
+    assert _packed(lib, 0, members + [0, a["scale"], 1.0, 1.0]) == lib.pa_tree_attention(*_attn(**kw))
+    b = _attn(**kw)
+    assert _packed(lib, 0, members + [1, a["scale"], 0.5, 0.25]) == \
+        lib.pa_tree_attention_fp8(*b[:18], 0.5, 0.25, *b[18:])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(num_seqs=0), dict(accepted=None), dict(num=None), dict(next=None), dict(target=FAKE + 2),
+    dict(draft=FAKE + 2), dict(ts=99), dict(ds=99), dict(tokens=None), dict(cu=None),
+    dict(parents=None), dict(accept_u=None), dict(sample_u=None), dict(max_tree=65),
+    dict(vocab=0), dict(total=-1), dict(num_seqs=-1)])
+def test_packed_tree_verify_decides_as_the_plain_call(lib, kw):
+    a = dict(zip(("accepted num next target ts draft ds tokens cu parents num_seqs total max_tree "
+                  "vocab accept_u sample_u stream").split(), _verify(**kw)))
+    names = ("accepted num next target draft tokens cu parents accept_u sample_u stream ts ds "
+             "num_seqs total max_tree vocab").split()
+    assert _packed(lib, 1, [a[n] for n in names]) == lib.pa_tree_verify(*_verify(**kw))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(num_seqs=0), dict(kv=FAKE + 8), dict(accepted=None), dict(num=None), dict(cu=None),
+    dict(bt=None), dict(seq_lens=None), dict(new=FAKE), dict(num_seqs=-1), dict(max_blocks=0),
+    dict(max_tree=65), dict(head_size=32), dict(block_size=12), dict(num_kv_heads=0),
+    dict(num_blocks=0)])
+def test_packed_tree_accept_decides_as_the_plain_call(lib, kw):
+    a = dict(kv=FAKE, num_blocks=10, block_size=16, num_kv_heads=8, head_size=128, accepted=FAKE,
+             num=FAKE, cu=FAKE, num_seqs=3, max_tree=8, bt=FAKE, max_blocks=4, seq_lens=FAKE,
+             new=None, stream=None)
+    a.update(kw)
+    names = ("kv accepted num cu bt seq_lens new stream num_blocks block_size num_kv_heads "
+             "head_size num_seqs max_tree max_blocks").split()
+    for kv8 in (0, 1):
+        want = (lib.pa_tree_accept_fp8 if kv8 else lib.pa_tree_accept)(*a.values())
+        assert _packed(lib, 2, [a[n] for n in names] + [kv8]) == want
