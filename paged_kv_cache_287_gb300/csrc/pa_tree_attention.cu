@@ -46,11 +46,12 @@
 // Measured (GB300, HBM copy 6689 GB/s, whole call): 32 sequences of 512-4096 tokens with
 // 12-16 nodes, 32 query and 8 KV heads of 128: 60 us, 5.2 TB/s; 8 sequences of 1024-131072
 // tokens with 7-23 nodes: 142 us, 6.1 TB/s; 16 sequences of 1024-8192 tokens, 33-64 nodes,
-// 64 and 8 heads: 131 us, 910 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool,
+// 64 and 8 heads: 128 us, 930 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool,
 // 64 sequences, chains of 3-8: 78 us, 3.9 TB/s.  Per call some 5 us until the first products,
-// 4 to 6 us for the merge.  In the wide case and the FP8 one shared memory bounds a tile: the
-// products read the query tile anew for every 64 keys, some 100 KB a tile and CTA with V's
-// conversion, 1500 cycles for a pair of CTAs at 128 bytes a cycle (measured 1400 to 1800).
+// 4 to 8 us for the merge.  The wide case keeps the tensor pipe 51 % busy, the FP8 one 41 %
+// with DRAM at 3.9 TB/s: the chain of a tile, scores, softmax, output, scores over the same
+// buffer, takes 1400 to 1800 cycles per tile and CTA, and the two CTAs of an SM do not fill
+// each other's gaps entirely.
 #include <algorithm>
 #include <cmath>
 
@@ -1279,24 +1280,32 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
 // Merge the pieces of segments that were split across CTAs: a lane per row, a warp per
 // D / 16 dims, joined by log-sum-exp in one pass, several pieces' loads in flight.
 //
-// With many segments a block (w, 32 rows) looks whether CTA w's range starts inside a segment
-// whose first piece is that of the team before.  Few segments (at most a quarter of the CTAs)
+// With many segments block w looks whether CTA w's range starts inside a segment whose first
+// piece is that of the team before, and takes its rows 32 at a time.  Few segments (at most a quarter of the CTAs)
 // are split into many pieces: a block per segment, 32 rows and quarter of the dims, whose warps
 // also share the pieces out among four groups, joined through shared memory (8 sequences of
 // 1024 .. 131072 tokens, up to some 80 pieces: 143.6 -> 142.4 us for the whole call).
-constexpr int kMergeWarps = 16;
+constexpr int kMergeWarps = 16, kMaxCtas = 512;
 
 template <int D, bool kFew>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeAttnArgs a) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 2) tree_merge_kernel(const TreeAttnArgs a) {
     constexpr int kUnits = D / 4 / kMergeWarps;  // float4 of a row that a thread joins
     constexpr int kSplit = kFew ? 4 : 1;         // groups of warps that share the pieces
     __shared__ int s_first, s_count;
     __shared__ float s_part[kFew ? kMergeWarps : 1][4 * kUnits + 2][32];
+    __shared__ int4 s_start[kMaxCtas];
     pdl_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row0 = blockIdx.y * 32;
+    // Every range's start at once: looked up one after the other they cost a memory latency
+    // each.
+    for (int i = threadIdx.x; i < a.ctas; i += blockDim.x) s_start[i] = a.starts[i];
+    if (kFew && threadIdx.x == 0) {
+        s_first = a.ctas;
+        s_count = 0;
+    }
+    __syncthreads();
     auto start_of = [&](int i) {
-        return i >= 0 && i < a.ctas ? a.starts[i] : make_int4(-1, 0, 0, 0);
+        return i >= 0 && i < a.ctas ? s_start[i] : make_int4(-1, 0, 0, 0);
     };
     auto step_of = [&](int key) {  // a team's CTAs
         return a.row_groups == 1 ? 1 : max(1, groups_of(a, (key >> 8) & 255));
@@ -1306,13 +1315,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     if constexpr (kFew) {
         const int rg = blockIdx.x % a.row_groups, sh = blockIdx.x / a.row_groups;
         const int seq = sh / a.num_kv_heads, head = sh - seq * a.num_kv_heads;
-        if (threadIdx.x == 0) {
-            s_first = a.ctas;
-            s_count = 0;
-        }
-        __syncthreads();
         for (int i = threadIdx.x; i < a.ctas; i += blockDim.x) {
-            const int4 e = a.starts[i];
+            const int4 e = s_start[i];
             if (e.x == seq && (e.y & 255) == head && e.y >> 16 == rg && e.z > 0) {
                 atomicMin(&s_first, i);
                 atomicAdd(&s_count, 1);
@@ -1350,105 +1354,106 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     }
     const int nodes = (key >> 8) & 255, head = key & 255, rg = key >> 16;
     const int rows = min(a.q_tile, nodes - rg * a.q_tile) * a.group;
-    if (row0 >= rows) return;
-    const int row = min(row0 + lane, rows - 1);
     const int unit0 = (kFew ? blockIdx.z * (kMergeWarps / kSplit) + warp % (kMergeWarps / kSplit)
                             : warp) * kUnits;
     const int first = kFew ? warp / (kMergeWarps / kSplit) : 0;
     const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
     const float4 *acc = reinterpret_cast<const float4 *>(a.part_acc);
-    float M = -INFINITY, den = 0.f;
-    float4 num[kUnits];
+    for (int row0 = 32 * blockIdx.y; row0 < rows; row0 += 32 * gridDim.y) {
+        const int row = min(row0 + lane, rows - 1);
+        float M = -INFINITY, den = 0.f;
+        float4 num[kUnits];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) num[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 4;
-    for (int k0 = first; k0 < n; k0 += kBatch * kSplit) {
-        auto at = [&](int k) { return k0 + k * kSplit; };  // the batch's k-th piece
-        float2 e[kBatch];
-        float4 v[kBatch][kUnits];
+        for (int i = 0; i < kUnits; ++i) num[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 4;
+        for (int k0 = first; k0 < n; k0 += kBatch * kSplit) {
+            auto at = [&](int k) { return k0 + k * kSplit; };  // the batch's k-th piece
+            float2 e[kBatch];
+            float4 v[kBatch][kUnits];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            if (at(k) < n) {
-                const size_t cta = (size_t)(w + (at(k) - 1) * step);
-                const size_t rec = cta * 2 + (at(k) == 0 && !prev_same ? 1 : 0);
-                e[k] = ml[rec * a.part_rows + row];
+            for (int k = 0; k < kBatch; ++k) {
+                if (at(k) < n) {
+                    const size_t cta = (size_t)(w + (at(k) - 1) * step);
+                    const size_t rec = cta * 2 + (at(k) == 0 && !prev_same ? 1 : 0);
+                    e[k] = ml[rec * a.part_rows + row];
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i)
-                    v[k][i] = acc[(rec * (D / 4) + unit0 + i) * a.part_rows + row];
+                    for (int i = 0; i < kUnits; ++i)
+                        v[k][i] = acc[(rec * (D / 4) + unit0 + i) * a.part_rows + row];
+                }
             }
-        }
-        // A row that sees no key of a piece has m = -inf and nothing in it.
-        float mn = M;
+            // A row that sees no key of a piece has m = -inf and nothing in it.
+            float mn = M;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (at(k) < n) mn = fmaxf(mn, e[k].x);
-        const float ref = mn == -INFINITY ? 0.f : mn, c = fast_exp2(M - ref);
-        M = mn;
-        den *= c;
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            num[i].x *= c;
-            num[i].y *= c;
-            num[i].z *= c;
-            num[i].w *= c;
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            if (at(k) >= n) break;
-            const float g = fast_exp2(e[k].x - ref);
-            den += g * e[k].y;
-#pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-                num[i].x += g * v[k][i].x;
-                num[i].y += g * v[k][i].y;
-                num[i].z += g * v[k][i].z;
-                num[i].w += g * v[k][i].w;
-            }
-        }
-    }
-    if constexpr (kFew) {
-        float *own = &s_part[warp][0][lane];
-        own[0] = M;
-        own[32] = den;
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            own[32 * (2 + 4 * i)] = num[i].x;
-            own[32 * (3 + 4 * i)] = num[i].y;
-            own[32 * (4 + 4 * i)] = num[i].z;
-            own[32 * (5 + 4 * i)] = num[i].w;
-        }
-        __syncthreads();
-        if (first != 0) return;
-#pragma unroll
-        for (int p = 1; p < kSplit; ++p) {
-            const float *o = &s_part[warp + p * (kMergeWarps / kSplit)][0][lane];
-            const float mn = fmaxf(M, o[0]), ref = mn == -INFINITY ? 0.f : mn;
-            const float c = fast_exp2(M - ref), g = fast_exp2(o[0] - ref);
+            for (int k = 0; k < kBatch; ++k)
+                if (at(k) < n) mn = fmaxf(mn, e[k].x);
+            const float ref = mn == -INFINITY ? 0.f : mn, c = fast_exp2(M - ref);
             M = mn;
-            den = den * c + g * o[32];
+            den *= c;
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) {
-                num[i].x = num[i].x * c + g * o[32 * (2 + 4 * i)];
-                num[i].y = num[i].y * c + g * o[32 * (3 + 4 * i)];
-                num[i].z = num[i].z * c + g * o[32 * (4 + 4 * i)];
-                num[i].w = num[i].w * c + g * o[32 * (5 + 4 * i)];
+                num[i].x *= c;
+                num[i].y *= c;
+                num[i].z *= c;
+                num[i].w *= c;
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (at(k) >= n) break;
+                const float g = fast_exp2(e[k].x - ref);
+                den += g * e[k].y;
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    num[i].x += g * v[k][i].x;
+                    num[i].y += g * v[k][i].y;
+                    num[i].z += g * v[k][i].z;
+                    num[i].w += g * v[k][i].w;
+                }
             }
         }
-    }
-    if (row0 + lane >= rows) return;
-    const float inv = 1.f / den;
-    const int node = node0 + rg * a.q_tile + row / a.group;
-    uint2 *dst = reinterpret_cast<uint2 *>(
-        a.out + ((size_t)node * a.num_heads + (size_t)head * a.group + row % a.group) * D) + unit0;
-    uint2 o[kUnits];
+        if constexpr (kFew) {
+            float *own = &s_part[warp][0][lane];
+            own[0] = M;
+            own[32] = den;
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-        o[i] = make_uint2(pack_bf16(num[i].x * inv, num[i].y * inv),
-                          pack_bf16(num[i].z * inv, num[i].w * inv));
-    if constexpr (kUnits == 2)
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
-    else
-        dst[0] = o[0];
+            for (int i = 0; i < kUnits; ++i) {
+                own[32 * (2 + 4 * i)] = num[i].x;
+                own[32 * (3 + 4 * i)] = num[i].y;
+                own[32 * (4 + 4 * i)] = num[i].z;
+                own[32 * (5 + 4 * i)] = num[i].w;
+            }
+            __syncthreads();
+            if (first != 0) continue;
+#pragma unroll
+            for (int p = 1; p < kSplit; ++p) {
+                const float *o = &s_part[warp + p * (kMergeWarps / kSplit)][0][lane];
+                const float mn = fmaxf(M, o[0]), ref = mn == -INFINITY ? 0.f : mn;
+                const float c = fast_exp2(M - ref), g = fast_exp2(o[0] - ref);
+                M = mn;
+                den = den * c + g * o[32];
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    num[i].x = num[i].x * c + g * o[32 * (2 + 4 * i)];
+                    num[i].y = num[i].y * c + g * o[32 * (3 + 4 * i)];
+                    num[i].z = num[i].z * c + g * o[32 * (4 + 4 * i)];
+                    num[i].w = num[i].w * c + g * o[32 * (5 + 4 * i)];
+                }
+            }
+        }
+        if (row0 + lane >= rows) continue;
+        const float inv = 1.f / den;
+        const int node = node0 + rg * a.q_tile + row / a.group;
+        uint2 *dst = reinterpret_cast<uint2 *>(
+            a.out + ((size_t)node * a.num_heads + (size_t)head * a.group + row % a.group) * D) + unit0;
+        uint2 o[kUnits];
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+            o[i] = make_uint2(pack_bf16(num[i].x * inv, num[i].y * inv),
+                              pack_bf16(num[i].z * inv, num[i].w * inv));
+        if constexpr (kUnits == 2)
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0].x, o[0].y, o[1].x, o[1].y);
+        else
+            dst[0] = o[0];
+    }
 }
 
 // Launch shape for trees of at most max_tree nodes.
@@ -1461,7 +1466,8 @@ Shape shape_of(int max_tree, int group, int head_size, int sm_count) {
     Shape s;
     s.q_tile = kRows / group;
     s.row_groups = (max_tree + s.q_tile - 1) / s.q_tile;
-    s.ctas = std::max(kGroups * (kGroups + 1) / 2, 2 * sm_count);  // a team of every class
+    // A team of every list at least, two CTAs per SM.
+    s.ctas = std::min(kMaxCtas, std::max(kGroups * (kGroups + 1) / 2, 2 * sm_count));
     s.part_rows = std::min(s.q_tile, max_tree) * group;
     const size_t recs = (size_t)s.ctas * 2 * s.part_rows;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -1485,8 +1491,8 @@ cudaError_t launch_rows(const CUtensorMap &map, const CUtensorMap &q_map, const 
     if (4 * segments <= a.ctas)
         return launch_pdl(tree_merge_kernel<D, true>, dim3((unsigned)segments, rows, 4),
                           kMergeWarps * 32, 0, 1, stream, a);
-    return launch_pdl(tree_merge_kernel<D, false>, dim3((unsigned)a.ctas, rows),
-                      kMergeWarps * 32, 0, 1, stream, a);
+    return launch_pdl(tree_merge_kernel<D, false>, dim3((unsigned)a.ctas), kMergeWarps * 32, 0, 1,
+                      stream, a);
 }
 
 template <int D, bool KV8>
