@@ -453,7 +453,7 @@ size_t pa_tree_attention_workspace_bytes(int num_seqs, int max_tree_len, int num
  * K[t][h/G]) V[t][h/G] over those tokens t.  Nodes that are no ancestors of a
  * node have no part in its result, whatever their K/V hold.  A tree of one node
  * is pa_decode, a chain is pa_prefill_chunk of its rows.
- *   out, q        [total_nodes][num_heads][head_size] bf16
+ *   out, q        [total_nodes][num_heads][head_size] bf16, must not overlap
  *   max_seq_len   host-side upper bound of seq_lens (a longer sequence is skipped
  *                 and flagged PA_ERR_OOB)
  *   workspace     device scratch of >= pa_tree_attention_workspace_bytes(...)

@@ -178,6 +178,29 @@ def test_a_visible_infinity_in_v_reaches_the_rows_that_see_it():
         assert sees or torch.isfinite(got[i]).all()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [9, 64])
+def test_queries_of_zeros_tiny_huge_and_nan_rows(fp8, T):
+    """Each query row has its own scale over an FP8 pool; a NaN or an infinity stays in
+    its row (and head)."""
+    c = Case([100, 700], [T, 5], 8, 2, 128, 16, seed=25, fp8=fp8, scale=1e-3)
+    q = c.b.q
+    q[1, 0] = 0.0
+    q[2, 1] = 1e-39  # a subnormal: scores far below one
+    q[3, 2] *= 1000.0
+    q[4, 3, ::2] *= 2.0 ** -12  # elements far below the row's largest
+    want, tol = c.reference()
+    _tree.assert_attention(c.run(), want, tol)
+    clean = q.clone()
+    q[0, 4, 5], q[T, 7, 127], q[T + 1, 0, 0] = float("nan"), float("inf"), float("-inf")
+    out = c.run()
+    hit = torch.zeros(out.shape[:2], dtype=torch.bool)
+    hit[0, 4] = hit[T, 7] = hit[T + 1, 0] = True
+    assert out.cpu()[hit].isnan().all()
+    q.copy_(clean)
+    assert np.array_equal(bits(out.cpu()[~hit]), bits(c.run().cpu()[~hit]))
+
+
 def test_an_infinity_or_nan_in_the_context_reaches_every_row():
     c = Case([200], [6], 2, 1, 64, 16, seed=6)
     blk, off = int(c.b.block_tables[0, 3]), 5
