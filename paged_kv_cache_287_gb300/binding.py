@@ -699,6 +699,15 @@ def pa_tree_verify(accepted: torch.Tensor, num_accepted: torch.Tensor, next_toke
               and sample_u.get_device() == dev and sample_u.is_contiguous()
               and target_probs.get_device() == dev
               and (draft_probs is None or draft_probs.get_device() == dev))
+        # Rows of probabilities may lie apart: the rest of _prob_rows' checks, at once.
+        ts, one = target_probs.stride()
+        plain = target_probs.dtype is _F32 and one == 1 and ts >= V
+        dp = ds = 0
+        if draft_probs is not None:
+            ds, one = draft_probs.stride()
+            plain = (plain and draft_probs.dtype is _F32 and one == 1 and ds >= V
+                     and draft_probs.shape == (rows, V))
+            dp = draft_probs.data_ptr()
     except (AttributeError, TypeError, ValueError):
         ok = False
     if not ok:
@@ -716,11 +725,10 @@ def pa_tree_verify(accepted: torch.Tensor, num_accepted: torch.Tensor, next_toke
         _same_device(accepted, num_accepted, next_tokens, tokens, cu_tree_lens, parents,
                      accept_u, sample_u, target_probs, draft_probs)
         raise ValueError("inconsistent tree verification shapes")
-    ts = _prob_rows(target_probs, "target_probs", rows, V)
-    dp = ds = 0
-    if draft_probs is not None:
-        ds = _prob_rows(draft_probs, "draft_probs", rows, V)
-        dp = draft_probs.data_ptr()
+    if not plain:
+        ts = _prob_rows(target_probs, "target_probs", rows, V)
+        if draft_probs is not None:
+            ds = _prob_rows(draft_probs, "draft_probs", rows, V)
     L = _lib if _lib is not None else lib()
     buf, addr = _tree_args()
     TREE_ARGS[1].pack_into(

@@ -523,6 +523,31 @@ def test_verify_flags_bad_data():
             binding.pa_error_check()
 
 
+def test_verify_takes_apart_rows_and_refuses_other_layouts():
+    d = _tree.random_drafts(31, [4, 1], 40, True)
+    args = [x.to(DEV) for x in (d.tokens, d.cu, d.parents, d.accept_u, d.sample_u)]
+    acc = torch.empty(2, 4, dtype=I32, device=DEV)
+    num, nxt = (torch.empty(2, dtype=I32, device=DEV) for _ in range(2))
+    p, q = d.target.to(DEV), d.draft.to(DEV)
+
+    def call(p, q):
+        binding.pa_tree_verify(acc, num, nxt, p, q, *args)
+        return nxt.tolist()
+    wide = torch.zeros(5, 97, device=DEV)
+    wide[:, 20:60] = q
+    assert call(p, wide[:, 20:60]) == call(p, q) == d.reference[1]
+    one = _tree.random_drafts(32, [1], 40, True)  # a single row's stride says nothing
+    binding.pa_tree_verify(acc[:1], num[:1], nxt[:1], one.target.to(DEV).expand(1, 40), None,
+                           *(x.to(DEV) for x in (one.tokens, one.cu, one.parents, one.accept_u,
+                                                 one.sample_u)))
+    assert nxt.tolist()[0] == one.reference[1][0]
+    for bad in (q[:1].expand(5, 40), q.t().contiguous().t(), q.double(), q[:, :39], q[:4],
+                q.cpu(), q.flatten(), q.half()):
+        for pair in ((p, bad), (bad, q)):
+            with pytest.raises(ValueError):
+                call(*pair)
+
+
 def test_verify_replays_in_a_graph_and_on_a_side_stream():
     T = [7, 30, 2]
     d = _tree.random_drafts(21, T, 5000, True)
