@@ -46,7 +46,7 @@
 // Measured (GB300, HBM copy 6689 GB/s, whole call): 32 sequences of 512-4096 tokens with
 // 12-16 nodes, 32 query and 8 KV heads of 128: 60 us, 5.2 TB/s; 8 sequences of 1024-131072
 // tokens with 7-23 nodes: 142 us, 6.1 TB/s; 16 sequences of 1024-8192 tokens, 33-64 nodes,
-// 64 and 8 heads: 128 us, 930 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool,
+// 64 and 8 heads: 128-132 us, 910 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool,
 // 64 sequences, chains of 3-8: 78 us, 3.9 TB/s.  Per call some 5 us until the first products,
 // 4 to 8 us for the merge.  The wide case keeps the tensor pipe 51 % busy, the FP8 one 41 %
 // with DRAM at 3.9 TB/s: the chain of a tile, scores, softmax, output, scores over the same
@@ -1281,10 +1281,11 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
 // D / 16 dims, joined by log-sum-exp in one pass, several pieces' loads in flight.
 //
 // With many segments block w looks whether CTA w's range starts inside a segment whose first
-// piece is that of the team before, and takes its rows 32 at a time.  Few segments (at most a quarter of the CTAs)
-// are split into many pieces: a block per segment, 32 rows and quarter of the dims, whose warps
-// also share the pieces out among four groups, joined through shared memory (8 sequences of
-// 1024 .. 131072 tokens, up to some 80 pieces: 143.6 -> 142.4 us for the whole call).
+// piece is that of the team before, and takes its rows 32 at a time.  Few segments (at most a
+// quarter of the CTAs) are split into many pieces: a block per segment, 32 rows and quarter of
+// the dims, whose warps also share the pieces out among four groups, joined through shared
+// memory (8 sequences of 1024 .. 131072 tokens, up to some 80 pieces: 143.6 -> 142.4 us for the
+// whole call).
 constexpr int kMergeWarps = 16, kMaxCtas = 512;
 
 template <int D, bool kFew>
@@ -1442,8 +1443,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) tree_merge_kernel(const T
         if (row0 + lane >= rows) continue;
         const float inv = 1.f / den;
         const int node = node0 + rg * a.q_tile + row / a.group;
-        uint2 *dst = reinterpret_cast<uint2 *>(
-            a.out + ((size_t)node * a.num_heads + (size_t)head * a.group + row % a.group) * D) + unit0;
+        const size_t orow = (size_t)node * a.num_heads + (size_t)head * a.group + row % a.group;
+        uint2 *dst = reinterpret_cast<uint2 *>(a.out + orow * D) + unit0;
         uint2 o[kUnits];
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)

@@ -27,8 +27,8 @@
 // sums took 1433 us where the batch's bytes take 40 (256 chains, 131072 tokens), and
 // 64-bit sums across the 16 warps of each CTA alone some 2 us a pass.
 //
-// Measured (GB300): those 256 chains 56 us, 4.8 TB/s; 48 trees of 9-31 nodes with sibling
-// rounds, 50021 tokens, 28 us; 64 trees of 33-64 proposed nodes, 131072 tokens, 23 us; one
+// Measured (GB300): those 256 chains 52 us, 5.2 TB/s; 48 trees of 9-31 nodes with sibling
+// rounds, 50021 tokens, 24 us; 64 trees of 33-64 proposed nodes, 131072 tokens, 18 us; one
 // chain of 6, 32000 tokens, 7 us (13 000 cycles: gathers 2000, walk 1200, pass 3000, cluster
 // sum 2000, draw 4500).
 #include <algorithm>
@@ -44,8 +44,9 @@ constexpr int kNodes = 64;
 constexpr int kWarps = 16;
 constexpr int kMaxCluster = 8;
 // What a thread loads at once: groups of four tokens of p and q (twice as many of p alone;
-// 256 chains 56.0 -> 53.5 us, 64 wide trees 22.8 -> 20.6, against eight tokens one by one;
-// more groups spill), or of a short slice kept in shared memory tokens one by one.
+// 256 chains 56.0 -> 53.5 us, 64 wide trees 22.8 -> 20.6, against eight tokens one by one),
+// or of a short slice kept in shared memory tokens one by one.  (A kernel per kind of
+// probabilities keeps all that in registers: 51.9 and 18.3 us, 48 trees 28 -> 24.)
 constexpr int kU = 2, kS = 8;
 
 struct VerifyArgs {
@@ -702,11 +703,10 @@ cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)(t.num_seqs * c));
-    if (kept)
-        return launch_pdl(tree_verify_kernel<true, true>, grid, kWarps * 32, smem, c, stream, a);
-    return draft ? launch_pdl(tree_verify_kernel<true, false>, grid, kWarps * 32, smem, c, stream, a)
-                 : launch_pdl(tree_verify_kernel<false, false>, grid, kWarps * 32, smem, c, stream,
-                              a);
+    auto *kern = kept    ? tree_verify_kernel<true, true>
+                 : draft ? tree_verify_kernel<true, false>
+                         : tree_verify_kernel<false, false>;
+    return launch_pdl(kern, grid, kWarps * 32, smem, c, stream, a);
 }
 
 }  // namespace pa

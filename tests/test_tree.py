@@ -232,8 +232,8 @@ def test_packed_tree_attention_decides_as_the_plain_call(lib, kw):
     names = ("out q cu parents kv bt seq_lens ws ws_bytes stream num_seqs total max_tree "
              "num_blocks block_size num_heads num_kv_heads head_size max_blocks max_seq").split()
     members = [a[n] for n in names]
-    assert _packed(lib, 0, members + [0, a["scale"], 1.0, 1.0]) == lib.pa_tree_attention(*_attn(**kw))
     b = _attn(**kw)
+    assert _packed(lib, 0, members + [0, a["scale"], 1.0, 1.0]) == lib.pa_tree_attention(*b)
     assert _packed(lib, 0, members + [1, a["scale"], 0.5, 0.25]) == \
         lib.pa_tree_attention_fp8(*b[:18], 0.5, 0.25, *b[18:])
 
