@@ -185,9 +185,15 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, int rank) {
     return r;
 }
 
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
 }
 
 // kDraft: with draft probabilities; kKept: r and q of the slice are kept in shared memory.
@@ -232,6 +238,11 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
         }
         return;
     }
+    // A CTA's shared memory may be written by its peers once it has started: every CTA says so
+    // here, and waits for the others before its first store to them (a pass later, so that the
+    // gathers and the pass cover the wait).
+    if (C > 1) cluster_arrive();
+    bool peers = C == 1;  // the others have started
     const int n = span.n, V = a.vocab;
     constexpr bool with = kDraft;
     if (tid < kNodes) {
@@ -477,6 +488,8 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
             const Pair t = warp_sum(acc[0]);
             if (lane == 0) s_tot[warp] = t;
             __syncthreads();
+            if (!peers) cluster_wait();
+            peers = true;
             if (warp == 0) {
                 // This CTA's sum to every CTA of the cluster.
                 const Pair sum =

@@ -1,0 +1,75 @@
+"""Draft trees on the GPU in the regimes that large batches and vocabularies bring:
+clusters of CTAs per sequence, ranges of many tiles, many segments per range.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_287_gb300 import binding
+from tests import _tree
+from tests.test_gpu_tree import Case, run_verify
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+I32 = torch.int32
+
+
+@pytest.fixture(autouse=True)
+def _clean_errors():
+    binding.pa_error_check()
+    yield
+    binding.pa_error_check()
+
+
+# ---------------------------------------------------------------- verification in clusters
+@pytest.mark.parametrize("vocab", [5000, 16384, 40000])  # 2, 8 and 8 CTAs per sequence
+@pytest.mark.parametrize("with_draft", [True, False])
+def test_verify_in_clusters_beside_other_work(vocab, with_draft):
+    """Clusters that start while other kernels hold parts of the GPU: every call gives the
+    walk's result."""
+    d = _tree.random_drafts(vocab, [20, 0, 3, 64, 1], vocab, with_draft, "star")
+    args = [x if x is None else x.to(DEV)
+            for x in (d.target, d.draft, d.tokens, d.cu, d.parents, d.accept_u, d.sample_u)]
+    paths, nexts = d.reference
+    a = torch.randn(1500, 1500, device=DEV)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty(5, 64, dtype=I32, device=DEV), torch.empty(5, dtype=I32, device=DEV),
+             torch.empty(5, dtype=I32, device=DEV)] for _ in range(40)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i, out in enumerate(outs):
+        if i % 3 == 0:
+            with torch.cuda.stream(streams[1 - i % 2]):
+                a = (a @ a).clamp_(-1, 1)
+        with torch.cuda.stream(streams[i % 2]):
+            binding.pa_tree_verify(*out, *args)
+    torch.cuda.synchronize()
+    for acc, num, nxt in outs:
+        assert nxt.tolist() == nexts
+        assert [acc[i, :n].tolist() for i, n in enumerate(num.tolist())] == paths
+
+
+@pytest.mark.parametrize("vocab", [16384, 50021])
+def test_verify_falls_back_in_clusters(vocab):
+    """Nothing left to draw from, with eight CTAs per sequence: the lowest token of the
+    target's largest probability, wherever its CTA's slice; and a draw whose goal no running
+    sum exceeds: the last token with weight."""
+    for lo, hi in ((3, vocab - 2), (vocab // 2 - 1, vocab // 2 + 1), (vocab - 9, vocab - 3)):
+        p = torch.zeros(4, vocab)
+        p[:, lo], p[:, hi] = 0.5, 0.5
+        cu = torch.tensor([0, 4], dtype=I32)
+        star = torch.tensor([-1, 0, 0, 0], dtype=I32)
+        tokens = torch.tensor([0, hi, hi, lo], dtype=I32)
+        d = _tree.Drafts(p, p.clone(), tokens, star, cu, torch.ones(4), torch.tensor([0.7]), [4])
+        assert run_verify(d) == d.reference == ([[0]], [lo])
+        d = _tree.Drafts(p, None, torch.tensor([0, hi, lo, lo], dtype=I32), star, cu,
+                         torch.ones(4), torch.tensor([0.7]), [4])
+        assert run_verify(d) == d.reference == ([[0]], [lo])
+        one = torch.tensor([0, 1], dtype=I32)
+        d = _tree.Drafts(p[:1], None, tokens[:1], star[:1], one, torch.zeros(1),
+                         torch.tensor([1.0]), [1])
+        assert run_verify(d) == d.reference == ([[0]], [hi])
