@@ -812,7 +812,10 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             }
             for (int r = max(r0, r1) + lane / kC; r < kKeys; r += 32 / kC)
                 *at(r) = make_uint4(0, 0, 0, 0);
+            // Every lane's stores, before lane 0 issues the product that reads them (a vote
+            // orders no memory).
             fence_proxy_async_smem();
+            __syncwarp();
             return bad;
         };
         // Up to `last` tiles' scores, of segments up to max_seg, one thread.  It also fetches the

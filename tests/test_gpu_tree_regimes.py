@@ -25,6 +25,36 @@ def _clean_errors():
     binding.pa_error_check()
 
 
+# ---------------------------------------------------------------- attention
+@pytest.mark.parametrize("T,heads", [(5, 4), (64, 16)])
+def test_cleared_values_are_handed_over_on_every_call(T, heads):
+    """V of unseen nodes and of what lies behind the sequences holds NaN and infinities, in
+    tiles that are cleared by 32 lanes and read by a product that one issues: fifty calls,
+    the same finite result."""
+    c = Case([70, 500, 129, 60], [T, T, 1, T], heads, 2, 128, 16, seed=33, shape="star")
+    b = c.b
+    ends = b.seq_lens.tolist()
+    want, tol = c.reference()
+    for s, n in enumerate(ends):  # behind the sequence, to the end of its block
+        blk = int(b.block_tables[s, (n - 1) // 16])
+        if n % 16:
+            c.pool[blk, :, :, n % 16:] = float("nan")
+    rows = []
+    for s, lo in enumerate(b.cu_q_lens.tolist()[:-1]):
+        if c.T[s] > 2:  # node 2 is seen by itself alone
+            slot = int(b.slot_mapping[lo + 2])
+            c.pool[slot // 16, 1, :, slot % 16, ::3] = float("inf")
+            rows.append(lo + 2)
+    keep = [r for r in range(b.q.shape[0]) if r not in rows]
+    first, ws = c.run(), c.workspace()
+    _tree.assert_attention(first[keep], want[keep], tol[keep])
+    out = torch.empty_like(first)
+    for i in range(50):
+        out.fill_(float("nan"))
+        c.run(out=out, ws=ws)
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16)), i
+
+
 # ---------------------------------------------------------------- verification in clusters
 @pytest.mark.parametrize("vocab", [5000, 16384, 40000])  # 2, 8 and 8 CTAs per sequence
 @pytest.mark.parametrize("with_draft", [True, False])

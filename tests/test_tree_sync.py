@@ -9,8 +9,6 @@ from __future__ import annotations
 import os
 import re
 
-import pytest
-
 from paged_kv_cache_287_gb300 import build
 
 
@@ -41,3 +39,13 @@ def test_a_peers_shared_memory_is_written_once_its_cta_has_started():
     assert 0 <= arrive < wait < min(stores)
     # Sequences without work leave before they arrive.
     assert body.index("if (span.n <= 0)") < arrive
+
+
+def test_shared_memory_written_by_a_warp_is_handed_over_by_a_warp_barrier():
+    """Stores of several lanes that a product reads (or that lane 0 announces): the fence to
+    the asynchronous side, by every lane, then a barrier of the warp."""
+    text = source("pa_tree_attention.cu")
+    fences = [m.end() for m in re.finditer(r"fence_proxy_async_smem\(\);", text)]
+    assert len(fences) >= 3
+    for at in fences:
+        assert re.match(r"\s*__syncwarp\(\);", text[at:]), text[at:at + 80]
