@@ -56,6 +56,7 @@
 #include <cmath>
 
 #include "pa_tree.cuh"
+#include "pa_tree_ring.h"
 
 namespace pa {
 namespace {
@@ -108,15 +109,14 @@ struct Tlay {
     static constexpr int kPanels = D / 64;
     static constexpr int kQPanel = kRows * 128;  // 64 dims of 128 rows
     static constexpr int kQ = kPanels * kQPanel;
-    // Tiles of K and V as the products read them.  A bf16 pool's share a ring in the order of
-    // their use, K of a tile two outputs ahead: K0 K1 V0 K2 V1 K3 V2 ..  (A ring of two for K
-    // and one of three for V left K's loads in the chain: 16 wide trees 137 us.)
+    // Tiles of K and V as the products read them, in the places that the ring gives them.
     // An FP8 pool's K is read as codes; its V lands as codes and is converted.
+    using Ring = TreeRing<D, KV8>;
     static constexpr int kVTile = kPanels * kKeys * 128;
     static constexpr int kKTile = KV8 ? kKeys * 128 : kVTile;
-    static constexpr int kRing = D == 64 ? 8 : 5;  // bf16
-    static constexpr int kKSlots = 3, kVSlots = 2, kStages = KV8 ? 3 : 0;  // FP8
-    static constexpr int kSlots = KV8 ? kKSlots + kVSlots : kRing;
+    static constexpr int kRing = Ring::kRing, kSlots = Ring::kSlots;
+    static constexpr int kKSlots = Ring::kKSlots, kVSlots = Ring::kVSlots;
+    static constexpr int kStages = KV8 ? 3 : 0;
     // The warp that issues the scores' products (1: the outputs' one), and the one that fetches
     // V (0: K's one).  A thread each for the products and a warp each for the copies let wide
     // bf16 trees run at 1400 cycles a tile instead of 1750.  Of up to 64 rows V stays with K
@@ -143,19 +143,15 @@ struct Tlay {
         uint32_t at;
         __device__ __forceinline__ uint32_t parity() const { return (uint32_t)use & 1u; }
     };
-    static __device__ __forceinline__ Place in_ring(int n) {
-        return {n % kRing, n / kRing, (uint32_t)(kQ + n % kRing * kVTile)};
-    }
     static __device__ __forceinline__ Place k(int i) {
-        if constexpr (KV8)
-            return {i % kKSlots, i / kKSlots, (uint32_t)(kQ + i % kKSlots * kKTile)};
-        return in_ring(i ? 2 * i - 1 : 0);
+        const auto p = Ring::k(i);
+        return {p.slot, p.use, (uint32_t)(kQ + p.slot * kKTile)};
     }
     static __device__ __forceinline__ Place v(int i) {
-        if constexpr (KV8)
-            return {kKSlots + i % kVSlots, i / kVSlots,
-                    (uint32_t)(kQ + kKSlots * kKTile + i % kVSlots * kVTile)};
-        return in_ring(2 * i + 2);
+        const auto p = Ring::v(i);
+        return {p.slot, p.use,
+                (uint32_t)(KV8 ? kQ + kKSlots * kKTile + (p.slot - kKSlots) * kVTile
+                               : kQ + p.slot * kVTile)};
     }
 };
 
@@ -549,18 +545,15 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                                  policy);
         }
     };
+    auto read_wait = [&](typename L::Ring::After r) -> bool {
+        return r.what == TreeRead::scores   ? tile_wait(sy.s_done, r.tile)
+               : r.what == TreeRead::output ? tile_wait(sy.pv_done, r.tile)
+                                            : true;
+    };
     // K / V of tile i, once what lay in the slot before is read.
     auto load_k = [&](int i, int row) -> bool {
         const auto p = L::k(i);
-        bool ok = true;
-        if constexpr (KV8) {
-            if (i >= L::kKSlots) ok = tile_wait(sy.s_done, i - L::kKSlots);
-        } else if constexpr (D == 128) {  // V of tile i - 4 (K 0 before K 3)
-            if (i >= 4) ok = tile_wait(sy.pv_done, i - 4);
-            if (i == 3) ok = tile_wait(sy.s_done, 0);
-        } else {
-            if (i >= 5) ok = tile_wait(sy.s_done, i - 4);
-        }
+        const bool ok = read_wait(L::Ring::k_after(i));
         if (ok) copy(smem + p.at, &sy.full[p.slot], (uint32_t)L::kKTile, row);
         return ok;
     };
@@ -574,28 +567,22 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
             return true;
         } else {
             const auto p = L::v(i);
-            bool ok = true;
-            if constexpr (D == 128) {  // K of tile i - 1
-                if (i >= 2) ok = tile_wait(sy.s_done, i - 1);
-            } else {  // V of tile i - 4 (K 0 before V 3)
-                if (i >= 4) ok = tile_wait(sy.pv_done, i - 4);
-                if (i == 3) ok = tile_wait(sy.s_done, 0);
-            }
+            const bool ok = read_wait(L::Ring::v_after(i));
             if (ok) copy(smem + p.at, &sy.full[p.slot], (uint32_t)L::kVTile, row);
             return ok;
         }
     };
     // The copies of the first n tiles have landed.
     auto land_k = [&](int n) {
-        for (int i = max(0, n - (KV8 ? 3 : 4)); i < n; ++i) {
-            if constexpr (!KV8 && D == 128)  // (V of tile i + 1 may already have the slot)
+        for (int i = max(0, n - L::Ring::kInFlight); i < n; ++i) {
+            if constexpr (L::Ring::kKLandsByScores)
                 tile_wait(sy.s_done, i);
             else
                 mbar_wait_bounded(&sy.full[L::k(i).slot], L::k(i).parity());
         }
     };
     auto land_v = [&](int n) {
-        for (int i = max(0, n - (KV8 ? 3 : 4)); i < n; ++i) {
+        for (int i = max(0, n - L::Ring::kInFlight); i < n; ++i) {
             if constexpr (KV8)
                 mbar_wait_bounded(&sy.staged[i % L::kStages], (uint32_t)(i / L::kStages) & 1u);
             else
@@ -1233,7 +1220,7 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
                     in[c] = make_uint4(clear(in[c].x), clear(in[c].y), clear(in[c].z),
                                        clear(in[c].w));
             }
-            if (i >= L::kVSlots && !tile_wait(sy.pv_done, i - L::kVSlots)) return false;
+            if (!read_wait(L::Ring::v_after(i))) return false;
             uint8_t *base = smem + p.at + (r >> 3) * L::kGroup + (r & 7) * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {

@@ -4,6 +4,8 @@ clusters of CTAs per sequence, ranges of many tiles, many segments per range.
 
 from __future__ import annotations
 
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -26,6 +28,48 @@ def _clean_errors():
 
 
 # ---------------------------------------------------------------- attention
+def check_some(c, which, out=None, what=""):
+    """The rows of sequences `which` of a batch, each against the definition over its own
+    blocks."""
+    out = c.run() if out is None else out
+    b, cu = c.b, _tree.cu_of(c.T)
+    for s in which:
+        n = int(b.seq_lens[s])
+        ids = b.block_tables[s, :-(-n // b.block_size)].long()
+        rows = slice(int(cu[s]), int(cu[s + 1]))
+        table = torch.arange(len(ids)).view(1, -1)
+        want, tol = _tree.tree_attention(b.q[rows], c.pool[ids], table, [n], [c.T[s]],
+                                         c.up[rows], b.scale, c.scales)
+        _tree.assert_attention(out[rows], want, tol, f"{what} sequence {s}")
+    assert torch.isfinite(out.float()).all()
+
+
+def workers():
+    """CTAs of a large batch: two per SM."""
+    return 2 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("tiles", [3, 4, 5, 8, 9, 13])
+@pytest.mark.parametrize("heads,T", [(8, 6), (64, 40)])  # up to 64 rows, and more
+def test_ranges_of_few_tiles_of_head_size_64(tiles, heads, T):
+    """Every CTA walks this many 64-key tiles (the ring of K and V holds four of each): no
+    wait runs out, which would take seconds and be flagged."""
+    kv_heads = 8
+    groups = -(-T * (heads // kv_heads) // 128)
+    per_seq = max(7, -(-workers() * tiles // (kv_heads * groups * 2)))
+    ctx = [per_seq * 64 - T - i for i in range(2)]
+    c = Case(ctx, [T] * 2, heads, kv_heads, 64, 16, seed=tiles)
+    c.run()
+    torch.cuda.synchronize()
+    ws, out = c.workspace(), torch.empty_like(c.b.q)
+    start = time.perf_counter()
+    for _ in range(20):
+        c.run(out=out, ws=ws)
+    torch.cuda.synchronize()
+    assert time.perf_counter() - start < 1.0
+    check_some(c, [0, 1], out)
+
+
 @pytest.mark.parametrize("T,heads", [(5, 4), (64, 16)])
 def test_cleared_values_are_handed_over_on_every_call(T, heads):
     """V of unseen nodes and of what lies behind the sequences holds NaN and infinities, in
