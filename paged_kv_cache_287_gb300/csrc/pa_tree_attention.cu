@@ -100,7 +100,10 @@ struct TreeAttnArgs {
     int change;          // units of a change of segment
     int negate_q;
     float scale_log2;  // |scale| * log2(e), at least 1e-30
-    float k_scale, v_scale;
+    // An FP8 pool: scale_log2 * k_scale = qk_mant 2^qk_exp, qk_mant in [0.5, 1).
+    float qk_mant;
+    int qk_exp;
+    float v_scale;
 };
 
 // Two: queries of up to 64 rows, held twice.
@@ -505,12 +508,14 @@ __global__ void __launch_bounds__(Tlay<D, KV8, Two>::kThreads, 2)
         __syncwarp();
     };
     auto rows_of = [&](const Seg &g) { return min(QT, g.n() - g.rg() * QT) * G; };
-    // What a row's scores are multiplied with (FP8: from its exponent).
+    // What a row's scores are multiplied with, always above zero (a hidden key's -inf stays what
+    // it is).  FP8: with its own power of two too, held to the normal fp32 numbers: a smaller
+    // factor than 2^-126 leaves every visible key the same weight as well.
     auto row_scale = [&](int exponent) -> float {
         if constexpr (!KV8) return a.scale_log2;
-        return exponent == 255
-                   ? NAN
-                   : a.scale_log2 * a.k_scale * __uint_as_float((uint32_t)exponent << 23);
+        const int e = max(-125, min(127, a.qk_exp + exponent - 127));
+        return exponent == 255 ? NAN
+                               : a.qk_mant * __uint_as_float((uint32_t)(e + 127) << 23);
     };
 
     // K and V come through the block table, a block's rows of one head per copy (a box), the
@@ -1548,7 +1553,7 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
     // zero becomes a value far too small to change any finite score.
     a.negate_q = scale < 0.f ? 1 : 0;
     a.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
-    a.k_scale = k_scale;
+    a.qk_mant = (float)std::frexp((double)a.scale_log2 * (double)k_scale, &a.qk_exp);
     a.v_scale = v_scale;
     // Contexts of a few tiles: a range of whole segments costs at most those tiles (about
     // 0.6 us each) and saves the merge's launch.

@@ -99,6 +99,23 @@ def test_cleared_values_are_handed_over_on_every_call(T, heads):
         assert torch.equal(out.view(torch.int16), first.view(torch.int16)), i
 
 
+@pytest.mark.parametrize("T", [9, 64])  # up to 64 rows, and more
+@pytest.mark.parametrize("scale,k_scale", [(0.0, None), (0.1, 1e-9), (1e-12, 1e-30)])
+def test_tiny_queries_and_scales_over_an_fp8_pool(T, scale, k_scale):
+    """A row's factor (scale, K's scale and the row's own power of two) may lie below the
+    smallest fp32 number: the row still takes the mean of what it sees, and of nothing
+    else."""
+    c = Case([100, 700], [T, 5], 8, 2, 128, 16, seed=26, fp8=True, scale=scale)
+    if k_scale is not None:
+        c.scales = (k_scale, c.scales[1])
+    q = c.b.q
+    q[1] = 0.0
+    q[2] *= 2.0 ** -40
+    q[3] *= 2.0 ** -100
+    q[4, 1] = 1e-39  # a subnormal
+    c.check()
+
+
 # ---------------------------------------------------------------- verification in clusters
 @pytest.mark.parametrize("vocab", [5000, 16384, 40000])  # 2, 8 and 8 CTAs per sequence
 @pytest.mark.parametrize("with_draft", [True, False])
