@@ -1,10 +1,24 @@
 // pa_tree.cuh - draft trees: what the pa_tree_* kernels share.
 #pragma once
 
+#include <atomic>
+
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
 namespace pa {
+
+// Read a translation unit's device error word, and clear it where it is set; nothing to
+// read before this process's first launch of its kernels.  (A copy takes the host some 7 us:
+// with a read and a clearing of all six words pa_error_check took 84 us.)
+template <typename Word>
+cudaError_t take_error_word(const std::atomic<bool> &launched, Word &word, unsigned *bits) {
+    *bits = 0;
+    if (!launched.load()) return cudaSuccess;
+    const unsigned zero = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(bits, word, sizeof(unsigned));
+    return e == cudaSuccess && *bits ? cudaMemcpyToSymbol(word, &zero, sizeof(unsigned)) : e;
+}
 
 // Sequence s's tree: rows [row0, row0 + n) of the node arrays.  n = -1 where the
 // offsets are not those of a tree of at most max_tree nodes within the arrays.

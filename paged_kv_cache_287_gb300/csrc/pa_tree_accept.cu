@@ -24,6 +24,7 @@ namespace pa {
 namespace {
 
 __device__ unsigned g_err_tree_accept;
+std::atomic<bool> g_launched{false};  // in this process, on any device
 
 constexpr int kBatch = 8;
 
@@ -92,10 +93,7 @@ __global__ void __launch_bounds__(256) tree_accept_kernel(const AcceptArgs a) {
 }  // namespace
 
 cudaError_t take_error_tree_accept(unsigned *bits) {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_err_tree_accept, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_err_tree_accept, &zero, sizeof(unsigned));
-    return e;
+    return take_error_word(g_launched, g_err_tree_accept, bits);
 }
 
 cudaError_t launch_tree_accept(void *kv_cache, const KvGeom &g, int elem_bytes,
@@ -120,6 +118,7 @@ cudaError_t launch_tree_accept(void *kv_cache, const KvGeom &g, int elem_bytes,
     // At least the 64 threads that check a path.
     const int threads = std::min(256, std::max(64, (cols + 31) / 32 * 32));
     const dim3 grid((unsigned)t.num_seqs, (unsigned)((cols + threads - 1) / threads));
+    g_launched.store(true);
     return launch_pdl(tree_accept_kernel, grid, threads, 0, 1, stream, a);
 }
 

@@ -62,6 +62,7 @@ namespace pa {
 namespace {
 
 __device__ unsigned g_err_tree_attention;
+std::atomic<bool> g_launched{false};  // in this process, on any device
 
 constexpr int kRows = 128;  // query rows per tile (the MMA's M)
 // Keys per K/V tile: two buffers of scores beside O fit half of tensor memory.  (One of 128
@@ -1477,6 +1478,7 @@ template <int D, bool KV8, bool Two>
 cudaError_t launch_rows(const CUtensorMap &map, const CUtensorMap &q_map, const TreeAttnArgs &a,
                         cudaStream_t stream) {
     using L = Tlay<D, KV8, Two>;
+    g_launched.store(true);
     cudaError_t e = ensure_smem<tree_attention_kernel<D, KV8, Two>>(L::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(tree_attention_kernel<D, KV8, Two>, dim3((unsigned)a.ctas),
@@ -1501,10 +1503,7 @@ cudaError_t launch(const CUtensorMap &map, const CUtensorMap &q_map, const TreeA
 }  // namespace
 
 cudaError_t take_error_tree_attention(unsigned *bits) {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_err_tree_attention, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_err_tree_attention, &zero, sizeof(unsigned));
-    return e;
+    return take_error_word(g_launched, g_err_tree_attention, bits);
 }
 
 size_t tree_attention_workspace_bytes(int num_seqs, int max_tree, int group, int head_size,

@@ -39,6 +39,7 @@ namespace pa {
 namespace {
 
 __device__ unsigned g_err_tree_verify;
+std::atomic<bool> g_launched{false};  // in this process, on any device
 
 constexpr int kNodes = 64;
 constexpr int kWarps = 16;
@@ -666,10 +667,7 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
 }  // namespace
 
 cudaError_t take_error_tree_verify(unsigned *bits) {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_err_tree_verify, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_err_tree_verify, &zero, sizeof(unsigned));
-    return e;
+    return take_error_word(g_launched, g_err_tree_verify, bits);
 }
 
 cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t *next_tokens,
@@ -715,6 +713,7 @@ cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t
         const cudaError_t e = ensure_smem<tree_verify_kernel<true, true>>(keep);
         if (e != cudaSuccess) return e;
     }
+    g_launched.store(true);
     const dim3 grid((unsigned)(t.num_seqs * c));
     auto *kern = kept    ? tree_verify_kernel<true, true>
                  : draft ? tree_verify_kernel<true, false>
