@@ -522,9 +522,11 @@ pa_status pa_tree_attention_fp8(void *out, const void *q, const int32_t *cu_tree
  *                 probability 0 and is flagged PA_ERR_OOB (the roots' are unread)
  *   accept_u      [total_nodes] fp32 in [0, 1) (the roots' are unread)
  *   sample_u      [num_seqs] fp32 in [0, 1)
- * Probabilities (finite, >= 0) are taken as they are, not normalised.  Sums,
- * differences and products carry some 47 bits: the result is the formulas' unless
- * the two sides of a comparison agree to that.
+ * Probabilities (finite, >= 0) are taken as they are, not normalised.  Products,
+ * quotients and differences carry some 47 bits (fewer below 2^-100, where fp32
+ * underflows), a sum over the vocabulary is within 2^-38 of itself (some 2^-44 for
+ * ordinary data): the result is the formulas' unless the two sides of a comparison
+ * agree to that.
  * vocab_size from 1 to 1048576 (else PA_ERR_UNSUPPORTED).  fp32 pointers must be
  * 4-byte aligned.  No workspace.  num_seqs == 0 is a no-op.
  */

@@ -22,10 +22,12 @@
 //
 // Precision: whole numbers come out, so a sum must not be off by what separates
 // neighbouring tokens.  r and its sums are held as unevaluated pairs of fp32 numbers
-// (a head and the rounding error of the operation before; about 48 bits), since this
-// GPU's 64-bit units are some 60 times slower than its 32-bit ones: one CTA of 64-bit
+// (a head and the rounding error of the operation before; about 48 bits an operation), since
+// this GPU's 64-bit units are some 60 times slower than its 32-bit ones: one CTA of 64-bit
 // sums took 1433 us where the batch's bytes take 40 (256 chains, 131072 tokens), and
-// 64-bit sums across the 16 warps of each CTA alone some 2 us a pass.
+// 64-bit sums across the 16 warps of each CTA alone some 2 us a pass.  A thread's sum of up
+// to 512 numbers takes 64 additions to each of two accumulators, each off by at most 5 2^-48
+// of it, and 12 more join the threads': below 2^-38 of the whole, at random some 2^-44.
 //
 // Measured (GB300): those 256 chains 52 us, 5.2 TB/s; 48 trees of 9-31 nodes with sibling
 // rounds, 50021 tokens, 24 us; 64 trees of 33-64 proposed nodes, 131072 tokens, 18 us; one
@@ -78,6 +80,29 @@ __device__ __forceinline__ void add_to(Pair &acc, Pair x) {
     const Pair s = two_sum(acc.h, x.h);
     acc.h = s.h;
     acc.l = __fadd_rn(acc.l, __fadd_rn(s.l, x.l));
+}
+
+// The same into a thread's long sum, the tail folded into the head: a tail that only gathers
+// the errors of the heads grows with every addition and loses bits of its own (256 additions
+// left sums off by 2^-34).
+__device__ __forceinline__ void add_long(Pair &acc, Pair x) {
+    add_to(acc, x);
+    const float h = __fadd_rn(acc.h, acc.l);
+    acc.l = __fadd_rn(acc.l, -__fadd_rn(h, -acc.h));
+    acc.h = h;
+}
+
+// Four numbers' sum, by halves: fewer additions stand behind each other than in a chain.
+__device__ __forceinline__ Pair sum4(const float (&v)[4]) {
+    Pair a = two_sum(v[0], v[1]);
+    add_to(a, two_sum(v[2], v[3]));
+    return a;
+}
+__device__ __forceinline__ Pair sum4(Pair (&v)[4]) {
+    add_to(v[0], v[1]);
+    add_to(v[2], v[3]);
+    add_to(v[0], v[2]);
+    return v[0];
 }
 
 // The sum over kLanes consecutive lanes (those behind them hold nothing where fewer
@@ -428,7 +453,7 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
                     const Pair r = next_residual({s_rh[i], s_rl[i]}, s_qc[i], s_zinv[rej - 1]);
                     s_rh[i] = r.h;
                     s_rl[i] = r.l;
-                    add_to(acc[0], r);
+                    add_long(acc[0], r);
                 }
             } else if (with && rej > 0 && kKept) {
                 // A short slice: one token per lane, so that r's places lie side by side.
@@ -447,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
                             s_rl[x + 32 * k - c0] = r.l;
                             s_qc[x + 32 * k - c0] = qv[k];
                         }
-                        add_to(acc[k & 1], r);
+                        add_long(acc[k & 1], r);
                     }
                 }
             } else if (with && rej > 0) {
@@ -461,10 +486,13 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
                         load4(q, x + 128 * k, v0, v1, wide, qv[k]);
                     }
 #pragma unroll
-                    for (int k = 0; k < kU; ++k)
+                    for (int k = 0; k < kU; ++k) {
+                        Pair r[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            add_to(acc[e & 1], residual(pv[k][e], qv[k][e], rej, s_zinv));
+                            r[e] = residual(pv[k][e], qv[k][e], rej, s_zinv);
+                        add_long(acc[k & 1], sum4(r));
+                    }
                 }
             } else {
                 const int x0 = first4(p);
@@ -475,14 +503,15 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
                     for (int k = 0; k < 2 * kU; ++k)
                         load4(p, x + 128 * k, v0, v1, wide, pv[k]);
 #pragma unroll
-                    for (int k = 0; k < 2 * kU; ++k)
+                    for (int k = 0; k < 2 * kU; ++k) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int y = x + 128 * k + e, b = y - c0;
                             if (!with && y >= v0 && y < v1 && ((s_gone[b >> 5] >> (b & 31)) & 1u))
                                 pv[k][e] = 0.f;
-                            add_to(acc[e & 1], {pv[k][e], 0.f});
                         }
+                        add_long(acc[k & 1], sum4(pv[k]));
+                    }
                 }
             }
             add_to(acc[0], acc[1]);
@@ -589,6 +618,7 @@ __global__ void __launch_bounds__(kWarps * 32, 32 / kWarps)
                 eight(x, 32, y1, r);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) add_to(acc, r[k]);
+                acc = normal(acc);
             }
             acc = warp_sum(acc);
             if (lane == 0) s_sub[warp] = acc;

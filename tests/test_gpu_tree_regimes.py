@@ -164,3 +164,51 @@ def test_verify_falls_back_in_clusters(vocab):
         d = _tree.Drafts(p[:1], None, tokens[:1], star[:1], one, torch.zeros(1),
                          torch.tensor([1.0]), [1])
         assert run_verify(d) == d.reference == ([[0]], [hi])
+
+
+# ---------------------------------------------------------------- verification's sums
+def lossy_row(vocab):
+    """Probabilities whose sum a head with a tail in plain fp32 gets wrong by some 2^-34, and
+    a sample_u whose goal lies between: token 0 has 1, 255 tokens of the same thread a little
+    less than 2^-24 each, chosen so that the tail's rounding loses nearly half a unit every
+    time."""
+    at = [128 * (j // 2) + 2 * (j % 2) for j in range(256)]
+    step, tail, lost, t = 2.0 ** -48, np.float32(0), 0.0, [1.0]
+    for _ in range(1, 255):
+        x = 0.9 * 2.0 ** -24 // step * step
+        unit = 2.0 ** (np.floor(np.log2(float(tail) + x)) - 23)
+        if unit > step:
+            x += (0.5 * unit - step - (float(tail) + x) % unit) % unit
+            x -= unit * (x >= 2.0 ** -24)
+        assert x == float(np.float32(x)) and 0 < x < 2.0 ** -24
+        new = np.float32(float(tail) + x)
+        lost += float(tail) + x - float(new)
+        tail = new
+        t.append(x)
+    cum = np.cumsum(t)  # exact: multiples of 2^-48 below 2
+    # The last number puts u times the whole a third of what is lost past token j's sum.
+    u, j, x = next((u, j, x) for u in 1.0 - np.arange(40, 200) * 2.0 ** -24
+                   for j in range(100, 250) for x in [(cum[j] + lost / 3) / u - cum[-1]]
+                   if 2.0 ** -25 < x < 2.0 ** -24)
+    t.append(float(np.float32(x)))
+    total = cum[-1] + t[-1]
+    assert lost > 2.0 ** -35 and u * (total - lost) < cum[j] < u * total
+    row = torch.zeros(vocab)
+    row[at] = torch.tensor(t, dtype=torch.float64).float()
+    return row, float(u), at[j + 1]
+
+
+def test_verify_sums_many_small_numbers_to_more_than_a_heads_and_a_tails_bits():
+    """As many sequences as give each one CTA, so that a thread adds 256 numbers: the draw
+    depends on bits that a tail in plain fp32 loses."""
+    B, vocab = workers() // 2 + 8, 1 << 18
+    row, u, want = lossy_row(vocab)
+    target = torch.zeros(B, vocab)
+    target[:, 7] = 1.0
+    target[B // 2] = row
+    d = _tree.Drafts(target, None, torch.zeros(B, dtype=I32),
+                     torch.full((B,), -1, dtype=I32), torch.arange(B + 1, dtype=I32),
+                     torch.zeros(B), torch.full((B,), u), [1] * B)
+    got = run_verify(d)
+    assert d.reference[1][B // 2] == want
+    assert got == d.reference
