@@ -99,6 +99,97 @@ def test_cleared_values_are_handed_over_on_every_call(T, heads):
         assert torch.equal(out.view(torch.int16), first.view(torch.int16)), i
 
 
+KINDS = [(64, False), (128, False), (128, True)]  # head size, FP8 pool
+
+
+@pytest.mark.parametrize("D,fp8", KINDS)
+@pytest.mark.parametrize("wide", [False, True])
+def test_ranges_of_many_tiles_and_segments(D, fp8, wide):
+    """At least 14 tiles per CTA, so that ranges are cut with the weight of a change: rings
+    that wrap, many segments per range, ragged contexts, empty trees in between; wide: trees
+    of one to four row groups, whose CTAs walk side by side."""
+    rng = np.random.default_rng(40 + D + 2 * fp8 + wide)
+    B, heads, kv_heads = (24, 32, 4) if wide else (40, 32, 8)
+    T = [int(t) for t in rng.integers(1, 65 if wide else 17, B)]
+    T[:4] = [64, 1, 33, 17] if wide else [16, 1, 0, 9]
+    mean = 14 * workers() * 64 // (B * kv_heads)
+    ctx = [int(x) for x in rng.integers(mean // 4, 2 * mean, B)]
+    ctx[1], ctx[3] = 6 * mean, 5
+    c = Case(ctx, T, heads, kv_heads, D, 16, seed=41, fp8=fp8)
+    tiles = [-(-(a + t) // 64) * -(-t * heads // kv_heads // 128) for a, t in zip(ctx, T)]
+    assert kv_heads * sum(tiles) >= 12 * workers()
+    check_some(c, [0, 1, 3, int(rng.integers(4, B)), B - 1])
+
+
+@pytest.mark.parametrize("less", [0, 1])
+@pytest.mark.parametrize("D,fp8", KINDS)
+def test_ranges_on_both_sides_of_the_weight_of_a_change(less, D, fp8):
+    """Batches of exactly 12 tiles per CTA, and of one tile less."""
+    B, kv_heads = 2, 2
+    per_seq = 12 * workers() // (B * kv_heads)
+    lens = [64 * (per_seq + 5), 64 * (per_seq - 5 - less) - 3]
+    T = [6, 3]
+    assert kv_heads * sum(-(-n // 64) for n in lens) == 12 * workers() - kv_heads * less
+    check_some(Case([n - t for n, t in zip(lens, T)], T, 8, kv_heads, D, 32, seed=42, fp8=fp8),
+               [0, 1], what=f"less {less}")
+
+
+@pytest.mark.parametrize("n", [1, 40, 900])
+@pytest.mark.parametrize("heads,hi", [(8, 12), (64, 64)])
+def test_ranges_that_begin_and_end_inside_a_change(n, heads, hi):
+    """Segments of n tokens of context, thousands of ranges' borders among them: borders fall
+    on every unit of a change and of its tiles."""
+    rng = np.random.default_rng(n + heads)
+    kv_heads = 8
+    per = -(-(n + hi) // 64)
+    B = min(1500, 13 * workers() // (per * kv_heads) + 1)
+    T = [int(t) for t in rng.integers(1, hi + 1, B)]
+    c = Case([n + i % 7 for i in range(B)], T, heads, kv_heads, 64, 8, seed=43)
+    check_some(c, sorted({0, B - 1, *rng.integers(0, B, 14).tolist()}))
+
+
+@pytest.mark.parametrize("D,fp8", KINDS)
+@pytest.mark.parametrize("heads", [8, 32])
+def test_attention_in_other_batch_orders(D, fp8, heads):
+    """The same sequences in three orders: ranges are cut elsewhere, every result within the
+    definition's tolerance."""
+    rng = np.random.default_rng(44)
+    T = [9, 40, 16, 1, 64, 0, 5]
+    c = Case([700, 90, 4000, 64, 2000, 0, 1500], T, heads, 4, D, 16, seed=45, fp8=fp8)
+    b, cu = c.b, _tree.cu_of(T)
+    want, tol = c.reference()
+    for _ in range(3):
+        order = rng.permutation(len(T))
+        rows = np.concatenate([np.arange(cu[s], cu[s + 1]) for s in order])
+        at = torch.from_numpy(rows).to(DEV)
+        out = torch.full_like(b.q, float("nan"))
+        binding.pa_tree_attention(
+            out, b.q[at].contiguous(), torch.from_numpy(_tree.cu_of([T[s] for s in order])).to(DEV),
+            c.parents[at].contiguous(), c.max_tree, c.pool,
+            b.block_tables[torch.from_numpy(order).to(DEV)].contiguous(),
+            b.seq_lens[torch.from_numpy(order).to(DEV)].contiguous(), c.max_len, b.scale,
+            c.workspace(), kv_scales=c.scales)
+        _tree.assert_attention(out, want[rows], tol[rows], str(order))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_of_random_shapes(seed):
+    rng = np.random.default_rng(1000 + seed)
+    fp8 = bool(rng.integers(0, 2))
+    kv_heads, group = int(rng.choice([1, 2, 3, 8])), int(rng.integers(1, 9))
+    D, bs = (128 if fp8 else int(rng.choice([64, 128]))), int(rng.choice([8, 16, 32]))
+    B, hi = int(rng.integers(1, 9)), int(rng.choice([2, 8, 17, 64]))
+    T = [int(t) for t in rng.integers(0, hi + 1, B)]
+    T[0] = max(T[0], 1)
+    edges = [0, 1, 7, 63, 64, 65, 127, 128, 383, 384, 385, 1000]
+    ctx = [int(rng.choice(edges)) if rng.random() < 0.6 else int(rng.integers(0, 3000))
+           for _ in T]
+    shape = str(rng.choice(["tree", "chain", "star", "forest"]))
+    c = Case([x if t else 0 for x, t in zip(ctx, T)], T, kv_heads * group, kv_heads, D, bs,
+             seed=seed, shape=shape, fp8=fp8, scale=float(rng.choice([0.05, 0.2, -0.1])))
+    c.check(f"{kv_heads}x{group} D {D} block {bs} T {T} ctx {ctx} {shape}")
+
+
 @pytest.mark.parametrize("T", [9, 64])  # up to 64 rows, and more
 @pytest.mark.parametrize("scale,k_scale", [(0.0, None), (0.1, 1e-9), (1e-12, 1e-30)])
 def test_tiny_queries_and_scales_over_an_fp8_pool(T, scale, k_scale):
@@ -142,6 +233,28 @@ def test_verify_in_clusters_beside_other_work(vocab, with_draft):
     for acc, num, nxt in outs:
         assert nxt.tolist() == nexts
         assert [acc[i, :n].tolist() for i, n in enumerate(num.tolist())] == paths
+
+
+@pytest.mark.parametrize("with_draft", [True, False])
+@pytest.mark.parametrize("B,vocab", [(2, 1 << 20), (170, 600011)])
+def test_verify_of_the_largest_vocabularies(B, vocab, with_draft):
+    """Up to 1048576 tokens; and so large a batch that the clusters' size goes by the
+    vocabulary alone (four CTAs, each of at most 2^18 tokens)."""
+    T = [4 if s == B // 2 else 1 for s in range(B)]
+    g = torch.Generator(device=DEV).manual_seed(B)
+    target = torch.softmax(torch.randn(sum(T), vocab, generator=g, device=DEV) * 2, dim=1)
+    draft = torch.softmax(target.log() + torch.randn(sum(T), vocab, generator=g, device=DEV), 1)
+    up = sum((([-1, 0, 0, 1]) if t > 1 else [-1] for t in T), [])
+    cu = _tree.cu_of(T)
+    base = np.repeat(cu[:-1], T)
+    tokens = torch.tensor([int(draft[b + max(p, 0)].argmax()) if p >= 0 else 0
+                           for b, p in zip(base, up)], dtype=I32)
+    d = _tree.Drafts(target.cpu(), draft.cpu() if with_draft else None, tokens,
+                     torch.tensor(up, dtype=I32), torch.from_numpy(cu),
+                     torch.rand(sum(T), generator=torch.Generator().manual_seed(1)),
+                     torch.rand(B, generator=torch.Generator().manual_seed(2)), T)
+    del target, draft
+    assert run_verify(d) == d.reference
 
 
 @pytest.mark.parametrize("vocab", [16384, 50021])
