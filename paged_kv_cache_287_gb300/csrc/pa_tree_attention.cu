@@ -46,12 +46,15 @@
 // Measured (GB300, HBM copy 6689 GB/s, whole call): 32 sequences of 512-4096 tokens with
 // 12-16 nodes, 32 query and 8 KV heads of 128: 60 us, 5.2 TB/s; 8 sequences of 1024-131072
 // tokens with 7-23 nodes: 142 us, 6.1 TB/s; 16 sequences of 1024-8192 tokens, 33-64 nodes,
-// 64 and 8 heads: 128-132 us, 910 TFLOP/s (visible pairs); the first batch's kind from an FP8 pool,
-// 64 sequences, chains of 3-8: 78 us, 3.9 TB/s.  Per call some 5 us until the first products,
-// 4 to 8 us for the merge.  The wide case keeps the tensor pipe 51 % busy, the FP8 one 41 %
-// with DRAM at 3.9 TB/s: the chain of a tile, scores, softmax, output, scores over the same
-// buffer, takes 1400 to 1800 cycles per tile and CTA, and the two CTAs of an SM do not fill
-// each other's gaps entirely.
+// 64 and 8 heads: 130-136 us by machine, 880-910 TFLOP/s (visible pairs); the first batch's kind
+// from an FP8 pool, 64 sequences, chains of 3-8: 78 us, 3.9 TB/s.  Per call some 5 us until the
+// first products, 4 to 8 us for the merge.  The wide case keeps the tensor pipe 51 % busy, the
+// FP8 one 41 % with DRAM at 3.9 TB/s: the chain of a tile, scores, softmax, output, scores over
+// the same buffer, takes 1400 to 1800 cycles per tile and CTA, and the two CTAs of an SM do not
+// fill each other's gaps entirely.  (That is some 80 us of the wide kernel's 112; beside the
+// start, what the rest goes to has not been located.)  All figures here are of head size 128,
+// and of an FP8 pool for up to 64 rows: the rules drawn from them hold for the others too,
+// which are tested and not timed.
 #include <algorithm>
 #include <cmath>
 
@@ -1555,11 +1558,12 @@ cudaError_t launch_tree_attention(void *out, const void *q, const TreeGeom &t,
     a.qk_mant = (float)std::frexp((double)a.scale_log2 * (double)k_scale, &a.qk_exp);
     a.v_scale = v_scale;
     // Contexts of a few tiles: a range of whole segments costs at most those tiles (about
-    // 0.6 us each) and saves the merge's launch.
+    // 0.6 us each) and saves the merge's launch (one short sequence 9 us, 15-17 with it).
     a.whole_segments = max_seq_len <= kWholeTiles * kKeys;
     // A change costs some 7000 cycles, a tile 2400 where HBM bounds it (without: 32 sequences
     // 62.7 us, 61.2 with), 1400 to 1800 from an FP8 pool or with several row groups (without:
-    // 64 FP8 chains 93 us, 79 with; 16 wide trees 151, 141).
+    // 64 FP8 chains 93 us, 79 with; 16 wide trees 151, 141).  A tile of head size 64 moves half
+    // the bytes; its weight is the same here, unmeasured.
     a.change = kv8 || sh.row_groups > 1 ? 6 : 2;
     CUtensorMap q_map = {};
     if (!encode_rows_map(&q_map, q, g.head_size, num_heads, t.total_nodes, a.group,

@@ -29,8 +29,8 @@
 // to 512 numbers takes 64 additions to each of two accumulators, each off by at most 5 2^-48
 // of it, and 12 more join the threads': below 2^-38 of the whole, at random some 2^-44.
 //
-// Measured (GB300): those 256 chains 52 us, 5.2 TB/s; 48 trees of 9-31 nodes with sibling
-// rounds, 50021 tokens, 24 us; 64 trees of 33-64 proposed nodes, 131072 tokens, 18 us; one
+// Measured (GB300): those 256 chains 53 us, 5.1 TB/s; 48 trees of 9-31 nodes with sibling
+// rounds, 50021 tokens, 23-28 us; 64 trees of 33-64 proposed nodes, 131072 tokens, 19 us; one
 // chain of 6, 32000 tokens, 7 us (13 000 cycles: gathers 2000, walk 1200, pass 3000, cluster
 // sum 2000, draw 4500).
 #include <algorithm>
@@ -718,11 +718,12 @@ cudaError_t launch_tree_verify(int32_t *accepted, int32_t *num_accepted, int32_t
     a.sample_u = sample_u;
     a.t = t;
     a.vocab = vocab;
-    // CTAs per sequence: all of the batch resident at once (two per SM; with draft
-    // probabilities up to three, since sequences end after very different numbers of
-    // passes: 48 trees, 50021 tokens, 41 us with 8 CTAs each, 63 with 4 before r was
-    // kept between rejections), each with at least 2048 tokens, and slices whose bit
-    // sets fit 32 KB.
+    // CTAs per sequence: as many as fit the GPU at once, two per SM; with draft
+    // probabilities up to one and a half times that, since sequences end after very
+    // different numbers of passes and the last CTAs start where others have ended (48 trees,
+    // 50021 tokens, before r was kept between rejections: 41 us with 8 CTAs each, 384 of
+    // which 304 fit, 63 with 4).  Each with at least 2048 tokens, and slices whose bit sets
+    // fit 32 KB.
     const int sms = device_sm_count();
     const long long room = (draft ? 3LL : 2LL) * sms;
     int c = 1;
