@@ -618,6 +618,141 @@ pa_status pa_tree_accept_packed(const pa_tree_accept_args *args);
 size_t pa_tree_args_bytes(int call);
 
 /*
+ * 4-bit KV cache.  A 4-bit pool is uint8 [num_blocks][num_kv_heads][2][tile]: of every
+ * (block, KV head) K (index 0 of the third axis), then V, each a tile of block_size *
+ * head_size * 9 / 16 bytes: block_size rows of head_size / 2 bytes of codes, then block_size
+ * rows of head_size / 16 scales.  A code is OCP e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign),
+ * element 2i in the low four bits of byte i; a scale is OCP e4m3, one for each 16 consecutive
+ * elements.  An element is code * scale * k_scale (K) or v_scale (V), the tensor's scale
+ * (> 0, and 2688 times it, the largest element, finite; else PA_ERR_INVALID_ARG); largest
+ * element / 2688 uses the formats' whole range.  4.5 bits an element: 9/32 of the bf16 pool, 9/16 of the FP8 one.  A slot is
+ * physical_block * block_size + offset_in_block, as in the other pools; num_blocks *
+ * block_size must be below 2^31 (else PA_ERR_UNSUPPORTED).  The pool must be 16-byte aligned.
+ *
+ * The calls take their arguments in one struct, which is not kept; PA_ERR_INVALID_ARG for
+ * NULL.  They launch as programmatic dependents of what comes before on the stream and wait
+ * for it before they touch memory.
+ */
+
+/* Bytes of one block of a 4-bit pool, 2 * block_size * num_kv_heads * head_size * 9 / 16; 0
+ * for non-positive arguments or a head_size that is no multiple of 16. */
+size_t pa_kv_block_bytes_fp4(int block_size, int num_kv_heads, int head_size);
+
+/*
+ * pa_cache_write_fp4 - quantise rows into their slots of a 4-bit pool.
+ *
+ * Of each 16 consecutive elements x of a bf16 row, with g the tensor's scale: s =
+ * e4m3(max|x| / h), h = 6 * g rounded to binary32; d = s * g; the codes are e2m1(x / d).
+ * Products and divisions are binary32's; e4m3 and e2m1 are the nearest code, ties to the even
+ * one, saturating at 448 and 6.  Where d is 0 (the elements are too small for a scale) the
+ * codes are 0; a NaN among the elements makes the scale NaN, and so all 16.
+ *   k_rows, v_rows  [num_tokens][num_kv_heads][head_size] bf16; row i starts at element i *
+ *                 row_stride (>= num_kv_heads * head_size, a multiple of 8), 16-byte aligned
+ *   slot_mapping  [num_tokens] int32; slot < 0 skips the row; a slot beyond the pool is
+ *                 skipped and flagged PA_ERR_OOB
+ * The rest of the pool keeps its bytes.  Two rows with one slot: unspecified which lands.
+ *
+ * pa_cache_read_fp4 - the rows in those slots, back in bf16: k_rows and v_rows are written
+ * (with code * scale * g, the product with g rounded to binary32, then to bf16).  The rows of
+ * skipped slots are left as they were; several may read one slot.  k_rows and v_rows must not
+ * overlap.  With it a 4-bit context reaches what reads bf16 (a prompt's next chunk, a dump).
+ */
+typedef struct pa_cache_fp4_args {
+    void *kv_cache;
+    void *k_rows, *v_rows;
+    const int32_t *slot_mapping;
+    pa_stream_t stream;
+    int64_t row_stride;
+    int32_t num_blocks, block_size, num_kv_heads, head_size, num_tokens;
+    float k_scale, v_scale;
+} pa_cache_fp4_args;
+
+pa_status pa_cache_write_fp4(const pa_cache_fp4_args *args);
+pa_status pa_cache_read_fp4(const pa_cache_fp4_args *args);
+
+/*
+ * pa_decode_fp4 - pa_decode over a 4-bit pool (head_size 64 or 128).  Codes times scales are
+ * f16 numbers exactly; each query head is scaled by a power of two into f16 range (exact for
+ * elements down to 2^-14 of the head's largest), P is rounded to f16; products accumulate in
+ * fp32, softmax statistics are fp32.  The result is the same bits on every call.
+ *   seq_lens      a length below 0 or above max_seq_len is taken as the nearest of the two and
+ *                 flagged PA_ERR_OOB; 0 yields zero rows
+ *   workspace     >= pa_decode_fp4_workspace_bytes(...) bytes, 256-byte aligned, no
+ *                 initialisation needed; calls that overlap on the GPU must not share one
+ * A block id outside the pool is flagged PA_ERR_OOB and its tokens read as zeros.  Other
+ * arguments and errors as pa_decode.
+ */
+typedef struct pa_decode_fp4_args {
+    void *out;
+    const void *q;
+    const void *kv_cache;
+    const int32_t *block_tables;
+    const int32_t *seq_lens;
+    void *workspace;
+    size_t workspace_bytes;
+    pa_stream_t stream;
+    int32_t num_seqs, num_blocks, block_size, num_heads, num_kv_heads, head_size;
+    int32_t max_blocks_per_seq, max_seq_len;
+    float scale, k_scale, v_scale;
+} pa_decode_fp4_args;
+
+size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                     int head_size);
+pa_status pa_decode_fp4(const pa_decode_fp4_args *args);
+
+/*
+ * pa_qkv_rope_write - a projection's rows on their way to the attention, in one pass: norms of
+ * q and k per head, rotary positions, q out, K and V into the pool.
+ *
+ *   norm      x := x / sqrt(mean(x^2) + eps) * w over a head's elements; no norm where the
+ *             weights are NULL
+ *   rotation  of the first rot_dim elements of every q and k head: pair i < rot_dim / 2 is
+ *             elements (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved; (a, b) becomes
+ *             (a c - b s, b c + a s), c = cos_sin[p][i] and s = cos_sin[p][rot_dim / 2 + i]
+ *             at the token's position p = positions[axis][token], axis = pair_axis[i]
+ * in fp32, rounded to bf16 once; a 4-bit or FP8 pool then stores K as pa_cache_write_fp4 or
+ * pa_cache_write_fp8 would, V as it is in qkv.
+ *   q_out         [num_tokens][num_heads][head_size] bf16, written; must not overlap qkv
+ *   kv_cache      the pool: bf16 (kv_bits 16), FP8 (8) or 4-bit (4), in its own layout
+ *   qkv           rows of num_heads + 2 * num_kv_heads heads (q, k, v) bf16; row i starts at
+ *                 element i * row_stride (a multiple of 8), 16-byte aligned
+ *   q_weight, k_weight  [head_size] bf16 (16-byte aligned) or NULL, each by itself
+ *   cos_sin       [max_position][rot_dim] fp32: rot_dim / 2 cosines, then as many sines
+ *                 (with any scaling of frequencies or amplitude in them)
+ *   positions     [num_axes][num_tokens] int32.  A token with a position outside [0,
+ *                 max_position) on an axis that a pair uses is skipped (neither q nor K and V
+ *                 written) and flagged PA_ERR_OOB
+ *   pair_axis     [rot_dim / 2] int32 in [0, num_axes) (another is taken as 0 and flagged
+ *                 PA_ERR_OOB); may be NULL when num_axes is 1: axes of time, height and width
+ *                 for images and video, in sections or interleaved
+ *   slot_mapping  [num_tokens] int32; a negative slot leaves the pool alone (q is written), one
+ *                 beyond it likewise, flagged PA_ERR_OOB
+ *   rot_dim       a multiple of 16, 16 .. head_size (else PA_ERR_UNSUPPORTED)
+ *   num_axes      1 .. 8 (else PA_ERR_UNSUPPORTED)
+ *   eps           finite, >= 0 (read where there is a norm)
+ * num_tokens == 0 is a no-op.
+ */
+typedef struct pa_qkv_rope_write_args {
+    void *q_out;
+    void *kv_cache;
+    const void *qkv;
+    const void *q_weight, *k_weight;
+    const float *cos_sin;
+    const int32_t *positions, *pair_axis, *slot_mapping;
+    pa_stream_t stream;
+    int64_t row_stride;
+    int32_t num_tokens, num_blocks, block_size, num_heads, num_kv_heads, head_size;
+    int32_t rot_dim, max_position, num_axes, interleaved, kv_bits;
+    float eps, k_scale, v_scale;
+} pa_qkv_rope_write_args;
+
+pa_status pa_qkv_rope_write(const pa_qkv_rope_write_args *args);
+
+/* sizeof the struct of pa_cache_write_fp4 and pa_cache_read_fp4 (0), pa_decode_fp4 (1),
+ * pa_qkv_rope_write (2), for callers that lay it out themselves; 0 for another call. */
+size_t pa_fp4_args_bytes(int call);
+
+/*
  * Synchronise `stream`, then read and clear the device error word the kernels
  * of this library set on the current device.  Returns PA_OK, PA_ERR_TIMEOUT,
  * PA_ERR_OOB or PA_ERR_PRECONDITION (the first of these that was set, in this

@@ -36,6 +36,9 @@ EXPORTS = ("pa_status_string", "pa_kv_block_bytes", "pa_kv_block_bytes_dtype", "
            "pa_tree_attention_workspace_bytes", "pa_tree_attention", "pa_tree_attention_fp8",
            "pa_tree_verify", "pa_tree_accept", "pa_tree_accept_fp8", "pa_tree_attention_packed",
            "pa_tree_verify_packed", "pa_tree_accept_packed", "pa_tree_args_bytes",
+           "pa_kv_block_bytes_fp4", "pa_cache_write_fp4", "pa_cache_read_fp4",
+           "pa_decode_fp4_workspace_bytes", "pa_decode_fp4", "pa_qkv_rope_write",
+           "pa_fp4_args_bytes",
            "pa_error_check")
 
 # Nodes of a draft tree, at most (PA_TREE_MAX_NODES).
@@ -50,6 +53,8 @@ VARLEN_ARGS = struct.Struct("<12Q12i3f")
 # pa_tree_attention_args, pa_tree_verify_args and pa_tree_accept_args likewise, in the order
 # of their members.
 TREE_ARGS = (struct.Struct("<10Q11i3f"), struct.Struct("<11Q2q4i"), struct.Struct("<8Q8i"))
+# pa_cache_fp4_args, pa_decode_fp4_args and pa_qkv_rope_write_args.
+FP4_ARGS = (struct.Struct("<5Qq5i2f4x"), struct.Struct("<8Q8i3f4x"), struct.Struct("<10Qq11i3f"))
 _BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
 _tls = threading.local()  # one packed-argument buffer per thread
 
@@ -145,6 +150,18 @@ def lib(path: Optional[str] = None):
     for call, layout in enumerate(TREE_ARGS):
         if L.pa_tree_args_bytes(call) != layout.size:
             raise RuntimeError("the tree calls' argument structs differ from this binding's")
+    L.pa_kv_block_bytes_fp4.restype = sz
+    L.pa_kv_block_bytes_fp4.argtypes = [i, i, i]
+    L.pa_decode_fp4_workspace_bytes.restype = sz
+    L.pa_decode_fp4_workspace_bytes.argtypes = [i, i, i, i]
+    for f in (L.pa_cache_write_fp4, L.pa_cache_read_fp4, L.pa_decode_fp4, L.pa_qkv_rope_write):
+        f.restype = i
+        f.argtypes = [P]
+    L.pa_fp4_args_bytes.restype = sz
+    L.pa_fp4_args_bytes.argtypes = [i]
+    for call, layout in enumerate(FP4_ARGS):
+        if L.pa_fp4_args_bytes(call) != layout.size:
+            raise RuntimeError("the 4-bit calls' argument structs differ from this binding's")
     L.pa_error_check.restype = i
     L.pa_error_check.argtypes = [P]
     if path is None:
@@ -794,6 +811,255 @@ def pa_tree_accept(kv_cache: torch.Tensor, accepted: torch.Tensor, num_accepted:
     st = L.pa_tree_accept_packed(addr)
     if st:
         raise PaError(st, "pa_tree_accept_fp8" if dt is _U8 else "pa_tree_accept")
+
+
+def pa_kv_block_bytes_fp4(block_size: int, num_kv_heads: int, head_size: int) -> int:
+    return int(lib().pa_kv_block_bytes_fp4(block_size, num_kv_heads, head_size))
+
+
+def fp4_pool_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_size: int) -> tuple:
+    """Shape of a 4-bit pool (uint8): K's and V's tile of every (block, KV head)."""
+    return num_blocks, num_kv_heads, 2, block_size * head_size * 9 // 16
+
+
+def _fp4_args():
+    """This thread's buffer for the 4-bit calls' arguments, and its address."""
+    try:
+        return _tls.fp4
+    except AttributeError:
+        buf = ctypes.create_string_buffer(max(layout.size for layout in FP4_ARGS))
+        _tls.fp4 = (buf, ctypes.addressof(buf))
+        return _tls.fp4
+
+
+def _pool4_geom(kv_cache: torch.Tensor, head_size: int):
+    """Blocks, block size and KV heads of a 4-bit pool of heads of head_size."""
+    _need(kv_cache, "kv_cache", _U8, 4)
+    NB, Hkv, two, tile = kv_cache.shape
+    bs, rest = divmod(tile * 16, head_size * 9) if head_size > 0 else (0, 1)
+    if two != 2 or rest:
+        raise ValueError("kv_cache must be [num_blocks, num_kv_heads, 2, block_size * head_size "
+                         "* 9 / 16]")
+    return NB, bs, Hkv
+
+
+def _head_rows(t: torch.Tensor, name: str) -> int:
+    """Row stride of bf16 [rows, heads, D] whose rows may lie further apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [num_tokens, num_kv_heads, head_size]")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if d > 1 and s2 != 1 or h > 1 and s1 != d or n > 1 and s0 < h * d:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return s0 if n > 1 else h * d
+
+
+def _cache_fp4(where, k, v, kv_cache, slot_mapping, k_scale, v_scale, stream):
+    try:  # every tensor at once; on failure the per-argument checks name the culprit
+        dev = kv_cache.get_device()
+        NB, Hkv, two, tile = kv_cache.shape
+        N, heads, D = k.shape
+        bs, rest = divmod(tile * 16, D * 9)
+        stride = k.stride()
+        ok = (two == 2 and not rest and heads == Hkv and dev >= 0 and v.shape == k.shape
+              and kv_cache.dtype is _U8 and kv_cache.is_contiguous()
+              and k.dtype is _BF16 and k.get_device() == dev
+              and v.dtype is _BF16 and v.get_device() == dev
+              and stride == v.stride() and stride[2] == 1 and stride[1] == D
+              and (stride[0] >= heads * D or N <= 1)
+              and slot_mapping.shape == (N,) and slot_mapping.dtype is _I32
+              and slot_mapping.get_device() == dev and slot_mapping.is_contiguous())
+        stride = stride[0] if N > 1 else heads * D
+    except (AttributeError, TypeError, ValueError, ZeroDivisionError):
+        ok = False
+    if not ok:
+        stride = _head_rows(k, "K rows")
+        if _head_rows(v, "V rows") != stride:
+            raise ValueError("K and V rows must have one row stride")
+        _need(slot_mapping, "slot_mapping", _I32, 1)
+        N, heads, D = k.shape
+        NB, bs, Hkv = _pool4_geom(kv_cache, D)
+        dev = kv_cache.get_device()
+        _same_device(kv_cache, k, v, slot_mapping)
+        if v.shape != k.shape or heads != Hkv or slot_mapping.shape != (N,):
+            raise ValueError("K and V rows must be [num_tokens, num_kv_heads, head_size], "
+                             "slot_mapping [num_tokens]")
+    L = _lib if _lib is not None else lib()
+    buf, addr = _fp4_args()
+    FP4_ARGS[0].pack_into(buf, 0, kv_cache.data_ptr(), k.data_ptr(), v.data_ptr(),
+                          slot_mapping.data_ptr(), _launch_stream(stream, dev) or 0, stride, NB,
+                          bs, Hkv, D, N, k_scale, v_scale)
+    st = getattr(L, where)(addr)
+    if st:
+        raise PaError(st, where)
+
+
+def pa_cache_write_fp4(kv_cache: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                       slot_mapping: torch.Tensor, k_scale: float, v_scale: float,
+                       stream=None) -> None:
+    """Quantise bf16 k_new/v_new [N, Hkv, D] (rows may be strided, alike) into their slots [N] of
+    a 4-bit pool (see fp4_pool_shape)."""
+    _cache_fp4("pa_cache_write_fp4", k_new, v_new, kv_cache, slot_mapping, k_scale, v_scale,
+               stream)
+
+
+def pa_cache_read_fp4(k_out: torch.Tensor, v_out: torch.Tensor, kv_cache: torch.Tensor,
+                      slot_mapping: torch.Tensor, k_scale: float, v_scale: float,
+                      stream=None) -> None:
+    """The K and V rows in slots [N] of a 4-bit pool, in bf16, to k_out/v_out [N, Hkv, D] (rows
+    may be strided, alike); a negative slot leaves its row as it was."""
+    _cache_fp4("pa_cache_read_fp4", k_out, v_out, kv_cache, slot_mapping, k_scale, v_scale,
+               stream)
+
+
+def pa_decode_fp4_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int,
+                                  head_size: int) -> int:
+    return int(lib().pa_decode_fp4_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_size))
+
+
+def pa_decode_fp4(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor,
+                  block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                  scale: float, k_scale: float, v_scale: float, workspace: torch.Tensor,
+                  stream=None) -> None:
+    """Decode attention over a 4-bit pool: q/out [B, Hq, D], block_tables [B, MB], seq_lens
+    [B]."""
+    try:  # every tensor at once; on failure the per-argument checks name the culprit
+        dev = kv_cache.get_device()
+        NB, Hkv, two, tile = kv_cache.shape
+        B, Hq, D = qs = q.shape
+        bs, rest = divmod(tile * 16, D * 9)
+        tB, MB = block_tables.shape
+        ok = (two == 2 and not rest and tB == B and dev >= 0
+              and out.shape == qs and seq_lens.shape == (B,) and workspace.dim() == 1
+              and kv_cache.dtype is _U8 and kv_cache.is_contiguous()
+              and q.dtype is _BF16 and q.get_device() == dev and q.is_contiguous()
+              and out.dtype is _BF16 and out.get_device() == dev and out.is_contiguous()
+              and block_tables.dtype is _I32 and block_tables.get_device() == dev
+              and block_tables.is_contiguous()
+              and seq_lens.dtype is _I32 and seq_lens.get_device() == dev
+              and seq_lens.is_contiguous()
+              and workspace.dtype is _U8 and workspace.get_device() == dev
+              and workspace.is_contiguous())
+    except (AttributeError, TypeError, ValueError, ZeroDivisionError):
+        ok = False
+    if not ok:
+        _need(q, "q", _BF16, 3)
+        _need(out, "out", _BF16, 3)
+        _pool4_geom(kv_cache, q.shape[2])
+        _need(block_tables, "block_tables", _I32, 2)
+        _need(seq_lens, "seq_lens", _I32, 1)
+        _need(workspace, "workspace", _U8, 1)
+        _same_device(kv_cache, q, out, block_tables, seq_lens, workspace)
+        raise ValueError("inconsistent decode shapes")
+    L = _lib if _lib is not None else lib()
+    buf, addr = _fp4_args()
+    FP4_ARGS[1].pack_into(
+        buf, 0, out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _launch_stream(stream, dev) or 0, B, NB, bs, Hq, Hkv, D, MB, max_seq_len, scale, k_scale,
+        v_scale)
+    st = L.pa_decode_fp4(addr)
+    if st:
+        raise PaError(st, "pa_decode_fp4")
+
+
+def _rope_geom(q_out, kv_cache):
+    """Blocks, block size, KV heads and bits per element of any pool, by its type and rank."""
+    if kv_cache.dim() == 4:
+        return (*_pool4_geom(kv_cache, q_out.shape[2]), 4)
+    fp8 = kv_cache.dtype is _U8
+    NB, bs, Hkv, D = (_pool8_geom if fp8 else _pool_geom)(kv_cache)
+    if D != q_out.shape[2]:
+        raise ValueError("q_out and kv_cache must have one head_size")
+    return NB, bs, Hkv, 8 if fp8 else 16
+
+
+def pa_qkv_rope_write(q_out: torch.Tensor, qkv: torch.Tensor, kv_cache: torch.Tensor,
+                      slot_mapping: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                      q_weight: Optional[torch.Tensor] = None,
+                      k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      pair_axis: Optional[torch.Tensor] = None, interleaved: bool = False,
+                      kv_scales: Optional[tuple] = None, stream=None) -> None:
+    """Norms of q and k per head (q_weight/k_weight [D] bf16, or none), rotary positions, q to
+    q_out [N, Hq, D], K and V into their slots [N] of the pool, from the projection's rows qkv
+    [N, (Hq + 2 Hkv) * D] (rows may be strided).
+
+    positions [N] or [axes, N] int32; cos_sin [positions, rot_dim] fp32 (cosines, then sines);
+    pair_axis [rot_dim / 2] int32 names each pair's axis (needed for several).  The pool is bf16
+    or uint8 FP8 [blocks, 2, Hkv, bs, D], or 4-bit (see fp4_pool_shape); the latter two need
+    kv_scales = (k_scale, v_scale)."""
+    try:  # every tensor at once; on failure the per-argument checks name the culprit
+        dev = kv_cache.get_device()
+        N, Hq, D = q_out.shape
+        NB, bs, Hkv, bits = _rope_geom(q_out, kv_cache)
+        axes, cols = positions.shape if positions.dim() == 2 else (1, positions.shape[0])
+        max_pos, rot = cos_sin.shape
+        rows, width = qkv.shape
+        s0, s1 = qkv.stride()
+        ok = (dev >= 0 and rows == N and cols == N and width == (Hq + 2 * Hkv) * D and s1 == 1
+              and (s0 >= width or N <= 1)
+              and slot_mapping.shape == (N,)
+              and q_out.dtype is _BF16 and q_out.get_device() == dev and q_out.is_contiguous()
+              and qkv.dtype is _BF16 and qkv.get_device() == dev
+              and slot_mapping.dtype is _I32 and slot_mapping.get_device() == dev
+              and slot_mapping.is_contiguous()
+              and positions.dtype is _I32 and positions.get_device() == dev
+              and positions.is_contiguous()
+              and cos_sin.dtype is _F32 and cos_sin.get_device() == dev
+              and cos_sin.is_contiguous()
+              and (axes == 1 or pair_axis is not None))
+        qw = kw = pa = 0
+        for w in (q_weight, k_weight):
+            ok = ok and (w is None or w.shape == (D,) and w.dtype is _BF16
+                         and w.get_device() == dev and w.is_contiguous())
+        if q_weight is not None:
+            qw = q_weight.data_ptr()
+        if k_weight is not None:
+            kw = k_weight.data_ptr()
+        if pair_axis is not None:
+            ok = ok and (pair_axis.shape == (rot // 2,) and pair_axis.dtype is _I32
+                         and pair_axis.get_device() == dev and pair_axis.is_contiguous())
+            pa = pair_axis.data_ptr()
+        if N <= 1:
+            s0 = width
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        _need(q_out, "q_out", _BF16, 3)
+        if not isinstance(kv_cache, torch.Tensor):
+            raise ValueError("kv_cache must be a CUDA tensor")
+        _rope_geom(q_out, kv_cache)
+        _need(slot_mapping, "slot_mapping", _I32, 1)
+        _need(positions, "positions", _I32)
+        _need(cos_sin, "cos_sin", _F32, 2)
+        for t, name, dtype in ((q_weight, "q_weight", _BF16), (k_weight, "k_weight", _BF16),
+                               (pair_axis, "pair_axis", _I32)):
+            if t is not None:
+                _need(t, name, dtype, 1)
+        if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda or qkv.dtype is not _BF16:
+            raise ValueError(f"qkv must be a CUDA tensor of {_BF16}")
+        _same_device(kv_cache, q_out, qkv, slot_mapping, positions, cos_sin, q_weight, k_weight,
+                     pair_axis)
+        raise ValueError("inconsistent shapes: qkv [N, (Hq + 2 Hkv) * D] of contiguous rows, "
+                         "positions [N] or [axes, N] (several axes need pair_axis [rot_dim / 2]), "
+                         "cos_sin [positions, rot_dim], weights [D]")
+    ks, vs = kv_scales if bits != 16 and kv_scales is not None else (1.0, 1.0)
+    if bits != 16 and kv_scales is None:
+        raise ValueError("an FP8 or 4-bit pool needs kv_scales=(k_scale, v_scale)")
+    L = _lib if _lib is not None else lib()
+    buf, addr = _fp4_args()
+    FP4_ARGS[2].pack_into(
+        buf, 0, q_out.data_ptr(), kv_cache.data_ptr(), qkv.data_ptr(), qw, kw,
+        cos_sin.data_ptr(), positions.data_ptr(), pa, slot_mapping.data_ptr(),
+        _launch_stream(stream, dev) or 0, s0, N, NB, bs, Hq, Hkv, D, rot, max_pos, axes,
+        bool(interleaved), bits, eps, ks, vs)
+    st = L.pa_qkv_rope_write(addr)
+    if st:
+        raise PaError(st, "pa_qkv_rope_write")
 
 
 def pa_error_check(stream=None) -> None:

@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
 SOURCES = ["pa_api.cu", "pa_cache_write.cu", "pa_attention.cu",
            "pa_decode_noalloc.cu", "pa_tree_attention.cu", "pa_tree_verify.cu",
-           "pa_tree_accept.cu"]
+           "pa_tree_accept.cu", "pa_cache_fp4.cu", "pa_decode_fp4.cu", "pa_qkv_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -893,6 +893,149 @@ size_t pa_tree_args_bytes(int call) {
                        : 0;
 }
 
+size_t pa_kv_block_bytes_fp4(int block_size, int num_kv_heads, int head_size) {
+    if (block_size <= 0 || num_kv_heads <= 0 || head_size <= 0 || head_size % 16 != 0) return 0;
+    return (size_t)2 * (size_t)block_size * (size_t)num_kv_heads * ((size_t)head_size / 16 * 9);
+}
+
+// check_pool without its bound on the rows, which is that of a TMA map's row coordinate: the
+// 4-bit pool is addressed in bytes.
+static pa_status check_pool_fp4(const void *kv_cache, int num_blocks, int block_size,
+                                int num_kv_heads, int head_size) {
+    const pa_status st = check_pool(kv_cache, num_blocks > 0 ? 1 : num_blocks, block_size,
+                                    num_kv_heads, head_size);
+    if (st != PA_OK) return st;
+    return (long long)num_blocks * block_size < (1LL << 31) ? PA_OK : PA_ERR_UNSUPPORTED;
+}
+
+// A tensor's scale whose largest element, 6 * 448 scales, is finite.
+static bool good_scale_fp4(float s) { return good_scale(s) && s * 2688.f < 3.4e38f; }
+
+static pa_status cache_fp4_impl(const pa_cache_fp4_args *a, bool write) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    const pa_status st = check_pool_fp4(a->kv_cache, a->num_blocks, a->block_size,
+                                        a->num_kv_heads, a->head_size);
+    if (st != PA_OK) return st;
+    if (a->num_tokens < 0 || !good_scale_fp4(a->k_scale) || !good_scale_fp4(a->v_scale))
+        return PA_ERR_INVALID_ARG;
+    if (a->num_tokens == 0) return PA_OK;
+    if (!a->k_rows || !a->v_rows || !a->slot_mapping || !aligned(a->k_rows, 16) ||
+        !aligned(a->v_rows, 16) || !aligned(a->slot_mapping, 4))
+        return PA_ERR_INVALID_ARG;
+    if (a->row_stride < (int64_t)a->num_kv_heads * a->head_size || a->row_stride % 8 != 0)
+        return PA_ERR_INVALID_ARG;
+    const pa::KvGeom g{a->num_blocks, a->block_size, a->num_kv_heads, a->head_size};
+    return from_cuda(pa::launch_cache_fp4(write, a->kv_cache, g, a->k_rows, a->v_rows,
+                                          a->row_stride, a->slot_mapping, a->num_tokens,
+                                          a->k_scale, a->v_scale,
+                                          reinterpret_cast<cudaStream_t>(a->stream)));
+}
+
+pa_status pa_cache_write_fp4(const pa_cache_fp4_args *args) { return cache_fp4_impl(args, true); }
+
+pa_status pa_cache_read_fp4(const pa_cache_fp4_args *args) { return cache_fp4_impl(args, false); }
+
+size_t pa_decode_fp4_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                     int head_size) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || check_heads(num_heads, num_kv_heads) != PA_OK)
+        return 0;
+    if (head_size != 64 && head_size != 128) return 0;
+    return pa::decode_fp4_workspace_bytes(head_size, pa::device_sm_count());
+}
+
+pa_status pa_decode_fp4(const pa_decode_fp4_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    pa_status st = check_pool_fp4(a->kv_cache, a->num_blocks, a->block_size, a->num_kv_heads,
+                                  a->head_size);
+    if (st != PA_OK) return st;
+    if ((st = check_heads(a->num_heads, a->num_kv_heads)) != PA_OK) return st;
+    if (a->num_seqs < 0 || a->max_seq_len < 0 || a->max_blocks_per_seq <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!(a->scale == a->scale) || a->scale > 3.0e38f || a->scale < -3.0e38f)
+        return PA_ERR_INVALID_ARG;
+    if (!good_scale_fp4(a->k_scale) || !good_scale_fp4(a->v_scale)) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs == 0) return PA_OK;
+    if (!a->out || !a->q || !a->block_tables || !a->seq_lens || !aligned(a->out, 16) ||
+        !aligned(a->q, 16) || !aligned(a->block_tables, 4) || !aligned(a->seq_lens, 4))
+        return PA_ERR_INVALID_ARG;
+    if (a->max_seq_len > (long long)a->max_blocks_per_seq * a->block_size)
+        return PA_ERR_INVALID_ARG;
+    // Units of work over (sequence, KV head) fit 31 bits.
+    if ((long long)a->num_seqs * a->num_kv_heads * ((a->max_seq_len + 31LL) / 32 + 1) >=
+        (1LL << 31))
+        return PA_ERR_UNSUPPORTED;
+    const size_t need = pa::decode_fp4_workspace_bytes(a->head_size, pa::device_sm_count());
+    if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < need)
+        return PA_ERR_WORKSPACE;
+    const pa::KvGeom g{a->num_blocks, a->block_size, a->num_kv_heads, a->head_size};
+    return from_cuda(pa::launch_decode_fp4(a->out, a->q, a->kv_cache, g, a->num_heads,
+                                           a->block_tables, a->max_blocks_per_seq, a->seq_lens,
+                                           a->num_seqs, a->max_seq_len, a->scale, a->k_scale,
+                                           a->v_scale, a->workspace,
+                                           reinterpret_cast<cudaStream_t>(a->stream)));
+}
+
+pa_status pa_qkv_rope_write(const pa_qkv_rope_write_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    if (a->kv_bits != 16 && a->kv_bits != 8 && a->kv_bits != 4) return PA_ERR_INVALID_ARG;
+    // The kernel addresses every pool with 64-bit offsets.
+    pa_status st = check_pool_fp4(a->kv_cache, a->num_blocks, a->block_size, a->num_kv_heads,
+                                  a->head_size);
+    if (st != PA_OK) return st;
+    if ((st = check_heads(a->num_heads, a->num_kv_heads)) != PA_OK) return st;
+    if (a->num_tokens < 0 || a->max_position <= 0 || a->rot_dim <= 0 || a->num_axes <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (a->rot_dim % 16 != 0 || a->rot_dim > a->head_size || a->num_axes > 8)
+        return PA_ERR_UNSUPPORTED;
+    if ((a->q_weight || a->k_weight) && !(a->eps >= 0.f && a->eps < 3.0e38f))
+        return PA_ERR_INVALID_ARG;
+    if (a->kv_bits == 8 && (!good_scale(a->k_scale) || !good_scale(a->v_scale)))
+        return PA_ERR_INVALID_ARG;
+    if (a->kv_bits == 4 && (!good_scale_fp4(a->k_scale) || !good_scale_fp4(a->v_scale)))
+        return PA_ERR_INVALID_ARG;
+    if (a->num_tokens == 0) return PA_OK;
+    if (!a->q_out || !a->qkv || !a->cos_sin || !a->positions || !a->slot_mapping ||
+        (a->num_axes > 1 && !a->pair_axis) || !aligned(a->q_out, 16) || !aligned(a->qkv, 16) ||
+        !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16) || !aligned(a->cos_sin, 4) ||
+        !aligned(a->positions, 4) || !aligned(a->pair_axis, 4) || !aligned(a->slot_mapping, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t width = ((int64_t)a->num_heads + 2 * (int64_t)a->num_kv_heads) * a->head_size;
+    if (a->row_stride < width || a->row_stride % 8 != 0) return PA_ERR_INVALID_ARG;
+    pa::QkvRopeArgs r;
+    r.q_out = a->q_out;
+    r.kv = a->kv_cache;
+    r.qkv = static_cast<const uint16_t *>(a->qkv);
+    r.q_weight = a->q_weight;
+    r.k_weight = a->k_weight;
+    r.cos_sin = a->cos_sin;
+    r.positions = a->positions;
+    r.pair_axis = a->pair_axis;
+    r.slots = a->slot_mapping;
+    r.row_stride = a->row_stride;
+    r.num_tokens = a->num_tokens;
+    r.num_blocks = a->num_blocks;
+    r.block_size = a->block_size;
+    r.num_heads = a->num_heads;
+    r.num_kv_heads = a->num_kv_heads;
+    r.rot_dim = a->rot_dim;
+    r.max_position = a->max_position;
+    r.num_axes = a->num_axes;
+    r.interleaved = a->interleaved;
+    r.eps = a->eps;
+    r.k_scale = a->k_scale;
+    r.v_scale = a->v_scale;
+    r.chunks = 1;
+    return from_cuda(pa::launch_qkv_rope(r, a->head_size, a->kv_bits,
+                                         reinterpret_cast<cudaStream_t>(a->stream)));
+}
+
+size_t pa_fp4_args_bytes(int call) {
+    return call == 0   ? sizeof(pa_cache_fp4_args)
+           : call == 1 ? sizeof(pa_decode_fp4_args)
+           : call == 2 ? sizeof(pa_qkv_rope_write_args)
+                       : 0;
+}
+
 pa_status pa_error_check(pa_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return PA_ERR_CUDA;
@@ -908,6 +1051,12 @@ pa_status pa_error_check(pa_stream_t stream) {
     if (pa::take_error_tree_verify(&b) != cudaSuccess) return PA_ERR_CUDA;
     bits |= b;
     if (pa::take_error_tree_accept(&b) != cudaSuccess) return PA_ERR_CUDA;
+    bits |= b;
+    if (pa::take_error_cache_fp4(&b) != cudaSuccess) return PA_ERR_CUDA;
+    bits |= b;
+    if (pa::take_error_decode_fp4(&b) != cudaSuccess) return PA_ERR_CUDA;
+    bits |= b;
+    if (pa::take_error_qkv_rope(&b) != cudaSuccess) return PA_ERR_CUDA;
     bits |= b;
     if (bits & 2u) return PA_ERR_TIMEOUT;
     if (bits & 1u) return PA_ERR_OOB;

@@ -1,0 +1,97 @@
+// pa_fp4.cuh - the 4-bit pool: where a row lies, and how elements become codes and back.
+//
+// A pool is uint8 [num_blocks][num_kv_heads][2][tile]: K, then V, of one (block, head), each
+// tile = block_size rows of head_size / 2 bytes (element 2i is the low nibble of byte i, an OCP
+// e2m1 code), then block_size rows of head_size / 16 e4m3 scales, one per 16 elements.  An
+// element is code * scale * g, g the tensor's k_scale or v_scale.  K and V of a (block, head)
+// are one run of block_size * head_size * 9 / 8 bytes, which one bulk copy fetches.
+#pragma once
+
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+constexpr int kFp4Group = 16;  // elements that share a scale
+
+struct Fp4Row {
+    int64_t codes, scale;  // byte offsets of a row's codes and of its scales
+};
+
+template <int D>
+__device__ __forceinline__ Fp4Row fp4_row(int blk, int off, int head, int side, int num_kv_heads,
+                                          int block_size) {
+    const int tile = block_size * (D * 9 / 16);
+    const int64_t base = (((int64_t)blk * num_kv_heads + head) * 2 + side) * tile;
+    return {base + off * (D / 2), base + block_size * (D / 2) + off * (D / 16)};
+}
+
+// Two fp32 values to two e2m1 codes (nearest, ties to the even code, saturating at 6), lo in
+// the low nibble of the result's byte.
+__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
+        "mov.b32 %0, {b, 0, 0, 0};\n\t}"
+        : "=r"(r)
+        : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Eight e2m1 codes (the nibbles of w, lowest first) to four f16x2 words, exactly.
+__device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+}
+
+// Two e4m3 codes (the low bytes of w) to f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// max(|a|, |b|) of bf16 pairs, NaN if either is.
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+    return r;
+}
+
+// Sixteen bf16 elements (x[0] holds the first two) to their scale's e4m3 code (returned) and
+// e2m1 codes:  s = e4m3(max|x| / h), h = fp32(6 g);  d = fp32(s g);  code = e2m1(x / d), all
+// divisions binary32's, roundings to nearest even, saturating.  A group whose d is not above 0
+// (max|x| too small for a scale, or a NaN) has codes of 0; with a NaN its scale is NaN too, so
+// that all its elements are.
+__device__ __forceinline__ uint32_t fp4_quantise(const uint32_t (&x)[8], float g, float h,
+                                                 uint2 &codes) {
+    uint32_t m = absmax_bf16x2(x[0], x[1]);
+#pragma unroll
+    for (int i = 2; i < 8; ++i) m = absmax_bf16x2(m, x[i]);
+    m = absmax_bf16x2(m, m >> 16);
+    const uint32_t s = pack_e4m3x2(__fdiv_rn(bf16_lo(m), h), 0.f) & 0xffu;
+    const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s)), g);
+    uint32_t c[2] = {0u, 0u};
+    if (d > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            c[i >> 2] |= pack_e2m1x2(__fdiv_rn(bf16_lo(x[i]), d), __fdiv_rn(bf16_hi(x[i]), d))
+                         << (8 * (i & 3));
+    }
+    codes = make_uint2(c[0], c[1]);
+    return s;
+}
+
+}  // namespace pa

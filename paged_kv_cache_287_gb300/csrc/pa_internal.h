@@ -47,6 +47,9 @@ cudaError_t take_error_prefill(unsigned *bits);
 cudaError_t take_error_tree_attention(unsigned *bits);
 cudaError_t take_error_tree_verify(unsigned *bits);
 cudaError_t take_error_tree_accept(unsigned *bits);
+cudaError_t take_error_cache_fp4(unsigned *bits);
+cudaError_t take_error_decode_fp4(unsigned *bits);
+cudaError_t take_error_qkv_rope(unsigned *bits);
 
 // Encode a 2-D TMA map over the pool viewed as rows of head_size bf16 elements,
 // box = 64 elements x box_rows rows, 128-byte swizzle.  False on failure.  Maps
@@ -214,5 +217,30 @@ cudaError_t launch_tree_accept(void *kv_cache, const KvGeom &g, int elem_bytes,
                                const TreeGeom &t, const int32_t *block_tables,
                                int max_blocks_per_seq, const int32_t *seq_lens,
                                int32_t *new_seq_lens, cudaStream_t stream);
+
+// 4-bit pools (pa_fp4.cuh).  Rows into their slots (write) or out of them.
+cudaError_t launch_cache_fp4(bool write, void *kv_cache, const KvGeom &g, void *k_rows,
+                             void *v_rows, int64_t row_stride, const int32_t *slots,
+                             int num_tokens, float k_scale, float v_scale, cudaStream_t stream);
+size_t decode_fp4_workspace_bytes(int head_size, int sm_count);
+cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, const KvGeom &g,
+                              int num_heads, const int32_t *block_tables, int max_blocks_per_seq,
+                              const int32_t *seq_lens, int num_seqs, int max_seq_len, float scale,
+                              float k_scale, float v_scale, void *workspace, cudaStream_t stream);
+
+// The arguments of pa_qkv_rope_write, as its kernel takes them.
+struct QkvRopeArgs {
+    void *q_out, *kv;
+    const uint16_t *qkv;  // bf16 rows, row_stride elements apart
+    const void *q_weight, *k_weight;  // [head_size] bf16, or null: no norm
+    const float *cos_sin;             // [max_position][rot_dim]: cosines, then sines
+    const int32_t *positions, *pair_axis, *slots;
+    int64_t row_stride;
+    int num_tokens, num_blocks, block_size, num_heads, num_kv_heads;
+    int rot_dim, max_position, num_axes, interleaved;
+    float eps, k_scale, v_scale;
+    int chunks;  // warps that share a token's heads (set by the launch)
+};
+cudaError_t launch_qkv_rope(QkvRopeArgs a, int head_size, int kv_bits, cudaStream_t stream);
 
 }  // namespace pa
