@@ -964,6 +964,7 @@ pa_status pa_decode_fp4(const pa_decode_fp4_args *a) {
     if ((long long)a->num_seqs * a->num_kv_heads * ((a->max_seq_len + 31LL) / 32 + 1) >=
         (1LL << 31))
         return PA_ERR_UNSUPPORTED;
+    if (a->num_seqs > pa::decode_fp4_max_seqs(a->head_size)) return PA_ERR_UNSUPPORTED;
     const size_t need = pa::decode_fp4_workspace_bytes(a->head_size, pa::device_sm_count());
     if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < need)
         return PA_ERR_WORKSPACE;

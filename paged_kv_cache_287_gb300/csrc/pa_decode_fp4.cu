@@ -1,4 +1,27 @@
 // pa_decode_fp4.cu - decode attention over a 4-bit pool: one query token per sequence.
+//
+//   out[s][h] = v_scale sum_t P[t] (code s)_V[t] / sum_t P[t],
+//   P[t] = 2^(scale log2(e) k_scale q.(code s)_K[t] - m), m a running reference
+//
+// Bound by HBM: 9/16 of a byte per element, read once.  At that rate an SM meets some 43
+// elements a clock, so the work per element must stay below three instructions, and the layout
+// is chosen for that:
+//   * Tiles of 32 tokens of one (sequence, KV head): K and V, codes and scales, of a block are
+//     one run of memory and arrive by one bulk copy.  Every warp has a ring of tiles of its own
+//     and no warp waits for another in the loop.
+//   * S^T = K.Q^T by m16n8k16 (16 tokens x 8 query heads): a lane reads 32 dims (16 bytes) of
+//     its token at once; which of the MMA's k-slots a dim takes is free, so the query's
+//     fragments are laid out to match (32 consecutive dims a lane).  A byte of codes becomes an
+//     f16x2 by one conversion, times its scale by one multiplication, both exact.
+//   * O^T += V^T.P^T: MMA row g stands for dims 16 g .. 16 g + 15 over the m-tiles, so a lane's
+//     dims share one scale per token; two tokens' nibbles are interleaved (two shifts and two
+//     selects per 16 codes), and the conversion then gives pairs of tokens.  A lane ends with 16
+//     consecutive dims of two heads and stores them as they are.
+//   * Row r of a tile's 8 tokens is token r ^ ((r >> 1) & 1): without it the four tokens that a
+//     load of V takes would lie in the same banks.
+// The tiles of all (sequence, KV head) segments are one list, cut into equal ranges, one per
+// CTA and within it one per warp.  Pieces of a segment in one CTA are merged in shared memory,
+// those in several CTAs by a second kernel (a record per CTA and end of its range).
 #include <algorithm>
 #include <atomic>
 
@@ -11,102 +34,631 @@ namespace {
 __device__ unsigned g_err_decode_fp4;
 std::atomic<bool> g_launched{false};
 
+constexpr int kTokens = 32;  // of a tile
+constexpr int kWarps = 16;   // one CTA per SM
+constexpr int kHeads = 8;    // query heads per KV head, padded to the MMA's N
+// m is only raised when a score exceeds it by more than this (log2 units): P stays below 2^8.
+constexpr float kSlack = 8.f;
+constexpr float kLowest = -3.4028235e38f;  // m before the first score
+
+template <int D>
+constexpr int kStageBytes = kTokens *D * 9 / 8;
+template <int D>
+constexpr int kRecFloats = kHeads * (D + 2);  // acc [8][D], then (m, l) [8]
+// Tiles in flight per warp: 147 KB in flight per SM.
+template <int D>
+constexpr int kMaxStages = 256 / D;
+
 struct Args {
     __nv_bfloat16 *out;
     const __nv_bfloat16 *q;
     const uint8_t *kv;
     const int32_t *block_tables, *seq_lens;
-    int num_heads, num_kv_heads, group, block_size, max_blocks, num_blocks, max_seq_len;
-    float scale_log2, k_scale, v_scale;
+    float *recs;  // [CTAs][2][kRecFloats]: a segment's piece at the range's start, at its end
+    int4 *meta;   // [CTAs]: piece at the start, it ends here, piece at the end, its segment
+    int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, max_seq_len;
+    int stages;
+    int aligned;  // CTA c is segment c: no piece leaves its CTA
+    float scale_log2, v_scale;  // scale * log2(e) * k_scale
 };
 
-// A CTA per (sequence, KV head), eight warps that take every eighth token.
+// What a warp leaves for the merge in its CTA: a piece whose segment began before its range
+// (a), whether it ended there, and one that began in its range and goes on (b).
+struct WarpPieces {
+    int a, a_ends, b, b_seg;
+};
+
+__device__ __forceinline__ int clamped_len(const Args &a, int s) {
+    const int len = a.seq_lens[s];
+    return len < 0 ? 0 : (len > a.max_seq_len ? a.max_seq_len : len);
+}
+
+// 16 (D 128) or 8 consecutive dims of one head: acc[mt][e] and acc[mt][e + 2] are dims 2 mt and
+// 2 mt + 1 of them.
 template <int D>
-__global__ void __launch_bounds__(256) decode_fp4_kernel(const Args a) {
+__device__ __forceinline__ void store_rows(__nv_bfloat16 *dst, const float (&acc)[D / 16][4],
+                                           int e, float f) {
+    uint32_t w[D / 16];
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) w[mt] = pack_bf16(acc[mt][e] * f, acc[mt][e + 2] * f);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+        reinterpret_cast<uint4 *>(dst)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+template <int D>
+__device__ __forceinline__ void store_rec(float *rec, const float (&acc)[D / 16][4], int lane,
+                                          float m0, float l0, float m1, float l1) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        float4 *dst = reinterpret_cast<float4 *>(rec + (2 * c + e) * D + g * (D / 8));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            dst[i] = make_float4(acc[2 * i][e], acc[2 * i][e + 2], acc[2 * i + 1][e],
+                                 acc[2 * i + 1][e + 2]);
+    }
+    if (g == 0)
+        *reinterpret_cast<float4 *>(rec + kHeads * D + 4 * c) = make_float4(m0, l0, m1, l1);
+}
+
+template <int D, int BS>
+__global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a) {
+    constexpr int kStage = kStageBytes<D>, kRec = kRecFloats<D>;
+    constexpr int kTile = BS * D * 9 / 16;      // K's (or V's) bytes of a (block, head)
+    constexpr int kNB = kTokens / BS;           // blocks of a tile
+    constexpr int kRow = D / 2, kScRow = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int S = a.stages;
+    uint8_t *ring = smem;
+    float *recs = reinterpret_cast<float *>(ring + kWarps * S * kStage);
+    int4 *descs = reinterpret_cast<int4 *>(recs + kWarps * kRec);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(descs + kWarps * S);
+    WarpPieces *pieces = reinterpret_cast<WarpPieces *>(bars + kWarps * S);
+    int *sums = reinterpret_cast<int *>(pieces + kWarps);
+    int *pre = sums + kWarps;  // [num_seqs + 1], not aligned mode
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, c = lane & 3;
+    const int B = a.num_seqs, Hkv = a.num_kv_heads, G = a.group;
+    uint64_t *bar = bars + warp * S;
+    int4 *desc = descs + warp * S;
+    uint8_t *stages = ring + warp * S * kStage;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 1);
+        fence_barrier_init();
+        pieces[warp] = {0, 0, 0, 0};
+    }
+    __syncwarp();
     pdl_begin();
-    constexpr int E = D / 32;  // elements per lane
-    __shared__ float s_acc[8][8][D];
-    __shared__ float s_m[8][8], s_l[8][8];
-    const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
-    const int cap = min(a.max_seq_len, a.max_blocks * a.block_size);
-    int len = a.seq_lens[s];
-    if (len < 0 || len > cap) {
-        atomicOr(&g_err_decode_fp4, kErrOob);
-        len = len < 0 ? 0 : cap;
-    }
-    const __nv_bfloat16 *q = a.q + ((size_t)s * a.num_heads + (size_t)h * G) * D;
-    float acc[8][E], qv[8][E], m[8], l[8];
+
+    // This warp's tiles [t0, t1) of the list (aligned mode: of its CTA's segment).
+    int t0, t1, active;  // active: warps of this CTA with tiles
+    {
+        int r0, r1;
+        if (a.aligned) {
+            const int s = blockIdx.x / Hkv;
+            if (tid == 0) {
+                const int len = a.seq_lens[s];
+                if (len < 0 || len > a.max_seq_len) atomicOr(&g_err_decode_fp4, kErrOob);
+            }
+            r0 = 0;
+            r1 = (clamped_len(a, s) + kTokens - 1) / kTokens;
+        } else {
+            const int per = (B + kWarps * 32 - 1) / (kWarps * 32);
+            for (int s = tid; s < B; s += kWarps * 32) {
+                const int len = a.seq_lens[s];
+                if (len < 0 || len > a.max_seq_len) atomicOr(&g_err_decode_fp4, kErrOob);
+                pre[s] = (clamped_len(a, s) + kTokens - 1) / kTokens;
+            }
+            __syncthreads();
+            int sum = 0;
+            for (int i = tid * per; i < min(B, (tid + 1) * per); ++i) sum += pre[i];
+            int v = sum;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-        m[g] = -3.4028235e38f;
-        l[g] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            acc[g][e] = 0.f;
-            qv[g][e] = g < G ? __bfloat162float(q[g * D + lane * E + e]) : 0.f;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (lane == 31) sums[warp] = v;
+            __syncthreads();
+            int run = v - sum;
+            for (int w = 0; w < warp; ++w) run += sums[w];
+            for (int i = tid * per; i < min(B, (tid + 1) * per); ++i) {
+                const int n = pre[i];
+                pre[i] = run;
+                run += n;
+            }
+            if (tid == kWarps * 32 - 1) pre[B] = run;
+            __syncthreads();
+            const long long T = (long long)pre[B] * Hkv;
+            // With fewer tiles than CTAs the first T take one each: no range before another's
+            // is empty, so a segment's pieces are those of consecutive CTAs.
+            const long long ctas = T < gridDim.x ? T : gridDim.x;
+            r0 = blockIdx.x < ctas ? (int)(T * blockIdx.x / ctas) : 0;
+            r1 = blockIdx.x < ctas ? (int)(T * (blockIdx.x + 1) / ctas) : 0;
         }
+        const int n = r1 - r0;
+        active = min(n, kWarps);
+        t0 = warp < active ? r0 + (int)((long long)n * warp / active) : r0;
+        t1 = warp < active ? r0 + (int)((long long)n * (warp + 1) / active) : r0;
     }
-    auto element = [&](const Fp4Row &row, int e) {
-        const int d = lane * E + e;
-        const uint32_t byte = a.kv[row.codes + d / 2];
-        uint32_t f[4];
-        e2m1x8_to_f16x8(byte, f);
-        const float c = d & 1 ? f16_hi(f[0]) : f16_lo(f[0]);
-        return c * f16_lo(e4m3x2_to_f16x2(a.kv[row.scale + d / kFp4Group]));
+
+    // Rows of sequences without tokens.
+    for (int s = a.aligned ? blockIdx.x / Hkv : blockIdx.x; s < B;
+         s += a.aligned ? B : gridDim.x) {
+        if (a.aligned ? active > 0 : pre[s + 1] != pre[s]) continue;
+        const int rows = a.aligned ? G : a.num_heads;
+        uint4 *dst = reinterpret_cast<uint4 *>(
+            a.out + ((size_t)s * a.num_heads + (a.aligned ? blockIdx.x % Hkv * G : 0)) * D);
+        for (int i = tid; i < rows * (D / 8); i += kWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
+    }
+
+    // Tile t0 + 32 k + lane: its segment, place, tokens, and blocks.
+    struct Tile {
+        int4 d;  // (sequence << 8 | head), tile of the segment, tokens, whether it is the last
+        int ids[kNB];
     };
-    for (int t = warp; t < len; t += 8) {
-        const int blk = a.block_tables[(size_t)s * a.max_blocks + t / a.block_size];
-        const bool oob = blk < 0 || blk >= a.num_blocks;
-        if (oob) atomicOr(&g_err_decode_fp4, kErrOob);
-        const Fp4Row kr =
-            fp4_row<D>(oob ? 0 : blk, t % a.block_size, h, 0, a.num_kv_heads, a.block_size);
-        const Fp4Row vr =
-            fp4_row<D>(oob ? 0 : blk, t % a.block_size, h, 1, a.num_kv_heads, a.block_size);
-        float k[E], v[E];
+    const int n = t1 - t0;
+    auto describe = [&](int k) {
+        Tile t;
+        t.d = make_int4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            k[e] = oob ? 0.f : element(kr, e);
-            v[e] = oob ? 0.f : element(vr, e);
+        for (int b = 0; b < kNB; ++b) t.ids[b] = 0;
+        const int x = t0 + 32 * k + lane;
+        if (x >= t1) return t;
+        int s, h, j;
+        if (a.aligned) {
+            s = blockIdx.x / Hkv;
+            h = blockIdx.x - s * Hkv;
+            j = x;
+        } else {
+            int lo = 0, hi = B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (Hkv * pre[mid] <= x) lo = mid; else hi = mid - 1;
+            }
+            s = lo;
+            const int nt = pre[s + 1] - pre[s], r = x - Hkv * pre[s];
+            h = r / nt;
+            j = r - h * nt;
         }
+        const int left = clamped_len(a, s) - j * kTokens;
+        t.d = make_int4(s << 8 | h, j, min(left, kTokens), left <= kTokens);
+        const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks + j * kNB;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            if (g >= G) break;
-            float x = 0.f;
+        for (int b = 0; b < kNB; ++b)
+            if (b * BS < t.d.z) t.ids[b] = bt[b];
+        return t;
+    };
+    Tile tile = describe(0), next_tile = tile;
+    const uint64_t policy = policy_evict_first();
+
+    // Called by the whole warp, for i in order; lane i & 31 issues.
+    auto issue = [&](int i, int st) {
+        if ((i & 31) == 16 && (i | 31) + 1 < n) next_tile = describe((i >> 5) + 1);
+        if ((i & 31) == 0 && i > 0) tile = next_tile;
+        if (lane == (i & 31)) {
+            uint8_t *dst = stages + st * kStage;
+            desc[st] = tile.d;
+            const int blocks = (tile.d.z + BS - 1) / BS;
+            uint32_t bytes = 0;
+            bool ok[kNB];
 #pragma unroll
-            for (int e = 0; e < E; ++e) x += qv[g][e] * k[e];
+            for (int b = 0; b < kNB; ++b) {
+                ok[b] = b < blocks && tile.ids[b] >= 0 && tile.ids[b] < a.num_blocks;
+                if (ok[b]) bytes += 2 * kTile;
+                if (b < blocks && !ok[b]) {  // its tokens read as zeros
+                    atomicOr(&g_err_decode_fp4, kErrOob);
+                    for (int e = 0; e < 2 * kTile; e += 16)
+                        *reinterpret_cast<uint4 *>(dst + b * 2 * kTile + e) =
+                            make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&bar[st], bytes);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            x *= a.scale_log2 * a.k_scale;
-            const float mn = fmaxf(m[g], x), c = fast_exp2(m[g] - mn), p = fast_exp2(x - mn);
-            m[g] = mn;
-            l[g] = l[g] * c + p;
+            for (int b = 0; b < kNB; ++b)
+                if (ok[b])
+                    bulk_load_hint(dst + b * 2 * kTile,
+                                   a.kv + ((int64_t)tile.ids[b] * Hkv + (tile.d.x & 255)) *
+                                              (2 * kTile),
+                                   2 * kTile, &bar[st], policy);
+        }
+        __syncwarp();
+    };
+    for (int i = 0; i < min(n, S); ++i) issue(i, i);
+
+    float acc[D / 16][4];
+    uint32_t qf[D / 16][2];
+    float cs0 = 0.f, cs1 = 0.f, m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+    int seg = -1, first_j = 0;
+    // Offsets of 8-token group j's first row, and of this lane's rows: K's row g is token rk of
+    // the group, V's k-slots 2c and 2c + 1 are tokens rv and rv ^ 1.
+    auto codes_at = [](int j) { return 8 * j / BS * 2 * kTile + 8 * j % BS * kRow; };
+    auto scales_at = [](int j) { return 8 * j / BS * 2 * kTile + BS * kRow + 8 * j % BS * kScRow; };
+    const int rk = g ^ ((g >> 1) & 1), rv = 2 * c + (c & 1);
+    const int tok_v0 = rv, tok_v1 = rv ^ 1;
+
+    int st = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], phase))) {
+            // Give the copies in flight their time to land, and leave no piece.
+            if (lane == 0) atomicOr(&g_err_decode_fp4, kErrTimeout);
+            for (int k = 1; k < S && i + k < n; ++k)
+                mbar_wait_bounded(&bar[(st + k) % S], phase ^ (st + k >= S ? 1u : 0u));
+            break;
+        }
+        const uint8_t *buf = stages + st * kStage;
+        const int4 d = desc[st];
+        const int valid = d.z;
+        if (d.x != seg) {
+            // A new segment: its query heads, scaled by powers of two into [1, 2) at their
+            // largest element.
+            seg = d.x;
+            first_j = d.y;
+            float qv[D / 4];
+            float mx = 0.f;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                a.q + ((size_t)(seg >> 8) * a.num_heads + (seg & 255) * G + g) * D + c * (D / 4));
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[g][e] = acc[g][e] * c + p * v[e];
+            for (int k = 0; k < D / 32; ++k) {
+                const uint4 w = g < G ? src[k] : make_uint4(0, 0, 0, 0);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    qv[8 * k + 2 * e] = bf16_lo(u[e]);
+                    qv[8 * k + 2 * e + 1] = bf16_hi(u[e]);
+                    mx = fmax3(mx, fabsf(bf16_lo(u[e])), fabsf(bf16_hi(u[e])));
+                }
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            int ex = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 : 0;
+            ex = max(-126, min(126, ex));
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qf[k][0] = pack_f16(qv[4 * k] * down, qv[4 * k + 1] * down);
+                qf[k][1] = pack_f16(qv[4 * k + 2] * down, qv[4 * k + 3] * down);
+            }
+            const int e0 = __shfl_sync(0xffffffffu, ex, 8 * c);
+            const int e1 = __shfl_sync(0xffffffffu, ex, 8 * c + 4);
+            cs0 = a.scale_log2 * __uint_as_float((uint32_t)(127 + e0) << 23);
+            cs1 = a.scale_log2 * __uint_as_float((uint32_t)(127 + e1) << 23);
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
+            m0 = m1 = kLowest;
+            l0 = l1 = 0.f;
+        }
+
+        // Scores of two halves of 16 tokens: [0], [1] are heads 2c, 2c + 1 of row g, [2], [3] of
+        // row g + 8.
+        float x[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+            constexpr int kWords = D / 32;  // words of codes per lane and token
+            uint32_t w[2][kWords], sl[2], sh[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint8_t *row = buf + codes_at(2 * m + r) + rk * kRow + c * (D / 8);
+                const uint8_t *scl = buf + scales_at(2 * m + r) + rk * kScRow + c * (D / 64);
+                if constexpr (D == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(row);
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                    w[r][2] = v.z;
+                    w[r][3] = v.w;
+                    const uint32_t s2 =
+                        e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(scl));
+                    sl[r] = prmt(s2, 0u, 0x1010u);
+                    sh[r] = prmt(s2, 0u, 0x3232u);
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(row);
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                    const uint32_t b = *scl;
+                    sl[r] = sh[r] = e4m3x2_to_f16x2(b | b << 8);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                uint32_t f0[4], f1[4];
+                e2m1x8_to_f16x8(w[0][k], f0);
+                e2m1x8_to_f16x8(w[1][k], f1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f0[e] = hmul2_u32(f0[e], 2 * k < kWords ? sl[0] : sh[0]);
+                    f1[e] = hmul2_u32(f1[e], 2 * k < kWords ? sl[1] : sh[1]);
+                }
+                const uint32_t p[4] = {f0[0], f1[0], f0[1], f1[1]};
+                const uint32_t q[4] = {f0[2], f1[2], f0[3], f1[3]};
+                mma_f16(sc, p, qf[2 * k][0], qf[2 * k][1]);
+                mma_f16(sd, q, qf[2 * k + 1][0], qf[2 * k + 1][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[m][e] = (sc[e] + sd[e]) * (e & 1 ? cs1 : cs0);
+        }
+        if (valid < kTokens) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                if (16 * m + rk >= valid) x[m][0] = x[m][1] = -INFINITY;
+                if (16 * m + 8 + rk >= valid) x[m][2] = x[m][3] = -INFINITY;
+            }
+        }
+        float t0x = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+        float t1x = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+        if (__any_sync(0xffffffffu, t0x > m0 + kSlack || t1x > m1 + kSlack)) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                t0x = fmaxf(t0x, __shfl_xor_sync(0xffffffffu, t0x, o));
+                t1x = fmaxf(t1x, __shfl_xor_sync(0xffffffffu, t1x, o));
+            }
+            const float n0 = fmaxf(m0, t0x), n1 = fmaxf(m1, t1x);
+            const float r0 = fast_exp2(m0 - n0), r1 = fast_exp2(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= r0;
+            l1 *= r1;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                acc[mt][0] *= r0;
+                acc[mt][1] *= r1;
+                acc[mt][2] *= r0;
+                acc[mt][3] *= r1;
+            }
+        }
+        // P, summed in fp32 before its rounding to f16; transposed to the MMA's B operand.
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const float p0 = fast_exp2(x[m][0] - m0), p1 = fast_exp2(x[m][1] - m1);
+            const float p2 = fast_exp2(x[m][2] - m0), p3 = fast_exp2(x[m][3] - m1);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            pb[m][0] = movmatrix_t(pack_f16(p0, p1));
+            pb[m][1] = movmatrix_t(pack_f16(p2, p3));
+        }
+
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            constexpr int kWords = D / 64;  // words of codes per lane and token
+            uint32_t ws[2];                 // scales of the tokens of slots 2c, 2c + 1 (+ 8)
+            uint32_t ev[2][kWords], od[2][kWords];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint8_t *row = buf + kTile + codes_at(2 * m + r) + g * (D / 16);
+                const uint8_t *scl = buf + kTile + scales_at(2 * m + r) + (D == 128 ? g : g >> 1);
+                uint32_t s0 = scl[tok_v0 * kScRow], s1 = scl[tok_v1 * kScRow];
+                if (valid < kTokens) {  // what lies behind the sequence may be anything: zero
+                    if (16 * m + 8 * r + tok_v0 >= valid) s0 = 0u;
+                    if (16 * m + 8 * r + tok_v1 >= valid) s1 = 0u;
+                }
+                ws[r] = e4m3x2_to_f16x2(s0 | s1 << 8);
+                uint32_t u[kWords], v[kWords];
+                if constexpr (D == 128) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(row + tok_v0 * kRow);
+                    const uint2 z = *reinterpret_cast<const uint2 *>(row + tok_v1 * kRow);
+                    u[0] = y.x;
+                    u[1] = y.y;
+                    v[0] = z.x;
+                    v[1] = z.y;
+                } else {
+                    u[0] = *reinterpret_cast<const uint32_t *>(row + tok_v0 * kRow);
+                    v[0] = *reinterpret_cast<const uint32_t *>(row + tok_v1 * kRow);
+                }
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) {
+                    ev[r][k] = (u[k] & 0x0f0f0f0fu) | ((v[k] << 4) & 0xf0f0f0f0u);
+                    od[r][k] = ((u[k] >> 4) & 0x0f0f0f0fu) | (v[k] & 0xf0f0f0f0u);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                uint32_t f[4][4];
+                e2m1x8_to_f16x8(ev[0][k], f[0]);
+                e2m1x8_to_f16x8(od[0][k], f[1]);
+                e2m1x8_to_f16x8(ev[1][k], f[2]);
+                e2m1x8_to_f16x8(od[1][k], f[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t p[4] = {hmul2_u32(f[0][e], ws[0]), hmul2_u32(f[1][e], ws[0]),
+                                           hmul2_u32(f[2][e], ws[1]), hmul2_u32(f[3][e], ws[1])};
+                    mma_f16(acc[4 * k + e], p, pb[m][0], pb[m][1]);
+                }
+            }
+        }
+
+        if (d.w || i == n - 1) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+            }
+            if (first_j == 0 && d.w) {
+                __nv_bfloat16 *row =
+                    a.out + ((size_t)(seg >> 8) * a.num_heads + (seg & 255) * G + 2 * c) * D +
+                    g * (D / 8);
+                if (2 * c < G) store_rows<D>(row, acc, 0, a.v_scale / l0);
+                if (2 * c + 1 < G) store_rows<D>(row + D, acc, 1, a.v_scale / l1);
+            } else if (first_j != 0) {
+                store_rec<D>(recs + warp * kRec, acc, lane, m0, l0, m1, l1);
+                if (lane == 0) {
+                    pieces[warp].a = 1;
+                    pieces[warp].a_ends = d.w;
+                }
+            } else {  // the range's last tile: every copy of the ring has been used
+                __syncwarp();
+                store_rec<D>(reinterpret_cast<float *>(stages), acc, lane, m0, l0, m1, l1);
+                if (lane == 0) {
+                    pieces[warp].b = 1;
+                    pieces[warp].b_seg = seg;
+                }
+            }
+            seg = -1;
+        }
+        __syncwarp();
+        if (i + S < n) issue(i + S, st);
+        if (++st == S) {
+            st = 0;
+            phase ^= 1u;
         }
     }
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-        if (lane == 0) {
-            s_m[warp][g] = m[g];
-            s_l[warp][g] = l[g];
+
+    // The pieces of segments that span warps: from the range's start, then from each warp in
+    // which one begins.
+    __syncthreads();
+    int4 mine = make_int4(0, 0, 0, 0);
+    for (int w = -1; w < active; ++w) {
+        if (w < 0 ? !pieces[0].a : !pieces[w].b) continue;
+        int e = w < 0 ? 0 : w;  // the last warp of this group
+        bool ends = w < 0 && pieces[0].a_ends;
+        while (!ends && e + 1 < active && pieces[e + 1].a) {
+            ++e;
+            ends = pieces[e].a_ends;
         }
+        if (w < 0) {
+            mine.x = 1;
+            mine.y = ends;
+        } else if (!ends) {
+            mine.z = 1;
+            mine.w = pieces[w].b_seg;
+        }
+        auto rec_of = [&](int k) {
+            return k == w ? reinterpret_cast<const float *>(ring + k * S * kStage)
+                          : recs + k * kRec;
+        };
+        const int from = w < 0 ? 0 : w;
+        constexpr int E = kHeads * D / (kWarps * 32);  // consecutive elements of a thread
+        const int hd = tid * E / D, dim = tid * E % D;
+        if (hd >= G) continue;
+        float M = kLowest, den = 0.f, num[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_acc[warp][g][lane * E + e] = acc[g][e];
+        for (int j = 0; j < E; ++j) num[j] = 0.f;
+        for (int k = from; k <= e; ++k) M = fmaxf(M, rec_of(k)[kHeads * D + 2 * hd]);
+        for (int k = from; k <= e; ++k) {
+            const float *r = rec_of(k);
+            const float f = fast_exp2(r[kHeads * D + 2 * hd] - M);
+            den += f * r[kHeads * D + 2 * hd + 1];
+#pragma unroll
+            for (int j = 0; j < E; ++j) num[j] += f * r[hd * D + dim + j];
+        }
+        if (w >= 0 && ends) {
+            const int sg = pieces[w].b_seg;
+            __nv_bfloat16 *row =
+                a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + hd) * D + dim;
+            const float f = a.v_scale / den;
+            if constexpr (E == 2)
+                *reinterpret_cast<uint32_t *>(row) = pack_bf16(num[0] * f, num[1] * f);
+            else
+                *row = __float2bfloat16_rn(num[0] * f);
+        } else {
+            float *r = a.recs + ((size_t)blockIdx.x * 2 + (w >= 0)) * kRec;
+#pragma unroll
+            for (int j = 0; j < E; ++j) r[hd * D + dim + j] = num[j];
+            if (dim == 0) {
+                r[kHeads * D + 2 * hd] = M;
+                r[kHeads * D + 2 * hd + 1] = den;
+            }
+        }
+    }
+    if (!a.aligned && tid == 0) a.meta[blockIdx.x] = mine;
+}
+
+// Block i merges the segment that begins in CTA i and goes on: CTA i's record at its end, then
+// the next CTAs' at their starts, up to the one in which it ends.
+template <int D>
+__global__ void __launch_bounds__(256) decode_fp4_merge_kernel(const Args a, int ctas) {
+    pdl_begin();
+    constexpr int kRec = kRecFloats<D>;
+    extern __shared__ float weights[];  // [pieces][8]
+    __shared__ int s_last;
+    __shared__ float s_den[kHeads];
+    const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.group;
+    const int4 mine = a.meta[i];
+    if (!mine.z) return;
+    if (tid == 0) s_last = ctas - 1;
+    __syncthreads();
+    for (int k = i + 1 + tid; k < ctas; k += 256) {
+        const int4 m = a.meta[k];
+        if (!m.x || m.y) atomicMin(&s_last, m.x ? k : k - 1);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < G * D; i += 256) {
-        const int g = i / D, d = i % D;
-        float M = s_m[0][g], num = 0.f, den = 0.f;
-        for (int w = 1; w < 8; ++w) M = fmaxf(M, s_m[w][g]);
-        for (int w = 0; w < 8; ++w) {
-            const float c = fast_exp2(s_m[w][g] - M);
-            num += c * s_acc[w][g][d];
-            den += c * s_l[w][g];
+    const int np = s_last - i + 1;
+    auto rec_of = [&](int p) {
+        return a.recs + (p == 0 ? (size_t)i * 2 + 1 : (size_t)(i + p) * 2) * kRec;
+    };
+    {  // a warp per head: the pieces' weights, and the denominator
+        float M = kLowest;
+        for (int p = lane; p < np; p += 32) {
+            const float m = rec_of(p)[kHeads * D + 2 * warp];
+            if (warp < G) M = fmaxf(M, m);
         }
-        a.out[((size_t)s * a.num_heads + (size_t)h * G + g) * D + d] =
-            __float2bfloat16_rn(len == 0 ? 0.f : num / den * a.v_scale);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float den = 0.f;
+        for (int p = lane; p < np; p += 32) {
+            const float2 ml = *reinterpret_cast<const float2 *>(rec_of(p) + kHeads * D + 2 * warp);
+            const float f = fast_exp2(ml.x - M);
+            weights[p * kHeads + warp] = f;
+            den += f * ml.y;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        if (lane == 0) s_den[warp] = den;
     }
+    __syncthreads();
+    const int hd = tid * 4 / D, dim = tid * 4 % D;
+    if (hd >= G) return;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int p = 0; p < np; ++p) {
+        const float4 v = *reinterpret_cast<const float4 *>(rec_of(p) + hd * D + dim);
+        const float f = weights[p * kHeads + hd];
+        num.x += f * v.x;
+        num.y += f * v.y;
+        num.z += f * v.z;
+        num.w += f * v.w;
+    }
+    const float f = a.v_scale / s_den[hd];
+    *reinterpret_cast<uint2 *>(
+        a.out + ((size_t)(mine.w >> 8) * a.num_heads + (mine.w & 255) * G + hd) * D + dim) =
+        make_uint2(pack_bf16(num.x * f, num.y * f), pack_bf16(num.z * f, num.w * f));
+}
+
+template <int D>
+size_t smem_bytes(int stages, int num_seqs) {
+    return (size_t)kWarps * stages * (kStageBytes<D> + sizeof(int4) + 8) +
+           (size_t)kWarps * (kRecFloats<D> * 4 + sizeof(WarpPieces) + 4) +
+           ((size_t)num_seqs + 1) * 4;
+}
+
+constexpr size_t kSmemMax = 232448;
+
+template <int D>
+int max_seqs() {
+    return (int)((kSmemMax - smem_bytes<D>(1, 0)) / 4);
+}
+
+template <int D, int BS>
+cudaError_t launch(Args a, int grid, cudaStream_t stream) {
+    int stages = kMaxStages<D>;
+    const int table = a.aligned ? 0 : a.num_seqs;
+    while (stages > 1 && smem_bytes<D>(stages, table) > kSmemMax) --stages;
+    a.stages = stages;
+    const size_t smem = smem_bytes<D>(stages, table);
+    cudaError_t e = ensure_smem<decode_fp4_kernel<D, BS>>(smem);
+    if (e != cudaSuccess) return e;
+    g_launched.store(true);
+    e = launch_pdl(decode_fp4_kernel<D, BS>, dim3((unsigned)grid), kWarps * 32, smem, 1, stream, a);
+    if (e != cudaSuccess || a.aligned) return e;
+    return launch_pdl(decode_fp4_merge_kernel<D>, dim3((unsigned)grid), 256,
+                      (size_t)grid * kHeads * 4, 1, stream, a, grid);
 }
 
 }  // namespace
@@ -116,35 +668,48 @@ cudaError_t take_error_decode_fp4(unsigned *bits) {
 }
 
 size_t decode_fp4_workspace_bytes(int head_size, int sm_count) {
-    return (size_t)sm_count * 2 * 8 * (head_size + 2) * 4 + 256;
+    return (size_t)sm_count * (2 * kHeads * (head_size + 2) * 4 + sizeof(int4));
 }
+
+int decode_fp4_max_seqs(int head_size) { return head_size == 128 ? max_seqs<128>() : max_seqs<64>(); }
 
 cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, const KvGeom &g,
                               int num_heads, const int32_t *block_tables, int max_blocks_per_seq,
                               const int32_t *seq_lens, int num_seqs, int max_seq_len, float scale,
                               float k_scale, float v_scale, void *workspace,
                               cudaStream_t stream) {
+    const int sms = device_sm_count();
     Args a;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.kv = static_cast<const uint8_t *>(kv_cache);
     a.block_tables = block_tables;
     a.seq_lens = seq_lens;
+    a.recs = static_cast<float *>(workspace);
+    a.meta = reinterpret_cast<int4 *>(a.recs + (size_t)sms * 2 * kHeads * (g.head_size + 2));
+    a.num_seqs = num_seqs;
     a.num_heads = num_heads;
     a.num_kv_heads = g.num_kv_heads;
     a.group = num_heads / g.num_kv_heads;
-    a.block_size = g.block_size;
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = g.num_blocks;
     a.max_seq_len = max_seq_len;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.k_scale = k_scale;
+    a.scale_log2 = scale * 1.4426950408889634f * k_scale;
     a.v_scale = v_scale;
-    g_launched.store(true);
-    const dim3 grid((unsigned)num_seqs * (unsigned)g.num_kv_heads);
-    if (g.head_size == 128)
-        return launch_pdl(decode_fp4_kernel<128>, grid, 256, 0, 1, stream, a);
-    return launch_pdl(decode_fp4_kernel<64>, grid, 256, 0, 1, stream, a);
+    const long long segs = (long long)num_seqs * g.num_kv_heads;
+    const long long tiles = (max_seq_len + kTokens - 1) / kTokens;
+    // A CTA per segment when that leaves at most four tiles to a warp and none of the SMs two
+    // segments: no scan of the lengths, no second kernel.
+    a.aligned = segs <= sms && tiles <= 4 * kWarps;
+    const int grid = (int)(a.aligned ? segs : std::min<long long>(sms, std::max(1LL, segs * tiles)));
+    if (g.head_size == 128) {
+        if (g.block_size == 8) return launch<128, 8>(a, grid, stream);
+        if (g.block_size == 16) return launch<128, 16>(a, grid, stream);
+        return launch<128, 32>(a, grid, stream);
+    }
+    if (g.block_size == 8) return launch<64, 8>(a, grid, stream);
+    if (g.block_size == 16) return launch<64, 16>(a, grid, stream);
+    return launch<64, 32>(a, grid, stream);
 }
 
 }  // namespace pa
