@@ -291,6 +291,15 @@ __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
         : "f"(a0), "f"(a1));
 }
 
+// (d0, d1) *= (a0, a1) as one packed fp32 instruction.
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1) {
+    asm("{\n\t.reg .b64 ra, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rd, {%0, %1};\n\t"
+        "mul.rn.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
+}
+
 // 2^x with the hardware approximation (flushes denormals; 2^-inf = 0).
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

@@ -1,7 +1,7 @@
 // pa_decode_fp4.cu - decode attention over a 4-bit pool: one query token per sequence.
 //
 //   out[s][h] = v_scale sum_t P[t] (code s)_V[t] / sum_t P[t],
-//   P[t] = 2^(scale log2(e) k_scale q.(code s)_K[t] - m), m a running reference
+//   P[t] = 2^(scale log2(e) k_scale (x[t] - m)), x[t] = q.(code s)_K[t], m a running reference
 //
 // Bound by HBM: 9/16 of a byte per element, read once.  At that rate an SM meets some 43
 // elements a clock, so the work per element must stay below three instructions, and the layout
@@ -38,6 +38,7 @@ constexpr int kTokens = 32;  // of a tile
 constexpr int kWarps = 16;   // one CTA per SM
 constexpr int kHeads = 8;    // query heads per KV head, padded to the MMA's N
 // m is only raised when a score exceeds it by more than this (log2 units): P stays below 2^8.
+// It is kept in the scores' own units, so that the difference is taken before any scaling.
 constexpr float kSlack = 8.f;
 constexpr float kLowest = -3.4028235e38f;  // m before the first score
 
@@ -56,20 +57,20 @@ struct Args {
     const int32_t *block_tables, *seq_lens;
     float *recs;  // [CTAs][2][kRecFloats]: a segment's piece at the range's start, at its end
     int4 *meta;   // [CTAs]: piece at the start, it ends here, piece at the end, its segment
+    int64_t block_bytes;
     int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, max_seq_len;
     int stages;
     int aligned;  // CTA c is segment c: no piece leaves its CTA
     float scale_log2, v_scale;  // scale * log2(e) * k_scale
 };
 
-// What a warp leaves for the merge in its CTA: a piece whose segment began before its range
-// (a), whether it ended there, and one that began in its range and goes on (b).
+// What a warp leaves for the merge in its CTA: a piece of a segment that began before its range
+// (a) and whether the segment ended there; one that began in its range and goes on (b).
 struct WarpPieces {
     int a, a_ends, b, b_seg;
 };
 
-__device__ __forceinline__ int clamped_len(const Args &a, int s) {
-    const int len = a.seq_lens[s];
+__device__ __forceinline__ int clamped(const Args &a, int len) {
     return len < 0 ? 0 : (len > a.max_seq_len ? a.max_seq_len : len);
 }
 
@@ -117,11 +118,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
     uint64_t *bars = reinterpret_cast<uint64_t *>(descs + kWarps * S);
     WarpPieces *pieces = reinterpret_cast<WarpPieces *>(bars + kWarps * S);
     int *sums = reinterpret_cast<int *>(pieces + kWarps);
-    int *pre = sums + kWarps;  // [num_seqs + 1], not aligned mode
+    const int B = a.num_seqs, Hkv = a.num_kv_heads, G = a.group;
+    int *lens = sums + kWarps;  // [num_seqs], and their tiles' prefix sums [num_seqs + 1];
+    int *pre = lens + B;        // not in aligned mode
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int B = a.num_seqs, Hkv = a.num_kv_heads, G = a.group;
     uint64_t *bar = bars + warp * S;
     int4 *desc = descs + warp * S;
     uint8_t *stages = ring + warp * S * kStage;
@@ -135,22 +137,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 
     // This warp's tiles [t0, t1) of the list (aligned mode: of its CTA's segment).
     int t0, t1, active;  // active: warps of this CTA with tiles
+    int own_len = 0;     // aligned mode: the segment's tokens
     {
         int r0, r1;
         if (a.aligned) {
-            const int s = blockIdx.x / Hkv;
-            if (tid == 0) {
-                const int len = a.seq_lens[s];
-                if (len < 0 || len > a.max_seq_len) atomicOr(&g_err_decode_fp4, kErrOob);
-            }
+            const int len = a.seq_lens[blockIdx.x / Hkv];
+            if (tid == 0 && (len < 0 || len > a.max_seq_len))
+                atomicOr(&g_err_decode_fp4, kErrOob);
+            own_len = clamped(a, len);
             r0 = 0;
-            r1 = (clamped_len(a, s) + kTokens - 1) / kTokens;
+            r1 = (own_len + kTokens - 1) / kTokens;
         } else {
             const int per = (B + kWarps * 32 - 1) / (kWarps * 32);
             for (int s = tid; s < B; s += kWarps * 32) {
                 const int len = a.seq_lens[s];
                 if (len < 0 || len > a.max_seq_len) atomicOr(&g_err_decode_fp4, kErrOob);
-                pre[s] = (clamped_len(a, s) + kTokens - 1) / kTokens;
+                lens[s] = clamped(a, len);
+                pre[s] = (clamped(a, len) + kTokens - 1) / kTokens;
             }
             __syncthreads();
             int sum = 0;
@@ -195,9 +198,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         for (int i = tid; i < rows * (D / 8); i += kWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
     }
 
-    // Tile t0 + 32 k + lane: its segment, place, tokens, and blocks.
+    // Tile t0 + 32 k + lane: its segment, place, tokens, and blocks (-1: outside the pool).
     struct Tile {
-        int4 d;  // (sequence << 8 | head), tile of the segment, tokens, whether it is the last
+        int4 d;  // (sequence << 8 | head), tile of the segment, tokens, 1: its last tile, 2: all
+                 // of its blocks are there
         int ids[kNB];
     };
     const int n = t1 - t0;
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         Tile t;
         t.d = make_int4(0, 0, 0, 0);
 #pragma unroll
-        for (int b = 0; b < kNB; ++b) t.ids[b] = 0;
+        for (int b = 0; b < kNB; ++b) t.ids[b] = -1;
         const int x = t0 + 32 * k + lane;
         if (x >= t1) return t;
         int s, h, j;
@@ -224,12 +228,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             h = r / nt;
             j = r - h * nt;
         }
-        const int left = clamped_len(a, s) - j * kTokens;
-        t.d = make_int4(s << 8 | h, j, min(left, kTokens), left <= kTokens);
+        const int left = (a.aligned ? own_len : lens[s]) - j * kTokens;
         const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks + j * kNB;
+        bool all = left >= kTokens;
 #pragma unroll
-        for (int b = 0; b < kNB; ++b)
-            if (b * BS < t.d.z) t.ids[b] = bt[b];
+        for (int b = 0; b < kNB; ++b) {
+            if (b * BS >= left) continue;
+            const int id = bt[b];
+            if (id >= 0 && id < a.num_blocks) {
+                t.ids[b] = id;
+            } else {
+                atomicOr(&g_err_decode_fp4, kErrOob);
+                all = false;
+            }
+        }
+        t.d = make_int4(s << 8 | h, j, min(left, kTokens), (left <= kTokens) | (all ? 2 : 0));
         return t;
     };
     Tile tile = describe(0), next_tile = tile;
@@ -242,29 +255,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         if (lane == (i & 31)) {
             uint8_t *dst = stages + st * kStage;
             desc[st] = tile.d;
-            const int blocks = (tile.d.z + BS - 1) / BS;
-            uint32_t bytes = 0;
-            bool ok[kNB];
+            const int64_t head = (int64_t)(tile.d.x & 255) * (2 * kTile);
+            auto src = [&](int b) {
+                return a.kv + (int64_t)tile.ids[b] * a.block_bytes + head;
+            };
+            if (tile.d.w & 2) {
+                mbar_arrive_expect_tx(&bar[st], kStage);
 #pragma unroll
-            for (int b = 0; b < kNB; ++b) {
-                ok[b] = b < blocks && tile.ids[b] >= 0 && tile.ids[b] < a.num_blocks;
-                if (ok[b]) bytes += 2 * kTile;
-                if (b < blocks && !ok[b]) {  // its tokens read as zeros
-                    atomicOr(&g_err_decode_fp4, kErrOob);
-                    for (int e = 0; e < 2 * kTile; e += 16)
-                        *reinterpret_cast<uint4 *>(dst + b * 2 * kTile + e) =
-                            make_uint4(0, 0, 0, 0);
+                for (int b = 0; b < kNB; ++b)
+                    bulk_load_hint(dst + b * 2 * kTile, src(b), 2 * kTile, &bar[st], policy);
+            } else {
+                uint32_t bytes = 0;
+#pragma unroll
+                for (int b = 0; b < kNB; ++b) {
+                    if (tile.ids[b] >= 0) {
+                        bytes += 2 * kTile;
+                    } else if (b * BS < tile.d.z) {  // outside the pool: its tokens are zeros
+                        for (int e = 0; e < 2 * kTile; e += 16)
+                            *reinterpret_cast<uint4 *>(dst + b * 2 * kTile + e) =
+                                make_uint4(0, 0, 0, 0);
+                    }
                 }
-            }
-            fence_proxy_async_smem();
-            mbar_arrive_expect_tx(&bar[st], bytes);
+                fence_proxy_async_smem();
+                mbar_arrive_expect_tx(&bar[st], bytes);
 #pragma unroll
-            for (int b = 0; b < kNB; ++b)
-                if (ok[b])
-                    bulk_load_hint(dst + b * 2 * kTile,
-                                   a.kv + ((int64_t)tile.ids[b] * Hkv + (tile.d.x & 255)) *
-                                              (2 * kTile),
-                                   2 * kTile, &bar[st], policy);
+                for (int b = 0; b < kNB; ++b)
+                    if (tile.ids[b] >= 0)
+                        bulk_load_hint(dst + b * 2 * kTile, src(b), 2 * kTile, &bar[st], policy);
+            }
         }
         __syncwarp();
     };
@@ -272,7 +290,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 
     float acc[D / 16][4];
     uint32_t qf[D / 16][2];
-    float cs0 = 0.f, cs1 = 0.f, m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+    // Of heads 2c and 2c + 1: what brings a score to log2 units, minus the reference and the
+    // slack in the score's own units, the sum of P.
+    float cs0 = 0.f, cs1 = 0.f, nm0 = 0.f, nm1 = 0.f, slack0 = 0.f, slack1 = 0.f;
+    float l0 = 0.f, l1 = 0.f;
     int seg = -1, first_j = 0;
     // Offsets of 8-token group j's first row, and of this lane's rows: K's row g is token rk of
     // the group, V's k-slots 2c and 2c + 1 are tokens rv and rv ^ 1.
@@ -318,7 +339,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             int ex = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 : 0;
             ex = max(-126, min(126, ex));
-            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+            float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+            if (a.scale_log2 < 0.f) down = -down;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 qf[k][0] = pack_f16(qv[4 * k] * down, qv[4 * k + 1] * down);
@@ -326,28 +348,47 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             const int e0 = __shfl_sync(0xffffffffu, ex, 8 * c);
             const int e1 = __shfl_sync(0xffffffffu, ex, 8 * c + 4);
-            cs0 = a.scale_log2 * __uint_as_float((uint32_t)(127 + e0) << 23);
-            cs1 = a.scale_log2 * __uint_as_float((uint32_t)(127 + e1) << 23);
+            // Positive and finite, so that -inf stays -inf; at their least every score is 0.
+            cs0 = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e0) << 23);
+            cs1 = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e1) << 23);
+            cs0 = fminf(fmaxf(cs0, 1.1754944e-38f), -kLowest);
+            cs1 = fminf(fmaxf(cs1, 1.1754944e-38f), -kLowest);
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
-            m0 = m1 = kLowest;
+            nm0 = nm1 = -kLowest;
+            slack0 = kSlack / cs0;
+            slack1 = kSlack / cs1;
             l0 = l1 = 0.f;
+        }
+
+        if (valid < kTokens) {
+            // What lies behind the sequence may be anything: V's scales there are zero (and the
+            // scores below -inf).
+            if (lane >= valid) {
+                const int j = lane / 8, o = lane % 8;
+                uint8_t *scl = stages + st * kStage + kTile + 8 * j / BS * 2 * kTile + BS * kRow +
+                               (8 * j % BS + o) * kScRow;
+                if constexpr (D == 128)
+                    *reinterpret_cast<uint2 *>(scl) = make_uint2(0u, 0u);
+                else
+                    *reinterpret_cast<uint32_t *>(scl) = 0u;
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
         }
 
         // Scores of two halves of 16 tokens: [0], [1] are heads 2c, 2c + 1 of row g, [2], [3] of
         // row g + 8.
-        float x[2][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
+        float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
             constexpr int kWords = D / 32;  // words of codes per lane and token
-            uint32_t w[2][kWords], sl[2], sh[2];
+            uint32_t w[4][kWords], sl[4], sh[4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint8_t *row = buf + codes_at(2 * m + r) + rk * kRow + c * (D / 8);
-                const uint8_t *scl = buf + scales_at(2 * m + r) + rk * kScRow + c * (D / 64);
+            for (int r = 0; r < 4; ++r) {
+                const uint8_t *row = buf + codes_at(r) + rk * kRow + c * (D / 8);
+                const uint8_t *scl = buf + scales_at(r) + rk * kScRow + c * (D / 64);
                 if constexpr (D == 128) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(row);
                     w[r][0] = v.x;
@@ -368,21 +409,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
 #pragma unroll
             for (int k = 0; k < kWords; ++k) {
-                uint32_t f0[4], f1[4];
-                e2m1x8_to_f16x8(w[0][k], f0);
-                e2m1x8_to_f16x8(w[1][k], f1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f0[e] = hmul2_u32(f0[e], 2 * k < kWords ? sl[0] : sh[0]);
-                    f1[e] = hmul2_u32(f1[e], 2 * k < kWords ? sl[1] : sh[1]);
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t f0[4], f1[4];
+                    e2m1x8_to_f16x8(w[2 * m][k], f0);
+                    e2m1x8_to_f16x8(w[2 * m + 1][k], f1);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f0[e] = hmul2_u32(f0[e], 2 * k < kWords ? sl[2 * m] : sh[2 * m]);
+                        f1[e] = hmul2_u32(f1[e], 2 * k < kWords ? sl[2 * m + 1] : sh[2 * m + 1]);
+                    }
+                    const uint32_t p[4] = {f0[0], f1[0], f0[1], f1[1]};
+                    const uint32_t q[4] = {f0[2], f1[2], f0[3], f1[3]};
+                    mma_f16(x[m], p, qf[2 * k][0], qf[2 * k][1]);
+                    mma_f16(x[m], q, qf[2 * k + 1][0], qf[2 * k + 1][1]);
                 }
-                const uint32_t p[4] = {f0[0], f1[0], f0[1], f1[1]};
-                const uint32_t q[4] = {f0[2], f1[2], f0[3], f1[3]};
-                mma_f16(sc, p, qf[2 * k][0], qf[2 * k][1]);
-                mma_f16(sd, q, qf[2 * k + 1][0], qf[2 * k + 1][1]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[m][e] = (sc[e] + sd[e]) * (e & 1 ? cs1 : cs0);
         }
         if (valid < kTokens) {
 #pragma unroll
@@ -391,18 +433,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 if (16 * m + 8 + rk >= valid) x[m][2] = x[m][3] = -INFINITY;
             }
         }
-        float t0x = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        float t1x = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-        if (__any_sync(0xffffffffu, t0x > m0 + kSlack || t1x > m1 + kSlack)) {
+        float t0x = fmaxf(fmax3(x[0][0], x[0][2], x[1][0]), x[1][2]);
+        float t1x = fmaxf(fmax3(x[0][1], x[0][3], x[1][1]), x[1][3]);
+        if (__any_sync(0xffffffffu, t0x > slack0 - nm0 || t1x > slack1 - nm1)) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 t0x = fmaxf(t0x, __shfl_xor_sync(0xffffffffu, t0x, o));
                 t1x = fmaxf(t1x, __shfl_xor_sync(0xffffffffu, t1x, o));
             }
-            const float n0 = fmaxf(m0, t0x), n1 = fmaxf(m1, t1x);
-            const float r0 = fast_exp2(m0 - n0), r1 = fast_exp2(m1 - n1);
-            m0 = n0;
-            m1 = n1;
+            const float n0 = fminf(nm0, -t0x), n1 = fminf(nm1, -t1x);
+            const float r0 = fast_exp2((n0 - nm0) * cs0), r1 = fast_exp2((n1 - nm1) * cs1);
+            nm0 = n0;
+            nm1 = n1;
             l0 *= r0;
             l1 *= r1;
 #pragma unroll
@@ -417,84 +459,91 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         uint32_t pb[2][2];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            const float p0 = fast_exp2(x[m][0] - m0), p1 = fast_exp2(x[m][1] - m1);
-            const float p2 = fast_exp2(x[m][2] - m0), p3 = fast_exp2(x[m][3] - m1);
-            l0 += p0 + p2;
-            l1 += p1 + p3;
-            pb[m][0] = movmatrix_t(pack_f16(p0, p1));
-            pb[m][1] = movmatrix_t(pack_f16(p2, p3));
+            float p[4] = {x[m][0], x[m][1], x[m][2], x[m][3]};
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                add2(p[e], p[e + 1], nm0, nm1);
+                mul2(p[e], p[e + 1], cs0, cs1);
+                p[e] = fast_exp2(p[e]);
+                p[e + 1] = fast_exp2(p[e + 1]);
+                add2(l0, l1, p[e], p[e + 1]);
+            }
+            pb[m][0] = movmatrix_t(pack_f16(p[0], p[1]));
+            pb[m][1] = movmatrix_t(pack_f16(p[2], p[3]));
         }
 
+        // V: all of it into registers, tokens interleaved, and the stage is free for its next
+        // tile while they are multiplied.
+        constexpr int kWords = D / 64;  // words of codes per lane and token
+        uint32_t ws[4];                 // scales of the tokens of slots 2c, 2c + 1 of 8-token groups
+        uint32_t ev[4][kWords], od[4][kWords];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            constexpr int kWords = D / 64;  // words of codes per lane and token
-            uint32_t ws[2];                 // scales of the tokens of slots 2c, 2c + 1 (+ 8)
-            uint32_t ev[2][kWords], od[2][kWords];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint8_t *row = buf + kTile + codes_at(2 * m + r) + g * (D / 16);
-                const uint8_t *scl = buf + kTile + scales_at(2 * m + r) + (D == 128 ? g : g >> 1);
-                uint32_t s0 = scl[tok_v0 * kScRow], s1 = scl[tok_v1 * kScRow];
-                if (valid < kTokens) {  // what lies behind the sequence may be anything: zero
-                    if (16 * m + 8 * r + tok_v0 >= valid) s0 = 0u;
-                    if (16 * m + 8 * r + tok_v1 >= valid) s1 = 0u;
-                }
-                ws[r] = e4m3x2_to_f16x2(s0 | s1 << 8);
-                uint32_t u[kWords], v[kWords];
-                if constexpr (D == 128) {
-                    const uint2 y = *reinterpret_cast<const uint2 *>(row + tok_v0 * kRow);
-                    const uint2 z = *reinterpret_cast<const uint2 *>(row + tok_v1 * kRow);
-                    u[0] = y.x;
-                    u[1] = y.y;
-                    v[0] = z.x;
-                    v[1] = z.y;
-                } else {
-                    u[0] = *reinterpret_cast<const uint32_t *>(row + tok_v0 * kRow);
-                    v[0] = *reinterpret_cast<const uint32_t *>(row + tok_v1 * kRow);
-                }
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) {
-                    ev[r][k] = (u[k] & 0x0f0f0f0fu) | ((v[k] << 4) & 0xf0f0f0f0u);
-                    od[r][k] = ((u[k] >> 4) & 0x0f0f0f0fu) | (v[k] & 0xf0f0f0f0u);
-                }
+        for (int r = 0; r < 4; ++r) {
+            const uint8_t *row = buf + kTile + codes_at(r) + g * (D / 16);
+            const uint8_t *scl = buf + kTile + scales_at(r) + (D == 128 ? g : g >> 1);
+            const uint32_t s0 = scl[tok_v0 * kScRow], s1 = scl[tok_v1 * kScRow];
+            ws[r] = e4m3x2_to_f16x2(prmt(s0, s1, 0x0040u));
+            uint32_t u[kWords], v[kWords];
+            if constexpr (D == 128) {
+                const uint2 y = *reinterpret_cast<const uint2 *>(row + tok_v0 * kRow);
+                const uint2 z = *reinterpret_cast<const uint2 *>(row + tok_v1 * kRow);
+                u[0] = y.x;
+                u[1] = y.y;
+                v[0] = z.x;
+                v[1] = z.y;
+            } else {
+                u[0] = *reinterpret_cast<const uint32_t *>(row + tok_v0 * kRow);
+                v[0] = *reinterpret_cast<const uint32_t *>(row + tok_v1 * kRow);
             }
 #pragma unroll
             for (int k = 0; k < kWords; ++k) {
+                ev[r][k] = (u[k] & 0x0f0f0f0fu) | ((v[k] << 4) & 0xf0f0f0f0u);
+                od[r][k] = ((u[k] >> 4) & 0x0f0f0f0fu) | (v[k] & 0xf0f0f0f0u);
+            }
+        }
+        __syncwarp();
+        if (i + S < n) issue(i + S, st);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
                 uint32_t f[4][4];
-                e2m1x8_to_f16x8(ev[0][k], f[0]);
-                e2m1x8_to_f16x8(od[0][k], f[1]);
-                e2m1x8_to_f16x8(ev[1][k], f[2]);
-                e2m1x8_to_f16x8(od[1][k], f[3]);
+                e2m1x8_to_f16x8(ev[2 * m][k], f[0]);
+                e2m1x8_to_f16x8(od[2 * m][k], f[1]);
+                e2m1x8_to_f16x8(ev[2 * m + 1][k], f[2]);
+                e2m1x8_to_f16x8(od[2 * m + 1][k], f[3]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t p[4] = {hmul2_u32(f[0][e], ws[0]), hmul2_u32(f[1][e], ws[0]),
-                                           hmul2_u32(f[2][e], ws[1]), hmul2_u32(f[3][e], ws[1])};
+                    const uint32_t p[4] = {hmul2_u32(f[0][e], ws[2 * m]),
+                                           hmul2_u32(f[1][e], ws[2 * m]),
+                                           hmul2_u32(f[2][e], ws[2 * m + 1]),
+                                           hmul2_u32(f[3][e], ws[2 * m + 1])};
                     mma_f16(acc[4 * k + e], p, pb[m][0], pb[m][1]);
                 }
             }
         }
 
-        if (d.w || i == n - 1) {
+        const bool last = d.w & 1;
+        if (last || i == n - 1) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 l0 += __shfl_xor_sync(0xffffffffu, l0, o);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, o);
             }
-            if (first_j == 0 && d.w) {
+            if (first_j == 0 && last) {
                 __nv_bfloat16 *row =
                     a.out + ((size_t)(seg >> 8) * a.num_heads + (seg & 255) * G + 2 * c) * D +
                     g * (D / 8);
                 if (2 * c < G) store_rows<D>(row, acc, 0, a.v_scale / l0);
                 if (2 * c + 1 < G) store_rows<D>(row + D, acc, 1, a.v_scale / l1);
             } else if (first_j != 0) {
-                store_rec<D>(recs + warp * kRec, acc, lane, m0, l0, m1, l1);
+                store_rec<D>(recs + warp * kRec, acc, lane, -nm0 * cs0, l0, -nm1 * cs1, l1);
                 if (lane == 0) {
                     pieces[warp].a = 1;
-                    pieces[warp].a_ends = d.w;
+                    pieces[warp].a_ends = last;
                 }
             } else {  // the range's last tile: every copy of the ring has been used
-                __syncwarp();
-                store_rec<D>(reinterpret_cast<float *>(stages), acc, lane, m0, l0, m1, l1);
+                store_rec<D>(reinterpret_cast<float *>(stages), acc, lane, -nm0 * cs0, l0, -nm1 * cs1, l1);
                 if (lane == 0) {
                     pieces[warp].b = 1;
                     pieces[warp].b_seg = seg;
@@ -502,130 +551,134 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             seg = -1;
         }
-        __syncwarp();
-        if (i + S < n) issue(i + S, st);
         if (++st == S) {
             st = 0;
             phase ^= 1u;
         }
     }
 
-    // The pieces of segments that span warps: from the range's start, then from each warp in
-    // which one begins.
+    // The pieces of segments that span warps: warp w merges those of the segment that began in
+    // warp w's range, the last warp those of the one that began before the CTA's.
     __syncthreads();
-    int4 mine = make_int4(0, 0, 0, 0);
-    for (int w = -1; w < active; ++w) {
-        if (w < 0 ? !pieces[0].a : !pieces[w].b) continue;
-        int e = w < 0 ? 0 : w;  // the last warp of this group
-        bool ends = w < 0 && pieces[0].a_ends;
-        while (!ends && e + 1 < active && pieces[e + 1].a) {
-            ++e;
-            ends = pieces[e].a_ends;
-        }
-        if (w < 0) {
-            mine.x = 1;
-            mine.y = ends;
-        } else if (!ends) {
-            mine.z = 1;
-            mine.w = pieces[w].b_seg;
-        }
+    const WarpPieces lp = lane < kWarps ? pieces[lane] : WarpPieces{0, 0, 0, 0};
+    const uint32_t through = __ballot_sync(0xffffffffu, lp.a && !lp.a_ends);  // a whole range
+    const uint32_t ending = __ballot_sync(0xffffffffu, lp.a_ends);
+    const uint32_t begun = __ballot_sync(0xffffffffu, lp.b);
+    // The last warp of the pieces that follow warp e - 1's, and whether the segment ends there.
+    auto follow = [&](int e, bool &ends) {
+        while (through >> e & 1) ++e;
+        ends = ending >> e & 1;
+        return ends ? e : e - 1;
+    };
+    auto merge = [&](bool head, int w) {
+        bool ends;
+        const int from = head ? 0 : w, e = follow(head ? 0 : w + 1, ends);
         auto rec_of = [&](int k) {
-            return k == w ? reinterpret_cast<const float *>(ring + k * S * kStage)
-                          : recs + k * kRec;
+            return !head && k == w ? reinterpret_cast<const float *>(ring + k * S * kStage)
+                                   : recs + k * kRec;
         };
-        const int from = w < 0 ? 0 : w;
-        constexpr int E = kHeads * D / (kWarps * 32);  // consecutive elements of a thread
-        const int hd = tid * E / D, dim = tid * E % D;
-        if (hd >= G) continue;
-        float M = kLowest, den = 0.f, num[E];
-#pragma unroll
-        for (int j = 0; j < E; ++j) num[j] = 0.f;
-        for (int k = from; k <= e; ++k) M = fmaxf(M, rec_of(k)[kHeads * D + 2 * hd]);
-        for (int k = from; k <= e; ++k) {
-            const float *r = rec_of(k);
-            const float f = fast_exp2(r[kHeads * D + 2 * hd] - M);
-            den += f * r[kHeads * D + 2 * hd + 1];
-#pragma unroll
-            for (int j = 0; j < E; ++j) num[j] += f * r[hd * D + dim + j];
-        }
-        if (w >= 0 && ends) {
-            const int sg = pieces[w].b_seg;
-            __nv_bfloat16 *row =
-                a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + hd) * D + dim;
-            const float f = a.v_scale / den;
-            if constexpr (E == 2)
-                *reinterpret_cast<uint32_t *>(row) = pack_bf16(num[0] * f, num[1] * f);
-            else
-                *row = __float2bfloat16_rn(num[0] * f);
-        } else {
-            float *r = a.recs + ((size_t)blockIdx.x * 2 + (w >= 0)) * kRec;
-#pragma unroll
-            for (int j = 0; j < E; ++j) r[hd * D + dim + j] = num[j];
-            if (dim == 0) {
-                r[kHeads * D + 2 * hd] = M;
-                r[kHeads * D + 2 * hd + 1] = den;
+        const int sg = head ? 0 : pieces[w].b_seg;
+        const bool whole = !head && ends;
+        float *out_rec = a.recs + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * kRec;
+        for (int q = lane; q < G * (D / 4); q += 32) {
+            const int hd = q / (D / 4), dim = q % (D / 4) * 4;
+            float M = kLowest, den = 0.f;
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = from; k <= e; ++k) M = fmaxf(M, rec_of(k)[kHeads * D + 2 * hd]);
+            for (int k = from; k <= e; ++k) {
+                const float *r = rec_of(k);
+                const float2 ml = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * hd);
+                const float4 v = *reinterpret_cast<const float4 *>(r + hd * D + dim);
+                const float f = fast_exp2(ml.x - M);
+                den += f * ml.y;
+                num.x += f * v.x;
+                num.y += f * v.y;
+                num.z += f * v.z;
+                num.w += f * v.w;
+            }
+            if (whole) {
+                const float f = a.v_scale / den;
+                *reinterpret_cast<uint2 *>(
+                    a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + hd) * D + dim) =
+                    make_uint2(pack_bf16(num.x * f, num.y * f), pack_bf16(num.z * f, num.w * f));
+            } else {
+                *reinterpret_cast<float4 *>(out_rec + hd * D + dim) = num;
+                if (dim == 0)
+                    *reinterpret_cast<float2 *>(out_rec + kHeads * D + 2 * hd) =
+                        make_float2(M, den);
             }
         }
+    };
+    if (begun >> warp & 1) merge(false, warp);
+    if (warp == kWarps - 1 && pieces[0].a) merge(true, 0);
+    if (!a.aligned && tid == 0) {
+        bool head_ends = false, tail_ends = true;
+        follow(0, head_ends);
+        const int w = 31 - __clz(begun);  // the one piece that may leave the CTA begins here
+        if (begun) follow(w + 1, tail_ends);
+        a.meta[blockIdx.x] = make_int4(lp.a, head_ends, !tail_ends,
+                                       begun ? pieces[w].b_seg : 0);
     }
-    if (!a.aligned && tid == 0) a.meta[blockIdx.x] = mine;
 }
 
 // Block i merges the segment that begins in CTA i and goes on: CTA i's record at its end, then
-// the next CTAs' at their starts, up to the one in which it ends.
+// the next CTAs' at their starts, up to the one in which it ends.  A thread per head and four
+// dims; eight pieces are requested at once, weights and all.
 template <int D>
-__global__ void __launch_bounds__(256) decode_fp4_merge_kernel(const Args a, int ctas) {
+__global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const Args a, int ctas) {
     pdl_begin();
-    constexpr int kRec = kRecFloats<D>;
-    extern __shared__ float weights[];  // [pieces][8]
+    constexpr int kRec = kRecFloats<D>, kThreads = kHeads * D / 4, kBatch = 8;
     __shared__ int s_last;
-    __shared__ float s_den[kHeads];
-    const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.group;
-    const int4 mine = a.meta[i];
-    if (!mine.z) return;
+    const int i = blockIdx.x, tid = threadIdx.x, G = a.group;
     if (tid == 0) s_last = ctas - 1;
+    const int4 mine = a.meta[i];
     __syncthreads();
-    for (int k = i + 1 + tid; k < ctas; k += 256) {
-        const int4 m = a.meta[k];
+    if (!mine.z) return;
+    for (int k = i + 1 + tid; k < ctas; k += kThreads) {
+        const int2 m = *reinterpret_cast<const int2 *>(a.meta + k);
         if (!m.x || m.y) atomicMin(&s_last, m.x ? k : k - 1);
     }
     __syncthreads();
     const int np = s_last - i + 1;
-    auto rec_of = [&](int p) {
-        return a.recs + (p == 0 ? (size_t)i * 2 + 1 : (size_t)(i + p) * 2) * kRec;
-    };
-    {  // a warp per head: the pieces' weights, and the denominator
-        float M = kLowest;
-        for (int p = lane; p < np; p += 32) {
-            const float m = rec_of(p)[kHeads * D + 2 * warp];
-            if (warp < G) M = fmaxf(M, m);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float den = 0.f;
-        for (int p = lane; p < np; p += 32) {
-            const float2 ml = *reinterpret_cast<const float2 *>(rec_of(p) + kHeads * D + 2 * warp);
-            const float f = fast_exp2(ml.x - M);
-            weights[p * kHeads + warp] = f;
-            den += f * ml.y;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-        if (lane == 0) s_den[warp] = den;
-    }
-    __syncthreads();
     const int hd = tid * 4 / D, dim = tid * 4 % D;
     if (hd >= G) return;
+    float M = kLowest, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int p = 0; p < np; ++p) {
-        const float4 v = *reinterpret_cast<const float4 *>(rec_of(p) + hd * D + dim);
-        const float f = weights[p * kHeads + hd];
-        num.x += f * v.x;
-        num.y += f * v.y;
-        num.z += f * v.z;
-        num.w += f * v.w;
+    for (int p0 = 0; p0 < np; p0 += kBatch) {
+        float2 ml[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int p = p0 + k;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p < np) {
+                const float *r = a.recs + (p == 0 ? (size_t)i * 2 + 1 : (size_t)(i + p) * 2) * kRec;
+                ml[k] = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * hd);
+                v[k] = *reinterpret_cast<const float4 *>(r + hd * D + dim);
+            }
+        }
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) m = fmaxf(m, ml[k].x);
+        const float back = fast_exp2(M - m);
+        M = m;
+        den *= back;
+        num.x *= back;
+        num.y *= back;
+        num.z *= back;
+        num.w *= back;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float f = fast_exp2(ml[k].x - m);
+            den += f * ml[k].y;
+            num.x += f * v[k].x;
+            num.y += f * v[k].y;
+            num.z += f * v[k].z;
+            num.w += f * v[k].w;
+        }
     }
-    const float f = a.v_scale / s_den[hd];
+    const float f = a.v_scale / den;
     *reinterpret_cast<uint2 *>(
         a.out + ((size_t)(mine.w >> 8) * a.num_heads + (mine.w & 255) * G + hd) * D + dim) =
         make_uint2(pack_bf16(num.x * f, num.y * f), pack_bf16(num.z * f, num.w * f));
@@ -635,14 +688,14 @@ template <int D>
 size_t smem_bytes(int stages, int num_seqs) {
     return (size_t)kWarps * stages * (kStageBytes<D> + sizeof(int4) + 8) +
            (size_t)kWarps * (kRecFloats<D> * 4 + sizeof(WarpPieces) + 4) +
-           ((size_t)num_seqs + 1) * 4;
+           ((size_t)num_seqs * 2 + 1) * 4;
 }
 
 constexpr size_t kSmemMax = 232448;
 
 template <int D>
 int max_seqs() {
-    return (int)((kSmemMax - smem_bytes<D>(1, 0)) / 4);
+    return (int)((kSmemMax - smem_bytes<D>(1, 0)) / 8);
 }
 
 template <int D, int BS>
@@ -657,8 +710,8 @@ cudaError_t launch(Args a, int grid, cudaStream_t stream) {
     g_launched.store(true);
     e = launch_pdl(decode_fp4_kernel<D, BS>, dim3((unsigned)grid), kWarps * 32, smem, 1, stream, a);
     if (e != cudaSuccess || a.aligned) return e;
-    return launch_pdl(decode_fp4_merge_kernel<D>, dim3((unsigned)grid), 256,
-                      (size_t)grid * kHeads * 4, 1, stream, a, grid);
+    return launch_pdl(decode_fp4_merge_kernel<D>, dim3((unsigned)grid), kHeads * D / 4, 0, 1,
+                      stream, a, grid);
 }
 
 }  // namespace
@@ -691,6 +744,7 @@ cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, co
     a.num_heads = num_heads;
     a.num_kv_heads = g.num_kv_heads;
     a.group = num_heads / g.num_kv_heads;
+    a.block_bytes = (int64_t)g.block_size * g.num_kv_heads * g.head_size / 8 * 9;
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = g.num_blocks;
     a.max_seq_len = max_seq_len;
