@@ -166,8 +166,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             if (lane == 31) sums[warp] = v;
             __syncthreads();
-            int run = v - sum;
-            for (int w = 0; w < warp; ++w) run += sums[w];
+            // The sums of the warps before this one, lane w holding warp w's.
+            int run = lane < warp ? sums[lane] : 0;
+#pragma unroll
+            for (int o = 1; o < kWarps; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
+            run = __shfl_sync(0xffffffffu, run, 0) + v - sum;
             for (int i = tid * per; i < min(B, (tid + 1) * per); ++i) {
                 const int n = pre[i];
                 pre[i] = run;
@@ -175,17 +178,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             if (tid == kWarps * 32 - 1) pre[B] = run;
             __syncthreads();
-            const long long T = (long long)pre[B] * Hkv;
+            const int T = pre[B] * Hkv;  // below 2^31
             // With fewer tiles than CTAs the first T take one each: no range before another's
             // is empty, so a segment's pieces are those of consecutive CTAs.
-            const long long ctas = T < gridDim.x ? T : gridDim.x;
-            r0 = blockIdx.x < ctas ? (int)(T * blockIdx.x / ctas) : 0;
-            r1 = blockIdx.x < ctas ? (int)(T * (blockIdx.x + 1) / ctas) : 0;
+            const int ctas = max(1, min(T, (int)gridDim.x));
+            const int cta = blockIdx.x, each = T / ctas, rest = T - each * ctas;
+            r0 = cta < ctas ? cta * each + min(cta, rest) : 0;
+            r1 = cta < ctas ? r0 + each + (cta < rest) : 0;
         }
         const int n = r1 - r0;
         active = min(n, kWarps);
-        t0 = warp < active ? r0 + (int)((long long)n * warp / active) : r0;
-        t1 = warp < active ? r0 + (int)((long long)n * (warp + 1) / active) : r0;
+        const int each = n / kWarps, rest = n % kWarps;
+        t0 = r0 + warp * each + min(warp, rest);
+        t1 = t0 + each + (warp < rest);
     }
 
     // Rows of sequences without tokens.
@@ -557,8 +562,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         }
     }
 
-    // The pieces of segments that span warps: warp w merges those of the segment that began in
-    // warp w's range, the last warp those of the one that began before the CTA's.
+    // The pieces of segments that span warps, a group of them per warp in which such a segment
+    // began and one for the segment that began before the CTA's range: a warp per group and
+    // head.
     __syncthreads();
     const WarpPieces lp = lane < kWarps ? pieces[lane] : WarpPieces{0, 0, 0, 0};
     const uint32_t through = __ballot_sync(0xffffffffu, lp.a && !lp.a_ends);  // a whole range
@@ -570,47 +576,57 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         ends = ending >> e & 1;
         return ends ? e : e - 1;
     };
-    auto merge = [&](bool head, int w) {
+    const int groups = __popc(begun) + pieces[0].a;
+    for (int item = warp; item < groups * G; item += kWarps) {
+        const int hd = item % G;
+        int nth = item / G;
+        const bool head = nth == __popc(begun);
+        uint32_t left = begun;
+        for (; nth > 0 && left; --nth) left &= left - 1;
+        const int w = head ? 0 : __ffs(left) - 1;  // the first piece's warp
         bool ends;
-        const int from = head ? 0 : w, e = follow(head ? 0 : w + 1, ends);
-        auto rec_of = [&](int k) {
-            return !head && k == w ? reinterpret_cast<const float *>(ring + k * S * kStage)
-                                   : recs + k * kRec;
+        const int e = follow(head ? 0 : w + 1, ends), np = e - w + 1;
+        auto rec_of = [&](int k) {  // piece k
+            return k == 0 && !head ? reinterpret_cast<const float *>(ring + w * S * kStage)
+                                   : recs + (w + k) * kRec;
         };
-        const int sg = head ? 0 : pieces[w].b_seg;
-        const bool whole = !head && ends;
-        float *out_rec = a.recs + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * kRec;
-        for (int q = lane; q < G * (D / 4); q += 32) {
-            const int hd = q / (D / 4), dim = q % (D / 4) * 4;
-            float M = kLowest, den = 0.f;
-            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = from; k <= e; ++k) M = fmaxf(M, rec_of(k)[kHeads * D + 2 * hd]);
-            for (int k = from; k <= e; ++k) {
-                const float *r = rec_of(k);
-                const float2 ml = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * hd);
-                const float4 v = *reinterpret_cast<const float4 *>(r + hd * D + dim);
-                const float f = fast_exp2(ml.x - M);
-                den += f * ml.y;
-                num.x += f * v.x;
-                num.y += f * v.y;
-                num.z += f * v.z;
-                num.w += f * v.w;
-            }
-            if (whole) {
-                const float f = a.v_scale / den;
-                *reinterpret_cast<uint2 *>(
-                    a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + hd) * D + dim) =
-                    make_uint2(pack_bf16(num.x * f, num.y * f), pack_bf16(num.z * f, num.w * f));
-            } else {
-                *reinterpret_cast<float4 *>(out_rec + hd * D + dim) = num;
-                if (dim == 0)
-                    *reinterpret_cast<float2 *>(out_rec + kHeads * D + 2 * hd) =
-                        make_float2(M, den);
+        float M = kLowest, den = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < np; ++k) M = fmaxf(M, rec_of(k)[kHeads * D + 2 * hd]);
+        constexpr int E = D / 32;  // consecutive dims of a lane
+        float num[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) num[j] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < np; ++k) {
+            const float *r = rec_of(k);
+            const float2 ml = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * hd);
+            const float f = fast_exp2(ml.x - M);
+            den += f * ml.y;
+#pragma unroll
+            for (int j = 0; j < E; j += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(r + hd * D + lane * E + j);
+                num[j] += f * v.x;
+                num[j + 1] += f * v.y;
             }
         }
-    };
-    if (begun >> warp & 1) merge(false, warp);
-    if (warp == kWarps - 1 && pieces[0].a) merge(true, 0);
+        if (!head && ends) {
+            const int sg = pieces[w].b_seg;
+            const float inv = a.v_scale / den;
+            uint32_t *row = reinterpret_cast<uint32_t *>(
+                a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + hd) * D + lane * E);
+#pragma unroll
+            for (int j = 0; j < E; j += 2) row[j / 2] = pack_bf16(num[j] * inv, num[j + 1] * inv);
+        } else {
+            float *r = a.recs + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * kRec;
+#pragma unroll
+            for (int j = 0; j < E; j += 2)
+                *reinterpret_cast<float2 *>(r + hd * D + lane * E + j) =
+                    make_float2(num[j], num[j + 1]);
+            if (lane == 0)
+                *reinterpret_cast<float2 *>(r + kHeads * D + 2 * hd) = make_float2(M, den);
+        }
+    }
     if (!a.aligned && tid == 0) {
         bool head_ends = false, tail_ends = true;
         follow(0, head_ends);
@@ -632,12 +648,14 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
     const int i = blockIdx.x, tid = threadIdx.x, G = a.group;
     if (tid == 0) s_last = ctas - 1;
     const int4 mine = a.meta[i];
-    __syncthreads();
-    if (!mine.z) return;
+    int stop = ctas - 1;  // of the CTAs that this thread looks at, the first to end the segment
     for (int k = i + 1 + tid; k < ctas; k += kThreads) {
         const int2 m = *reinterpret_cast<const int2 *>(a.meta + k);
-        if (!m.x || m.y) atomicMin(&s_last, m.x ? k : k - 1);
+        if (!m.x || m.y) stop = min(stop, m.x ? k : k - 1);
     }
+    __syncthreads();
+    if (!mine.z) return;
+    if (stop < ctas - 1) atomicMin(&s_last, stop);
     __syncthreads();
     const int np = s_last - i + 1;
     const int hd = tid * 4 / D, dim = tid * 4 % D;
