@@ -717,7 +717,7 @@ pa_status pa_decode_fp4(const pa_decode_fp4_args *args);
  *   qkv           rows of num_heads + 2 * num_kv_heads heads (q, k, v) bf16; row i starts at
  *                 element i * row_stride (a multiple of 8), 16-byte aligned
  *   q_weight, k_weight  [head_size] bf16 (16-byte aligned) or NULL, each by itself
- *   cos_sin       [max_position][rot_dim] fp32: rot_dim / 2 cosines, then as many sines
+ *   cos_sin       [max_position][rot_dim] fp32, 16-byte aligned: rot_dim / 2 cosines, then sines
  *                 (with any scaling of frequencies or amplitude in them)
  *   positions     [num_axes][num_tokens] int32.  A token with a position outside [0,
  *                 max_position) on an axis that a pair uses is skipped (neither q nor K and V

@@ -997,7 +997,7 @@ pa_status pa_qkv_rope_write(const pa_qkv_rope_write_args *a) {
     if (a->num_tokens == 0) return PA_OK;
     if (!a->q_out || !a->qkv || !a->cos_sin || !a->positions || !a->slot_mapping ||
         (a->num_axes > 1 && !a->pair_axis) || !aligned(a->q_out, 16) || !aligned(a->qkv, 16) ||
-        !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16) || !aligned(a->cos_sin, 4) ||
+        !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16) || !aligned(a->cos_sin, 16) ||
         !aligned(a->positions, 4) || !aligned(a->pair_axis, 4) || !aligned(a->slot_mapping, 4))
         return PA_ERR_INVALID_ARG;
     const int64_t width = ((int64_t)a->num_heads + 2 * (int64_t)a->num_kv_heads) * a->head_size;

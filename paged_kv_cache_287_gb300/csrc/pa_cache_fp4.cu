@@ -2,7 +2,9 @@
 //
 // A thread per 16 elements, the group that shares a scale: 32 bytes of bf16 on one side, 8 bytes
 // of codes and one of scale on the other.  Both directions are bound by HBM: 2.56 bytes an
-// element, each moved once.
+// element, each moved once.  A block's threads lie over the groups of one token's K and V rows
+// (several tokens where those are few), so that a thread keeps its column and finds only the
+// token's slot anew; it takes two or four tokens at once to have as many loads in flight.
 #include <algorithm>
 #include <atomic>
 
@@ -15,69 +17,106 @@ namespace {
 __device__ unsigned g_err_cache_fp4;
 std::atomic<bool> g_launched{false};
 
+constexpr int kThreads = 256;
+// Tokens of a thread in flight, and blocks per SM (quantising takes the registers).
+template <bool kWrite>
+constexpr int kTokens = kWrite ? 2 : 4;
+template <bool kWrite>
+constexpr int kPerSm = kWrite ? 3 : 4;
+
 struct RowsArgs {
     uint8_t *kv;
-    uint4 *k, *v;  // rows of the caller's, row_vecs 16-byte vectors apart
+    uint8_t *k, *v;  // rows of the caller's, row_bytes apart
     const int32_t *slots;
-    int64_t row_vecs, num_slots;
-    int num_tokens, block_size, num_kv_heads;
+    int64_t row_bytes, num_slots;
+    int num_tokens, block_shift, num_kv_heads;
+    int wide;  // rows lie on 32-byte boundaries
     float gk, gv, hk, hv;  // k_scale, v_scale, and six times those
 };
 
-// The slot of token tok, or -1 for none.
-__device__ __forceinline__ int slot_of(const RowsArgs &a, int tok) {
-    const int slot = a.slots[tok];
-    if (slot >= 0 && slot >= a.num_slots) {
-        atomicOr(&g_err_cache_fp4, kErrOob);
-        return -1;
-    }
-    return slot;
-}
-
 template <int D, bool kWrite>
-__global__ void __launch_bounds__(256) rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm<kWrite>) rows_kernel(const RowsArgs a) {
     pdl_begin();
     constexpr int kGroups = D / kFp4Group;  // of a head's row
-    const int per_side = a.num_kv_heads * kGroups;
-    const int64_t total = (int64_t)a.num_tokens * 2 * per_side;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
-        const int tok = (int)(i / (2 * per_side));
-        const int r = (int)(i - (int64_t)tok * 2 * per_side);
-        const int side = r >= per_side;
-        const int col = r - side * per_side, head = col / kGroups, grp = col % kGroups;
-        const int slot = slot_of(a, tok);
-        if (slot < 0) continue;
-        const int blk = slot / a.block_size;
-        const Fp4Row row =
-            fp4_row<D>(blk, slot - blk * a.block_size, head, side, a.num_kv_heads, a.block_size);
-        uint4 *rows = (side ? a.v : a.k) + (int64_t)tok * a.row_vecs + 2 * col;
-        uint2 *codes = reinterpret_cast<uint2 *>(a.kv + row.codes) + grp;
-        const float g = side ? a.gv : a.gk;
-        if constexpr (kWrite) {
-            const uint4 x0 = rows[0], x1 = rows[1];
-            const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            uint2 c;
-            const uint32_t s = fp4_quantise(x, g, side ? a.hv : a.hk, c);
-            *codes = c;
-            a.kv[row.scale + grp] = (uint8_t)s;
-        } else {
-            const uint2 c = *codes;
-            const uint32_t s = a.kv[row.scale + grp];
-            const uint32_t sc = e4m3x2_to_f16x2(s | s << 8);
-            uint32_t o[8];
+    constexpr int kTok = kTokens<kWrite>;
+    const int per_side = a.num_kv_heads * kGroups, cols = 2 * per_side;
+    const int width = min(cols, kThreads), at_once = kThreads / width;  // tokens of a block's pass
+    const int first = threadIdx.x / width;
+    if (first >= at_once) return;
+    const int bs = 1 << a.block_shift, step = gridDim.x * at_once;
+    for (int col = threadIdx.x - first * width; col < cols; col += width) {
+        const int side = col >= per_side, c = col - side * per_side;
+        const int head = c / kGroups, grp = c % kGroups;
+        const float g = side ? a.gv : a.gk, h = side ? a.hv : a.hk;
+        uint8_t *rows = (side ? a.v : a.k) + c * 32;
+        for (int tok = blockIdx.x * at_once + first; tok < a.num_tokens; tok += kTok * step) {
+            uint32_t x[kTok][8];
+            uint2 codes[kTok];
+            uint32_t scale[kTok];
+            int slot[kTok];
+            Fp4Row row[kTok];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t f[4];
-                e2m1x8_to_f16x8(k ? c.y : c.x, f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t p = hmul2_u32(f[j], sc);  // exact
-                    o[4 * k + j] = pack_bf16(__fmul_rn(f16_lo(p), g), __fmul_rn(f16_hi(p), g));
+            for (int k = 0; k < kTok; ++k) {
+                // (a sum past the last token may wrap: compared as unsigned)
+                const unsigned t = (unsigned)tok + (unsigned)k * (unsigned)step;
+                slot[k] = t < (unsigned)a.num_tokens ? a.slots[t] : -1;
+                if (slot[k] >= a.num_slots) {
+                    atomicOr(&g_err_cache_fp4, kErrOob);
+                    slot[k] = -1;
                 }
             }
-            rows[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            rows[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+                if (slot[k] < 0) continue;
+                row[k] = fp4_row<D>(slot[k] >> a.block_shift, slot[k] & (bs - 1), head, side,
+                                    a.num_kv_heads, bs);
+                if constexpr (kWrite) {
+                    const uint8_t *p = rows + (int64_t)(tok + k * step) * a.row_bytes;
+                    if (a.wide) {
+                        ld_32(x[k], p);
+                    } else {
+                        const uint4 y = reinterpret_cast<const uint4 *>(p)[0];
+                        const uint4 z = reinterpret_cast<const uint4 *>(p)[1];
+                        x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+                        x[k][4] = z.x, x[k][5] = z.y, x[k][6] = z.z, x[k][7] = z.w;
+                    }
+                } else {
+                    codes[k] = reinterpret_cast<const uint2 *>(a.kv + row[k].codes)[grp];
+                    scale[k] = a.kv[row[k].scale + grp];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+                if (slot[k] < 0) continue;
+                if constexpr (kWrite) {
+                    uint2 q;
+                    const uint32_t s = fp4_quantise(x[k], g, h, q);
+                    reinterpret_cast<uint2 *>(a.kv + row[k].codes)[grp] = q;
+                    a.kv[row[k].scale + grp] = (uint8_t)s;
+                } else {
+                    const uint32_t sc = e4m3x2_to_f16x2(scale[k] | scale[k] << 8);
+                    uint32_t o[8];
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        uint32_t f[4];
+                        e2m1x8_to_f16x8(w ? codes[k].y : codes[k].x, f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t p = hmul2_u32(f[j], sc);  // exact
+                            float lo = f16_lo(p), hi = f16_hi(p);
+                            mul2(lo, hi, g, g);
+                            o[4 * w + j] = pack_bf16(lo, hi);
+                        }
+                    }
+                    uint8_t *p = rows + (int64_t)(tok + k * step) * a.row_bytes;
+                    if (a.wide) {
+                        st_32(p, o);
+                    } else {
+                        reinterpret_cast<uint4 *>(p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        reinterpret_cast<uint4 *>(p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+            }
         }
     }
 }
@@ -93,26 +132,30 @@ cudaError_t launch_cache_fp4(bool write, void *kv_cache, const KvGeom &g, void *
                              int num_tokens, float k_scale, float v_scale, cudaStream_t stream) {
     RowsArgs a;
     a.kv = static_cast<uint8_t *>(kv_cache);
-    a.k = static_cast<uint4 *>(k_rows);
-    a.v = static_cast<uint4 *>(v_rows);
+    a.k = static_cast<uint8_t *>(k_rows);
+    a.v = static_cast<uint8_t *>(v_rows);
     a.slots = slots;
-    a.row_vecs = row_stride / 8;
+    a.row_bytes = row_stride * 2;
     a.num_slots = (int64_t)g.num_blocks * g.block_size;
     a.num_tokens = num_tokens;
-    a.block_size = g.block_size;
+    a.block_shift = g.block_size == 8 ? 3 : (g.block_size == 16 ? 4 : 5);
     a.num_kv_heads = g.num_kv_heads;
+    a.wide = (reinterpret_cast<uintptr_t>(k_rows) | reinterpret_cast<uintptr_t>(v_rows) |
+              (uintptr_t)a.row_bytes) % 32 == 0;
     a.gk = k_scale;
     a.gv = v_scale;
     a.hk = 6.f * k_scale;
     a.hv = 6.f * v_scale;
-    const long long work =
-        (long long)num_tokens * 2 * g.num_kv_heads * (g.head_size / kFp4Group);
-    const int blocks =
-        (int)std::min<long long>((work + 255) / 256, (long long)device_sm_count() * 8);
+    const int cols = 2 * g.num_kv_heads * (g.head_size / kFp4Group);
+    const int at_once = kThreads / std::min(cols, kThreads);
+    // Blocks that fill the GPU once, or a token per thread where that takes fewer.
+    const long long passes = ((long long)num_tokens + at_once - 1) / at_once;
+    const int blocks = (int)std::min<long long>(passes, (long long)device_sm_count() *
+                                                               (write ? kPerSm<true> : kPerSm<false>));
     g_launched.store(true);
     auto kern = g.head_size == 128 ? (write ? rows_kernel<128, true> : rows_kernel<128, false>)
                                    : (write ? rows_kernel<64, true> : rows_kernel<64, false>);
-    return launch_pdl(kern, dim3((unsigned)blocks), 256, 0, 1, stream, a);
+    return launch_pdl(kern, dim3((unsigned)blocks), kThreads, 0, 1, stream, a);
 }
 
 }  // namespace pa

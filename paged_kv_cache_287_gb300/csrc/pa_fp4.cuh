@@ -26,15 +26,18 @@ __device__ __forceinline__ Fp4Row fp4_row(int blk, int off, int head, int side, 
     return {base + off * (D / 2), base + block_size * (D / 2) + off * (D / 16)};
 }
 
-// Two fp32 values to two e2m1 codes (nearest, ties to the even code, saturating at 6), lo in
-// the low nibble of the result's byte.
-__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi) {
+// Eight fp32 values to e2m1 codes (nearest, ties to the even code, saturating at 6), the first
+// in the lowest four bits.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&v)[8]) {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-        "mov.b32 %0, {b, 0, 0, 0};\n\t}"
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
-        : "f"(hi), "f"(lo));
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
 }
 
@@ -75,6 +78,13 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
 // divisions binary32's, roundings to nearest even, saturating.  A group whose d is not above 0
 // (max|x| too small for a scale, or a NaN) has codes of 0; with a NaN its scale is NaN too, so
 // that all its elements are.
+//
+// A division for each element would be most of the work (390 instructions a warp and group
+// against 150).  With r within 2^-23 of 1 / d, x r (1 - 2^-20) and x r (1 + 2^-20) lie on both
+// sides of the quotient and of its rounding (off by 2^-23, and 2^-24 for each of r's factor, the
+// product and the quotient: five of sixteen 2^-24), and a code does not fall as the quotient's
+// magnitude rises: where both give one code it is the quotient's.  The others, next to a tie,
+// are divided.
 __device__ __forceinline__ uint32_t fp4_quantise(const uint32_t (&x)[8], float g, float h,
                                                  uint2 &codes) {
     uint32_t m = absmax_bf16x2(x[0], x[1]);
@@ -83,15 +93,45 @@ __device__ __forceinline__ uint32_t fp4_quantise(const uint32_t (&x)[8], float g
     m = absmax_bf16x2(m, m >> 16);
     const uint32_t s = pack_e4m3x2(__fdiv_rn(bf16_lo(m), h), 0.f) & 0xffu;
     const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s)), g);
-    uint32_t c[2] = {0u, 0u};
-    if (d > 0.f) {
+    codes = make_uint2(0u, 0u);
+    if (!(d > 0.f)) return s;
+    const bool tame = d > 1e-30f && d < 1e30f;  // 1 / d and the products are normal numbers
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    const float r0 = r * (1.f - 0x1p-20f), r1 = r * (1.f + 0x1p-20f);
+    uint32_t c[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            c[i >> 2] |= pack_e2m1x2(__fdiv_rn(bf16_lo(x[i]), d), __fdiv_rn(bf16_hi(x[i]), d))
-                         << (8 * (i & 3));
+    for (int w = 0; w < 2; ++w) {
+        float v[8], lo[8], hi[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            lo[i] = hi[i] = v[i] = bf16_lo(x[4 * w + i / 2]);
+            lo[i + 1] = hi[i + 1] = v[i + 1] = bf16_hi(x[4 * w + i / 2]);
+            mul2(lo[i], lo[i + 1], r0, r0);
+            mul2(hi[i], hi[i + 1], r1, r1);
+        }
+        c[w] = pack_e2m1x8(lo);
+        if (!tame || c[w] != pack_e2m1x8(hi)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], d);
+            c[w] = pack_e2m1x8(v);
+        }
     }
     codes = make_uint2(c[0], c[1]);
     return s;
+}
+
+// 32 bytes at once (p 32-byte aligned).
+__device__ __forceinline__ void ld_32(uint32_t (&v)[8], const void *p) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void st_32(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 }  // namespace pa

@@ -13,7 +13,8 @@
 // Bound by HBM: every element read once and written once.  A thread holds the two 8-element
 // vectors that a rotation pairs (t and t + rot_dim / 16 vectors further; or 2t and 2t + 1), so
 // rotating needs no exchange; head_size / 16 threads make a head, a warp 4 or 8 heads.  The
-// cosines and sines of a token stay in registers for all heads that a warp takes of it.
+// cosines and sines of a token stay in registers for all heads that a warp takes of it, and the
+// first heads' rows are asked for before the position is known.
 #include <algorithm>
 #include <atomic>
 
@@ -50,158 +51,258 @@ __device__ __forceinline__ uint2 fp8_codes(const uint4 &v, float scale) {
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
+#ifndef RT
+#define RT 256
+#define RB 4
+#define RW 32
+#define RD 5
+#endif
+constexpr int kThreads = RT;
+constexpr int kRing = RD;  // groups of heads in flight per warp
+
+__device__ __forceinline__ void copy16(uint4 *dst, const uint4 *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the last N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D, int kBits>
-__global__ void __launch_bounds__(256) qkv_rope_kernel(const QkvRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, RB) qkv_rope_kernel(const QkvRopeArgs a) {
+    constexpr int kLanes = D / 16;       // threads of a head
+    constexpr int kHeads = 32 / kLanes;  // heads of a warp
+    __shared__ uint4 ring[kThreads / 32][kRing][2][32];
+    __shared__ float weights[2][D];  // of q's and K's norms
     pdl_begin();
-    constexpr int kLanes = D / 16;            // threads of a head
-    constexpr int kHeads = 32 / kLanes;       // heads of a warp
     const int lane = threadIdx.x & 31, t = lane % kLanes;
-    const int warp = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int heads = a.num_heads + 2 * a.num_kv_heads;
+    const int warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int heads = a.num_heads + 2 * a.num_kv_heads, rot_heads = a.num_heads + a.num_kv_heads;
     const int groups = (heads + kHeads - 1) / kHeads;
     const int tok = warp / a.chunks, chunk = warp - tok * a.chunks;
-    if (tok >= a.num_tokens) return;
+    const bool idle = tok >= a.num_tokens;
 
-    // This thread's vectors of a rotated head, and its pairs' cosines and sines.
+    // This thread's vectors of a rotated head; of V's it takes 2t and 2t + 1.
     const bool turns = t < a.rot_dim / 16;
     const bool split = turns && !a.interleaved;
     const int v0 = split ? t : 2 * t, v1 = split ? t + a.rot_dim / 16 : 2 * t + 1;
+
+    // The first rows are asked for before what the rest hangs on.
+    const uint4 *row = reinterpret_cast<const uint4 *>(a.qkv + (int64_t)tok * a.row_stride);
+    uint4(*mine)[2][32] = ring[threadIdx.x >> 5];
+    auto fetch = [&](int grp, int at) {
+        const int hd = grp * kHeads + lane / kLanes;
+        if (hd < heads) {
+            const uint4 *head = row + hd * (D / 8);
+            copy16(&mine[at][0][lane], head + (hd < rot_heads ? v0 : 2 * t));
+            copy16(&mine[at][1][lane], head + (hd < rot_heads ? v1 : 2 * t + 1));
+        }
+        copies_commit();
+    };
+    int slot = -1, pos[8], axis[8];
+    if (!idle) {
+#pragma unroll
+        for (int k = 0; k < kRing; ++k) fetch(min(chunk + k * a.chunks, groups), k);
+        slot = a.slots[tok];
+        if (a.pair_axis) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) axis[i] = turns ? a.pair_axis[8 * t + i] : 0;
+        } else {
+            pos[0] = a.positions[tok];
+        }
+    }
+    if (a.q_weight || a.k_weight) {
+        for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+            const void *w = i < D ? a.q_weight : a.k_weight;
+            if (w) (&weights[0][0])[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i % D]);
+        }
+        __syncthreads();
+    }
+    if (idle) return;
+
+    // The cosines and sines of its pairs.
     float c[8], s[8];
-    bool bad = false;
+    bool bad = false, one = true;  // one: a single position for all pairs of this thread
+    if (a.pair_axis) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (axis[i] < 0 || axis[i] >= a.num_axes) {
+                atomicOr(&g_err_qkv_rope, kErrOob);
+                axis[i] = 0;
+            }
+            one = one && axis[i] == axis[0];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i > 0 && one) break;
+            pos[i] = a.positions[(int64_t)axis[i] * a.num_tokens + tok];
+            bad = bad || (turns && (pos[i] < 0 || pos[i] >= a.max_position));
+        }
+    } else {
+        bad = turns && (pos[0] < 0 || pos[0] >= a.max_position);
+    }
+    if (__any_sync(0xffffffffu, bad)) {  // nothing of this token is written
+        if (lane == 0) atomicOr(&g_err_qkv_rope, kErrOob);
+        copies_wait<0>();
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         c[i] = 1.f;
         s[i] = 0.f;
-        if (turns) {
-            int axis = a.pair_axis ? a.pair_axis[8 * t + i] : 0;
-            if (axis < 0 || axis >= a.num_axes) {
-                atomicOr(&g_err_qkv_rope, kErrOob);
-                axis = 0;
+    }
+    if (turns) {
+        if (one) {
+            const float4 *cs =
+                reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos[0] * a.rot_dim + 8 * t);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 p = cs[k], q = cs[a.rot_dim / 8 + k];
+                c[4 * k] = p.x, c[4 * k + 1] = p.y, c[4 * k + 2] = p.z, c[4 * k + 3] = p.w;
+                s[4 * k] = q.x, s[4 * k + 1] = q.y, s[4 * k + 2] = q.z, s[4 * k + 3] = q.w;
             }
-            const int pos = a.positions[(int64_t)axis * a.num_tokens + tok];
-            if (pos < 0 || pos >= a.max_position) {
-                bad = true;
-            } else {
-                const float *row = a.cos_sin + (int64_t)pos * a.rot_dim + 8 * t + i;
-                c[i] = row[0];
-                s[i] = row[a.rot_dim / 2];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float *cs = a.cos_sin + (int64_t)pos[i] * a.rot_dim + 8 * t + i;
+                c[i] = cs[0];
+                s[i] = cs[a.rot_dim / 2];
             }
         }
     }
-    if (__any_sync(0xffffffffu, bad)) {  // nothing of this token is written
-        if (lane == 0) atomicOr(&g_err_qkv_rope, kErrOob);
-        return;
-    }
-    int slot = a.slots[tok];
     if (slot >= 0 && slot >= (int64_t)a.num_blocks * a.block_size) {
         if (lane == 0) atomicOr(&g_err_qkv_rope, kErrOob);
         slot = -1;
     }
     const int blk = slot < 0 ? 0 : slot / a.block_size, off = slot - blk * a.block_size;
 
-    for (int grp = chunk; grp < groups; grp += a.chunks) {
-        const int hd = grp * kHeads + lane / kLanes;
-        const bool live = hd < heads;
-        const bool is_q = hd < a.num_heads, is_v = hd >= a.num_heads + a.num_kv_heads;
-        const int side = is_v ? 1 : 0, kvh = hd - a.num_heads - side * a.num_kv_heads;
-        const int i0 = is_v ? 2 * t : v0, i1 = is_v ? 2 * t + 1 : v1;
-        uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
-        if (live) {
-            const uint4 *row = reinterpret_cast<const uint4 *>(a.qkv + (int64_t)tok * a.row_stride +
-                                                               (int64_t)hd * D);
-            y0 = row[i0];
-            y1 = row[i1];
-        }
-        if (!is_v || !live) {
-            float x0[8], x1[8];
-            unpack8(y0, x0);
-            unpack8(y1, x1);
-            float r = 1.f;
-            const uint4 *w = static_cast<const uint4 *>(is_q ? a.q_weight : a.k_weight);
-            if (w) {
-                float q = 0.f;
+    // Pair i of this thread: elements i of its two vectors, or two neighbours.
+    auto turn = [&](float (&x0)[8], float (&x1)[8]) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) q += x0[i] * x0[i] + x1[i] * x1[i];
-                // The lanes of this head: those of V's heads are not here.
-                const uint32_t mask = ((1u << kLanes) - 1u) << (lane - t);
-#pragma unroll
-                for (int o = 1; o < kLanes; o <<= 1) q += __shfl_xor_sync(mask, q, o);
-                r = 1.f / sqrtf(q * (1.f / D) + a.eps);
-                float w0[8], w1[8];
-                unpack8(w[i0], w0);
-                unpack8(w[i1], w1);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x0[i] = x0[i] * r * w0[i];
-                    x1[i] = x1[i] * r * w1[i];
-                }
-            }
-            if (turns) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // pair i of this thread: (x0[i], x1[i]), or two neighbours
-                    float &p = split ? x0[i] : (i < 4 ? x0[2 * (i & 3)] : x1[2 * (i & 3)]);
-                    float &q = split ? x1[i] : (i < 4 ? x0[2 * (i & 3) + 1] : x1[2 * (i & 3) + 1]);
-                    const float pc = __fmul_rn(p, c[i]), qs = __fmul_rn(q, s[i]);
-                    const float qc = __fmul_rn(q, c[i]), ps = __fmul_rn(p, s[i]);
-                    p = __fsub_rn(pc, qs);
-                    q = __fadd_rn(qc, ps);
-                }
-            }
-            y0 = pack8(x0);
-            y1 = pack8(x1);
-        }
-        __syncwarp();
-        if (live && is_q) {
-            uint4 *o = reinterpret_cast<uint4 *>(a.q_out) +
-                       ((int64_t)tok * a.num_heads + hd) * (D / 8);
-            o[i0] = y0;
-            o[i1] = y1;
-        }
-        if constexpr (kBits == 4) {
-            // A scale's 16 elements are vectors 2t and 2t + 1: fetch them from where they are.
-            const int half = a.rot_dim / 16;
-            uint32_t x[8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int v = 2 * t + k;
-                int from = t, second = k;  // lane of the head, and which of its two vectors
-                if (!is_v && !a.interleaved && v < 2 * half) {
-                    from = v < half ? v : v - half;
-                    second = v < half ? 0 : 1;
-                }
-                const int src = lane - t + from;
-                const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w};
-                const uint32_t w1[4] = {y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t p = __shfl_sync(0xffffffffu, w0[i], src);
-                    const uint32_t q = __shfl_sync(0xffffffffu, w1[i], src);
-                    x[4 * k + i] = second ? q : p;
-                }
-            }
-            if (live && !is_q && slot >= 0) {
-                const Fp4Row row = fp4_row<D>(blk, off, kvh, side, a.num_kv_heads, a.block_size);
-                const float g = side ? a.v_scale : a.k_scale;
-                uint2 codes;
-                uint8_t *kv = static_cast<uint8_t *>(a.kv);
-                kv[row.scale + t] = (uint8_t)fp4_quantise(x, g, 6.f * g, codes);
-                reinterpret_cast<uint2 *>(kv + row.codes)[t] = codes;
-            }
-        } else if (live && !is_q && slot >= 0) {
-            const int64_t row =
-                ((((int64_t)blk * 2 + side) * a.num_kv_heads + kvh) * a.block_size + off) * (D / 8);
-            if constexpr (kBits == 16) {
-                uint4 *kv = static_cast<uint4 *>(a.kv) + row;
-                kv[i0] = y0;
-                kv[i1] = y1;
+        for (int i = 0; i < 8; i += 2) {
+            float p0, p1, q0, q1;  // pairs i and i + 1
+            if (split) {
+                p0 = x0[i], p1 = x0[i + 1], q0 = x1[i], q1 = x1[i + 1];
             } else {
-                uint2 *kv = static_cast<uint2 *>(a.kv) + row;
-                const float g = side ? a.v_scale : a.k_scale;
-                kv[i0] = fp8_codes(y0, g);
-                kv[i1] = fp8_codes(y1, g);
+                const float *e = i < 4 ? x0 + 2 * i : x1 + 2 * (i - 4);
+                p0 = e[0], q0 = e[1], p1 = e[2], q1 = e[3];
+            }
+            float pc0 = p0, pc1 = p1, qs0 = q0, qs1 = q1, qc0 = q0, qc1 = q1, ps0 = p0, ps1 = p1;
+            mul2(pc0, pc1, c[i], c[i + 1]);
+            mul2(qs0, qs1, s[i], s[i + 1]);
+            mul2(qc0, qc1, c[i], c[i + 1]);
+            mul2(ps0, ps1, s[i], s[i + 1]);
+            fma2(pc0, pc1, qs0, qs1, -1.f, -1.f, pc0, pc1);  // pc - qs, rounded once
+            add2(qc0, qc1, ps0, ps1);
+            if (split) {
+                x0[i] = pc0, x0[i + 1] = pc1, x1[i] = qc0, x1[i + 1] = qc1;
+            } else {
+                float *e = i < 4 ? x0 + 2 * i : x1 + 2 * (i - 4);
+                e[0] = pc0, e[1] = qc0, e[2] = pc1, e[3] = qc1;
             }
         }
+    };
+
+    int at = 0;
+    for (int grp = chunk; grp < groups; grp += a.chunks) {
+            const int hd = grp * kHeads + lane / kLanes;
+            const bool live = hd < heads, is_q = hd < a.num_heads, is_v = hd >= rot_heads;
+            const int i0 = is_v ? 2 * t : v0, i1 = is_v ? 2 * t + 1 : v1;
+            copies_wait<kRing - 1>();
+            uint4 y0 = mine[at][0][lane], y1 = mine[at][1][lane];
+            if (!is_v) {
+                float x0[8], x1[8];
+                unpack8(y0, x0);
+                unpack8(y1, x1);
+                if (is_q ? a.q_weight : a.k_weight) {
+                    float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        fma2(sum0, sum1, x0[i], x0[i + 1], x0[i], x0[i + 1], sum0, sum1);
+                        fma2(sum0, sum1, x1[i], x1[i + 1], x1[i], x1[i + 1], sum0, sum1);
+                    }
+                    float sum = sum0 + sum1;
+                    // The lanes of this head: those of V's heads are not here.
+                    const uint32_t mask = ((1u << kLanes) - 1u) << (lane - t);
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+                    const float r = rsqrtf(sum * (1.f / D) + a.eps);
+                    const float *w = weights[is_q ? 0 : 1];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 p = *reinterpret_cast<const float2 *>(w + 8 * i0 + i);
+                        const float2 q = *reinterpret_cast<const float2 *>(w + 8 * i1 + i);
+                        mul2(x0[i], x0[i + 1], r, r);
+                        mul2(x1[i], x1[i + 1], r, r);
+                        mul2(x0[i], x0[i + 1], p.x, p.y);
+                        mul2(x1[i], x1[i + 1], q.x, q.y);
+                    }
+                }
+                if (turns) turn(x0, x1);
+                y0 = pack8(x0);
+                y1 = pack8(x1);
+            }
+            fetch(min(grp + kRing * a.chunks, groups), at);
+            at = at + 1 == kRing ? 0 : at + 1;
+            __syncwarp();
+            if (live && is_q) {
+                uint4 *o = reinterpret_cast<uint4 *>(a.q_out) +
+                           ((int64_t)tok * a.num_heads + hd) * (D / 8);
+                o[i0] = y0;
+                o[i1] = y1;
+            }
+            if (slot < 0) continue;
+            const int side = is_v ? 1 : 0, kvh = hd - a.num_heads - side * a.num_kv_heads;
+            const float g = side ? a.v_scale : a.k_scale;
+            if constexpr (kBits == 4) {
+                // A scale's 16 elements are vectors 2t and 2t + 1: of a head turned in halves
+                // they are fetched from where they are.
+                uint32_t x[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                if (!a.interleaved && __any_sync(0xffffffffu, live && !is_q && !is_v)) {
+                    const int half = a.rot_dim / 16;
+                    const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w};
+                    const uint32_t w1[4] = {y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int v = 2 * t + e;
+                        const bool moved = !is_v && v < 2 * half;
+                        const int src = lane - t + (!moved ? t : (v < half ? v : v - half));
+                        const bool second = moved ? v >= half : e != 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t p = __shfl_sync(0xffffffffu, w0[i], src);
+                            const uint32_t q = __shfl_sync(0xffffffffu, w1[i], src);
+                            x[4 * e + i] = second ? q : p;
+                        }
+                    }
+                }
+                if (live && !is_q) {
+                    const Fp4Row to =
+                        fp4_row<D>(blk, off, kvh, side, a.num_kv_heads, a.block_size);
+                    uint2 codes;
+                    uint8_t *kv = static_cast<uint8_t *>(a.kv);
+                    kv[to.scale + t] = (uint8_t)fp4_quantise(x, g, 6.f * g, codes);
+                    reinterpret_cast<uint2 *>(kv + to.codes)[t] = codes;
+                }
+            } else if (live && !is_q) {
+                const int64_t to =
+                    ((((int64_t)blk * 2 + side) * a.num_kv_heads + kvh) * a.block_size + off) *
+                    (D / 8);
+                if constexpr (kBits == 16) {
+                    uint4 *kv = static_cast<uint4 *>(a.kv) + to;
+                    kv[i0] = y0;
+                    kv[i1] = y1;
+                } else {
+                    uint2 *kv = static_cast<uint2 *>(a.kv) + to;
+                    kv[i0] = fp8_codes(y0, g);
+                    kv[i1] = fp8_codes(y1, g);
+                }
+            }
     }
 }
 
@@ -215,13 +316,13 @@ cudaError_t launch_qkv_rope(QkvRopeArgs a, int head_size, int kv_bits, cudaStrea
     const int per_warp = 32 / (head_size / 16);
     const int groups = (a.num_heads + 2 * a.num_kv_heads + per_warp - 1) / per_warp;
     // A warp takes a token's heads, or a share of them while that leaves warps idle.
-    const long long want = (long long)device_sm_count() * 32;
+    const long long want = (long long)device_sm_count() * RW;
     a.chunks = (int)std::min<long long>(groups, (want + a.num_tokens - 1) / a.num_tokens);
     const long long warps = (long long)a.num_tokens * a.chunks;
-    const dim3 grid((unsigned)((warps + 7) / 8));
+    const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     g_launched.store(true);
     auto pick = [&](auto k128, auto k64) {
-        return launch_pdl(head_size == 128 ? k128 : k64, grid, 256, 0, 1, stream, a);
+        return launch_pdl(head_size == 128 ? k128 : k64, grid, kThreads, 0, 1, stream, a);
     };
     if (kv_bits == 16) return pick(qkv_rope_kernel<128, 16>, qkv_rope_kernel<64, 16>);
     if (kv_bits == 8) return pick(qkv_rope_kernel<128, 8>, qkv_rope_kernel<64, 8>);
