@@ -994,39 +994,49 @@ def pa_qkv_rope_write(q_out: torch.Tensor, qkv: torch.Tensor, kv_cache: torch.Te
     kv_scales = (k_scale, v_scale)."""
     try:  # every tensor at once; on failure the per-argument checks name the culprit
         dev = kv_cache.get_device()
+        dt = kv_cache.dtype
         N, Hq, D = q_out.shape
-        NB, bs, Hkv, bits = _rope_geom(q_out, kv_cache)
-        axes, cols = positions.shape if positions.dim() == 2 else (1, positions.shape[0])
+        if kv_cache.dim() == 5:
+            NB, two, Hkv, bs, rest = kv_cache.shape
+            rest -= D
+            bits = 16 if dt is _BF16 else 8
+        else:
+            NB, Hkv, two, tile = kv_cache.shape
+            bs, rest = divmod(tile * 16, D * 9)
+            bits = 4
+        ps = positions.shape
+        axes, cols = ps if len(ps) == 2 else (1, *ps)
         max_pos, rot = cos_sin.shape
-        rows, width = qkv.shape
+        width = (Hq + 2 * Hkv) * D
         s0, s1 = qkv.stride()
-        ok = (dev >= 0 and rows == N and cols == N and width == (Hq + 2 * Hkv) * D and s1 == 1
-              and (s0 >= width or N <= 1)
-              and slot_mapping.shape == (N,)
+        ok = (two == 2 and not rest and dev >= 0 and (dt is _U8 or bits == 16)
+              and kv_cache.is_contiguous()
+              and qkv.shape == (N, width) and cols == N and s1 == 1 and (s0 >= width or N <= 1)
               and q_out.dtype is _BF16 and q_out.get_device() == dev and q_out.is_contiguous()
               and qkv.dtype is _BF16 and qkv.get_device() == dev
-              and slot_mapping.dtype is _I32 and slot_mapping.get_device() == dev
-              and slot_mapping.is_contiguous()
+              and slot_mapping.shape == (N,) and slot_mapping.dtype is _I32
+              and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()
               and positions.dtype is _I32 and positions.get_device() == dev
               and positions.is_contiguous()
               and cos_sin.dtype is _F32 and cos_sin.get_device() == dev
               and cos_sin.is_contiguous()
               and (axes == 1 or pair_axis is not None))
         qw = kw = pa = 0
-        for w in (q_weight, k_weight):
-            ok = ok and (w is None or w.shape == (D,) and w.dtype is _BF16
-                         and w.get_device() == dev and w.is_contiguous())
         if q_weight is not None:
+            ok = (ok and q_weight.shape == (D,) and q_weight.dtype is _BF16
+                  and q_weight.get_device() == dev and q_weight.is_contiguous())
             qw = q_weight.data_ptr()
         if k_weight is not None:
+            ok = (ok and k_weight.shape == (D,) and k_weight.dtype is _BF16
+                  and k_weight.get_device() == dev and k_weight.is_contiguous())
             kw = k_weight.data_ptr()
         if pair_axis is not None:
-            ok = ok and (pair_axis.shape == (rot // 2,) and pair_axis.dtype is _I32
-                         and pair_axis.get_device() == dev and pair_axis.is_contiguous())
+            ok = (ok and pair_axis.shape == (rot // 2,) and pair_axis.dtype is _I32
+                  and pair_axis.get_device() == dev and pair_axis.is_contiguous())
             pa = pair_axis.data_ptr()
         if N <= 1:
             s0 = width
-    except (AttributeError, TypeError, ValueError):
+    except (AttributeError, TypeError, ValueError, ZeroDivisionError):
         ok = False
     if not ok:
         _need(q_out, "q_out", _BF16, 3)

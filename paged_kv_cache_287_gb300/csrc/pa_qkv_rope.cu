@@ -12,9 +12,13 @@
 //
 // Bound by HBM: every element read once and written once.  A thread holds the two 8-element
 // vectors that a rotation pairs (t and t + rot_dim / 16 vectors further; or 2t and 2t + 1), so
-// rotating needs no exchange; head_size / 16 threads make a head, a warp 4 or 8 heads.  The
-// cosines and sines of a token stay in registers for all heads that a warp takes of it, and the
-// first heads' rows are asked for before the position is known.
+// rotating needs no exchange; head_size / 16 threads make a head, a warp a group of 4 or 8 heads
+// (1 KB).  A warp takes a token, whose cosines and sines stay in registers for all its heads,
+// and copies its next groups into shared memory ahead (each thread its own vectors, so nothing
+// is synchronised).  4344 tokens of 32 + 2 x 8 heads of 128 with norms and three axes: 21.7 us,
+// 5.0 TB/s (75 % of the copy rate; a fill alone writes 3.6 TB/s here); with the rows loaded to
+// registers two groups at a time 28.8, with rings of 4, 5, 8 groups 22.1, 22.3, 27.8 (fewer
+// blocks), with a token shared by two warps 25.3, with blocks of 128 and 64 threads 22.2, 22.8.
 #include <algorithm>
 #include <atomic>
 
@@ -27,38 +31,50 @@ namespace {
 __device__ unsigned g_err_qkv_rope;
 std::atomic<bool> g_launched{false};
 
-// One 8-element bf16 vector as 8 floats, and back.
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The 16 elements of a thread as 8 pairs (p[i], q[i]): the elements of its two vectors, or
+// neighbours; and back.
+template <bool kNeighbours>
+__device__ __forceinline__ void unpack(const uint4 &y0, const uint4 &y1, float (&p)[8],
+                                       float (&q)[8]) {
+    const uint32_t w[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (kNeighbours) {
+            p[i] = bf16_lo(w[i]);
+            q[i] = bf16_hi(w[i]);
+        } else {
+            float(&x)[8] = i < 4 ? p : q;
+            x[2 * i % 8] = bf16_lo(w[i]);
+            x[2 * i % 8 + 1] = bf16_hi(w[i]);
+        }
     }
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                      pack_bf16(x[6], x[7]));
+template <bool kNeighbours>
+__device__ __forceinline__ void pack(const float (&p)[8], const float (&q)[8], uint4 &y0,
+                                     uint4 &y1) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float(&x)[8] = i < 4 ? p : q;
+        w[i] = kNeighbours ? pack_bf16(p[i], q[i]) : pack_bf16(x[2 * i % 8], x[2 * i % 8 + 1]);
+    }
+    y0 = make_uint4(w[0], w[1], w[2], w[3]);
+    y1 = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 __device__ __forceinline__ uint2 fp8_codes(const uint4 &v, float scale) {
-    float x[8];
-    unpack8(v, x);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        c[i] = pack_e4m3x2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
+        c[i] = pack_e4m3x2(__fdiv_rn(bf16_lo(w[i]), scale), __fdiv_rn(bf16_hi(w[i]), scale));
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-#ifndef RT
-#define RT 256
-#define RB 4
-#define RW 32
-#define RD 5
-#endif
-constexpr int kThreads = RT;
-constexpr int kRing = RD;  // groups of heads in flight per warp
+constexpr int kThreads = 256;
+constexpr int kRing = 3;        // groups of heads (1 KB each) in flight per warp
+constexpr int kPerSm = 4;       // blocks; 32 warps of 64 registers
+constexpr int kWarpsPerSm = 24; // a token's heads are shared out while there are fewer warps
 
 __device__ __forceinline__ void copy16(uint4 *dst, const uint4 *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
@@ -73,12 +89,13 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D, int kBits>
-__global__ void __launch_bounds__(kThreads, RB) qkv_rope_kernel(const QkvRopeArgs a) {
+// kNeighbours: pairs are neighbours (interleaved).
+template <int D, int kBits, bool kNeighbours>
+__global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRopeArgs a) {
     constexpr int kLanes = D / 16;       // threads of a head
     constexpr int kHeads = 32 / kLanes;  // heads of a warp
     __shared__ uint4 ring[kThreads / 32][kRing][2][32];
-    __shared__ float weights[2][D];  // of q's and K's norms
+    __shared__ __align__(16) float weights[2][D];  // of q's and K's norms
     pdl_begin();
     const int lane = threadIdx.x & 31, t = lane % kLanes;
     const int warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -89,8 +106,9 @@ __global__ void __launch_bounds__(kThreads, RB) qkv_rope_kernel(const QkvRopeArg
 
     // This thread's vectors of a rotated head; of V's it takes 2t and 2t + 1.
     const bool turns = t < a.rot_dim / 16;
-    const bool split = turns && !a.interleaved;
+    const bool split = !kNeighbours && turns;
     const int v0 = split ? t : 2 * t, v1 = split ? t + a.rot_dim / 16 : 2 * t + 1;
+    const int first = lane / kLanes * (D / 8);  // its head's first vector in a group's 64
 
     // The first rows are asked for before what the rest hangs on.
     const uint4 *row = reinterpret_cast<const uint4 *>(a.qkv + (int64_t)tok * a.row_stride);
@@ -98,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, RB) qkv_rope_kernel(const QkvRopeArg
     auto fetch = [&](int grp, int at) {
         const int hd = grp * kHeads + lane / kLanes;
         if (hd < heads) {
-            const uint4 *head = row + hd * (D / 8);
+            const uint4 *head = row + 64 * grp + first;
             copy16(&mine[at][0][lane], head + (hd < rot_heads ? v0 : 2 * t));
             copy16(&mine[at][1][lane], head + (hd < rot_heads ? v1 : 2 * t + 1));
         }
@@ -117,9 +135,13 @@ __global__ void __launch_bounds__(kThreads, RB) qkv_rope_kernel(const QkvRopeArg
         }
     }
     if (a.q_weight || a.k_weight) {
+        // (neighbours: of each 16 the first ones of the pairs, then the second ones)
         for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
             const void *w = i < D ? a.q_weight : a.k_weight;
-            if (w) (&weights[0][0])[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[i % D]);
+            const int from = kNeighbours ? (i & ~15) | (2 * i & 14) | (i >> 3 & 1) : i;
+            if (w)
+                (&weights[0][0])[i] =
+                    __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[from % D]);
         }
         __syncthreads();
     }
@@ -180,129 +202,116 @@ __global__ void __launch_bounds__(kThreads, RB) qkv_rope_kernel(const QkvRopeArg
         slot = -1;
     }
     const int blk = slot < 0 ? 0 : slot / a.block_size, off = slot - blk * a.block_size;
-
-    // Pair i of this thread: elements i of its two vectors, or two neighbours.
-    auto turn = [&](float (&x0)[8], float (&x1)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float p0, p1, q0, q1;  // pairs i and i + 1
-            if (split) {
-                p0 = x0[i], p1 = x0[i + 1], q0 = x1[i], q1 = x1[i + 1];
-            } else {
-                const float *e = i < 4 ? x0 + 2 * i : x1 + 2 * (i - 4);
-                p0 = e[0], q0 = e[1], p1 = e[2], q1 = e[3];
-            }
-            float pc0 = p0, pc1 = p1, qs0 = q0, qs1 = q1, qc0 = q0, qc1 = q1, ps0 = p0, ps1 = p1;
-            mul2(pc0, pc1, c[i], c[i + 1]);
-            mul2(qs0, qs1, s[i], s[i + 1]);
-            mul2(qc0, qc1, c[i], c[i + 1]);
-            mul2(ps0, ps1, s[i], s[i + 1]);
-            fma2(pc0, pc1, qs0, qs1, -1.f, -1.f, pc0, pc1);  // pc - qs, rounded once
-            add2(qc0, qc1, ps0, ps1);
-            if (split) {
-                x0[i] = pc0, x0[i + 1] = pc1, x1[i] = qc0, x1[i + 1] = qc1;
-            } else {
-                float *e = i < 4 ? x0 + 2 * i : x1 + 2 * (i - 4);
-                e[0] = pc0, e[1] = qc0, e[2] = pc1, e[3] = qc1;
-            }
-        }
-    };
+    uint4 *q_out = static_cast<uint4 *>(a.q_out) + (int64_t)tok * a.num_heads * (D / 8);
 
     int at = 0;
     for (int grp = chunk; grp < groups; grp += a.chunks) {
-            const int hd = grp * kHeads + lane / kLanes;
-            const bool live = hd < heads, is_q = hd < a.num_heads, is_v = hd >= rot_heads;
-            const int i0 = is_v ? 2 * t : v0, i1 = is_v ? 2 * t + 1 : v1;
-            copies_wait<kRing - 1>();
-            uint4 y0 = mine[at][0][lane], y1 = mine[at][1][lane];
-            if (!is_v) {
-                float x0[8], x1[8];
-                unpack8(y0, x0);
-                unpack8(y1, x1);
-                if (is_q ? a.q_weight : a.k_weight) {
-                    float sum0 = 0.f, sum1 = 0.f;
+        const int hd = grp * kHeads + lane / kLanes;
+        const bool live = hd < heads, is_q = hd < a.num_heads, is_v = hd >= rot_heads;
+        const int i0 = is_v ? 2 * t : v0, i1 = is_v ? 2 * t + 1 : v1;
+        copies_wait<kRing - 1>();
+        uint4 y0 = mine[at][0][lane], y1 = mine[at][1][lane];
+        if (!is_v) {
+            float p[8], q[8];
+            unpack<kNeighbours>(y0, y1, p, q);
+            if (is_q ? a.q_weight : a.k_weight) {
+                float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        fma2(sum0, sum1, x0[i], x0[i + 1], x0[i], x0[i + 1], sum0, sum1);
-                        fma2(sum0, sum1, x1[i], x1[i + 1], x1[i], x1[i + 1], sum0, sum1);
-                    }
-                    float sum = sum0 + sum1;
-                    // The lanes of this head: those of V's heads are not here.
-                    const uint32_t mask = ((1u << kLanes) - 1u) << (lane - t);
-#pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
-                    const float r = rsqrtf(sum * (1.f / D) + a.eps);
-                    const float *w = weights[is_q ? 0 : 1];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float2 p = *reinterpret_cast<const float2 *>(w + 8 * i0 + i);
-                        const float2 q = *reinterpret_cast<const float2 *>(w + 8 * i1 + i);
-                        mul2(x0[i], x0[i + 1], r, r);
-                        mul2(x1[i], x1[i + 1], r, r);
-                        mul2(x0[i], x0[i + 1], p.x, p.y);
-                        mul2(x1[i], x1[i + 1], q.x, q.y);
-                    }
+                for (int i = 0; i < 8; i += 2) {
+                    fma2(sum0, sum1, p[i], p[i + 1], p[i], p[i + 1], sum0, sum1);
+                    fma2(sum0, sum1, q[i], q[i + 1], q[i], q[i + 1], sum0, sum1);
                 }
-                if (turns) turn(x0, x1);
-                y0 = pack8(x0);
-                y1 = pack8(x1);
-            }
-            fetch(min(grp + kRing * a.chunks, groups), at);
-            at = at + 1 == kRing ? 0 : at + 1;
-            __syncwarp();
-            if (live && is_q) {
-                uint4 *o = reinterpret_cast<uint4 *>(a.q_out) +
-                           ((int64_t)tok * a.num_heads + hd) * (D / 8);
-                o[i0] = y0;
-                o[i1] = y1;
-            }
-            if (slot < 0) continue;
-            const int side = is_v ? 1 : 0, kvh = hd - a.num_heads - side * a.num_kv_heads;
-            const float g = side ? a.v_scale : a.k_scale;
-            if constexpr (kBits == 4) {
-                // A scale's 16 elements are vectors 2t and 2t + 1: of a head turned in halves
-                // they are fetched from where they are.
-                uint32_t x[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-                if (!a.interleaved && __any_sync(0xffffffffu, live && !is_q && !is_v)) {
-                    const int half = a.rot_dim / 16;
-                    const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w};
-                    const uint32_t w1[4] = {y1.x, y1.y, y1.z, y1.w};
+                float sum = sum0 + sum1;
+                // The lanes of this head: those of V's heads are not here.
+                const uint32_t mask = ((1u << kLanes) - 1u) << (lane - t);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int v = 2 * t + e;
-                        const bool moved = !is_v && v < 2 * half;
-                        const int src = lane - t + (!moved ? t : (v < half ? v : v - half));
-                        const bool second = moved ? v >= half : e != 0;
+                for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+                const float r = rsqrtf(sum * (1.f / D) + a.eps);
+                const float4 *wp = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i0);
+                const float4 *wq = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i1);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t p = __shfl_sync(0xffffffffu, w0[i], src);
-                            const uint32_t q = __shfl_sync(0xffffffffu, w1[i], src);
-                            x[4 * e + i] = second ? q : p;
-                        }
-                    }
-                }
-                if (live && !is_q) {
-                    const Fp4Row to =
-                        fp4_row<D>(blk, off, kvh, side, a.num_kv_heads, a.block_size);
-                    uint2 codes;
-                    uint8_t *kv = static_cast<uint8_t *>(a.kv);
-                    kv[to.scale + t] = (uint8_t)fp4_quantise(x, g, 6.f * g, codes);
-                    reinterpret_cast<uint2 *>(kv + to.codes)[t] = codes;
-                }
-            } else if (live && !is_q) {
-                const int64_t to =
-                    ((((int64_t)blk * 2 + side) * a.num_kv_heads + kvh) * a.block_size + off) *
-                    (D / 8);
-                if constexpr (kBits == 16) {
-                    uint4 *kv = static_cast<uint4 *>(a.kv) + to;
-                    kv[i0] = y0;
-                    kv[i1] = y1;
-                } else {
-                    uint2 *kv = static_cast<uint2 *>(a.kv) + to;
-                    kv[i0] = fp8_codes(y0, g);
-                    kv[i1] = fp8_codes(y1, g);
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 u = wp[i / 4], v = wq[i / 4];
+                    mul2(p[i], p[i + 1], r, r);
+                    mul2(p[i + 2], p[i + 3], r, r);
+                    mul2(q[i], q[i + 1], r, r);
+                    mul2(q[i + 2], q[i + 3], r, r);
+                    mul2(p[i], p[i + 1], u.x, u.y);
+                    mul2(p[i + 2], p[i + 3], u.z, u.w);
+                    mul2(q[i], q[i + 1], v.x, v.y);
+                    mul2(q[i + 2], q[i + 3], v.z, v.w);
                 }
             }
+            if (turns) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    float pc0 = p[i], pc1 = p[i + 1], ps0 = p[i], ps1 = p[i + 1];
+                    float qc0 = q[i], qc1 = q[i + 1], qs0 = q[i], qs1 = q[i + 1];
+                    mul2(pc0, pc1, c[i], c[i + 1]);
+                    mul2(ps0, ps1, s[i], s[i + 1]);
+                    mul2(qc0, qc1, c[i], c[i + 1]);
+                    mul2(qs0, qs1, s[i], s[i + 1]);
+                    fma2(p[i], p[i + 1], qs0, qs1, -1.f, -1.f, pc0, pc1);  // pc - qs, one rounding
+                    add2(qc0, qc1, ps0, ps1);
+                    q[i] = qc0;
+                    q[i + 1] = qc1;
+                }
+            }
+            pack<kNeighbours>(p, q, y0, y1);
+        }
+        fetch(min(grp + kRing * a.chunks, groups), at);
+        at = at + 1 == kRing ? 0 : at + 1;
+        __syncwarp();
+        if (live && is_q) {
+            uint4 *o = q_out + 64 * grp + first;
+            o[i0] = y0;
+            o[i1] = y1;
+        }
+        if (slot < 0 || (grp + 1) * kHeads <= a.num_heads) continue;  // no K or V here
+        const int side = is_v ? 1 : 0, kvh = hd - a.num_heads - side * a.num_kv_heads;
+        const float g = side ? a.v_scale : a.k_scale;
+        if constexpr (kBits == 4) {
+            // A scale's 16 elements are vectors 2t and 2t + 1: of a head turned in halves they
+            // are fetched from where they are.
+            uint32_t x[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+            if (!kNeighbours && __any_sync(0xffffffffu, live && !is_q && !is_v)) {
+                const int half = a.rot_dim / 16;
+                const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w};
+                const uint32_t w1[4] = {y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int v = 2 * t + e;
+                    const bool moved = !is_v && v < 2 * half;
+                    const int src = lane - t + (!moved ? t : (v < half ? v : v - half));
+                    const bool second = moved ? v >= half : e != 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t p = __shfl_sync(0xffffffffu, w0[i], src);
+                        const uint32_t q = __shfl_sync(0xffffffffu, w1[i], src);
+                        x[4 * e + i] = second ? q : p;
+                    }
+                }
+            }
+            if (live && !is_q) {
+                const Fp4Row to = fp4_row<D>(blk, off, kvh, side, a.num_kv_heads, a.block_size);
+                uint2 codes;
+                uint8_t *kv = static_cast<uint8_t *>(a.kv);
+                kv[to.scale + t] = (uint8_t)fp4_quantise(x, g, 6.f * g, codes);
+                reinterpret_cast<uint2 *>(kv + to.codes)[t] = codes;
+            }
+        } else if (live && !is_q) {
+            const int64_t to =
+                ((((int64_t)blk * 2 + side) * a.num_kv_heads + kvh) * a.block_size + off) * (D / 8);
+            if constexpr (kBits == 16) {
+                uint4 *kv = static_cast<uint4 *>(a.kv) + to;
+                kv[i0] = y0;
+                kv[i1] = y1;
+            } else {
+                uint2 *kv = static_cast<uint2 *>(a.kv) + to;
+                kv[i0] = fp8_codes(y0, g);
+                kv[i1] = fp8_codes(y1, g);
+            }
+        }
     }
 }
 
@@ -316,17 +325,24 @@ cudaError_t launch_qkv_rope(QkvRopeArgs a, int head_size, int kv_bits, cudaStrea
     const int per_warp = 32 / (head_size / 16);
     const int groups = (a.num_heads + 2 * a.num_kv_heads + per_warp - 1) / per_warp;
     // A warp takes a token's heads, or a share of them while that leaves warps idle.
-    const long long want = (long long)device_sm_count() * RW;
+    const long long want = (long long)device_sm_count() * kWarpsPerSm;
     a.chunks = (int)std::min<long long>(groups, (want + a.num_tokens - 1) / a.num_tokens);
     const long long warps = (long long)a.num_tokens * a.chunks;
     const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     g_launched.store(true);
-    auto pick = [&](auto k128, auto k64) {
-        return launch_pdl(head_size == 128 ? k128 : k64, grid, kThreads, 0, 1, stream, a);
+    auto pick = [&](auto k128, auto k64, auto n128, auto n64) {
+        return launch_pdl(a.interleaved ? (head_size == 128 ? n128 : n64)
+                                        : (head_size == 128 ? k128 : k64),
+                          grid, kThreads, 0, 1, stream, a);
     };
-    if (kv_bits == 16) return pick(qkv_rope_kernel<128, 16>, qkv_rope_kernel<64, 16>);
-    if (kv_bits == 8) return pick(qkv_rope_kernel<128, 8>, qkv_rope_kernel<64, 8>);
-    return pick(qkv_rope_kernel<128, 4>, qkv_rope_kernel<64, 4>);
+    if (kv_bits == 16)
+        return pick(qkv_rope_kernel<128, 16, false>, qkv_rope_kernel<64, 16, false>,
+                    qkv_rope_kernel<128, 16, true>, qkv_rope_kernel<64, 16, true>);
+    if (kv_bits == 8)
+        return pick(qkv_rope_kernel<128, 8, false>, qkv_rope_kernel<64, 8, false>,
+                    qkv_rope_kernel<128, 8, true>, qkv_rope_kernel<64, 8, true>);
+    return pick(qkv_rope_kernel<128, 4, false>, qkv_rope_kernel<64, 4, false>,
+                qkv_rope_kernel<128, 4, true>, qkv_rope_kernel<64, 4, true>);
 }
 
 }  // namespace pa
