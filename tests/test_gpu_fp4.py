@@ -141,6 +141,39 @@ def test_read_gives_the_values(d, bs, hkv, n):
         assert (got._base[:, hkv:] == 7).all()
 
 
+@pytest.mark.parametrize("hkv, d, shift", [(40, 128, 8), (255, 64, 0), (40, 128, 16), (3, 64, 24)])
+def test_many_heads_and_rows_off_the_wide_boundary(hkv, d, shift):
+    """More columns than a block has threads; rows 16 bytes off a 32-byte boundary."""
+    gen = torch.Generator().manual_seed(hkv)
+    n, bs = 11, 16
+    wide = bf16((2, n, hkv * d + 32), gen)
+    k, v = (x[:, shift:shift + hkv * d].unflatten(1, (hkv, d)) for x in wide)
+    kd, vd = (x[:, shift:shift + hkv * d].unflatten(1, (hkv, d)) for x in wide.to(DEV))
+    pool = random_pool(4, hkv, bs, d, gen)
+    slots = torch.randperm(64, generator=gen)[:n]
+    want = pool.numpy().copy()
+    _fp4.write_rows(want, k, v, slots.tolist(), bs, SCALES)
+    got = pool.to(DEV)
+    binding.pa_cache_write_fp4(got, kd, vd, ints(slots), *SCALES)
+    assert np.array_equal(got.cpu().numpy(), want)
+    back = torch.full(wide.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    kb, vb = (x[:, shift:shift + hkv * d].unflatten(1, (hkv, d)) for x in back)
+    binding.pa_cache_read_fp4(kb, vb, got, ints(slots), *SCALES)
+    for x, y in zip((kb, vb), _fp4.read_rows(want, slots.numpy(), bs, d, SCALES)):
+        assert torch.equal(x.cpu(), _fp4.bf16_of_product(y))
+    assert (back[:, :, :shift] == 7).all() and (back[:, :, shift + hkv * d:] == 7).all()
+    binding.pa_error_check()
+
+
+def test_no_rows_are_a_no_op():
+    pool = random_pool(2, 1, 16, 64, torch.Generator().manual_seed(1)).to(DEV)
+    rows = torch.empty(0, 1, 64, dtype=torch.bfloat16, device=DEV)
+    before = pool.clone()
+    binding.pa_cache_write_fp4(pool, rows, rows, ints([]), *SCALES)
+    binding.pa_cache_read_fp4(rows, rows, pool, ints([]), *SCALES)
+    assert torch.equal(pool, before)
+
+
 def test_every_code_and_scale_reads_back():
     pool = torch.zeros(binding.fp4_pool_shape(32, 1, 8, 64), dtype=torch.uint8)
     row = torch.arange(512).view(32, 1, 2, 8, 1)
@@ -391,6 +424,45 @@ def test_decode_far_in_a_large_pool():
     binding.pa_error_check()
 
 
+@pytest.mark.parametrize("n", [1, 40, 700])
+def test_decode_of_nothing_but_empty_sequences(n):
+    b = Batch([0] * n, 4, 2, 128, 16)
+    assert (b.run(max_len=0) == 0).all()
+    assert (b.run(max_len=16) == 0).all()
+    binding.pa_error_check()
+
+
+def test_decode_batches_beyond_the_tables_are_refused():
+    for d, n in ((128, 30000), (64, 40000)):
+        b = Batch([1], 1, 1, d, 16)
+        out = torch.empty(n, 1, d, dtype=torch.bfloat16, device=DEV)
+        with pytest.raises(binding.PaError, match="UNSUPPORTED"):
+            binding.pa_decode_fp4(out, out, b.pool.to(DEV),
+                                  torch.zeros(n, 2, dtype=torch.int32, device=DEV),
+                                  torch.ones(n, dtype=torch.int32, device=DEV), 1, 1.0, 1.0, 1.0,
+                                  b.workspace())
+
+
+def test_decode_of_the_largest_batches():
+    """The ring shrinks as the tables grow."""
+    for d, n in ((128, 10000), (64, 18000)):
+        lens = [(i * 5) % 34 for i in range(n)]
+        b = Batch(lens, 1, 1, d, 32, seed=n)
+        out = b.run()
+        binding.pa_error_check()
+        b.check(out, seqs=range(0, n, n // 50))
+
+
+def test_decode_where_every_boundary_falls():
+    """Segments of every number of tiles, so that ranges begin and end anywhere in them."""
+    for n, hkv, length in ((20, 8, 97), (8, 20, 1000), (160, 1, 65), (3, 60, 321), (152, 1, 33),
+                           (153, 1, 32), (77, 2, 640), (1, 200, 2049)):
+        b = Batch([length] * n, hkv * 2, hkv, 64, 16, seed=n, table_pad=256)
+        out = b.run(max_len=4096)
+        binding.pa_error_check()
+        b.check(out, seqs=range(0, n, max(1, n // 10)))
+
+
 # ------------------------------------------------------------------ rotation
 class Turn:
     def __init__(self, n, hq, hkv, d, bs, rot, axes=1, interleaved=False, norm=(True, True),
@@ -460,6 +532,9 @@ TURNS = [
     dict(n=2500, hq=4, hkv=2, d=64, bs=16, rot=32, norm=(False, False)),
     dict(n=700, hq=32, hkv=8, d=128, bs=16, rot=128),
     dict(n=6000, hq=3, hkv=1, d=128, bs=16, rot=80),
+    dict(n=5, hq=40, hkv=40, d=64, bs=8, rot=64, interleaved=True, axes=3),
+    dict(n=3, hq=9, hkv=3, d=128, bs=32, rot=112, interleaved=True, norm=(True, False)),
+    dict(n=1, hq=1, hkv=1, d=128, bs=16, rot=16, axes=4),
 ]
 
 
@@ -645,6 +720,57 @@ def test_a_step_captured_and_replayed(lens, d, bs):
         s.run()
         assert torch.equal(first.view(torch.int16), s.out.view(torch.int16))
     binding.pa_error_check()
+
+
+def test_two_graphs_and_eager_calls_take_turns_with_one_workspace():
+    a, b = Step([700, 30, 1500], 8, 2, 128, 16, 128, seed=3), Step([900] * 40, 8, 2, 128, 16, 64, 4)
+    a.ws = b.ws = a.ws if a.ws.numel() >= b.ws.numel() else b.ws
+    a.run()
+    b.run()
+    torch.cuda.synchronize()
+    want = a.out.clone(), b.out.clone()
+    graphs = []
+    for step in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step.run()
+        graphs.append(g)
+    for order in ("ab", "ba", "aabb"):
+        a.ws.copy_(torch.randint(0, 256, a.ws.shape, dtype=torch.uint8, device=DEV))
+        for x in order:
+            step = a if x == "a" else b
+            step.out.fill_(math.nan)
+            graphs[x == "b"].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(step.out.view(torch.int16), want[x == "b"].view(torch.int16))
+            step.run()
+    binding.pa_error_check()
+
+
+def test_calls_on_another_stream():
+    """The stream argument, and PyTorch's current one; work behind a long kernel waits for it."""
+    s = Step([300, 77], 8, 2, 128, 16, 128, seed=5)
+    s.run()
+    torch.cuda.synchronize()
+    want = s.out.clone()
+    side = torch.cuda.Stream()
+    fresh = s.qkv.clone()
+    s.qkv.zero_()
+    torch.cuda.synchronize()
+    big = torch.randn(4096, 4096, device=DEV)
+    with torch.cuda.stream(side):
+        for _ in range(8):
+            big = big @ big * 1e-3
+        s.qkv.copy_(fresh)
+        s.run()
+    side.synchronize()
+    assert torch.equal(s.out.view(torch.int16), want.view(torch.int16))
+    s.out.fill_(0)
+    torch.cuda.synchronize()
+    binding.pa_decode_fp4(s.out, s.q, s.pool, s.tables, s.lens, 300, s.b.scale, *SCALES, s.ws,
+                          stream=side)
+    side.synchronize()
+    assert torch.equal(s.out.view(torch.int16), want.view(torch.int16))
 
 
 def test_two_steps_at_once_on_their_own_streams():
