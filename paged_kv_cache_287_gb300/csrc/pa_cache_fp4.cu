@@ -31,7 +31,7 @@ struct RowsArgs {
     int64_t row_bytes, num_slots;
     int num_tokens, block_shift, num_kv_heads;
     int wide;  // rows lie on 32-byte boundaries
-    float gk, gv, hk, hv;  // k_scale, v_scale, and six times those
+    Fp4Scale ks, vs;
 };
 
 template <int D, bool kWrite>
@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kWrite>) rows_kernel(const Ro
     for (int col = threadIdx.x - first * width; col < cols; col += width) {
         const int side = col >= per_side, c = col - side * per_side;
         const int head = c / kGroups, grp = c % kGroups;
-        const float g = side ? a.gv : a.gk, h = side ? a.hv : a.hk;
+        const Fp4Scale scale_of = side ? a.vs : a.ks;
+        const float g = scale_of.g;
         uint8_t *rows = (side ? a.v : a.k) + c * 32;
         for (int tok = blockIdx.x * at_once + first; tok < a.num_tokens; tok += kTok * step) {
             uint32_t x[kTok][8];
@@ -60,18 +61,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kWrite>) rows_kernel(const Ro
                 // (a sum past the last token may wrap: compared as unsigned)
                 const unsigned t = (unsigned)tok + (unsigned)k * (unsigned)step;
                 slot[k] = t < (unsigned)a.num_tokens ? a.slots[t] : -1;
-                if (slot[k] >= a.num_slots) {
-                    atomicOr(&g_err_cache_fp4, kErrOob);
-                    slot[k] = -1;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-                if (slot[k] < 0) continue;
-                row[k] = fp4_row<D>(slot[k] >> a.block_shift, slot[k] & (bs - 1), head, side,
-                                    a.num_kv_heads, bs);
-                if constexpr (kWrite) {
-                    const uint8_t *p = rows + (int64_t)(tok + k * step) * a.row_bytes;
+                if (kWrite && t < (unsigned)a.num_tokens) {  // a skipped row's is there as well
+                    const uint8_t *p = rows + (int64_t)t * a.row_bytes;
                     if (a.wide) {
                         ld_32(x[k], p);
                     } else {
@@ -80,7 +71,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kWrite>) rows_kernel(const Ro
                         x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
                         x[k][4] = z.x, x[k][5] = z.y, x[k][6] = z.z, x[k][7] = z.w;
                     }
-                } else {
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+                if (slot[k] >= a.num_slots) {
+                    atomicOr(&g_err_cache_fp4, kErrOob);
+                    slot[k] = -1;
+                }
+                if (slot[k] < 0) continue;
+                row[k] = fp4_row<D>(slot[k] >> a.block_shift, slot[k] & (bs - 1), head, side,
+                                    a.num_kv_heads, bs);
+                if constexpr (!kWrite) {
                     codes[k] = reinterpret_cast<const uint2 *>(a.kv + row[k].codes)[grp];
                     scale[k] = a.kv[row[k].scale + grp];
                 }
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kWrite>) rows_kernel(const Ro
                 if (slot[k] < 0) continue;
                 if constexpr (kWrite) {
                     uint2 q;
-                    const uint32_t s = fp4_quantise(x[k], g, h, q);
+                    const uint32_t s = fp4_quantise(x[k], scale_of, q);
                     reinterpret_cast<uint2 *>(a.kv + row[k].codes)[grp] = q;
                     a.kv[row[k].scale + grp] = (uint8_t)s;
                 } else {
@@ -142,10 +144,8 @@ cudaError_t launch_cache_fp4(bool write, void *kv_cache, const KvGeom &g, void *
     a.num_kv_heads = g.num_kv_heads;
     a.wide = (reinterpret_cast<uintptr_t>(k_rows) | reinterpret_cast<uintptr_t>(v_rows) |
               (uintptr_t)a.row_bytes) % 32 == 0;
-    a.gk = k_scale;
-    a.gv = v_scale;
-    a.hk = 6.f * k_scale;
-    a.hv = 6.f * v_scale;
+    a.ks = fp4_scale(k_scale);
+    a.vs = fp4_scale(v_scale);
     const int cols = 2 * g.num_kv_heads * (g.head_size / kFp4Group);
     const int at_once = kThreads / std::min(cols, kThreads);
     // Blocks that fill the GPU once, or a token per thread where that takes fewer.

@@ -73,29 +73,71 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// Quotients by d without dividing.  With r within 2^-23 of 1 / d (relatively), x r (1 - 2^-20)
+// and x r (1 + 2^-20) lie on both sides of the quotient x / d and of its rounding to binary32 (off
+// by 2^-23, and by 2^-24 for each of r's factor, the product and the quotient: five of sixteen
+// 2^-24), and a code does not fall as its value's magnitude rises: where both products give one
+// code it is the quotient's.  The rest, next to a tie, is divided.
+struct Around {
+    float lo, hi;  // r (1 - 2^-20), r (1 + 2^-20); 0 where 1 / d or the products may not be normal
+};
+
+// Of a positive divisor known on the host.
+inline Around around(float d) {
+    if (!(d > 1e-30f && d < 1e30f)) return {0.f, 0.f};
+    return {(float)((1.0 - 0x1p-20) / d), (float)((1.0 + 0x1p-20) / d)};
+}
+
+// Eight bf16 elements over d as e4m3 codes (nearest, ties to even, saturating).
+__device__ __forceinline__ uint2 e4m3_of_quotients(const uint4 &x, float d, const Around &r) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t c[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float v[4], lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            lo[i] = hi[i] = v[i] = bf16_lo(w[2 * k + i / 2]);
+            lo[i + 1] = hi[i + 1] = v[i + 1] = bf16_hi(w[2 * k + i / 2]);
+            mul2(lo[i], lo[i + 1], r.lo, r.lo);
+            mul2(hi[i], hi[i + 1], r.hi, r.hi);
+        }
+        c[k] = pack_e4m3x2(lo[0], lo[1]) | pack_e4m3x2(lo[2], lo[3]) << 16;
+        if (r.lo == 0.f ||
+            c[k] != (pack_e4m3x2(hi[0], hi[1]) | pack_e4m3x2(hi[2], hi[3]) << 16))
+            c[k] = pack_e4m3x2(__fdiv_rn(v[0], d), __fdiv_rn(v[1], d)) |
+                   pack_e4m3x2(__fdiv_rn(v[2], d), __fdiv_rn(v[3], d)) << 16;
+    }
+    return make_uint2(c[0], c[1]);
+}
+
+// A tensor's scale g, h = fp32(6 g), and what divides by h.
+struct Fp4Scale {
+    float g, h;
+    Around by_h;
+};
+inline Fp4Scale fp4_scale(float g) { return {g, 6.f * g, around(6.f * g)}; }
+
 // Sixteen bf16 elements (x[0] holds the first two) to their scale's e4m3 code (returned) and
-// e2m1 codes:  s = e4m3(max|x| / h), h = fp32(6 g);  d = fp32(s g);  code = e2m1(x / d), all
-// divisions binary32's, roundings to nearest even, saturating.  A group whose d is not above 0
-// (max|x| too small for a scale, or a NaN) has codes of 0; with a NaN its scale is NaN too, so
-// that all its elements are.
-//
-// A division for each element would be most of the work (390 instructions a warp and group
-// against 150).  With r within 2^-23 of 1 / d, x r (1 - 2^-20) and x r (1 + 2^-20) lie on both
-// sides of the quotient and of its rounding (off by 2^-23, and 2^-24 for each of r's factor, the
-// product and the quotient: five of sixteen 2^-24), and a code does not fall as the quotient's
-// magnitude rises: where both give one code it is the quotient's.  The others, next to a tie,
-// are divided.
-__device__ __forceinline__ uint32_t fp4_quantise(const uint32_t (&x)[8], float g, float h,
+// e2m1 codes:  s = e4m3(max|x| / h);  d = fp32(s g);  code = e2m1(x / d), all divisions
+// binary32's, roundings to nearest even, saturating.  A group whose d is not above 0 (max|x| too
+// small for a scale, or a NaN) has codes of 0; with a NaN its scale is NaN too, so that all its
+// elements are.  (A division per element took 390 instructions for a warp's 32 groups; this
+// takes some 190.)
+__device__ __forceinline__ uint32_t fp4_quantise(const uint32_t (&x)[8], const Fp4Scale &t,
                                                  uint2 &codes) {
     uint32_t m = absmax_bf16x2(x[0], x[1]);
 #pragma unroll
     for (int i = 2; i < 8; ++i) m = absmax_bf16x2(m, x[i]);
     m = absmax_bf16x2(m, m >> 16);
-    const uint32_t s = pack_e4m3x2(__fdiv_rn(bf16_lo(m), h), 0.f) & 0xffu;
-    const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s)), g);
+    const float top = bf16_lo(m);
+    uint32_t s = pack_e4m3x2(top * t.by_h.lo, top * t.by_h.hi);
+    if (t.by_h.lo == 0.f || (s & 0xffu) != s >> 8) s = pack_e4m3x2(__fdiv_rn(top, t.h), 0.f);
+    s &= 0xffu;
+    const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s)), t.g);
     codes = make_uint2(0u, 0u);
     if (!(d > 0.f)) return s;
-    const bool tame = d > 1e-30f && d < 1e30f;  // 1 / d and the products are normal numbers
+    const bool tame = d > 1e-30f && d < 1e30f;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     const float r0 = r * (1.f - 0x1p-20f), r1 = r * (1.f + 0x1p-20f);

@@ -62,15 +62,6 @@ __device__ __forceinline__ void pack(const float (&p)[8], const float (&q)[8], u
     y1 = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-__device__ __forceinline__ uint2 fp8_codes(const uint4 &v, float scale) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        c[i] = pack_e4m3x2(__fdiv_rn(bf16_lo(w[i]), scale), __fdiv_rn(bf16_hi(w[i]), scale));
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-}
-
 constexpr int kThreads = 256;
 constexpr int kRing = 3;        // groups of heads (1 KB each) in flight per warp
 constexpr int kPerSm = 4;       // blocks; 32 warps of 64 registers
@@ -89,9 +80,15 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// What divides K and V: by the scales (FP8), by six times those (4 bits).
+struct Divisors {
+    Around k, v;
+};
+
 // kNeighbours: pairs are neighbours (interleaved).
 template <int D, int kBits, bool kNeighbours>
-__global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRopeArgs a,
+                                                                  const Divisors by) {
     constexpr int kLanes = D / 16;       // threads of a head
     constexpr int kHeads = 32 / kLanes;  // heads of a warp
     __shared__ uint4 ring[kThreads / 32][kRing][2][32];
@@ -269,7 +266,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
         }
         if (slot < 0 || (grp + 1) * kHeads <= a.num_heads) continue;  // no K or V here
         const int side = is_v ? 1 : 0, kvh = hd - a.num_heads - side * a.num_kv_heads;
-        const float g = side ? a.v_scale : a.k_scale;
         if constexpr (kBits == 4) {
             // A scale's 16 elements are vectors 2t and 2t + 1: of a head turned in halves they
             // are fetched from where they are.
@@ -296,7 +292,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
                 const Fp4Row to = fp4_row<D>(blk, off, kvh, side, a.num_kv_heads, a.block_size);
                 uint2 codes;
                 uint8_t *kv = static_cast<uint8_t *>(a.kv);
-                kv[to.scale + t] = (uint8_t)fp4_quantise(x, g, 6.f * g, codes);
+                kv[to.scale + t] = (uint8_t)fp4_quantise(
+                    x, side ? Fp4Scale{a.v_scale, 6.f * a.v_scale, by.v}
+                            : Fp4Scale{a.k_scale, 6.f * a.k_scale, by.k},
+                    codes);
                 reinterpret_cast<uint2 *>(kv + to.codes)[t] = codes;
             }
         } else if (live && !is_q) {
@@ -308,8 +307,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
                 kv[i1] = y1;
             } else {
                 uint2 *kv = static_cast<uint2 *>(a.kv) + to;
-                kv[i0] = fp8_codes(y0, g);
-                kv[i1] = fp8_codes(y1, g);
+                const float g = side ? a.v_scale : a.k_scale;
+                const Around r = side ? by.v : by.k;
+                kv[i0] = e4m3_of_quotients(y0, g, r);
+                kv[i1] = e4m3_of_quotients(y1, g, r);
             }
         }
     }
@@ -329,11 +330,13 @@ cudaError_t launch_qkv_rope(QkvRopeArgs a, int head_size, int kv_bits, cudaStrea
     a.chunks = (int)std::min<long long>(groups, (want + a.num_tokens - 1) / a.num_tokens);
     const long long warps = (long long)a.num_tokens * a.chunks;
     const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
+    const float times = kv_bits == 4 ? 6.f : 1.f;
+    const Divisors by{around(times * a.k_scale), around(times * a.v_scale)};
     g_launched.store(true);
     auto pick = [&](auto k128, auto k64, auto n128, auto n64) {
         return launch_pdl(a.interleaved ? (head_size == 128 ? n128 : n64)
                                         : (head_size == 128 ? k128 : k64),
-                          grid, kThreads, 0, 1, stream, a);
+                          grid, kThreads, 0, 1, stream, a, by);
     };
     if (kv_bits == 16)
         return pick(qkv_rope_kernel<128, 16, false>, qkv_rope_kernel<64, 16, false>,
