@@ -11,8 +11,8 @@
 // gives the same bits as the formula's steps in fp32.
 //
 // Bound by HBM: every element read once and written once.  A thread holds the two 8-element
-// vectors that a rotation pairs (t and t + rot_dim / 16 vectors further; or 2t and 2t + 1), so
-// rotating needs no exchange; head_size / 16 threads make a head, a warp a group of 4 or 8 heads
+// vectors that a rotation pairs (t and t + rot_dim / 16 vectors further; or two with pairs of
+// their own), so rotating needs no exchange; head_size / 16 threads make a head, a warp a group of 4 or 8 heads
 // (1 KB).  A warp takes a token, whose cosines and sines stay in registers for all its heads,
 // and copies its next groups into shared memory ahead (each thread its own vectors, so nothing
 // is synchronised).  4344 tokens of 32 + 2 x 8 heads of 128 with norms and three axes: 21.7 us,
@@ -101,10 +101,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
     const int tok = warp / a.chunks, chunk = warp - tok * a.chunks;
     const bool idle = tok >= a.num_tokens;
 
-    // This thread's vectors of a rotated head; of V's it takes 2t and 2t + 1.
-    const bool turns = t < a.rot_dim / 16;
-    const bool split = !kNeighbours && turns;
-    const int v0 = split ? t : 2 * t, v1 = split ? t + a.rot_dim / 16 : 2 * t + 1;
+    // This thread's two vectors of a rotated head: those that a pair joins, or kLanes apart where
+    // pairs are neighbours (a warp's 16-byte accesses then lie side by side: with 2t and 2t + 1
+    // the 4344 tokens took 29 us instead of 20); of V's, too, but for a 4-bit pool's, where
+    // vectors 2t and 2t + 1 share a scale.
+    const bool split = !kNeighbours && t < a.rot_dim / 16;
+    const int v0 = split || kNeighbours ? t : 2 * t;
+    const int v1 = split ? t + a.rot_dim / 16 : (kNeighbours ? t + kLanes : 2 * t + 1);
+    const int u0 = kBits == 4 ? 2 * t : t, u1 = kBits == 4 ? 2 * t + 1 : t + kLanes;
+    // Its pairs, four and four: whether they turn, and the first.
+    const bool turns[2] = {kNeighbours ? 8 * v0 < a.rot_dim : split,
+                           kNeighbours ? 8 * v1 < a.rot_dim : split};
+    const int pair[2] = {kNeighbours ? 4 * v0 : 8 * t, kNeighbours ? 4 * v1 : 8 * t + 4};
     const int first = lane / kLanes * (D / 8);  // its head's first vector in a group's 64
 
     // The first rows are asked for before what the rest hangs on.
@@ -114,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
         const int hd = grp * kHeads + lane / kLanes;
         if (hd < heads) {
             const uint4 *head = row + 64 * grp + first;
-            copy16(&mine[at][0][lane], head + (hd < rot_heads ? v0 : 2 * t));
-            copy16(&mine[at][1][lane], head + (hd < rot_heads ? v1 : 2 * t + 1));
+            copy16(&mine[at][0][lane], head + (hd < rot_heads ? v0 : u0));
+            copy16(&mine[at][1][lane], head + (hd < rot_heads ? v1 : u1));
         }
         copies_commit();
     };
@@ -126,16 +134,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
         slot = a.slots[tok];
         if (a.pair_axis) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) axis[i] = turns ? a.pair_axis[8 * t + i] : 0;
+            for (int i = 0; i < 8; ++i)
+                axis[i] = turns[i / 4] ? a.pair_axis[pair[i / 4] + i % 4] : 0;
         } else {
             pos[0] = a.positions[tok];
         }
     }
     if (a.q_weight || a.k_weight) {
-        // (neighbours: of each 16 the first ones of the pairs, then the second ones)
+        // (neighbours: of each vector the first ones of its pairs, then the second ones)
         for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
             const void *w = i < D ? a.q_weight : a.k_weight;
-            const int from = kNeighbours ? (i & ~15) | (2 * i & 14) | (i >> 3 & 1) : i;
+            const int from = kNeighbours ? (i & ~7) | (2 * i & 6) | (i >> 2 & 1) : i;
             if (w)
                 (&weights[0][0])[i] =
                     __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[from % D]);
@@ -144,9 +153,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
     }
     if (idle) return;
 
-    // The cosines and sines of its pairs.
+    // Their positions, cosines and sines.
     float c[8], s[8];
-    bool bad = false, one = true;  // one: a single position for all pairs of this thread
+    bool bad = false, one[2] = {true, true};  // one: a single position for the four
     if (a.pair_axis) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -154,16 +163,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
                 atomicOr(&g_err_qkv_rope, kErrOob);
                 axis[i] = 0;
             }
-            one = one && axis[i] == axis[0];
+            one[i / 4] = one[i / 4] && axis[i] == axis[i & 4];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i > 0 && one) break;
+            if (i % 4 && one[i / 4]) continue;
             pos[i] = a.positions[(int64_t)axis[i] * a.num_tokens + tok];
-            bad = bad || (turns && (pos[i] < 0 || pos[i] >= a.max_position));
+            bad = bad || (turns[i / 4] && (pos[i] < 0 || pos[i] >= a.max_position));
         }
     } else {
-        bad = turns && (pos[0] < 0 || pos[0] >= a.max_position);
+        pos[4] = pos[0];
+        bad = (turns[0] || turns[1]) && (pos[0] < 0 || pos[0] >= a.max_position);
     }
     if (__any_sync(0xffffffffu, bad)) {  // nothing of this token is written
         if (lane == 0) atomicOr(&g_err_qkv_rope, kErrOob);
@@ -171,26 +181,25 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-    }
-    if (turns) {
-        if (one) {
-            const float4 *cs =
-                reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos[0] * a.rot_dim + 8 * t);
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 p = cs[k], q = cs[a.rot_dim / 8 + k];
-                c[4 * k] = p.x, c[4 * k + 1] = p.y, c[4 * k + 2] = p.z, c[4 * k + 3] = p.w;
-                s[4 * k] = q.x, s[4 * k + 1] = q.y, s[4 * k + 2] = q.z, s[4 * k + 3] = q.w;
-            }
+        for (int i = 4 * h; i < 4 * h + 4; ++i) {
+            c[i] = 1.f;
+            s[i] = 0.f;
+        }
+        if (!turns[h]) continue;
+        if (one[h]) {
+            const float *cs = a.cos_sin + (int64_t)pos[4 * h] * a.rot_dim + pair[h];
+            const float4 u = *reinterpret_cast<const float4 *>(cs);
+            const float4 v = *reinterpret_cast<const float4 *>(cs + a.rot_dim / 2);
+            c[4 * h] = u.x, c[4 * h + 1] = u.y, c[4 * h + 2] = u.z, c[4 * h + 3] = u.w;
+            s[4 * h] = v.x, s[4 * h + 1] = v.y, s[4 * h + 2] = v.z, s[4 * h + 3] = v.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float *cs = a.cos_sin + (int64_t)pos[i] * a.rot_dim + 8 * t + i;
-                c[i] = cs[0];
-                s[i] = cs[a.rot_dim / 2];
+            for (int i = 0; i < 4; ++i) {
+                const float *cs = a.cos_sin + (int64_t)pos[4 * h + i] * a.rot_dim + pair[h] + i;
+                c[4 * h + i] = cs[0];
+                s[4 * h + i] = cs[a.rot_dim / 2];
             }
         }
     }
@@ -205,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
     for (int grp = chunk; grp < groups; grp += a.chunks) {
         const int hd = grp * kHeads + lane / kLanes;
         const bool live = hd < heads, is_q = hd < a.num_heads, is_v = hd >= rot_heads;
-        const int i0 = is_v ? 2 * t : v0, i1 = is_v ? 2 * t + 1 : v1;
+        const int i0 = is_v ? u0 : v0, i1 = is_v ? u1 : v1;
         copies_wait<kRing - 1>();
         uint4 y0 = mine[at][0][lane], y1 = mine[at][1][lane];
         if (!is_v) {
@@ -224,11 +233,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
 #pragma unroll
                 for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
                 const float r = rsqrtf(sum * (1.f / D) + a.eps);
-                const float4 *wp = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i0);
-                const float4 *wq = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i1);
+                // Of the pairs' first and second elements: a vector's each, or half of both.
+                const float4 *w0 = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i0);
+                const float4 *w1 = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i1);
 #pragma unroll
                 for (int i = 0; i < 8; i += 4) {
-                    const float4 u = wp[i / 4], v = wq[i / 4];
+                    const float4 u = kNeighbours ? (i ? w1[0] : w0[0]) : w0[i / 4];
+                    const float4 v = kNeighbours ? (i ? w1[1] : w0[1]) : w1[i / 4];
                     mul2(p[i], p[i + 1], r, r);
                     mul2(p[i + 2], p[i + 3], r, r);
                     mul2(q[i], q[i + 1], r, r);
@@ -239,9 +250,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
                     mul2(q[i + 2], q[i + 3], v.z, v.w);
                 }
             }
-            if (turns) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
+            for (int h = 0; h < 2; ++h) {
+                if (!turns[h]) continue;
+#pragma unroll
+                for (int i = 4 * h; i < 4 * h + 4; i += 2) {
                     float pc0 = p[i], pc1 = p[i + 1], ps0 = p[i], ps1 = p[i + 1];
                     float qc0 = q[i], qc1 = q[i + 1], qs0 = q[i], qs1 = q[i + 1];
                     mul2(pc0, pc1, c[i], c[i + 1]);
@@ -267,11 +280,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
         if (slot < 0 || (grp + 1) * kHeads <= a.num_heads) continue;  // no K or V here
         const int side = is_v ? 1 : 0, kvh = hd - a.num_heads - side * a.num_kv_heads;
         if constexpr (kBits == 4) {
-            // A scale's 16 elements are vectors 2t and 2t + 1: of a head turned in halves they
-            // are fetched from where they are.
+            // A scale's 16 elements are vectors 2t and 2t + 1: of K they are fetched from where
+            // they are.
             uint32_t x[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-            if (!kNeighbours && __any_sync(0xffffffffu, live && !is_q && !is_v)) {
-                const int half = a.rot_dim / 16;
+            if (__any_sync(0xffffffffu, live && !is_q && !is_v)) {
+                const int half = kNeighbours ? kLanes : a.rot_dim / 16;
                 const uint32_t w0[4] = {y0.x, y0.y, y0.z, y0.w};
                 const uint32_t w1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
