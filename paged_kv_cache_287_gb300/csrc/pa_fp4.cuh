@@ -7,6 +7,8 @@
 // are one run of block_size * head_size * 9 / 8 bytes, which one bulk copy fetches.
 #pragma once
 
+#include <cmath>
+
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -85,6 +87,8 @@ struct Around {
 // Of a positive divisor known on the host.
 inline Around around(float d) {
     if (!(d > 1e-30f && d < 1e30f)) return {0.f, 0.f};
+    int e;
+    if (std::frexp(d, &e) == 0.5f) return {1.f / d, 1.f / d};  // a power of two: exact
     return {(float)((1.0 - 0x1p-20) / d), (float)((1.0 + 0x1p-20) / d)};
 }
 
@@ -138,6 +142,11 @@ __device__ __forceinline__ uint32_t fp4_quantise(const uint32_t (&x)[8], const F
     codes = make_uint2(0u, 0u);
     if (!(d > 0.f)) return s;
     const bool tame = d > 1e-30f && d < 1e30f;
+    // With a d of at most 12 bits (any s, g a power of two) ties are common, and nothing else is
+    // near one: x has 8 bits, the middle between two codes 3, so a quotient that is not the
+    // middle is off it by 2^-15 at least.  There one product is enough, rounded to 18 bits, which
+    // takes a tie's error (below 2^-22) away and moves no other across.
+    const bool few_bits = (__float_as_uint(d) & 0xfffu) == 0u;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     const float r0 = r * (1.f - 0x1p-20f), r1 = r * (1.f + 0x1p-20f);
@@ -147,8 +156,23 @@ __device__ __forceinline__ uint32_t fp4_quantise(const uint32_t (&x)[8], const F
         float v[8], lo[8], hi[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            lo[i] = hi[i] = v[i] = bf16_lo(x[4 * w + i / 2]);
-            lo[i + 1] = hi[i + 1] = v[i + 1] = bf16_hi(x[4 * w + i / 2]);
+            v[i] = bf16_lo(x[4 * w + i / 2]);
+            v[i + 1] = bf16_hi(x[4 * w + i / 2]);
+        }
+        if (tame && few_bits) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                mul2(v[i], v[i + 1], r, r);
+                v[i] = __uint_as_float((__float_as_uint(v[i]) + 0x20u) & ~0x3fu);
+                v[i + 1] = __uint_as_float((__float_as_uint(v[i + 1]) + 0x20u) & ~0x3fu);
+            }
+            c[w] = pack_e2m1x8(v);
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            lo[i] = hi[i] = v[i];
+            lo[i + 1] = hi[i + 1] = v[i + 1];
             mul2(lo[i], lo[i + 1], r0, r0);
             mul2(hi[i], hi[i + 1], r1, r1);
         }

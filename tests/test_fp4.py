@@ -88,6 +88,38 @@ def test_quantiser_special_groups():
     assert s[5, 0] == 0 and (codes[5] == 0).all()  # 2^-9 / 6 rounds to no scale
 
 
+def test_codes_without_a_division():
+    """The kernels' shortcuts give the quotient's code for every bf16 x: two products around it
+    that agree, and, where the divisor has at most 12 bits, one rounded to 18 bits; with a
+    reciprocal off by up to 2^-23 either way."""
+    x = (np.arange(65536, dtype=np.uint32) << 16).view(np.float32)
+    x = x[np.isfinite(x)]
+    rng = np.random.default_rng(0)
+
+    def code(v):
+        v = np.minimum(np.abs(v), np.float32(6)).astype(np.float64)
+        return _fp4.nearest_even(v, _fp4.E2M1[:8])
+
+    for n in range(300):
+        if n % 2:
+            d = np.float32(rng.integers(1, 4096) * 2.0 ** rng.integers(-90, 80))
+        else:
+            d = np.float32(_fp4.E4M3[rng.integers(1, 127)] * rng.random() * 10.0 ** rng.integers(
+                -20, 20))
+        if not 1e-30 < d < 1e30:
+            continue
+        near = x[(np.abs(x) <= d * 8) & (np.abs(x) >= d * 0.1)]
+        want = code(near / d)
+        for off in (-1, 0, 1):
+            r = np.float32((1 + off * 2.0 ** -23) / np.float64(d))
+            lo = code(near * np.float32(r * np.float32(1 - 2.0 ** -20)))
+            hi = code(near * np.float32(r * np.float32(1 + 2.0 ** -20)))
+            assert (lo[lo == hi] == want[lo == hi]).all()
+            if d.view(np.uint32) & 0xfff == 0:
+                q = (near * r).view(np.uint32) + np.uint32(0x20) & np.uint32(0xffffffc0)
+                assert (code(q.view(np.float32)) == want).all()
+
+
 # ------------------------------------------------------------------ refusals
 def _cache(**kw):
     a = dict(kv=FAKE, k=FAKE, v=FAKE, slots=FAKE, stream=0, stride=8 * 128, nb=10, bs=16, hkv=8,

@@ -87,6 +87,42 @@ def test_write_of_every_kind_of_number(g):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+def test_write_at_many_tensor_scales():
+    """Scales of few bits and of many, values whose quotients meet ties again and again."""
+    gen = torch.Generator().manual_seed(30)
+    scales = [2.0 ** e for e in (-30, -9, 0, 7)] + [3.0, 0.75, 1 / 3, 0.1, 5 / 2688, 0.7, 1.1e-3]
+    n, bs = 256, 32
+    k = bf16((n, 2, 128), gen)
+    k[::2] = (k[::2].float() * 8).round().to(torch.bfloat16) / 8
+    for a, b in zip(scales, scales[1:] + scales[:1]):
+        kk = (k.float() * a * 200).to(torch.bfloat16)
+        v = (k.float() * b).to(torch.bfloat16)
+        pool = torch.zeros(binding.fp4_pool_shape(n // bs, 2, bs, 128), dtype=torch.uint8)
+        want = pool.numpy().copy()
+        _fp4.write_rows(want, kk, v, range(n), bs, (a, b))
+        got = pool.to(DEV)
+        binding.pa_cache_write_fp4(got, kk.to(DEV), v.to(DEV), ints(range(n)), a, b)
+        assert np.array_equal(got.cpu().numpy(), want), (a, b)
+
+
+@pytest.mark.parametrize("scales", [(1.0, 2.0 ** -6), (1 / 3, 0.0123), (1e-35, 1e35),
+                                    (2.0 ** 100, 2.0 ** -126), (1e-40, 3.3)])
+def test_rope_into_an_fp8_pool_at_many_scales(scales):
+    t = Turn(40, 4, 2, 128, 16, 64, norm=(False, False), seed=9)
+    t.wide[1] *= 1e30
+    t.wide[2] *= 1e-30
+    t.wide[4, 3] = math.inf
+    t.wide[5, 7] = math.nan
+    _, pool16 = t.run()
+    t.bits = 8
+    start = torch.zeros(pool16.shape, dtype=torch.uint8, device=DEV)
+    _, pool = t.run(pool=start.clone(), scales=scales)
+    slot = t.slots.clamp(min=0).long()
+    k, v = (pool16[slot // 16, side, :, slot % 16].contiguous() for side in (0, 1))
+    binding.pa_cache_write_fp8(start, k, v, t.slots.to(DEV), *scales)
+    assert torch.equal(pool, start)
+
+
 def test_write_of_strided_rows_leaves_the_rest():
     gen = torch.Generator().manual_seed(8)
     n, hkv, d, bs = 21, 2, 64, 8
