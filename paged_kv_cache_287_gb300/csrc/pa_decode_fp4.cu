@@ -21,7 +21,17 @@
 //     load of V takes would lie in the same banks.
 // The tiles of all (sequence, KV head) segments are one list, cut into equal ranges, one per
 // CTA and within it one per warp.  Pieces of a segment in one CTA are merged in shared memory,
-// those in several CTAs by a second kernel (a record per CTA and end of its range).
+// those in several CTAs by a second kernel (a record per CTA and end of its range); few or short
+// segments go to CTAs whole (rules at launch_decode_fp4).
+//
+// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 121 us, 84 %
+// of the copy rate, 32 of up to 131072 tokens 165 us, 89 %.  In the steady state a tile takes
+// 0.75 ns of the whole GPU (92 %); without V's products it would be 0.69 (100 %): of 594 warp
+// instructions a tile 302 are the products with their conversions, 39 the softmax, 95 loads,
+// scales and interleaving, the rest waits, issue and bookkeeping, at 2.6 a clock.  Tried and
+// slower: 12 or 14 warps (131, 135; the registers allow 16), 8 with four stages each (154), the
+// last of the CTAs to come merging a segment in place of the second kernel (125), copies of 16
+// bytes by every lane (120.5, but 24.3 against 23.2 for 47 sequences, and spills).
 #include <algorithm>
 #include <atomic>
 
@@ -60,7 +70,8 @@ struct Args {
     int64_t block_bytes;
     int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, max_seq_len;
     int stages;
-    int aligned;  // CTA c is segment c: no piece leaves its CTA
+    int aligned;  // CTA c is segment c
+    int whole;    // every CTA takes whole segments: no piece leaves it
     float scale_log2, v_scale;  // scale * log2(e) * k_scale
 };
 
@@ -72,6 +83,16 @@ struct WarpPieces {
 
 __device__ __forceinline__ int clamped(const Args &a, int len) {
     return len < 0 ? 0 : (len > a.max_seq_len ? a.max_seq_len : len);
+}
+
+// The sequence of tile x of the list: the last that begins at or before it.
+__device__ __forceinline__ int sequence_of(const int *pre, int num_seqs, int num_kv_heads, int x) {
+    int lo = 0, hi = num_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (num_kv_heads * pre[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
 }
 
 // 16 (D 128) or 8 consecutive dims of one head: acc[mt][e] and acc[mt][e + 2] are dims 2 mt and
@@ -185,6 +206,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             const int cta = blockIdx.x, each = T / ctas, rest = T - each * ctas;
             r0 = cta < ctas ? cta * each + min(cta, rest) : 0;
             r1 = cta < ctas ? r0 + each + (cta < rest) : 0;
+            if (a.whole) {  // the nearest ends of segments
+                auto end_near = [&](int x) {
+                    if (x >= T) return T;
+                    const int s = sequence_of(pre, B, Hkv, x), nt = pre[s + 1] - pre[s];
+                    const int j = (x - Hkv * pre[s]) % nt;
+                    return 2 * j < nt ? x - j : x - j + nt;
+                };
+                r0 = end_near(r0);
+                r1 = end_near(r1);
+            }
         }
         const int n = r1 - r0;
         active = min(n, kWarps);
@@ -223,12 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             h = blockIdx.x - s * Hkv;
             j = x;
         } else {
-            int lo = 0, hi = B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (Hkv * pre[mid] <= x) lo = mid; else hi = mid - 1;
-            }
-            s = lo;
+            s = sequence_of(pre, B, Hkv, x);
             const int nt = pre[s + 1] - pre[s], r = x - Hkv * pre[s];
             h = r / nt;
             j = r - h * nt;
@@ -627,7 +653,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 *reinterpret_cast<float2 *>(r + kHeads * D + 2 * hd) = make_float2(M, den);
         }
     }
-    if (!a.aligned && tid == 0) {
+    if (!a.whole && tid == 0) {
         bool head_ends = false, tail_ends = true;
         follow(0, head_ends);
         const int w = 31 - __clz(begun);  // the one piece that may leave the CTA begins here
@@ -727,7 +753,7 @@ cudaError_t launch(Args a, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     g_launched.store(true);
     e = launch_pdl(decode_fp4_kernel<D, BS>, dim3((unsigned)grid), kWarps * 32, smem, 1, stream, a);
-    if (e != cudaSuccess || a.aligned) return e;
+    if (e != cudaSuccess || a.whole) return e;
     return launch_pdl(decode_fp4_merge_kernel<D>, dim3((unsigned)grid), kHeads * D / 4, 0, 1,
                       stream, a, grid);
 }
@@ -770,9 +796,17 @@ cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, co
     a.v_scale = v_scale;
     const long long segs = (long long)num_seqs * g.num_kv_heads;
     const long long tiles = (max_seq_len + kTokens - 1) / kTokens;
-    // A CTA per segment when that leaves at most four tiles to a warp and none of the SMs two
-    // segments: no scan of the lengths, no second kernel.
-    a.aligned = segs <= sms && tiles <= 4 * kWarps;
+    // A CTA per segment: no scan of the lengths, no second kernel, but a segment has one SM's
+    // rate, 0.105 us a tile, where the split has a share of all SMs and some 4 us more.  Measured
+    // (us, CTA per segment against the split; 8 segments): 8.0 / 9.8 at 1024 tokens, 11.0 / 9.3 at
+    // 2048; 32 segments 8.4 / 8.3, 11.7 / 9.6; 144 segments 14.2 / 17.1 at 2048, 21.0 / 22.7 at
+    // 4096, where it ends: one long sequence among short ones would have the one SM.
+    a.aligned = segs <= sms && tiles <= 128 && tiles * (sms - segs) <= 38LL * sms;
+    // More segments than SMs: whole segments to a CTA, by the prefix sums, spare the second kernel
+    // (1.5 to 2 us) and cost up to half a segment of imbalance.  376 segments of up to 256, 512,
+    // 1024, 2048 tokens: 8.5 / 9.7, 10.6 / 12.4, 14.3 / 14.8, 21.8 / 21.0; 2048 segments 19.4 /
+    // 20.8, 28.1 / 30.2, 41.8 / 41.6, 65.7 / 67.2.
+    a.whole = a.aligned || tiles <= 24;
     const int grid = (int)(a.aligned ? segs : std::min<long long>(sms, std::max(1LL, segs * tiles)));
     if (g.head_size == 128) {
         if (g.block_size == 8) return launch<128, 8>(a, grid, stream);
