@@ -210,75 +210,97 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
     const int blk = slot < 0 ? 0 : slot / a.block_size, off = slot - blk * a.block_size;
     uint4 *q_out = static_cast<uint4 *>(a.q_out) + (int64_t)tok * a.num_heads * (D / 8);
 
-    int at = 0;
-    for (int grp = chunk; grp < groups; grp += a.chunks) {
-        const int hd = grp * kHeads + lane / kLanes;
-        const bool live = hd < heads, is_q = hd < a.num_heads, is_v = hd >= rot_heads;
+    // Norm and rotation of this thread's 16 elements of a head.
+    const bool whole = a.rot_dim == D;
+    auto transform = [&](uint4 &y0, uint4 &y1, bool norm, const float *w) {
+        float p[8], q[8];
+        unpack<kNeighbours>(y0, y1, p, q);
+        if (norm) {
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                fma2(sum0, sum1, p[i], p[i + 1], p[i], p[i + 1], sum0, sum1);
+                fma2(sum0, sum1, q[i], q[i + 1], q[i], q[i + 1], sum0, sum1);
+            }
+            float sum = sum0 + sum1;
+            // The lanes of this head: in a group with V's heads not all are here.
+            const uint32_t mask = ((1u << kLanes) - 1u) << (lane - t);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+            const float r = rsqrtf(sum * (1.f / D) + a.eps);
+            // Of the pairs' first and second elements: a vector's each, or half of both.
+            const float4 *w0 = reinterpret_cast<const float4 *>(w + 8 * v0);
+            const float4 *w1 = reinterpret_cast<const float4 *>(w + 8 * v1);
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 u = kNeighbours ? (i ? w1[0] : w0[0]) : w0[i / 4];
+                const float4 v = kNeighbours ? (i ? w1[1] : w0[1]) : w1[i / 4];
+                mul2(p[i], p[i + 1], r, r);
+                mul2(p[i + 2], p[i + 3], r, r);
+                mul2(q[i], q[i + 1], r, r);
+                mul2(q[i + 2], q[i + 3], r, r);
+                mul2(p[i], p[i + 1], u.x, u.y);
+                mul2(p[i + 2], p[i + 3], u.z, u.w);
+                mul2(q[i], q[i + 1], v.x, v.y);
+                mul2(q[i + 2], q[i + 3], v.z, v.w);
+            }
+        }
+        auto turn = [&](int i) {  // pairs i and i + 1
+            float pc0 = p[i], pc1 = p[i + 1], ps0 = p[i], ps1 = p[i + 1];
+            float qc0 = q[i], qc1 = q[i + 1], qs0 = q[i], qs1 = q[i + 1];
+            mul2(pc0, pc1, c[i], c[i + 1]);
+            mul2(ps0, ps1, s[i], s[i + 1]);
+            mul2(qc0, qc1, c[i], c[i + 1]);
+            mul2(qs0, qs1, s[i], s[i + 1]);
+            fma2(p[i], p[i + 1], qs0, qs1, -1.f, -1.f, pc0, pc1);  // pc - qs, rounded once
+            add2(qc0, qc1, ps0, ps1);
+            q[i] = qc0;
+            q[i + 1] = qc1;
+        };
+        if (whole) {  // no lane but turns
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) turn(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+                if (turns[i / 4]) turn(i);
+        }
+        pack<kNeighbours>(p, q, y0, y1);
+    };
+
+    // Groups of q's heads alone, then the others.
+    int at = 0, grp = chunk;
+    for (; (grp + 1) * kHeads <= a.num_heads; grp += a.chunks) {
+        copies_wait<kRing - 1>();
+        uint4 y0 = mine[at][0][lane], y1 = mine[at][1][lane];
+        transform(y0, y1, a.q_weight != nullptr, weights[0]);
+        fetch(min(grp + kRing * a.chunks, groups), at);
+        at = at + 1 == kRing ? 0 : at + 1;
+        uint4 *o = q_out + 64 * grp + first;
+        o[v0] = y0;
+        o[v1] = y1;
+    }
+    // K's and V's heads lie one after the other in the pool's block, too (not in a 4-bit one).
+    const int64_t at_slot =
+        ((int64_t)blk * 2 * a.num_kv_heads * a.block_size + off) * (D / 8);
+    for (; grp < groups; grp += a.chunks) {
+        const int hd = grp * kHeads + lane / kLanes, kvh2 = hd - a.num_heads;
+        const bool live = hd < heads, is_q = kvh2 < 0, is_v = hd >= rot_heads;
         const int i0 = is_v ? u0 : v0, i1 = is_v ? u1 : v1;
         copies_wait<kRing - 1>();
         uint4 y0 = mine[at][0][lane], y1 = mine[at][1][lane];
-        if (!is_v) {
-            float p[8], q[8];
-            unpack<kNeighbours>(y0, y1, p, q);
-            if (is_q ? a.q_weight : a.k_weight) {
-                float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    fma2(sum0, sum1, p[i], p[i + 1], p[i], p[i + 1], sum0, sum1);
-                    fma2(sum0, sum1, q[i], q[i + 1], q[i], q[i + 1], sum0, sum1);
-                }
-                float sum = sum0 + sum1;
-                // The lanes of this head: those of V's heads are not here.
-                const uint32_t mask = ((1u << kLanes) - 1u) << (lane - t);
-#pragma unroll
-                for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
-                const float r = rsqrtf(sum * (1.f / D) + a.eps);
-                // Of the pairs' first and second elements: a vector's each, or half of both.
-                const float4 *w0 = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i0);
-                const float4 *w1 = reinterpret_cast<const float4 *>(weights[is_q ? 0 : 1] + 8 * i1);
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const float4 u = kNeighbours ? (i ? w1[0] : w0[0]) : w0[i / 4];
-                    const float4 v = kNeighbours ? (i ? w1[1] : w0[1]) : w1[i / 4];
-                    mul2(p[i], p[i + 1], r, r);
-                    mul2(p[i + 2], p[i + 3], r, r);
-                    mul2(q[i], q[i + 1], r, r);
-                    mul2(q[i + 2], q[i + 3], r, r);
-                    mul2(p[i], p[i + 1], u.x, u.y);
-                    mul2(p[i + 2], p[i + 3], u.z, u.w);
-                    mul2(q[i], q[i + 1], v.x, v.y);
-                    mul2(q[i + 2], q[i + 3], v.z, v.w);
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!turns[h]) continue;
-#pragma unroll
-                for (int i = 4 * h; i < 4 * h + 4; i += 2) {
-                    float pc0 = p[i], pc1 = p[i + 1], ps0 = p[i], ps1 = p[i + 1];
-                    float qc0 = q[i], qc1 = q[i + 1], qs0 = q[i], qs1 = q[i + 1];
-                    mul2(pc0, pc1, c[i], c[i + 1]);
-                    mul2(ps0, ps1, s[i], s[i + 1]);
-                    mul2(qc0, qc1, c[i], c[i + 1]);
-                    mul2(qs0, qs1, s[i], s[i + 1]);
-                    fma2(p[i], p[i + 1], qs0, qs1, -1.f, -1.f, pc0, pc1);  // pc - qs, one rounding
-                    add2(qc0, qc1, ps0, ps1);
-                    q[i] = qc0;
-                    q[i + 1] = qc1;
-                }
-            }
-            pack<kNeighbours>(p, q, y0, y1);
-        }
+        if (!is_v)
+            transform(y0, y1, (is_q ? a.q_weight : a.k_weight) != nullptr, weights[is_q ? 0 : 1]);
         fetch(min(grp + kRing * a.chunks, groups), at);
         at = at + 1 == kRing ? 0 : at + 1;
         __syncwarp();
-        if (live && is_q) {
+        if (is_q) {
             uint4 *o = q_out + 64 * grp + first;
             o[i0] = y0;
             o[i1] = y1;
         }
-        if (slot < 0 || (grp + 1) * kHeads <= a.num_heads) continue;  // no K or V here
-        const int side = is_v ? 1 : 0, kvh = hd - a.num_heads - side * a.num_kv_heads;
+        if (slot < 0) continue;
+        const int side = is_v ? 1 : 0;
         if constexpr (kBits == 4) {
             // A scale's 16 elements are vectors 2t and 2t + 1: of K they are fetched from where
             // they are.
@@ -302,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
                 }
             }
             if (live && !is_q) {
-                const Fp4Row to = fp4_row<D>(blk, off, kvh, side, a.num_kv_heads, a.block_size);
+                const Fp4Row to = fp4_row<D>(blk, off, kvh2 - side * a.num_kv_heads, side,
+                                             a.num_kv_heads, a.block_size);
                 uint2 codes;
                 uint8_t *kv = static_cast<uint8_t *>(a.kv);
                 kv[to.scale + t] = (uint8_t)fp4_quantise(
@@ -312,8 +335,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
                 reinterpret_cast<uint2 *>(kv + to.codes)[t] = codes;
             }
         } else if (live && !is_q) {
-            const int64_t to =
-                ((((int64_t)blk * 2 + side) * a.num_kv_heads + kvh) * a.block_size + off) * (D / 8);
+            const int64_t to = at_slot + kvh2 * a.block_size * (D / 8);
             if constexpr (kBits == 16) {
                 uint4 *kv = static_cast<uint4 *>(a.kv) + to;
                 kv[i0] = y0;
