@@ -5,6 +5,12 @@
 // element, each moved once.  A block's threads lie over the groups of one token's K and V rows
 // (several tokens where those are few), so that a thread keeps its column and finds only the
 // token's slot anew; it takes two or four tokens at once to have as many loads in flight.
+//
+// 4344 tokens of 2 x 8 heads of 128, in a graph: written in 7.2 us (7.5 at a scale of 1, whose
+// ties are common; 10.9 when each tie was divided, 12 with a division per element), read back in
+// 5.9; 32768 tokens 36.5 and 30.9, 4.7 and 5.6 TB/s.  Reading back is bound by the writes: to
+// fill its 134 MB of output alone takes 37 us (3.6 TB/s); stores with other cache policies
+// (evict first, streaming, write through) change nothing.
 #include <algorithm>
 #include <atomic>
 

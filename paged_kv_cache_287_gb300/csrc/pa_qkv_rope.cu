@@ -15,10 +15,14 @@
 // their own), so rotating needs no exchange; head_size / 16 threads make a head, a warp a group of 4 or 8 heads
 // (1 KB).  A warp takes a token, whose cosines and sines stay in registers for all its heads,
 // and copies its next groups into shared memory ahead (each thread its own vectors, so nothing
-// is synchronised).  4344 tokens of 32 + 2 x 8 heads of 128 with norms and three axes: 21.7 us,
-// 5.0 TB/s (75 % of the copy rate; a fill alone writes 3.6 TB/s here); with the rows loaded to
-// registers two groups at a time 28.8, with rings of 4, 5, 8 groups 22.1, 22.3, 27.8 (fewer
-// blocks), with a token shared by two warps 25.3, with blocks of 128 and 64 threads 22.2, 22.8.
+// is synchronised); 151 instructions a group of query heads with a norm, 96 without.
+//
+// 4344 tokens of 32 + 2 x 8 heads of 128, bf16 pool, in a graph over three states: 18.9 us with
+// one axis (5.7 TB/s moved, 85 % of the copy rate; norms make no difference), 20.7 with three;
+// FP8 pool 18.5, 4-bit 21.1 (64 bytes of codes and 8 of scales a head scatter more).  When the
+// ring came (three axes): 21.7; with the rows loaded to registers two groups at a time 28.8,
+// rings of 4, 5, 8 groups 22.1, 22.3, 27.8 (fewer blocks fit), a token shared by two warps 25.3,
+// blocks of 128 and 64 threads 22.2, 22.8.
 #include <algorithm>
 #include <atomic>
 
