@@ -532,6 +532,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 od[r][k] = ((u[k] >> 4) & 0x0f0f0f0fu) | (v[k] & 0xf0f0f0f0u);
             }
         }
+        // (the loads are done before the copy that takes their place)
+        fence_proxy_async_smem();
         __syncwarp();
         if (i + S < n) issue(i + S, st);
 #pragma unroll
@@ -792,10 +794,10 @@ cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, co
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = g.num_blocks;
     a.max_seq_len = max_seq_len;
-    a.scale_log2 = scale * 1.4426950408889634f * k_scale;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634 * k_scale);
     a.v_scale = v_scale;
     const long long segs = (long long)num_seqs * g.num_kv_heads;
-    const long long tiles = (max_seq_len + kTokens - 1) / kTokens;
+    const long long tiles = (max_seq_len + (long long)kTokens - 1) / kTokens;
     // A CTA per segment: no scan of the lengths, no second kernel, but a segment has one SM's
     // rate, 0.105 us a tile, where the split has a share of all SMs and some 4 us more.  Measured
     // (us, CTA per segment against the split; 8 segments): 8.0 / 9.8 at 1024 tokens, 11.0 / 9.3 at

@@ -345,7 +345,8 @@ def test_decode_scales(scale):
             assert (np.abs(got[s, h] - want) <= 2.0 ** -8 * np.abs(want) + 1e-30).all()
 
 
-@pytest.mark.parametrize("scales", [(1.0, 1.0), (2.0 ** -60, 2.0 ** 60), (2.0 ** 30, 2.0 ** -100)])
+@pytest.mark.parametrize("scales", [(1.0, 1.0), (2.0 ** -60, 2.0 ** 60), (2.0 ** 30, 2.0 ** -100),
+                                    (2.0 ** -130, 1.0), (2.0 ** 110, 1.0)])
 def test_decode_tensor_scales(scales):
     b = Batch([150, 40], 8, 2, 128, 16, seed=7)
     scale = 0.02 / scales[0]
