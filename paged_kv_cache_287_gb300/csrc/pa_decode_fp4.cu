@@ -7,8 +7,9 @@
 // elements a clock, so the work per element must stay below three instructions, and the layout
 // is chosen for that:
 //   * Tiles of 32 tokens of one (sequence, KV head): K and V, codes and scales, of a block are
-//     one run of memory and arrive by one bulk copy.  Every warp has a ring of tiles of its own
-//     and no warp waits for another in the loop.
+//     one run of memory, which the lanes of a warp copy 16 bytes each (asynchronously, nine
+//     copies a tile).  Every warp has a ring of tiles of its own and no warp waits for another
+//     in the loop; a stage is filled anew as soon as its V is in registers.
 //   * S^T = K.Q^T by m16n8k16 (16 tokens x 8 query heads): a lane reads 32 dims (16 bytes) of
 //     its token at once; which of the MMA's k-slots a dim takes is free, so the query's
 //     fragments are laid out to match (32 consecutive dims a lane).  A byte of codes becomes an
@@ -24,14 +25,15 @@
 // those in several CTAs by a second kernel (a record per CTA and end of its range); few or short
 // segments go to CTAs whole (rules at launch_decode_fp4).
 //
-// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 121 us, 84 %
-// of the copy rate, 32 of up to 131072 tokens 165 us, 89 %.  In the steady state a tile takes
-// 0.75 ns of the whole GPU (92 %); without V's products it would be 0.69 (100 %): of 594 warp
+// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 120 us, 85 %
+// of the copy rate, 32 of up to 131072 tokens 163 us, 90 %.  In the steady state a tile takes
+// 0.75 ns of the whole GPU (92 %); without V's products it would be 0.69 (100 %): of 596 warp
 // instructions a tile 302 are the products with their conversions, 39 the softmax, 95 loads,
-// scales and interleaving, the rest waits, issue and bookkeeping, at 2.6 a clock.  Tried and
-// slower: 12 or 14 warps (131, 135; the registers allow 16), 8 with four stages each (154), the
-// last of the CTAs to come merging a segment in place of the second kernel (125), copies of 16
-// bytes by every lane (120.5, but 24.3 against 23.2 for 47 sequences, and spills).
+// scales and interleaving, the rest copies, waits and bookkeeping, at 2.6 a clock.  Tried and
+// slower: a bulk copy per block by one lane, completing on an mbarrier (122.5, 167; the copies'
+// uniform operands cost as many instructions, and the loads a fence before the next copy), 12
+// or 14 warps (131, 135; the registers allow 16), 8 with four stages each (154), the last of the
+// CTAs to come merging a segment in place of the second kernel (125).
 #include <algorithm>
 #include <atomic>
 
@@ -136,8 +138,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
     uint8_t *ring = smem;
     float *recs = reinterpret_cast<float *>(ring + kWarps * S * kStage);
     int4 *descs = reinterpret_cast<int4 *>(recs + kWarps * kRec);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(descs + kWarps * S);
-    WarpPieces *pieces = reinterpret_cast<WarpPieces *>(bars + kWarps * S);
+    WarpPieces *pieces = reinterpret_cast<WarpPieces *>(descs + kWarps * S);
     int *sums = reinterpret_cast<int *>(pieces + kWarps);
     const int B = a.num_seqs, Hkv = a.num_kv_heads, G = a.group;
     int *lens = sums + kWarps;  // [num_seqs], and their tiles' prefix sums [num_seqs + 1];
@@ -145,15 +146,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    uint64_t *bar = bars + warp * S;
     int4 *desc = descs + warp * S;
     uint8_t *stages = ring + warp * S * kStage;
-    if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 1);
-        fence_barrier_init();
-        pieces[warp] = {0, 0, 0, 0};
-    }
-    __syncwarp();
+    if (lane == 0) pieces[warp] = {0, 0, 0, 0};
     pdl_begin();
 
     // This warp's tiles [t0, t1) of the list (aligned mode: of its CTA's segment).
@@ -234,10 +229,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         for (int i = tid; i < rows * (D / 8); i += kWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
     }
 
-    // Tile t0 + 32 k + lane: its segment, place, tokens, and blocks (-1: outside the pool).
+    // Tile t0 + 32 k + lane: its segment, place, tokens, and blocks (-1: none, or outside the pool).
     struct Tile {
-        int4 d;  // (sequence << 8 | head), tile of the segment, tokens, 1: its last tile, 2: all
-                 // of its blocks are there
+        int4 d;  // (sequence << 8 | head), tile of the segment, tokens, whether it is the last
         int ids[kNB];
     };
     const int n = t1 - t0;
@@ -261,63 +255,63 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         }
         const int left = (a.aligned ? own_len : lens[s]) - j * kTokens;
         const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks + j * kNB;
-        bool all = left >= kTokens;
 #pragma unroll
         for (int b = 0; b < kNB; ++b) {
             if (b * BS >= left) continue;
             const int id = bt[b];
-            if (id >= 0 && id < a.num_blocks) {
+            if (id >= 0 && id < a.num_blocks)
                 t.ids[b] = id;
-            } else {
+            else
                 atomicOr(&g_err_decode_fp4, kErrOob);
-                all = false;
-            }
         }
-        t.d = make_int4(s << 8 | h, j, min(left, kTokens), (left <= kTokens) | (all ? 2 : 0));
+        t.d = make_int4(s << 8 | h, j, min(left, kTokens), left <= kTokens);
         return t;
     };
     Tile tile = describe(0), next_tile = tile;
     const uint64_t policy = policy_evict_first();
 
-    // Called by the whole warp, for i in order; lane i & 31 issues.
+    // Called by the whole warp, for i in order: a group of copies, empty past the last tile.  A
+    // lane copies every 32nd chunk of 16 bytes; a block that is not there becomes zeros.
+    constexpr int kChunks = 2 * kTile / 16;  // of a block
+    const uint32_t stages_at = smem_u32(stages) + lane * 16;
     auto issue = [&](int i, int st) {
-        if ((i & 31) == 16 && (i | 31) + 1 < n) next_tile = describe((i >> 5) + 1);
-        if ((i & 31) == 0 && i > 0) tile = next_tile;
-        if (lane == (i & 31)) {
-            uint8_t *dst = stages + st * kStage;
-            desc[st] = tile.d;
-            const int64_t head = (int64_t)(tile.d.x & 255) * (2 * kTile);
-            auto src = [&](int b) {
-                return a.kv + (int64_t)tile.ids[b] * a.block_bytes + head;
+        if (i < n) {
+            if (i > 0 && i % 16 == 0) {
+                if (i % 32 == 0) tile = next_tile;
+                else next_tile = describe(i / 32 + 1);
+            }
+            const int from = i % 32;
+            if (lane == from) desc[st] = tile.d;
+            const int head = __shfl_sync(0xffffffffu, tile.d.x, from) & 255;
+            int id = __shfl_sync(0xffffffffu, tile.ids[0], from);
+            // Chunk `lane` of a tile that began with block b.
+            auto base = [&](int b) {
+                return a.kv + (int64_t)max(id, 0) * a.block_bytes +
+                       (head * 2 * kTile + lane * 16 - b * 2 * kTile);
             };
-            if (tile.d.w & 2) {
-                mbar_arrive_expect_tx(&bar[st], kStage);
+            const uint8_t *src = base(0);
+            bool live = id >= 0;
+            const uint32_t dst = stages_at + st * kStage;
 #pragma unroll
-                for (int b = 0; b < kNB; ++b)
-                    bulk_load_hint(dst + b * 2 * kTile, src(b), 2 * kTile, &bar[st], policy);
-            } else {
-                uint32_t bytes = 0;
-#pragma unroll
-                for (int b = 0; b < kNB; ++b) {
-                    if (tile.ids[b] >= 0) {
-                        bytes += 2 * kTile;
-                    } else if (b * BS < tile.d.z) {  // outside the pool: its tokens are zeros
-                        for (int e = 0; e < 2 * kTile; e += 16)
-                            *reinterpret_cast<uint4 *>(dst + b * 2 * kTile + e) =
-                                make_uint4(0, 0, 0, 0);
-                    }
+            for (int k = 0; k < (kNB * kChunks + 31) / 32; ++k) {
+                // A block ends inside these 32 chunks, or none does (no block begins with them).
+                const int b1 = (32 * k + 31) / kChunks;
+                if (b1 > 32 * k / kChunks && b1 < kNB) {
+                    const uint8_t *before = src;
+                    const bool live_before = live, up = lane >= b1 * kChunks - 32 * k;
+                    id = __shfl_sync(0xffffffffu, tile.ids[b1], from);
+                    src = base(b1);
+                    live = id >= 0;
+                    copy16_hint(dst + 512 * k, (up ? src : before) + 512 * k,
+                                up ? live : live_before, policy);
+                } else if (32 * k + 32 <= kNB * kChunks || lane < kNB * kChunks - 32 * k) {
+                    copy16_hint(dst + 512 * k, src + 512 * k, live, policy);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive_expect_tx(&bar[st], bytes);
-#pragma unroll
-                for (int b = 0; b < kNB; ++b)
-                    if (tile.ids[b] >= 0)
-                        bulk_load_hint(dst + b * 2 * kTile, src(b), 2 * kTile, &bar[st], policy);
             }
         }
-        __syncwarp();
+        copies_commit();
     };
-    for (int i = 0; i < min(n, S); ++i) issue(i, i);
+    for (int i = 0; i < S; ++i) issue(i, i);
 
     float acc[D / 16][4];
     uint32_t qf[D / 16][2];
@@ -334,15 +328,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
     const int tok_v0 = rv, tok_v1 = rv ^ 1;
 
     int st = 0;
-    uint32_t phase = 0;
     for (int i = 0; i < n; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bar[st], phase))) {
-            // Give the copies in flight their time to land, and leave no piece.
-            if (lane == 0) atomicOr(&g_err_decode_fp4, kErrTimeout);
-            for (int k = 1; k < S && i + k < n; ++k)
-                mbar_wait_bounded(&bar[(st + k) % S], phase ^ (st + k >= S ? 1u : 0u));
-            break;
-        }
+        // Of the S groups in flight the oldest is this tile.
+        if (S == 1) copies_wait<0>();
+        else if (S == 2) copies_wait<1>();
+        else if (S == 3) copies_wait<2>();
+        else copies_wait<3>();
+        __syncwarp();
         const uint8_t *buf = stages + st * kStage;
         const int4 d = desc[st];
         const int valid = d.z;
@@ -405,7 +397,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                     *reinterpret_cast<uint2 *>(scl) = make_uint2(0u, 0u);
                 else
                     *reinterpret_cast<uint32_t *>(scl) = 0u;
-                fence_proxy_async_smem();
             }
             __syncwarp();
         }
@@ -532,10 +523,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 od[r][k] = ((u[k] >> 4) & 0x0f0f0f0fu) | (v[k] & 0xf0f0f0f0u);
             }
         }
-        // (the loads are done before the copy that takes their place)
-        fence_proxy_async_smem();
         __syncwarp();
-        if (i + S < n) issue(i + S, st);
+        issue(i + S, st);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
@@ -575,7 +564,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                     pieces[warp].a = 1;
                     pieces[warp].a_ends = last;
                 }
-            } else {  // the range's last tile: every copy of the ring has been used
+            } else {  // the range's last tile: the ring is empty
                 store_rec<D>(reinterpret_cast<float *>(stages), acc, lane, -nm0 * cs0, l0, -nm1 * cs1, l1);
                 if (lane == 0) {
                     pieces[warp].b = 1;
@@ -584,10 +573,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             seg = -1;
         }
-        if (++st == S) {
-            st = 0;
-            phase ^= 1u;
-        }
+        if (++st == S) st = 0;
     }
 
     // The pieces of segments that span warps, a group of them per warp in which such a segment
@@ -732,7 +718,7 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
 
 template <int D>
 size_t smem_bytes(int stages, int num_seqs) {
-    return (size_t)kWarps * stages * (kStageBytes<D> + sizeof(int4) + 8) +
+    return (size_t)kWarps * stages * (kStageBytes<D> + sizeof(int4)) +
            (size_t)kWarps * (kRecFloats<D> * 4 + sizeof(WarpPieces) + 4) +
            ((size_t)num_seqs * 2 + 1) * 4;
 }

@@ -4,7 +4,7 @@
 // tile = block_size rows of head_size / 2 bytes (element 2i is the low nibble of byte i, an OCP
 // e2m1 code), then block_size rows of head_size / 16 e4m3 scales, one per 16 elements.  An
 // element is code * scale * g, g the tensor's k_scale or v_scale.  K and V of a (block, head)
-// are one run of block_size * head_size * 9 / 8 bytes, which one bulk copy fetches.
+// are one run of block_size * head_size * 9 / 8 bytes.
 #pragma once
 
 #include <cmath>

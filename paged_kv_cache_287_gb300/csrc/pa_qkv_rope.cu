@@ -71,19 +71,6 @@ constexpr int kRing = 3;        // groups of heads (1 KB each) in flight per war
 constexpr int kPerSm = 4;       // blocks; 32 warps of 64 registers
 constexpr int kWarpsPerSm = 24; // a token's heads are shared out while there are fewer warps
 
-__device__ __forceinline__ void copy16(uint4 *dst, const uint4 *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// All but the last N groups of this thread's copies have landed.
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // What divides K and V: by the scales (FP8), by six times those (4 bits).
 struct Divisors {
     Around k, v;
