@@ -680,7 +680,8 @@ pa_status pa_cache_read_fp4(const pa_cache_fp4_args *args);
  *   workspace     >= pa_decode_fp4_workspace_bytes(...) bytes, 256-byte aligned, no
  *                 initialisation needed; calls that overlap on the GPU must not share one
  * A block id outside the pool is flagged PA_ERR_OOB and its tokens read as zeros.  num_seqs up
- * to 11447 (head_size 128) or 20151 (64), else PA_ERR_UNSUPPORTED.  out and q must not overlap.
+ * to 9943 (head_size 128) or 18647 (64), else PA_ERR_UNSUPPORTED (512 more with blocks of 16 or
+ * 32).  out and q must not overlap.
  * Other arguments and errors as pa_decode.
  */
 typedef struct pa_decode_fp4_args {

@@ -960,12 +960,15 @@ pa_status pa_decode_fp4(const pa_decode_fp4_args *a) {
         return PA_ERR_INVALID_ARG;
     if (a->max_seq_len > (long long)a->max_blocks_per_seq * a->block_size)
         return PA_ERR_INVALID_ARG;
-    // Units of work over (sequence, KV head), and a length rounded up to a tile, fit 31 bits.
-    if ((long long)a->num_seqs * a->num_kv_heads * ((a->max_seq_len + 31LL) / 32 + 1) >=
+    // Units of work over (sequence, KV head), a length rounded up to a tile, and (block, KV head)
+    // numbers fit 31 bits.
+    if ((long long)a->num_blocks * a->num_kv_heads >= (1LL << 31) ||
+        (long long)a->num_seqs * a->num_kv_heads * ((a->max_seq_len + 31LL) / 32 + 1) >=
             (1LL << 31) ||
         a->max_seq_len > INT32_MAX - 31)
         return PA_ERR_UNSUPPORTED;
-    if (a->num_seqs > pa::decode_fp4_max_seqs(a->head_size)) return PA_ERR_UNSUPPORTED;
+    if (a->num_seqs > pa::decode_fp4_max_seqs(a->head_size, a->block_size))
+        return PA_ERR_UNSUPPORTED;
     const size_t need = pa::decode_fp4_workspace_bytes(a->head_size, pa::device_sm_count());
     if (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < need)
         return PA_ERR_WORKSPACE;

@@ -58,7 +58,7 @@ template <int D>
 constexpr int kStageBytes = kTokens *D * 9 / 8;
 template <int D>
 constexpr int kRecFloats = kHeads * (D + 2);  // acc [8][D], then (m, l) [8]
-// Tiles in flight per warp: 147 KB in flight per SM.
+// Tiles in flight per warp: 147 KB in flight per SM; one where the batch's tables need the room.
 template <int D>
 constexpr int kMaxStages = 256 / D;
 
@@ -69,9 +69,7 @@ struct Args {
     const int32_t *block_tables, *seq_lens;
     float *recs;  // [CTAs][2][kRecFloats]: a segment's piece at the range's start, at its end
     int4 *meta;   // [CTAs]: piece at the start, it ends here, piece at the end, its segment
-    int64_t block_bytes;
     int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, max_seq_len;
-    int stages;
     int aligned;  // CTA c is segment c
     int whole;    // every CTA takes whole segments: no piece leaves it
     float scale_log2, v_scale;  // scale * log2(e) * k_scale
@@ -96,6 +94,12 @@ __device__ __forceinline__ int sequence_of(const int *pre, int num_seqs, int num
     }
     return lo;
 }
+
+// Flags of a tile beside its tokens: the last, the first of its segment.
+constexpr int kLast = 64, kFirst = 128;
+// Ints of a tile's entry: segment, flags, blocks; a multiple of two.
+template <int BS>
+constexpr int kEntryInts = BS == 8 ? 6 : 4;
 
 // 16 (D 128) or 8 consecutive dims of one head: acc[mt][e] and acc[mt][e + 2] are dims 2 mt and
 // 2 mt + 1 of them.
@@ -127,18 +131,19 @@ __device__ __forceinline__ void store_rec(float *rec, const float (&acc)[D / 16]
         *reinterpret_cast<float4 *>(rec + kHeads * D + 4 * c) = make_float4(m0, l0, m1, l1);
 }
 
-template <int D, int BS>
+template <int D, int BS, int S>
 __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a) {
     constexpr int kStage = kStageBytes<D>, kRec = kRecFloats<D>;
     constexpr int kTile = BS * D * 9 / 16;      // K's (or V's) bytes of a (block, head)
     constexpr int kNB = kTokens / BS;           // blocks of a tile
     constexpr int kRow = D / 2, kScRow = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int S = a.stages;
+    constexpr int kEntry = kEntryInts<BS>;
     uint8_t *ring = smem;
     float *recs = reinterpret_cast<float *>(ring + kWarps * S * kStage);
-    int4 *descs = reinterpret_cast<int4 *>(recs + kWarps * kRec);
-    WarpPieces *pieces = reinterpret_cast<WarpPieces *>(descs + kWarps * S);
+    int *entries = reinterpret_cast<int *>(recs + kWarps * kRec) + (threadIdx.x >> 5) * 32 * kEntry;
+    WarpPieces *pieces =
+        reinterpret_cast<WarpPieces *>(recs + kWarps * (kRec + 32 * kEntry));
     int *sums = reinterpret_cast<int *>(pieces + kWarps);
     const int B = a.num_seqs, Hkv = a.num_kv_heads, G = a.group;
     int *lens = sums + kWarps;  // [num_seqs], and their tiles' prefix sums [num_seqs + 1];
@@ -146,7 +151,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    int4 *desc = descs + warp * S;
     uint8_t *stages = ring + warp * S * kStage;
     if (lane == 0) pieces[warp] = {0, 0, 0, 0};
     pdl_begin();
@@ -229,68 +233,65 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         for (int i = tid; i < rows * (D / 8); i += kWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
     }
 
-    // Tile t0 + 32 k + lane: its segment, place, tokens, and blocks (-1: none, or outside the pool).
-    struct Tile {
-        int4 d;  // (sequence << 8 | head), tile of the segment, tokens, whether it is the last
-        int ids[kNB];
-    };
+    // Tile i of this warp has entry i % 32 of a table: its segment (sequence << 8 | head), its
+    // tokens | kLast | kFirst, and its blocks as numbers of a (block, head) (-1: none, or outside
+    // the pool).  `count` entries from tile `from` on, a lane each.
     const int n = t1 - t0;
-    auto describe = [&](int k) {
-        Tile t;
-        t.d = make_int4(0, 0, 0, 0);
+    auto describe = [&](int from, int count) {
+        const int i = from + lane, x = t0 + i;
+        if (lane < count && i < n) {
+            int s, h, j;
+            if (a.aligned) {
+                s = blockIdx.x / Hkv;
+                h = blockIdx.x - s * Hkv;
+                j = x;
+            } else {
+                s = sequence_of(pre, B, Hkv, x);
+                const int nt = pre[s + 1] - pre[s], r = x - Hkv * pre[s];
+                h = r / nt;
+                j = r - h * nt;
+            }
+            const int left = (a.aligned ? own_len : lens[s]) - j * kTokens;
+            const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks + j * kNB;
+            int *e = entries + i % 32 * kEntry;
+            *reinterpret_cast<int2 *>(e) =
+                make_int2(s << 8 | h, min(left, kTokens) | (left <= kTokens ? kLast : 0) |
+                                          (j == 0 ? kFirst : 0));
 #pragma unroll
-        for (int b = 0; b < kNB; ++b) t.ids[b] = -1;
-        const int x = t0 + 32 * k + lane;
-        if (x >= t1) return t;
-        int s, h, j;
-        if (a.aligned) {
-            s = blockIdx.x / Hkv;
-            h = blockIdx.x - s * Hkv;
-            j = x;
-        } else {
-            s = sequence_of(pre, B, Hkv, x);
-            const int nt = pre[s + 1] - pre[s], r = x - Hkv * pre[s];
-            h = r / nt;
-            j = r - h * nt;
+            for (int b = 0; b < kNB; ++b) {
+                int unit = -1;
+                if (b * BS < left) {
+                    const int id = bt[b];
+                    if (id >= 0 && id < a.num_blocks)
+                        unit = id * Hkv + h;
+                    else
+                        atomicOr(&g_err_decode_fp4, kErrOob);
+                }
+                e[2 + b] = unit;
+            }
         }
-        const int left = (a.aligned ? own_len : lens[s]) - j * kTokens;
-        const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks + j * kNB;
-#pragma unroll
-        for (int b = 0; b < kNB; ++b) {
-            if (b * BS >= left) continue;
-            const int id = bt[b];
-            if (id >= 0 && id < a.num_blocks)
-                t.ids[b] = id;
-            else
-                atomicOr(&g_err_decode_fp4, kErrOob);
-        }
-        t.d = make_int4(s << 8 | h, j, min(left, kTokens), left <= kTokens);
-        return t;
+        __syncwarp();
     };
-    Tile tile = describe(0), next_tile = tile;
+    describe(0, 32);
     const uint64_t policy = policy_evict_first();
 
     // Called by the whole warp, for i in order: a group of copies, empty past the last tile.  A
     // lane copies every 32nd chunk of 16 bytes; a block that is not there becomes zeros.
     constexpr int kChunks = 2 * kTile / 16;  // of a block
     const uint32_t stages_at = smem_u32(stages) + lane * 16;
+    const uint8_t *kv = a.kv + lane * 16;
     auto issue = [&](int i, int st) {
         if (i < n) {
-            if (i > 0 && i % 16 == 0) {
-                if (i % 32 == 0) tile = next_tile;
-                else next_tile = describe(i / 32 + 1);
-            }
-            const int from = i % 32;
-            if (lane == from) desc[st] = tile.d;
-            const int head = __shfl_sync(0xffffffffu, tile.d.x, from) & 255;
-            int id = __shfl_sync(0xffffffffu, tile.ids[0], from);
+            // The table's older half has been used (S is at most 8).
+            if (i % 16 == 8 && i >= 24) describe(i + 8, 16);
+            const int *units = entries + i % 32 * kEntry + 2;
             // Chunk `lane` of a tile that began with block b.
+            int unit = units[0];
             auto base = [&](int b) {
-                return a.kv + (int64_t)max(id, 0) * a.block_bytes +
-                       (head * 2 * kTile + lane * 16 - b * 2 * kTile);
+                return kv + (int64_t)max(unit, 0) * (2 * kTile) - b * 2 * kTile;
             };
             const uint8_t *src = base(0);
-            bool live = id >= 0;
+            bool live = unit >= 0;
             const uint32_t dst = stages_at + st * kStage;
 #pragma unroll
             for (int k = 0; k < (kNB * kChunks + 31) / 32; ++k) {
@@ -299,9 +300,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 if (b1 > 32 * k / kChunks && b1 < kNB) {
                     const uint8_t *before = src;
                     const bool live_before = live, up = lane >= b1 * kChunks - 32 * k;
-                    id = __shfl_sync(0xffffffffu, tile.ids[b1], from);
+                    unit = units[b1];
                     src = base(b1);
-                    live = id >= 0;
+                    live = unit >= 0;
                     copy16_hint(dst + 512 * k, (up ? src : before) + 512 * k,
                                 up ? live : live_before, policy);
                 } else if (32 * k + 32 <= kNB * kChunks || lane < kNB * kChunks - 32 * k) {
@@ -311,15 +312,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         }
         copies_commit();
     };
+#pragma unroll
     for (int i = 0; i < S; ++i) issue(i, i);
 
     float acc[D / 16][4];
     uint32_t qf[D / 16][2];
-    // Of heads 2c and 2c + 1: what brings a score to log2 units, minus the reference and the
-    // slack in the score's own units, the sum of P.
-    float cs0 = 0.f, cs1 = 0.f, nm0 = 0.f, nm1 = 0.f, slack0 = 0.f, slack1 = 0.f;
+    // Of heads 2c and 2c + 1: what brings a score to log2 units; in the score's own units minus
+    // the reference, and the score above which it is raised; the sum of P.
+    float cs0 = 0.f, cs1 = 0.f, nm0 = 0.f, nm1 = 0.f, bar0 = 0.f, bar1 = 0.f;
     float l0 = 0.f, l1 = 0.f;
-    int seg = -1, first_j = 0;
+    int seg = -1;
+    bool inside = false;  // whether this piece begins inside its segment
     // Offsets of 8-token group j's first row, and of this lane's rows: K's row g is token rk of
     // the group, V's k-slots 2c and 2c + 1 are tokens rv and rv ^ 1.
     auto codes_at = [](int j) { return 8 * j / BS * 2 * kTile + 8 * j % BS * kRow; };
@@ -330,19 +333,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
     int st = 0;
     for (int i = 0; i < n; ++i) {
         // Of the S groups in flight the oldest is this tile.
-        if (S == 1) copies_wait<0>();
-        else if (S == 2) copies_wait<1>();
-        else if (S == 3) copies_wait<2>();
-        else copies_wait<3>();
+        copies_wait<S - 1>();
         __syncwarp();
         const uint8_t *buf = stages + st * kStage;
-        const int4 d = desc[st];
-        const int valid = d.z;
+        const int2 d = *reinterpret_cast<const int2 *>(entries + i % 32 * kEntry);
+        const int valid = d.y & 63;
         if (d.x != seg) {
             // A new segment: its query heads, scaled by powers of two into [1, 2) at their
             // largest element.
             seg = d.x;
-            first_j = d.y;
+            inside = !(d.y & kFirst);
             float qv[D / 4];
             float mx = 0.f;
             const uint4 *src = reinterpret_cast<const uint4 *>(
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
             nm0 = nm1 = -kLowest;
-            slack0 = kSlack / cs0;
-            slack1 = kSlack / cs1;
+            bar0 = kSlack / cs0 - nm0;
+            bar1 = kSlack / cs1 - nm1;
             l0 = l1 = 0.f;
         }
 
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         }
         float t0x = fmaxf(fmax3(x[0][0], x[0][2], x[1][0]), x[1][2]);
         float t1x = fmaxf(fmax3(x[0][1], x[0][3], x[1][1]), x[1][3]);
-        if (__any_sync(0xffffffffu, t0x > slack0 - nm0 || t1x > slack1 - nm1)) {
+        if (__any_sync(0xffffffffu, t0x > bar0 || t1x > bar1)) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 t0x = fmaxf(t0x, __shfl_xor_sync(0xffffffffu, t0x, o));
@@ -467,6 +467,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             const float r0 = fast_exp2((n0 - nm0) * cs0), r1 = fast_exp2((n1 - nm1) * cs1);
             nm0 = n0;
             nm1 = n1;
+            bar0 = kSlack / cs0 - nm0;
+            bar1 = kSlack / cs1 - nm1;
             l0 *= r0;
             l1 *= r1;
 #pragma unroll
@@ -545,20 +547,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
         }
 
-        const bool last = d.w & 1;
+        const bool last = d.y & kLast;
         if (last || i == n - 1) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 l0 += __shfl_xor_sync(0xffffffffu, l0, o);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, o);
             }
-            if (first_j == 0 && last) {
+            if (!inside && last) {
                 __nv_bfloat16 *row =
                     a.out + ((size_t)(seg >> 8) * a.num_heads + (seg & 255) * G + 2 * c) * D +
                     g * (D / 8);
                 if (2 * c < G) store_rows<D>(row, acc, 0, a.v_scale / l0);
                 if (2 * c + 1 < G) store_rows<D>(row + D, acc, 1, a.v_scale / l1);
-            } else if (first_j != 0) {
+            } else if (inside) {
                 store_rec<D>(recs + warp * kRec, acc, lane, -nm0 * cs0, l0, -nm1 * cs1, l1);
                 if (lane == 0) {
                     pieces[warp].a = 1;
@@ -716,31 +718,37 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
         make_uint2(pack_bf16(num.x * f, num.y * f), pack_bf16(num.z * f, num.w * f));
 }
 
-template <int D>
+template <int D, int BS>
 size_t smem_bytes(int stages, int num_seqs) {
-    return (size_t)kWarps * stages * (kStageBytes<D> + sizeof(int4)) +
-           (size_t)kWarps * (kRecFloats<D> * 4 + sizeof(WarpPieces) + 4) +
+    return (size_t)kWarps * (stages * kStageBytes<D> + kRecFloats<D> * 4 + 32 * kEntryInts<BS> * 4 +
+                             sizeof(WarpPieces) + 4) +
            ((size_t)num_seqs * 2 + 1) * 4;
 }
 
 constexpr size_t kSmemMax = 232448;
 
 template <int D>
-int max_seqs() {
-    return (int)((kSmemMax - smem_bytes<D>(1, 0)) / 8);
+int max_seqs(int block_size) {
+    const size_t rest = block_size == 8 ? smem_bytes<D, 8>(1, 0) : smem_bytes<D, 16>(1, 0);
+    return (int)((kSmemMax - rest) / 8);
+}
+
+template <int D, int BS, int S>
+cudaError_t launch_stages(const Args &a, int grid, cudaStream_t stream) {
+    const size_t smem = smem_bytes<D, BS>(S, a.aligned ? 0 : a.num_seqs);
+    const cudaError_t e = ensure_smem<decode_fp4_kernel<D, BS, S>>(smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(decode_fp4_kernel<D, BS, S>, dim3((unsigned)grid), kWarps * 32, smem, 1,
+                      stream, a);
 }
 
 template <int D, int BS>
-cudaError_t launch(Args a, int grid, cudaStream_t stream) {
-    int stages = kMaxStages<D>;
-    const int table = a.aligned ? 0 : a.num_seqs;
-    while (stages > 1 && smem_bytes<D>(stages, table) > kSmemMax) --stages;
-    a.stages = stages;
-    const size_t smem = smem_bytes<D>(stages, table);
-    cudaError_t e = ensure_smem<decode_fp4_kernel<D, BS>>(smem);
-    if (e != cudaSuccess) return e;
+cudaError_t launch(const Args &a, int grid, cudaStream_t stream) {
     g_launched.store(true);
-    e = launch_pdl(decode_fp4_kernel<D, BS>, dim3((unsigned)grid), kWarps * 32, smem, 1, stream, a);
+    const bool room =
+        smem_bytes<D, BS>(kMaxStages<D>, a.aligned ? 0 : a.num_seqs) <= kSmemMax;
+    const cudaError_t e = room ? launch_stages<D, BS, kMaxStages<D>>(a, grid, stream)
+                               : launch_stages<D, BS, 1>(a, grid, stream);
     if (e != cudaSuccess || a.whole) return e;
     return launch_pdl(decode_fp4_merge_kernel<D>, dim3((unsigned)grid), kHeads * D / 4, 0, 1,
                       stream, a, grid);
@@ -756,7 +764,9 @@ size_t decode_fp4_workspace_bytes(int head_size, int sm_count) {
     return (size_t)sm_count * (2 * kHeads * (head_size + 2) * 4 + sizeof(int4));
 }
 
-int decode_fp4_max_seqs(int head_size) { return head_size == 128 ? max_seqs<128>() : max_seqs<64>(); }
+int decode_fp4_max_seqs(int head_size, int block_size) {
+    return head_size == 128 ? max_seqs<128>(block_size) : max_seqs<64>(block_size);
+}
 
 cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, const KvGeom &g,
                               int num_heads, const int32_t *block_tables, int max_blocks_per_seq,
@@ -776,7 +786,6 @@ cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, co
     a.num_heads = num_heads;
     a.num_kv_heads = g.num_kv_heads;
     a.group = num_heads / g.num_kv_heads;
-    a.block_bytes = (int64_t)g.block_size * g.num_kv_heads * g.head_size / 8 * 9;
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = g.num_blocks;
     a.max_seq_len = max_seq_len;

@@ -224,7 +224,7 @@ cudaError_t launch_cache_fp4(bool write, void *kv_cache, const KvGeom &g, void *
                              int num_tokens, float k_scale, float v_scale, cudaStream_t stream);
 size_t decode_fp4_workspace_bytes(int head_size, int sm_count);
 // Largest num_seqs whose table fits beside a ring of one tile per warp.
-int decode_fp4_max_seqs(int head_size);
+int decode_fp4_max_seqs(int head_size, int block_size);
 cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, const KvGeom &g,
                               int num_heads, const int32_t *block_tables, int max_blocks_per_seq,
                               const int32_t *seq_lens, int num_seqs, int max_seq_len, float scale,

@@ -173,8 +173,9 @@ def test_cache_refusals(lib, status, kw):
     (2, dict(d=256)), (2, dict(bs=64)), (1, dict(mb=0)), (1, dict(max_len=65)),
     (1, dict(max_len=-1)), (1, dict(scale=NAN)), (1, dict(scale=INF)), (1, dict(ks=0.0)),
     (1, dict(vs=NAN)), (1, dict(ks=1e36)), (2, dict(b=1 << 20, mb=1 << 16, max_len=1 << 20)),
-    (2, dict(b=1, mb=1 << 28, max_len=(1 << 31) - 1)), (2, dict(b=11448)),
-    (2, dict(b=20152, d=64)), (6, dict(ws=0)),
+    (2, dict(b=1, mb=1 << 28, max_len=(1 << 31) - 1)), (2, dict(b=10456)),
+    (2, dict(b=19160, d=64)), (2, dict(b=9944, bs=8, max_len=9)),
+    (2, dict(b=18648, bs=8, d=64, max_len=9)), (6, dict(ws=0)),
     (6, dict(ws=FAKE + 128)), (6, dict(ws_bytes=100)), (0, dict(b=0)),
 ])
 def test_decode_refusals(lib, status, kw):
