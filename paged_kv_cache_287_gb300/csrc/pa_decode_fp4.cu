@@ -25,15 +25,16 @@
 // those in several CTAs by a second kernel (a record per CTA and end of its range); few or short
 // segments go to CTAs whole (rules at launch_decode_fp4).
 //
-// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 120 us, 85 %
-// of the copy rate, 32 of up to 131072 tokens 163 us, 90 %.  In the steady state a tile takes
-// 0.75 ns of the whole GPU (92 %); without V's products it would be 0.69 (100 %): of 596 warp
-// instructions a tile 302 are the products with their conversions, 39 the softmax, 95 loads,
-// scales and interleaving, the rest copies, waits and bookkeeping, at 2.6 a clock.  Tried and
-// slower: a bulk copy per block by one lane, completing on an mbarrier (122.5, 167; the copies'
-// uniform operands cost as many instructions, and the loads a fence before the next copy), 12
-// or 14 warps (131, 135; the registers allow 16), 8 with four stages each (154), the last of the
-// CTAs to come merging a segment in place of the second kernel (125).
+// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 113.5 us,
+// 90 % of the copy rate, 32 of up to 131072 tokens 154 us, 95 %.  Of 524 warp instructions a
+// tile 302 are the products with their conversions, 39 the softmax, 95 loads, scales and
+// interleaving, the rest copies, waits and bookkeeping.  Each of these brought its part: the
+// tiles' blocks found 16 tiles at a time by all lanes and kept in a table (120, 163 without),
+// the loop unrolled by its stages, so that their addresses are constants (118, 161 without).
+// Tried and slower: a bulk copy per block by one lane, completing on an mbarrier (by 2 %; the
+// copies' uniform operands cost as many instructions, and the loads a fence before the next
+// copy), 12 or 14 warps (by a tenth; the registers allow 16), 8 with four stages each (by a
+// quarter), the last of the CTAs to come merging a segment in place of the second kernel (by 4 %).
 #include <algorithm>
 #include <atomic>
 
@@ -280,10 +281,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
     constexpr int kChunks = 2 * kTile / 16;  // of a block
     const uint32_t stages_at = smem_u32(stages) + lane * 16;
     const uint8_t *kv = a.kv + lane * 16;
+    int refill = 24;  // the tile before whose copy the table's older half is written anew
     auto issue = [&](int i, int st) {
         if (i < n) {
-            // The table's older half has been used (S is at most 8).
-            if (i % 16 == 8 && i >= 24) describe(i + 8, 16);
+            // (the table's older half has been used: S is at most 8)
+            if (i == refill) {
+                describe(i + 8, 16);
+                refill += 16;
+            }
             const int *units = entries + i % 32 * kEntry + 2;
             // Chunk `lane` of a tile that began with block b.
             int unit = units[0];
@@ -330,8 +335,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
     const int rk = g ^ ((g >> 1) & 1), rv = 2 * c + (c & 1);
     const int tok_v0 = rv, tok_v1 = rv ^ 1;
 
-    int st = 0;
-    for (int i = 0; i < n; ++i) {
+    auto step = [&](int i, int st) __attribute__((always_inline)) {
         // Of the S groups in flight the oldest is this tile.
         copies_wait<S - 1>();
         __syncwarp();
@@ -386,21 +390,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             l0 = l1 = 0.f;
         }
 
-        if (valid < kTokens) {
-            // What lies behind the sequence may be anything: V's scales there are zero (and the
-            // scores below -inf).
-            if (lane >= valid) {
-                const int j = lane / 8, o = lane % 8;
-                uint8_t *scl = stages + st * kStage + kTile + 8 * j / BS * 2 * kTile + BS * kRow +
-                               (8 * j % BS + o) * kScRow;
-                if constexpr (D == 128)
-                    *reinterpret_cast<uint2 *>(scl) = make_uint2(0u, 0u);
-                else
-                    *reinterpret_cast<uint32_t *>(scl) = 0u;
-            }
-            __syncwarp();
-        }
-
         // Scores of two halves of 16 tokens: [0], [1] are heads 2c, 2c + 1 of row g, [2], [3] of
         // row g + 8.
         float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -449,11 +438,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
         }
         if (valid < kTokens) {
+            // What lies behind the sequence may be anything: its scores are -inf, V's scales zero.
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 if (16 * m + rk >= valid) x[m][0] = x[m][1] = -INFINITY;
                 if (16 * m + 8 + rk >= valid) x[m][2] = x[m][3] = -INFINITY;
             }
+            if (lane >= valid) {
+                const int j = lane / 8, o = lane % 8;
+                uint8_t *scl = stages + st * kStage + kTile + 8 * j / BS * 2 * kTile + BS * kRow +
+                               (8 * j % BS + o) * kScRow;
+                if constexpr (D == 128)
+                    *reinterpret_cast<uint2 *>(scl) = make_uint2(0u, 0u);
+                else
+                    *reinterpret_cast<uint32_t *>(scl) = 0u;
+            }
+            __syncwarp();
         }
         float t0x = fmaxf(fmax3(x[0][0], x[0][2], x[1][0]), x[1][2]);
         float t1x = fmaxf(fmax3(x[0][1], x[0][3], x[1][1]), x[1][3]);
@@ -575,7 +575,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             seg = -1;
         }
-        if (++st == S) st = 0;
+    };
+    if constexpr (S == 2) {  // (a stage's addresses are constants then)
+        for (int i = 0; i < n; i += 2) {
+            step(i, 0);
+            if (i + 1 < n) step(i + 1, 1);
+        }
+    } else {
+        for (int i = 0, st = 0; i < n; ++i, st = st + 1 == S ? 0 : st + 1) step(i, st);
     }
 
     // The pieces of segments that span warps, a group of them per warp in which such a segment
