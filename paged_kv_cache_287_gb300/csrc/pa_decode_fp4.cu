@@ -25,8 +25,11 @@
 // those in several CTAs by a second kernel (a record per CTA and end of its range); few or short
 // segments go to CTAs whole (rules at launch_decode_fp4).
 //
-// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 113.5 us,
-// 90 % of the copy rate, 32 of up to 131072 tokens 154 us, 95 %.  Of 524 warp instructions a
+// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 112 us,
+// 91 % of the copy rate, 32 of up to 131072 tokens 154 us, 95 %; in the steady state 0.66 ns a
+// tile of the whole GPU, 7.0 TB/s, so what is left are the ends (of 256 sequences: 2.4 us to the
+// first copy, 4 from the first warp's end to the median CTA's last, 2 to the last CTA's, 2 of
+// merges, 1.1 of hand-over, 1.3 the second kernel).  Of 524 warp instructions a
 // tile 302 are the products with their conversions, 39 the softmax, 95 loads, scales and
 // interleaving, the rest copies, waits and bookkeeping.  Each of these brought its part: the
 // tiles' blocks found 16 tiles at a time by all lanes and kept in a table (120, 163 without),
@@ -37,6 +40,7 @@
 // quarter), the last of the CTAs to come merging a segment in place of the second kernel (by 4 %).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "pa_fp4.cuh"
 #include "pa_tree.cuh"
@@ -587,7 +591,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 
     // The pieces of segments that span warps, a group of them per warp in which such a segment
     // began and one for the segment that began before the CTA's range: a warp per group and
-    // head.
+    // two heads.  (Mostly the latency of few instructions, fetched for the first time: 2.2 us at
+    // 16 groups of 4 heads one by one, 1.7 so; four heads at once 0.5 faster there, as much slower
+    // for the one segment of a short context.)
     __syncthreads();
     const WarpPieces lp = lane < kWarps ? pieces[lane] : WarpPieces{0, 0, 0, 0};
     const uint32_t through = __ballot_sync(0xffffffffu, lp.a && !lp.a_ends);  // a whole range
@@ -599,10 +605,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         ends = ending >> e & 1;
         return ends ? e : e - 1;
     };
-    const int groups = __popc(begun) + pieces[0].a;
-    for (int item = warp; item < groups * G; item += kWarps) {
-        const int hd = item % G;
-        int nth = item / G;
+    constexpr int kTogether = 2;
+    const int groups = __popc(begun) + pieces[0].a, parts = (G + kTogether - 1) / kTogether;
+    for (int item = warp; item < groups * parts; item += kWarps) {
+        // Of an odd group's last part the second head is the first again.
+        const int hd = item % parts * kTogether, next = hd + kTogether <= G ? 1 : 0;
+        int nth = item / parts;
         const bool head = nth == __popc(begun);
         uint32_t left = begun;
         for (; nth > 0 && left; --nth) left &= left - 1;
@@ -613,41 +621,59 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             return k == 0 && !head ? reinterpret_cast<const float *>(ring + w * S * kStage)
                                    : recs + (w + k) * kRec;
         };
-        float M = kLowest, den = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < np; ++k) M = fmaxf(M, rec_of(k)[kHeads * D + 2 * hd]);
+        float M[kTogether], den[kTogether];
         constexpr int E = D / 32;  // consecutive dims of a lane
-        float num[E];
+        using Dims = std::conditional_t<D == 128, float4, float2>;
+        float num[kTogether][E];
 #pragma unroll
-        for (int j = 0; j < E; ++j) num[j] = 0.f;
-#pragma unroll 4
+        for (int u = 0; u < kTogether; ++u) {
+            M[u] = kLowest;
+            den[u] = 0.f;
+#pragma unroll
+            for (int j = 0; j < E; ++j) num[u][j] = 0.f;
+        }
+#pragma unroll 2
+        for (int k = 0; k < np; ++k) {
+            const float *r = rec_of(k) + kHeads * D;
+#pragma unroll
+            for (int u = 0; u < kTogether; ++u) M[u] = fmaxf(M[u], r[2 * (hd + u * next)]);
+        }
+#pragma unroll 2
         for (int k = 0; k < np; ++k) {
             const float *r = rec_of(k);
-            const float2 ml = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * hd);
-            const float f = fast_exp2(ml.x - M);
-            den += f * ml.y;
 #pragma unroll
-            for (int j = 0; j < E; j += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(r + hd * D + lane * E + j);
-                num[j] += f * v.x;
-                num[j + 1] += f * v.y;
+            for (int u = 0; u < kTogether; ++u) {
+                const int at = hd + u * next;
+                const float2 ml = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * at);
+                const Dims v = *reinterpret_cast<const Dims *>(r + at * D + lane * E);
+                const float f = fast_exp2(ml.x - M[u]);
+                den[u] += f * ml.y;
+#pragma unroll
+                for (int j = 0; j < E; ++j) num[u][j] += f * reinterpret_cast<const float *>(&v)[j];
             }
         }
-        if (!head && ends) {
-            const int sg = pieces[w].b_seg;
-            const float inv = a.v_scale / den;
-            uint32_t *row = reinterpret_cast<uint32_t *>(
-                a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + hd) * D + lane * E);
+        const int sg = pieces[w].b_seg;
 #pragma unroll
-            for (int j = 0; j < E; j += 2) row[j / 2] = pack_bf16(num[j] * inv, num[j + 1] * inv);
-        } else {
-            float *r = a.recs + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * kRec;
+        for (int u = 0; u < kTogether; ++u) {
+            const int at = hd + u * next;
+            if (!head && ends) {
+                const float inv = a.v_scale / den[u];
+                uint32_t *row = reinterpret_cast<uint32_t *>(
+                    a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + at) * D +
+                    lane * E);
 #pragma unroll
-            for (int j = 0; j < E; j += 2)
-                *reinterpret_cast<float2 *>(r + hd * D + lane * E + j) =
-                    make_float2(num[j], num[j + 1]);
-            if (lane == 0)
-                *reinterpret_cast<float2 *>(r + kHeads * D + 2 * hd) = make_float2(M, den);
+                for (int j = 0; j < E; j += 2)
+                    row[j / 2] = pack_bf16(num[u][j] * inv, num[u][j + 1] * inv);
+            } else {
+                float *r = a.recs + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * kRec;
+                Dims v;
+#pragma unroll
+                for (int j = 0; j < E; ++j) reinterpret_cast<float *>(&v)[j] = num[u][j];
+                *reinterpret_cast<Dims *>(r + at * D + lane * E) = v;
+                if (lane == 0)
+                    *reinterpret_cast<float2 *>(r + kHeads * D + 2 * at) =
+                        make_float2(M[u], den[u]);
+            }
         }
     }
     if (!a.whole && tid == 0) {
@@ -662,15 +688,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 
 // Block i merges the segment that begins in CTA i and goes on: CTA i's record at its end, then
 // the next CTAs' at their starts, up to the one in which it ends.  A thread per head and four
-// dims; eight pieces are requested at once, weights and all.
+// dims.  The first two pieces are requested before it is known whether there are any (0.5 us),
+// more of them eight at once.
 template <int D>
 __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const Args a, int ctas) {
     pdl_begin();
     constexpr int kRec = kRecFloats<D>, kThreads = kHeads * D / 4, kBatch = 8;
     __shared__ int s_last;
     const int i = blockIdx.x, tid = threadIdx.x, G = a.group;
+    const int hd = tid * 4 / D, dim = tid * 4 % D;
+    auto rec_of = [&](int p) {
+        return a.recs + (p == 0 ? (size_t)i * 2 + 1 : (size_t)(i + p) * 2) * kRec;
+    };
     if (tid == 0) s_last = ctas - 1;
     const int4 mine = a.meta[i];
+    float2 ml[kBatch];
+    float4 v[kBatch];
+    auto request = [&](int k, int p) {
+        ml[k] = *reinterpret_cast<const float2 *>(rec_of(p) + kHeads * D + 2 * hd);
+        v[k] = *reinterpret_cast<const float4 *>(rec_of(p) + hd * D + dim);
+    };
+    request(0, 0);
+    request(1, i + 1 < ctas ? 1 : 0);
     int stop = ctas - 1;  // of the CTAs that this thread looks at, the first to end the segment
     for (int k = i + 1 + tid; k < ctas; k += kThreads) {
         const int2 m = *reinterpret_cast<const int2 *>(a.meta + k);
@@ -681,27 +720,14 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
     if (stop < ctas - 1) atomicMin(&s_last, stop);
     __syncthreads();
     const int np = s_last - i + 1;
-    const int hd = tid * 4 / D, dim = tid * 4 % D;
     if (hd >= G) return;
     float M = kLowest, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < np; p0 += kBatch) {
-        float2 ml[kBatch];
-        float4 v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int p = p0 + k;
-            ml[k] = make_float2(-INFINITY, 0.f);
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p < np) {
-                const float *r = a.recs + (p == 0 ? (size_t)i * 2 + 1 : (size_t)(i + p) * 2) * kRec;
-                ml[k] = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * hd);
-                v[k] = *reinterpret_cast<const float4 *>(r + hd * D + dim);
-            }
-        }
+    auto add = [&](int count) {
         float m = M;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) m = fmaxf(m, ml[k].x);
+        for (int k = 0; k < kBatch; ++k)
+            if (k < count) m = fmaxf(m, ml[k].x);
         const float back = fast_exp2(M - m);
         M = m;
         den *= back;
@@ -711,6 +737,7 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
         num.w *= back;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
+            if (k >= count) continue;
             const float f = fast_exp2(ml[k].x - m);
             den += f * ml[k].y;
             num.x += f * v[k].x;
@@ -718,6 +745,13 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
             num.z += f * v[k].z;
             num.w += f * v[k].w;
         }
+    };
+    add(min(np, 2));
+    for (int p0 = 2; p0 < np; p0 += kBatch) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (p0 + k < np) request(k, p0 + k);
+        add(np - p0);
     }
     const float f = a.v_scale / den;
     *reinterpret_cast<uint2 *>(
