@@ -835,15 +835,16 @@ cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, co
     const long long segs = (long long)num_seqs * g.num_kv_heads;
     const long long tiles = (max_seq_len + (long long)kTokens - 1) / kTokens;
     // A CTA per segment: no scan of the lengths, no second kernel, but a segment has one SM's
-    // rate, 0.105 us a tile, where the split has a share of all SMs and some 4 us more.  Measured
-    // (us, CTA per segment against the split; 8 segments): 8.0 / 9.8 at 1024 tokens, 11.0 / 9.3 at
-    // 2048; 32 segments 8.4 / 8.3, 11.7 / 9.6; 144 segments 14.2 / 17.1 at 2048, 21.0 / 22.7 at
-    // 4096, where it ends: one long sequence among short ones would have the one SM.
-    a.aligned = segs <= sms && tiles <= 128 && tiles * (sms - segs) <= 38LL * sms;
+    // rate, 0.1 us a tile, where the split has a share of all SMs and some 3 us more.  Measured
+    // (us, CTA per segment against the split): 8 segments 7.8 / 8.6 at 768 tokens, 9.2 / 8.6 at
+    // 1152; 32 segments 7.8 / 7.9 at 640, 9.4 / 8.6 at 1152; 72 segments 10.6 / 11.8 at 1536, 12.3 /
+    // 12.3 at 2048; 144 segments 14.5 / 17.2 at 2048, 20.8 / 23.2 at 4096, where it ends: one long
+    // sequence among short ones would have the one SM.
+    a.aligned = segs <= sms && tiles <= 128 && tiles * (sms - segs) <= 30LL * sms;
     // More segments than SMs: whole segments to a CTA, by the prefix sums, spare the second kernel
-    // (1.5 to 2 us) and cost up to half a segment of imbalance.  376 segments of up to 256, 512,
-    // 1024, 2048 tokens: 8.5 / 9.7, 10.6 / 12.4, 14.3 / 14.8, 21.8 / 21.0; 2048 segments 19.4 /
-    // 20.8, 28.1 / 30.2, 41.8 / 41.6, 65.7 / 67.2.
+    // and cost up to half a segment of imbalance.  376 segments of up to 256, 512, 768, 1024
+    // tokens: 8.5 / 9.0, 10.4 / 11.5, 11.9 / 12.1, 15.1 / 15.0; 2048 segments 18.3 / 19.0, 26.8 /
+    // 27.6, 33.6 / 34.6, 38.6 / 38.6.
     a.whole = a.aligned || tiles <= 24;
     const int grid = (int)(a.aligned ? segs : std::min<long long>(sms, std::max(1LL, segs * tiles)));
     if (g.head_size == 128) {
