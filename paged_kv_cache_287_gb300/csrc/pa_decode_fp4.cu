@@ -25,19 +25,20 @@
 // those in several CTAs by a second kernel (a record per CTA and end of its range); few or short
 // segments go to CTAs whole (rules at launch_decode_fp4).
 //
-// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 112 us,
-// 91 % of the copy rate, 32 of up to 131072 tokens 154 us, 95 %; in the steady state 0.66 ns a
+// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 111.5 us,
+// 92 % of the copy rate, 32 of up to 131072 tokens 153 us, 96 %; in the steady state 0.66 ns a
 // tile of the whole GPU, 7.0 TB/s, so what is left are the ends (of 256 sequences: 2.4 us to the
-// first copy, 4 from the first warp's end to the median CTA's last, 2 to the last CTA's, 2 of
-// merges, 1.1 of hand-over, 1.3 the second kernel).  Of 524 warp instructions a
-// tile 302 are the products with their conversions, 39 the softmax, 95 loads, scales and
-// interleaving, the rest copies, waits and bookkeeping.  Each of these brought its part: the
-// tiles' blocks found 16 tiles at a time by all lanes and kept in a table (120, 163 without),
-// the loop unrolled by its stages, so that their addresses are constants (118, 161 without).
-// Tried and slower: a bulk copy per block by one lane, completing on an mbarrier (by 2 %; the
-// copies' uniform operands cost as many instructions, and the loads a fence before the next
-// copy), 12 or 14 warps (by a tenth; the registers allow 16), 8 with four stages each (by a
-// quarter), the last of the CTAs to come merging a segment in place of the second kernel (by 4 %).
+// first copy, 2 from the median CTA's last tile to the last CTA's, 2 of merges, 1.1 of hand-over,
+// 1.3 the second kernel).  Of 524 warp instructions a tile 302 are the products with their
+// conversions, 39 the softmax, 95 loads, scales and interleaving, the rest copies, waits and
+// bookkeeping.  Each of these brought its part: the tiles' blocks found 16 tiles at a time by all
+// lanes and kept in a table (120, 163 without), the loop unrolled by its stages, so that their
+// addresses are constants (118, 161 without).  Tried and slower: 12, 14 or 15 warps (117, 125,
+// 119; the registers allow 16), 12 with three stages each (122); before those steps a bulk copy
+// per block by one lane, completing on an mbarrier (by 2 %; the copies' uniform operands cost as
+// many instructions, and the loads a fence before the next copy), 8 warps with four stages each
+// (by a quarter), the last of the CTAs to come merging a segment in place of the second kernel
+// (by 4 %).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

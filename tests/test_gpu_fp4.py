@@ -490,6 +490,28 @@ def test_decode_of_the_largest_batches():
         b.check(out, seqs=range(0, n, n // 50))
 
 
+@pytest.mark.parametrize("d, bs, n, lens", [
+    (128, 8, 128, [4577, 3001, 4096, 4200]), (128, 16, 128, [4577, 3001, 4096, 4200]),
+    (128, 32, 128, [4577, 3001, 4096, 4200]), (64, 8, 128, [4577, 3001, 4096, 4200]),
+    (64, 32, 128, [4577, 3001, 4096, 4200]), (64, 16, 61, [9001, 40, 8999]),
+    (128, 8, 1300, [577, 449, 500, 33]), (128, 32, 1300, [577, 449, 500, 33]),
+    (64, 8, 5400, [133, 90, 128, 60, 0])])
+def test_decode_of_many_tiles_a_warp(d, bs, n, lens):
+    """Some 50 tiles a warp and more, of few sequences that come again and again."""
+    b = Batch(lens, 32, 8, d, bs, seed=n + d + bs)
+    which = [(i * 7 + i // 5) % len(lens) for i in range(n)]
+    out = torch.full((n, 32, d), math.nan, dtype=torch.bfloat16, device=DEV)
+    binding.pa_decode_fp4(out, b.q[which].to(DEV), b.pool.to(DEV), b.tables[which].to(DEV),
+                          ints([lens[i] for i in which]), max(lens), b.scale, *SCALES,
+                          b.workspace(0xff))
+    binding.pa_error_check()
+    got, which = np64(out), np.array(which)
+    for s in range(len(lens)):
+        want, tol = _fp4.attend(np64(b.q[s]), *b.rows(s), b.scale, lens[s])
+        off = np.abs(got[which == s] - want)
+        assert (off <= tol).all(), (s, off.max(), (off / tol).max())
+
+
 def test_decode_where_every_boundary_falls():
     """Segments of every number of tiles, so that ranges begin and end anywhere in them."""
     for n, hkv, length in ((20, 8, 97), (8, 20, 1000), (160, 1, 65), (3, 60, 321), (152, 1, 33),
