@@ -18,7 +18,8 @@
 // is synchronised); 151 instructions a group of query heads with a norm, 96 without.
 //
 // 4344 tokens of 32 + 2 x 8 heads of 128, bf16 pool, in a graph over three states: 18.9 us with
-// one axis (5.7 TB/s moved, 85 % of the copy rate; norms make no difference), 20.7 with three;
+// one axis (5.7 TB/s moved, 85 % of the copy rate; norms make no difference), 20.1 with three
+// (a lane holds an axis' position, asked for before the axes are known: 20.7 without);
 // FP8 pool 18.5, 4-bit 21.1 (64 bytes of codes and 8 of scales a head scatter more).  When the
 // ring came (three axes): 21.7; with the rows loaded to registers two groups at a time 28.8,
 // rings of 4, 5, 8 groups 22.1, 22.3, 27.8 (fewer blocks fit), a token shared by two warps 25.3,
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
         }
         copies_commit();
     };
-    int slot = -1, pos[8], axis[8];
+    int slot = -1, pos[8], axis[8], own = 0;  // own: the position of axis `lane`
     if (!idle) {
 #pragma unroll
         for (int k = 0; k < kRing; ++k) fetch(min(chunk + k * a.chunks, groups), k);
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 axis[i] = turns[i / 4] ? a.pair_axis[pair[i / 4] + i % 4] : 0;
+            if (lane < a.num_axes) own = a.positions[(int64_t)lane * a.num_tokens + tok];
         } else {
             pos[0] = a.positions[tok];
         }
@@ -158,8 +160,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qkv_rope_kernel(const QkvRop
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i % 4 && one[i / 4]) continue;
-            pos[i] = a.positions[(int64_t)axis[i] * a.num_tokens + tok];
+            pos[i] = __shfl_sync(0xffffffffu, own, axis[i]);
             bad = bad || (turns[i / 4] && (pos[i] < 0 || pos[i] >= a.max_position));
         }
     } else {
