@@ -49,14 +49,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kWrite>) rows_kernel(const Ro
     const int width = min(cols, kThreads), at_once = kThreads / width;  // tokens of a block's pass
     const int first = threadIdx.x / width;
     if (first >= at_once) return;
-    const int bs = 1 << a.block_shift, step = gridDim.x * at_once;
+    const int bs = 1 << a.block_shift;
+    const unsigned step = gridDim.x * at_once, tokens = a.num_tokens;  // (sums pass 2^31)
     for (int col = threadIdx.x - first * width; col < cols; col += width) {
         const int side = col >= per_side, c = col - side * per_side;
         const int head = c / kGroups, grp = c % kGroups;
         const Fp4Scale scale_of = side ? a.vs : a.ks;
         const float g = scale_of.g;
         uint8_t *rows = (side ? a.v : a.k) + c * 32;
-        for (int tok = blockIdx.x * at_once + first; tok < a.num_tokens; tok += kTok * step) {
+        for (unsigned tok = blockIdx.x * at_once + first; tok < tokens; tok += kTok * step) {
             uint32_t x[kTok][8];
             uint2 codes[kTok];
             uint32_t scale[kTok];
@@ -64,10 +65,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kWrite>) rows_kernel(const Ro
             Fp4Row row[kTok];
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
-                // (a sum past the last token may wrap: compared as unsigned)
-                const unsigned t = (unsigned)tok + (unsigned)k * (unsigned)step;
-                slot[k] = t < (unsigned)a.num_tokens ? a.slots[t] : -1;
-                if (kWrite && t < (unsigned)a.num_tokens) {  // a skipped row's is there as well
+                const unsigned t = tok + k * step;
+                slot[k] = t < tokens ? a.slots[t] : -1;
+                if (kWrite && t < tokens) {  // a skipped row's is there as well
                     const uint8_t *p = rows + (int64_t)t * a.row_bytes;
                     if (a.wide) {
                         ld_32(x[k], p);
