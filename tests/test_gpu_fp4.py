@@ -421,6 +421,15 @@ def test_decode_bad_tables_and_lengths_are_flagged():
         assert torch.equal(out[1], good[1]) if bad > 0 else (out[1] == 0).all()
 
 
+def test_decode_of_the_most_heads():
+    """255 KV heads of 8 query heads, whole segments to a CTA and split."""
+    for lens in ([40, 0, 200], [900, 33, 1]):
+        b = Batch(lens, 2040, 255, 64, 16, seed=sum(lens))
+        out = b.run()
+        binding.pa_error_check()
+        b.check(out)
+
+
 def test_decode_sharing_blocks():
     b = Batch([200, 210, 220, 64], 8, 2, 128, 16, seed=12, shared=3)
     b.check(b.run())
@@ -634,6 +643,17 @@ def test_rope_into_quantised_pools_is_the_write_of_its_bf16_rows(case, bits):
     write(want, k, v, t.slots.to(DEV), *SCALES)
     assert torch.equal(pool, want)
     binding.pa_error_check()
+
+
+def test_rope_of_the_most_heads():
+    t = Turn(2, 2040, 255, 64, 16, 32, axes=8, seed=6)
+    q, pool = t.run()
+    binding.pa_error_check()
+    wq, wk, sq, sk = t.want()
+    close(q, wq, sq)
+    b, o = t.slots.long() // 16, t.slots.long() % 16
+    close(pool.cpu()[b, 0, :, o], wk, sk)
+    assert torch.equal(pool.cpu()[b, 1, :, o], t.v())
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
