@@ -193,10 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             if (lane == 31) sums[warp] = v;
             __syncthreads();
             // The sums of the warps before this one, lane w holding warp w's.
-            int run = lane < warp ? sums[lane] : 0;
-#pragma unroll
-            for (int o = 1; o < kWarps; o <<= 1) run += __shfl_xor_sync(0xffffffffu, run, o);
-            run = __shfl_sync(0xffffffffu, run, 0) + v - sum;
+            int run = __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0) + v - sum;
             for (int i = tid * per; i < min(B, (tid + 1) * per); ++i) {
                 const int n = pre[i];
                 pre[i] = run;
@@ -227,16 +224,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         const int each = n / kWarps, rest = n % kWarps;
         t0 = r0 + warp * each + min(warp, rest);
         t1 = t0 + each + (warp < rest);
-    }
-
-    // Rows of sequences without tokens.
-    for (int s = a.aligned ? blockIdx.x / Hkv : blockIdx.x; s < B;
-         s += a.aligned ? B : gridDim.x) {
-        if (a.aligned ? active > 0 : pre[s + 1] != pre[s]) continue;
-        const int rows = a.aligned ? G : a.num_heads;
-        uint4 *dst = reinterpret_cast<uint4 *>(
-            a.out + ((size_t)s * a.num_heads + (a.aligned ? blockIdx.x % Hkv * G : 0)) * D);
-        for (int i = tid; i < rows * (D / 8); i += kWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
     }
 
     // Tile i of this warp has entry i % 32 of a table: its segment (sequence << 8 | head), its
@@ -324,6 +311,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
     };
 #pragma unroll
     for (int i = 0; i < S; ++i) issue(i, i);
+
+    // Rows of sequences without tokens (while the first tiles are on their way).
+    for (int s = a.aligned ? blockIdx.x / Hkv : blockIdx.x; s < B;
+         s += a.aligned ? B : gridDim.x) {
+        if (a.aligned ? active > 0 : pre[s + 1] != pre[s]) continue;
+        const int rows = a.aligned ? G : a.num_heads;
+        uint4 *dst = reinterpret_cast<uint4 *>(
+            a.out + ((size_t)s * a.num_heads + (a.aligned ? blockIdx.x % Hkv * G : 0)) * D);
+        for (int i = tid; i < rows * (D / 8); i += kWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
+    }
 
     float acc[D / 16][4];
     uint32_t qf[D / 16][2];
