@@ -27,7 +27,7 @@
 //
 // Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 111.5 us,
 // 92 % of the copy rate, 32 of up to 131072 tokens 153 us, 96 %; in the steady state 0.66 ns a
-// tile of the whole GPU, 7.0 TB/s, so what is left are the ends (of 256 sequences: 2.4 us to the
+// tile of the whole GPU, 7.0 TB/s, so what is left are the ends (of 256 sequences: 2.1 us to the
 // first copy, 2 from the median CTA's last tile to the last CTA's, 2 of merges, 1.1 of hand-over,
 // 1.3 the second kernel).  Of 524 warp instructions a tile 302 are the products with their
 // conversions, 39 the softmax, 95 loads, scales and interleaving, the rest copies, waits and
