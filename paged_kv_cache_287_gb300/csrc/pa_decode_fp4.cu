@@ -108,13 +108,15 @@ template <int BS>
 constexpr int kEntryInts = BS == 8 ? 6 : 4;
 
 // 16 (D 128) or 8 consecutive dims of one head: acc[mt][e] and acc[mt][e + 2] are dims 2 mt and
-// 2 mt + 1 of them.
+// 2 mt + 1 of them.  V's scale after the division by l: their quotient may be no normal number.
 template <int D>
 __device__ __forceinline__ void store_rows(__nv_bfloat16 *dst, const float (&acc)[D / 16][4],
-                                           int e, float f) {
+                                           int e, float l, float v_scale) {
+    const float inv = 1.f / l;
     uint32_t w[D / 16];
 #pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt) w[mt] = pack_bf16(acc[mt][e] * f, acc[mt][e + 2] * f);
+    for (int mt = 0; mt < D / 16; ++mt)
+        w[mt] = pack_bf16(acc[mt][e] * inv * v_scale, acc[mt][e + 2] * inv * v_scale);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i)
         reinterpret_cast<uint4 *>(dst)[i] =
@@ -560,8 +562,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 __nv_bfloat16 *row =
                     a.out + ((size_t)(seg >> 8) * a.num_heads + (seg & 255) * G + 2 * c) * D +
                     g * (D / 8);
-                if (2 * c < G) store_rows<D>(row, acc, 0, a.v_scale / l0);
-                if (2 * c + 1 < G) store_rows<D>(row + D, acc, 1, a.v_scale / l1);
+                if (2 * c < G) store_rows<D>(row, acc, 0, l0, a.v_scale);
+                if (2 * c + 1 < G) store_rows<D>(row + D, acc, 1, l1, a.v_scale);
             } else if (inside) {
                 store_rec<D>(recs + warp * kRec, acc, lane, -nm0 * cs0, l0, -nm1 * cs1, l1);
                 if (lane == 0) {
@@ -655,13 +657,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
         for (int u = 0; u < kTogether; ++u) {
             const int at = hd + u * next;
             if (!head && ends) {
-                const float inv = a.v_scale / den[u];
+                const float inv = 1.f / den[u];
                 uint32_t *row = reinterpret_cast<uint32_t *>(
                     a.out + ((size_t)(sg >> 8) * a.num_heads + (sg & 255) * G + at) * D +
                     lane * E);
 #pragma unroll
                 for (int j = 0; j < E; j += 2)
-                    row[j / 2] = pack_bf16(num[u][j] * inv, num[u][j + 1] * inv);
+                    row[j / 2] = pack_bf16(num[u][j] * inv * a.v_scale,
+                                           num[u][j + 1] * inv * a.v_scale);
             } else {
                 float *r = a.recs + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * kRec;
                 Dims v;
@@ -751,10 +754,11 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
             if (p0 + k < np) request(k, p0 + k);
         add(np - p0);
     }
-    const float f = a.v_scale / den;
+    const float f = 1.f / den;
     *reinterpret_cast<uint2 *>(
         a.out + ((size_t)(mine.w >> 8) * a.num_heads + (mine.w & 255) * G + hd) * D + dim) =
-        make_uint2(pack_bf16(num.x * f, num.y * f), pack_bf16(num.z * f, num.w * f));
+        make_uint2(pack_bf16(num.x * f * a.v_scale, num.y * f * a.v_scale),
+                   pack_bf16(num.z * f * a.v_scale, num.w * f * a.v_scale));
 }
 
 template <int D, int BS>
