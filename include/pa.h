@@ -673,8 +673,9 @@ pa_status pa_cache_read_fp4(const pa_cache_fp4_args *args);
 /*
  * pa_decode_fp4 - pa_decode over a 4-bit pool (head_size 64 or 128).  Codes times scales are
  * f16 numbers exactly; each query head is scaled by a power of two into f16 range (exact for
- * elements down to 2^-14 of the head's largest), P is rounded to f16; products accumulate in
- * fp32, softmax statistics are fp32.  The result is the same bits on every call.
+ * elements down to 2^-14 of the head's largest), P is rounded to f16 (2^-11 of a weight down to
+ * 2^-25 of the largest, 2^-36 of the largest below that); products accumulate in fp32, softmax
+ * statistics are fp32.  The result is the same bits on every call.
  *   seq_lens      a length below 0 or above max_seq_len is taken as the nearest of the two and
  *                 flagged PA_ERR_OOB; 0 yields zero rows
  *   workspace     >= pa_decode_fp4_workspace_bytes(...) bytes, 256-byte aligned, no

@@ -55,9 +55,12 @@ std::atomic<bool> g_launched{false};
 constexpr int kTokens = 32;  // of a tile
 constexpr int kWarps = 16;   // one CTA per SM
 constexpr int kHeads = 8;    // query heads per KV head, padded to the MMA's N
-// m is only raised when a score exceeds it by more than this (log2 units): P stays below 2^8.
-// It is kept in the scores' own units, so that the difference is taken before any scaling.
-constexpr float kSlack = 8.f;
+// m lies kLift powers of two below a running maximum, and is only raised when a score exceeds that
+// by more than kSlack: P reaches 2^15 (f16 ends at 2^16), and the weights of a tail keep f16's 11
+// bits down to 2^-25 of the largest and are lost below 2^-36.  (With m at the maximum itself a tail
+// of 2^-25 was in l, which is summed in fp32, but not in the product.)  m is kept in the scores' own
+// units, so that the difference is taken before any scaling.
+constexpr float kLift = 11.f, kSlack = 4.f;
 constexpr float kLowest = -3.4028235e38f;  // m before the first score
 
 template <int D>
@@ -99,6 +102,14 @@ __device__ __forceinline__ int sequence_of(const int *pre, int num_seqs, int num
         if (num_kv_heads * pre[mid] <= x) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// The score above which the reference -nm is raised, of a factor cs to log2 units.  It is rounded
+// down and the reference up, so that no P passes 2^15 where scores are so large that their own steps
+// come to several powers of two.  (The quotients may be off by their last bits; a cs above 2^126
+// makes them 0, less than a step of any score.)
+__device__ __forceinline__ float raised_above(float nm, float cs) {
+    return __fsub_rd(__fdividef(kLift + kSlack, cs), nm);
 }
 
 // Flags of a tile beside its tokens: the last, the first of its segment.
@@ -389,8 +400,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
             nm0 = nm1 = -kLowest;
-            bar0 = kSlack / cs0 - nm0;
-            bar1 = kSlack / cs1 - nm1;
+            bar0 = raised_above(nm0, cs0);
+            bar1 = raised_above(nm1, cs1);
             l0 = l1 = 0.f;
         }
 
@@ -467,12 +478,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 t0x = fmaxf(t0x, __shfl_xor_sync(0xffffffffu, t0x, o));
                 t1x = fmaxf(t1x, __shfl_xor_sync(0xffffffffu, t1x, o));
             }
-            const float n0 = fminf(nm0, -t0x), n1 = fminf(nm1, -t1x);
+            const float n0 = fminf(nm0, __fsub_rd(__fdividef(kLift, cs0), t0x));
+            const float n1 = fminf(nm1, __fsub_rd(__fdividef(kLift, cs1), t1x));
             const float r0 = fast_exp2((n0 - nm0) * cs0), r1 = fast_exp2((n1 - nm1) * cs1);
             nm0 = n0;
             nm1 = n1;
-            bar0 = kSlack / cs0 - nm0;
-            bar1 = kSlack / cs1 - nm1;
+            bar0 = raised_above(nm0, cs0);
+            bar1 = raised_above(nm1, cs1);
             l0 *= r0;
             l1 *= r1;
 #pragma unroll

@@ -43,3 +43,110 @@ def test_v_scales_next_to_the_smallest(shape, v_scale):
     out = b.run(scales=scales)
     assert (np64(out) > 100 * v_scale).all()
     b.check(out, scales=scales, seqs=range(0, len(b.lens), 37))
+
+
+def tail_bound(p, v, out, n):
+    """How far a kernel's row may be off whose scores are exact: the output's rounding to bf16
+    (2^-8); P's rounding to f16, 2^-11 of a weight, or half a step of f16's smallest numbers,
+    2^-25, where the largest weight is 2^11 or more; n tokens' sums, each of n / 8 (the weights
+    of a lane) and n / 16 (a product's) additions rounded by 2^-24 and 2^-23 at most; 2^-17 for the
+    exponential, its argument (up to 32, four roundings of 2^-24) and the merges."""
+    mass = p @ np.abs(v)
+    return (2.0 ** -8 * np.abs(out) + (2.0 ** -11 + n * 2.0 ** -26 + 2.0 ** -17) * mass
+            + 2.0 ** -36 * p.max() * np.abs(v).sum(0) + 2.0 ** -133)
+
+
+def peaked(shape, peak, level):
+    """One key `level` powers of two above the others, whose V alone is not zero (and positive):
+    the output is what the tail brings."""
+    b = Batch(*shape, seed=5)
+    codes, sc = parts(b)
+    codes[:, :, 0], sc[:, :, 0] = 0, 0x38
+    codes[:, :, 1] &= 0x77
+    for s, n in enumerate(b.lens):
+        at = peak % n
+        blk, o = int(b.tables[s, at // b.bs]), at % b.bs
+        codes[blk, :, 0, o], codes[blk, :, 1, o] = 0x77, 0
+    b.q.fill_(1.0)
+    return b, level * math.log(2.0) / (6 * b.d)
+
+
+@SHAPES
+@pytest.mark.parametrize("peak", [0, 77, -1])
+@pytest.mark.parametrize("level", [12.3, 25.1, 27.6, 31.0])
+def test_weights_far_below_the_largest(shape, peak, level):
+    b, scale = peaked(shape, peak, level)
+    scales = (1.0, 0.37)
+    out = np64(b.run(scales=scales, scale=scale))
+    binding.pa_error_check()
+    for s in range(0, len(b.lens), 103):
+        k, v = b.rows(s, scales)
+        x = k[:, 0].sum(-1) * scale
+        p = np.exp(x - x.max())
+        p /= p.sum()
+        for h in range(b.hq):
+            vh = v[:, h * b.hkv // b.hq]
+            want = p @ vh
+            assert want.max() > 0
+            off = np.abs(out[s, h] - want)
+            assert (off <= tail_bound(p, vh, want, b.lens[s])).all(), (s, h, (off / want).max())
+
+
+@pytest.mark.parametrize("level, near", [(25.1, False), (25.1, True), (0.0, True)])
+def test_a_long_tail_in_one_warp(level, near):
+    """131072 tokens to each warp of the GPU (the sequences share their blocks), one key far above
+    the others, its V zero or beside theirs; and no key above the others."""
+    n, hkv, d, bs = 131072, 8, 64, 32
+    b, scale = peaked(([n], hkv, hkv, d, bs), 1000, level)
+    codes, _ = parts(b)
+    if near:
+        blk, o = int(b.tables[0, 1000 // bs]), 1000 % bs
+        codes[blk, :, 1, o] = 0x21
+    warps = 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    count = -(-warps // hkv)
+    q = torch.ones(count, hkv, d, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    ws = torch.empty(binding.pa_decode_fp4_workspace_bytes(count, hkv, hkv, d),
+                     dtype=torch.uint8, device=DEV)
+    tables = b.tables.to(DEV).expand(count, -1).contiguous()
+    binding.pa_decode_fp4(out, q, b.pool.to(DEV), tables, ints([n] * count), n, scale, 1.0, 0.37,
+                          ws)
+    binding.pa_error_check()
+    k, v = b.rows(0, (1.0, 0.37))
+    x = k[:, 0].sum(-1) * scale
+    p = np.exp(x - x.max())
+    p /= p.sum()
+    got = np64(out)
+    for h in range(hkv):
+        want = p @ v[:, h]
+        off = np.abs(got[:, h] - want)
+        assert (off <= tail_bound(p, v[:, h], want, n)).all(), (h, (off / want).max())
+
+
+def test_a_long_context_of_any_numbers():
+    b = Batch([131072, 5], 4, 1, 128, 16, seed=6, q_mult=2.0)
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("odd", [0, 1])
+def test_no_weight_leaves_f16_where_scores_step_far(odd):
+    """Scores so large that their own steps are `u` powers of two of weight: whatever the steps
+    above the reference, the weights stay finite and the output between the values."""
+    b = Batch(*WARP, seed=7)
+    codes, sc = parts(b)
+    codes[:, :, 0], sc[:, :, 0, :, 1:] = 0x77, 0x7e
+    codes[:, :, 0, :, :8], sc[:, :, 0, :, :1] = 0, 0x08  # the first 16: steps of 2^-7
+    for s, n in enumerate(b.lens):
+        for blk, first in zip(b.tables[s].tolist(), range(0, n, b.bs)):
+            step = odd + min(first // 96, 4)
+            codes[blk, :, 0, :, 0] = step
+    codes[:, :, 1] &= 0x77
+    b.q.fill_(1.0)
+    seqs = range(0, len(b.lens), 103)
+    most = {s: np.abs(b.rows(s, (1.0, 1.0))[1]).max(0) for s in seqs}
+    for u in (1.0, 2.0, 4.0, 7.5, 8.0, 12.0, 14.9, 15.0, 15.9, 15.9999, 16.0, 16.1, 24.0, 32.0, 64.0):
+        out = np64(b.run(scales=(1.0, 1.0), scale=u * 128 * math.log(2.0)))
+        for s in seqs:
+            top = most[s].repeat(b.hq // b.hkv, 0)
+            assert np.isfinite(out[s]).all(), (u, s)
+            assert (out[s] >= 0).all() and (out[s] <= top * (1 + 2.0 ** -7)).all(), (u, s)
