@@ -62,6 +62,10 @@ constexpr int kHeads = 8;    // query heads per KV head, padded to the MMA's N
 // units, so that the difference is taken before any scaling.
 constexpr float kLift = 11.f, kSlack = 4.f;
 constexpr float kLowest = -3.4028235e38f;  // m before the first score
+// A record's m is in log2 units times this: a score is below 2^21 units of its own and their factor
+// below 2^128, so that their product may be beyond binary32 and the differences that count not.
+// That factor is at least kLeast, with which every weight is the same.
+constexpr float kRecUnit = 0x1p-40f, kPerRecUnit = 0x1p40f, kLeast = 0x1p-80f;
 
 template <int D>
 constexpr int kStageBytes = kTokens *D * 9 / 8;
@@ -390,11 +394,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             const int e0 = __shfl_sync(0xffffffffu, ex, 8 * c);
             const int e1 = __shfl_sync(0xffffffffu, ex, 8 * c + 4);
-            // Positive and finite, so that -inf stays -inf; at their least every score is 0.
+            // Positive and finite, so that -inf stays -inf.
             cs0 = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e0) << 23);
             cs1 = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e1) << 23);
-            cs0 = fminf(fmaxf(cs0, 1.1754944e-38f), -kLowest);
-            cs1 = fminf(fmaxf(cs1, 1.1754944e-38f), -kLowest);
+            cs0 = fminf(fmaxf(cs0, kLeast), -kLowest);
+            cs1 = fminf(fmaxf(cs1, kLeast), -kLowest);
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
@@ -577,13 +581,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 if (2 * c < G) store_rows<D>(row, acc, 0, l0, a.v_scale);
                 if (2 * c + 1 < G) store_rows<D>(row + D, acc, 1, l1, a.v_scale);
             } else if (inside) {
-                store_rec<D>(recs + warp * kRec, acc, lane, -nm0 * cs0, l0, -nm1 * cs1, l1);
+                store_rec<D>(recs + warp * kRec, acc, lane, -nm0 * (cs0 * kRecUnit), l0,
+                             -nm1 * (cs1 * kRecUnit), l1);
                 if (lane == 0) {
                     pieces[warp].a = 1;
                     pieces[warp].a_ends = last;
                 }
             } else {  // the range's last tile: the ring is empty
-                store_rec<D>(reinterpret_cast<float *>(stages), acc, lane, -nm0 * cs0, l0, -nm1 * cs1, l1);
+                store_rec<D>(reinterpret_cast<float *>(stages), acc, lane, -nm0 * (cs0 * kRecUnit),
+                             l0, -nm1 * (cs1 * kRecUnit), l1);
                 if (lane == 0) {
                     pieces[warp].b = 1;
                     pieces[warp].b_seg = seg;
@@ -658,7 +664,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
                 const int at = hd + u * next;
                 const float2 ml = *reinterpret_cast<const float2 *>(r + kHeads * D + 2 * at);
                 const Dims v = *reinterpret_cast<const Dims *>(r + at * D + lane * E);
-                const float f = fast_exp2(ml.x - M[u]);
+                const float f = fast_exp2((ml.x - M[u]) * kPerRecUnit);
                 den[u] += f * ml.y;
 #pragma unroll
                 for (int j = 0; j < E; ++j) num[u][j] += f * reinterpret_cast<const float *>(&v)[j];
@@ -741,7 +747,7 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (k < count) m = fmaxf(m, ml[k].x);
-        const float back = fast_exp2(M - m);
+        const float back = fast_exp2((M - m) * kPerRecUnit);
         M = m;
         den *= back;
         num.x *= back;
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kHeads * D / 4) decode_fp4_merge_kernel(const 
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             if (k >= count) continue;
-            const float f = fast_exp2(ml[k].x - m);
+            const float f = fast_exp2((ml[k].x - m) * kPerRecUnit);
             den += f * ml[k].y;
             num.x += f * v[k].x;
             num.y += f * v[k].y;

@@ -150,3 +150,32 @@ def test_no_weight_leaves_f16_where_scores_step_far(odd):
             top = most[s].repeat(b.hq // b.hkv, 0)
             assert np.isfinite(out[s]).all(), (u, s)
             assert (out[s] >= 0).all() and (out[s] <= top * (1 + 2.0 ** -7)).all(), (u, s)
+
+
+@SHAPES
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_beyond_binary32(shape, sign):
+    """The factor of a score is finite, the scores times it are not: the largest key takes all,
+    whichever pieces its segment is merged from; also where every score is negative."""
+    b = Batch(*shape, seed=11)
+    b.q[:] = b.q[:, :1].abs() * 1e6
+    codes, _ = parts(b)
+    codes[:, :, 0] &= 0x77
+    if sign < 0:
+        codes[:, :, 0] |= 0x88
+    out = np64(b.run(scales=(1.0, 0.37), scale=2e31))
+    binding.pa_error_check()
+    checked = 0
+    for s in range(0, len(b.lens), 53):
+        k, v = b.rows(s, (1.0, 0.37))
+        for h in range(b.hq):
+            kv = h * b.hkv // b.hq
+            x = k[:, kv] @ np64(b.q[s])[h]
+            top = np.sort(np.abs(x))
+            top = top[:2] if sign < 0 else top[::-1][:2]
+            if abs(top[0] - top[1]) < 1e-4 * top[1]:  # nearer than the fp32 sums tell apart
+                continue
+            want = v[x.argmax(), kv]
+            assert (np.abs(out[s, h] - want) <= 2.0 ** -8 * np.abs(want)).all(), (s, h)
+            checked += 1
+    assert checked
