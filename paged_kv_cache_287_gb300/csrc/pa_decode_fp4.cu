@@ -41,6 +41,7 @@
 // (by 4 %).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "pa_fp4.cuh"
@@ -85,7 +86,8 @@ struct Args {
     int num_seqs, num_heads, num_kv_heads, group, max_blocks, num_blocks, max_seq_len;
     int aligned;  // CTA c is segment c
     int whole;    // every CTA takes whole segments: no piece leaves it
-    float scale_log2, v_scale;  // scale * log2(e) * k_scale
+    float factor, v_scale;  // factor * 2^factor_exp: scale * log2(e) * k_scale
+    int factor_exp;
 };
 
 // What a warp leaves for the merge in its CTA: a piece of a segment that began before its range
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             int ex = mx > 0.f ? (int)(__float_as_uint(mx) >> 23) - 127 : 0;
             ex = max(-126, min(126, ex));
             float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-            if (a.scale_log2 < 0.f) down = -down;
+            if (a.factor < 0.f) down = -down;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 qf[k][0] = pack_f16(qv[4 * k] * down, qv[4 * k + 1] * down);
@@ -394,9 +396,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_fp4_kernel(const Args a
             }
             const int e0 = __shfl_sync(0xffffffffu, ex, 8 * c);
             const int e1 = __shfl_sync(0xffffffffu, ex, 8 * c + 4);
-            // Positive and finite, so that -inf stays -inf.
-            cs0 = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e0) << 23);
-            cs1 = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 + e1) << 23);
+            // The factor's exponent meets the query's before anything is rounded.  Positive and
+            // finite, so that -inf stays -inf.
+            const int f0 = max(-126, min(127, a.factor_exp + e0));
+            const int f1 = max(-126, min(127, a.factor_exp + e1));
+            cs0 = fabsf(a.factor) * __uint_as_float((uint32_t)(127 + f0) << 23);
+            cs1 = fabsf(a.factor) * __uint_as_float((uint32_t)(127 + f1) << 23);
             cs0 = fminf(fmaxf(cs0, kLeast), -kLowest);
             cs1 = fminf(fmaxf(cs1, kLeast), -kLowest);
 #pragma unroll
@@ -850,7 +855,7 @@ cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, co
     a.max_blocks = max_blocks_per_seq;
     a.num_blocks = g.num_blocks;
     a.max_seq_len = max_seq_len;
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634 * k_scale);
+    a.factor = (float)std::frexp((double)scale * 1.4426950408889634 * k_scale, &a.factor_exp);
     a.v_scale = v_scale;
     const long long segs = (long long)num_seqs * g.num_kv_heads;
     const long long tiles = (max_seq_len + (long long)kTokens - 1) / kTokens;

@@ -179,3 +179,31 @@ def test_scores_beyond_binary32(shape, sign):
             assert (np.abs(out[s, h] - want) <= 2.0 ** -8 * np.abs(want)).all(), (s, h)
             checked += 1
     assert checked
+
+
+@SHAPES
+def test_a_small_factor_of_large_queries(shape):
+    """scale * k_scale below binary32's normal numbers, the scores not."""
+    b = Batch(*shape, seed=12)
+    codes, sc = parts(b)
+    codes[:] = codes[:, :, :1, :, :1] & 0x0f  # a row's elements are alike, K's and V's too
+    codes |= codes << 4
+    sc.clamp_(min=0x7e)
+    b.q.fill_(2.0 ** 126)
+    scales, scale = (1.34375 * 2.0 ** -73, 0.37), 1.3125 * 2.0 ** -73  # 20.4 steps of the smallest
+    b.check(b.run(scales=scales, scale=scale), scales=scales, scale=scale,
+            seqs=range(0, len(b.lens), 37))
+
+
+@SHAPES
+def test_a_large_factor_of_small_queries(shape):
+    """scale * k_scale beyond binary32, the scores around one: queries of 2^-126 on keys of a
+    single element of the smallest code and scale."""
+    b = Batch(*shape, seed=13)
+    codes, sc = parts(b)
+    codes[:, :, 0, :, 1:], sc[:, :, 0] = 0, 0x01
+    codes[:, :, 0, :, 0] &= 0x09  # element 0: 0, 0.5 and their negatives
+    b.q.fill_(2.0 ** -126)
+    scales, scale = (2.0 ** 30 / 3, 0.37), 2.0 ** 106 * 1.1
+    b.check(b.run(scales=scales, scale=scale), scales=scales, scale=scale,
+            seqs=range(0, len(b.lens), 37))
