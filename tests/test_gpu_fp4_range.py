@@ -207,3 +207,45 @@ def test_a_large_factor_of_small_queries(shape):
     scales, scale = (2.0 ** 30 / 3, 0.37), 2.0 ** 106 * 1.1
     b.check(b.run(scales=scales, scale=scale), scales=scales, scale=scale,
             seqs=range(0, len(b.lens), 37))
+
+
+def test_every_attention_over_a_context_read_back_is_the_formula():
+    """pa_decode and pa_prefill_chunk over the rows read back, pa_decode_fp4 over the pool itself:
+    each against the formula over the numbers that it reads.  The bf16 kernels' P is rounded to
+    bf16, 2^-8 of a weight."""
+    gen = torch.Generator().manual_seed(23)
+    n, hq, hkv, d, bs, nb = 333, 8, 2, 128, 16, 30
+    sc = (0.0017, 0.0021)
+    k, v = bf16((n, hkv, d), gen), bf16((n, hkv, d), gen)
+    perm = torch.randperm(nb, generator=gen)[:21]
+    slots = (perm[:, None] * bs + torch.arange(bs)).reshape(-1)[:n]
+    pool = torch.zeros(binding.fp4_pool_shape(nb, hkv, bs, d), dtype=torch.uint8, device=DEV)
+    binding.pa_cache_write_fp4(pool, k.to(DEV), v.to(DEV), ints(slots), *sc)
+    kb, vb = (torch.empty(n, hkv, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    binding.pa_cache_read_fp4(kb, vb, pool, ints(slots), *sc)
+    wide = torch.zeros(nb, 2, hkv, bs, d, dtype=torch.bfloat16, device=DEV)
+    binding.pa_cache_write(wide, kb, vb, ints(slots))
+    tables, lens = ints(perm)[None].contiguous(), ints([n])
+    q = bf16((1, hq, d), gen, 2.0).to(DEV)
+    out4, out16, chunk = (torch.empty_like(q) for _ in range(3))
+    ws = torch.empty(max(binding.pa_decode_fp4_workspace_bytes(1, hq, hkv, d),
+                         binding.pa_decode_workspace_bytes(1, hq, hkv, d)), dtype=torch.uint8,
+                     device=DEV)
+    scale = d ** -0.5
+    binding.pa_decode_fp4(out4, q, pool, tables, lens, n, scale, *sc, ws)
+    binding.pa_decode(out16, q, wide, tables, lens, n, scale, ws)
+    binding.pa_prefill_chunk(chunk, q, ints([0, 1]), 1, wide, tables, lens, scale)
+    binding.pa_error_check()
+    q = np64(q[0])
+    want, tol = _fp4.attend(q, *_fp4.read_rows(pool.cpu().numpy(), slots, bs, d, sc), scale, n)
+    assert (np.abs(np64(out4[0]) - want) <= tol).all()
+    assert tol.max() < np.abs(want).max() / 20
+    k64, v64 = np64(kb), np64(vb)
+    want, tol = _fp4.attend(q, k64, v64, scale, n)
+    for h in range(hq):
+        x = k64[:, h * hkv // hq] @ q[h] * scale
+        p = np.exp(x - x.max())
+        tol[h] += 2.0 ** -8 * (p / p.sum()) @ np.abs(v64[:, h * hkv // hq])
+    assert tol.max() < np.abs(want).max() / 20
+    for out in (out16, chunk):
+        assert (np.abs(np64(out[0]) - want) <= tol).all()
