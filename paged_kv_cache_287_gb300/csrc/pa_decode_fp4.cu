@@ -834,6 +834,26 @@ int decode_fp4_max_seqs(int head_size, int block_size) {
     return head_size == 128 ? max_seqs<128>(block_size) : max_seqs<64>(block_size);
 }
 
+// Whether every segment (of up to `tiles` tiles) gets a CTA of its own: no scan of the lengths, no
+// second kernel, but a segment has one SM's rate, 0.1 us a tile (0.06 at head size 64), where the
+// split has a share of all SMs, costs some 2 us and grows with the tiles of all segments.  Equal where
+// tiles * (5/8 SMs - segments) = slope * SMs; up to 8 segments later, as the second kernel is slow
+// over many pieces.  Nowhere above 4096 tokens: one long sequence among short ones would have the one
+// SM.  Measured (us, CTA per segment / split, by segments and tokens; the border lies between):
+//   head size 128:  2: 1280 9.3/9.1, 1536 10.2/10.1   4: 1280 9.3/9.8, 1792 10.9/10.9
+//     8: 1024 8.7/9.1, 1152 9.1/8.6   16: 768 8.0/8.1, 896 8.3/7.9   32: 768 8.0/8.1, 896 8.4/8.3
+//     48: 1024 9.0/9.0, 1152 9.5/9.4   72: 2048 12.5/13.8, 4096 19.1/17.4   144: 4096 20.7/23.4
+//   head size 64:  1: 2560 9.6/11.9, 4096 12.6/15.2   4: 2048 8.5/9.7, 2560 9.5/8.9
+//     8: 1536 7.6/7.9, 1792 8.1/7.6   16: 1152 7.1/7.0, 1280 7.3/6.9   32: 1280 7.3/7.6, 1536 7.8/7.8
+//     48: 2048 8.9/9.2, 2560 9.9/9.4   72: 2560 9.9/10.4, 4096 13.5/13.2   144: 4096 14.9/17.7
+static bool cta_per_segment(long long segs, long long tiles, int sms, int head_size) {
+    const bool wide = head_size == 128;
+    if (segs > sms || tiles > 128) return false;
+    if (segs <= 4) return tiles <= (wide ? 44 : 144 - 18 * segs);
+    if (segs <= 8) return tiles <= (wide ? 33 : 50);
+    return tiles <= 24 || tiles * (5 * sms - 8 * segs) <= 8LL * (wide ? 11 : 19) * sms;
+}
+
 cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, const KvGeom &g,
                               int num_heads, const int32_t *block_tables, int max_blocks_per_seq,
                               const int32_t *seq_lens, int num_seqs, int max_seq_len, float scale,
@@ -859,17 +879,13 @@ cudaError_t launch_decode_fp4(void *out, const void *q, const void *kv_cache, co
     a.v_scale = v_scale;
     const long long segs = (long long)num_seqs * g.num_kv_heads;
     const long long tiles = (max_seq_len + (long long)kTokens - 1) / kTokens;
-    // A CTA per segment: no scan of the lengths, no second kernel, but a segment has one SM's
-    // rate, 0.1 us a tile, where the split has a share of all SMs and some 3 us more.  Measured
-    // (us, CTA per segment against the split): 8 segments 7.8 / 8.6 at 768 tokens, 9.2 / 8.6 at
-    // 1152; 32 segments 7.8 / 7.9 at 640, 9.4 / 8.6 at 1152; 72 segments 10.6 / 11.8 at 1536, 12.3 /
-    // 12.3 at 2048; 144 segments 14.5 / 17.2 at 2048, 20.8 / 23.2 at 4096, where it ends: one long
-    // sequence among short ones would have the one SM.
-    a.aligned = segs <= sms && tiles <= 128 && tiles * (sms - segs) <= 30LL * sms;
+    a.aligned = cta_per_segment(segs, tiles, sms, g.head_size);
     // More segments than SMs: whole segments to a CTA, by the prefix sums, spare the second kernel
-    // and cost up to half a segment of imbalance.  376 segments of up to 256, 512, 768, 1024
-    // tokens: 8.5 / 9.0, 10.4 / 11.5, 11.9 / 12.1, 15.1 / 15.0; 2048 segments 18.3 / 19.0, 26.8 /
-    // 27.6, 33.6 / 34.6, 38.6 / 38.6.
+    // and cost up to half a segment of imbalance.  160 segments of one length, whole / split:
+    // 9.9 / 11.3 us at 512 tokens, 11.7 / 11.6 at 768, 12.6 / 12.0 at 896 (head size 64: 7.7 / 9.1,
+    // 8.8 / 9.2, 9.4 / 9.4); 376 of any length up to 512, 768, 1024: 10.3 / 11.4, 12.1 / 12.3, 15.0 /
+    // 14.7 (8.2 / 9.2, 9.1 / 9.6, 10.4 / 10.4); 2048 of up to 768, 1024: 33.6 / 34.5, 38.4 / 38.7
+    // (25.1 / 25.9, 28.1 / 28.3).
     a.whole = a.aligned || tiles <= 24;
     const int grid = (int)(a.aligned ? segs : std::min<long long>(sms, std::max(1LL, segs * tiles)));
     if (g.head_size == 128) {

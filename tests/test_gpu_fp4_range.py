@@ -249,3 +249,18 @@ def test_every_attention_over_a_context_read_back_is_the_formula():
     assert tol.max() < np.abs(want).max() / 20
     for out in (out16, chunk):
         assert (np.abs(np64(out[0]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("d, segs, tokens", [
+    (128, 4, 1408), (128, 8, 1056), (128, 16, 768), (128, 32, 832), (128, 72, 2304),
+    (128, 144, 4096), (64, 1, 4032), (64, 2, 3456), (64, 4, 2304), (64, 8, 1600), (64, 24, 1280),
+    (64, 72, 4000)])
+def test_both_sides_of_a_cta_per_segment(d, segs, tokens):
+    """At the rule's border for 152 SMs and one token beyond: the tile more moves the batch to
+    the other side, whose sums have another order, but not the result."""
+    hkv = math.gcd(segs, 8)
+    for n in (tokens, tokens + 1):
+        b = Batch([n - (i % 3) * 7 for i in range(segs // hkv)], 2 * hkv, hkv, d, 16, seed=tokens)
+        out = b.run()
+        binding.pa_error_check()
+        b.check(out, seqs=range(0, segs // hkv, 5))
