@@ -650,7 +650,9 @@ size_t pa_kv_block_bytes_fp4(int block_size, int num_kv_heads, int head_size);
  *                 row_stride (>= num_kv_heads * head_size, a multiple of 8), 16-byte aligned
  *   slot_mapping  [num_tokens] int32; slot < 0 skips the row; a slot beyond the pool is
  *                 skipped and flagged PA_ERR_OOB
- * The rest of the pool keeps its bytes.  Two rows with one slot: unspecified which lands.
+ * The rest of the pool keeps its bytes.  Two rows with the same slot in one call are a
+ * precondition violation: what the slot then holds is unspecified (codes of one row may meet
+ * scales of the other); no other slot is touched.
  *
  * pa_cache_read_fp4 - the rows in those slots, back in bf16: k_rows and v_rows are written
  * (with code * scale * g, the product with g rounded to binary32, then to bf16).  The rows of
@@ -713,8 +715,9 @@ pa_status pa_decode_fp4(const pa_decode_fp4_args *args);
  *             elements (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved; (a, b) becomes
  *             (a c - b s, b c + a s), c = cos_sin[p][i] and s = cos_sin[p][rot_dim / 2 + i]
  *             at the token's position p = positions[axis][token], axis = pair_axis[i]
- * in fp32, rounded to bf16 once; a 4-bit or FP8 pool then stores K as pa_cache_write_fp4 or
- * pa_cache_write_fp8 would, V as it is in qkv.
+ * in fp32 (a norm's squares, too: a head's elements are below 2^60, and above 2^-60 somewhere
+ * where eps is 0), rounded to bf16 once; a 4-bit or FP8 pool then stores K as pa_cache_write_fp4
+ * or pa_cache_write_fp8 would, V as it is in qkv.
  *   q_out         [num_tokens][num_heads][head_size] bf16, written; must not overlap qkv
  *   kv_cache      the pool: bf16 (kv_bits 16), FP8 (8) or 4-bit (4), in its own layout
  *   qkv           rows of num_heads + 2 * num_kv_heads heads (q, k, v) bf16; row i starts at
@@ -729,7 +732,8 @@ pa_status pa_decode_fp4(const pa_decode_fp4_args *args);
  *                 PA_ERR_OOB); may be NULL when num_axes is 1: axes of time, height and width
  *                 for images and video, in sections or interleaved
  *   slot_mapping  [num_tokens] int32; a negative slot leaves the pool alone (q is written), one
- *                 beyond it likewise, flagged PA_ERR_OOB
+ *                 beyond it likewise, flagged PA_ERR_OOB.  Two tokens with the same slot: as in
+ *                 pa_cache_write_fp4
  *   rot_dim       a multiple of 16, 16 .. head_size (else PA_ERR_UNSUPPORTED)
  *   num_axes      1 .. 8 (else PA_ERR_UNSUPPORTED)
  *   eps           finite, >= 0 (read where there is a norm)

@@ -1,16 +1,18 @@
 // pa_cache_fp4.cu - rows of K and V into a 4-bit pool (quantised) and back (bf16).
 //
 // A thread per 16 elements, the group that shares a scale: 32 bytes of bf16 on one side, 8 bytes
-// of codes and one of scale on the other.  Both directions are bound by HBM: 2.56 bytes an
-// element, each moved once.  A block's threads lie over the groups of one token's K and V rows
+// of codes and one of scale on the other: 2.56 bytes an element, each moved once.  What bounds the
+// write is its quantising, during which a thread has no loads in flight, and the starts and ends of
+// its passes (3.2 TB/s at 4344 tokens, 4.6 at 32768); the read-back waits for memory (ncu: 10 of 14
+// cycles between a warp's instructions; 83 % of the copy rate).  A block's threads lie over the groups of one token's K and V rows
 // (several tokens where those are few), so that a thread keeps its column and finds only the
 // token's slot anew; it takes two or four tokens at once to have as many loads in flight.
 //
 // 4344 tokens of 2 x 8 heads of 128, in a graph: written in 7.2 us (7.5 at a scale of 1, whose
 // ties are common; 10.9 when each tie was divided, 12 with a division per element), read back in
-// 5.9; 32768 tokens 36.5 and 30.9, 4.7 and 5.6 TB/s.  Reading back is bound by the writes: to
-// fill its 134 MB of output alone takes 37 us (3.6 TB/s); stores with other cache policies
-// (evict first, streaming, write through) change nothing.
+// 5.9 (6.0 and 4.7 where three pools in turn stay in L2); 32768 tokens 37 and 30.9, 4.6 and 5.6
+// TB/s.  Stores with other cache policies (evict first, streaming, write through) change nothing in
+// the read-back.
 #include <algorithm>
 #include <atomic>
 

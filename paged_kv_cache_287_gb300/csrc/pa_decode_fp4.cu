@@ -2,6 +2,7 @@
 //
 //   out[s][h] = v_scale sum_t P[t] (code s)_V[t] / sum_t P[t],
 //   P[t] = 2^(scale log2(e) k_scale (x[t] - m)), x[t] = q.(code s)_K[t], m a running reference
+//   that gives the largest 2^11 to 2^15
 //
 // Bound by HBM: 9/16 of a byte per element, read once.  At that rate an SM meets some 43
 // elements a clock, so the work per element must stay below three instructions, and the layout
@@ -25,8 +26,9 @@
 // those in several CTAs by a second kernel (a record per CTA and end of its range); few or short
 // segments go to CTAs whole (rules at launch_decode_fp4).
 //
-// Measured (32 + 8 heads of 128, calls in a row): 256 sequences of 512 - 4096 tokens 111.5 us,
-// 92 % of the copy rate, 32 of up to 131072 tokens 153 us, 96 %; in the steady state 0.66 ns a
+// Measured (32 + 8 heads of 128, in a graph): 256 sequences of 512 - 4096 tokens 111.7 us,
+// 92 % of the copy rate, 32 of up to 131072 tokens 154 us, 95 % (heads of 64: 256 sequences 74.5 us,
+// 69 %, by its instructions, with a rolled loop of four stages); in the steady state 0.66 ns a
 // tile of the whole GPU, 7.0 TB/s, so what is left are the ends (of 256 sequences: 2.1 us to the
 // first copy, 2 from the median CTA's last tile to the last CTA's, 2 of merges, 1.1 of hand-over,
 // 1.3 the second kernel).  Of 524 warp instructions a tile 302 are the products with their
